@@ -7,7 +7,8 @@ h_{t-1} read as 0 where doc_start marks token t (and at token 0 without an initi
 
 8-bit activation checkpoint of x (..., D): blocks of 64 consecutive channels of one token, m the block's
 largest magnitude (at least 2^-100), in 32-bit arithmetic
-    scale = m / 127,   q = round(x * (127 / m)) (ties to even),   value = q * scale.
+    scale = m / 127,   q = round(x * (127 / m)) (ties to even),   value = q * scale;
+the scales are laid out (blocks, ...): the tokens of one block of channels lie next to each other.
 
 `own` selects the framework's kernels; the plain forms are elementary torch operations in 32 bits."""
 
@@ -239,12 +240,12 @@ def _pack(x):
     xb = _blocks(x)
     m = torch.clamp(xb.abs().amax(-1, keepdim=True), min=TINY)
     q = torch.round(xb * (127.0 / m)).to(torch.int8)
-    return q.reshape(*x.shape[:-1], -1)[..., :x.shape[-1]].contiguous(), (m / 127.0)[..., 0].contiguous()
+    return q.reshape(*x.shape[:-1], -1)[..., :x.shape[-1]].contiguous(), (m / 127.0)[..., 0].movedim(-1, 0).contiguous()
 
 
 def _unpack(q, scale):
     D = q.shape[-1]
-    return q.float() * torch.repeat_interleave(scale, BLOCK, -1)[..., :D]
+    return q.float() * torch.repeat_interleave(scale.movedim(0, -1), BLOCK, -1)[..., :D]
 
 
 def _conv_bwd(x, weight, bias, du, doc_start):
@@ -369,7 +370,7 @@ def _codes64(x):
     for xb in torch.split(x.float(), BLOCK, -1):
         m = torch.maximum(xb.abs().max(-1, keepdim=True).values, torch.tensor(TINY, device=x.device))
         parts.append((torch.round((127.0 / m) * xb).double(), (m / 127.0).double()))
-    return torch.cat([q * s for q, s in parts], -1), torch.cat([s for _, s in parts], -1)
+    return torch.cat([q * s for q, s in parts], -1), torch.stack([s[..., 0] for _, s in parts])
 
 
 def _terms64(x, gate_a, gate_x, a_param):
@@ -449,7 +450,7 @@ def exact(case, seed):
         x, scale = _codes64(s["x"])
         return {"x": x, "scale": scale}
     if op == "conv_bwd":
-        sc = torch.repeat_interleave(s["scale"].double(), BLOCK, -1)[..., :D]
+        sc = torch.repeat_interleave(s["scale"].double().permute(1, 2, 0), BLOCK, -1)[..., :D]
         x = (s["q"].double() * sc).requires_grad_(True)
         del sc
         w = s["weight"].double().requires_grad_(True)
