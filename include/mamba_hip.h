@@ -21,9 +21,11 @@
  *       packing paragraph (recurrent state restarts at every document start).
  *
  * Further entry points: the two in one call (mamba_conv_scan_fwd), one-token
- * decode steps, and the backward passes of the conv and of the scan
- * (mamba_causal_conv1d_bwd, mamba_selective_scan_bwd), each described at its
- * declaration below.
+ * decode steps, the backward passes of the conv and of the scan
+ * (mamba_causal_conv1d_bwd, mamba_selective_scan_bwd), a gated linear recurrence
+ * (forward, backward, one-token step: mamba_gated_recurrence_*) and 8-bit
+ * activation checkpoints (mamba_activation_pack, mamba_activation_unpack), each
+ * described at its declaration below.
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE pointers owned by the caller; the library
@@ -374,6 +376,137 @@ int mamba_conv_state_update(const mamba_scan_dims_t* dims, const void* x, void* 
                             const float* conv_bias, float* state, const void* delta, const float* A, const void* B,
                             const void* C, const float* D, const void* z, const float* delta_bias,
                             const uint8_t* reset, void* u_out, void* out, void* stream);
+
+/* ---- Activation checkpoints in 8 bits (training: what the forward keeps for
+ * the backward; axolotl page, gradient-checkpointing paragraph).  x (rows, D),
+ * rows = B L tokens, is kept as int8 codes (rows, D) and one float32 scale per
+ * token and block of 64 consecutive channels, 1.0625 bytes an element.  With m
+ * the block's largest magnitude (at least 2^-100), every quotient and product
+ * rounded to float32,
+ *   scale = m (1 / 127),   code = round(x ((1 / m) 127)) (ties to even),
+ *   value = code scale,
+ * so a value is off by at most half a scale.  A block that holds a NaN or an
+ * infinity gets a NaN scale: every value of it reads back as NaN.  The last block
+ * of a token holds the channels that are left.  The codes and scales a call
+ * writes depend on its inputs alone. */
+#define MAMBA_PACK_BLOCK 64
+typedef struct {
+    int8_t* q;    /* (rows, D), dense                                              */
+    float* scale; /* (ceil(D / 64), rows): the tokens of a block lie side by side  */
+} mamba_packed_t;
+
+/* Writes the checkpoint of x (rows, D).
+ *   ld         elements between two rows of x (0: dense, D; else at least D).
+ * Alignment: x to its element size, scale to 4 bytes (D and ld multiples of 4
+ * with x aligned to four elements and q to 4 bytes select the vectorised kernel).
+ * Outputs must not overlap x or each other.  rows or D of 0 is a no-op. */
+int mamba_activation_pack(const void* x, int8_t* q, float* scale, int64_t rows, int64_t dim, int64_t ld,
+                          int32_t dtype, void* stream);
+
+/* out (rows, D), dtype `dtype`: the values a checkpoint stands for (rounded to
+ * nearest even with bf16). */
+int mamba_activation_unpack(const int8_t* q, const float* scale, void* out, int64_t rows, int64_t dim,
+                            int32_t dtype, void* stream);
+
+/* mamba_causal_conv1d_bwd with x read from its checkpoint (x_q (B, L, D), x_scale
+ * (ceil(D / 64), B L)): the gradients at the values the checkpoint stands for, the
+ * same as for those values given in float32.  conv_state and the gradients
+ * keep `dtype`. */
+int mamba_causal_conv1d_bwd_packed(const int8_t* x_q, const float* x_scale, const float* weight, const float* bias,
+                                   const uint8_t* doc_start, const void* conv_state, const void* du, void* dx,
+                                   float* dweight, float* dbias, float* d_conv_state, int64_t batch, int64_t seqlen,
+                                   int64_t dim, int32_t width, int32_t dtype, int32_t apply_silu, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* ---- Gated linear recurrence: the linear recurrence of the Mamba skill page
+ * ("Hardware-Aware Parallel Scan": h_t = a_t h_{t-1} + b_t with an associative
+ * operator) with one state per channel and both the decay and the input gated by
+ * the token.  Per row, token and channel, with
+ *   r = sigmoid(gate_a),  i = sigmoid(gate_x),  log a = -c softplus(a_param) r,
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t,   out_t = h_t silu(z_t).
+ * Documents, token 0 and initial_state as in mamba_selective_scan_fwd: a start
+ * makes h_{t-1} read as 0, whatever it is (a NaN or an infinity included). */
+#define MAMBA_RECURRENCE_CHUNK 128
+typedef struct {
+    int64_t batch;     /* B                                                        */
+    int64_t seqlen;    /* L                                                        */
+    int64_t dim;       /* D                                                        */
+    int64_t ld_x;      /* elements between two tokens of x, of gate_a, of gate_x,  */
+    int64_t ld_gate_a; /* of z and of dout: 0 for dense (D), else at least D, as   */
+    int64_t ld_gate_x; /* in a slice of one projection's output; tokens of two     */
+    int64_t ld_z;      /* rows follow each other at the same distance.  Outputs    */
+    int64_t ld_dout;   /* and checkpoints are dense.                               */
+    int32_t dtype;     /* mamba_dtype_t of x, gate_a, gate_x, z, out, dout, grads  */
+    float c;           /* decay constant, finite and > 0 (8 is usual)              */
+} mamba_recurrence_dims_t;
+
+/* Bytes of device workspace mamba_gated_recurrence_fwd needs (12 bytes, or 8 with
+ * `states` given, per channel and 128 tokens; 0 for L <= 128). */
+int mamba_gated_recurrence_workspace_bytes(const mamba_recurrence_dims_t* dims, int32_t have_states, size_t* bytes);
+
+/* Forward.
+ *   x, gate_a, gate_x (B, L, D), z (B, L, D) or NULL: `dtype`, strides in dims.
+ *   a_param    (D,) float32, finite.
+ *   doc_start  (B, L) uint8 or NULL.
+ *   initial_state (B, D) float32 or NULL.
+ *   out        (B, L, D), `dtype`.
+ *   final_state (B, D) float32 or NULL: h after token L - 1.
+ *   states     (B, ceil(L / 128), D) float32 or NULL: the states entering tokens
+ *              0, 128, 256, ... (before a document start there takes effect), for
+ *              the backward.
+ *   save       NULL, or four checkpoints to write for x, gate_a, gate_x and z (the
+ *              last with NULL pointers when z is NULL): what
+ *              mamba_activation_pack writes for each, from the values this call
+ *              has read anyway.
+ *   workspace  at least mamba_gated_recurrence_workspace_bytes bytes, 256-byte
+ *              aligned; may be NULL when that is 0.
+ * Supported: D and strides up to 2^21, L up to 3,000,000 and at most 8,000,000
+ * tiles of 128 tokens x 64 channels, else MAMBA_ERR_UNSUPPORTED.  Any alignment to
+ * the element size; D and strides that are multiples of 4 with pointers aligned to
+ * four elements (checkpoint codes to 4 bytes) select the vectorised kernels.
+ * Arithmetic and states are float32.  L of 0 writes final_state = initial_state (or
+ * 0).  Outputs must not overlap anything else of the call.  Repeated calls give
+ * bitwise identical results. */
+int mamba_gated_recurrence_fwd(const mamba_recurrence_dims_t* dims, const void* x, const void* gate_a,
+                               const void* gate_x, const float* a_param, const void* z, const uint8_t* doc_start,
+                               const float* initial_state, void* out, float* final_state, float* states,
+                               const mamba_packed_t* save, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace mamba_gated_recurrence_bwd needs. */
+int mamba_gated_recurrence_bwd_workspace_bytes(const mamba_recurrence_dims_t* dims, int32_t have_states,
+                                               size_t* bytes);
+
+/* Backward: the gradients of sum(dout out) + sum(d_final_state final_state).
+ *   dims ... initial_state: as the forward call.
+ *   packed     NULL, or the four checkpoints of x, gate_a, gate_x, z (z's with NULL
+ *              pointers when there is none); x, gate_a, gate_x and z are then NULL
+ *              and the gradients are taken at the values the checkpoints stand for.
+ *   states     what the forward wrote, or NULL: recomputed from the inputs (with
+ *              `packed`, from the checkpoints).  Given, the states inside a chunk
+ *              of 128 tokens are rebuilt from the one entering it.
+ *   dout       (B, L, D); d_final_state (B, D) float32 or NULL (0).
+ *   dx, dgate_a, dgate_x (B, L, D), dense, `dtype`; da_param (D,) float32.
+ *   dz         (B, L, D); non-NULL exactly when there is a z.
+ *   d_initial_state (B, D) float32 or NULL; requires initial_state.
+ *   workspace  at least mamba_gated_recurrence_bwd_workspace_bytes, 256-byte aligned.
+ * Where 1 - a_t^2 is below 2^-126 the input's weight and its derivative, which is
+ * unbounded towards 0, are taken as 0.  L of 0 writes da_param = 0 and d_initial_state
+ * = d_final_state (or 0).  Repeated calls give bitwise identical results. */
+int mamba_gated_recurrence_bwd(const mamba_recurrence_dims_t* dims, const void* x, const void* gate_a,
+                               const void* gate_x, const float* a_param, const void* z, const uint8_t* doc_start,
+                               const float* initial_state, const mamba_packed_t* packed, const float* states,
+                               const void* dout, const float* d_final_state, void* dx, void* dgate_a, void* dgate_x,
+                               float* da_param, void* dz, float* d_initial_state, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* One token per row: h <- a h + sqrt(1 - a^2) i x (h read as 0 where reset is set),
+ * out = h silu(z).
+ *   dims       with seqlen == 1; strides are between rows.
+ *   state      (B, D) float32, in place.
+ *   x, gate_a, gate_x, z (B, D); reset (B,) uint8 or NULL; out (B, D). */
+int mamba_gated_recurrence_update(const mamba_recurrence_dims_t* dims, float* state, const void* x,
+                                  const void* gate_a, const void* gate_x, const float* a_param, const void* z,
+                                  const uint8_t* reset, void* out, void* stream);
 
 #ifdef __cplusplus
 }

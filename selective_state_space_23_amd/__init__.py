@@ -17,12 +17,23 @@ missing or the tensors are not on a GPU the calls raise.
     out_t = selective_state_update(h, u_t, delta_t, A, B_t, C_t, D, z_t, delta_bias)
     # or both in one launch
     out_t = conv_state_update(x_t, conv_state, weight, bias, h, delta_t, A, B_t, C_t, D, z_t, delta_bias)
+
+    # gated linear recurrence; training keeps its inputs as 8-bit checkpoints
+    out, h, kept = gated_recurrence_fwd(x, gate_a, gate_x, a_param, z, doc_start, save="packed")
+    g = gated_recurrence_bwd(kept["x"], kept["gate_a"], kept["gate_x"], a_param, dout, kept["z"], doc_start,
+                             states=kept["states"])
+    out_t = gated_recurrence_update(h, x_t, gate_a_t, gate_x_t, a_param, z_t)
+
+    # 8-bit checkpoints of any activation: the conv backward reads them as they are
+    p = activation_pack(x)
+    dx, dweight, dbias = causal_conv1d_bwd(p, weight, du, bias, doc_start)
+    u = activation_unpack(activation_pack(u), torch.bfloat16)          # e.g. for selective_scan_bwd
 """
 
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+from typing import NamedTuple, Optional
 
 from . import _lib
 from ._lib import MambaArgumentError, MambaError, ScanDims  # noqa: F401
@@ -40,6 +51,14 @@ __all__ = [
     "scan_bwd_workspace_bytes",
     "causal_conv1d_bwd",
     "conv_bwd_workspace_bytes",
+    "gated_recurrence_fwd",
+    "gated_recurrence_bwd",
+    "gated_recurrence_update",
+    "gated_recurrence_workspace_bytes",
+    "gated_recurrence_bwd_workspace_bytes",
+    "PackedActivation",
+    "activation_pack",
+    "activation_unpack",
     "MambaError",
     "MambaArgumentError",
     "library_path",
@@ -478,8 +497,13 @@ def causal_conv1d_bwd(x, weight, du, bias=None, doc_start=None, apply_silu: bool
     """Gradients of sum(du * u) for u = causal_conv1d_fwd(x, weight, bias, doc_start,
     conv_state, apply_silu); see mamba_causal_conv1d_bwd.  Returns (dx, dweight
     (D, 4) float32, dbias (D,) float32 or None when bias is None), and with a
-    conv_state (B, D, 3) also d_conv_state (B, D, 3) float32 as a fourth item."""
+    conv_state (B, D, 3) also d_conv_state (B, D, 3) float32 as a fourth item.
+    ``x`` may be a PackedActivation: the gradients at the values it stands for, in
+    du's dtype (mamba_causal_conv1d_bwd_packed)."""
     torch = _torch()
+    packed = x if isinstance(x, PackedActivation) else None
+    if packed is not None:
+        x = du
     dev = _check_device(x)
     if x.dim() != 3:
         raise ValueError("x must be (B, L, D)")
@@ -503,8 +527,13 @@ def causal_conv1d_bwd(x, weight, du, bias=None, doc_start=None, apply_silu: bool
                "mamba_causal_conv1d_bwd_workspace_bytes")
     if workspace is None:
         workspace = torch.empty(max(int(need.value), 1), dtype=torch.uint8, device=dev)
-    st = lib.mamba_causal_conv1d_bwd(
-        _ptr(x, "x", dev), _ptr(weight, "weight", dev, torch.float32, (Dm, W)),
+    if packed is None:
+        call, name, xs = lib.mamba_causal_conv1d_bwd, "mamba_causal_conv1d_bwd", (_ptr(x, "x", dev),)
+    else:
+        call, name = lib.mamba_causal_conv1d_bwd_packed, "mamba_causal_conv1d_bwd_packed"
+        xs = _packed_ptrs(packed, "x", dev, (Bt, L, Dm))
+    st = call(
+        *xs, _ptr(weight, "weight", dev, torch.float32, (Dm, W)),
         _ptr(bias, "bias", dev, torch.float32, (Dm,)),
         _ptr(doc_start, "doc_start", dev, torch.uint8, (Bt, L)),
         _ptr(conv_state, "conv_state", dev, x.dtype, (Bt, Dm, 3)),
@@ -513,7 +542,317 @@ def causal_conv1d_bwd(x, weight, du, bias=None, doc_start=None, apply_silu: bool
         _ptr(d_conv_state, "d_conv_state", dev, torch.float32, (Bt, Dm, 3)),
         Bt, L, Dm, W, _dtype_code(x), int(bool(apply_silu)),
         _ptr(workspace, "workspace", dev, torch.uint8), workspace.numel(), _stream(dev))
-    _lib.check(st, "mamba_causal_conv1d_bwd")
+    _lib.check(st, name)
     if conv_state is not None:
         return dx, dweight, dbias, d_conv_state
     return dx, dweight, dbias
+
+
+class PackedActivation(NamedTuple):
+    """An activation kept in 8 bits: ``q`` int8 codes (..., D) and ``scale`` float32
+    (ceil(D / 64), ...), one per token and block of 64 channels; the values are
+    q * scale.  A block that held a NaN or an infinity has a NaN scale."""
+
+    q: object
+    scale: object
+
+
+def _packed_ptrs(p, name, dev, shape):
+    torch = _torch()
+    if not isinstance(p, PackedActivation):
+        raise TypeError(f"{name} must be a PackedActivation")
+    blocks = -(-shape[-1] // _lib.PACK_BLOCK)
+    return (_ptr(p.q, f"{name}.q", dev, torch.int8, shape),
+            _ptr(p.scale, f"{name}.scale", dev, torch.float32, (blocks,) + tuple(shape[:-1])))
+
+
+def _packed_empty(shape, dev):
+    torch = _torch()
+    return PackedActivation(torch.empty(shape, dtype=torch.int8, device=dev),
+                            torch.empty((-(-shape[-1] // _lib.PACK_BLOCK),) + tuple(shape[:-1]), dtype=torch.float32,
+                                        device=dev))
+
+
+def _strided(t, name, dev, dtype, shape):
+    """(pointer, elements between two tokens) of a (..., D) tensor whose channels are
+    contiguous and whose tokens lie at one distance: a dense tensor, or a slice of the
+    channels of one.  (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    D = shape[-1]
+    if D > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: channels must be contiguous")
+    ld, want = None, None   # distance of two tokens, of two steps of the dimension looked at
+    for i in range(len(shape) - 2, -1, -1):
+        if shape[i] == 1:
+            continue
+        if ld is None:
+            ld = want = t.stride(i)
+        if t.stride(i) != want:
+            raise ValueError(f"{name}: tokens must lie at one distance")
+        want *= shape[i]
+    ld = D if ld is None else ld
+    if ld < D:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return t.data_ptr(), ld
+
+
+class _on_device:
+    """The tensors' device made current for the launches, if it is not."""
+
+    def __init__(self, dev):
+        torch = _torch()
+        self._guard = None if dev.index is None or torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def activation_pack(x, packed=None) -> PackedActivation:
+    """The 8-bit checkpoint of x (..., D), float32/bfloat16; see mamba_activation_pack.
+    x's channels are contiguous and its tokens lie at one distance.  ``packed``: an
+    optional PackedActivation to fill."""
+    dev = _check_device(x)
+    if x.dim() < 1:
+        raise ValueError("x must be (..., D)")
+    code = _dtype_code(x)
+    shape = tuple(x.shape)
+    ptr, ld = _strided(x, "x", dev, x.dtype, shape)
+    if packed is None:
+        packed = _packed_empty(shape, dev)
+    q, scale = _packed_ptrs(packed, "packed", dev, shape)
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    with _on_device(dev):
+        st = _lib.load().mamba_activation_pack(ptr, q, scale, rows, shape[-1], ld, code, _stream(dev))
+    _lib.check(st, "mamba_activation_pack")
+    return packed
+
+
+def activation_unpack(packed, dtype=None, out=None):
+    """The values a PackedActivation stands for, float32 or bfloat16 (``dtype``,
+    bfloat16 if not given; or ``out``, a contiguous tensor of q's shape); see
+    mamba_activation_unpack."""
+    torch = _torch()
+    if not isinstance(packed, PackedActivation):
+        raise TypeError("packed must be a PackedActivation")
+    dev = _check_device(packed.q)
+    shape = tuple(packed.q.shape)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=dev)
+    elif dtype is not None and out.dtype != dtype:
+        raise ValueError(f"out must be {dtype}, got {out.dtype}")
+    q, scale = _packed_ptrs(packed, "packed", dev, shape)
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    with _on_device(dev):
+        st = _lib.load().mamba_activation_unpack(q, scale, _ptr(out, "out", dev, out.dtype, shape), rows, shape[-1],
+                                                 _dtype_code(out), _stream(dev))
+    _lib.check(st, "mamba_activation_unpack")
+    return out
+
+
+def _recurrence_dims(batch, seqlen, dim, code, c, lds=(0, 0, 0, 0, 0)) -> _lib.RecurrenceDims:
+    return _lib.RecurrenceDims(batch, seqlen, dim, *lds, code, c)
+
+
+def _recurrence_workspace(call, name, dims, have_states, dev):
+    need = ctypes.c_size_t(0)
+    _lib.check(call(ctypes.byref(dims), int(have_states), ctypes.byref(need)), name)
+    return _torch().empty(int(need.value), dtype=_torch().uint8, device=dev) if need.value else None
+
+
+def gated_recurrence_workspace_bytes(batch, seqlen, dim, dtype="bf16", states=False) -> int:
+    dims = _recurrence_dims(batch, seqlen, dim, _lib.MAMBA_DTYPE_BF16 if dtype == "bf16" else _lib.MAMBA_DTYPE_F32, 8.0)
+    n = ctypes.c_size_t(0)
+    _lib.check(_lib.load().mamba_gated_recurrence_workspace_bytes(ctypes.byref(dims), int(bool(states)),
+                                                                  ctypes.byref(n)),
+               "mamba_gated_recurrence_workspace_bytes")
+    return int(n.value)
+
+
+def gated_recurrence_bwd_workspace_bytes(batch, seqlen, dim, dtype="bf16", states=False) -> int:
+    dims = _recurrence_dims(batch, seqlen, dim, _lib.MAMBA_DTYPE_BF16 if dtype == "bf16" else _lib.MAMBA_DTYPE_F32, 8.0)
+    n = ctypes.c_size_t(0)
+    _lib.check(_lib.load().mamba_gated_recurrence_bwd_workspace_bytes(ctypes.byref(dims), int(bool(states)),
+                                                                      ctypes.byref(n)),
+               "mamba_gated_recurrence_bwd_workspace_bytes")
+    return int(n.value)
+
+
+def gated_recurrence_fwd(x, gate_a, gate_x, a_param, z=None, doc_start=None, c: float = 8.0, initial_state=None,
+                         final_state=True, out=None, save=None, workspace=None):
+    """Gated linear recurrence; see mamba_gated_recurrence_fwd.
+
+    x, gate_a, gate_x, z (B, L, D) float32/bfloat16, dense or slices of the channels
+    of one projection's output; a_param (D,) float32; doc_start (B, L) uint8/bool;
+    initial_state (B, D) float32.  ``final_state``: True to allocate and return it,
+    False/None to skip, or a (B, D) float32 tensor to fill.  ``save``: None;
+    "states" to keep the states the backward starts its chunks from; "packed" to
+    keep them and 8-bit checkpoints of x, gate_a, gate_x and z; or a dict of such
+    tensors to fill ("states" (B, ceil(L / 128), D) float32, and all or none of the
+    PackedActivations "x", "gate_a", "gate_x" and, with a z, "z").  Returns (out,
+    final_state or None), with ``save`` also the dict of what was kept."""
+    torch = _torch()
+    dev = _check_device(x)
+    if x.dim() != 3:
+        raise ValueError("x must be (B, L, D)")
+    code, dt, f32 = _dtype_code(x), x.dtype, torch.float32
+    shape = x.shape
+    Bt, L, Dm = shape
+    if doc_start is not None and doc_start.dtype == torch.bool:
+        doc_start = doc_start.to(torch.uint8)
+    if out is None:
+        out = torch.empty((Bt, L, Dm), dtype=dt, device=dev)
+    if final_state is True:
+        final_state = torch.empty((Bt, Dm), dtype=f32, device=dev)
+    elif final_state is False:
+        final_state = None
+    px, lx = _strided(x, "x", dev, dt, shape)
+    pa, la = _strided(gate_a, "gate_a", dev, dt, shape)
+    pg, lg = _strided(gate_x, "gate_x", dev, dt, shape)
+    pz, lz = _strided(z, "z", dev, dt, shape)
+    names = ("x", "gate_a", "gate_x") + (() if z is None else ("z",))
+    kept, states, pk = None, None, None
+    if save is not None:
+        if isinstance(save, dict):
+            kept = save
+            unknown = set(kept) - {"states", "x", "gate_a", "gate_x", "z"}
+            if unknown:
+                raise ValueError(f"save: unknown entries {sorted(unknown)}")
+            if any(n in kept for n in ("x", "gate_a", "gate_x", "z")) and \
+                    {n for n in ("x", "gate_a", "gate_x", "z") if n in kept} != set(names):
+                raise ValueError(f"save: checkpoints of {names} are kept together")
+        elif save in ("states", "packed"):
+            kept = {"states": torch.empty((Bt, -(-L // _lib.RECURRENCE_CHUNK), Dm), dtype=f32, device=dev)}
+            if save == "packed":
+                kept.update((n, _packed_empty((Bt, L, Dm), dev)) for n in names)
+        else:
+            raise ValueError('save must be None, "states", "packed" or a dict')
+        states = kept.get("states")
+        if "x" in kept:
+            pk = (_lib.Packed * 4)(*(_packed_ptrs(kept[n], n, dev, (Bt, L, Dm)) for n in names))
+    dims = _recurrence_dims(Bt, L, Dm, code, c, (lx, la, lg, lz, 0))
+    lib = _lib.load()
+    if workspace is None and L > _lib.RECURRENCE_CHUNK:
+        workspace = _recurrence_workspace(lib.mamba_gated_recurrence_workspace_bytes,
+                                          "mamba_gated_recurrence_workspace_bytes", dims, states is not None, dev)
+    with _on_device(dev):
+        st = lib.mamba_gated_recurrence_fwd(
+            ctypes.byref(dims), px, pa, pg, _ptr(a_param, "a_param", dev, f32, (Dm,)), pz,
+            _ptr(doc_start, "doc_start", dev, torch.uint8, (Bt, L)),
+            _ptr(initial_state, "initial_state", dev, f32, (Bt, Dm)),
+            _ptr(out, "out", dev, dt, (Bt, L, Dm)),
+            _ptr(final_state, "final_state", dev, f32, (Bt, Dm)),
+            _ptr(states, "states", dev, f32, (Bt, -(-L // _lib.RECURRENCE_CHUNK), Dm)), pk,
+            _ptr(workspace, "workspace", dev, torch.uint8), 0 if workspace is None else workspace.numel(),
+            _stream(dev))
+    _lib.check(st, "mamba_gated_recurrence_fwd")
+    return (out, final_state) if save is None else (out, final_state, kept)
+
+
+def gated_recurrence_bwd(x, gate_a, gate_x, a_param, dout, z=None, doc_start=None, c: float = 8.0,
+                         initial_state=None, d_final_state=None, states=None, workspace=None, grads=None):
+    """Gradients of sum(dout * out) + sum(d_final_state * final_state) for the gated
+    linear recurrence; see mamba_gated_recurrence_bwd.
+
+    x, gate_a, gate_x and z as given to gated_recurrence_fwd, or all of them the
+    PackedActivations it kept; ``states`` what it kept (or None: recomputed); dout
+    (B, L, D), dense or a slice.  Returns a dict with dx, dgate_a, dgate_x (dout's
+    dtype), da_param (D,) float32 and, for each optional input given, dz and
+    d_initial_state (B, D) float32.  ``grads``: optional dict of preallocated outputs
+    with the same keys."""
+    torch = _torch()
+    dev = _check_device(dout)
+    if dout.dim() != 3:
+        raise ValueError("dout must be (B, L, D)")
+    code, dt, f32 = _dtype_code(dout), dout.dtype, torch.float32
+    shape = dout.shape
+    Bt, L, Dm = shape
+    if doc_start is not None and doc_start.dtype == torch.bool:
+        doc_start = doc_start.to(torch.uint8)
+    inputs = (("x", x), ("gate_a", gate_a), ("gate_x", gate_x)) + ((("z", z),) if z is not None else ())
+    is_packed = [isinstance(t, PackedActivation) for _, t in inputs]
+    if any(is_packed) and not all(is_packed):
+        raise ValueError("x, gate_a, gate_x and z must be all tensors or all PackedActivations")
+    ptrs, lds, pk = [None] * 4, [0] * 4, None
+    if all(is_packed):
+        pk = (_lib.Packed * 4)(*(_packed_ptrs(t, n, dev, (Bt, L, Dm)) for n, t in inputs))
+    else:
+        for i, (n, t) in enumerate(inputs):
+            ptrs[i], lds[i] = _strided(t, n, dev, dt, shape)
+    po, lo = _strided(dout, "dout", dev, dt, shape)
+    shapes = {"dx": ((Bt, L, Dm), dt), "dgate_a": ((Bt, L, Dm), dt), "dgate_x": ((Bt, L, Dm), dt),
+              "da_param": ((Dm,), f32)}
+    if z is not None:
+        shapes["dz"] = ((Bt, L, Dm), dt)
+    if initial_state is not None:
+        shapes["d_initial_state"] = ((Bt, Dm), f32)
+    g = dict(grads) if grads else {}
+    for k, (sh, d) in shapes.items():
+        if k not in g:
+            g[k] = torch.empty(sh, dtype=d, device=dev)
+    dims = _recurrence_dims(Bt, L, Dm, code, c, (*lds, lo))
+    lib = _lib.load()
+    if workspace is None:
+        workspace = _recurrence_workspace(lib.mamba_gated_recurrence_bwd_workspace_bytes,
+                                          "mamba_gated_recurrence_bwd_workspace_bytes", dims, states is not None, dev)
+    res = lambda k: _ptr(g[k], k, dev, shapes[k][1], shapes[k][0]) if k in shapes else None  # noqa: E731
+    with _on_device(dev):
+        st = lib.mamba_gated_recurrence_bwd(
+            ctypes.byref(dims), ptrs[0], ptrs[1], ptrs[2], _ptr(a_param, "a_param", dev, f32, (Dm,)), ptrs[3],
+            _ptr(doc_start, "doc_start", dev, torch.uint8, (Bt, L)),
+            _ptr(initial_state, "initial_state", dev, f32, (Bt, Dm)), pk,
+            _ptr(states, "states", dev, f32, (Bt, -(-L // _lib.RECURRENCE_CHUNK), Dm)), po,
+            _ptr(d_final_state, "d_final_state", dev, f32, (Bt, Dm)),
+            res("dx"), res("dgate_a"), res("dgate_x"), res("da_param"), res("dz"), res("d_initial_state"),
+            _ptr(workspace, "workspace", dev, torch.uint8), 0 if workspace is None else workspace.numel(),
+            _stream(dev))
+    _lib.check(st, "mamba_gated_recurrence_bwd")
+    return {k: g[k] for k in shapes}
+
+
+def gated_recurrence_update(state, x, gate_a, gate_x, a_param, z=None, reset=None, c: float = 8.0, out=None):
+    """One step of the gated linear recurrence per row; see
+    mamba_gated_recurrence_update.  state (B, D) float32, updated in place; x, gate_a,
+    gate_x, z (B, D), dense or slices; reset (B,) uint8/bool.  Returns out (B, D)."""
+    torch = _torch()
+    dev = _check_device(x)
+    if x.dim() != 2:
+        raise ValueError("x must be (B, D)")
+    dt, f32 = x.dtype, torch.float32
+    shape = x.shape
+    Bt, Dm = shape
+    if reset is not None and reset.dtype == torch.bool:
+        reset = reset.to(torch.uint8)
+    if out is None:
+        out = torch.empty((Bt, Dm), dtype=dt, device=dev)
+    px, lx = _strided(x, "x", dev, dt, shape)
+    pa, la = _strided(gate_a, "gate_a", dev, dt, shape)
+    pg, lg = _strided(gate_x, "gate_x", dev, dt, shape)
+    pz, lz = _strided(z, "z", dev, dt, shape)
+    dims = _recurrence_dims(Bt, 1, Dm, _dtype_code(x), c, (lx, la, lg, lz, 0))
+    with _on_device(dev):
+        st = _lib.load().mamba_gated_recurrence_update(
+            ctypes.byref(dims), _ptr(state, "state", dev, f32, (Bt, Dm)), px, pa, pg,
+            _ptr(a_param, "a_param", dev, f32, (Dm,)), pz, _ptr(reset, "reset", dev, torch.uint8, (Bt,)),
+            _ptr(out, "out", dev, dt, (Bt, Dm)), _stream(dev))
+    _lib.check(st, "mamba_gated_recurrence_update")
+    return out

@@ -33,7 +33,18 @@ EXPORTED = (
     "mamba_causal_conv1d_bwd",
     "mamba_conv_state_update",
     "mamba_selective_scan_fwd_noalloc",
+    "mamba_activation_pack",
+    "mamba_activation_unpack",
+    "mamba_causal_conv1d_bwd_packed",
+    "mamba_gated_recurrence_workspace_bytes",
+    "mamba_gated_recurrence_fwd",
+    "mamba_gated_recurrence_bwd_workspace_bytes",
+    "mamba_gated_recurrence_bwd",
+    "mamba_gated_recurrence_update",
 )
+
+PACK_BLOCK = 64          # MAMBA_PACK_BLOCK: channels that share one scale
+RECURRENCE_CHUNK = 128   # MAMBA_RECURRENCE_CHUNK: tokens between two saved states
 
 
 class ScanDims(ctypes.Structure):
@@ -49,6 +60,29 @@ class ScanDims(ctypes.Structure):
         ("dtype", ctypes.c_int32),
         ("delta_softplus", ctypes.c_int32),
     ]
+
+
+class RecurrenceDims(ctypes.Structure):
+    """mamba_recurrence_dims_t"""
+
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("dim", ctypes.c_int64),
+        ("ld_x", ctypes.c_int64),
+        ("ld_gate_a", ctypes.c_int64),
+        ("ld_gate_x", ctypes.c_int64),
+        ("ld_z", ctypes.c_int64),
+        ("ld_dout", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("c", ctypes.c_float),
+    ]
+
+
+class Packed(ctypes.Structure):
+    """mamba_packed_t"""
+
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
 
 class MambaError(RuntimeError):
@@ -107,6 +141,22 @@ def load() -> ctypes.CDLL:
     lib.mamba_conv_state_update.restype = ctypes.c_int
     lib.mamba_selective_scan_fwd_noalloc.argtypes = [ctypes.POINTER(ScanDims)] + [vp] * 13
     lib.mamba_selective_scan_fwd_noalloc.restype = ctypes.c_int
+    lib.mamba_activation_pack.argtypes = [vp, vp, vp, i64, i64, i64, i32, vp]
+    lib.mamba_activation_pack.restype = ctypes.c_int
+    lib.mamba_activation_unpack.argtypes = [vp, vp, vp, i64, i64, i32, vp]
+    lib.mamba_activation_unpack.restype = ctypes.c_int
+    lib.mamba_causal_conv1d_bwd_packed.argtypes = [vp] * 11 + [i64, i64, i64, i32, i32, i32, vp, sz, vp]
+    lib.mamba_causal_conv1d_bwd_packed.restype = ctypes.c_int
+    rd, pk = ctypes.POINTER(RecurrenceDims), ctypes.POINTER(Packed)
+    for name in ("mamba_gated_recurrence_workspace_bytes", "mamba_gated_recurrence_bwd_workspace_bytes"):
+        getattr(lib, name).argtypes = [rd, i32, ctypes.POINTER(sz)]
+        getattr(lib, name).restype = ctypes.c_int
+    lib.mamba_gated_recurrence_fwd.argtypes = [rd] + [vp] * 10 + [pk, vp, sz, vp]
+    lib.mamba_gated_recurrence_fwd.restype = ctypes.c_int
+    lib.mamba_gated_recurrence_bwd.argtypes = [rd] + [vp] * 7 + [pk] + [vp] * 9 + [vp, sz, vp]
+    lib.mamba_gated_recurrence_bwd.restype = ctypes.c_int
+    lib.mamba_gated_recurrence_update.argtypes = [rd] + [vp] * 9
+    lib.mamba_gated_recurrence_update.restype = ctypes.c_int
     _lib = lib
     return lib
 

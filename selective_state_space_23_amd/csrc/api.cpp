@@ -8,31 +8,14 @@
 #include <climits>
 #include <cstdint>
 
+#include "api_checks.hpp"
 #include "fill.hpp"
 #include "launch.hpp"
+#include "recurrence_launch.hpp"
 
 namespace {
 
-constexpr int64_t kMaxDim = int64_t(1) << 24;        // channels per row
-constexpr int64_t kMaxElems = int64_t(1) << 40;      // elements per tensor
-constexpr int64_t kMaxSeqlen = 3000000;              // grid.y limits of the kernels
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// [p, p + bytes) and [q, q + qbytes) overlap (null or empty ranges never do).
-bool overlap(const void* p, size_t bytes, const void* q, size_t qbytes) {
-    if (!p || !q || bytes == 0 || qbytes == 0) return false;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return a < b + qbytes && b < a + bytes;
-}
-
-bool mul_ok(int64_t a, int64_t b, int64_t c, int64_t* out) {
-    if (a < 0 || b < 0 || c < 0) return false;
-    __int128 r = static_cast<__int128>(a) * b * c;
-    if (r > kMaxElems) return false;
-    *out = static_cast<int64_t>(r);
-    return true;
-}
+using namespace mamba::api;
 
 int check_dims(const mamba_scan_dims_t* d) {
     if (!d) return MAMBA_ERR_INVALID_ARGUMENT;
@@ -478,10 +461,12 @@ int mamba_causal_conv1d_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64
     return MAMBA_OK;
 }
 
-int mamba_causal_conv1d_bwd(const void* x, const float* weight, const float* bias, const uint8_t* doc_start,
-                            const void* conv_state, const void* du, void* dx, float* dweight, float* dbias,
-                            float* d_conv_state, int64_t batch, int64_t seqlen, int64_t dim, int32_t width,
-                            int32_t dtype, int32_t apply_silu, void* workspace, size_t workspace_bytes, void* stream) {
+// The conv backward from x, or from its 8-bit checkpoint (q, scale) with x null.
+static int conv1d_bwd_call(const void* x, const int8_t* q, const float* scale, const float* weight,
+                           const float* bias, const uint8_t* doc_start, const void* conv_state, const void* du,
+                           void* dx, float* dweight, float* dbias, float* d_conv_state, int64_t batch,
+                           int64_t seqlen, int64_t dim, int32_t width, int32_t dtype, int32_t apply_silu,
+                           void* workspace, size_t workspace_bytes, void* stream) {
     if (batch < 0 || seqlen < 0 || dim < 0) return MAMBA_ERR_INVALID_ARGUMENT;
     if (dtype != MAMBA_DTYPE_F32 && dtype != MAMBA_DTYPE_BF16) return MAMBA_ERR_INVALID_ARGUMENT;
     if (width != 4) return MAMBA_ERR_UNSUPPORTED;
@@ -497,24 +482,28 @@ int mamba_causal_conv1d_bwd(const void* x, const float* weight, const float* bia
         const int64_t zn[] = {dim * 4, dim, batch * dim * 3};
         return zero_outputs(zs, zn, 3, stream);
     }
-    if (!x || !weight || !du || !dx || !dweight) return MAMBA_ERR_INVALID_ARGUMENT;
+    const bool packed = q != nullptr || scale != nullptr;
+    if (packed ? (!q || !scale) : !x) return MAMBA_ERR_INVALID_ARGUMENT;
+    if (!weight || !du || !dx || !dweight) return MAMBA_ERR_INVALID_ARGUMENT;
     const size_t esz = dtype == MAMBA_DTYPE_BF16 ? 2 : 4;
-    if (!aligned(x, esz) || !aligned(du, esz) || !aligned(dx, esz) || !aligned(weight, 4) || !aligned(dweight, 4) ||
-        (bias && !aligned(bias, 4)) || (dbias && !aligned(dbias, 4)) || (conv_state && !aligned(conv_state, esz)) ||
-        (d_conv_state && !aligned(d_conv_state, 4)))
+    if ((x && !aligned(x, esz)) || (scale && !aligned(scale, 4)) || !aligned(du, esz) || !aligned(dx, esz) ||
+        !aligned(weight, 4) || !aligned(dweight, 4) || (bias && !aligned(bias, 4)) || (dbias && !aligned(dbias, 4)) ||
+        (conv_state && !aligned(conv_state, esz)) || (d_conv_state && !aligned(d_conv_state, 4)))
         return MAMBA_ERR_MISALIGNED;
     const size_t act = static_cast<size_t>(n) * esz;
     const size_t hist = static_cast<size_t>(batch * dim * 3);
     const size_t need = mamba::conv_bwd_workspace_bytes(batch, seqlen, dim);
     if (!workspace || workspace_bytes < need) return MAMBA_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return MAMBA_ERR_MISALIGNED;
-    const void* ins[] = {x, weight, bias, doc_start, du, conv_state};
+    const int64_t blocks = (dim + mamba::kPackBlock - 1) / mamba::kPackBlock;
+    const void* ins[] = {x, weight, bias, doc_start, du, conv_state, q, scale};
     const size_t insz[] = {act, static_cast<size_t>(dim) * 16, static_cast<size_t>(dim) * 4,
-                           static_cast<size_t>(batch * seqlen), act, hist * esz};
+                           static_cast<size_t>(batch * seqlen), act, hist * esz, static_cast<size_t>(n),
+                           static_cast<size_t>(batch * seqlen * blocks) * 4};
     const void* outs[] = {dx, dweight, dbias, d_conv_state, workspace};
     const size_t outsz[] = {act, static_cast<size_t>(dim) * 16, static_cast<size_t>(dim) * 4, hist * 4, need};
     for (int o = 0; o < 5; ++o) {
-        for (int i = 0; i < 6; ++i)
+        for (int i = 0; i < 8; ++i)
             if (overlap(outs[o], outsz[o], ins[i], insz[i])) return MAMBA_ERR_INVALID_ARGUMENT;
         for (int k = o + 1; k < 5; ++k)
             if (overlap(outs[o], outsz[o], outs[k], outsz[k])) return MAMBA_ERR_INVALID_ARGUMENT;
@@ -526,10 +515,36 @@ int mamba_causal_conv1d_bwd(const void* x, const float* weight, const float* bia
     a.batch = batch; a.seqlen = seqlen; a.dim = dim;
     a.bf16 = dtype == MAMBA_DTYPE_BF16;
     const size_t vbytes = 2 * esz;           // channel pairs
-    a.vectorized = (dim % 2) == 0 && aligned(x, vbytes) && aligned(du, vbytes) && aligned(dx, vbytes);
+    a.vectorized = (dim % 2) == 0 && aligned(packed ? q : x, packed ? 2 : vbytes) && aligned(du, vbytes) &&
+                   aligned(dx, vbytes);
     a.apply_silu = apply_silu != 0;
     a.stream = static_cast<hipStream_t>(stream);
+    if (packed) {
+        mamba::Packed in;
+        in.q = const_cast<int8_t*>(q);
+        in.scale = const_cast<float*>(scale);
+        return mamba::launch_causal_conv1d_bwd_packed(a, in) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
+    }
     return mamba::launch_causal_conv1d_bwd(a) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
+}
+
+int mamba_causal_conv1d_bwd(const void* x, const float* weight, const float* bias, const uint8_t* doc_start,
+                            const void* conv_state, const void* du, void* dx, float* dweight, float* dbias,
+                            float* d_conv_state, int64_t batch, int64_t seqlen, int64_t dim, int32_t width,
+                            int32_t dtype, int32_t apply_silu, void* workspace, size_t workspace_bytes, void* stream) {
+    return conv1d_bwd_call(x, nullptr, nullptr, weight, bias, doc_start, conv_state, du, dx, dweight, dbias,
+                           d_conv_state, batch, seqlen, dim, width, dtype, apply_silu, workspace, workspace_bytes,
+                           stream);
+}
+
+int mamba_causal_conv1d_bwd_packed(const int8_t* x_q, const float* x_scale, const float* weight, const float* bias,
+                                   const uint8_t* doc_start, const void* conv_state, const void* du, void* dx,
+                                   float* dweight, float* dbias, float* d_conv_state, int64_t batch, int64_t seqlen,
+                                   int64_t dim, int32_t width, int32_t dtype, int32_t apply_silu, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+    return conv1d_bwd_call(nullptr, x_q, x_scale, weight, bias, doc_start, conv_state, du, dx, dweight, dbias,
+                           d_conv_state, batch, seqlen, dim, width, dtype, apply_silu, workspace, workspace_bytes,
+                           stream);
 }
 
 int mamba_selective_scan_bwd_workspace_bytes(const mamba_scan_dims_t* dims, size_t* bytes) {

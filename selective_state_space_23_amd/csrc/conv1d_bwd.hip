@@ -25,6 +25,7 @@
 // tokens 0..2 complete it.
 #include "device_common.hpp"
 #include "launch.hpp"
+#include "recurrence_launch.hpp"
 
 namespace mamba {
 
@@ -56,9 +57,36 @@ namespace {
 constexpr int kTile = 48;          // tokens per thread; kTile + 6 <= 64 for one ballot
 constexpr int kBlock = 256;
 
-template <typename T, int VEC, bool SILU>
+// The conv's input: x as stored, or its 8-bit checkpoint (codes (tokens, D), one
+// scale per token and 64 channels laid out (blocks, tokens)).  The channels of a
+// thread lie in one block: its scale comes with one 4-byte load per token, the
+// same address in the lanes of a block.
+template <typename T, int VEC> struct PlainX {
+    const void* __restrict__ x;
+    __device__ __forceinline__ void load(int64_t token, int dim, int d0, float (&v)[VEC]) const {
+        VecIO<T, VEC>::load(x, token * dim + d0, v);
+    }
+};
+template <int VEC> struct PackedX {
+    const int8_t* __restrict__ q;
+    const float* __restrict__ scale;
+    int64_t tokens;
+    __device__ __forceinline__ void load(int64_t token, int dim, int d0, float (&v)[VEC]) const {
+        const float s = scale[(d0 / kPackBlock) * tokens + token];
+        const int8_t* p = q + token * dim + d0;
+        if constexpr (VEC == 2) {
+            const uint32_t w = *reinterpret_cast<const uint16_t*>(p);
+            v[0] = static_cast<float>(static_cast<int8_t>(w & 0xff)) * s;
+            v[1] = static_cast<float>(static_cast<int8_t>(w >> 8)) * s;
+        } else {
+            v[0] = static_cast<float>(p[0]) * s;
+        }
+    }
+};
+
+template <typename T, int VEC, bool SILU, typename X>
 __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(
-    const void* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
+    const X x, const float* __restrict__ weight, const float* __restrict__ bias,
     const uint8_t* __restrict__ doc_start, const void* __restrict__ conv_state, const void* __restrict__ du,
     void* __restrict__ dx, float* __restrict__ d_conv_state, float* __restrict__ part, int64_t seqlen, int dim) {
     const int ngroups = (dim + VEC - 1) / VEC;
@@ -94,7 +122,7 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(
         const int64_t t = t0 - 3 + k;
         float xv[VEC];
         if (t >= 0) {
-            VecIO<T, VEC>::load(x, (row + t) * dim + d0, xv);
+            x.load(row + t, dim, d0, xv);
         } else if (conv_state != nullptr) {  // (B, D, 3): x_{-3}, x_{-2}, x_{-1} of each channel
 #pragma unroll
             for (int i = 0; i < VEC; ++i) xv[i] = Elem<T>::load(conv_state, (b * dim + d0 + i) * 3 + (3 + t));
@@ -129,7 +157,7 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(
     // x and du of the next token are fetched while the current one computes.
     auto fetch = [&](int64_t t, float (&xv)[VEC], float (&gv)[VEC]) {
         if (t < seqlen) {
-            VecIO<T, VEC>::load(x, (row + t) * dim + d0, xv);
+            x.load(row + t, dim, d0, xv);
             VecIO<T, VEC>::load(du, (row + t) * dim + d0, gv);
         } else {
 #pragma unroll
@@ -240,17 +268,17 @@ __global__ __launch_bounds__(1024) void conv1d_bwd_reduce_kernel(const float* __
     else if (dbias) dbias[d] = tot;
 }
 
-template <typename T, int VEC>
-hipError_t launch_conv_bwd_vec(const ConvBwdArgs& a) {
+template <typename T, int VEC, typename X>
+hipError_t launch_conv_bwd_x(const ConvBwdArgs& a, const X& x) {
     const int ngroups = static_cast<int>((a.dim + VEC - 1) / VEC);
     const int64_t ntiles = (a.seqlen + kTile - 1) / kTile;
     dim3 grid((ngroups + kBlock - 1) / kBlock, static_cast<unsigned>(ntiles), static_cast<unsigned>(a.batch));
     if (a.apply_silu)
-        hipLaunchKernelGGL((conv1d_bwd_kernel<T, VEC, true>), grid, dim3(kBlock), 0, a.stream, a.x, a.weight,
+        hipLaunchKernelGGL((conv1d_bwd_kernel<T, VEC, true, X>), grid, dim3(kBlock), 0, a.stream, x, a.weight,
                            a.bias, a.doc_start, a.conv_state, a.du, a.dx, a.d_conv_state, a.ws, a.seqlen,
                            static_cast<int>(a.dim));
     else
-        hipLaunchKernelGGL((conv1d_bwd_kernel<T, VEC, false>), grid, dim3(kBlock), 0, a.stream, a.x, a.weight,
+        hipLaunchKernelGGL((conv1d_bwd_kernel<T, VEC, false, X>), grid, dim3(kBlock), 0, a.stream, x, a.weight,
                            a.bias, a.doc_start, a.conv_state, a.du, a.dx, a.d_conv_state, a.ws, a.seqlen,
                            static_cast<int>(a.dim));
     hipError_t e = hipGetLastError();
@@ -259,6 +287,19 @@ hipError_t launch_conv_bwd_vec(const ConvBwdArgs& a) {
                        a.stream, static_cast<const float*>(a.ws), a.dweight, a.dbias, a.batch * ntiles,
                        static_cast<int>(a.dim));
     return hipGetLastError();
+}
+
+template <typename T, int VEC>
+hipError_t launch_conv_bwd_vec(const ConvBwdArgs& a, const Packed* in) {
+    if (in != nullptr)
+        return launch_conv_bwd_x<T, VEC>(a, PackedX<VEC>{in->q, in->scale, a.batch * a.seqlen});
+    return launch_conv_bwd_x<T, VEC>(a, PlainX<T, VEC>{a.x});
+}
+
+hipError_t launch_conv_bwd(const ConvBwdArgs& a, const Packed* in) {
+    constexpr int V = 2;
+    if (a.bf16) return a.vectorized ? launch_conv_bwd_vec<bf16_t, V>(a, in) : launch_conv_bwd_vec<bf16_t, 1>(a, in);
+    return a.vectorized ? launch_conv_bwd_vec<float, V>(a, in) : launch_conv_bwd_vec<float, 1>(a, in);
 }
 
 }  // namespace
@@ -271,10 +312,7 @@ size_t conv_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
 // registers of 2 channels leave room for 8 waves per SIMD, which hides the
 // loads' latency better than 4 channels a thread at 4 waves (measured 187 vs
 // 233 us on the packed 32K workload; fetching 2 or 3 tokens ahead did not help).
-hipError_t launch_causal_conv1d_bwd(const ConvBwdArgs& a) {
-    constexpr int V = 2;
-    if (a.bf16) return a.vectorized ? launch_conv_bwd_vec<bf16_t, V>(a) : launch_conv_bwd_vec<bf16_t, 1>(a);
-    return a.vectorized ? launch_conv_bwd_vec<float, V>(a) : launch_conv_bwd_vec<float, 1>(a);
-}
+hipError_t launch_causal_conv1d_bwd(const ConvBwdArgs& a) { return launch_conv_bwd(a, nullptr); }
+hipError_t launch_causal_conv1d_bwd_packed(const ConvBwdArgs& a, const Packed& in) { return launch_conv_bwd(a, &in); }
 
 }  // namespace mamba
