@@ -440,9 +440,9 @@ typedef struct {
     float c;           /* decay constant, finite and > 0 (8 is usual)              */
 } mamba_recurrence_dims_t;
 
-/* Bytes of device workspace mamba_gated_recurrence_fwd needs (12 bytes, or 8 with
- * `states` given, per channel and 128 tokens; 0 for L <= 128). */
-int mamba_gated_recurrence_workspace_bytes(const mamba_recurrence_dims_t* dims, int32_t have_states, size_t* bytes);
+/* Bytes of device workspace mamba_gated_recurrence_fwd needs (12 bytes per channel,
+ * in whole blocks of 64, and 128 tokens; 0 for L <= 128). */
+int mamba_gated_recurrence_workspace_bytes(const mamba_recurrence_dims_t* dims, size_t* bytes);
 
 /* Forward.
  *   x, gate_a, gate_x (B, L, D), z (B, L, D) or NULL: `dtype`, strides in dims.

@@ -673,17 +673,16 @@ def _recurrence_dims(batch, seqlen, dim, code, c, lds=(0, 0, 0, 0, 0)) -> _lib.R
     return _lib.RecurrenceDims(batch, seqlen, dim, *lds, code, c)
 
 
-def _recurrence_workspace(call, name, dims, have_states, dev):
+def _recurrence_workspace(call, name, dev, *args):
     need = ctypes.c_size_t(0)
-    _lib.check(call(ctypes.byref(dims), int(have_states), ctypes.byref(need)), name)
+    _lib.check(call(*args, ctypes.byref(need)), name)
     return _torch().empty(int(need.value), dtype=_torch().uint8, device=dev) if need.value else None
 
 
-def gated_recurrence_workspace_bytes(batch, seqlen, dim, dtype="bf16", states=False) -> int:
+def gated_recurrence_workspace_bytes(batch, seqlen, dim, dtype="bf16") -> int:
     dims = _recurrence_dims(batch, seqlen, dim, _lib.MAMBA_DTYPE_BF16 if dtype == "bf16" else _lib.MAMBA_DTYPE_F32, 8.0)
     n = ctypes.c_size_t(0)
-    _lib.check(_lib.load().mamba_gated_recurrence_workspace_bytes(ctypes.byref(dims), int(bool(states)),
-                                                                  ctypes.byref(n)),
+    _lib.check(_lib.load().mamba_gated_recurrence_workspace_bytes(ctypes.byref(dims), ctypes.byref(n)),
                "mamba_gated_recurrence_workspace_bytes")
     return int(n.value)
 
@@ -753,7 +752,7 @@ def gated_recurrence_fwd(x, gate_a, gate_x, a_param, z=None, doc_start=None, c: 
     lib = _lib.load()
     if workspace is None and L > _lib.RECURRENCE_CHUNK:
         workspace = _recurrence_workspace(lib.mamba_gated_recurrence_workspace_bytes,
-                                          "mamba_gated_recurrence_workspace_bytes", dims, states is not None, dev)
+                                          "mamba_gated_recurrence_workspace_bytes", dev, ctypes.byref(dims))
     with _on_device(dev):
         st = lib.mamba_gated_recurrence_fwd(
             ctypes.byref(dims), px, pa, pg, _ptr(a_param, "a_param", dev, f32, (Dm,)), pz,
@@ -813,7 +812,8 @@ def gated_recurrence_bwd(x, gate_a, gate_x, a_param, dout, z=None, doc_start=Non
     lib = _lib.load()
     if workspace is None:
         workspace = _recurrence_workspace(lib.mamba_gated_recurrence_bwd_workspace_bytes,
-                                          "mamba_gated_recurrence_bwd_workspace_bytes", dims, states is not None, dev)
+                                          "mamba_gated_recurrence_bwd_workspace_bytes", dev, ctypes.byref(dims),
+                                          int(states is not None))
     res = lambda k: _ptr(g[k], k, dev, shapes[k][1], shapes[k][0]) if k in shapes else None  # noqa: E731
     with _on_device(dev):
         st = lib.mamba_gated_recurrence_bwd(

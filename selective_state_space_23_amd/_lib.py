@@ -148,9 +148,10 @@ def load() -> ctypes.CDLL:
     lib.mamba_causal_conv1d_bwd_packed.argtypes = [vp] * 11 + [i64, i64, i64, i32, i32, i32, vp, sz, vp]
     lib.mamba_causal_conv1d_bwd_packed.restype = ctypes.c_int
     rd, pk = ctypes.POINTER(RecurrenceDims), ctypes.POINTER(Packed)
-    for name in ("mamba_gated_recurrence_workspace_bytes", "mamba_gated_recurrence_bwd_workspace_bytes"):
-        getattr(lib, name).argtypes = [rd, i32, ctypes.POINTER(sz)]
-        getattr(lib, name).restype = ctypes.c_int
+    lib.mamba_gated_recurrence_workspace_bytes.argtypes = [rd, ctypes.POINTER(sz)]
+    lib.mamba_gated_recurrence_workspace_bytes.restype = ctypes.c_int
+    lib.mamba_gated_recurrence_bwd_workspace_bytes.argtypes = [rd, i32, ctypes.POINTER(sz)]
+    lib.mamba_gated_recurrence_bwd_workspace_bytes.restype = ctypes.c_int
     lib.mamba_gated_recurrence_fwd.argtypes = [rd] + [vp] * 10 + [pk, vp, sz, vp]
     lib.mamba_gated_recurrence_fwd.restype = ctypes.c_int
     lib.mamba_gated_recurrence_bwd.argtypes = [rd] + [vp] * 7 + [pk] + [vp] * 9 + [vp, sz, vp]

@@ -27,18 +27,18 @@ __global__ __launch_bounds__(256) void pack_kernel(const PackArgs a, int nct) {
     const int64_t r0 = static_cast<int64_t>(blockIdx.x / static_cast<unsigned>(nct)) * kTileRows;
     const int nv = a.rows - r0 < kTileRows ? static_cast<int>(a.rows - r0) : kTileRows;
     const int c = ct * kTileChannels + 4 * li;
-    const int c_ld = ALIGNED ? (c < dim ? c : dim - 4) : c;
-    const char* xb = static_cast<const char*>(a.x) + r0 * a.ld * Elem<T>::kBytes;
-    Raw4<T> raw[kRows];
+    constexpr int esz = Elem<T>::kBytes;
+    const Rsrc xs = rows_rsrc<esz>(a.x, r0, nv, a.ld, dim);
+    const Rsrc qs = rows_rsrc<1>(a.p.q, r0, nv, dim, dim);
+    const Rsrc ss = tile_rsrc(a.p.scale + ct * a.rows + r0, nv * 4);
+    const uint32_t step = static_cast<uint32_t>(a.ld) * esz, row = grp * kRows;
+    Raw<T, 4> raw[kRows];
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-        const int t = grp * kRows + k < nv ? grp * kRows + k : nv - 1;
-        raw[k] = load4<T, ALIGNED>(xb, static_cast<uint32_t>(t) * static_cast<uint32_t>(a.ld), c_ld, dim);
-    }
+    for (int k = 0; k < kRows; ++k) raw[k] = load_raw<T, 4, ALIGNED>(xs, (row + k) * step + static_cast<uint32_t>(c) * esz);
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
         float v[4];
-        unpack4(raw[k], v);
+        unpack(raw[k], v);
         uint32_t m = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -52,12 +52,8 @@ __global__ __launch_bounds__(256) void pack_kernel(const PackArgs a, int nct) {
         m = umax(m, dpp_u32<0x128>(m));
         float scale, inv;
         block_scale(m, scale, inv);
-        const int t = grp * kRows + k;
-        if (t < nv) {
-            if (li == 0) a.p.scale[ct * a.rows + r0 + t] = scale;
-            store_codes<ALIGNED>(a.p.q + r0 * a.dim, static_cast<uint32_t>(t) * static_cast<uint32_t>(dim), c, dim,
-                                 encode4(v, inv));
-        }
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(scale), ss, li == 0 ? 4 * (row + k) : kNoStore, 0, 0);
+        store_codes<4, ALIGNED>(qs, c < dim ? (row + k) * static_cast<uint32_t>(dim) + c : kNoStore, dim - c, encode(v, inv));
     }
 }
 
@@ -69,22 +65,23 @@ __global__ __launch_bounds__(256) void unpack_kernel(const PackArgs a, int nct) 
     const int64_t r0 = static_cast<int64_t>(blockIdx.x / static_cast<unsigned>(nct)) * kTileRows;
     const int nv = a.rows - r0 < kTileRows ? static_cast<int>(a.rows - r0) : kTileRows;
     const int c = ct * kTileChannels + 4 * li;
-    const int c_ld = ALIGNED ? (c < dim ? c : dim - 4) : c;
+    constexpr int esz = Elem<T>::kBytes;
+    const Rsrc qs = rows_rsrc<1>(a.p.q, r0, nv, dim, dim);
+    const Rsrc ss = tile_rsrc(a.p.scale + ct * a.rows + r0, nv * 4);
+    const Rsrc os = rows_rsrc<esz>(a.out, r0, nv, dim, dim);
+    const uint32_t row = grp * kRows;
     uint32_t q[kRows];
     float s[kRows];
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
-        const int t = grp * kRows + k < nv ? grp * kRows + k : nv - 1;
-        q[k] = load_codes<ALIGNED>(a.p.q + r0 * a.dim, static_cast<uint32_t>(t) * static_cast<uint32_t>(dim), c_ld, dim);
-        s[k] = a.p.scale[ct * a.rows + r0 + t];
+        q[k] = load_codes<4, ALIGNED>(qs, (row + k) * static_cast<uint32_t>(dim) + c);
+        s[k] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ss, 4 * (row + k), 0, 0));
     }
-    char* ob = static_cast<char*>(a.out) + r0 * a.dim * Elem<T>::kBytes;
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
         float v[4];
-        decode4(q[k], s[k], v);
-        const int t = grp * kRows + k;
-        if (t < nv) store4<T, ALIGNED>(ob, static_cast<uint32_t>(t) * static_cast<uint32_t>(dim), c, dim, v);
+        decode(q[k], s[k], v);
+        store_vals<T, 4, ALIGNED>(os, c < dim ? ((row + k) * static_cast<uint32_t>(dim) + c) * esz : kNoStore, dim - c, v);
     }
 }
 

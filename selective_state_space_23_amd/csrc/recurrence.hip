@@ -13,226 +13,275 @@
 
 namespace mamba {
 
-namespace {
-
 using namespace rec;
 
-constexpr int kK = 4;                                // tokens a lane walks
-constexpr int kWaves = kTileTokens / (4 * kK);       // 4 groups of 16 lanes a wave
+namespace {
+
+constexpr int kK = 8;                                // tokens a lane walks
+constexpr int kWaves = kTileTokens / (2 * kK);       // two halves of 32 lanes a wave
 constexpr int kThreads = kWaves * 64;
 
-enum { kAggregate = 0, kOutput = 1 };
+// One pass over the data.  A workgroup works off tiles until none is left (rows
+// of one tile: one workgroup each); a tile's maps stay in registers while the value
+// entering it is found by wave 0, and the next tile's inputs are loaded as soon as
+// the maps are formed, so memory is busy through the scan, the wait and the
+// output.  OUT: writes out, the final state and the checkpoints; else the states
+// alone (the backward's recomputation).
+struct RecFwdKernelArgs {
+    RecFwdArgs a;
+    Chain ch;
+    int nct, ntiles;
+};
 
-// One workgroup per tile.  kAggregate writes the tile's composed map (P, H) per
-// channel; kOutput starts from the state entering the tile (a.states, or the
-// initial state in a row of one tile) and writes out, the final state and the
-// checkpoints.
-template <typename T, bool ALIGNED, bool PIN, bool HAS_Z, bool SAVE, int MODE>
-__global__ __launch_bounds__(kThreads, 4) void rec_fwd_kernel(const RecFwdArgs a, int nct,
-                                                                                    int ntiles,
-                                                                                    float2* __restrict__ agg) {
-    __shared__ float s_k2[kTileChannels];
-    __shared__ float2 s_agg[kWaves][kTileChannels];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int li = lane & 15, ts = lane >> 4;
-    const unsigned nchain = static_cast<unsigned>(nct) * static_cast<unsigned>(a.batch);
-    const unsigned chain = blockIdx.x % nchain;
-    const int tile = static_cast<int>(blockIdx.x / nchain);
-    const int ct = static_cast<int>(chain % static_cast<unsigned>(nct));
-    const int64_t b = chain / static_cast<unsigned>(nct);
-    const int dim = static_cast<int>(a.dim);
-    const int64_t t0 = static_cast<int64_t>(tile) * kTileTokens;
-    const int64_t row_tok = b * a.seqlen + t0;
-    const int64_t left = a.seqlen - t0;
-    const int nv = left < kTileTokens ? static_cast<int>(left) : kTileTokens;
-    const int tok = (wave * 4 + ts) * kK;
-    const int c = ct * kTileChannels + 4 * li;
-    const int c_ld = ALIGNED ? (c < dim ? c : dim - 4) : c;
-    const int64_t rows = a.batch * a.seqlen;
+template <typename T, bool ALIGNED, bool PIN, bool HAS_Z, bool SAVE, bool OUT>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void rec_fwd_kernel(const RecFwdKernelArgs) {
+    __shared__ float s_rate[kTileChannels];
+    __shared__ float s_in[kWaves][kTileChannels];
+    __shared__ float2 s_agg[kWaves + 1][kTileChannels];   // the last row takes what no one reads
+    __shared__ int s_ticket;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int li = lane % kRow, half = lane / kRow;
+    const auto first = kernel_args<RecFwdKernelArgs>();
+    const int dim = static_cast<int>(first->a.dim), nct = first->nct, ntiles = first->ntiles;
+    const int tok = (wave * 2 + half) * kK;
+    Walk walk;
+    walk.init(nct, ntiles, static_cast<int>(first->a.batch));
+    auto draw = [&]() { return walk.draw(kernel_args<RecFwdKernelArgs>()->ch.next); };
+    auto place = [&](int ticket) { return walk.place<false>(ticket, kernel_args<RecFwdKernelArgs>()->a.seqlen); };
 
     LaneIn<T, ALIGNED, PIN, kK> xi, ai, gi;
     LaneIn<T, ALIGNED, false, kK> zi;
-    ai.load(a.gate_a, a.in[1], row_tok, a.ld_a, tok, nv, c_ld, dim, ct, rows);
-    gi.load(a.gate_x, a.in[2], row_tok, a.ld_g, tok, nv, c_ld, dim, ct, rows);
-    xi.load(a.x, a.in[0], row_tok, a.ld_x, tok, nv, c_ld, dim, ct, rows);
-    if constexpr (HAS_Z && MODE != kAggregate) zi.load(a.z, a.in[0], row_tok, a.ld_z, tok, nv, c_ld, dim, ct, rows);
-    const TileStarts starts = tile_starts(a.doc_start, b * a.seqlen, t0, a.seqlen);
-
-    if (threadIdx.x < kTileChannels) {
-        const int d = ct * kTileChannels + threadIdx.x;
-        s_k2[threadIdx.x] = -a.c * kLog2e * softplus_exact(a.a_param[d < dim ? d : dim - 1]);
-    }
-    lds_barrier();
-    float k2[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) k2[j] = s_k2[4 * li + j];
-
-    if constexpr (SAVE) {
-        if (a.save[0].q != nullptr) save_packed<T, ALIGNED, kK>(xi, a.save[0], row_tok, tok, nv, c, dim, ct, rows);
-        if (a.save[1].q != nullptr) save_packed<T, ALIGNED, kK>(ai, a.save[1], row_tok, tok, nv, c, dim, ct, rows);
-        if (a.save[2].q != nullptr) save_packed<T, ALIGNED, kK>(gi, a.save[2], row_tok, tok, nv, c, dim, ct, rows);
-        if constexpr (HAS_Z)
-            if (a.save[3].q != nullptr) save_packed<T, ALIGNED, kK>(zi, a.save[3], row_tok, tok, nv, c, dim, ct, rows);
-    }
-
-    auto body = [&](auto gen) {
-        constexpr bool GEN = decltype(gen)::value;   // document starts or tokens past the row end in the tile
-        const uint32_t st = GEN ? starts.bits(tok, kK) : 0u;
-        float P[kK][4], H[kK][4];
-        static_for<kK>([&](auto kc) {
-            constexpr int k = decltype(kc)::value;
-            float ga[4], gx[4], x[4];
-            ai.template get<k>(ga);
-            gi.template get<k>(gx);
-            xi.template get<k>(x);
-            const bool start = GEN && ((st >> k) & 1u), out = GEN && tok + k >= nv;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float al, om;
-                decay_terms(k2[j] * sigmoid_f(ga[j]), al, om);
-                float bb = __builtin_amdgcn_sqrtf(om) * (sigmoid_f(gx[j]) * x[j]);
-                if constexpr (GEN) {
-                    al = out ? 1.0f : al;
-                    bb = out ? 0.0f : bb;
-                }
-                if constexpr (k == 0) {
-                    P[k][j] = al;
-                    H[k][j] = bb;
-                } else {
-                    P[k][j] = P[k - 1][j] * al;
-                    H[k][j] = __builtin_fmaf(al, H[k - 1][j], bb);
-                }
-                if constexpr (GEN) {
-                    P[k][j] = start ? -0.0f : P[k][j];
-                    H[k][j] = start ? bb : H[k][j];
-                }
-            }
-        });
-        // prefixes over the wave's four groups of lanes
-        float wp[4], wh[4], ep[4], eh[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float p = P[kK - 1][j], h = H[kK - 1][j];
-            float p1 = __shfl_up(p, 16), h1 = __shfl_up(h, 16);
-            if (ts >= 1) compose(p, h, p1, h1);
-            p1 = __shfl_up(p, 32); h1 = __shfl_up(h, 32);
-            if (ts >= 2) compose(p, h, p1, h1);
-            wp[j] = p; wh[j] = h;
-            p1 = __shfl_up(p, 16); h1 = __shfl_up(h, 16);
-            ep[j] = ts >= 1 ? p1 : 1.0f;
-            eh[j] = ts >= 1 ? h1 : 0.0f;
+    StartFlags fl;
+    float rate[kV];
+    auto fetch = [&](const Tile& t) {
+        const int c = t.ct * kTileChannels + kV * li;
+        const auto p = kernel_args<RecFwdKernelArgs>();
+        const auto& a = p->a;
+        const int64_t rows = a.batch * a.seqlen;
+        ai.load(a.gate_a, a.in[1], t, a.ld_a, tok, c, dim, rows);
+        gi.load(a.gate_x, a.in[2], t, a.ld_g, tok, c, dim, rows);
+        xi.load(a.x, a.in[0], t, a.ld_x, tok, c, dim, rows);
+        if constexpr (HAS_Z && OUT) zi.load(a.z, a.in[0], t, a.ld_z, tok, c, dim, rows);
+        fl.load(a.doc_start, t.row_tok, t.nv);
+        if (ntiles > 1) {
+            const float2 r = *reinterpret_cast<const float2*>(p->ch.rate + c);   // padded to whole channel tiles
+            rate[0] = r.x; rate[1] = r.y;
         }
-        if (ts == 3) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s_agg[wave][4 * li + j] = make_float2(wp[j], wh[j]);
+    };
+
+    int cur, next;
+    if (ntiles > 1) {
+        if (wave == 0) s_ticket = draw();
+        lds_barrier();
+        cur = __builtin_amdgcn_readfirstlane(s_ticket);
+        lds_barrier();
+        if (wave == 0) s_ticket = draw();
+        if (cur >= walk.tickets) return;
+        fetch(place(cur));
+        lds_barrier();
+        next = __builtin_amdgcn_readfirstlane(s_ticket);
+        lds_barrier();
+    } else {
+        cur = static_cast<int>(blockIdx.x);
+        next = 0x7fffffff;
+        const Tile t = place(cur);
+        fetch(t);
+        if (threadIdx.x < kTileChannels) {
+            const int d = t.ct * kTileChannels + threadIdx.x;
+            s_rate[threadIdx.x] = -first->a.c * kLog2e * softplus_exact(first->a.a_param[d < dim ? d : dim - 1]);
         }
         lds_barrier();
-        if constexpr (MODE == kAggregate) {
-            if (threadIdx.x < kTileChannels) {
-                float2 t = s_agg[0][threadIdx.x];
 #pragma unroll
-                for (int w = 1; w < kWaves; ++w) {
-                    float2 u = s_agg[w][threadIdx.x];
-                    compose(u.x, u.y, t.x, t.y);
-                    t = u;
-                }
-                const int d = ct * kTileChannels + threadIdx.x;
-                if (d < dim) agg[(b * ntiles + tile) * a.dim + d] = t;
-            }
-            return;
-        }
-        float e[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int d = c + j < dim ? c + j : dim - 1;
-            e[j] = ntiles > 1 ? a.states[(b * ntiles + tile) * a.dim + d]
-                              : (a.initial_state != nullptr ? a.initial_state[b * a.dim + d] : 0.0f);
-            for (int w = 0; w < wave; ++w) {
-                const float2 u = s_agg[w][4 * li + j];
-                e[j] = apply(u.x, u.y, e[j]);
-            }
-            e[j] = apply(ep[j], eh[j], e[j]);
-        }
-        char* ob = static_cast<char*>(a.out) + row_tok * a.dim * Elem<T>::kBytes;
-        static_for<kK>([&](auto kc) {
-            constexpr int k = decltype(kc)::value;
-            float o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                o[j] = GEN ? apply(P[k][j], H[k][j], e[j]) : __builtin_fmaf(P[k][j], e[j], H[k][j]);
-            if (k == kK - 1 && tile == ntiles - 1 && wave == kWaves - 1 && ts == 3 && a.final_state != nullptr) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (c + j < dim) a.final_state[b * a.dim + c + j] = o[j];
-            }
-            if constexpr (HAS_Z) {
-                float z[4];
-                zi.template get<k>(z);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[j] *= silu_f(z[j]);
-            }
-            if (!GEN || tok + k < nv)
-                store4<T, ALIGNED>(ob, static_cast<uint32_t>(tok + k) * static_cast<uint32_t>(dim), c, dim, o);
-        });
-    };
-    // the same in every wave of the workgroup: body holds a barrier
-    if (starts.any() || nv < kTileTokens) body(std::true_type{});
-    else body(std::false_type{});
-}
+        for (int j = 0; j < kV; ++j) rate[j] = s_rate[kV * li + j];
+    }
 
-// States entering every tile: each channel's maps applied in order.
-__global__ __launch_bounds__(256) void rec_carry_kernel(const float2* __restrict__ agg,
-                                                        const float* __restrict__ initial_state,
-                                                        float* __restrict__ states, int64_t batch, int64_t dim,
-                                                        int ntiles) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= batch * dim) return;
-    const int64_t b = i / dim, d = i % dim;
-    float h = initial_state != nullptr ? initial_state[i] : 0.0f;
-    const int64_t base = b * ntiles * dim + d;
-    for (int t = 0; t < ntiles; ++t) {
-        states[base + t * dim] = h;
-        if (t + 1 < ntiles) {
-            const float2 u = agg[base + t * dim];
-            h = apply(u.x, u.y, h);
+    for (;;) {
+        const Tile t = place(cur);
+        const int c = t.ct * kTileChannels + kV * li;
+        const TileStarts starts = fl.starts();
+        if constexpr (SAVE) {
+            const auto p = kernel_args<RecFwdKernelArgs>();
+            const auto& a = p->a;
+            const int64_t rows = a.batch * a.seqlen;
+            save_packed<T, ALIGNED, kK>(xi, a.save[0], t, tok, c, dim, rows);
+            save_packed<T, ALIGNED, kK>(ai, a.save[1], t, tok, c, dim, rows);
+            save_packed<T, ALIGNED, kK>(gi, a.save[2], t, tok, c, dim, rows);
+            if constexpr (HAS_Z) save_packed<T, ALIGNED, kK>(zi, a.save[3], t, tok, c, dim, rows);
         }
+        // Maps of the lane's tokens from its first one on.  GEN: the tile has document
+        // starts or ends behind the row (decided for the whole workgroup).
+        float P[kK][kV], H[kK][kV];
+        const bool general = starts.any() || t.nv < kTileTokens;
+        auto maps = [&](auto gen) {
+            constexpr bool GEN = decltype(gen)::value;
+            const uint32_t st = GEN ? starts.bits(tok, kK) : 0u;
+            static_for<kK>([&](auto kc) {
+                constexpr int k = decltype(kc)::value;
+                float ga[kV], gx[kV], x[kV];
+                ai.template take<k>(ga);
+                gi.template take<k>(gx);
+                xi.template take<k>(x);
+                const bool start = GEN && ((st >> k) & 1u), out = GEN && tok + k >= t.nv;
+#pragma unroll
+                for (int j = 0; j < kV; ++j) {
+                    float al, om;
+                    decay_terms(rate[j] * sigmoid_f(ga[j]), al, om);
+                    float bb = __builtin_amdgcn_sqrtf(om) * (sigmoid_f(gx[j]) * x[j]);
+                    if constexpr (GEN) {
+                        al = out ? 1.0f : al;
+                        bb = out ? 0.0f : bb;
+                    }
+                    if constexpr (k == 0) {
+                        P[k][j] = al;
+                        H[k][j] = bb;
+                    } else {
+                        P[k][j] = P[k - 1][j] * al;
+                        H[k][j] = __builtin_fmaf(al, H[k - 1][j], bb);
+                    }
+                    if constexpr (GEN) {
+                        P[k][j] = start ? -0.0f : P[k][j];
+                        H[k][j] = start ? bb : H[k][j];
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        };
+        if (general) maps(std::true_type{});
+        else maps(std::false_type{});
+
+        // what the wave's first half does before its second, and the wave's map
+        float ep[kV], eh[kV];
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            float p = P[kK - 1][j], h = H[kK - 1][j];
+            const float p1 = __shfl_xor(p, 32), h1 = __shfl_xor(h, 32);
+            ep[j] = half ? p1 : 1.0f;
+            eh[j] = half ? h1 : 0.0f;
+            compose(p, h, ep[j], eh[j]);
+            s_agg[half ? wave : kWaves][kV * li + j] = make_float2(p, h);
+        }
+        LaneIn<T, ALIGNED, false, kK> zc = zi;
+        lds_barrier();
+        if (wave == 0) {   // a lane per channel: the value entering the tile, the waves and the next tile
+            const int d = t.ct * kTileChannels + lane;
+            const auto p = kernel_args<RecFwdKernelArgs>();
+            const auto& a = p->a;
+            const auto& ch = p->ch;
+            const int64_t word = walk.word(t, lane);
+            const int64_t at = word + static_cast<int64_t>(t.tile) * kTileChannels;
+            float in = row_load(a.initial_state, t.b, a.dim, d);
+            float2 m = s_agg[0][lane];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) {
+                float2 v = s_agg[w][lane];
+                compose(v.x, v.y, m.x, m.y);
+                m = v;
+            }
+            if (t.tile + 1 < ntiles) publish_map(ch.map + at, m.x, m.y);
+            in = look_back(ch.map + word, ch.value + word, t.tile, in);
+            if (t.tile + 1 < ntiles) publish_value(ch.value + at, apply(m.x, m.y, in));
+            row_store(a.states, t.b * ntiles + t.tile, a.dim, d, in);
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                s_in[w][lane] = in;
+                const float2 v = s_agg[w][lane];
+                in = apply(v.x, v.y, in);
+            }
+            if (OUT && t.tile == ntiles - 1) row_store(a.final_state, t.b, a.dim, d, in);
+            if (next < walk.tickets) s_ticket = draw();
+        }
+        fetch(place(next));   // past the last ticket: a tile of no tokens, nothing is read
+        lds_barrier();
+        if constexpr (OUT) {
+            float e[kV];
+#pragma unroll
+            for (int j = 0; j < kV; ++j) e[j] = apply(ep[j], eh[j], s_in[wave][kV * li + j]);
+            constexpr int esz = Elem<T>::kBytes;
+            const Rsrc ob = rows_rsrc<esz>(kernel_args<RecFwdKernelArgs>()->a.out, t.row_tok, t.nv, dim, dim);
+            const uint32_t step = static_cast<uint32_t>(dim) * esz;
+            uint32_t off = store_offset(tok, step, c * esz, c < dim);
+            auto put = [&](auto gen) {
+                constexpr bool GEN = decltype(gen)::value;
+                static_for<kK>([&](auto kc) {
+                    constexpr int k = decltype(kc)::value;
+                    float o[kV];
+#pragma unroll
+                    for (int j = 0; j < kV; ++j) o[j] = apply<GEN>(P[k][j], H[k][j], e[j]);
+                    if constexpr (HAS_Z) {
+                        float z[kV];
+                        zc.template take<k>(z);
+#pragma unroll
+                        for (int j = 0; j < kV; ++j) o[j] *= silu_f(z[j]);
+                    }
+                    store_vals<T, kV, ALIGNED>(ob, off, dim - c, o);
+                    off = next_offset(off, step);
+                });
+            };
+            if (general) put(std::true_type{});
+            else put(std::false_type{});
+        }
+        if (next >= walk.tickets) return;
+        cur = next;
+        next = __builtin_amdgcn_readfirstlane(s_ticket);   // written before the last barrier
     }
 }
 
-template <typename T, bool ALIGNED, bool PIN, bool HAS_Z, bool SAVE>
+// Before a launch: nothing published, no ticket drawn, the channels' rates.
+__global__ __launch_bounds__(256) void rec_clear_kernel(uint4* __restrict__ words, int64_t n, uint32_t* __restrict__ next,
+                                                        float* __restrict__ rate, int nrate,
+                                                        const float* __restrict__ a_param, int dim, float c) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i < n) words[i] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
+    if (i < 8) next[i] = 0;
+    if (i < nrate) rate[i] = -c * kLog2e * softplus_exact(a_param[i < dim ? i : dim - 1]);
+}
+
+constexpr int kResident = 512;   // two workgroups a CU: 4 waves per SIMD
+
+template <typename T, bool ALIGNED, bool PIN, bool HAS_Z, bool SAVE, bool OUT>
 hipError_t launch_fwd(const RecFwdArgs& a) {
     const int nct = static_cast<int>((a.dim + kTileChannels - 1) / kTileChannels);
     const int ntiles = static_cast<int>((a.seqlen + kTileTokens - 1) / kTileTokens);
-    const unsigned grid = static_cast<unsigned>(nct) * static_cast<unsigned>(a.batch) * static_cast<unsigned>(ntiles);
-    RecFwdArgs b = a;
-    float2* agg = static_cast<float2*>(a.ws);
-    hipError_t e;
-    if (ntiles > 1) {
-        if (b.states == nullptr) b.states = reinterpret_cast<float*>(agg + a.batch * ntiles * a.dim);
-        hipLaunchKernelGGL((rec_fwd_kernel<T, ALIGNED, PIN, false, false, kAggregate>), dim3(grid), dim3(kThreads), 0,
-                           a.stream, b, nct, ntiles, agg);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    if (ntiles > 1 || a.states != nullptr) {
-        hipLaunchKernelGGL(rec_carry_kernel, dim3(static_cast<unsigned>((a.batch * a.dim + 255) / 256)), dim3(256), 0,
-                           a.stream, agg, a.initial_state, b.states, a.batch, a.dim, ntiles);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    if (a.out == nullptr) return hipSuccess;   // the states alone (the backward's recomputation)
-    if constexpr (!PIN) {
-        hipLaunchKernelGGL((rec_fwd_kernel<T, ALIGNED, false, HAS_Z, SAVE, kOutput>), dim3(grid), dim3(kThreads), 0,
-                           a.stream, b, nct, ntiles, agg);
-        return hipGetLastError();
-    }
-    return hipSuccess;
+    const int64_t tiles = nct * a.batch * ntiles;
+    Chain ch;
+    const hipError_t e = clear_chains(a.ws, a.batch, a.dim, ntiles, a.a_param, a.c, &ch, a.stream);
+    if (e != hipSuccess) return e;
+    const int64_t grid = ntiles > 1 && tiles > kResident ? kResident : tiles;
+    hipLaunchKernelGGL((rec_fwd_kernel<T, ALIGNED, PIN, HAS_Z, SAVE, OUT>), dim3(static_cast<unsigned>(grid)),
+                       dim3(kThreads), 0, a.stream, RecFwdKernelArgs{a, ch, nct, ntiles});
+    return hipGetLastError();
 }
 
 template <typename T, bool ALIGNED>
 hipError_t launch_fwd_typed(const RecFwdArgs& a) {
-    if (a.in[0].q != nullptr) return launch_fwd<T, ALIGNED, true, false, false>(a);
+    if (a.in[0].q != nullptr) return launch_fwd<T, ALIGNED, true, false, false, false>(a);
+    if (a.out == nullptr) return launch_fwd<T, ALIGNED, false, false, false, false>(a);
     if (a.save[0].q != nullptr)
-        return a.z != nullptr ? launch_fwd<T, ALIGNED, false, true, true>(a) : launch_fwd<T, ALIGNED, false, false, true>(a);
-    return a.z != nullptr ? launch_fwd<T, ALIGNED, false, true, false>(a) : launch_fwd<T, ALIGNED, false, false, false>(a);
+        return a.z != nullptr ? launch_fwd<T, ALIGNED, false, true, true, true>(a)
+                              : launch_fwd<T, ALIGNED, false, false, true, true>(a);
+    return a.z != nullptr ? launch_fwd<T, ALIGNED, false, true, false, true>(a)
+                          : launch_fwd<T, ALIGNED, false, false, false, true>(a);
+}
+
+// Four channels at an element offset, `left` of which exist.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void quad_load(const void* p, int64_t off, int left, float (&v)[4]) {
+    if constexpr (ALIGNED) {
+        VecIO<T, 4>::load(p, off, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = j < left ? Elem<T>::load(p, off + j) : 0.0f;
+    }
+}
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void quad_store(void* p, int64_t off, int left, const float (&v)[4]) {
+    if constexpr (ALIGNED) {
+        VecIO<T, 4>::store(p, off, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < left) Elem<T>::store(p, off + j, v[j]);
+    }
 }
 
 // One token per row: a thread per four channels.
@@ -244,14 +293,13 @@ __global__ __launch_bounds__(256) void rec_update_kernel(const RecUpdateArgs a) 
     if (i >= a.batch * quads) return;
     const int64_t b = i / quads;
     const int c = static_cast<int>(i % quads) * 4;
+    const int left = dim - c;
     float ga[4], gx[4], x[4], z[4], h[4];
-    unpack4(load4<T, ALIGNED>(static_cast<const char*>(a.gate_a) + b * a.ld_a * Elem<T>::kBytes, 0, c, dim), ga);
-    unpack4(load4<T, ALIGNED>(static_cast<const char*>(a.gate_x) + b * a.ld_g * Elem<T>::kBytes, 0, c, dim), gx);
-    unpack4(load4<T, ALIGNED>(static_cast<const char*>(a.x) + b * a.ld_x * Elem<T>::kBytes, 0, c, dim), x);
-    if (a.z != nullptr)
-        unpack4(load4<T, ALIGNED>(static_cast<const char*>(a.z) + b * a.ld_z * Elem<T>::kBytes, 0, c, dim), z);
-    char* sb = reinterpret_cast<char*>(a.state + b * a.dim);
-    unpack4(load4<float, ALIGNED>(sb, 0, c, dim), h);
+    quad_load<T, ALIGNED>(a.gate_a, b * a.ld_a + c, left, ga);
+    quad_load<T, ALIGNED>(a.gate_x, b * a.ld_g + c, left, gx);
+    quad_load<T, ALIGNED>(a.x, b * a.ld_x + c, left, x);
+    if (a.z != nullptr) quad_load<T, ALIGNED>(a.z, b * a.ld_z + c, left, z);
+    quad_load<float, ALIGNED>(a.state, b * a.dim + c, left, h);
     const bool clear = a.reset != nullptr && a.reset[b] != 0;
     float o[4];
 #pragma unroll
@@ -263,16 +311,35 @@ __global__ __launch_bounds__(256) void rec_update_kernel(const RecUpdateArgs a) 
         h[j] = clear ? bb : __builtin_fmaf(al, h[j], bb);
         o[j] = a.z != nullptr ? h[j] * silu_f(z[j]) : h[j];
     }
-    store4<float, ALIGNED>(sb, 0, c, dim, h);
-    store4<T, ALIGNED>(static_cast<char*>(a.out) + b * a.dim * Elem<T>::kBytes, 0, c, dim, o);
+    quad_store<float, ALIGNED>(a.state, b * a.dim + c, left, h);
+    quad_store<T, ALIGNED>(a.out, b * a.dim + c, left, o);
 }
 
 }  // namespace
 
-size_t recurrence_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, bool have_states) {
+size_t recurrence_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
     const int64_t ntiles = (seqlen + kRecChunk - 1) / kRecChunk;
+    const int64_t width = (dim + kPackBlock - 1) / kPackBlock * kPackBlock;
     if (ntiles <= 1) return 0;
-    return static_cast<size_t>(batch * ntiles * dim) * (have_states ? 8 : 12);
+    return static_cast<size_t>(batch * width * ntiles) * 12 + 64 + static_cast<size_t>(width) * 4;
+}
+
+hipError_t clear_chains(void* ws, int64_t batch, int64_t dim, int64_t ntiles, const float* a_param, float c, Chain* ch,
+                        hipStream_t stream) {
+    *ch = Chain{nullptr, nullptr, nullptr, nullptr};
+    if (ntiles <= 1) return hipSuccess;
+    const int64_t width = (dim + kTileChannels - 1) / kTileChannels * kTileChannels;
+    const int64_t words = batch * width * ntiles;
+    ch->map = static_cast<uint64_t*>(ws);
+    ch->value = reinterpret_cast<uint32_t*>(ch->map + words);
+    ch->next = ch->value + words;
+    float* rate = reinterpret_cast<float*>(ch->next + 16);
+    ch->rate = rate;
+    const int64_t n = words * 12 / 16;   // words is a multiple of 64, and 3 words at least a width: n covers the rates
+    hipLaunchKernelGGL(rec_clear_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream,
+                       static_cast<uint4*>(ws), n, ch->next, rate, static_cast<int>(width), a_param,
+                       static_cast<int>(dim), c);
+    return hipGetLastError();
 }
 
 hipError_t launch_recurrence_fwd(const RecFwdArgs& a) {

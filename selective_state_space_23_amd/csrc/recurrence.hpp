@@ -1,11 +1,12 @@
 // Device helpers of the gated linear recurrence (recurrence.hip,
 // recurrence_bwd.hip) and of the 8-bit activation checkpoints (checkpoint.hip).
 //
-// A tile is 128 tokens x 64 channels of one row.  16 consecutive lanes hold one
-// token's 64 channels, 4 each (8 bytes of bf16, 16 of fp32), so a row of a tile
-// is one contiguous span; a lane walks K consecutive tokens in registers, the
-// wave's 4 groups of 16 lanes and then the workgroup's waves take the following
-// ones.
+// A tile is 128 tokens x 64 channels of one row.  In the recurrence 32
+// consecutive lanes hold one token's 64 channels, 2 each (4 bytes of bf16, 8 of
+// fp32), so a row of a tile is one contiguous span; a lane walks K consecutive
+// tokens in registers, the wave's two halves and then the workgroup's waves take
+// the following ones.  (4 channels a lane, 16 lanes a token, halve the loads but
+// need three exchanges across the wave's four groups where two halves need one.)
 #pragma once
 
 #include "device_common.hpp"
@@ -20,113 +21,172 @@ namespace rec {
 constexpr int kTileTokens = kRecChunk;   // 128: also the distance of two saved states
 constexpr int kTileChannels = kPackBlock;  // 64: also the channels that share a scale
 
-// Four consecutive channels of one token as stored.
-template <typename T> struct Raw4;
-template <> struct Raw4<bf16_t> { uint32_t w[2]; };
-template <> struct Raw4<float> { float w[4]; };
+// V (2 or 4) consecutive channels of one token as stored.
+template <typename T, int V> struct Raw {
+    uint32_t w[V * Elem<T>::kBytes / 4];
+};
 
-__device__ __forceinline__ void unpack4(const Raw4<bf16_t>& r, float (&v)[4]) {
-    v[0] = __uint_as_float(r.w[0] << 16);
-    v[1] = __uint_as_float(r.w[0] & 0xffff0000u);
-    v[2] = __uint_as_float(r.w[1] << 16);
-    v[3] = __uint_as_float(r.w[1] & 0xffff0000u);
-}
-__device__ __forceinline__ void unpack4(const Raw4<float>& r, float (&v)[4]) {
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Raw<T, V>& r, float (&v)[V]) {
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = r.w[j];
+        for (int j = 0; j < V; ++j)
+            v[j] = __uint_as_float(j % 2 == 0 ? r.w[j / 2] << 16 : r.w[j / 2] & 0xffff0000u);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = __uint_as_float(r.w[j]);
+    }
 }
 
-// Codes of four channels (bytes) times the block's scale.  A code q is decoded
-// as (q + 128) s - 128 s: the flipped sign bit makes the byte unsigned, which
-// the hardware converts in one instruction, and the fma rounds once.
-__device__ __forceinline__ void decode4(uint32_t codes, float s, float (&v)[4]) {
+// Codes of V channels (bytes) times the block's scale.  A code q is decoded as
+// (q + 128) s - 128 s: the flipped sign bit makes the byte unsigned, which the
+// hardware converts in one instruction, and the fma rounds once.
+template <int V>
+__device__ __forceinline__ void decode(uint32_t codes, float s, float (&v)[V]) {
     const uint32_t u = codes ^ 0x80808080u;
     const float off = -128.0f * s;
-    v[0] = __builtin_fmaf(static_cast<float>(u & 0xffu), s, off);
-    v[1] = __builtin_fmaf(static_cast<float>((u >> 8) & 0xffu), s, off);
-    v[2] = __builtin_fmaf(static_cast<float>((u >> 16) & 0xffu), s, off);
-    v[3] = __builtin_fmaf(static_cast<float>(u >> 24), s, off);
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = __builtin_fmaf(static_cast<float>((u >> (8 * j)) & 0xffu), s, off);
 }
 
-// Loads and stores of four channels c .. c+3 at `base` (the address of the row's
-// tile, channel 0) plus a 32-bit element offset of the token.  ALIGNED: D and
-// every stride are multiples of 4 and every pointer is aligned to four elements,
-// so a quad is wholly inside or outside the row; `c` is then already clamped to
-// a quad inside.  Otherwise each channel is read by itself, clamped to D - 1.
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ Raw4<T> load4(const char* __restrict__ base, uint32_t tok, int c, int dim) {
-    Raw4<T> r;
-    constexpr uint32_t esz = Elem<T>::kBytes;
-    if constexpr (ALIGNED) {
-        const char* p = base + (tok + static_cast<uint32_t>(c)) * esz;
-        if constexpr (esz == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(p);
-            r.w[0] = v.x; r.w[1] = v.y;
-        } else {
-            const float4 v = *reinterpret_cast<const float4*>(p);
-            r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+// A tile's rows of one tensor as a buffer: `n` tokens of `dim` channels, `ld`
+// elements apart, from the tile's first token on.  Reads behind the last token
+// give zero and writes there are dropped (the buffer's range check), so tokens
+// past the row end need no other care.  Byte offsets in a tile fit 31 bits.
+constexpr uint32_t kNoStore = 0x7fffff00u;   // a lane offset past any tile
+using Rsrc = __amdgpu_buffer_rsrc_t;
+__device__ __forceinline__ Rsrc tile_rsrc(const void* first, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(first), 0, static_cast<int>(bytes), 0x00027000);
+}
+template <int ESZ>
+__device__ __forceinline__ Rsrc rows_rsrc(const void* p, int64_t token, int n, int64_t ld, int dim) {
+    return tile_rsrc(static_cast<const char*>(p) + token * ld * ESZ, n > 0 ? ((n - 1) * ld + dim) * ESZ : 0);
+}
+
+// Kernels that work off many tiles read their arguments anew where they need them
+// (scalar loads that hit the cache): held in registers across the loop, the
+// pointers and sizes of a dozen tensors overflow the scalar registers.  The
+// argument struct is the kernel's only parameter, at the start of its arguments.
+template <typename Args> using ArgsPtr = const __attribute__((address_space(4))) Args*;
+template <typename Args>
+__device__ __forceinline__ ArgsPtr<Args> kernel_args() {
+    auto p = (ArgsPtr<Args>)(__builtin_amdgcn_kernarg_segment_ptr());
+    asm volatile("" : "+s"(p));
+    return p;
+}
+
+// tok * step + c for a token of a tile and a step below 2^24, and the offset one
+// step on: formed where they are used, for the same reason.
+__device__ __forceinline__ uint32_t next_offset(uint32_t off, uint32_t step) {
+    off += step;
+    asm volatile("" : "+v"(off));
+    return off;
+}
+__device__ __forceinline__ uint32_t tile_offset(int tok, uint32_t step, int c) {
+    asm volatile("" : "+v"(tok));
+    return __umul24(static_cast<uint32_t>(tok), step) + static_cast<uint32_t>(c);
+}
+
+// One float of row `row` of a (rows, dim) array per lane: channels past dim, and a
+// null array, read 0 and store nothing.  The loops over tiles have no divergent
+// branch at all (range checks and selects in their place): the compiler has been
+// seen to copy live registers at the join of such a branch before it restores the
+// execution mask, which leaves the masked lanes' copies behind.
+__device__ __forceinline__ Rsrc row_rsrc(const float* p, int64_t row, int64_t dim) {
+    return tile_rsrc(p + row * dim, p != nullptr ? dim * 4 : 0);
+}
+__device__ __forceinline__ float row_load(const float* p, int64_t row, int64_t dim, int d) {
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(row_rsrc(p, row, dim), 4 * d, 0, 0));
+}
+__device__ __forceinline__ void row_store(float* p, int64_t row, int64_t dim, int d, float v) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), row_rsrc(p, row, dim), 4 * d, 0, 0);
+}
+
+// The same for a store: past the buffer where the channel is past D.
+__device__ __forceinline__ uint32_t store_offset(int tok, uint32_t step, int c, bool inside) {
+    const uint32_t off = tile_offset(tok, step, c);
+    return inside ? off : kNoStore;
+}
+
+// V consecutive channels at a byte offset.  ALIGNED: D and every stride are
+// multiples of 4 and every pointer is aligned to four elements; else element by
+// element.  Channels past D read what follows (another token's, or zero).
+template <typename T, int V, bool ALIGNED>
+__device__ __forceinline__ Raw<T, V> load_raw(Rsrc rs, uint32_t off) {
+    Raw<T, V> r;
+    constexpr int kWords = sizeof(r.w) / 4;
+    if constexpr (ALIGNED && kWords == 1) {
+        r.w[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0);
+    } else if constexpr (ALIGNED && kWords == 2) {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0);
+        r.w[0] = v[0]; r.w[1] = v[1];
+    } else if constexpr (ALIGNED) {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.w[j] = v[j];
+    } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            const uint32_t lo = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(rs, off + 2 * j, 0, 0));
+            const uint32_t hi = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(rs, off + 2 * j + 2, 0, 0));
+            r.w[j / 2] = lo | (hi << 16);
         }
     } else {
-        uint32_t o[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int cc = c + j < dim ? c + j : dim - 1;
-            o[j] = (tok + static_cast<uint32_t>(cc)) * esz;
-        }
-        if constexpr (esz == 2) {
-            uint32_t h[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = *reinterpret_cast<const uint16_t*>(base + o[j]);
-            r.w[0] = h[0] | (h[1] << 16);
-            r.w[1] = h[2] | (h[3] << 16);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) r.w[j] = *reinterpret_cast<const float*>(base + o[j]);
-        }
+        for (int j = 0; j < V; ++j) r.w[j] = __builtin_amdgcn_raw_buffer_load_b32(rs, off + 4 * j, 0, 0);
     }
     return r;
 }
 
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ void store4(char* __restrict__ base, uint32_t tok, int c, int dim, const float (&v)[4]) {
-    constexpr uint32_t esz = Elem<T>::kBytes;
-    char* p = base + (tok + static_cast<uint32_t>(c)) * esz;
-    if constexpr (ALIGNED) {
-        if (c >= dim) return;
-        if constexpr (esz == 2)
-            *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-        else
-            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
+// `off` is past the buffer where the first channel is past D; `left` of the
+// channels exist (looked at only when not ALIGNED).
+template <typename T, int V, bool ALIGNED>
+__device__ __forceinline__ void store_vals(Rsrc rs, uint32_t off, int left, const float (&v)[V]) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    if constexpr (!ALIGNED) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (c + j < dim) Elem<T>::store(p, j, v[j]);
+        for (int j = 0; j < V; ++j) {
+            const uint32_t o = j < left ? off + j * Elem<T>::kBytes : kNoStore;
+            if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v[j]), rs, o, 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[j]), rs, o, 0, 0);
+        }
+    } else if constexpr (sizeof(T) == 2 && V == 2) {
+        __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(v[0], v[1]), rs, off, 0, 0);
+    } else if constexpr (sizeof(T) == 2) {
+        const u32x2 w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        __builtin_amdgcn_raw_buffer_store_b64(w, rs, off, 0, 0);
+    } else if constexpr (V == 2) {
+        const u32x2 w = {__float_as_uint(v[0]), __float_as_uint(v[1])};
+        __builtin_amdgcn_raw_buffer_store_b64(w, rs, off, 0, 0);
+    } else {
+        const u32x4 w = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+        __builtin_amdgcn_raw_buffer_store_b128(w, rs, off, 0, 0);
     }
 }
 
-// Four code bytes of channels c .. c+3.
-template <bool ALIGNED>
-__device__ __forceinline__ uint32_t load_codes(const int8_t* __restrict__ base, uint32_t tok, int c, int dim) {
-    const uint8_t* p = reinterpret_cast<const uint8_t*>(base);
-    if constexpr (ALIGNED) return *reinterpret_cast<const uint32_t*>(p + (tok + static_cast<uint32_t>(c)));
+// V code bytes.
+template <int V, bool ALIGNED>
+__device__ __forceinline__ uint32_t load_codes(Rsrc rs, uint32_t off) {
+    if constexpr (ALIGNED && V == 4) return __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0);
+    if constexpr (ALIGNED && V == 2) return static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(rs, off, 0, 0));
     uint32_t w = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int cc = c + j < dim ? c + j : dim - 1;
-        w |= static_cast<uint32_t>(p[tok + static_cast<uint32_t>(cc)]) << (8 * j);
-    }
+    for (int j = 0; j < V; ++j)
+        w |= static_cast<uint32_t>(static_cast<uint8_t>(__builtin_amdgcn_raw_buffer_load_b8(rs, off + j, 0, 0))) << (8 * j);
     return w;
 }
 
-template <bool ALIGNED>
-__device__ __forceinline__ void store_codes(int8_t* __restrict__ base, uint32_t tok, int c, int dim, uint32_t w) {
-    uint8_t* p = reinterpret_cast<uint8_t*>(base) + (tok + static_cast<uint32_t>(c));
-    if constexpr (ALIGNED) {
-        if (c < dim) *reinterpret_cast<uint32_t*>(p) = w;
+template <int V, bool ALIGNED>
+__device__ __forceinline__ void store_codes(Rsrc rs, uint32_t off, int left, uint32_t w) {
+    if constexpr (ALIGNED && V == 4) {
+        __builtin_amdgcn_raw_buffer_store_b32(w, rs, off, 0, 0);
+    } else if constexpr (ALIGNED) {
+        __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(w), rs, off, 0, 0);
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (c + j < dim) p[j] = static_cast<uint8_t>(w >> (8 * j));
+        for (int j = 0; j < V; ++j)
+            __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(w >> (8 * j)), rs, j < left ? off + j : kNoStore, 0, 0);
     }
 }
 
@@ -142,18 +202,17 @@ struct TileStarts {
     }
 };
 
-__device__ __forceinline__ TileStarts tile_starts(const uint8_t* __restrict__ doc_start, int64_t row, int64_t t0,
-                                                  int64_t seqlen) {
-    TileStarts s{0, 0};
-    if (doc_start == nullptr) return s;
-    const int lane = threadIdx.x & 63;
-    const int64_t ta = t0 + lane, tb = ta + 64;
-    const bool a = ta < seqlen && doc_start[row + ta] != 0;
-    const bool b = tb < seqlen && doc_start[row + tb] != 0;
-    s.lo = __ballot(a);
-    s.hi = __ballot(b);
-    return s;
-}
+// The lane's two flags of a tile, loaded ahead of their use.
+struct StartFlags {
+    uint32_t a, b;
+    __device__ __forceinline__ void load(const uint8_t* doc_start, int64_t row_tok, int nv) {
+        const int lane = threadIdx.x & 63;
+        const Rsrc rs = tile_rsrc(doc_start + row_tok, doc_start != nullptr ? nv : 0);
+        a = static_cast<uint8_t>(__builtin_amdgcn_raw_buffer_load_b8(rs, lane, 0, 0));
+        b = static_cast<uint8_t>(__builtin_amdgcn_raw_buffer_load_b8(rs, lane + 64, 0, 0));
+    }
+    __device__ __forceinline__ TileStarts starts() const { return TileStarts{__ballot(a != 0), __ballot(b != 0)}; }
+};
 
 // softplus of the decay parameter: once per channel and workgroup, with the math
 // library's own functions (its error goes into every token's decay alike).
@@ -163,20 +222,20 @@ __device__ __forceinline__ float softplus_exact(float v) {
 
 __device__ __forceinline__ float sigmoid_f(float v) { return rcp_fast(1.0f + exp2_fast(-v * kLog2e)); }
 
-// The decay a = 2^la2 and 1 - a^2 for la2 = log2 a <= 0.  1 - a comes from the
-// series of 1 - e^-t, t = -log a, where 1 - a would cancel (t < 0.35: the first
-// term left out is below 2e-8 of the sum) and from a itself above.
+// The decay a = 2^la2 and 1 - a^2 for la2 = log2 a <= 0.  1 - a^2 cancels where a
+// is near 1: with y = -2 log a it is y p(y) there, p a degree-4 Chebyshev
+// interpolant of (1 - e^-y) / y on [0, 0.35], off by at most 3e-8 of it.  Above
+// 0.35 the subtraction loses at most two bits.
 __device__ __forceinline__ void decay_terms(float la2, float& a, float& om) {
     a = exp2_fast(la2);
-    const float t = -kLn2 * la2;
-    float p = __builtin_fmaf(t, 1.0f / 5040.0f, -1.0f / 720.0f);
-    p = __builtin_fmaf(t, p, 1.0f / 120.0f);
-    p = __builtin_fmaf(t, p, -1.0f / 24.0f);
-    p = __builtin_fmaf(t, p, 1.0f / 6.0f);
-    p = __builtin_fmaf(t, p, -0.5f);
-    p = __builtin_fmaf(t, p, 1.0f);
-    const float d = t < 0.35f ? t * p : 1.0f - a;
-    om = d * (1.0f + a);
+    const float y = (-2.0f * kLn2) * la2;
+    float p = __builtin_fmaf(y, 0.00721255037933588f, -0.04133278876543045f);
+    p = __builtin_fmaf(y, p, 0.1666254997253418f);
+    p = __builtin_fmaf(y, p, -0.49999821186065674f);
+    p = __builtin_fmaf(y, p, 1.0f);
+    float near = y * p, far = __builtin_fmaf(-a, a, 1.0f);
+    asm volatile("" : "+v"(near), "+v"(far));   // both formed: the choice stays a select, not a branch
+    om = y < 0.35f ? near : far;
 }
 
 // Value of lane `16 * (lane / 16) + N` in every lane of the row of 16
@@ -192,52 +251,51 @@ __device__ __forceinline__ uint32_t dpp_u32(uint32_t x) {
     return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, 0xf, 0xf, false));
 }
 
-// Largest magnitude of a block as bits: comparing the bit patterns of |x| as
-// integers orders NaN above infinity above every finite number.
-__device__ __forceinline__ uint32_t abs_bits_max4(const float (&v)[4], uint32_t m) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t b = __float_as_uint(v[j]) & 0x7fffffffu;
-        m = b > m ? b : m;
-    }
-    return m;
-}
-
-// Scale and inverse step of a block whose largest magnitude has the bits m:
+// Scale and inverse step of a block whose largest magnitude has the bits m (the
+// bit patterns of |x| compared as integers order NaN above infinity above every
+// finite number):
 // scale = m (1 / 127) and inv = (1 / m) 127, each factor and product rounded.
 // A NaN or an infinity makes both NaN, so that the whole block decodes to NaN;
 // blocks below 2^-100 use m = 2^-100, which keeps inv finite.
 __device__ __forceinline__ void block_scale(uint32_t mbits, float& scale, float& inv) {
     float m = __uint_as_float(mbits);
     m = m < 0x1p-100f ? 0x1p-100f : m;
-    scale = m * (1.0f / 127.0f);
-    inv = (1.0f / m) * 127.0f;
-    if (mbits >= 0x7f800000u) scale = inv = __uint_as_float(0x7fc00000u);
+    float s = m * (1.0f / 127.0f), i = (1.0f / m) * 127.0f;
+    asm volatile("" : "+v"(s), "+v"(i));   // a select below, not a branch
+    const bool finite = mbits < 0x7f800000u;
+    scale = finite ? s : __uint_as_float(0x7fc00000u);
+    inv = finite ? i : __uint_as_float(0x7fc00000u);
 }
 
-// round(v * inv) to the nearest integer, ties to even, as a byte: the product is
+// round(v * inv) to the nearest integer, ties to even, as bytes: the product is
 // rounded first, then adding 1.5 * 2^23 leaves the integer in the low bits.
-__device__ __forceinline__ uint32_t encode4(const float (&v)[4], float inv) {
+template <int V>
+__device__ __forceinline__ uint32_t encode(const float (&v)[V], float inv) {
 #pragma clang fp contract(off)
-    uint32_t b[4];
+    uint32_t w = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < V; ++j) {
         const float t = v[j] * inv;
-        b[j] = __float_as_uint(t + 12582912.0f) & 0xffu;
+        w |= (__float_as_uint(t + 12582912.0f) & 0xffu) << (8 * j);
     }
-    return b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
+    return w;
 }
 
 // Affine maps h -> P h + H of stretches of tokens.  The sign of P marks a map
-// that ignores its input (a document start inside the stretch).
+// that ignores its input (a document start inside the stretch); CUT false: no such
+// map can occur.
 __device__ __forceinline__ bool is_reset(float P) { return __float_as_uint(P) >> 31; }
-// (P, H) after (p, h): first the earlier tokens' map (p, h), then (P, H).
-__device__ __forceinline__ void compose(float& P, float& H, float p, float h) {
-    const bool cut = is_reset(P);
-    H = cut ? H : __builtin_fmaf(P, h, H);
-    P = cut ? P : P * p;
+template <bool CUT = true>
+__device__ __forceinline__ float apply(float P, float H, float h) {
+    const float r = __builtin_fmaf(P, h, H);
+    return CUT && is_reset(P) ? H : r;
 }
-__device__ __forceinline__ float apply(float P, float H, float h) { return is_reset(P) ? H : __builtin_fmaf(P, h, H); }
+// (P, H) after (p, h): first the earlier tokens' map (p, h), then (P, H).
+template <bool CUT = true>
+__device__ __forceinline__ void compose(float& P, float& H, float p, float h) {
+    H = apply<CUT>(P, H, h);
+    P = CUT && is_reset(P) ? P : P * p;
+}
 
 template <int N, typename F, int... I>
 __device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
@@ -248,86 +306,257 @@ __device__ __forceinline__ void static_for(F&& f) {
     static_for_impl<N>(f, std::make_integer_sequence<int, N>{});
 }
 
-// A lane's K quads of one input, plain or 8-bit.
+// A tile's place: uniform over the workgroup.
+struct Tile {
+    int ct, tile, nv;      // channel tile, token tile, tokens in it (0: no such tile)
+    int pos;               // position in the chain
+    int64_t b, row_tok;    // row, first token counted over all rows
+};
+
+// A lane's place in a tile of the recurrence's kernels.
+constexpr int kV = 2;                            // channels of a lane
+constexpr int kRow = kTileChannels / kV;         // lanes of a token
+
+// A lane's K pairs of one input, plain or 8-bit: tokens tok .. tok + K - 1 of the
+// tile, channels c and c + 1.
 template <typename T, bool ALIGNED, bool PIN, int K> struct LaneIn {
-    Raw4<T> r[K];
-    __device__ __forceinline__ void load(const void* p, const Packed&, int64_t row_tok, int64_t ld, int tok, int nv,
-                                         int c, int dim, int, int64_t) {
-        const char* base = static_cast<const char*>(p) + row_tok * ld * Elem<T>::kBytes;
+    Raw<T, kV> r[K];
+    template <typename P>
+    __device__ __forceinline__ void load(const void* p, const P&, const Tile& t, int ld, int tok, int c, int dim,
+                                         int64_t) {
+        constexpr int esz = Elem<T>::kBytes;
+        const Rsrc rs = rows_rsrc<esz>(p, t.row_tok, t.nv, ld, dim);
+        const uint32_t step = static_cast<uint32_t>(ld) * esz;
+        uint32_t off = tile_offset(tok, step, c * esz);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int t = tok + k < nv ? tok + k : nv - 1;
-            r[k] = load4<T, ALIGNED>(base, static_cast<uint32_t>(t) * static_cast<uint32_t>(ld), c, dim);
+            r[k] = load_raw<T, kV, ALIGNED>(rs, off);
+            off = next_offset(off, step);
         }
     }
-    template <int k> __device__ __forceinline__ void get(float (&v)[4]) const { unpack4(r[k], v); }
+    template <int k> __device__ __forceinline__ void get(float (&v)[kV]) const { unpack(r[k], v); }
+    // The same, unpacked here and not where the compiler could do it for several
+    // uses at once (twice the registers across everything in between).
+    template <int k> __device__ __forceinline__ void take(float (&v)[kV]) {
+#pragma unroll
+        for (auto& w : r[k].w) asm volatile("" : "+v"(w));
+        unpack(r[k], v);
+    }
 };
 template <typename T, bool ALIGNED, int K> struct LaneIn<T, ALIGNED, true, K> {
     uint32_t q[K];
-    static constexpr int kPer = 16 / K;   // lanes of a row of 16 that hold one token's scale
+    static constexpr int kPer = 16 / K;   // lanes of a DPP row of 16 that hold one token's scale
     float s;                              // scale of token (lane % 16) / kPer of the lane's K
-    __device__ __forceinline__ void load(const void*, const Packed& p, int64_t row_tok, int64_t, int tok, int nv,
-                                         int c, int dim, int ct, int64_t rows) {
-        const int8_t* base = p.q + row_tok * dim;
+    template <typename P>
+    __device__ __forceinline__ void load(const void*, const P& p, const Tile& t, int, int tok, int c, int dim,
+                                         int64_t rows) {
+        const Rsrc rs = rows_rsrc<1>(p.q, t.row_tok, t.nv, dim, dim);
+        uint32_t off = tile_offset(tok, dim, c);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int t = tok + k < nv ? tok + k : nv - 1;
-            q[k] = load_codes<ALIGNED>(base, static_cast<uint32_t>(t) * static_cast<uint32_t>(dim), c, dim);
+            q[k] = load_codes<kV, ALIGNED>(rs, off);
+            off = next_offset(off, dim);
         }
-        const int st = tok + static_cast<int>(threadIdx.x & 15) / kPer;
-        s = p.scale[ct * rows + row_tok + (st < nv ? st : nv - 1)];
+        const Rsrc ss = tile_rsrc(p.scale + t.ct * rows + t.row_tok, t.nv * 4);
+        s = __uint_as_float(
+            __builtin_amdgcn_raw_buffer_load_b32(ss, 4 * (tok + static_cast<int>(threadIdx.x & 15) / kPer), 0, 0));
     }
-    template <int k> __device__ __forceinline__ void get(float (&v)[4]) const { decode4(q[k], row16_bcast<kPer * k>(s), v); }
+    template <int k> __device__ __forceinline__ void take(float (&v)[kV]) {
+        asm volatile("" : "+v"(q[k]));
+        decode(q[k], row16_bcast<kPer * k>(s), v);
+    }
 };
 
-// Writes the 8-bit checkpoint of a lane's K = 4 quads.  The magnitudes of the 4
-// tokens are reduced over the 16 lanes by halving: at each of the first two
-// steps a lane keeps half of its tokens and takes the partner's values for them
-// (5 exchanges in place of 4 four-step reductions), after which lanes 4 k .. 4 k
-// + 3 of the row hold token k's, do its two divisions once, and the scales of
-// the wave's 16 tokens are one contiguous store.
-template <typename T, bool ALIGNED, int K>
-__device__ __forceinline__ void save_packed(const LaneIn<T, ALIGNED, false, K>& in, const Packed& p, int64_t row_tok,
-                                            int tok, int nv, int c, int dim, int ct, int64_t rows) {
-    static_assert(K == 4, "the halving below is written for four tokens");
+// Writes the 8-bit checkpoint of a lane's K = 8 pairs.  The magnitudes of the 8
+// tokens are reduced over a DPP row of 16 lanes by halving: at each of three steps
+// a lane keeps half of its tokens and takes its partner's values for them (7
+// exchanges in place of 8 four-step reductions); two more steps join the lanes and
+// the token's other 16.  Lanes 2 k and 2 k + 1 of a row then hold token k's, do
+// its division once, and the scales of the wave's 16 tokens are one contiguous
+// store.
+template <typename T, bool ALIGNED, int K, typename P>
+__device__ __forceinline__ void save_packed(const LaneIn<T, ALIGNED, false, K>& in, const P& p, const Tile& t,
+                                            int tok, int c, int dim, int64_t rows) {
+    static_assert(K == 8, "the halving below is written for eight tokens");
     const int li = threadIdx.x & 15;
-    uint32_t m[4];
-    static_for<4>([&](auto kc) {
+    uint32_t m[8], keep[kV];   // magnitude bits of the channels that exist
+#pragma unroll
+    for (int j = 0; j < kV; ++j) keep[j] = c + j < dim ? 0x7fffffffu : 0u;
+    static_for<8>([&](auto kc) {
         constexpr int k = decltype(kc)::value;
-        float v[4];
+        float v[kV];
         in.template get<k>(v);
         m[k] = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t b = __float_as_uint(v[j]) & 0x7fffffffu;
-            if (ALIGNED || c + j < dim) m[k] = b > m[k] ? b : m[k];
+        for (int j = 0; j < kV; ++j) {
+            const uint32_t b = __float_as_uint(v[j]) & keep[j];
+            m[k] = b > m[k] ? b : m[k];
         }
-        if (ALIGNED && c >= dim) m[k] = 0;
     });
     auto umax = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
-    const bool b3 = li & 8, b2 = li & 4;
-    uint32_t m2[2];
+    const bool b3 = li & 8, b2 = li & 4, b1 = li & 2;
+    uint32_t m4[4], m2[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-        m2[k] = umax(b3 ? m[k + 2] : m[k], dpp_u32<0x128>(b3 ? m[k] : m[k + 2]));   // row_ror:8
-    // row_half_mirror: lane i of a half-row reads lane 7 - i, in its other quad
-    uint32_t m1 = umax(b2 ? m2[1] : m2[0], dpp_u32<0x141>(b2 ? m2[0] : m2[1]));
-    m1 = umax(m1, dpp_u32<0x4E>(m1));   // quad_perm [2, 3, 0, 1]
-    m1 = umax(m1, dpp_u32<0xB1>(m1));   // quad_perm [1, 0, 3, 2]
+    for (int k = 0; k < 4; ++k) m4[k] = umax(b3 ? m[k + 4] : m[k], dpp_u32<0x128>(b3 ? m[k] : m[k + 4]));   // row_ror:8
+#pragma unroll
+    for (int k = 0; k < 2; ++k)   // row_half_mirror: lane i of a half-row reads lane 7 - i, in its other quad
+        m2[k] = umax(b2 ? m4[k + 2] : m4[k], dpp_u32<0x141>(b2 ? m4[k] : m4[k + 2]));
+    uint32_t m1 = umax(b1 ? m2[1] : m2[0], dpp_u32<0x4E>(b1 ? m2[0] : m2[1]));   // quad_perm [2, 3, 0, 1]
+    m1 = umax(m1, dpp_u32<0xB1>(m1));                                            // quad_perm [1, 0, 3, 2]
+    m1 = umax(m1, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m1), 16)));
     float scale, inv;
     block_scale(m1, scale, inv);
-    const int t_sc = tok + (li >> 2);
-    if ((li & 3) == 0 && t_sc < nv) p.scale[ct * rows + row_tok + t_sc] = scale;
-    int8_t* base = p.q + row_tok * dim;
-    static_for<4>([&](auto kc) {
+    const Rsrc ss = tile_rsrc(p.scale + t.ct * rows + t.row_tok, t.nv * 4);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(scale), ss,
+                                          (threadIdx.x & 17) == 0 ? 4 * (tok + (li >> 1)) : kNoStore, 0, 0);
+    const Rsrc rs = rows_rsrc<1>(p.q, t.row_tok, t.nv, dim, dim);
+    uint32_t off = store_offset(tok, dim, c, c < dim);
+    static_for<8>([&](auto kc) {
         constexpr int k = decltype(kc)::value;
-        float v[4];
+        float v[kV];
         in.template get<k>(v);
-        const uint32_t w = encode4(v, row16_bcast<4 * k>(inv));
-        if (tok + k < nv)
-            store_codes<ALIGNED>(base, static_cast<uint32_t>(tok + k) * static_cast<uint32_t>(dim), c, dim, w);
+        store_codes<kV, ALIGNED>(rs, off, dim - c, encode(v, row16_bcast<2 * k>(inv)));
+        off = next_offset(off, dim);
     });
 }
 
+// Joining the tiles of a chain (one row, 64 channels) in one pass over the data.
+// Tiles are taken in order (position 0, 1, ... of a chain: from the left in the
+// forward, from the right in the backward).  Each publishes its composed map as
+// soon as it has it, then finds the value entering it from the nearest earlier
+// position whose outgoing value is published, applying the maps in between in
+// order.  That is the operation sequence of the tiles' own outgoing values, so
+// the result does not depend on how far a tile had to look.
+//
+// Every word is published by one relaxed agent-scope atomic store and read by
+// relaxed agent-scope atomic loads: a map is one 64-bit word (P, H), a value one
+// 32-bit word, and all bits set means "not there yet" (the launch clears the words
+// first; a NaN with that pattern is stored as the usual one).
+//
+// Every wait ends: workgroups draw tiles by tickets, position by position over the
+// chains of a group, and work on them in the order drawn.  The positions a
+// workgroup waits for have lower tickets: of the tickets not yet worked off, the
+// lowest is the current one of a workgroup that runs, and all that it waits for is
+// published.  Against a workspace that another call overwrites meanwhile (which
+// the caller has to exclude) the wait is bounded too: after kMaxPolls, seconds,
+// the value is NaN.
+struct Chain {
+    uint64_t* map;     // [chain][position][64]
+    uint32_t* value;   // [chain][position][64]
+    uint32_t* next;    // [group]: tickets drawn
+    const float* rate; // [64 * channel tiles]: -c log2(e) softplus(a_param)
+};
+
+// Chains in groups by chain % groups, each group with its own ticket counter and
+// the workgroups of one blockIdx % 8 (one XCD, as they are dealt out): as many
+// groups, up to 8, as divide the chains evenly.
+__host__ __device__ inline int chain_groups(int64_t nchain) {
+    return nchain % 8 == 0 ? 8 : nchain % 4 == 0 ? 4 : nchain % 2 == 0 ? 2 : 1;
+}
+
+constexpr int kLook = 4;             // earlier positions looked at
+constexpr int kMaxPolls = 1 << 22;   // about a microsecond each
+
+__device__ __forceinline__ uint32_t not_all_ones(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return b == 0xffffffffu ? 0x7fc00000u : b;
+}
+
+__device__ __forceinline__ void publish_map(uint64_t* p, float P, float H) {
+    const uint64_t w = (static_cast<uint64_t>(not_all_ones(H)) << 32) | __float_as_uint(P);
+    __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void publish_value(uint32_t* p, float v) {
+    __hip_atomic_store(p, not_all_ones(v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The value entering position `pos` for the lane's channel; `map` and `value` point
+// at the channel's word of position 0, `first` enters position 0.  All 64 lanes.
+__device__ __forceinline__ float look_back(const uint64_t* map, const uint32_t* value, int pos, float first) {
+    uint32_t v[kLook];
+    uint64_t m[kLook];
+#pragma unroll
+    for (int k = 0; k < kLook; ++k) {
+        v[k] = 0xffffffffu;
+        m[k] = ~0ull;
+    }
+    for (int polls = 0; polls < kMaxPolls; ++polls) {
+#pragma unroll
+        for (int k = 0; k < kLook; ++k) {
+            const int p = pos - 1 - k;
+            if (p < 0) {
+                if (p == -1) v[k] = not_all_ones(first);
+            } else {   // read again until every lane has its word
+                if (__any(v[k] == 0xffffffffu))
+                    v[k] = __hip_atomic_load(value + static_cast<int64_t>(p) * kTileChannels, __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT);
+                if (k < kLook - 1 && __any(m[k] == ~0ull))
+                    m[k] = __hip_atomic_load(map + static_cast<int64_t>(p) * kTileChannels, __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT);
+            }
+        }
+        bool ok = false;
+        float c = 0.0f;
+#pragma unroll
+        for (int k = kLook - 1; k >= 0; --k) {
+            const float through = apply(__uint_as_float(static_cast<uint32_t>(m[k])),
+                                        __uint_as_float(static_cast<uint32_t>(m[k] >> 32)), c);
+            const bool there = v[k] != 0xffffffffu;
+            c = there ? __uint_as_float(v[k]) : through;
+            ok = there || (ok && m[k] != ~0ull);
+        }
+        if (__all(ok)) return c;
+        __builtin_amdgcn_s_sleep(1);
+    }
+    return __uint_as_float(0x7fc00000u);
+}
+
+// The tiles a workgroup draws: tickets of its group, position by position over the
+// group's chains.
+struct Walk {
+    int nct, ntiles, groups, group, per_group, tickets;
+    __device__ __forceinline__ void init(int nct_, int ntiles_, int batch) {
+        nct = nct_;
+        ntiles = ntiles_;
+        groups = ntiles > 1 ? chain_groups(static_cast<int64_t>(nct) * batch) : 1;
+        group = static_cast<int>(blockIdx.x) % groups;
+        per_group = nct * batch / groups;
+        tickets = per_group * ntiles;
+    }
+    // By a whole wave: lane 0 adds 1 at agent scope, the other lanes' offsets lie
+    // past the counter.
+    __device__ __forceinline__ int draw(uint32_t* next) const {
+        constexpr int kAgentScope = 16;   // the cache-policy bit of device scope
+        const Rsrc rs = tile_rsrc(next + group, 4);
+        return __builtin_amdgcn_readfirstlane(__builtin_amdgcn_raw_ptr_buffer_atomic_add_i32(
+            1, rs, (threadIdx.x & 63) == 0 ? 0u : kNoStore, 0, kAgentScope));
+    }
+    // The tile of a ticket, counted from the row's end with REVERSE; of no tokens
+    // past the last ticket.
+    template <bool REVERSE>
+    __device__ __forceinline__ Tile place(int ticket, int64_t seqlen) const {
+        Tile t;
+        const int chain = group + groups * (ticket % per_group);
+        t.pos = ticket / per_group;
+        t.tile = REVERSE ? ntiles - 1 - t.pos : t.pos;
+        t.ct = chain % nct;
+        t.b = chain / nct;
+        const int64_t t0 = static_cast<int64_t>(t.tile) * kTileTokens;
+        const int64_t left = seqlen - t0;
+        t.row_tok = t.b * seqlen + t0;
+        t.nv = t.pos >= ntiles || left < 0 ? 0 : left < kTileTokens ? static_cast<int>(left) : kTileTokens;
+        return t;
+    }
+    // A channel's word of position 0 in the chain's arrays.
+    __device__ __forceinline__ int64_t word(const Tile& t, int channel) const {
+        return (t.b * nct + t.ct) * ntiles * kTileChannels + channel;
+    }
+};
+
 }  // namespace rec
+
+// The chains' words in a launch's workspace (recurrence_workspace_bytes), cleared on
+// the stream, and the rates (recurrence.hip).  Nothing for rows of one tile.
+hipError_t clear_chains(void* ws, int64_t batch, int64_t dim, int64_t ntiles, const float* a_param, float c,
+                        rec::Chain* ch, hipStream_t stream);
 }  // namespace mamba

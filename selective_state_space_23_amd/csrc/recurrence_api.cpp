@@ -139,13 +139,13 @@ int mamba_activation_unpack(const int8_t* q, const float* scale, void* out, int6
     return hip_status(mamba::launch_unpack(a));
 }
 
-int mamba_gated_recurrence_workspace_bytes(const mamba_recurrence_dims_t* dims, int32_t have_states, size_t* bytes) {
+int mamba_gated_recurrence_workspace_bytes(const mamba_recurrence_dims_t* dims, size_t* bytes) {
     if (!bytes) return MAMBA_ERR_INVALID_ARGUMENT;
     *bytes = 0;
     const int st = check_rec_dims(dims);
     if (st != MAMBA_OK) return st;
     if (dims->batch * dims->dim != 0)
-        *bytes = mamba::recurrence_workspace_bytes(dims->batch, dims->seqlen, dims->dim, have_states != 0);
+        *bytes = mamba::recurrence_workspace_bytes(dims->batch, dims->seqlen, dims->dim);
     return MAMBA_OK;
 }
 
@@ -171,14 +171,14 @@ int mamba_gated_recurrence_fwd(const mamba_recurrence_dims_t* dims, const void* 
     if (!aligned(x, esz) || !aligned(gate_a, esz) || !aligned(gate_x, esz) || (z && !aligned(z, esz)) ||
         !aligned(out, esz) || !aligned(a_param, 4))
         return MAMBA_ERR_MISALIGNED;
-    const size_t need = mamba::recurrence_workspace_bytes(B, L, D, states != nullptr);
+    const size_t need = mamba::recurrence_workspace_bytes(B, L, D);
     if (need && (!workspace || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
     if (need && !aligned(workspace, 256)) return MAMBA_ERR_MISALIGNED;
     mamba::RecFwdArgs a{};
-    a.ld_x = dims->ld_x ? dims->ld_x : D;
-    a.ld_a = dims->ld_gate_a ? dims->ld_gate_a : D;
-    a.ld_g = dims->ld_gate_x ? dims->ld_gate_x : D;
-    a.ld_z = dims->ld_z ? dims->ld_z : D;
+    a.ld_x = static_cast<int>(dims->ld_x ? dims->ld_x : D);
+    a.ld_a = static_cast<int>(dims->ld_gate_a ? dims->ld_gate_a : D);
+    a.ld_g = static_cast<int>(dims->ld_gate_x ? dims->ld_gate_x : D);
+    a.ld_z = static_cast<int>(dims->ld_z ? dims->ld_z : D);
     const int64_t rows = B * L;
     const size_t scb = static_cast<size_t>(rows * ceil_div(D, mamba::kPackBlock)) * 4;
     const size_t qb = static_cast<size_t>(rows * D);
@@ -259,11 +259,11 @@ int mamba_gated_recurrence_bwd(const mamba_recurrence_dims_t* dims, const void* 
     if (!workspace || workspace_bytes < need) return MAMBA_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return MAMBA_ERR_MISALIGNED;
     mamba::RecBwdArgs a{};
-    a.ld_x = dims->ld_x ? dims->ld_x : D;
-    a.ld_a = dims->ld_gate_a ? dims->ld_gate_a : D;
-    a.ld_g = dims->ld_gate_x ? dims->ld_gate_x : D;
-    a.ld_z = dims->ld_z ? dims->ld_z : D;
-    a.ld_o = dims->ld_dout ? dims->ld_dout : D;
+    a.ld_x = static_cast<int>(dims->ld_x ? dims->ld_x : D);
+    a.ld_a = static_cast<int>(dims->ld_gate_a ? dims->ld_gate_a : D);
+    a.ld_g = static_cast<int>(dims->ld_gate_x ? dims->ld_gate_x : D);
+    a.ld_z = static_cast<int>(dims->ld_z ? dims->ld_z : D);
+    a.ld_o = static_cast<int>(dims->ld_dout ? dims->ld_dout : D);
     const int64_t rows = B * L;
     const size_t scb = static_cast<size_t>(rows * ceil_div(D, mamba::kPackBlock)) * 4;
     const size_t qb = static_cast<size_t>(rows * D);
@@ -318,10 +318,10 @@ int mamba_gated_recurrence_update(const mamba_recurrence_dims_t* dims, float* st
         (z && !aligned(z, esz)) || !aligned(out, esz) || !aligned(a_param, 4))
         return MAMBA_ERR_MISALIGNED;
     mamba::RecUpdateArgs a{};
-    a.ld_x = dims->ld_x ? dims->ld_x : D;
-    a.ld_a = dims->ld_gate_a ? dims->ld_gate_a : D;
-    a.ld_g = dims->ld_gate_x ? dims->ld_gate_x : D;
-    a.ld_z = dims->ld_z ? dims->ld_z : D;
+    a.ld_x = static_cast<int>(dims->ld_x ? dims->ld_x : D);
+    a.ld_a = static_cast<int>(dims->ld_gate_a ? dims->ld_gate_a : D);
+    a.ld_g = static_cast<int>(dims->ld_gate_x ? dims->ld_gate_x : D);
+    a.ld_z = static_cast<int>(dims->ld_z ? dims->ld_z : D);
     const Span ins[] = {{x, span(B, D, a.ld_x, esz)}, {gate_a, span(B, D, a.ld_a, esz)},
                         {gate_x, span(B, D, a.ld_g, esz)}, {z, span(B, D, a.ld_z, esz)},
                         {a_param, static_cast<size_t>(D) * 4}, {reset, static_cast<size_t>(B)}};

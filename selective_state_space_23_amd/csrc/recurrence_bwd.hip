@@ -23,254 +23,282 @@ namespace {
 
 using namespace rec;
 
-constexpr int kK = 4;
-constexpr int kWaves = kTileTokens / (4 * kK);
+constexpr int kK = 4;                              // tokens a lane walks
+constexpr int kWaves = kTileTokens / (2 * kK);     // two halves of 32 lanes a wave
 constexpr int kThreads = kWaves * 64;
 
-enum { kAggregate = 0, kOutput = 1 };
+struct RecBwdKernelArgs {
+    RecBwdArgs a;
+    Chain ch;
+    float* part;       // (B * tiles, D): sum of r dlog a over a tile
+    int nct, ntiles;
+};
 
-__device__ __forceinline__ float silu_grad(float z, float sg) { return sg * __builtin_fmaf(z, 1.0f - sg, 1.0f); }
-
-// kAggregate writes the tile's adjoint map (P, X) per channel; kOutput starts
-// from the adjoint entering the tile from the right (adj) and writes the
-// gradients and the tile's part of sum r dlog a.
-template <typename T, bool ALIGNED, bool PIN, bool HAS_Z, int MODE>
-__global__ __launch_bounds__(kThreads, MODE == kOutput ? 2 : 4) void rec_bwd_kernel(const RecBwdArgs a, int nct, int ntiles,
-                                                              float2* __restrict__ agg,
-                                                              const float* __restrict__ adj,
-                                                              float* __restrict__ part) {
-    __shared__ float s_k2[kTileChannels];
-    __shared__ float s_P[kWaves][kTileChannels], s_H[kWaves][kTileChannels], s_X[kWaves][kTileChannels];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int li = lane & 15, ts = lane >> 4;
-    const unsigned nchain = static_cast<unsigned>(nct) * static_cast<unsigned>(a.batch);
-    const unsigned chain = blockIdx.x % nchain;
-    const int tile = ntiles - 1 - static_cast<int>(blockIdx.x / nchain);
-    const int ct = static_cast<int>(chain % static_cast<unsigned>(nct));
-    const int64_t b = chain / static_cast<unsigned>(nct);
-    const int dim = static_cast<int>(a.dim);
-    const int64_t t0 = static_cast<int64_t>(tile) * kTileTokens;
-    const int64_t row_tok = b * a.seqlen + t0;
-    const int64_t left = a.seqlen - t0;
-    const int nv = left < kTileTokens ? static_cast<int>(left) : kTileTokens;
-    const int tok = (wave * 4 + ts) * kK;
-    const int c = ct * kTileChannels + 4 * li;
-    const int c_ld = ALIGNED ? (c < dim ? c : dim - 4) : c;
-    const int64_t rows = a.batch * a.seqlen;
+// One pass over the data, from the row ends back.  A workgroup works off tiles as
+// the forward does; everything the gradients need of a token is formed once
+// (seven values a channel and token stay in registers) before the adjoint
+// entering the tile is known, and the next tile's inputs are loaded meanwhile.
+template <typename T, bool ALIGNED, bool PIN, bool HAS_Z>
+__global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArgs) {
+    __shared__ float s_rate[kTileChannels];
+    // the last row of an array takes what no one reads
+    __shared__ float s_P[kWaves + 1][kTileChannels], s_H[kWaves + 1][kTileChannels], s_X[kWaves + 1][kTileChannels];
+    __shared__ float s_in[kWaves][kTileChannels], s_adj[kWaves][kTileChannels], s_sum[kWaves + 1][kTileChannels];
+    __shared__ int s_ticket;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int li = lane % kRow, half = lane / kRow;
+    const auto first = kernel_args<RecBwdKernelArgs>();
+    const int dim = static_cast<int>(first->a.dim), nct = first->nct, ntiles = first->ntiles;
+    const int tok = (wave * 2 + half) * kK;
+    Walk walk;
+    walk.init(nct, ntiles, static_cast<int>(first->a.batch));
+    auto draw = [&]() { return walk.draw(kernel_args<RecBwdKernelArgs>()->ch.next); };
+    auto place = [&](int ticket) { return walk.place<true>(ticket, kernel_args<RecBwdKernelArgs>()->a.seqlen); };
 
     LaneIn<T, ALIGNED, PIN, kK> xi, ai, gi, zi;
     LaneIn<T, ALIGNED, false, kK> oi;
-    ai.load(a.gate_a, a.in[1], row_tok, a.ld_a, tok, nv, c_ld, dim, ct, rows);
-    oi.load(a.dout, a.in[0], row_tok, a.ld_o, tok, nv, c_ld, dim, ct, rows);
-    if constexpr (HAS_Z) zi.load(a.z, a.in[3], row_tok, a.ld_z, tok, nv, c_ld, dim, ct, rows);
-    if constexpr (MODE == kOutput) {
-        gi.load(a.gate_x, a.in[2], row_tok, a.ld_g, tok, nv, c_ld, dim, ct, rows);
-        xi.load(a.x, a.in[0], row_tok, a.ld_x, tok, nv, c_ld, dim, ct, rows);
-    }
-    const TileStarts starts = tile_starts(a.doc_start, b * a.seqlen, t0, a.seqlen);
-    if (threadIdx.x < kTileChannels) {
-        const int d = ct * kTileChannels + threadIdx.x;
-        s_k2[threadIdx.x] = -a.c * softplus_exact(a.a_param[d < dim ? d : dim - 1]);
-    }
-    lds_barrier();
-    float kc4[4];   // -c softplus(a_param)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) kc4[j] = s_k2[4 * li + j];
+    StartFlags fl;
+    float rate[kV];
+    auto fetch = [&](const Tile& t) {
+        const int c = t.ct * kTileChannels + kV * li;
+        const auto p = kernel_args<RecBwdKernelArgs>();
+        const auto& a = p->a;
+        const int64_t rows = a.batch * a.seqlen;
+        ai.load(a.gate_a, a.in[1], t, a.ld_a, tok, c, dim, rows);
+        gi.load(a.gate_x, a.in[2], t, a.ld_g, tok, c, dim, rows);
+        xi.load(a.x, a.in[0], t, a.ld_x, tok, c, dim, rows);
+        oi.load(a.dout, a.in[0], t, a.ld_o, tok, c, dim, rows);
+        if constexpr (HAS_Z) zi.load(a.z, a.in[3], t, a.ld_z, tok, c, dim, rows);
+        fl.load(a.doc_start, t.row_tok, t.nv);
+        if (ntiles > 1) {
+            const float2 r = *reinterpret_cast<const float2*>(p->ch.rate + c);   // padded to whole channel tiles
+            rate[0] = r.x; rate[1] = r.y;
+        }
+    };
 
-    auto body = [&](auto gen) {
-        constexpr bool GEN = decltype(gen)::value;
-        const uint32_t st = GEN ? starts.bits(tok, kK) : 0u;
-        float A[kK][4], B[kK][4];     // effective decays, inputs
-        float P[4], H[4], X[4];
-        static_for<kK>([&](auto kc) {
-            constexpr int k = decltype(kc)::value;
-            float ga[4], gx[4], x[4], dy[4], z[4];
-            ai.template get<k>(ga);
-            oi.template get<k>(dy);
-            if constexpr (HAS_Z) zi.template get<k>(z);
-            if constexpr (MODE == kOutput) {
-                gi.template get<k>(gx);
-                xi.template get<k>(x);
-            }
-            const bool start = GEN && ((st >> k) & 1u), out = GEN && tok + k >= nv;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float al, om = 0.0f, bb = 0.0f;
-                if constexpr (MODE == kOutput) {
-                    decay_terms(kc4[j] * kLog2e * sigmoid_f(ga[j]), al, om);
-                    bb = __builtin_amdgcn_sqrtf(om) * (sigmoid_f(gx[j]) * x[j]);
-                } else {
-                    al = exp2_fast(kc4[j] * kLog2e * sigmoid_f(ga[j]));
-                }
-                if constexpr (HAS_Z) dy[j] *= silu_f(z[j]);
-                if constexpr (GEN) {
-                    al = out ? 1.0f : al;
-                    bb = out ? 0.0f : bb;
-                    dy[j] = out ? 0.0f : dy[j];
-                }
-                A[k][j] = al;
-                B[k][j] = bb;
-                if constexpr (k == 0) {
-                    P[j] = start ? -0.0f : al;
-                    H[j] = bb;
-                    X[j] = start ? 0.0f : al * dy[j];
-                } else {
-                    P[j] = start ? -0.0f : P[j] * al;
-                    H[j] = start ? bb : __builtin_fmaf(al, H[j], bb);
-                    X[j] = GEN && is_reset(P[j]) ? X[j] : __builtin_fmaf(P[j], dy[j], X[j]);
-                }
-            }
-        });
-        // prefixes (forward) and suffixes (adjoint) over the wave's four groups
-        float fp[4], fh[4], rp[4], rx[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float p = P[j], x = X[j];
-            float p1 = __shfl_down(p, 16), x1 = __shfl_down(x, 16);
-            if (ts <= 2) { x = apply(p, x, x1); p = is_reset(p) ? p : p * p1; }
-            p1 = __shfl_down(p, 32); x1 = __shfl_down(x, 32);
-            if (ts <= 1) { x = apply(p, x, x1); p = is_reset(p) ? p : p * p1; }
-            if (ts == 0) {
-                s_P[wave][4 * li + j] = p;
-                s_X[wave][4 * li + j] = x;
-            }
-            p1 = __shfl_down(p, 16); x1 = __shfl_down(x, 16);
-            rp[j] = ts <= 2 ? p1 : 1.0f;
-            rx[j] = ts <= 2 ? x1 : 0.0f;
-            if constexpr (MODE == kOutput) {
-                p = P[j];
-                float h = H[j];
-                p1 = __shfl_up(p, 16);
-                float h1 = __shfl_up(h, 16);
-                if (ts >= 1) compose(p, h, p1, h1);
-                p1 = __shfl_up(p, 32); h1 = __shfl_up(h, 32);
-                if (ts >= 2) compose(p, h, p1, h1);
-                if (ts == 3) s_H[wave][4 * li + j] = h;
-                p1 = __shfl_up(p, 16); h1 = __shfl_up(h, 16);
-                fp[j] = ts >= 1 ? p1 : 1.0f;
-                fh[j] = ts >= 1 ? h1 : 0.0f;
-            }
+    int cur, next;
+    if (ntiles > 1) {
+        if (wave == 0) s_ticket = draw();
+        lds_barrier();
+        cur = __builtin_amdgcn_readfirstlane(s_ticket);
+        lds_barrier();
+        if (wave == 0) s_ticket = draw();
+        if (cur >= walk.tickets) return;
+        fetch(place(cur));
+        lds_barrier();
+        next = __builtin_amdgcn_readfirstlane(s_ticket);
+        lds_barrier();
+    } else {
+        cur = static_cast<int>(blockIdx.x);
+        next = 0x7fffffff;
+        const Tile t = place(cur);
+        fetch(t);
+        if (threadIdx.x < kTileChannels) {
+            const int d = t.ct * kTileChannels + threadIdx.x;
+            s_rate[threadIdx.x] = -first->a.c * kLog2e * softplus_exact(first->a.a_param[d < dim ? d : dim - 1]);
         }
         lds_barrier();
-        if constexpr (MODE == kAggregate) {
-            if (threadIdx.x < kTileChannels) {
-                float p = s_P[kWaves - 1][threadIdx.x], x = s_X[kWaves - 1][threadIdx.x];
 #pragma unroll
-                for (int w = kWaves - 2; w >= 0; --w) {
-                    const float pl = s_P[w][threadIdx.x];
-                    x = apply(pl, s_X[w][threadIdx.x], x);
-                    p = is_reset(pl) ? pl : pl * p;
-                }
-                const int d = ct * kTileChannels + threadIdx.x;
-                if (d < dim) agg[(b * ntiles + tile) * a.dim + d] = make_float2(p, x);
-            }
-            return;
-        } else {
-            float hp[kK][4], e[4], sum[4];
+        for (int j = 0; j < kV; ++j) rate[j] = s_rate[kV * li + j];
+    }
+
+    // A tile's part of sum r dlog a: its waves' sums added by one wave behind the
+    // next barrier.
+    int64_t part_row = -1;
+    int part_channel = 0;
+    auto add_part = [&]() {
+        if (part_row < 0) return;
+        float s = 0.0f;
+#pragma unroll 4
+        for (int w = 0; w < kWaves; ++w) s += s_sum[w][lane];
+        row_store(kernel_args<RecBwdKernelArgs>()->part, part_row, dim, part_channel + lane, s);
+    };
+
+    for (;;) {
+        const Tile t = place(cur);
+        const int c = t.ct * kTileChannels + kV * li;
+        const TileStarts starts = fl.starts();
+        const bool general = starts.any() || t.nv < kTileTokens;   // the same in the whole workgroup
+        const uint32_t st = starts.bits(tok, kK);
+        float kc[kV];   // -c softplus(a_param)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int d = c + j < dim ? c + j : dim - 1;
-                float h = a.states != nullptr ? a.states[(b * ntiles + tile) * a.dim + d]
-                                              : (a.initial_state != nullptr ? a.initial_state[b * a.dim + d] : 0.0f);
-                for (int w = 0; w < wave; ++w) h = apply(s_P[w][4 * li + j], s_H[w][4 * li + j], h);
-                h = apply(fp[j], fh[j], h);
+        for (int j = 0; j < kV; ++j) kc[j] = kLn2 * rate[j];
+        // Of every token: a, r, w v, w i, 1 - i, (r / w) a^2 v, dy and dout silu'(z).
+        float A[kK][kV], R[kK][kV], B[kK][kV], W[kK][kV], O[kK][kV], U[kK][kV], Y[kK][kV], Z[kK][kV];
+        float P[kV], H[kV], X[kV];
+        auto maps = [&](auto gen) {
+            constexpr bool GEN = decltype(gen)::value;
+            static_for<kK>([&](auto kcc) {
+                constexpr int k = decltype(kcc)::value;
+                float ga[kV], gx[kV], x[kV], z[kV];
+                ai.template take<k>(ga);
+                gi.template take<k>(gx);
+                xi.template take<k>(x);
+                oi.template take<k>(Y[k]);
+                if constexpr (HAS_Z) zi.template take<k>(z);
+                const bool start = GEN && ((st >> k) & 1u), out = GEN && tok + k >= t.nv;
 #pragma unroll
-                for (int k = 0; k < kK; ++k) {
-                    hp[k][j] = h;
-                    h = GEN && ((st >> k) & 1u) ? B[k][j] : __builtin_fmaf(A[k][j], h, B[k][j]);
-                }
-                e[j] = ntiles > 1 ? adj[(b * ntiles + tile) * a.dim + d]
-                                  : (a.d_final_state != nullptr ? a.d_final_state[b * a.dim + d] : 0.0f);
-                for (int w = kWaves - 1; w > wave; --w) e[j] = apply(s_P[w][4 * li + j], s_X[w][4 * li + j], e[j]);
-                e[j] = apply(rp[j], rx[j], e[j]);
-                sum[j] = 0.0f;
-            }
-            const int64_t ob = row_tok * a.dim * Elem<T>::kBytes;
-            static_for<kK>([&](auto kc) {
-                constexpr int k = kK - 1 - decltype(kc)::value;
-                float ga[4], gx[4], x[4], dy[4], z[4], dx[4], da[4], dg[4], dz[4];
-                ai.template get<k>(ga);
-                gi.template get<k>(gx);
-                xi.template get<k>(x);
-                oi.template get<k>(dy);
-                if constexpr (HAS_Z) zi.template get<k>(z);
-                const bool start = GEN && ((st >> k) & 1u), out = GEN && tok + k >= nv;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < kV; ++j) {
                     const float r = sigmoid_f(ga[j]);
                     float al, om;
-                    decay_terms(kc4[j] * kLog2e * r, al, om);
-                    const float rw = om >= 0x1p-126f ? __builtin_amdgcn_rsqf(om) : 0.0f;   // denormals count as 0
+                    decay_terms(rate[j] * r, al, om);
+                    float rw = __builtin_amdgcn_rsqf(om);
+                    asm volatile("" : "+v"(rw));
+                    rw = om >= 0x1p-126f ? rw : 0.0f;   // denormals count as 0
                     const float w = om * rw;
                     const float ig = sigmoid_f(gx[j]);
                     const float v = ig * x[j];
-                    const float ah = start ? 0.0f : A[k][j] * hp[k][j];
                     if constexpr (HAS_Z) {
                         const float sg = sigmoid_f(z[j]);
-                        dz[j] = dy[j] * (start ? B[k][j] : ah + B[k][j]) * silu_grad(z[j], sg);
-                        dy[j] *= z[j] * sg;
+                        Z[k][j] = Y[k][j] * (sg * __builtin_fmaf(z[j], 1.0f - sg, 1.0f));
+                        Y[k][j] *= z[j] * sg;
                     }
-                    if constexpr (GEN) dy[j] = out ? 0.0f : dy[j];
-                    const float G = dy[j] + e[j];
-                    const float gw = G * w;
-                    dx[j] = gw * ig;
-                    dg[j] = gw * v * (1.0f - ig);
-                    const float q = G * r * (ah - rw * (al * al) * v);
-                    da[j] = kc4[j] * (1.0f - r) * q;
-                    sum[j] += out ? 0.0f : q;
-                    e[j] = start ? 0.0f : A[k][j] * G;
+                    R[k][j] = r;
+                    W[k][j] = w * ig;
+                    O[k][j] = 1.0f - ig;
+                    U[k][j] = (r * rw) * (al * al) * v;
+                    float bb = w * v;
+                    if constexpr (GEN) {
+                        al = out ? 1.0f : al;
+                        bb = out ? 0.0f : bb;
+                        Y[k][j] = out ? 0.0f : Y[k][j];
+                    }
+                    A[k][j] = al;
+                    B[k][j] = bb;
+                    if constexpr (k == 0) {
+                        P[j] = start ? -0.0f : al;
+                        H[j] = bb;
+                        X[j] = start ? 0.0f : al * Y[k][j];
+                    } else {
+                        P[j] = start ? -0.0f : P[j] * al;
+                        H[j] = start ? bb : __builtin_fmaf(al, H[j], bb);
+                        X[j] = apply<GEN>(P[j], X[j], Y[k][j]);
+                    }
                 }
-                if (!GEN || !out) {
-                    const uint32_t to = static_cast<uint32_t>(tok + k) * static_cast<uint32_t>(dim);
-                    store4<T, ALIGNED>(static_cast<char*>(a.dx) + ob, to, c, dim, dx);
-                    store4<T, ALIGNED>(static_cast<char*>(a.dgate_a) + ob, to, c, dim, da);
-                    store4<T, ALIGNED>(static_cast<char*>(a.dgate_x) + ob, to, c, dim, dg);
-                    if constexpr (HAS_Z) store4<T, ALIGNED>(static_cast<char*>(a.dz) + ob, to, c, dim, dz);
-                }
+                __builtin_amdgcn_sched_barrier(0);
             });
-            if (tile == 0 && wave == 0 && ts == 0 && a.d_initial_state != nullptr) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (c + j < dim) a.d_initial_state[b * a.dim + c + j] = e[j];
-            }
-            lds_barrier();   // s_P is read above
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                sum[j] += __shfl_xor(sum[j], 16);
-                sum[j] += __shfl_xor(sum[j], 32);
-                if (ts == 0) s_P[wave][4 * li + j] = sum[j];
-            }
-            lds_barrier();
-            if (threadIdx.x < kTileChannels) {
-                float s = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w) s += s_P[w][threadIdx.x];
-                const int d = ct * kTileChannels + threadIdx.x;
-                if (d < dim) part[(b * ntiles + tile) * a.dim + d] = s;
-            }
-        }
-    };
-    if (starts.any() || nv < kTileTokens) body(std::true_type{});
-    else body(std::false_type{});
-}
+        };
+        if (general) maps(std::true_type{});
+        else maps(std::false_type{});
 
-// Adjoints entering every tile from the right.
-__global__ __launch_bounds__(256) void rec_bwd_carry_kernel(const float2* __restrict__ agg,
-                                                            const float* __restrict__ d_final_state,
-                                                            float* __restrict__ adj, int64_t batch, int64_t dim,
-                                                            int ntiles) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= batch * dim) return;
-    const int64_t b = i / dim, d = i % dim;
-    float e = d_final_state != nullptr ? d_final_state[i] : 0.0f;
-    const int64_t base = b * ntiles * dim + d;
-    for (int t = ntiles - 1; t >= 0; --t) {
-        adj[base + t * dim] = e;
-        if (t > 0) {
-            const float2 u = agg[base + t * dim];
-            e = apply(u.x, u.y, e);
+        // what the wave's other half does before (forward) or after (adjoint), and the wave's maps
+        float fp[kV], fh[kV], rp[kV], rx[kV];
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            const float p1 = __shfl_xor(P[j], 32), h1 = __shfl_xor(H[j], 32), x1 = __shfl_xor(X[j], 32);
+            const int row = half ? wave : kWaves, rev = half ? kWaves : wave;
+            s_P[row][kV * li + j] = is_reset(P[j]) ? P[j] : P[j] * p1;
+            s_H[row][kV * li + j] = apply(P[j], H[j], h1);
+            s_X[rev][kV * li + j] = apply(P[j], X[j], x1);
+            fp[j] = half ? p1 : 1.0f;   // the first half's map, for the second
+            fh[j] = half ? h1 : 0.0f;
+            rp[j] = half ? 1.0f : p1;   // the second half's adjoint map, for the first
+            rx[j] = half ? 0.0f : x1;
         }
+        lds_barrier();
+        if (wave == 0) {   // a lane per channel: the adjoint entering the tile from the right, and its waves
+            const int d = t.ct * kTileChannels + lane;
+            const auto p = kernel_args<RecBwdKernelArgs>();
+            const auto& a = p->a;
+            const int64_t word = walk.word(t, lane);
+            const int64_t at = word + static_cast<int64_t>(t.pos) * kTileChannels;
+            float e = row_load(a.d_final_state, t.b, a.dim, d);
+            float mp = s_P[kWaves - 1][lane], mx = s_X[kWaves - 1][lane];
+#pragma unroll 4
+            for (int w = kWaves - 2; w >= 0; --w) {
+                const float q = s_P[w][lane];
+                mx = apply(q, s_X[w][lane], mx);
+                mp = is_reset(q) ? q : q * mp;
+            }
+            if (t.pos + 1 < ntiles) publish_map(p->ch.map + at, mp, mx);
+            e = look_back(p->ch.map + word, p->ch.value + word, t.pos, e);
+            const float leaving = apply(mp, mx, e);
+            if (t.pos + 1 < ntiles) publish_value(p->ch.value + at, leaving);
+            if (t.tile == 0) row_store(a.d_initial_state, t.b, a.dim, d, leaving);
+#pragma unroll 4
+            for (int w = kWaves - 1; w >= 0; --w) {
+                s_adj[w][lane] = e;
+                e = apply(s_P[w][lane], s_X[w][lane], e);
+            }
+            if (next < walk.tickets) s_ticket = draw();
+        } else if (wave == 1) {   // the states entering the waves
+            const int d = t.ct * kTileChannels + lane;
+            const auto p = kernel_args<RecBwdKernelArgs>();
+            const auto& a = p->a;
+            float h = a.states != nullptr ? row_load(a.states, t.b * ntiles + t.tile, a.dim, d)
+                                          : row_load(a.initial_state, t.b, a.dim, d);
+#pragma unroll 4
+            for (int w = 0; w < kWaves; ++w) {
+                s_in[w][lane] = h;
+                h = apply(s_P[w][lane], s_H[w][lane], h);
+            }
+        } else if (wave == 2) {
+            add_part();
+            part_row = t.b * ntiles + t.tile;
+            part_channel = t.ct * kTileChannels;
+        }
+        fetch(place(next));   // past the last ticket: a tile of no tokens, nothing is read
+        lds_barrier();
+        {
+            constexpr int esz = Elem<T>::kBytes;
+            const auto p = kernel_args<RecBwdKernelArgs>();
+            const Rsrc to_x = rows_rsrc<esz>(p->a.dx, t.row_tok, t.nv, dim, dim);
+            const Rsrc to_a = rows_rsrc<esz>(p->a.dgate_a, t.row_tok, t.nv, dim, dim);
+            const Rsrc to_g = rows_rsrc<esz>(p->a.dgate_x, t.row_tok, t.nv, dim, dim);
+            const Rsrc to_z = rows_rsrc<esz>(p->a.dz, t.row_tok, HAS_Z ? t.nv : 0, dim, dim);
+            const uint32_t step = static_cast<uint32_t>(dim) * esz;
+            uint32_t off = store_offset(tok + kK - 1, step, c * esz, c < dim);
+            auto put = [&](auto gen) {
+                constexpr bool GEN = decltype(gen)::value;
+                float hp[kK][kV], e[kV], sum[kV];
+#pragma unroll
+                for (int j = 0; j < kV; ++j) {
+                    float h = apply<GEN>(fp[j], fh[j], s_in[wave][kV * li + j]);
+#pragma unroll
+                    for (int k = 0; k < kK; ++k) {
+                        hp[k][j] = h;
+                        h = GEN && ((st >> k) & 1u) ? B[k][j] : __builtin_fmaf(A[k][j], h, B[k][j]);
+                    }
+                    e[j] = apply<GEN>(rp[j], rx[j], s_adj[wave][kV * li + j]);
+                    sum[j] = 0.0f;
+                }
+                static_for<kK>([&](auto kcc) {
+                    constexpr int k = kK - 1 - decltype(kcc)::value;
+                    float dx[kV], da[kV], dg[kV], dz[kV];
+                    const bool start = GEN && ((st >> k) & 1u), out = GEN && tok + k >= t.nv;
+#pragma unroll
+                    for (int j = 0; j < kV; ++j) {
+                        const float G = Y[k][j] + e[j];
+                        const float ah = start ? 0.0f : A[k][j] * hp[k][j];
+                        dx[j] = G * W[k][j];
+                        dg[j] = G * B[k][j] * O[k][j];
+                        const float q = G * __builtin_fmaf(R[k][j], ah, -U[k][j]);
+                        da[j] = kc[j] * (1.0f - R[k][j]) * q;
+                        if constexpr (HAS_Z) dz[j] = Z[k][j] * (ah + B[k][j]);
+                        sum[j] += out ? 0.0f : q;
+                        e[j] = start ? 0.0f : A[k][j] * G;
+                    }
+                    store_vals<T, kV, ALIGNED>(to_x, off, dim - c, dx);
+                    store_vals<T, kV, ALIGNED>(to_a, off, dim - c, da);
+                    store_vals<T, kV, ALIGNED>(to_g, off, dim - c, dg);
+                    if constexpr (HAS_Z) store_vals<T, kV, ALIGNED>(to_z, off, dim - c, dz);
+                    off = next_offset(off, 0u - step);
+                });
+#pragma unroll
+                for (int j = 0; j < kV; ++j) {
+                    sum[j] += __shfl_xor(sum[j], 32);
+                    s_sum[half ? kWaves : wave][kV * li + j] = sum[j];
+                }
+            };
+            if (general) put(std::true_type{});
+            else put(std::false_type{});
+        }
+        if (next >= walk.tickets) break;
+        cur = next;
+        next = __builtin_amdgcn_readfirstlane(s_ticket);   // written before the last barrier
     }
+    lds_barrier();
+    if (wave == 2) add_part();
 }
 
 // da_param (D,): the tiles' parts summed in a fixed order, 16 threads a channel.
@@ -293,8 +321,10 @@ __global__ __launch_bounds__(1024) void rec_bwd_reduce_kernel(const float* __res
     da_param[d] = -c * t * sigmoid_f(a_param[d]);
 }
 
+constexpr int kResident = 256;   // one workgroup of 16 waves a CU
+
 struct BwdWs {
-    size_t agg, adj, part, states, fwd, total;
+    size_t part, chain, states, fwd, total;
 };
 
 BwdWs bwd_ws(int64_t batch, int64_t seqlen, int64_t dim, bool have_states) {
@@ -303,10 +333,9 @@ BwdWs bwd_ws(int64_t batch, int64_t seqlen, int64_t dim, bool have_states) {
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t o = off; off += (bytes + 255) / 256 * 256; return o; };
     w.part = take(n * 4);
-    w.agg = take(n * 8);
-    w.adj = take(n * 4);
+    w.chain = take(recurrence_workspace_bytes(batch, seqlen, dim));
     w.states = take(have_states ? 0 : n * 4);
-    w.fwd = take(have_states ? 0 : recurrence_workspace_bytes(batch, seqlen, dim, true));
+    w.fwd = take(have_states ? 0 : recurrence_workspace_bytes(batch, seqlen, dim));
     w.total = off;
     return w;
 }
@@ -315,13 +344,10 @@ template <typename T, bool ALIGNED, bool PIN, bool HAS_Z>
 hipError_t launch_bwd(const RecBwdArgs& a) {
     const int nct = static_cast<int>((a.dim + kTileChannels - 1) / kTileChannels);
     const int ntiles = static_cast<int>((a.seqlen + kTileTokens - 1) / kTileTokens);
-    const unsigned grid = static_cast<unsigned>(nct) * static_cast<unsigned>(a.batch) * static_cast<unsigned>(ntiles);
+    const int64_t tiles = nct * a.batch * ntiles;
     const BwdWs w = bwd_ws(a.batch, a.seqlen, a.dim, a.states != nullptr);
     char* ws = static_cast<char*>(a.ws);
-    float2* agg = reinterpret_cast<float2*>(ws + w.agg);
-    float* adj = reinterpret_cast<float*>(ws + w.adj);
-    float* part = reinterpret_cast<float*>(ws + w.part);
-    RecBwdArgs b = a;
+    RecBwdKernelArgs k{a, Chain{}, reinterpret_cast<float*>(ws + w.part), nct, ntiles};
     hipError_t e;
     if (a.states == nullptr && ntiles > 1) {
         RecFwdArgs f{};
@@ -334,21 +360,15 @@ hipError_t launch_bwd(const RecBwdArgs& a) {
         f.ld_x = a.ld_x; f.ld_a = a.ld_a; f.ld_g = a.ld_g;
         f.c = a.c; f.bf16 = a.bf16; f.aligned = a.aligned; f.stream = a.stream;
         if ((e = launch_recurrence_fwd(f)) != hipSuccess) return e;
-        b.states = f.states;
+        k.a.states = f.states;
     }
-    if (ntiles > 1) {
-        hipLaunchKernelGGL((rec_bwd_kernel<T, ALIGNED, PIN, HAS_Z, kAggregate>), dim3(grid), dim3(kThreads), 0,
-                           a.stream, b, nct, ntiles, agg, adj, part);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        hipLaunchKernelGGL(rec_bwd_carry_kernel, dim3(static_cast<unsigned>((a.batch * a.dim + 255) / 256)), dim3(256),
-                           0, a.stream, agg, a.d_final_state, adj, a.batch, a.dim, ntiles);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    hipLaunchKernelGGL((rec_bwd_kernel<T, ALIGNED, PIN, HAS_Z, kOutput>), dim3(grid), dim3(kThreads), 0, a.stream, b,
-                       nct, ntiles, agg, adj, part);
+    if ((e = clear_chains(ws + w.chain, a.batch, a.dim, ntiles, a.a_param, a.c, &k.ch, a.stream)) != hipSuccess) return e;
+    const int64_t grid = ntiles > 1 && tiles > kResident ? kResident : tiles;
+    hipLaunchKernelGGL((rec_bwd_kernel<T, ALIGNED, PIN, HAS_Z>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
+                       a.stream, k);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL(rec_bwd_reduce_kernel, dim3(static_cast<unsigned>((a.dim + 63) / 64)), dim3(1024), 0, a.stream,
-                       part, a.a_param, a.da_param, a.batch * ntiles, static_cast<int>(a.dim), a.c);
+                       k.part, a.a_param, a.da_param, a.batch * ntiles, static_cast<int>(a.dim), a.c);
     return hipGetLastError();
 }
 

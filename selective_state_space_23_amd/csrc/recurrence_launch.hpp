@@ -34,7 +34,7 @@ struct RecFwdArgs {
     Packed save[4];                // q null: not written
     void* ws;
     int64_t batch, seqlen, dim;
-    int64_t ld_x, ld_a, ld_g, ld_z;   // elements between two tokens
+    int ld_x, ld_a, ld_g, ld_z;       // elements between two tokens
     float c;
     bool bf16;
     bool aligned;                  // quads of channels: D, strides and pointers
@@ -61,7 +61,7 @@ struct RecBwdArgs {
     float* d_initial_state;        // or null
     void* ws;
     int64_t batch, seqlen, dim;
-    int64_t ld_x, ld_a, ld_g, ld_z, ld_o;
+    int ld_x, ld_a, ld_g, ld_z, ld_o;
     float c;
     bool bf16;
     bool aligned;
@@ -86,7 +86,7 @@ struct RecUpdateArgs {
     hipStream_t stream;
 };
 
-size_t recurrence_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, bool have_states);
+size_t recurrence_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim);
 size_t recurrence_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, bool have_states);
 hipError_t launch_recurrence_fwd(const RecFwdArgs& a);
 hipError_t launch_recurrence_bwd(const RecBwdArgs& a);

@@ -75,7 +75,7 @@ def test_dims(lib, kw, status):
     if one is not None:
         assert update(lib, dims(**one)) == status
     n = ctypes.c_size_t(7)
-    assert lib.mamba_gated_recurrence_workspace_bytes(ctypes.byref(dims(**kw)), 0, ctypes.byref(n)) == status
+    assert lib.mamba_gated_recurrence_workspace_bytes(ctypes.byref(dims(**kw)), ctypes.byref(n)) == status
     assert lib.mamba_gated_recurrence_bwd_workspace_bytes(ctypes.byref(dims(**kw)), 0, ctypes.byref(n)) == status
     assert n.value == 0
 
@@ -83,10 +83,10 @@ def test_dims(lib, kw, status):
 def test_workspace(lib):
     n = ctypes.c_size_t(7)
     query = lib.mamba_gated_recurrence_workspace_bytes
-    assert query(ctypes.byref(dims(seqlen=128)), 0, ctypes.byref(n)) == 0 and n.value == 0
-    assert query(ctypes.byref(dims(seqlen=129)), 0, ctypes.byref(n)) == 0 and n.value > 0
-    assert query(ctypes.byref(dims()), 0, None) == INVALID
-    assert query(None, 0, ctypes.byref(n)) == INVALID
+    assert query(ctypes.byref(dims(seqlen=128)), ctypes.byref(n)) == 0 and n.value == 0
+    assert query(ctypes.byref(dims(seqlen=129)), ctypes.byref(n)) == 0 and n.value > 0
+    assert query(ctypes.byref(dims()), None) == INVALID
+    assert query(None, ctypes.byref(n)) == INVALID
     query = lib.mamba_gated_recurrence_bwd_workspace_bytes
     assert query(ctypes.byref(dims(batch=0)), 0, ctypes.byref(n)) == 0 and n.value == 0
     assert query(ctypes.byref(dims()), 0, ctypes.byref(n)) == 0
