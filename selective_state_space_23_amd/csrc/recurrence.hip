@@ -23,9 +23,8 @@ constexpr int kThreads = kWaves * 64;
 
 // One pass over the data.  A workgroup works off tiles until none is left (rows
 // of one tile: one workgroup each); a tile's maps stay in registers while the value
-// entering it is found by wave 0, and the next tile's inputs are loaded as soon as
-// the maps are formed, so memory is busy through the scan, the wait and the
-// output.  OUT: writes out, the final state and the checkpoints; else the states
+// entering it is found by wave 0, and the next tile's inputs are under way from the
+// start of the tile on.  OUT: writes out, the final state and the checkpoints; else the states
 // alone (the backward's recomputation).
 struct RecFwdKernelArgs {
     RecFwdArgs a;
@@ -36,8 +35,9 @@ struct RecFwdKernelArgs {
 template <typename T, bool ALIGNED, bool PIN, bool HAS_Z, bool SAVE, bool OUT>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void rec_fwd_kernel(const RecFwdKernelArgs) {
     __shared__ float s_rate[kTileChannels];
-    __shared__ float s_in[kWaves][kTileChannels];
-    __shared__ float2 s_agg[kWaves + 1][kTileChannels];   // the last row takes what no one reads
+    __shared__ float s_in[kTileChannels];                 // the values entering the tile
+    __shared__ float2 s_agg[kWaves + 1][kTileChannels];   // the waves' maps; the last row takes what no one reads
+    __shared__ float2 s_pre[kWaves][kTileChannels];       // the maps of all before a wave
     __shared__ int s_ticket;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane % kRow, half = lane / kRow;
@@ -49,8 +49,17 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
     auto draw = [&]() { return walk.draw(kernel_args<RecFwdKernelArgs>()->ch.next); };
     auto place = [&](int ticket) { return walk.place<false>(ticket, kernel_args<RecFwdKernelArgs>()->a.seqlen); };
 
-    LaneIn<T, ALIGNED, PIN, kK> xi, ai, gi;
-    LaneIn<T, ALIGNED, false, kK> zi;
+    // The next tile's inputs: in LDS (each wave its own part), or in registers where
+    // these are plenty (float32, unaligned: two waves a SIMD).
+    constexpr bool kStaged = sizeof(T) == 2 && ALIGNED;
+    constexpr bool kZ = HAS_Z && OUT;
+    using In = LaneIn<T, ALIGNED, PIN, kK>;
+    using Plain = LaneIn<T, ALIGNED, false, kK>;
+    constexpr int kStage = 3 * In::kStageBytes + (kZ ? Plain::kStageBytes : 0);
+    __shared__ __attribute__((aligned(16))) char s_stage[kStaged ? kWaves * kStage : 16];
+    char* const stage = s_stage + (kStaged ? wave * kStage : 0);
+    In xi, ai, gi;
+    Plain zi;
     StartFlags fl;
     float rate[kV];
     auto fetch = [&](const Tile& t) {
@@ -58,10 +67,22 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
         const auto p = kernel_args<RecFwdKernelArgs>();
         const auto& a = p->a;
         const int64_t rows = a.batch * a.seqlen;
-        ai.load(a.gate_a, a.in[1], t, a.ld_a, tok, c, dim, rows);
-        gi.load(a.gate_x, a.in[2], t, a.ld_g, tok, c, dim, rows);
-        xi.load(a.x, a.in[0], t, a.ld_x, tok, c, dim, rows);
-        if constexpr (HAS_Z && OUT) zi.load(a.z, a.in[0], t, a.ld_z, tok, c, dim, rows);
+        if constexpr (kStaged) {
+            ai.stage(stage, a.gate_a, a.in[1], t, a.ld_a, wave, dim, rows);
+            gi.stage(stage + In::kStageBytes, a.gate_x, a.in[2], t, a.ld_g, wave, dim, rows);
+            xi.stage(stage + 2 * In::kStageBytes, a.x, a.in[0], t, a.ld_x, wave, dim, rows);
+            if constexpr (kZ) zi.stage(stage + 3 * In::kStageBytes, a.z, a.in[0], t, a.ld_z, wave, dim, rows);
+            if constexpr (PIN) {
+                ai.load_scale(a.in[1], t, tok, rows);
+                gi.load_scale(a.in[2], t, tok, rows);
+                xi.load_scale(a.in[0], t, tok, rows);
+            }
+        } else {
+            ai.load(a.gate_a, a.in[1], t, a.ld_a, tok, c, dim, rows);
+            gi.load(a.gate_x, a.in[2], t, a.ld_g, tok, c, dim, rows);
+            xi.load(a.x, a.in[0], t, a.ld_x, tok, c, dim, rows);
+            if constexpr (kZ) zi.load(a.z, a.in[0], t, a.ld_z, tok, c, dim, rows);
+        }
         fl.load(a.doc_start, t.row_tok, t.nv);
         if (ntiles > 1) {
             const float2 r = *reinterpret_cast<const float2*>(p->ch.rate + c);   // padded to whole channel tiles
@@ -95,18 +116,34 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
         for (int j = 0; j < kV; ++j) rate[j] = s_rate[kV * li + j];
     }
 
+    if constexpr (kStaged) wait_all_but<0>();
     for (;;) {
         const Tile t = place(cur);
         const int c = t.ct * kTileChannels + kV * li;
         const TileStarts starts = fl.starts();
+        // The next tile's inputs are on their way from here on (past the last ticket: a
+        // tile of no tokens, nothing is read).
+        In xc = xi, ac = ai, gc = gi;
+        Plain zc = zi;
+        float rc[kV];
+#pragma unroll
+        for (int j = 0; j < kV; ++j) rc[j] = rate[j];
+        if constexpr (kStaged) {
+            ac.read(stage, half, li);
+            gc.read(stage + In::kStageBytes, half, li);
+            xc.read(stage + 2 * In::kStageBytes, half, li);
+            if constexpr (kZ) zc.read(stage + 3 * In::kStageBytes, half, li);
+            wait_lds_reads();
+        }
+        fetch(place(next));
         if constexpr (SAVE) {
             const auto p = kernel_args<RecFwdKernelArgs>();
             const auto& a = p->a;
             const int64_t rows = a.batch * a.seqlen;
-            save_packed<T, ALIGNED, kK>(xi, a.save[0], t, tok, c, dim, rows);
-            save_packed<T, ALIGNED, kK>(ai, a.save[1], t, tok, c, dim, rows);
-            save_packed<T, ALIGNED, kK>(gi, a.save[2], t, tok, c, dim, rows);
-            if constexpr (HAS_Z) save_packed<T, ALIGNED, kK>(zi, a.save[3], t, tok, c, dim, rows);
+            save_packed<T, ALIGNED, kK>(xc, a.save[0], t, tok, c, dim, rows);
+            save_packed<T, ALIGNED, kK>(ac, a.save[1], t, tok, c, dim, rows);
+            save_packed<T, ALIGNED, kK>(gc, a.save[2], t, tok, c, dim, rows);
+            if constexpr (HAS_Z) save_packed<T, ALIGNED, kK>(zc, a.save[3], t, tok, c, dim, rows);
         }
         // Maps of the lane's tokens from its first one on.  GEN: the tile has document
         // starts or ends behind the row (decided for the whole workgroup).
@@ -118,14 +155,14 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
             static_for<kK>([&](auto kc) {
                 constexpr int k = decltype(kc)::value;
                 float ga[kV], gx[kV], x[kV];
-                ai.template take<k>(ga);
-                gi.template take<k>(gx);
-                xi.template take<k>(x);
+                ac.template take<k>(ga);
+                gc.template take<k>(gx);
+                xc.template take<k>(x);
                 const bool start = GEN && ((st >> k) & 1u), out = GEN && tok + k >= t.nv;
 #pragma unroll
                 for (int j = 0; j < kV; ++j) {
                     float al, om;
-                    decay_terms(rate[j] * sigmoid_f(ga[j]), al, om);
+                    decay_terms(rc[j] * sigmoid_f(ga[j]), al, om);
                     float bb = __builtin_amdgcn_sqrtf(om) * (sigmoid_f(gx[j]) * x[j]);
                     if constexpr (GEN) {
                         al = out ? 1.0f : al;
@@ -160,42 +197,39 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
             compose(p, h, ep[j], eh[j]);
             s_agg[half ? wave : kWaves][kV * li + j] = make_float2(p, h);
         }
-        LaneIn<T, ALIGNED, false, kK> zc = zi;
         lds_barrier();
         if (wave == 0) {   // a lane per channel: the value entering the tile, the waves and the next tile
             const int d = t.ct * kTileChannels + lane;
             const auto p = kernel_args<RecFwdKernelArgs>();
             const auto& a = p->a;
-            const auto& ch = p->ch;
-            const int64_t word = walk.word(t, lane);
-            const int64_t at = word + static_cast<int64_t>(t.tile) * kTileChannels;
+            const ChainWords words = walk.words(Chain{p->ch.map, p->ch.value, p->ch.next, p->ch.rate}, t);
             float in = row_load(a.initial_state, t.b, a.dim, d);
             float2 m = s_agg[0][lane];
+            s_pre[0][lane] = make_float2(1.0f, 0.0f);
 #pragma unroll
             for (int w = 1; w < kWaves; ++w) {
+                s_pre[w][lane] = m;
                 float2 v = s_agg[w][lane];
                 compose(v.x, v.y, m.x, m.y);
                 m = v;
             }
-            if (t.tile + 1 < ntiles) publish_map(ch.map + at, m.x, m.y);
-            in = look_back(ch.map + word, ch.value + word, t.tile, in);
-            if (t.tile + 1 < ntiles) publish_value(ch.value + at, apply(m.x, m.y, in));
+            if (t.tile + 1 < ntiles) words.publish_map(t.pos, m.x, m.y);
+            in = words.look_back(t.pos, in);
+            const float leaving = apply(m.x, m.y, in);
+            if (t.tile + 1 < ntiles) words.publish_value(t.pos, leaving);
+            else if (OUT) row_store(a.final_state, t.b, a.dim, d, leaving);
             row_store(a.states, t.b * ntiles + t.tile, a.dim, d, in);
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                s_in[w][lane] = in;
-                const float2 v = s_agg[w][lane];
-                in = apply(v.x, v.y, in);
-            }
-            if (OUT && t.tile == ntiles - 1) row_store(a.final_state, t.b, a.dim, d, in);
+            s_in[lane] = in;
             if (next < walk.tickets) s_ticket = draw();
         }
-        fetch(place(next));   // past the last ticket: a tile of no tokens, nothing is read
         lds_barrier();
         if constexpr (OUT) {
             float e[kV];
 #pragma unroll
-            for (int j = 0; j < kV; ++j) e[j] = apply(ep[j], eh[j], s_in[wave][kV * li + j]);
+            for (int j = 0; j < kV; ++j) {
+                const float2 pre = s_pre[wave][kV * li + j];
+                e[j] = apply(ep[j], eh[j], apply(pre.x, pre.y, s_in[kV * li + j]));
+            }
             constexpr int esz = Elem<T>::kBytes;
             const Rsrc ob = rows_rsrc<esz>(kernel_args<RecFwdKernelArgs>()->a.out, t.row_tok, t.nv, dim, dim);
             const uint32_t step = static_cast<uint32_t>(dim) * esz;
@@ -221,6 +255,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
             else put(std::false_type{});
         }
         if (next >= walk.tickets) return;
+        // Behind the staged loads this wave has issued the tile's kK stores at least.
+        if constexpr (kStaged) wait_all_but<OUT ? kK : 0>();
         cur = next;
         next = __builtin_amdgcn_readfirstlane(s_ticket);   // written before the last barrier
     }

@@ -313,13 +313,42 @@ struct Tile {
     int64_t b, row_tok;    // row, first token counted over all rows
 };
 
+// BYTES of a tile's rows (ROW bytes each, from token `first` on, at byte `col` of the
+// row) into LDS, row after row: a load moves 4 bytes a lane to lds + 4 lane, so each
+// covers 256 / ROW rows.  Issued by a whole wave; nothing waits here.
+template <int ROW, int BYTES>
+__device__ __forceinline__ void stage_rows(char* lds, Rsrc rs, uint32_t step, int first, uint32_t col) {
+    constexpr int kRows = 256 / ROW;   // rows of one load
+    const int lane = threadIdx.x & 63;
+    uint32_t off = tile_offset(first + lane / (ROW / 4), step, col + lane % (ROW / 4) * 4);
+#pragma unroll
+    for (int i = 0; i < BYTES / 256; ++i) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(lds + i * 256), 4, off, 0, 0,
+                                                 0);
+        off = next_offset(off, kRows * step);
+    }
+}
+
+// Waits until at most N of the wave's loads and stores are under way (they end in
+// order): what was issued before the last N is done.
+template <int N>
+__device__ __forceinline__ void wait_all_but() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// The wave's LDS reads are done.
+__device__ __forceinline__ void wait_lds_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 // A lane's place in a tile of the recurrence's kernels.
 constexpr int kV = 2;                            // channels of a lane
 constexpr int kRow = kTileChannels / kV;         // lanes of a token
 
 // A lane's K pairs of one input, plain or 8-bit: tokens tok .. tok + K - 1 of the
-// tile, channels c and c + 1.
+// tile, channels c and c + 1.  load() reads them from memory; stage() has memory
+// write the wave's tokens to LDS (no registers held while in flight) and read()
+// takes the lane's from there once they have landed.
 template <typename T, bool ALIGNED, bool PIN, int K> struct LaneIn {
+    static constexpr int kRowBytes = kTileChannels * Elem<T>::kBytes;   // one token's
+    static constexpr int kStageBytes = 2 * K * kRowBytes;               // one wave's
     Raw<T, kV> r[K];
     template <typename P>
     __device__ __forceinline__ void load(const void* p, const P&, const Tile& t, int ld, int tok, int c, int dim,
@@ -334,6 +363,18 @@ template <typename T, bool ALIGNED, bool PIN, int K> struct LaneIn {
             off = next_offset(off, step);
         }
     }
+    template <typename P>
+    __device__ __forceinline__ void stage(char* lds, const void* p, const P&, const Tile& t, int ld, int wave, int dim,
+                                          int64_t) {
+        constexpr int esz = Elem<T>::kBytes;
+        stage_rows<kRowBytes, kStageBytes>(lds, rows_rsrc<esz>(p, t.row_tok, t.nv, ld, dim),
+                                           static_cast<uint32_t>(ld) * esz, wave * 2 * K, t.ct * kRowBytes);
+    }
+    __device__ __forceinline__ void read(const char* lds, int half, int li) {
+        const char* p = lds + half * K * kRowBytes + li * kV * Elem<T>::kBytes;
+#pragma unroll
+        for (int k = 0; k < K; ++k) __builtin_memcpy(&r[k], p + k * kRowBytes, sizeof(r[k]));
+    }
     template <int k> __device__ __forceinline__ void get(float (&v)[kV]) const { unpack(r[k], v); }
     // The same, unpacked here and not where the compiler could do it for several
     // uses at once (twice the registers across everything in between).
@@ -344,9 +385,17 @@ template <typename T, bool ALIGNED, bool PIN, int K> struct LaneIn {
     }
 };
 template <typename T, bool ALIGNED, int K> struct LaneIn<T, ALIGNED, true, K> {
+    static constexpr int kRowBytes = kTileChannels;
+    static constexpr int kStageBytes = 2 * K * kRowBytes;
     uint32_t q[K];
     static constexpr int kPer = 16 / K;   // lanes of a DPP row of 16 that hold one token's scale
     float s;                              // scale of token (lane % 16) / kPer of the lane's K
+    template <typename P>
+    __device__ __forceinline__ void load_scale(const P& p, const Tile& t, int tok, int64_t rows) {
+        const Rsrc ss = tile_rsrc(p.scale + t.ct * rows + t.row_tok, t.nv * 4);
+        s = __uint_as_float(
+            __builtin_amdgcn_raw_buffer_load_b32(ss, 4 * (tok + static_cast<int>(threadIdx.x & 15) / kPer), 0, 0));
+    }
     template <typename P>
     __device__ __forceinline__ void load(const void*, const P& p, const Tile& t, int, int tok, int c, int dim,
                                          int64_t rows) {
@@ -357,9 +406,18 @@ template <typename T, bool ALIGNED, int K> struct LaneIn<T, ALIGNED, true, K> {
             q[k] = load_codes<kV, ALIGNED>(rs, off);
             off = next_offset(off, dim);
         }
-        const Rsrc ss = tile_rsrc(p.scale + t.ct * rows + t.row_tok, t.nv * 4);
-        s = __uint_as_float(
-            __builtin_amdgcn_raw_buffer_load_b32(ss, 4 * (tok + static_cast<int>(threadIdx.x & 15) / kPer), 0, 0));
+        load_scale(p, t, tok, rows);
+    }
+    template <typename P>
+    __device__ __forceinline__ void stage(char* lds, const void*, const P& p, const Tile& t, int, int wave, int dim,
+                                          int64_t) {
+        stage_rows<kRowBytes, kStageBytes>(lds, rows_rsrc<1>(p.q, t.row_tok, t.nv, dim, dim), dim, wave * 2 * K,
+                                           t.ct * kRowBytes);
+    }
+    __device__ __forceinline__ void read(const char* lds, int half, int li) {
+        const char* p = lds + half * K * kRowBytes + li * kV;
+#pragma unroll
+        for (int k = 0; k < K; ++k) q[k] = *reinterpret_cast<const uint16_t*>(p + k * kRowBytes);
     }
     template <int k> __device__ __forceinline__ void take(float (&v)[kV]) {
         asm volatile("" : "+v"(q[k]));
@@ -428,10 +486,10 @@ __device__ __forceinline__ void save_packed(const LaneIn<T, ALIGNED, false, K>& 
 // order.  That is the operation sequence of the tiles' own outgoing values, so
 // the result does not depend on how far a tile had to look.
 //
-// Every word is published by one relaxed agent-scope atomic store and read by
-// relaxed agent-scope atomic loads: a map is one 64-bit word (P, H), a value one
-// 32-bit word, and all bits set means "not there yet" (the launch clears the words
-// first; a NaN with that pattern is stored as the usual one).
+// Every word is published by one store and read by loads at agent scope, aligned
+// and so whole: a map is one 64-bit word (P, H), a value one 32-bit word.  All bits
+// set (in H) means "not there yet": the launch clears the words first, and a NaN
+// with that pattern is stored as the usual one.
 //
 // Every wait ends: workgroups draw tiles by tickets, position by position over the
 // chains of a group, and work on them in the order drawn.  The positions a
@@ -462,54 +520,64 @@ __device__ __forceinline__ uint32_t not_all_ones(float x) {
     return b == 0xffffffffu ? 0x7fc00000u : b;
 }
 
-__device__ __forceinline__ void publish_map(uint64_t* p, float P, float H) {
-    const uint64_t w = (static_cast<uint64_t>(not_all_ones(H)) << 32) | __float_as_uint(P);
-    __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ void publish_value(uint32_t* p, float v) {
-    __hip_atomic_store(p, not_all_ones(v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
-// The value entering position `pos` for the lane's channel; `map` and `value` point
-// at the channel's word of position 0, `first` enters position 0.  All 64 lanes.
-__device__ __forceinline__ float look_back(const uint64_t* map, const uint32_t* value, int pos, float first) {
-    uint32_t v[kLook];
-    uint64_t m[kLook];
-#pragma unroll
-    for (int k = 0; k < kLook; ++k) {
-        v[k] = 0xffffffffu;
-        m[k] = ~0ull;
+// The words of one chain, as buffers: accesses at agent scope (the cache-policy
+// bit kAgentScope), each word whole.
+constexpr int kAgentScope = 16;
+struct ChainWords {
+    Rsrc map, value;
+    __device__ __forceinline__ void init(uint64_t* maps, uint32_t* values, int64_t word0, int ntiles) {
+        map = tile_rsrc(maps + word0, static_cast<int64_t>(ntiles) * kTileChannels * 8);
+        value = tile_rsrc(values + word0, static_cast<int64_t>(ntiles) * kTileChannels * 4);
     }
-    for (int polls = 0; polls < kMaxPolls; ++polls) {
+    __device__ __forceinline__ void publish_map(int pos, float P, float H) const {
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        const u32x2 w = {__float_as_uint(P), not_all_ones(H)};
+        __builtin_amdgcn_raw_buffer_store_b64(w, map, (threadIdx.x & 63) * 8, pos * (kTileChannels * 8), kAgentScope);
+    }
+    __device__ __forceinline__ void publish_value(int pos, float v) const {
+        __builtin_amdgcn_raw_buffer_store_b32(not_all_ones(v), value, (threadIdx.x & 63) * 4, pos * (kTileChannels * 4),
+                                              kAgentScope);
+    }
+    // The value entering position `pos` for the lane's channel; `first` enters
+    // position 0.  All 64 lanes.
+    __device__ __forceinline__ float look_back(int pos, float first) const {
+        uint32_t v[kLook], mp[kLook], mh[kLook];
 #pragma unroll
-        for (int k = 0; k < kLook; ++k) {
-            const int p = pos - 1 - k;
-            if (p < 0) {
-                if (p == -1) v[k] = not_all_ones(first);
-            } else {   // read again until every lane has its word
-                if (__any(v[k] == 0xffffffffu))
-                    v[k] = __hip_atomic_load(value + static_cast<int64_t>(p) * kTileChannels, __ATOMIC_RELAXED,
-                                             __HIP_MEMORY_SCOPE_AGENT);
-                if (k < kLook - 1 && __any(m[k] == ~0ull))
-                    m[k] = __hip_atomic_load(map + static_cast<int64_t>(p) * kTileChannels, __ATOMIC_RELAXED,
-                                             __HIP_MEMORY_SCOPE_AGENT);
+        for (int k = 0; k < kLook; ++k) v[k] = mp[k] = mh[k] = 0xffffffffu;
+        for (int polls = 0; polls < kMaxPolls; ++polls) {
+            asm volatile("" ::: "memory");   // every poll reads memory
+#pragma unroll
+            for (int k = 0; k < kLook; ++k) {
+                const int p = __builtin_amdgcn_readfirstlane(pos - 1 - k);
+                if (p < 0) {
+                    if (p == -1) v[k] = not_all_ones(first);
+                } else {   // read again until every lane has its word
+                    if (__any(v[k] == 0xffffffffu))
+                        v[k] = __builtin_amdgcn_raw_buffer_load_b32(value, (threadIdx.x & 63) * 4,
+                                                                    p * (kTileChannels * 4), kAgentScope);
+                    if (k < kLook - 1 && __any(mh[k] == 0xffffffffu)) {
+                        const auto w = __builtin_amdgcn_raw_buffer_load_b64(map, (threadIdx.x & 63) * 8,
+                                                                            p * (kTileChannels * 8), kAgentScope);
+                        mp[k] = w[0];
+                        mh[k] = w[1];
+                    }
+                }
             }
-        }
-        bool ok = false;
-        float c = 0.0f;
+            bool ok = false;
+            float c = 0.0f;
 #pragma unroll
-        for (int k = kLook - 1; k >= 0; --k) {
-            const float through = apply(__uint_as_float(static_cast<uint32_t>(m[k])),
-                                        __uint_as_float(static_cast<uint32_t>(m[k] >> 32)), c);
-            const bool there = v[k] != 0xffffffffu;
-            c = there ? __uint_as_float(v[k]) : through;
-            ok = there || (ok && m[k] != ~0ull);
+            for (int k = kLook - 1; k >= 0; --k) {
+                const float through = apply(__uint_as_float(mp[k]), __uint_as_float(mh[k]), c);
+                const bool there = v[k] != 0xffffffffu;
+                c = there ? __uint_as_float(v[k]) : through;
+                ok = there || (ok && mh[k] != 0xffffffffu);
+            }
+            if (__all(ok)) return c;
+            __builtin_amdgcn_s_sleep(1);
         }
-        if (__all(ok)) return c;
-        __builtin_amdgcn_s_sleep(1);
+        return __uint_as_float(0x7fc00000u);
     }
-    return __uint_as_float(0x7fc00000u);
-}
+};
 
 // The tiles a workgroup draws: tickets of its group, position by position over the
 // group's chains.
@@ -526,7 +594,6 @@ struct Walk {
     // By a whole wave: lane 0 adds 1 at agent scope, the other lanes' offsets lie
     // past the counter.
     __device__ __forceinline__ int draw(uint32_t* next) const {
-        constexpr int kAgentScope = 16;   // the cache-policy bit of device scope
         const Rsrc rs = tile_rsrc(next + group, 4);
         return __builtin_amdgcn_readfirstlane(__builtin_amdgcn_raw_ptr_buffer_atomic_add_i32(
             1, rs, (threadIdx.x & 63) == 0 ? 0u : kNoStore, 0, kAgentScope));
@@ -547,9 +614,10 @@ struct Walk {
         t.nv = t.pos >= ntiles || left < 0 ? 0 : left < kTileTokens ? static_cast<int>(left) : kTileTokens;
         return t;
     }
-    // A channel's word of position 0 in the chain's arrays.
-    __device__ __forceinline__ int64_t word(const Tile& t, int channel) const {
-        return (t.b * nct + t.ct) * ntiles * kTileChannels + channel;
+    __device__ __forceinline__ ChainWords words(const Chain& ch, const Tile& t) const {
+        ChainWords w;
+        w.init(ch.map, ch.value, (t.b * nct + t.ct) * ntiles * kTileChannels, ntiles);
+        return w;
     }
 };
 

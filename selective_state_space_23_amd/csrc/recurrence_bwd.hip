@@ -35,15 +35,15 @@ struct RecBwdKernelArgs {
 };
 
 // One pass over the data, from the row ends back.  A workgroup works off tiles as
-// the forward does; everything the gradients need of a token is formed once
-// (seven values a channel and token stay in registers) before the adjoint
-// entering the tile is known, and the next tile's inputs are loaded meanwhile.
+// the forward does; everything the gradients need of a token is formed once, before
+// the adjoint entering the tile is known, and kept in registers.
 template <typename T, bool ALIGNED, bool PIN, bool HAS_Z>
 __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArgs) {
     __shared__ float s_rate[kTileChannels];
     // the last row of an array takes what no one reads
     __shared__ float s_P[kWaves + 1][kTileChannels], s_H[kWaves + 1][kTileChannels], s_X[kWaves + 1][kTileChannels];
-    __shared__ float s_in[kWaves][kTileChannels], s_adj[kWaves][kTileChannels], s_sum[kWaves + 1][kTileChannels];
+    __shared__ float s_in[kWaves][kTileChannels], s_adj[kTileChannels], s_sum[kWaves + 1][kTileChannels];
+    __shared__ float2 s_suf[kWaves][kTileChannels];    // the adjoint maps of all behind a wave
     __shared__ int s_ticket;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane % kRow, half = lane / kRow;
@@ -55,8 +55,16 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
     auto draw = [&]() { return walk.draw(kernel_args<RecBwdKernelArgs>()->ch.next); };
     auto place = [&](int ticket) { return walk.place<true>(ticket, kernel_args<RecBwdKernelArgs>()->a.seqlen); };
 
-    LaneIn<T, ALIGNED, PIN, kK> xi, ai, gi, zi;
-    LaneIn<T, ALIGNED, false, kK> oi;
+    // The next tile's inputs: staged in LDS (each wave its own part) while a tile is
+    // worked off; float32 (too large) and unaligned ones are loaded at its start.
+    constexpr bool kStaged = sizeof(T) == 2 && ALIGNED;
+    using In = LaneIn<T, ALIGNED, PIN, kK>;
+    using Plain = LaneIn<T, ALIGNED, false, kK>;
+    constexpr int kStage = (HAS_Z ? 4 : 3) * In::kStageBytes + Plain::kStageBytes;
+    __shared__ __attribute__((aligned(16))) char s_stage[kStaged ? kWaves * kStage : 16];
+    char* const stage = s_stage + (kStaged ? wave * kStage : 0);
+    In xi, ai, gi, zi;
+    Plain oi;
     StartFlags fl;
     float rate[kV];
     auto fetch = [&](const Tile& t) {
@@ -64,11 +72,26 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
         const auto p = kernel_args<RecBwdKernelArgs>();
         const auto& a = p->a;
         const int64_t rows = a.batch * a.seqlen;
-        ai.load(a.gate_a, a.in[1], t, a.ld_a, tok, c, dim, rows);
-        gi.load(a.gate_x, a.in[2], t, a.ld_g, tok, c, dim, rows);
-        xi.load(a.x, a.in[0], t, a.ld_x, tok, c, dim, rows);
-        oi.load(a.dout, a.in[0], t, a.ld_o, tok, c, dim, rows);
-        if constexpr (HAS_Z) zi.load(a.z, a.in[3], t, a.ld_z, tok, c, dim, rows);
+        if constexpr (kStaged) {
+            ai.stage(stage, a.gate_a, a.in[1], t, a.ld_a, wave, dim, rows);
+            gi.stage(stage + In::kStageBytes, a.gate_x, a.in[2], t, a.ld_g, wave, dim, rows);
+            xi.stage(stage + 2 * In::kStageBytes, a.x, a.in[0], t, a.ld_x, wave, dim, rows);
+            oi.stage(stage + 3 * In::kStageBytes, a.dout, a.in[0], t, a.ld_o, wave, dim, rows);
+            if constexpr (HAS_Z)
+                zi.stage(stage + 3 * In::kStageBytes + Plain::kStageBytes, a.z, a.in[3], t, a.ld_z, wave, dim, rows);
+            if constexpr (PIN) {
+                ai.load_scale(a.in[1], t, tok, rows);
+                gi.load_scale(a.in[2], t, tok, rows);
+                xi.load_scale(a.in[0], t, tok, rows);
+                if constexpr (HAS_Z) zi.load_scale(a.in[3], t, tok, rows);
+            }
+        } else {
+            ai.load(a.gate_a, a.in[1], t, a.ld_a, tok, c, dim, rows);
+            gi.load(a.gate_x, a.in[2], t, a.ld_g, tok, c, dim, rows);
+            xi.load(a.x, a.in[0], t, a.ld_x, tok, c, dim, rows);
+            oi.load(a.dout, a.in[0], t, a.ld_o, tok, c, dim, rows);
+            if constexpr (HAS_Z) zi.load(a.z, a.in[3], t, a.ld_z, tok, c, dim, rows);
+        }
         fl.load(a.doc_start, t.row_tok, t.nv);
         if (ntiles > 1) {
             const float2 r = *reinterpret_cast<const float2*>(p->ch.rate + c);   // padded to whole channel tiles
@@ -84,7 +107,7 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
         lds_barrier();
         if (wave == 0) s_ticket = draw();
         if (cur >= walk.tickets) return;
-        fetch(place(cur));
+        if constexpr (kStaged) fetch(place(cur));
         lds_barrier();
         next = __builtin_amdgcn_readfirstlane(s_ticket);
         lds_barrier();
@@ -114,15 +137,30 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
         row_store(kernel_args<RecBwdKernelArgs>()->part, part_row, dim, part_channel + lane, s);
     };
 
+    if constexpr (kStaged) wait_all_but<0>();
     for (;;) {
         const Tile t = place(cur);
         const int c = t.ct * kTileChannels + kV * li;
+        if constexpr (!kStaged) {
+            if (ntiles > 1) fetch(t);
+        }
         const TileStarts starts = fl.starts();
         const bool general = starts.any() || t.nv < kTileTokens;   // the same in the whole workgroup
         const uint32_t st = starts.bits(tok, kK);
-        float kc[kV];   // -c softplus(a_param)
+        In xc = xi, ac = ai, gc = gi, zc = zi;
+        Plain oc = oi;
+        float rc[kV];
 #pragma unroll
-        for (int j = 0; j < kV; ++j) kc[j] = kLn2 * rate[j];
+        for (int j = 0; j < kV; ++j) rc[j] = rate[j];
+        if constexpr (kStaged) {
+            ac.read(stage, half, li);
+            gc.read(stage + In::kStageBytes, half, li);
+            xc.read(stage + 2 * In::kStageBytes, half, li);
+            oc.read(stage + 3 * In::kStageBytes, half, li);
+            if constexpr (HAS_Z) zc.read(stage + 3 * In::kStageBytes + Plain::kStageBytes, half, li);
+            wait_lds_reads();
+            fetch(place(next));   // past the last ticket: a tile of no tokens, nothing is read
+        }
         // Of every token: a, r, w v, w i, 1 - i, (r / w) a^2 v, dy and dout silu'(z).
         float A[kK][kV], R[kK][kV], B[kK][kV], W[kK][kV], O[kK][kV], U[kK][kV], Y[kK][kV], Z[kK][kV];
         float P[kV], H[kV], X[kV];
@@ -131,17 +169,17 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
             static_for<kK>([&](auto kcc) {
                 constexpr int k = decltype(kcc)::value;
                 float ga[kV], gx[kV], x[kV], z[kV];
-                ai.template take<k>(ga);
-                gi.template take<k>(gx);
-                xi.template take<k>(x);
-                oi.template take<k>(Y[k]);
-                if constexpr (HAS_Z) zi.template take<k>(z);
+                ac.template take<k>(ga);
+                gc.template take<k>(gx);
+                xc.template take<k>(x);
+                oc.template take<k>(Y[k]);
+                if constexpr (HAS_Z) zc.template take<k>(z);
                 const bool start = GEN && ((st >> k) & 1u), out = GEN && tok + k >= t.nv;
 #pragma unroll
                 for (int j = 0; j < kV; ++j) {
                     const float r = sigmoid_f(ga[j]);
                     float al, om;
-                    decay_terms(rate[j] * r, al, om);
+                    decay_terms(rc[j] * r, al, om);
                     float rw = __builtin_amdgcn_rsqf(om);
                     asm volatile("" : "+v"(rw));
                     rw = om >= 0x1p-126f ? rw : 0.0f;   // denormals count as 0
@@ -200,26 +238,23 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
             const int d = t.ct * kTileChannels + lane;
             const auto p = kernel_args<RecBwdKernelArgs>();
             const auto& a = p->a;
-            const int64_t word = walk.word(t, lane);
-            const int64_t at = word + static_cast<int64_t>(t.pos) * kTileChannels;
+            const ChainWords words = walk.words(Chain{p->ch.map, p->ch.value, p->ch.next, p->ch.rate}, t);
             float e = row_load(a.d_final_state, t.b, a.dim, d);
             float mp = s_P[kWaves - 1][lane], mx = s_X[kWaves - 1][lane];
-#pragma unroll 4
+            s_suf[kWaves - 1][lane] = make_float2(1.0f, 0.0f);
+#pragma unroll 3
             for (int w = kWaves - 2; w >= 0; --w) {
+                s_suf[w][lane] = make_float2(mp, mx);
                 const float q = s_P[w][lane];
                 mx = apply(q, s_X[w][lane], mx);
                 mp = is_reset(q) ? q : q * mp;
             }
-            if (t.pos + 1 < ntiles) publish_map(p->ch.map + at, mp, mx);
-            e = look_back(p->ch.map + word, p->ch.value + word, t.pos, e);
+            if (t.pos + 1 < ntiles) words.publish_map(t.pos, mp, mx);
+            e = words.look_back(t.pos, e);
             const float leaving = apply(mp, mx, e);
-            if (t.pos + 1 < ntiles) publish_value(p->ch.value + at, leaving);
+            if (t.pos + 1 < ntiles) words.publish_value(t.pos, leaving);
             if (t.tile == 0) row_store(a.d_initial_state, t.b, a.dim, d, leaving);
-#pragma unroll 4
-            for (int w = kWaves - 1; w >= 0; --w) {
-                s_adj[w][lane] = e;
-                e = apply(s_P[w][lane], s_X[w][lane], e);
-            }
+            s_adj[lane] = e;
             if (next < walk.tickets) s_ticket = draw();
         } else if (wave == 1) {   // the states entering the waves
             const int d = t.ct * kTileChannels + lane;
@@ -227,7 +262,7 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
             const auto& a = p->a;
             float h = a.states != nullptr ? row_load(a.states, t.b * ntiles + t.tile, a.dim, d)
                                           : row_load(a.initial_state, t.b, a.dim, d);
-#pragma unroll 4
+#pragma unroll 2
             for (int w = 0; w < kWaves; ++w) {
                 s_in[w][lane] = h;
                 h = apply(s_P[w][lane], s_H[w][lane], h);
@@ -237,7 +272,6 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
             part_row = t.b * ntiles + t.tile;
             part_channel = t.ct * kTileChannels;
         }
-        fetch(place(next));   // past the last ticket: a tile of no tokens, nothing is read
         lds_barrier();
         {
             constexpr int esz = Elem<T>::kBytes;
@@ -259,7 +293,8 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
                         hp[k][j] = h;
                         h = GEN && ((st >> k) & 1u) ? B[k][j] : __builtin_fmaf(A[k][j], h, B[k][j]);
                     }
-                    e[j] = apply<GEN>(rp[j], rx[j], s_adj[wave][kV * li + j]);
+                    const float2 suf = s_suf[wave][kV * li + j];
+                    e[j] = apply<GEN>(rp[j], rx[j], apply(suf.x, suf.y, s_adj[kV * li + j]));
                     sum[j] = 0.0f;
                 }
                 static_for<kK>([&](auto kcc) {
@@ -273,7 +308,7 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
                         dx[j] = G * W[k][j];
                         dg[j] = G * B[k][j] * O[k][j];
                         const float q = G * __builtin_fmaf(R[k][j], ah, -U[k][j]);
-                        da[j] = kc[j] * (1.0f - R[k][j]) * q;
+                        da[j] = (kLn2 * rc[j]) * (1.0f - R[k][j]) * q;   // kLn2 rate = -c softplus(a_param)
                         if constexpr (HAS_Z) dz[j] = Z[k][j] * (ah + B[k][j]);
                         sum[j] += out ? 0.0f : q;
                         e[j] = start ? 0.0f : A[k][j] * G;
@@ -294,6 +329,8 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
             else put(std::false_type{});
         }
         if (next >= walk.tickets) break;
+        // Behind the staged loads this wave has issued the tile's stores at least.
+        if constexpr (kStaged) wait_all_but<(HAS_Z ? 4 : 3) * kK>();
         cur = next;
         next = __builtin_amdgcn_readfirstlane(s_ticket);   // written before the last barrier
     }
