@@ -72,11 +72,6 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
             gi.stage(stage + In::kStageBytes, a.gate_x, a.in[2], t, a.ld_g, wave, dim, rows);
             xi.stage(stage + 2 * In::kStageBytes, a.x, a.in[0], t, a.ld_x, wave, dim, rows);
             if constexpr (kZ) zi.stage(stage + 3 * In::kStageBytes, a.z, a.in[0], t, a.ld_z, wave, dim, rows);
-            if constexpr (PIN) {
-                ai.load_scale(a.in[1], t, tok, rows);
-                gi.load_scale(a.in[2], t, tok, rows);
-                xi.load_scale(a.in[0], t, tok, rows);
-            }
         } else {
             ai.load(a.gate_a, a.in[1], t, a.ld_a, tok, c, dim, rows);
             gi.load(a.gate_x, a.in[2], t, a.ld_g, tok, c, dim, rows);
@@ -92,11 +87,11 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
 
     int cur, next;
     if (ntiles > 1) {
-        if (wave == 0) s_ticket = draw();
+        if (wave == 0) s_ticket = __builtin_amdgcn_readfirstlane(draw());
         lds_barrier();
         cur = __builtin_amdgcn_readfirstlane(s_ticket);
         lds_barrier();
-        if (wave == 0) s_ticket = draw();
+        if (wave == 0) s_ticket = __builtin_amdgcn_readfirstlane(draw());
         if (cur >= walk.tickets) return;
         fetch(place(cur));
         lds_barrier();
@@ -197,12 +192,22 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
             compose(p, h, ep[j], eh[j]);
             s_agg[half ? wave : kWaves][kV * li + j] = make_float2(p, h);
         }
+        ChainWords::Seen seen = {};
+        auto words = [&]() {
+            const auto p = kernel_args<RecFwdKernelArgs>();
+            return walk.words(Chain{p->ch.map, p->ch.value, p->ch.next, p->ch.rate}, t);
+        };
+        int ticket = 0;   // wave 0's: the tile after the next one
+        if (wave == 0 && ntiles > 1) {
+            seen = words().peek(t.pos);
+            if (next < walk.tickets) ticket = draw();
+        }
         lds_barrier();
         if (wave == 0) {   // a lane per channel: the value entering the tile, the waves and the next tile
             const int d = t.ct * kTileChannels + lane;
             const auto p = kernel_args<RecFwdKernelArgs>();
             const auto& a = p->a;
-            const ChainWords words = walk.words(Chain{p->ch.map, p->ch.value, p->ch.next, p->ch.rate}, t);
+            const ChainWords chain = words();
             float in = row_load(a.initial_state, t.b, a.dim, d);
             float2 m = s_agg[0][lane];
             s_pre[0][lane] = make_float2(1.0f, 0.0f);
@@ -213,14 +218,14 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
                 compose(v.x, v.y, m.x, m.y);
                 m = v;
             }
-            if (t.tile + 1 < ntiles) words.publish_map(t.pos, m.x, m.y);
-            in = words.look_back(t.pos, in);
+            if (t.tile + 1 < ntiles) chain.publish_map(t.pos, m.x, m.y);
+            in = chain.look_back(t.pos, in, seen);
             const float leaving = apply(m.x, m.y, in);
-            if (t.tile + 1 < ntiles) words.publish_value(t.pos, leaving);
+            if (t.tile + 1 < ntiles) chain.publish_value(t.pos, leaving);
             else if (OUT) row_store(a.final_state, t.b, a.dim, d, leaving);
             row_store(a.states, t.b * ntiles + t.tile, a.dim, d, in);
             s_in[lane] = in;
-            if (next < walk.tickets) s_ticket = draw();
+            s_ticket = __builtin_amdgcn_readfirstlane(ticket);
         }
         lds_barrier();
         if constexpr (OUT) {

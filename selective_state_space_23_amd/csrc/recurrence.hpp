@@ -75,6 +75,13 @@ __device__ __forceinline__ ArgsPtr<Args> kernel_args() {
     return p;
 }
 
+// The lane, formed where it is used, for the same reason.
+__device__ __forceinline__ uint32_t lane_now() {
+    uint32_t t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t & 63;
+}
+
 // tok * step + c for a token of a tile and a step below 2^24, and the offset one
 // step on: formed where they are used, for the same reason.
 __device__ __forceinline__ uint32_t next_offset(uint32_t off, uint32_t step) {
@@ -287,14 +294,23 @@ __device__ __forceinline__ uint32_t encode(const float (&v)[V], float inv) {
 __device__ __forceinline__ bool is_reset(float P) { return __float_as_uint(P) >> 31; }
 template <bool CUT = true>
 __device__ __forceinline__ float apply(float P, float H, float h) {
-    const float r = __builtin_fmaf(P, h, H);
-    return CUT && is_reset(P) ? H : r;
+    float r = __builtin_fmaf(P, h, H);
+    if constexpr (CUT) {
+        asm volatile("" : "+v"(r));   // a select, not a branch
+        r = is_reset(P) ? H : r;
+    }
+    return r;
 }
 // (P, H) after (p, h): first the earlier tokens' map (p, h), then (P, H).
 template <bool CUT = true>
 __device__ __forceinline__ void compose(float& P, float& H, float p, float h) {
     H = apply<CUT>(P, H, h);
-    P = CUT && is_reset(P) ? P : P * p;
+    float r = P * p;
+    if constexpr (CUT) {
+        asm volatile("" : "+v"(r));
+        r = is_reset(P) ? P : r;
+    }
+    P = r;
 }
 
 template <int N, typename F, int... I>
@@ -314,19 +330,34 @@ struct Tile {
 };
 
 // BYTES of a tile's rows (ROW bytes each, from token `first` on, at byte `col` of the
-// row) into LDS, row after row: a load moves 4 bytes a lane to lds + 4 lane, so each
-// covers 256 / ROW rows.  Issued by a whole wave; nothing waits here.
+// row) into LDS, row after row: a load moves 16 bytes a lane to lds + 16 lane, or 4 to
+// lds + 4 lane where rows do not lie on 16 bytes or the wave has less than 1024.
+// Issued by a whole wave; nothing waits here.
 template <int ROW, int BYTES>
-__device__ __forceinline__ void stage_rows(char* lds, Rsrc rs, uint32_t step, int first, uint32_t col) {
-    constexpr int kRows = 256 / ROW;   // rows of one load
-    const int lane = threadIdx.x & 63;
-    uint32_t off = tile_offset(first + lane / (ROW / 4), step, col + lane % (ROW / 4) * 4);
+__device__ __forceinline__ void stage_rows(char* lds, Rsrc rs, uint32_t step, int first, uint32_t col, bool wide) {
+    typedef __attribute__((address_space(3))) void* Lds;
+    const int lane = lane_now();
+    if (BYTES % 1024 == 0 && wide) {
+        constexpr int kLanes = ROW / 16, kRows = 64 / kLanes;
+        uint32_t off = tile_offset(first + lane / kLanes, step, col + lane % kLanes * 16);
 #pragma unroll
-    for (int i = 0; i < BYTES / 256; ++i) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(lds + i * 256), 4, off, 0, 0,
-                                                 0);
-        off = next_offset(off, kRows * step);
+        for (int i = 0; i < BYTES; i += 1024) {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (Lds)(lds + i), 16, off, 0, 0, 0);
+            off = next_offset(off, kRows * step);
+        }
+    } else {
+        constexpr int kLanes = ROW / 4, kRows = 64 / kLanes;
+        uint32_t off = tile_offset(first + lane / kLanes, step, col + lane % kLanes * 4);
+#pragma unroll
+        for (int i = 0; i < BYTES; i += 256) {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (Lds)(lds + i), 4, off, 0, 0, 0);
+            off = next_offset(off, kRows * step);
+        }
     }
+}
+// Rows of `bytes` bytes, `step` apart, from p on: each starts and ends on 16 bytes.
+__device__ __forceinline__ bool rows_of_16(const void* p, uint32_t step, uint32_t bytes) {
+    return ((static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) | step | bytes) & 15) == 0;
 }
 
 // Waits until at most N of the wave's loads and stores are under way (they end in
@@ -341,6 +372,19 @@ __device__ __forceinline__ void wait_lds_reads() { asm volatile("s_waitcnt lgkmc
 // A lane's place in a tile of the recurrence's kernels.
 constexpr int kV = 2;                            // channels of a lane
 constexpr int kRow = kTileChannels / kV;         // lanes of a token
+
+// The lane's channel pair and half of the wave, and its first of K tokens: formed
+// where they are used, for registers.
+template <int K> struct LanePlace {
+    int li, half, tok;
+    __device__ __forceinline__ explicit LanePlace(int wave) {
+        const int lane = static_cast<int>(lane_now());
+        li = lane % kRow;
+        half = lane / kRow;
+        tok = (wave * 2 + half) * K;
+    }
+    __device__ __forceinline__ int channel(const Tile& t) const { return t.ct * kTileChannels + kV * li; }
+};
 
 // A lane's K pairs of one input, plain or 8-bit: tokens tok .. tok + K - 1 of the
 // tile, channels c and c + 1.  load() reads them from memory; stage() has memory
@@ -367,8 +411,9 @@ template <typename T, bool ALIGNED, bool PIN, int K> struct LaneIn {
     __device__ __forceinline__ void stage(char* lds, const void* p, const P&, const Tile& t, int ld, int wave, int dim,
                                           int64_t) {
         constexpr int esz = Elem<T>::kBytes;
-        stage_rows<kRowBytes, kStageBytes>(lds, rows_rsrc<esz>(p, t.row_tok, t.nv, ld, dim),
-                                           static_cast<uint32_t>(ld) * esz, wave * 2 * K, t.ct * kRowBytes);
+        const uint32_t step = static_cast<uint32_t>(ld) * esz;
+        stage_rows<kRowBytes, kStageBytes>(lds, rows_rsrc<esz>(p, t.row_tok, t.nv, ld, dim), step, wave * 2 * K,
+                                           t.ct * kRowBytes, rows_of_16(p, step, dim * esz));
     }
     __device__ __forceinline__ void read(const char* lds, int half, int li) {
         const char* p = lds + half * K * kRowBytes + li * kV * Elem<T>::kBytes;
@@ -386,16 +431,11 @@ template <typename T, bool ALIGNED, bool PIN, int K> struct LaneIn {
 };
 template <typename T, bool ALIGNED, int K> struct LaneIn<T, ALIGNED, true, K> {
     static constexpr int kRowBytes = kTileChannels;
-    static constexpr int kStageBytes = 2 * K * kRowBytes;
+    static constexpr int kCodeBytes = 2 * K * kRowBytes;
+    static constexpr int kStageBytes = kCodeBytes + 256;   // behind the codes the wave's 2 K scales
     uint32_t q[K];
     static constexpr int kPer = 16 / K;   // lanes of a DPP row of 16 that hold one token's scale
     float s;                              // scale of token (lane % 16) / kPer of the lane's K
-    template <typename P>
-    __device__ __forceinline__ void load_scale(const P& p, const Tile& t, int tok, int64_t rows) {
-        const Rsrc ss = tile_rsrc(p.scale + t.ct * rows + t.row_tok, t.nv * 4);
-        s = __uint_as_float(
-            __builtin_amdgcn_raw_buffer_load_b32(ss, 4 * (tok + static_cast<int>(threadIdx.x & 15) / kPer), 0, 0));
-    }
     template <typename P>
     __device__ __forceinline__ void load(const void*, const P& p, const Tile& t, int, int tok, int c, int dim,
                                          int64_t rows) {
@@ -406,18 +446,25 @@ template <typename T, bool ALIGNED, int K> struct LaneIn<T, ALIGNED, true, K> {
             q[k] = load_codes<kV, ALIGNED>(rs, off);
             off = next_offset(off, dim);
         }
-        load_scale(p, t, tok, rows);
+        const Rsrc ss = tile_rsrc(p.scale + t.ct * rows + t.row_tok, t.nv * 4);
+        s = __uint_as_float(
+            __builtin_amdgcn_raw_buffer_load_b32(ss, 4 * (tok + static_cast<int>(threadIdx.x & 15) / kPer), 0, 0));
     }
     template <typename P>
     __device__ __forceinline__ void stage(char* lds, const void*, const P& p, const Tile& t, int, int wave, int dim,
-                                          int64_t) {
-        stage_rows<kRowBytes, kStageBytes>(lds, rows_rsrc<1>(p.q, t.row_tok, t.nv, dim, dim), dim, wave * 2 * K,
-                                           t.ct * kRowBytes);
+                                          int64_t rows) {
+        stage_rows<kRowBytes, kCodeBytes>(lds, rows_rsrc<1>(p.q, t.row_tok, t.nv, dim, dim), dim, wave * 2 * K,
+                                          t.ct * kRowBytes, rows_of_16(p.q, dim, dim));
+        const Rsrc ss = tile_rsrc(p.scale + t.ct * rows + t.row_tok, t.nv * 4);
+        const int lane = lane_now();
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ss, (__attribute__((address_space(3))) void*)(lds + kCodeBytes), 4,
+                                                 lane < 2 * K ? 4 * (wave * 2 * K + lane) : kNoStore, 0, 0, 0);
     }
     __device__ __forceinline__ void read(const char* lds, int half, int li) {
         const char* p = lds + half * K * kRowBytes + li * kV;
 #pragma unroll
         for (int k = 0; k < K; ++k) q[k] = *reinterpret_cast<const uint16_t*>(p + k * kRowBytes);
+        s = *reinterpret_cast<const float*>(lds + kCodeBytes + 4 * (half * K + li % 16 / kPer));
     }
     template <int k> __device__ __forceinline__ void take(float (&v)[kV]) {
         asm volatile("" : "+v"(q[k]));
@@ -505,9 +552,9 @@ struct Chain {
     const float* rate; // [64 * channel tiles]: -c log2(e) softplus(a_param)
 };
 
-// Chains in groups by chain % groups, each group with its own ticket counter and
-// the workgroups of one blockIdx % 8 (one XCD, as they are dealt out): as many
-// groups, up to 8, as divide the chains evenly.
+// Chains in groups of neighbours, each group with its own ticket counter and the
+// workgroups of one blockIdx % 8 (one XCD, as they are dealt out): as many groups, up
+// to 8, as divide the chains evenly.
 __host__ __device__ inline int chain_groups(int64_t nchain) {
     return nchain % 8 == 0 ? 8 : nchain % 4 == 0 ? 4 : nchain % 2 == 0 ? 2 : 1;
 }
@@ -532,48 +579,64 @@ struct ChainWords {
     __device__ __forceinline__ void publish_map(int pos, float P, float H) const {
         typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
         const u32x2 w = {__float_as_uint(P), not_all_ones(H)};
-        __builtin_amdgcn_raw_buffer_store_b64(w, map, (threadIdx.x & 63) * 8, pos * (kTileChannels * 8), kAgentScope);
+        __builtin_amdgcn_raw_buffer_store_b64(w, map, lane_now() * 8, pos * (kTileChannels * 8), kAgentScope);
     }
     __device__ __forceinline__ void publish_value(int pos, float v) const {
-        __builtin_amdgcn_raw_buffer_store_b32(not_all_ones(v), value, (threadIdx.x & 63) * 4, pos * (kTileChannels * 4),
+        __builtin_amdgcn_raw_buffer_store_b32(not_all_ones(v), value, lane_now() * 4, pos * (kTileChannels * 4),
                                               kAgentScope);
+    }
+    // What the kLook positions before `pos` have published so far: read ahead of
+    // look_back().  Before position 0 the words read as zero (the range check).
+    struct Seen {
+        uint32_t v[kLook], mp[kLook - 1], mh[kLook - 1];
+    };
+    __device__ __forceinline__ void read_value(Seen& s, int k, int p) const {
+        s.v[k] = __builtin_amdgcn_raw_buffer_load_b32(value, p * (kTileChannels * 4) + lane_now() * 4, 0,
+                                                      kAgentScope);
+    }
+    __device__ __forceinline__ void read_map(Seen& s, int k, int p) const {
+        const auto w = __builtin_amdgcn_raw_buffer_load_b64(map, p * (kTileChannels * 8) + lane_now() * 8, 0,
+                                                            kAgentScope);
+        s.mp[k] = w[0];
+        s.mh[k] = w[1];
+    }
+    __device__ __forceinline__ Seen peek(int pos) const {
+        Seen s;
+#pragma unroll
+        for (int k = 0; k < kLook; ++k) {
+            read_value(s, k, pos - 1 - k);
+            if (k < kLook - 1) read_map(s, k, pos - 1 - k);
+        }
+        return s;
     }
     // The value entering position `pos` for the lane's channel; `first` enters
     // position 0.  All 64 lanes.
-    __device__ __forceinline__ float look_back(int pos, float first) const {
-        uint32_t v[kLook], mp[kLook], mh[kLook];
-#pragma unroll
-        for (int k = 0; k < kLook; ++k) v[k] = mp[k] = mh[k] = 0xffffffffu;
+    __device__ __forceinline__ float look_back(int pos, float first, Seen s) const {
         for (int polls = 0; polls < kMaxPolls; ++polls) {
-            asm volatile("" ::: "memory");   // every poll reads memory
-#pragma unroll
-            for (int k = 0; k < kLook; ++k) {
-                const int p = __builtin_amdgcn_readfirstlane(pos - 1 - k);
-                if (p < 0) {
-                    if (p == -1) v[k] = not_all_ones(first);
-                } else {   // read again until every lane has its word
-                    if (__any(v[k] == 0xffffffffu))
-                        v[k] = __builtin_amdgcn_raw_buffer_load_b32(value, (threadIdx.x & 63) * 4,
-                                                                    p * (kTileChannels * 4), kAgentScope);
-                    if (k < kLook - 1 && __any(mh[k] == 0xffffffffu)) {
-                        const auto w = __builtin_amdgcn_raw_buffer_load_b64(map, (threadIdx.x & 63) * 8,
-                                                                            p * (kTileChannels * 8), kAgentScope);
-                        mp[k] = w[0];
-                        mh[k] = w[1];
-                    }
-                }
-            }
             bool ok = false;
             float c = 0.0f;
 #pragma unroll
             for (int k = kLook - 1; k >= 0; --k) {
-                const float through = apply(__uint_as_float(mp[k]), __uint_as_float(mh[k]), c);
-                const bool there = v[k] != 0xffffffffu;
-                c = there ? __uint_as_float(v[k]) : through;
-                ok = there || (ok && mh[k] != 0xffffffffu);
+                if (k < kLook - 1) {
+                    c = apply(__uint_as_float(s.mp[k]), __uint_as_float(s.mh[k]), c);
+                    ok = ok && s.mh[k] != 0xffffffffu;
+                }
+                const bool there = s.v[k] != 0xffffffffu;
+                c = there ? __uint_as_float(s.v[k]) : c;
+                ok = ok || there;
+                if (pos - 1 - k == -1) {
+                    c = first;
+                    ok = true;
+                }
             }
             if (__all(ok)) return c;
             __builtin_amdgcn_s_sleep(1);
+            asm volatile("" ::: "memory");   // every poll reads memory
+#pragma unroll
+            for (int k = 0; k < kLook; ++k) {   // read again what some lane did not get
+                if (__any(s.v[k] == 0xffffffffu)) read_value(s, k, pos - 1 - k);
+                if (k < kLook - 1 && __any(s.mh[k < kLook - 1 ? k : 0] == 0xffffffffu)) read_map(s, k, pos - 1 - k);
+            }
         }
         return __uint_as_float(0x7fc00000u);
     }
@@ -592,18 +655,18 @@ struct Walk {
         tickets = per_group * ntiles;
     }
     // By a whole wave: lane 0 adds 1 at agent scope, the other lanes' offsets lie
-    // past the counter.
+    // past the counter.  The ticket is lane 0's.
     __device__ __forceinline__ int draw(uint32_t* next) const {
         const Rsrc rs = tile_rsrc(next + group, 4);
-        return __builtin_amdgcn_readfirstlane(__builtin_amdgcn_raw_ptr_buffer_atomic_add_i32(
-            1, rs, (threadIdx.x & 63) == 0 ? 0u : kNoStore, 0, kAgentScope));
+        return __builtin_amdgcn_raw_ptr_buffer_atomic_add_i32(1, rs, lane_now() == 0 ? 0u : kNoStore, 0,
+                                                              kAgentScope);
     }
     // The tile of a ticket, counted from the row's end with REVERSE; of no tokens
     // past the last ticket.
     template <bool REVERSE>
     __device__ __forceinline__ Tile place(int ticket, int64_t seqlen) const {
         Tile t;
-        const int chain = group + groups * (ticket % per_group);
+        const int chain = group * per_group + ticket % per_group;   // neighbours share an L2
         t.pos = ticket / per_group;
         t.tile = REVERSE ? ntiles - 1 - t.pos : t.pos;
         t.ct = chain % nct;

@@ -41,15 +41,13 @@ template <typename T, bool ALIGNED, bool PIN, bool HAS_Z>
 __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArgs) {
     __shared__ float s_rate[kTileChannels];
     // the last row of an array takes what no one reads
-    __shared__ float s_P[kWaves + 1][kTileChannels], s_H[kWaves + 1][kTileChannels], s_X[kWaves + 1][kTileChannels];
+    __shared__ float2 s_map[kWaves + 1][kTileChannels], s_rev[kWaves + 1][kTileChannels];   // (P, H) and (P, X)
     __shared__ float s_in[kWaves][kTileChannels], s_adj[kTileChannels], s_sum[kWaves + 1][kTileChannels];
-    __shared__ float2 s_suf[kWaves][kTileChannels];    // the adjoint maps of all behind a wave
     __shared__ int s_ticket;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int li = lane % kRow, half = lane / kRow;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    using Place = LanePlace<kK>;
     const auto first = kernel_args<RecBwdKernelArgs>();
     const int dim = static_cast<int>(first->a.dim), nct = first->nct, ntiles = first->ntiles;
-    const int tok = (wave * 2 + half) * kK;
     Walk walk;
     walk.init(nct, ntiles, static_cast<int>(first->a.batch));
     auto draw = [&]() { return walk.draw(kernel_args<RecBwdKernelArgs>()->ch.next); };
@@ -60,37 +58,36 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
     constexpr bool kStaged = sizeof(T) == 2 && ALIGNED;
     using In = LaneIn<T, ALIGNED, PIN, kK>;
     using Plain = LaneIn<T, ALIGNED, false, kK>;
-    constexpr int kStage = (HAS_Z ? 4 : 3) * In::kStageBytes + Plain::kStageBytes;
+    // x, dout and z are read twice, at both ends of a tile, and so have two places each.
+    constexpr int kTwice = (HAS_Z ? 2 : 1) * In::kStageBytes + Plain::kStageBytes;
+    constexpr int kStage = 2 * In::kStageBytes + 2 * kTwice;
     __shared__ __attribute__((aligned(16))) char s_stage[kStaged ? kWaves * kStage : 16];
     char* const stage = s_stage + (kStaged ? wave * kStage : 0);
+    int twice = 2 * In::kStageBytes;   // of the tile fetched last
     In xi, ai, gi, zi;
     Plain oi;
     StartFlags fl;
     float rate[kV];
     auto fetch = [&](const Tile& t) {
-        const int c = t.ct * kTileChannels + kV * li;
+        const Place l(wave);
+        const int c = l.channel(t);
         const auto p = kernel_args<RecBwdKernelArgs>();
         const auto& a = p->a;
         const int64_t rows = a.batch * a.seqlen;
         if constexpr (kStaged) {
             ai.stage(stage, a.gate_a, a.in[1], t, a.ld_a, wave, dim, rows);
             gi.stage(stage + In::kStageBytes, a.gate_x, a.in[2], t, a.ld_g, wave, dim, rows);
-            xi.stage(stage + 2 * In::kStageBytes, a.x, a.in[0], t, a.ld_x, wave, dim, rows);
-            oi.stage(stage + 3 * In::kStageBytes, a.dout, a.in[0], t, a.ld_o, wave, dim, rows);
+            twice = 4 * In::kStageBytes + kTwice - twice;
+            xi.stage(stage + twice, a.x, a.in[0], t, a.ld_x, wave, dim, rows);
+            oi.stage(stage + twice + In::kStageBytes, a.dout, a.in[0], t, a.ld_o, wave, dim, rows);
             if constexpr (HAS_Z)
-                zi.stage(stage + 3 * In::kStageBytes + Plain::kStageBytes, a.z, a.in[3], t, a.ld_z, wave, dim, rows);
-            if constexpr (PIN) {
-                ai.load_scale(a.in[1], t, tok, rows);
-                gi.load_scale(a.in[2], t, tok, rows);
-                xi.load_scale(a.in[0], t, tok, rows);
-                if constexpr (HAS_Z) zi.load_scale(a.in[3], t, tok, rows);
-            }
+                zi.stage(stage + twice + In::kStageBytes + Plain::kStageBytes, a.z, a.in[3], t, a.ld_z, wave, dim, rows);
         } else {
-            ai.load(a.gate_a, a.in[1], t, a.ld_a, tok, c, dim, rows);
-            gi.load(a.gate_x, a.in[2], t, a.ld_g, tok, c, dim, rows);
-            xi.load(a.x, a.in[0], t, a.ld_x, tok, c, dim, rows);
-            oi.load(a.dout, a.in[0], t, a.ld_o, tok, c, dim, rows);
-            if constexpr (HAS_Z) zi.load(a.z, a.in[3], t, a.ld_z, tok, c, dim, rows);
+            ai.load(a.gate_a, a.in[1], t, a.ld_a, l.tok, c, dim, rows);
+            gi.load(a.gate_x, a.in[2], t, a.ld_g, l.tok, c, dim, rows);
+            xi.load(a.x, a.in[0], t, a.ld_x, l.tok, c, dim, rows);
+            oi.load(a.dout, a.in[0], t, a.ld_o, l.tok, c, dim, rows);
+            if constexpr (HAS_Z) zi.load(a.z, a.in[3], t, a.ld_z, l.tok, c, dim, rows);
         }
         fl.load(a.doc_start, t.row_tok, t.nv);
         if (ntiles > 1) {
@@ -101,11 +98,11 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
 
     int cur, next;
     if (ntiles > 1) {
-        if (wave == 0) s_ticket = draw();
+        if (wave == 0) s_ticket = __builtin_amdgcn_readfirstlane(draw());
         lds_barrier();
         cur = __builtin_amdgcn_readfirstlane(s_ticket);
         lds_barrier();
-        if (wave == 0) s_ticket = draw();
+        if (wave == 0) s_ticket = __builtin_amdgcn_readfirstlane(draw());
         if (cur >= walk.tickets) return;
         if constexpr (kStaged) fetch(place(cur));
         lds_barrier();
@@ -122,7 +119,7 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
         }
         lds_barrier();
 #pragma unroll
-        for (int j = 0; j < kV; ++j) rate[j] = s_rate[kV * li + j];
+        for (int j = 0; j < kV; ++j) rate[j] = s_rate[kV * Place(wave).li + j];
     }
 
     // A tile's part of sum r dlog a: its waves' sums added by one wave behind the
@@ -131,6 +128,7 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
     int part_channel = 0;
     auto add_part = [&]() {
         if (part_row < 0) return;
+        const int lane = static_cast<int>(lane_now());
         float s = 0.0f;
 #pragma unroll 4
         for (int w = 0; w < kWaves; ++w) s += s_sum[w][lane];
@@ -140,41 +138,47 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
     if constexpr (kStaged) wait_all_but<0>();
     for (;;) {
         const Tile t = place(cur);
-        const int c = t.ct * kTileChannels + kV * li;
         if constexpr (!kStaged) {
             if (ntiles > 1) fetch(t);
         }
         const TileStarts starts = fl.starts();
         const bool general = starts.any() || t.nv < kTileTokens;   // the same in the whole workgroup
-        const uint32_t st = starts.bits(tok, kK);
+        const uint32_t st = starts.bits(Place(wave).tok, kK);
+        const int left = t.nv - Place(wave).tok;   // of the lane's tokens, those in the row
         In xc = xi, ac = ai, gc = gi, zc = zi;
         Plain oc = oi;
         float rc[kV];
 #pragma unroll
         for (int j = 0; j < kV; ++j) rc[j] = rate[j];
+        const int here = twice;
+        auto read_twice = [&]() {
+            const Place l(wave);
+            xc.read(stage + here, l.half, l.li);
+            oc.read(stage + here + In::kStageBytes, l.half, l.li);
+            if constexpr (HAS_Z) zc.read(stage + here + In::kStageBytes + Plain::kStageBytes, l.half, l.li);
+        };
         if constexpr (kStaged) {
-            ac.read(stage, half, li);
-            gc.read(stage + In::kStageBytes, half, li);
-            xc.read(stage + 2 * In::kStageBytes, half, li);
-            oc.read(stage + 3 * In::kStageBytes, half, li);
-            if constexpr (HAS_Z) zc.read(stage + 3 * In::kStageBytes + Plain::kStageBytes, half, li);
+            const Place l(wave);
+            ac.read(stage, l.half, l.li);
+            gc.read(stage + In::kStageBytes, l.half, l.li);
+            read_twice();
             wait_lds_reads();
-            fetch(place(next));   // past the last ticket: a tile of no tokens, nothing is read
         }
-        // Of every token: a, r, w v, w i, 1 - i, (r / w) a^2 v, dy and dout silu'(z).
-        float A[kK][kV], R[kK][kV], B[kK][kV], W[kK][kV], O[kK][kV], U[kK][kV], Y[kK][kV], Z[kK][kV];
+        if constexpr (kStaged) fetch(place(next));   // past the last ticket: a tile of no tokens, nothing is read
+        // Of every token: a, r, w i, 1 - i and (r / w) a^2 v.
+        float A[kK][kV], R[kK][kV], W[kK][kV], O[kK][kV], U[kK][kV];
         float P[kV], H[kV], X[kV];
         auto maps = [&](auto gen) {
             constexpr bool GEN = decltype(gen)::value;
             static_for<kK>([&](auto kcc) {
                 constexpr int k = decltype(kcc)::value;
-                float ga[kV], gx[kV], x[kV], z[kV];
+                float ga[kV], gx[kV], x[kV], y[kV], z[kV];
                 ac.template take<k>(ga);
                 gc.template take<k>(gx);
                 xc.template take<k>(x);
-                oc.template take<k>(Y[k]);
+                oc.template take<k>(y);
                 if constexpr (HAS_Z) zc.template take<k>(z);
-                const bool start = GEN && ((st >> k) & 1u), out = GEN && tok + k >= t.nv;
+                const bool start = GEN && ((st >> k) & 1u), out = GEN && k >= left;
 #pragma unroll
                 for (int j = 0; j < kV; ++j) {
                     const float r = sigmoid_f(ga[j]);
@@ -186,31 +190,28 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
                     const float w = om * rw;
                     const float ig = sigmoid_f(gx[j]);
                     const float v = ig * x[j];
-                    if constexpr (HAS_Z) {
-                        const float sg = sigmoid_f(z[j]);
-                        Z[k][j] = Y[k][j] * (sg * __builtin_fmaf(z[j], 1.0f - sg, 1.0f));
-                        Y[k][j] *= z[j] * sg;
-                    }
+                    if constexpr (HAS_Z) y[j] *= silu_f(z[j]);
                     R[k][j] = r;
                     W[k][j] = w * ig;
                     O[k][j] = 1.0f - ig;
                     U[k][j] = (r * rw) * (al * al) * v;
-                    float bb = w * v;
+                    float bb = W[k][j] * x[j];
                     if constexpr (GEN) {
                         al = out ? 1.0f : al;
                         bb = out ? 0.0f : bb;
-                        Y[k][j] = out ? 0.0f : Y[k][j];
+                        y[j] = out ? 0.0f : y[j];
                     }
                     A[k][j] = al;
-                    B[k][j] = bb;
                     if constexpr (k == 0) {
                         P[j] = start ? -0.0f : al;
                         H[j] = bb;
-                        X[j] = start ? 0.0f : al * Y[k][j];
+                        X[j] = start ? 0.0f : al * y[j];
                     } else {
-                        P[j] = start ? -0.0f : P[j] * al;
-                        H[j] = start ? bb : __builtin_fmaf(al, H[j], bb);
-                        X[j] = apply<GEN>(P[j], X[j], Y[k][j]);
+                        float p = P[j] * al, h = __builtin_fmaf(al, H[j], bb);
+                        if constexpr (GEN) asm volatile("" : "+v"(p), "+v"(h));   // selects, not a branch
+                        P[j] = start ? -0.0f : p;
+                        H[j] = start ? bb : h;
+                        X[j] = apply<GEN>(P[j], X[j], y[j]);
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -220,52 +221,64 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
         else maps(std::false_type{});
 
         // what the wave's other half does before (forward) or after (adjoint), and the wave's maps
-        float fp[kV], fh[kV], rp[kV], rx[kV];
+        float op[kV], oh[kV];
+        {
+            const Place l(wave);
+            const int row = l.half ? wave : kWaves, rev = l.half ? kWaves : wave;
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            const float p1 = __shfl_xor(P[j], 32), h1 = __shfl_xor(H[j], 32), x1 = __shfl_xor(X[j], 32);
-            const int row = half ? wave : kWaves, rev = half ? kWaves : wave;
-            s_P[row][kV * li + j] = is_reset(P[j]) ? P[j] : P[j] * p1;
-            s_H[row][kV * li + j] = apply(P[j], H[j], h1);
-            s_X[rev][kV * li + j] = apply(P[j], X[j], x1);
-            fp[j] = half ? p1 : 1.0f;   // the first half's map, for the second
-            fh[j] = half ? h1 : 0.0f;
-            rp[j] = half ? 1.0f : p1;   // the second half's adjoint map, for the first
-            rx[j] = half ? 0.0f : x1;
+            for (int j = 0; j < kV; ++j) {
+                const float p1 = __shfl_xor(P[j], 32), h1 = __shfl_xor(H[j], 32), x1 = __shfl_xor(X[j], 32);
+                const float pw = is_reset(P[j]) ? P[j] : P[j] * p1;
+                s_map[row][kV * l.li + j] = make_float2(pw, apply(P[j], H[j], h1));
+                s_rev[rev][kV * l.li + j] = make_float2(pw, apply(P[j], X[j], x1));
+                op[j] = p1;   // the first half's map, for the second; the second half's adjoint map, for the first
+                oh[j] = l.half ? h1 : x1;
+            }
+        }
+        ChainWords::Seen seen = {};
+        auto words = [&]() {
+            const auto p = kernel_args<RecBwdKernelArgs>();
+            return walk.words(Chain{p->ch.map, p->ch.value, p->ch.next, p->ch.rate}, t);
+        };
+        int ticket = 0;   // wave 0's: the tile after the next one
+        if (wave == 0 && ntiles > 1) {
+            seen = words().peek(t.pos);
+            if (next < walk.tickets) ticket = draw();
         }
         lds_barrier();
         if (wave == 0) {   // a lane per channel: the adjoint entering the tile from the right, and its waves
-            const int d = t.ct * kTileChannels + lane;
+            const int lane = static_cast<int>(lane_now()), d = t.ct * kTileChannels + lane;
             const auto p = kernel_args<RecBwdKernelArgs>();
             const auto& a = p->a;
-            const ChainWords words = walk.words(Chain{p->ch.map, p->ch.value, p->ch.next, p->ch.rate}, t);
+            const ChainWords chain = words();
             float e = row_load(a.d_final_state, t.b, a.dim, d);
-            float mp = s_P[kWaves - 1][lane], mx = s_X[kWaves - 1][lane];
-            s_suf[kWaves - 1][lane] = make_float2(1.0f, 0.0f);
-#pragma unroll 3
+            float2 m = s_rev[kWaves - 1][lane];
+            s_rev[kWaves - 1][lane] = make_float2(1.0f, 0.0f);   // from here on of all behind a wave
+#pragma unroll 5
             for (int w = kWaves - 2; w >= 0; --w) {
-                s_suf[w][lane] = make_float2(mp, mx);
-                const float q = s_P[w][lane];
-                mx = apply(q, s_X[w][lane], mx);
-                mp = is_reset(q) ? q : q * mp;
+                float2 v = s_rev[w][lane];
+                s_rev[w][lane] = m;
+                compose(v.x, v.y, m.x, m.y);
+                m = v;
             }
-            if (t.pos + 1 < ntiles) words.publish_map(t.pos, mp, mx);
-            e = words.look_back(t.pos, e);
-            const float leaving = apply(mp, mx, e);
-            if (t.pos + 1 < ntiles) words.publish_value(t.pos, leaving);
+            if (t.pos + 1 < ntiles) chain.publish_map(t.pos, m.x, m.y);
+            e = chain.look_back(t.pos, e, seen);
+            const float leaving = apply(m.x, m.y, e);
+            if (t.pos + 1 < ntiles) chain.publish_value(t.pos, leaving);
             if (t.tile == 0) row_store(a.d_initial_state, t.b, a.dim, d, leaving);
             s_adj[lane] = e;
-            if (next < walk.tickets) s_ticket = draw();
+            s_ticket = __builtin_amdgcn_readfirstlane(ticket);
         } else if (wave == 1) {   // the states entering the waves
-            const int d = t.ct * kTileChannels + lane;
+            const int lane = static_cast<int>(lane_now()), d = t.ct * kTileChannels + lane;
             const auto p = kernel_args<RecBwdKernelArgs>();
             const auto& a = p->a;
             float h = a.states != nullptr ? row_load(a.states, t.b * ntiles + t.tile, a.dim, d)
                                           : row_load(a.initial_state, t.b, a.dim, d);
-#pragma unroll 2
+#pragma unroll 4
             for (int w = 0; w < kWaves; ++w) {
                 s_in[w][lane] = h;
-                h = apply(s_P[w][lane], s_H[w][lane], h);
+                const float2 m = s_map[w][lane];
+                h = apply(m.x, m.y, h);
             }
         } else if (wave == 2) {
             add_part();
@@ -281,35 +294,58 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
             const Rsrc to_g = rows_rsrc<esz>(p->a.dgate_x, t.row_tok, t.nv, dim, dim);
             const Rsrc to_z = rows_rsrc<esz>(p->a.dz, t.row_tok, HAS_Z ? t.nv : 0, dim, dim);
             const uint32_t step = static_cast<uint32_t>(dim) * esz;
-            uint32_t off = store_offset(tok + kK - 1, step, c * esz, c < dim);
+            const Place l(wave);
+            const int li = l.li, half = l.half, c = l.channel(t);
+            uint32_t off = store_offset(l.tok + kK - 1, step, c * esz, c < dim);
             auto put = [&](auto gen) {
                 constexpr bool GEN = decltype(gen)::value;
-                float hp[kK][kV], e[kV], sum[kV];
+                float h[kK + 1][kV], e[kV], sum[kV];   // the states before and behind the tokens
+                if constexpr (kStaged) read_twice();
 #pragma unroll
                 for (int j = 0; j < kV; ++j) {
-                    float h = apply<GEN>(fp[j], fh[j], s_in[wave][kV * li + j]);
+                    const float in = s_in[wave][kV * li + j];
+                    const float mid = apply<GEN>(op[j], oh[j], in);
+                    h[0][j] = half ? mid : in;
+                }
+                static_for<kK>([&](auto kcc) {
+                    constexpr int k = decltype(kcc)::value;
+                    float x[kV];
+                    xc.template take<k>(x);
 #pragma unroll
-                    for (int k = 0; k < kK; ++k) {
-                        hp[k][j] = h;
-                        h = GEN && ((st >> k) & 1u) ? B[k][j] : __builtin_fmaf(A[k][j], h, B[k][j]);
+                    for (int j = 0; j < kV; ++j) {
+                        const float b = W[k][j] * x[j];
+                        h[k + 1][j] = GEN && ((st >> k) & 1u) ? b : __builtin_fmaf(A[k][j], h[k][j], b);
                     }
-                    const float2 suf = s_suf[wave][kV * li + j];
-                    e[j] = apply<GEN>(rp[j], rx[j], apply(suf.x, suf.y, s_adj[kV * li + j]));
+                });
+#pragma unroll
+                for (int j = 0; j < kV; ++j) {
+                    const float2 suf = s_rev[wave][kV * li + j];
+                    const float in = apply(suf.x, suf.y, s_adj[kV * li + j]);
+                    const float mid = apply<GEN>(op[j], oh[j], in);
+                    e[j] = half ? in : mid;
                     sum[j] = 0.0f;
                 }
                 static_for<kK>([&](auto kcc) {
                     constexpr int k = kK - 1 - decltype(kcc)::value;
-                    float dx[kV], da[kV], dg[kV], dz[kV];
-                    const bool start = GEN && ((st >> k) & 1u), out = GEN && tok + k >= t.nv;
+                    float dx[kV], da[kV], dg[kV], dz[kV], x[kV], y[kV], z[kV];
+                    xc.template take<k>(x);
+                    oc.template take<k>(y);
+                    if constexpr (HAS_Z) zc.template take<k>(z);
+                    const bool start = GEN && ((st >> k) & 1u), out = GEN && k >= left;
 #pragma unroll
                     for (int j = 0; j < kV; ++j) {
-                        const float G = Y[k][j] + e[j];
-                        const float ah = start ? 0.0f : A[k][j] * hp[k][j];
+                        const float ah = start ? 0.0f : A[k][j] * h[k][j];
+                        if constexpr (HAS_Z) {
+                            const float sg = sigmoid_f(z[j]);
+                            dz[j] = y[j] * (sg * __builtin_fmaf(z[j], 1.0f - sg, 1.0f)) * h[k + 1][j];
+                            y[j] *= z[j] * sg;
+                        }
+                        if constexpr (GEN) y[j] = out ? 0.0f : y[j];
+                        const float G = y[j] + e[j];
                         dx[j] = G * W[k][j];
-                        dg[j] = G * B[k][j] * O[k][j];
+                        dg[j] = dx[j] * x[j] * O[k][j];
                         const float q = G * __builtin_fmaf(R[k][j], ah, -U[k][j]);
                         da[j] = (kLn2 * rc[j]) * (1.0f - R[k][j]) * q;   // kLn2 rate = -c softplus(a_param)
-                        if constexpr (HAS_Z) dz[j] = Z[k][j] * (ah + B[k][j]);
                         sum[j] += out ? 0.0f : q;
                         e[j] = start ? 0.0f : A[k][j] * G;
                     }
