@@ -38,7 +38,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
     __shared__ float s_in[kTileChannels];                 // the values entering the tile
     __shared__ float2 s_agg[kWaves + 1][kTileChannels];   // the waves' maps; the last row takes what no one reads
     __shared__ float2 s_pre[kWaves][kTileChannels];       // the maps of all before a wave
-    __shared__ int s_ticket;
+    __shared__ int s_ticket, s_second;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane % kRow, half = lane / kRow;
     const auto first = kernel_args<RecFwdKernelArgs>();
@@ -87,19 +87,21 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
 
     int cur, next;
     if (ntiles > 1) {
-        if (wave == 0) s_ticket = __builtin_amdgcn_readfirstlane(draw());
+        if (wave == 0) {   // both tickets are under way together
+            const int t0 = draw();
+            int t1 = kNone;
+            if (!walk.once) t1 = draw();
+            s_ticket = __builtin_amdgcn_readfirstlane(t0);
+            s_second = __builtin_amdgcn_readfirstlane(t1);
+        }
         lds_barrier();
         cur = __builtin_amdgcn_readfirstlane(s_ticket);
-        lds_barrier();
-        if (wave == 0) s_ticket = __builtin_amdgcn_readfirstlane(draw());
+        next = __builtin_amdgcn_readfirstlane(s_second);
         if (cur >= walk.tickets) return;
         fetch(place(cur));
-        lds_barrier();
-        next = __builtin_amdgcn_readfirstlane(s_ticket);
-        lds_barrier();
     } else {
         cur = static_cast<int>(blockIdx.x);
-        next = 0x7fffffff;
+        next = kNone;
         const Tile t = place(cur);
         fetch(t);
         if (threadIdx.x < kTileChannels) {
@@ -131,15 +133,6 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
             wait_lds_reads();
         }
         fetch(place(next));
-        if constexpr (SAVE) {
-            const auto p = kernel_args<RecFwdKernelArgs>();
-            const auto& a = p->a;
-            const int64_t rows = a.batch * a.seqlen;
-            save_packed<T, ALIGNED, kK>(xc, a.save[0], t, tok, c, dim, rows);
-            save_packed<T, ALIGNED, kK>(ac, a.save[1], t, tok, c, dim, rows);
-            save_packed<T, ALIGNED, kK>(gc, a.save[2], t, tok, c, dim, rows);
-            if constexpr (HAS_Z) save_packed<T, ALIGNED, kK>(zc, a.save[3], t, tok, c, dim, rows);
-        }
         // Maps of the lane's tokens from its first one on.  GEN: the tile has document
         // starts or ends behind the row (decided for the whole workgroup).
         float P[kK][kV], H[kK][kV];
@@ -226,6 +219,15 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
             row_store(a.states, t.b * ntiles + t.tile, a.dim, d, in);
             s_in[lane] = in;
             s_ticket = __builtin_amdgcn_readfirstlane(ticket);
+        }
+        if constexpr (SAVE) {   // while wave 0 waits for the value entering
+            const auto p = kernel_args<RecFwdKernelArgs>();
+            const auto& a = p->a;
+            const int64_t rows = a.batch * a.seqlen;
+            save_packed<T, ALIGNED, kK>(xc, a.save[0], t, tok, c, dim, rows);
+            save_packed<T, ALIGNED, kK>(ac, a.save[1], t, tok, c, dim, rows);
+            save_packed<T, ALIGNED, kK>(gc, a.save[2], t, tok, c, dim, rows);
+            if constexpr (HAS_Z) save_packed<T, ALIGNED, kK>(zc, a.save[3], t, tok, c, dim, rows);
         }
         lds_barrier();
         if constexpr (OUT) {

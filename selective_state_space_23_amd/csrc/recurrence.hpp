@@ -38,15 +38,11 @@ __device__ __forceinline__ void unpack(const Raw<T, V>& r, float (&v)[V]) {
     }
 }
 
-// Codes of V channels (bytes) times the block's scale.  A code q is decoded as
-// (q + 128) s - 128 s: the flipped sign bit makes the byte unsigned, which the
-// hardware converts in one instruction, and the fma rounds once.
+// Codes of V channels (bytes) times the block's scale: rounded once.
 template <int V>
 __device__ __forceinline__ void decode(uint32_t codes, float s, float (&v)[V]) {
-    const uint32_t u = codes ^ 0x80808080u;
-    const float off = -128.0f * s;
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = __builtin_fmaf(static_cast<float>((u >> (8 * j)) & 0xffu), s, off);
+    for (int j = 0; j < V; ++j) v[j] = static_cast<float>(static_cast<int8_t>(codes >> (8 * j))) * s;
 }
 
 // A tile's rows of one tensor as a buffer: `n` tokens of `dim` channels, `ld`
@@ -279,13 +275,16 @@ __device__ __forceinline__ void block_scale(uint32_t mbits, float& scale, float&
 template <int V>
 __device__ __forceinline__ uint32_t encode(const float (&v)[V], float inv) {
 #pragma clang fp contract(off)
-    uint32_t w = 0;
+    static_assert(V % 2 == 0);
+    uint32_t w[V / 2];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const float t = v[j] * inv;
-        w |= (__float_as_uint(t + 12582912.0f) & 0xffu) << (8 * j);
+    for (int j = 0; j < V; j += 2) {
+        const float lo = v[j] * inv, hi = v[j + 1] * inv;
+        // byte 0 of both
+        w[j / 2] = __builtin_amdgcn_perm(__float_as_uint(hi + 12582912.0f), __float_as_uint(lo + 12582912.0f), 0x0c0c0400u);
     }
-    return w;
+    if constexpr (V == 2) return w[0];
+    else return w[0] | (w[1] << 16);
 }
 
 // Affine maps h -> P h + H of stretches of tokens.  The sign of P marks a map
@@ -484,21 +483,30 @@ __device__ __forceinline__ void save_packed(const LaneIn<T, ALIGNED, false, K>& 
                                             int tok, int c, int dim, int64_t rows) {
     static_assert(K == 8, "the halving below is written for eight tokens");
     const int li = threadIdx.x & 15;
-    uint32_t m[8], keep[kV];   // magnitude bits of the channels that exist
+    // Magnitude bits of the channels that exist: bfloat16 ones as halves of a word, whose
+    // maxima are taken side by side.
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    uint32_t keep[kV];
 #pragma unroll
     for (int j = 0; j < kV; ++j) keep[j] = c + j < dim ? 0x7fffffffu : 0u;
+    uint32_t m[8];
     static_for<8>([&](auto kc) {
         constexpr int k = decltype(kc)::value;
-        float v[kV];
-        in.template get<k>(v);
-        m[k] = 0;
-#pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            const uint32_t b = __float_as_uint(v[j]) & keep[j];
-            m[k] = b > m[k] ? b : m[k];
+        if constexpr (sizeof(T) == 2) {
+            m[k] = in.r[k].w[0] & ((keep[0] >> 16) | (keep[1] & 0xffff0000u));
+        } else {
+            const uint32_t a = in.r[k].w[0] & keep[0], b = in.r[k].w[1] & keep[1];
+            m[k] = a > b ? a : b;
         }
     });
-    auto umax = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
+    auto umax = [](uint32_t x, uint32_t y) {
+        if constexpr (sizeof(T) == 2) {
+            const u16x2 a = __builtin_bit_cast(u16x2, x), b = __builtin_bit_cast(u16x2, y);
+            return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(a, b));
+        } else {
+            return x > y ? x : y;
+        }
+    };
     const bool b3 = li & 8, b2 = li & 4, b1 = li & 2;
     uint32_t m4[4], m2[2];
 #pragma unroll
@@ -509,6 +517,10 @@ __device__ __forceinline__ void save_packed(const LaneIn<T, ALIGNED, false, K>& 
     uint32_t m1 = umax(b1 ? m2[1] : m2[0], dpp_u32<0x4E>(b1 ? m2[0] : m2[1]));   // quad_perm [2, 3, 0, 1]
     m1 = umax(m1, dpp_u32<0xB1>(m1));                                            // quad_perm [1, 0, 3, 2]
     m1 = umax(m1, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m1), 16)));
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t lo = m1 << 16, hi = m1 & 0xffff0000u;
+        m1 = lo > hi ? lo : hi;
+    }
     float scale, inv;
     block_scale(m1, scale, inv);
     const Rsrc ss = tile_rsrc(p.scale + t.ct * rows + t.row_tok, t.nv * 4);
@@ -559,7 +571,7 @@ __host__ __device__ inline int chain_groups(int64_t nchain) {
     return nchain % 8 == 0 ? 8 : nchain % 4 == 0 ? 4 : nchain % 2 == 0 ? 2 : 1;
 }
 
-constexpr int kLook = 4;             // earlier positions looked at
+constexpr int kLook = 2;             // earlier positions looked at
 constexpr int kMaxPolls = 1 << 22;   // about a microsecond each
 
 __device__ __forceinline__ uint32_t not_all_ones(float x) {
@@ -642,10 +654,13 @@ struct ChainWords {
     }
 };
 
+constexpr int kNone = 0x7fffffff;   // a ticket behind all others
+
 // The tiles a workgroup draws: tickets of its group, position by position over the
 // group's chains.
 struct Walk {
     int nct, ntiles, groups, group, per_group, tickets;
+    bool once;   // a workgroup for every tile
     __device__ __forceinline__ void init(int nct_, int ntiles_, int batch) {
         nct = nct_;
         ntiles = ntiles_;
@@ -653,6 +668,7 @@ struct Walk {
         group = static_cast<int>(blockIdx.x) % groups;
         per_group = nct * batch / groups;
         tickets = per_group * ntiles;
+        once = static_cast<unsigned>(tickets) * groups <= gridDim.x;
     }
     // By a whole wave: lane 0 adds 1 at agent scope, the other lanes' offsets lie
     // past the counter.  The ticket is lane 0's.

@@ -43,7 +43,7 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
     // the last row of an array takes what no one reads
     __shared__ float2 s_map[kWaves + 1][kTileChannels], s_rev[kWaves + 1][kTileChannels];   // (P, H) and (P, X)
     __shared__ float s_in[kWaves][kTileChannels], s_adj[kTileChannels], s_sum[kWaves + 1][kTileChannels];
-    __shared__ int s_ticket;
+    __shared__ int s_ticket, s_second;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     using Place = LanePlace<kK>;
     const auto first = kernel_args<RecBwdKernelArgs>();
@@ -98,19 +98,21 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
 
     int cur, next;
     if (ntiles > 1) {
-        if (wave == 0) s_ticket = __builtin_amdgcn_readfirstlane(draw());
+        if (wave == 0) {   // both tickets are under way together
+            const int t0 = draw();
+            int t1 = kNone;
+            if (!walk.once) t1 = draw();
+            s_ticket = __builtin_amdgcn_readfirstlane(t0);
+            s_second = __builtin_amdgcn_readfirstlane(t1);
+        }
         lds_barrier();
         cur = __builtin_amdgcn_readfirstlane(s_ticket);
-        lds_barrier();
-        if (wave == 0) s_ticket = __builtin_amdgcn_readfirstlane(draw());
+        next = __builtin_amdgcn_readfirstlane(s_second);
         if (cur >= walk.tickets) return;
         if constexpr (kStaged) fetch(place(cur));
-        lds_barrier();
-        next = __builtin_amdgcn_readfirstlane(s_ticket);
-        lds_barrier();
     } else {
         cur = static_cast<int>(blockIdx.x);
-        next = 0x7fffffff;
+        next = kNone;
         const Tile t = place(cur);
         fetch(t);
         if (threadIdx.x < kTileChannels) {
@@ -254,12 +256,19 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
             float e = row_load(a.d_final_state, t.b, a.dim, d);
             float2 m = s_rev[kWaves - 1][lane];
             s_rev[kWaves - 1][lane] = make_float2(1.0f, 0.0f);   // from here on of all behind a wave
-#pragma unroll 5
-            for (int w = kWaves - 2; w >= 0; --w) {
-                float2 v = s_rev[w][lane];
-                s_rev[w][lane] = m;
-                compose(v.x, v.y, m.x, m.y);
-                m = v;
+            constexpr int kRows = 5;   // read ahead of the chain of compositions
+            static_assert((kWaves - 1) % kRows == 0);
+#pragma unroll 1
+            for (int w = kWaves - 2; w >= 0; w -= kRows) {
+                float2 v[kRows];
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) v[i] = s_rev[w - i][lane];
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    s_rev[w - i][lane] = m;
+                    compose(v[i].x, v[i].y, m.x, m.y);
+                    m = v[i];
+                }
             }
             if (t.pos + 1 < ntiles) chain.publish_map(t.pos, m.x, m.y);
             e = chain.look_back(t.pos, e, seen);
@@ -274,11 +283,16 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
             const auto& a = p->a;
             float h = a.states != nullptr ? row_load(a.states, t.b * ntiles + t.tile, a.dim, d)
                                           : row_load(a.initial_state, t.b, a.dim, d);
-#pragma unroll 4
-            for (int w = 0; w < kWaves; ++w) {
-                s_in[w][lane] = h;
-                const float2 m = s_map[w][lane];
-                h = apply(m.x, m.y, h);
+#pragma unroll 1
+            for (int w = 0; w < kWaves; w += 4) {
+                float2 m[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m[i] = s_map[w + i][lane];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s_in[w + i][lane] = h;
+                    h = apply(m[i].x, m[i].y, h);
+                }
             }
         } else if (wave == 2) {
             add_part();
@@ -383,8 +397,10 @@ __global__ __launch_bounds__(1024) void rec_bwd_reduce_kernel(const float* __res
     const int o = threadIdx.x & 63, g = threadIdx.x >> 6;
     const int d = static_cast<int>(blockIdx.x) * 64 + o;
     float s = 0.0f;
-    if (d < dim)
+    if (d < dim) {
+#pragma unroll 8
         for (int64_t i = g; i < nparts; i += 16) s += part[i * dim + d];
+    }
     red[g][o] = s;
     __syncthreads();
     if (g != 0 || d >= dim) return;
