@@ -275,7 +275,7 @@ __global__ __launch_bounds__(256) void rec_clear_kernel(uint4* __restrict__ word
                                                         const float* __restrict__ a_param, int dim, float c) {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i < n) words[i] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
-    if (i < 8) next[i] = 0;
+    if (i == 0) next[0] = 0;
     if (i < nrate) rate[i] = -c * kLog2e * softplus_exact(a_param[i < dim ? i : dim - 1]);
 }
 

@@ -227,18 +227,17 @@ __device__ __forceinline__ float sigmoid_f(float v) { return rcp_fast(1.0f + exp
 
 // The decay a = 2^la2 and 1 - a^2 for la2 = log2 a <= 0.  1 - a^2 cancels where a
 // is near 1: with y = -2 log a it is y p(y) there, p a degree-4 Chebyshev
-// interpolant of (1 - e^-y) / y on [0, 0.35], off by at most 3e-8 of it.  Above
-// 0.35 the subtraction loses at most two bits.
+// interpolant of (1 - e^-y) / y on [0, 0.35] written in la2 = -y / (2 log 2), off by
+// at most 4e-8 of it.  Above 0.35 the subtraction loses at most two bits.
 __device__ __forceinline__ void decay_terms(float la2, float& a, float& om) {
     a = exp2_fast(la2);
-    const float y = (-2.0f * kLn2) * la2;
-    float p = __builtin_fmaf(y, 0.00721255037933588f, -0.04133278876543045f);
-    p = __builtin_fmaf(y, p, 0.1666254997253418f);
-    p = __builtin_fmaf(y, p, -0.49999821186065674f);
-    p = __builtin_fmaf(y, p, 1.0f);
-    float near = y * p, far = __builtin_fmaf(-a, a, 1.0f);
+    float p = __builtin_fmaf(la2, -0.03692888095974922f, -0.1526569277048111f);
+    p = __builtin_fmaf(la2, p, -0.4439232051372528f);
+    p = __builtin_fmaf(la2, p, -0.9609025716781616f);
+    p = __builtin_fmaf(la2, p, -1.3862943649291992f);
+    float near = la2 * p, far = __builtin_fmaf(-a, a, 1.0f);
     asm volatile("" : "+v"(near), "+v"(far));   // both formed: the choice stays a select, not a branch
-    om = y < 0.35f ? near : far;
+    om = la2 > -0.25247162580490112f ? near : far;
 }
 
 // Value of lane `16 * (lane / 16) + N` in every lane of the row of 16
@@ -423,9 +422,12 @@ template <typename T, bool ALIGNED, bool PIN, int K> struct LaneIn {
     // The same, unpacked here and not where the compiler could do it for several
     // uses at once (twice the registers across everything in between).
     template <int k> __device__ __forceinline__ void take(float (&v)[kV]) {
-#pragma unroll
-        for (auto& w : r[k].w) asm volatile("" : "+v"(w));
-        unpack(r[k], v);
+        if constexpr (sizeof(T) == 2) {
+            asm volatile("v_lshlrev_b32 %0, 16, %1" : "=v"(v[0]) : "v"(r[k].w[0]));
+            asm volatile("v_and_b32 %0, 0xffff0000, %1" : "=v"(v[1]) : "v"(r[k].w[0]));
+        } else {
+            unpack(r[k], v);
+        }
     }
 };
 template <typename T, bool ALIGNED, int K> struct LaneIn<T, ALIGNED, true, K> {
@@ -551,7 +553,7 @@ __device__ __forceinline__ void save_packed(const LaneIn<T, ALIGNED, false, K>& 
 // with that pattern is stored as the usual one.
 //
 // Every wait ends: workgroups draw tiles by tickets, position by position over the
-// chains of a group, and work on them in the order drawn.  The positions a
+// chains (so that neighbours in a row, whose lines meet, are near in time), and work on them in the order drawn.  The positions a
 // workgroup waits for have lower tickets: of the tickets not yet worked off, the
 // lowest is the current one of a workgroup that runs, and all that it waits for is
 // published.  Against a workspace that another call overwrites meanwhile (which
@@ -560,16 +562,9 @@ __device__ __forceinline__ void save_packed(const LaneIn<T, ALIGNED, false, K>& 
 struct Chain {
     uint64_t* map;     // [chain][position][64]
     uint32_t* value;   // [chain][position][64]
-    uint32_t* next;    // [group]: tickets drawn
+    uint32_t* next;    // tickets drawn
     const float* rate; // [64 * channel tiles]: -c log2(e) softplus(a_param)
 };
-
-// Chains in groups of neighbours, each group with its own ticket counter and the
-// workgroups of one blockIdx % 8 (one XCD, as they are dealt out): as many groups, up
-// to 8, as divide the chains evenly.
-__host__ __device__ inline int chain_groups(int64_t nchain) {
-    return nchain % 8 == 0 ? 8 : nchain % 4 == 0 ? 4 : nchain % 2 == 0 ? 2 : 1;
-}
 
 constexpr int kLook = 2;             // earlier positions looked at
 constexpr int kMaxPolls = 1 << 22;   // about a microsecond each
@@ -656,34 +651,30 @@ struct ChainWords {
 
 constexpr int kNone = 0x7fffffff;   // a ticket behind all others
 
-// The tiles a workgroup draws: tickets of its group, position by position over the
-// group's chains.
+// The tiles a workgroup draws: by tickets, position by position over the chains.
 struct Walk {
-    int nct, ntiles, groups, group, per_group, tickets;
+    int nct, ntiles, chains, tickets;
     bool once;   // a workgroup for every tile
     __device__ __forceinline__ void init(int nct_, int ntiles_, int batch) {
         nct = nct_;
         ntiles = ntiles_;
-        groups = ntiles > 1 ? chain_groups(static_cast<int64_t>(nct) * batch) : 1;
-        group = static_cast<int>(blockIdx.x) % groups;
-        per_group = nct * batch / groups;
-        tickets = per_group * ntiles;
-        once = static_cast<unsigned>(tickets) * groups <= gridDim.x;
+        chains = nct * batch;
+        tickets = chains * ntiles;
+        once = static_cast<unsigned>(tickets) <= gridDim.x;
     }
     // By a whole wave: lane 0 adds 1 at agent scope, the other lanes' offsets lie
     // past the counter.  The ticket is lane 0's.
     __device__ __forceinline__ int draw(uint32_t* next) const {
-        const Rsrc rs = tile_rsrc(next + group, 4);
-        return __builtin_amdgcn_raw_ptr_buffer_atomic_add_i32(1, rs, lane_now() == 0 ? 0u : kNoStore, 0,
-                                                              kAgentScope);
+        const Rsrc rs = tile_rsrc(next, 4);
+        return __builtin_amdgcn_raw_ptr_buffer_atomic_add_i32(1, rs, lane_now() == 0 ? 0u : kNoStore, 0, kAgentScope);
     }
     // The tile of a ticket, counted from the row's end with REVERSE; of no tokens
     // past the last ticket.
     template <bool REVERSE>
     __device__ __forceinline__ Tile place(int ticket, int64_t seqlen) const {
         Tile t;
-        const int chain = group * per_group + ticket % per_group;   // neighbours share an L2
-        t.pos = ticket / per_group;
+        const int chain = ticket % chains;
+        t.pos = ticket / chains;
         t.tile = REVERSE ? ntiles - 1 - t.pos : t.pos;
         t.ct = chain % nct;
         t.b = chain / nct;

@@ -299,6 +299,24 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
             part_row = t.b * ntiles + t.tile;
             part_channel = t.ct * kTileChannels;
         }
+        // Meanwhile of every token dy and dout silu'(z).
+        float Y[kK][kV], Z[kK][kV];
+        if constexpr (HAS_Z) {
+            if constexpr (kStaged) read_twice();
+            static_for<kK>([&](auto kcc) {
+                constexpr int k = decltype(kcc)::value;
+                float y[kV], z[kV];
+                oc.template take<k>(y);
+                zc.template take<k>(z);
+#pragma unroll
+                for (int j = 0; j < kV; ++j) {
+                    const float sg = sigmoid_f(z[j]);
+                    Z[k][j] = y[j] * (sg * __builtin_fmaf(z[j], 1.0f - sg, 1.0f));
+                    Y[k][j] = y[j] * (z[j] * sg);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        }
         lds_barrier();
         {
             constexpr int esz = Elem<T>::kBytes;
@@ -341,18 +359,16 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
                 }
                 static_for<kK>([&](auto kcc) {
                     constexpr int k = kK - 1 - decltype(kcc)::value;
-                    float dx[kV], da[kV], dg[kV], dz[kV], x[kV], y[kV], z[kV];
+                    float dx[kV], da[kV], dg[kV], dz[kV], x[kV], y[kV];
                     xc.template take<k>(x);
-                    oc.template take<k>(y);
-                    if constexpr (HAS_Z) zc.template take<k>(z);
+                    if constexpr (!HAS_Z) oc.template take<k>(y);
                     const bool start = GEN && ((st >> k) & 1u), out = GEN && k >= left;
 #pragma unroll
                     for (int j = 0; j < kV; ++j) {
                         const float ah = start ? 0.0f : A[k][j] * h[k][j];
                         if constexpr (HAS_Z) {
-                            const float sg = sigmoid_f(z[j]);
-                            dz[j] = y[j] * (sg * __builtin_fmaf(z[j], 1.0f - sg, 1.0f)) * h[k + 1][j];
-                            y[j] *= z[j] * sg;
+                            dz[j] = Z[k][j] * h[k + 1][j];
+                            y[j] = Y[k][j];
                         }
                         if constexpr (GEN) y[j] = out ? 0.0f : y[j];
                         const float G = y[j] + e[j];
