@@ -23,9 +23,15 @@ namespace {
 
 using namespace rec;
 
-constexpr int kK = 4;                              // tokens a lane walks
-constexpr int kWaves = kTileTokens / (2 * kK);     // two halves of 32 lanes a wave
-constexpr int kThreads = kWaves * 64;
+// Inputs of 16 bits are staged in LDS and 4 waves share a SIMD; unaligned ones are read
+// into registers, and so is float32 (too large to stage): twice the tokens in twice the
+// registers of half as many waves.
+template <typename T, bool ALIGNED> struct Shape {
+    static constexpr bool kStaged = sizeof(T) == 2 && ALIGNED;
+    static constexpr int kK = sizeof(T) == 2 ? 4 : 8;                 // tokens a lane walks
+    static constexpr int kWaves = kTileTokens / (2 * kK);             // two halves of 32 lanes a wave
+    static constexpr int kThreads = kWaves * 64;
+};
 
 struct RecBwdKernelArgs {
     RecBwdArgs a;
@@ -38,7 +44,9 @@ struct RecBwdKernelArgs {
 // the forward does; everything the gradients need of a token is formed once, before
 // the adjoint entering the tile is known, and kept in registers.
 template <typename T, bool ALIGNED, bool PIN, bool HAS_Z>
-__global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArgs) {
+__global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(const RecBwdKernelArgs) {
+    constexpr bool kStaged = Shape<T, ALIGNED>::kStaged;
+    constexpr int kK = Shape<T, ALIGNED>::kK, kWaves = Shape<T, ALIGNED>::kWaves;
     __shared__ float s_rate[kTileChannels];
     // the last row of an array takes what no one reads
     __shared__ float2 s_map[kWaves + 1][kTileChannels], s_rev[kWaves + 1][kTileChannels];   // (P, H) and (P, X)
@@ -55,7 +63,6 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
 
     // The next tile's inputs: staged in LDS (each wave its own part) while a tile is
     // worked off; float32 (too large) and unaligned ones are loaded at its start.
-    constexpr bool kStaged = sizeof(T) == 2 && ALIGNED;
     using In = LaneIn<T, ALIGNED, PIN, kK>;
     using Plain = LaneIn<T, ALIGNED, false, kK>;
     // x, dout and z are read twice, at both ends of a tile, and so have two places each.
@@ -219,7 +226,9 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
                 __builtin_amdgcn_sched_barrier(0);
             });
         };
-        if (general) maps(std::true_type{});
+        // (Not staged: one form for both, or the compiler moves what they share, and its
+        // registers, ahead of the choice.)
+        if (general || !kStaged) maps(std::true_type{});
         else maps(std::false_type{});
 
         // what the wave's other half does before (forward) or after (adjoint), and the wave's maps
@@ -256,7 +265,7 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
             float e = row_load(a.d_final_state, t.b, a.dim, d);
             float2 m = s_rev[kWaves - 1][lane];
             s_rev[kWaves - 1][lane] = make_float2(1.0f, 0.0f);   // from here on of all behind a wave
-            constexpr int kRows = 5;   // read ahead of the chain of compositions
+            constexpr int kRows = kWaves == 16 ? 5 : 7;   // read ahead of the chain of compositions
             static_assert((kWaves - 1) % kRows == 0);
 #pragma unroll 1
             for (int w = kWaves - 2; w >= 0; w -= kRows) {
@@ -391,7 +400,7 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(const RecBwdKernelArg
                     s_sum[half ? kWaves : wave][kV * li + j] = sum[j];
                 }
             };
-            if (general) put(std::true_type{});
+            if (general || !kStaged) put(std::true_type{});
             else put(std::false_type{});
         }
         if (next >= walk.tickets) break;
@@ -426,7 +435,7 @@ __global__ __launch_bounds__(1024) void rec_bwd_reduce_kernel(const float* __res
     da_param[d] = -c * t * sigmoid_f(a_param[d]);
 }
 
-constexpr int kResident = 256;   // one workgroup of 16 waves a CU
+constexpr int kResident = 256;   // one workgroup a CU
 
 struct BwdWs {
     size_t part, chain, states, fwd, total;
@@ -469,8 +478,8 @@ hipError_t launch_bwd(const RecBwdArgs& a) {
     }
     if ((e = clear_chains(ws + w.chain, a.batch, a.dim, ntiles, a.a_param, a.c, &k.ch, a.stream)) != hipSuccess) return e;
     const int64_t grid = ntiles > 1 && tiles > kResident ? kResident : tiles;
-    hipLaunchKernelGGL((rec_bwd_kernel<T, ALIGNED, PIN, HAS_Z>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
-                       a.stream, k);
+    hipLaunchKernelGGL((rec_bwd_kernel<T, ALIGNED, PIN, HAS_Z>), dim3(static_cast<unsigned>(grid)),
+                       dim3(Shape<T, ALIGNED>::kThreads), 0, a.stream, k);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL(rec_bwd_reduce_kernel, dim3(static_cast<unsigned>((a.dim + 63) / 64)), dim3(1024), 0, a.stream,
                        k.part, a.a_param, a.da_param, a.batch * ntiles, static_cast<int>(a.dim), a.c);
