@@ -92,14 +92,13 @@ def _dtype_code(t) -> int:
 def _ptr(t, name, device, dtype=None, shape=None) -> Optional[int]:
     if t is None:
         return None
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -583,7 +582,7 @@ def _strided(t, name, dev, dtype, shape):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -843,7 +842,7 @@ def gated_recurrence_update(state, x, gate_a, gate_x, a_param, z=None, reset=Non
     if reset is not None and reset.dtype == torch.bool:
         reset = reset.to(torch.uint8)
     if out is None:
-        out = torch.empty((Bt, Dm), dtype=dt, device=dev)
+        out = torch.empty(shape, dtype=dt, device=dev)
     px, lx = _strided(x, "x", dev, dt, shape)
     pa, la = _strided(gate_a, "gate_a", dev, dt, shape)
     pg, lg = _strided(gate_x, "gate_x", dev, dt, shape)
@@ -851,8 +850,8 @@ def gated_recurrence_update(state, x, gate_a, gate_x, a_param, z=None, reset=Non
     dims = _recurrence_dims(Bt, 1, Dm, _dtype_code(x), c, (lx, la, lg, lz, 0))
     with _on_device(dev):
         st = _lib.load().mamba_gated_recurrence_update(
-            ctypes.byref(dims), _ptr(state, "state", dev, f32, (Bt, Dm)), px, pa, pg,
+            ctypes.byref(dims), _ptr(state, "state", dev, f32, shape), px, pa, pg,
             _ptr(a_param, "a_param", dev, f32, (Dm,)), pz, _ptr(reset, "reset", dev, torch.uint8, (Bt,)),
-            _ptr(out, "out", dev, dt, (Bt, Dm)), _stream(dev))
+            _ptr(out, "out", dev, dt, shape), _stream(dev))
     _lib.check(st, "mamba_gated_recurrence_update")
     return out
