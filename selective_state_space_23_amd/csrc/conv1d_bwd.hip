@@ -54,6 +54,27 @@ template <> struct VecIO<float, 2> {
 
 namespace {
 
+// VEC consecutive channels of a token as stored, at element offset off + d0.
+template <typename T, int VEC> struct VecRaw {
+    using type = typename std::conditional<sizeof(T) * VEC == 8, uint2,
+                                           typename std::conditional<sizeof(T) * VEC == 4, uint32_t, uint16_t>::type>::type;
+    __device__ __forceinline__ static type load(const void* base, int64_t off, int d0) {
+        const char* p = static_cast<const char*>(base) + off * static_cast<int64_t>(sizeof(T));
+        return *reinterpret_cast<const type*>(p + static_cast<uint32_t>(d0) * static_cast<uint32_t>(sizeof(T)));
+    }
+    __device__ __forceinline__ static void get(const type& r, float (&v)[VEC]) {
+        if constexpr (sizeof(T) == 2) {
+            v[0] = __uint_as_float(static_cast<uint32_t>(r) << 16);
+            if constexpr (VEC == 2) v[1] = __uint_as_float(static_cast<uint32_t>(r) & 0xffff0000u);
+        } else if constexpr (VEC == 2) {
+            v[0] = __uint_as_float(r.x);
+            v[1] = __uint_as_float(r.y);
+        } else {
+            v[0] = __uint_as_float(r);
+        }
+    }
+};
+
 constexpr int kTile = 48;          // tokens per thread; kTile + 6 <= 64 for one ballot
 constexpr int kBlock = 256;
 
@@ -62,25 +83,33 @@ constexpr int kBlock = 256;
 // thread lie in one block: its scale comes with one 4-byte load per token, the
 // same address in the lanes of a block.
 template <typename T, int VEC> struct PlainX {
+    using Raw = typename VecRaw<T, VEC>::type;
     const void* __restrict__ x;
+    __device__ __forceinline__ Raw fetch(int64_t token, int dim, int d0) const {
+        return VecRaw<T, VEC>::load(x, token * dim, d0);
+    }
+    __device__ __forceinline__ static void get(const Raw& r, float (&v)[VEC]) { VecRaw<T, VEC>::get(r, v); }
     __device__ __forceinline__ void load(int64_t token, int dim, int d0, float (&v)[VEC]) const {
         VecIO<T, VEC>::load(x, token * dim + d0, v);
     }
 };
 template <int VEC> struct PackedX {
+    struct Raw { uint32_t q; float s; };
     const int8_t* __restrict__ q;
     const float* __restrict__ scale;
     int64_t tokens;
+    __device__ __forceinline__ Raw fetch(int64_t token, int dim, int d0) const {
+        const uint32_t d = static_cast<uint32_t>(d0);
+        const int8_t* p = q + token * dim;
+        const uint32_t w = VEC == 2 ? *reinterpret_cast<const uint16_t*>(p + d) : static_cast<uint8_t>(p[d]);
+        return Raw{w, scale[(d0 / kPackBlock) * tokens + token]};
+    }
+    __device__ __forceinline__ static void get(const Raw& r, float (&v)[VEC]) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) v[k] = static_cast<float>(static_cast<int8_t>(r.q >> (8 * k))) * r.s;
+    }
     __device__ __forceinline__ void load(int64_t token, int dim, int d0, float (&v)[VEC]) const {
-        const float s = scale[(d0 / kPackBlock) * tokens + token];
-        const int8_t* p = q + token * dim + d0;
-        if constexpr (VEC == 2) {
-            const uint32_t w = *reinterpret_cast<const uint16_t*>(p);
-            v[0] = static_cast<float>(static_cast<int8_t>(w & 0xff)) * s;
-            v[1] = static_cast<float>(static_cast<int8_t>(w >> 8)) * s;
-        } else {
-            v[0] = static_cast<float>(p[0]) * s;
-        }
+        get(fetch(token, dim, d0), v);
     }
 };
 
@@ -154,71 +183,138 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(
     for (int k = 0; k < 3; ++k)
         if ((starts >> k) & 1ull) since = 3 - k;
     const int64_t own_end = (t0 + kTile < seqlen) ? t0 + kTile : seqlen;
-    // x and du of the next token are fetched while the current one computes.
-    auto fetch = [&](int64_t t, float (&xv)[VEC], float (&gv)[VEC]) {
-        if (t < seqlen) {
-            x.load(row + t, dim, d0, xv);
-            VecIO<T, VEC>::load(du, (row + t) * dim + d0, gv);
-        } else {
+    // Tiles inside a row without a document start among their tokens, the 3 before and
+    // the 3 after take every tap: the same operations without the masks, four tokens at a
+    // time, the next four under way.
+    const bool all_taps = t0 >= 3 && t0 + kTile + 3 <= seqlen && (starts & ((1ull << (kTile + 6)) - 1)) == 0;
+    if (all_taps) {
+        constexpr int kStep = 4;
+        static_assert(kTile % kStep == 0);
+        typename X::Raw xn[kStep];
+        typename VecRaw<T, VEC>::type gn[kStep];
+        auto fetch = [&](int k, int64_t t) {
+            t = t < seqlen ? t : seqlen - 1;
+            xn[k] = x.fetch(row + t, dim, d0);
+            gn[k] = VecRaw<T, VEC>::load(du, (row + t) * dim, d0);
+        };
+        // Of token t, given its inputs: dx_{t-3}, complete with it, in out.
+        auto taps = [&](const float (&xv)[VEC], float (&gv)[VEC], float (&out)[VEC], bool own) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) xv[i] = gv[i] = 0.0f;
-        }
-    };
-    float xn[VEC], gn[VEC];
-    fetch(t0, xn, gn);
-    for (int64_t t = t0; t < own_end + 3; ++t) {
-        const bool in_row = t < seqlen;
-        float xv[VEC], gv[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            xv[i] = xn[i];
-            gv[i] = gn[i];
-        }
-        fetch(t + 1, xn, gn);
-        if (in_row && ((starts >> (t - t0 + 3)) & 1ull)) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) h1[i] = h2[i] = h3[i] = 0.0f;
-            since = 0;
-        }
-        const bool own = t < own_end;
-        const float m1 = since >= 1 ? 1.0f : 0.0f;
-        const float m2 = since >= 2 ? 1.0f : 0.0f;
-        const float m3 = since >= 3 ? 1.0f : 0.0f;
-        float out[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            float acc = __builtin_fmaf(w3[i], xv[i], bs[i]);
-            acc = __builtin_fmaf(w2[i], h1[i], acc);
-            acc = __builtin_fmaf(w1[i], h2[i], acc);
-            acc = __builtin_fmaf(w0[i], h3[i], acc);
-            float g = gv[i];
-            if constexpr (SILU) {
-                const float sg = rcp_fast(1.0f + exp2_fast(-acc * kLog2e));
-                g *= sg * __builtin_fmaf(acc, 1.0f - sg, 1.0f);
+            for (int i = 0; i < VEC; ++i) {
+                float acc = __builtin_fmaf(w3[i], xv[i], bs[i]);
+                acc = __builtin_fmaf(w2[i], h1[i], acc);
+                acc = __builtin_fmaf(w1[i], h2[i], acc);
+                acc = __builtin_fmaf(w0[i], h3[i], acc);
+                float g = gv[i];
+                if constexpr (SILU) {
+                    const float sg = rcp_fast(1.0f + exp2_fast(-acc * kLog2e));
+                    g *= sg * __builtin_fmaf(acc, 1.0f - sg, 1.0f);
+                }
+                if (own) {
+                    gb[i] += g;
+                    gw3[i] = __builtin_fmaf(g, xv[i], gw3[i]);
+                    gw2[i] = __builtin_fmaf(g, h1[i], gw2[i]);
+                    gw1[i] = __builtin_fmaf(g, h2[i], gw1[i]);
+                    gw0[i] = __builtin_fmaf(g, h3[i], gw0[i]);
+                }
+                out[i] = __builtin_fmaf(g, w0[i], p3[i]);
+                p3[i] = __builtin_fmaf(g, w1[i], p2[i]);
+                p2[i] = __builtin_fmaf(g, w2[i], p1[i]);
+                p1[i] = g * w3[i];
+                h3[i] = h2[i];
+                h2[i] = h1[i];
+                h1[i] = xv[i];
             }
-            if (own) {
-                gb[i] += g;
-                gw3[i] = __builtin_fmaf(g, xv[i], gw3[i]);
-                gw2[i] = __builtin_fmaf(g, h1[i], gw2[i]);
-                gw1[i] = __builtin_fmaf(g, h2[i], gw1[i]);
-                gw0[i] = __builtin_fmaf(g, h3[i], gw0[i]);
-            }
-            // dx_{t-3} is complete after token t's tap; shift the others along.
-            out[i] = __builtin_fmaf(g * m3, w0[i], p3[i]);
-            p3[i] = __builtin_fmaf(g * m2, w1[i], p2[i]);
-            p2[i] = __builtin_fmaf(g * m1, w2[i], p1[i]);
-            p1[i] = g * w3[i];
-            h3[i] = h2[i];
-            h2[i] = h1[i];
-            h1[i] = xv[i];
-        }
-        since = since < 3 ? since + 1 : 3;
-        const int64_t s = t - 3;
-        if (s >= t0 && s < own_end) {
-            VecIO<T, VEC>::store(dx, (row + s) * dim + d0, out);
-        } else if (s < 0 && d_conv_state != nullptr) {
+        };
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) d_conv_state[(b * dim + d0 + i) * 3 + (3 + s)] = out[i];
+        for (int k = 0; k < kStep; ++k) fetch(k, t0 + k);
+#pragma unroll 1
+        for (int64_t t = t0; t < t0 + kTile; t += kStep) {
+#pragma unroll
+            for (int k = 0; k < kStep; ++k) {
+                float xv[VEC], gv[VEC], out[VEC];
+                X::get(xn[k], xv);
+                VecRaw<T, VEC>::get(gn[k], gv);
+                fetch(k, t + kStep + k);
+                taps(xv, gv, out, true);
+                if (t + k >= t0 + 3) VecIO<T, VEC>::store(dx, (row + t + k - 3) * dim + d0, out);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            float xv[VEC], gv[VEC], out[VEC];
+            X::get(xn[k], xv);
+            VecRaw<T, VEC>::get(gn[k], gv);
+            taps(xv, gv, out, false);
+            VecIO<T, VEC>::store(dx, (row + t0 + kTile + k - 3) * dim + d0, out);
+        }
+    } else {
+        // x and du of the next token are fetched while the current one computes.
+        auto fetch = [&](int64_t t, float (&xv)[VEC], float (&gv)[VEC]) {
+            if (t < seqlen) {
+                x.load(row + t, dim, d0, xv);
+                VecIO<T, VEC>::load(du, (row + t) * dim + d0, gv);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) xv[i] = gv[i] = 0.0f;
+            }
+        };
+        float xn[VEC], gn[VEC];
+        fetch(t0, xn, gn);
+        for (int64_t t = t0; t < own_end + 3; ++t) {
+            const bool in_row = t < seqlen;
+            float xv[VEC], gv[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                xv[i] = xn[i];
+                gv[i] = gn[i];
+            }
+            fetch(t + 1, xn, gn);
+            if (in_row && ((starts >> (t - t0 + 3)) & 1ull)) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) h1[i] = h2[i] = h3[i] = 0.0f;
+                since = 0;
+            }
+            const bool own = t < own_end;
+            const float m1 = since >= 1 ? 1.0f : 0.0f;
+            const float m2 = since >= 2 ? 1.0f : 0.0f;
+            const float m3 = since >= 3 ? 1.0f : 0.0f;
+            float out[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                float acc = __builtin_fmaf(w3[i], xv[i], bs[i]);
+                acc = __builtin_fmaf(w2[i], h1[i], acc);
+                acc = __builtin_fmaf(w1[i], h2[i], acc);
+                acc = __builtin_fmaf(w0[i], h3[i], acc);
+                float g = gv[i];
+                if constexpr (SILU) {
+                    const float sg = rcp_fast(1.0f + exp2_fast(-acc * kLog2e));
+                    g *= sg * __builtin_fmaf(acc, 1.0f - sg, 1.0f);
+                }
+                if (own) {
+                    gb[i] += g;
+                    gw3[i] = __builtin_fmaf(g, xv[i], gw3[i]);
+                    gw2[i] = __builtin_fmaf(g, h1[i], gw2[i]);
+                    gw1[i] = __builtin_fmaf(g, h2[i], gw1[i]);
+                    gw0[i] = __builtin_fmaf(g, h3[i], gw0[i]);
+                }
+                // dx_{t-3} is complete after token t's tap; shift the others along.
+                out[i] = __builtin_fmaf(g * m3, w0[i], p3[i]);
+                p3[i] = __builtin_fmaf(g * m2, w1[i], p2[i]);
+                p2[i] = __builtin_fmaf(g * m1, w2[i], p1[i]);
+                p1[i] = g * w3[i];
+                h3[i] = h2[i];
+                h2[i] = h1[i];
+                h1[i] = xv[i];
+            }
+            since = since < 3 ? since + 1 : 3;
+            const int64_t s = t - 3;
+            if (s >= t0 && s < own_end) {
+                VecIO<T, VEC>::store(dx, (row + s) * dim + d0, out);
+            } else if (s < 0 && d_conv_state != nullptr) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) d_conv_state[(b * dim + d0 + i) * 3 + (3 + s)] = out[i];
+            }
         }
     }
     // Per-tile partials: [b][tile][5][D] (dw columns 0..3, then dbias).
@@ -250,6 +346,7 @@ __global__ __launch_bounds__(1024) void conv1d_bwd_reduce_kernel(const float* __
     float s0 = 0.0f, s1 = 0.0f;
     if (e < nout) {
         int64_t i = g;
+#pragma unroll 8
         for (; i + kGroups < nparts; i += 2 * kGroups) {
             s0 += part[i * nout + e];
             s1 += part[(i + kGroups) * nout + e];
