@@ -5,7 +5,7 @@
 //     G_t = dy_t + e_{t+1},   e_t = a_t G_t  (0 at a document start),
 // e after the last token being d_final_state:
 //     dx = G w i,   dgate_x = G w v (1 - i),   dz = dout h silu'(z),
-//     r dlog a = G (r a h_{t-1} - (r / w) a^2 v),
+//     r dlog a = G a (r h_{t-1} - a r v / w),
 //     dgate_a = -c softplus(a_param) (1 - r) r dlog a,
 //     da_param = -c sigmoid(a_param) sum r dlog a,   d_initial_state = e_0.
 // r / w stays finite as r -> 0 (w goes with sqrt r), where dlog a alone does not;
@@ -174,8 +174,8 @@ __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(
             wait_lds_reads();
         }
         if constexpr (kStaged) fetch(place(next));   // past the last ticket: a tile of no tokens, nothing is read
-        // Of every token: a, r, w i, 1 - i and (r / w) a^2 v.
-        float A[kK][kV], R[kK][kV], W[kK][kV], O[kK][kV], U[kK][kV];
+        // Of every token: a, r, w i, 1 - i and r v / w.
+        float A[kK][kV], R[kK][kV], W[kK][kV], O[kK][kV], V[kK][kV];
         float P[kV], H[kV], X[kV];
         auto maps = [&](auto gen) {
             constexpr bool GEN = decltype(gen)::value;
@@ -196,14 +196,13 @@ __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(
                     float rw = __builtin_amdgcn_rsqf(om);
                     asm volatile("" : "+v"(rw));
                     rw = om >= 0x1p-126f ? rw : 0.0f;   // denormals count as 0
-                    const float w = om * rw;
                     const float ig = sigmoid_f(gx[j]);
-                    const float v = ig * x[j];
+                    rw *= ig;
                     if constexpr (HAS_Z) y[j] *= silu_f(z[j]);
                     R[k][j] = r;
-                    W[k][j] = w * ig;
+                    W[k][j] = om * rw;
                     O[k][j] = 1.0f - ig;
-                    U[k][j] = (r * rw) * (al * al) * v;
+                    V[k][j] = (r * rw) * x[j];
                     float bb = W[k][j] * x[j];
                     if constexpr (GEN) {
                         al = out ? 1.0f : al;
@@ -322,6 +321,7 @@ __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(
                     const float sg = sigmoid_f(z[j]);
                     Z[k][j] = y[j] * (sg * __builtin_fmaf(z[j], 1.0f - sg, 1.0f));
                     Y[k][j] = y[j] * (z[j] * sg);
+                    asm volatile("" : "+v"(Y[k][j]), "+v"(Z[k][j]));   // here, not behind the barrier
                 }
                 __builtin_amdgcn_sched_barrier(0);
             });
@@ -374,7 +374,7 @@ __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(
                     const bool start = GEN && ((st >> k) & 1u), out = GEN && k >= left;
 #pragma unroll
                     for (int j = 0; j < kV; ++j) {
-                        const float ah = start ? 0.0f : A[k][j] * h[k][j];
+                        const float before = start ? 0.0f : h[k][j];
                         if constexpr (HAS_Z) {
                             dz[j] = Z[k][j] * h[k + 1][j];
                             y[j] = Y[k][j];
@@ -383,7 +383,7 @@ __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(
                         const float G = y[j] + e[j];
                         dx[j] = G * W[k][j];
                         dg[j] = dx[j] * x[j] * O[k][j];
-                        const float q = G * __builtin_fmaf(R[k][j], ah, -U[k][j]);
+                        const float q = G * (A[k][j] * __builtin_fmaf(-A[k][j], V[k][j], R[k][j] * before));
                         da[j] = (kLn2 * rc[j]) * (1.0f - R[k][j]) * q;   // kLn2 rate = -c softplus(a_param)
                         sum[j] += out ? 0.0f : q;
                         e[j] = start ? 0.0f : A[k][j] * G;
