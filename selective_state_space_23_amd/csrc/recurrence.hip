@@ -38,7 +38,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
     __shared__ float s_in[kTileChannels];                 // the values entering the tile
     __shared__ float2 s_agg[kWaves + 1][kTileChannels];   // the waves' maps; the last row takes what no one reads
     __shared__ float2 s_pre[kWaves][kTileChannels];       // the maps of all before a wave
-    __shared__ int s_ticket, s_second;
+    __shared__ int s_ticket, s_first;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane % kRow, half = lane / kRow;
     const auto first = kernel_args<RecFwdKernelArgs>();
@@ -85,23 +85,15 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
         }
     };
 
-    int cur, next;
+    int cur;
     if (ntiles > 1) {
-        if (wave == 0) {   // both tickets are under way together
-            const int t0 = draw();
-            int t1 = kNone;
-            if (!walk.once) t1 = draw();
-            s_ticket = __builtin_amdgcn_readfirstlane(t0);
-            s_second = __builtin_amdgcn_readfirstlane(t1);
-        }
+        if (wave == 0) s_first = __builtin_amdgcn_readfirstlane(draw());
         lds_barrier();
-        cur = __builtin_amdgcn_readfirstlane(s_ticket);
-        next = __builtin_amdgcn_readfirstlane(s_second);
+        cur = __builtin_amdgcn_readfirstlane(s_first);
         if (cur >= walk.tickets) return;
         fetch(place(cur));
     } else {
         cur = static_cast<int>(blockIdx.x);
-        next = kNone;
         const Tile t = place(cur);
         fetch(t);
         if (threadIdx.x < kTileChannels) {
@@ -118,8 +110,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
         const Tile t = place(cur);
         const int c = t.ct * kTileChannels + kV * li;
         const TileStarts starts = fl.starts();
-        // The next tile's inputs are on their way from here on (past the last ticket: a
-        // tile of no tokens, nothing is read).
+        int ticket = kNone;   // wave 0's: the next tile
+        if (wave == 0 && !walk.once) ticket = draw();
         In xc = xi, ac = ai, gc = gi;
         Plain zc = zi;
         float rc[kV];
@@ -132,7 +124,6 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
             if constexpr (kZ) zc.read(stage + 3 * In::kStageBytes, half, li);
             wait_lds_reads();
         }
-        fetch(place(next));
         // Maps of the lane's tokens from its first one on.  GEN: the tile has document
         // starts or ends behind the row (decided for the whole workgroup).
         float P[kK][kV], H[kK][kV];
@@ -190,19 +181,15 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
             const auto p = kernel_args<RecFwdKernelArgs>();
             return walk.words(Chain{p->ch.map, p->ch.value, p->ch.next, p->ch.rate}, t);
         };
-        int ticket = 0;   // wave 0's: the tile after the next one
-        if (wave == 0 && ntiles > 1) {
-            seen = words().peek(t.pos);
-            if (next < walk.tickets) ticket = draw();
+        if (wave == 0) {
+            if (ntiles > 1) seen = words().peek(t.pos);
+            s_ticket = __builtin_amdgcn_readfirstlane(ticket);
         }
         lds_barrier();
-        if (wave == 0) {   // a lane per channel: the value entering the tile, the waves and the next tile
-            const int d = t.ct * kTileChannels + lane;
-            const auto p = kernel_args<RecFwdKernelArgs>();
-            const auto& a = p->a;
-            const ChainWords chain = words();
-            float in = row_load(a.initial_state, t.b, a.dim, d);
-            float2 m = s_agg[0][lane];
+        const int next = __builtin_amdgcn_readfirstlane(s_ticket);
+        float2 m = make_float2(1.0f, 0.0f);   // wave 0's, a lane per channel: the tile's map
+        if (wave == 0) {
+            m = s_agg[0][lane];
             s_pre[0][lane] = make_float2(1.0f, 0.0f);
 #pragma unroll
             for (int w = 1; w < kWaves; ++w) {
@@ -211,14 +198,23 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
                 compose(v.x, v.y, m.x, m.y);
                 m = v;
             }
-            if (t.tile + 1 < ntiles) chain.publish_map(t.pos, m.x, m.y);
+            if (t.tile + 1 < ntiles) words().publish_map(t.pos, m.x, m.y);
+        }
+        // The next tile's inputs are on their way from here on (past the last ticket: a
+        // tile of no tokens, nothing is read).
+        fetch(place(next));
+        if (wave == 0) {   // the value entering the tile
+            const int d = t.ct * kTileChannels + lane;
+            const auto p = kernel_args<RecFwdKernelArgs>();
+            const auto& a = p->a;
+            const ChainWords chain = words();
+            float in = row_load(a.initial_state, t.b, a.dim, d);
             in = chain.look_back(t.pos, in, seen);
             const float leaving = apply(m.x, m.y, in);
             if (t.tile + 1 < ntiles) chain.publish_value(t.pos, leaving);
             else if (OUT) row_store(a.final_state, t.b, a.dim, d, leaving);
             row_store(a.states, t.b * ntiles + t.tile, a.dim, d, in);
             s_in[lane] = in;
-            s_ticket = __builtin_amdgcn_readfirstlane(ticket);
         }
         if constexpr (SAVE) {   // while wave 0 waits for the value entering
             const auto p = kernel_args<RecFwdKernelArgs>();
@@ -265,7 +261,6 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
         // Behind the staged loads this wave has issued the tile's kK stores at least.
         if constexpr (kStaged) wait_all_but<OUT ? kK : 0>();
         cur = next;
-        next = __builtin_amdgcn_readfirstlane(s_ticket);   // written before the last barrier
     }
 }
 
