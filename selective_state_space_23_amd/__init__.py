@@ -75,9 +75,15 @@ def version() -> str:
     return f"{v >> 16}.{(v >> 8) & 255}.{v & 255}"
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
@@ -106,7 +112,22 @@ def _ptr(t, name, device, dtype=None, shape=None) -> Optional[int]:
 
 
 def _stream(device) -> int:
-    return _torch().cuda.current_stream(device).cuda_stream
+    """The current stream's handle.  (torch's own generated code asks for it by the
+    first call, which makes no Stream object: 2 us less a launch.)"""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None or device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return raw(device.index)
+
+
+def _launch(device, call, *args) -> int:
+    """call(*args, stream) with the tensors' device current."""
+    torch = _torch()
+    if device.index is None or torch.cuda.current_device() == device.index:
+        return call(*args, _stream(device))
+    with torch.cuda.device(device):
+        return call(*args, _stream(device))
 
 
 def _check_device(x):
@@ -531,8 +552,8 @@ def causal_conv1d_bwd(x, weight, du, bias=None, doc_start=None, apply_silu: bool
     else:
         call, name = lib.mamba_causal_conv1d_bwd_packed, "mamba_causal_conv1d_bwd_packed"
         xs = _packed_ptrs(packed, "x", dev, (Bt, L, Dm))
-    st = call(
-        *xs, _ptr(weight, "weight", dev, torch.float32, (Dm, W)),
+    st = _launch(
+        dev, call, *xs, _ptr(weight, "weight", dev, torch.float32, (Dm, W)),
         _ptr(bias, "bias", dev, torch.float32, (Dm,)),
         _ptr(doc_start, "doc_start", dev, torch.uint8, (Bt, L)),
         _ptr(conv_state, "conv_state", dev, x.dtype, (Bt, Dm, 3)),
@@ -540,7 +561,7 @@ def causal_conv1d_bwd(x, weight, du, bias=None, doc_start=None, apply_silu: bool
         _ptr(dweight, "dweight", dev, torch.float32, (Dm, W)), _ptr(dbias, "dbias", dev, torch.float32, (Dm,)),
         _ptr(d_conv_state, "d_conv_state", dev, torch.float32, (Bt, Dm, 3)),
         Bt, L, Dm, W, _dtype_code(x), int(bool(apply_silu)),
-        _ptr(workspace, "workspace", dev, torch.uint8), workspace.numel(), _stream(dev))
+        _ptr(workspace, "workspace", dev, torch.uint8), workspace.numel())
     _lib.check(st, name)
     if conv_state is not None:
         return dx, dweight, dbias, d_conv_state
@@ -606,22 +627,6 @@ def _strided(t, name, dev, dtype, shape):
     return t.data_ptr(), ld
 
 
-class _on_device:
-    """The tensors' device made current for the launches, if it is not."""
-
-    def __init__(self, dev):
-        torch = _torch()
-        self._guard = None if dev.index is None or torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-
-
 def activation_pack(x, packed=None) -> PackedActivation:
     """The 8-bit checkpoint of x (..., D), float32/bfloat16; see mamba_activation_pack.
     x's channels are contiguous and its tokens lie at one distance.  ``packed``: an
@@ -638,8 +643,7 @@ def activation_pack(x, packed=None) -> PackedActivation:
     rows = 1
     for n in shape[:-1]:
         rows *= n
-    with _on_device(dev):
-        st = _lib.load().mamba_activation_pack(ptr, q, scale, rows, shape[-1], ld, code, _stream(dev))
+    st = _launch(dev, _lib.load().mamba_activation_pack, ptr, q, scale, rows, shape[-1], ld, code)
     _lib.check(st, "mamba_activation_pack")
     return packed
 
@@ -661,9 +665,8 @@ def activation_unpack(packed, dtype=None, out=None):
     rows = 1
     for n in shape[:-1]:
         rows *= n
-    with _on_device(dev):
-        st = _lib.load().mamba_activation_unpack(q, scale, _ptr(out, "out", dev, out.dtype, shape), rows, shape[-1],
-                                                 _dtype_code(out), _stream(dev))
+    st = _launch(dev, _lib.load().mamba_activation_unpack, q, scale, _ptr(out, "out", dev, out.dtype, shape), rows,
+                 shape[-1], _dtype_code(out))
     _lib.check(st, "mamba_activation_unpack")
     return out
 
@@ -752,16 +755,15 @@ def gated_recurrence_fwd(x, gate_a, gate_x, a_param, z=None, doc_start=None, c: 
     if workspace is None and L > _lib.RECURRENCE_CHUNK:
         workspace = _recurrence_workspace(lib.mamba_gated_recurrence_workspace_bytes,
                                           "mamba_gated_recurrence_workspace_bytes", dev, ctypes.byref(dims))
-    with _on_device(dev):
-        st = lib.mamba_gated_recurrence_fwd(
-            ctypes.byref(dims), px, pa, pg, _ptr(a_param, "a_param", dev, f32, (Dm,)), pz,
-            _ptr(doc_start, "doc_start", dev, torch.uint8, (Bt, L)),
-            _ptr(initial_state, "initial_state", dev, f32, (Bt, Dm)),
-            _ptr(out, "out", dev, dt, (Bt, L, Dm)),
-            _ptr(final_state, "final_state", dev, f32, (Bt, Dm)),
-            _ptr(states, "states", dev, f32, (Bt, -(-L // _lib.RECURRENCE_CHUNK), Dm)), pk,
-            _ptr(workspace, "workspace", dev, torch.uint8), 0 if workspace is None else workspace.numel(),
-            _stream(dev))
+    st = _launch(
+        dev, lib.mamba_gated_recurrence_fwd,
+        ctypes.byref(dims), px, pa, pg, _ptr(a_param, "a_param", dev, f32, (Dm,)), pz,
+        _ptr(doc_start, "doc_start", dev, torch.uint8, (Bt, L)),
+        _ptr(initial_state, "initial_state", dev, f32, (Bt, Dm)),
+        _ptr(out, "out", dev, dt, shape),
+        _ptr(final_state, "final_state", dev, f32, (Bt, Dm)),
+        _ptr(states, "states", dev, f32, (Bt, -(-L // _lib.RECURRENCE_CHUNK), Dm)), pk,
+        _ptr(workspace, "workspace", dev, torch.uint8), 0 if workspace is None else workspace.numel())
     _lib.check(st, "mamba_gated_recurrence_fwd")
     return (out, final_state) if save is None else (out, final_state, kept)
 
@@ -814,16 +816,15 @@ def gated_recurrence_bwd(x, gate_a, gate_x, a_param, dout, z=None, doc_start=Non
                                           "mamba_gated_recurrence_bwd_workspace_bytes", dev, ctypes.byref(dims),
                                           int(states is not None))
     res = lambda k: _ptr(g[k], k, dev, shapes[k][1], shapes[k][0]) if k in shapes else None  # noqa: E731
-    with _on_device(dev):
-        st = lib.mamba_gated_recurrence_bwd(
-            ctypes.byref(dims), ptrs[0], ptrs[1], ptrs[2], _ptr(a_param, "a_param", dev, f32, (Dm,)), ptrs[3],
-            _ptr(doc_start, "doc_start", dev, torch.uint8, (Bt, L)),
-            _ptr(initial_state, "initial_state", dev, f32, (Bt, Dm)), pk,
-            _ptr(states, "states", dev, f32, (Bt, -(-L // _lib.RECURRENCE_CHUNK), Dm)), po,
-            _ptr(d_final_state, "d_final_state", dev, f32, (Bt, Dm)),
-            res("dx"), res("dgate_a"), res("dgate_x"), res("da_param"), res("dz"), res("d_initial_state"),
-            _ptr(workspace, "workspace", dev, torch.uint8), 0 if workspace is None else workspace.numel(),
-            _stream(dev))
+    st = _launch(
+        dev, lib.mamba_gated_recurrence_bwd,
+        ctypes.byref(dims), ptrs[0], ptrs[1], ptrs[2], _ptr(a_param, "a_param", dev, f32, (Dm,)), ptrs[3],
+        _ptr(doc_start, "doc_start", dev, torch.uint8, (Bt, L)),
+        _ptr(initial_state, "initial_state", dev, f32, (Bt, Dm)), pk,
+        _ptr(states, "states", dev, f32, (Bt, -(-L // _lib.RECURRENCE_CHUNK), Dm)), po,
+        _ptr(d_final_state, "d_final_state", dev, f32, (Bt, Dm)),
+        res("dx"), res("dgate_a"), res("dgate_x"), res("da_param"), res("dz"), res("d_initial_state"),
+        _ptr(workspace, "workspace", dev, torch.uint8), 0 if workspace is None else workspace.numel())
     _lib.check(st, "mamba_gated_recurrence_bwd")
     return {k: g[k] for k in shapes}
 
@@ -848,10 +849,10 @@ def gated_recurrence_update(state, x, gate_a, gate_x, a_param, z=None, reset=Non
     pg, lg = _strided(gate_x, "gate_x", dev, dt, shape)
     pz, lz = _strided(z, "z", dev, dt, shape)
     dims = _recurrence_dims(Bt, 1, Dm, _dtype_code(x), c, (lx, la, lg, lz, 0))
-    with _on_device(dev):
-        st = _lib.load().mamba_gated_recurrence_update(
-            ctypes.byref(dims), _ptr(state, "state", dev, f32, shape), px, pa, pg,
-            _ptr(a_param, "a_param", dev, f32, (Dm,)), pz, _ptr(reset, "reset", dev, torch.uint8, (Bt,)),
-            _ptr(out, "out", dev, dt, shape), _stream(dev))
+    st = _launch(
+        dev, _lib.load().mamba_gated_recurrence_update,
+        ctypes.byref(dims), _ptr(state, "state", dev, f32, shape), px, pa, pg,
+        _ptr(a_param, "a_param", dev, f32, (Dm,)), pz, _ptr(reset, "reset", dev, torch.uint8, (Bt,)),
+        _ptr(out, "out", dev, dt, shape))
     _lib.check(st, "mamba_gated_recurrence_update")
     return out
