@@ -356,6 +356,36 @@ def test_decode_continues_the_prefill(ssm, dtype):
     assert state[[0, 2]].isfinite().all() and state[1].isnan().all()
 
 
+@pytest.mark.parametrize("B,D,dtype", [(1, 1, "f32"), (5, 63, "bf16"), (3, 260, "f32"), (1027, 1022, "f32"),
+                                       (1029, 1026, "bf16"), (259, 4104, "bf16"), (65535, 17, "f32"), (8193, 128, "bf16")])
+def test_update_of_many_rows(ssm, B, D, dtype):
+    """Rows and widths that leave threads and groups of rows partly used, also of
+    inputs sliced out of one tensor; a row's result does not depend on the others."""
+    import torch
+
+    v = draw(B, 1, D, dtype, True, None, True, seed=23)
+    d = dev(v, dtype)
+    ref = oracle_fwd(v)
+    names = ("x", "gate_a", "gate_x", "z")
+    dense = [d[n][:, 0] for n in names]
+    sliced = torch.cat(dense, 1).split(D, 1)
+    got = []
+    for x, ga, gx, z in (dense, sliced):
+        guard = torch.full((2 * B * D,), 5.0, device="cuda")
+        state = guard[: B * D].view(B, D)
+        state.copy_(d["initial_state"])
+        out = ssm.gated_recurrence_update(state, x, ga, gx, d["a_param"], z)
+        close(out, ref[0][:, 0], dtype, "out")
+        close(state, ref[1], "f32", "state")
+        assert (guard[B * D :] == 5.0).all()
+        got.append((out, state))
+    assert equal(got[0][0], got[1][0]) and equal(got[0][1], got[1][1])
+    rows = [0, B // 2, B - 1]
+    state = d["initial_state"][rows].contiguous()
+    out = ssm.gated_recurrence_update(state, *[t[rows].contiguous() for t in dense[:3]], d["a_param"], dense[3][rows].contiguous())
+    assert equal(out, got[0][0][rows]) and equal(state, got[0][1][rows])
+
+
 def test_split_rows(ssm):
     """A row cut in two: states carried forwards, gradients backwards."""
     B, L, D, n = 2, 500, 40, 201
