@@ -264,11 +264,14 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
     }
 }
 
-// Before a launch: nothing published, no ticket drawn, the channels' rates.
-__global__ __launch_bounds__(256) void rec_clear_kernel(uint4* __restrict__ words, int64_t n, uint32_t* __restrict__ next,
-                                                        float* __restrict__ rate, int nrate,
+// Before a launch: nothing published, no ticket drawn, the channels' rates.  A
+// workspace per blockIdx.y.
+__global__ __launch_bounds__(256) void rec_clear_kernel(char* __restrict__ ws, size_t stride, int64_t n, int nrate,
                                                         const float* __restrict__ a_param, int dim, float c) {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    uint4* words = reinterpret_cast<uint4*>(ws + blockIdx.y * stride);
+    uint32_t* next = reinterpret_cast<uint32_t*>(words + n);
+    float* rate = reinterpret_cast<float*>(next + 16);
     if (i < n) words[i] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
     if (i == 0) next[0] = 0;
     if (i < nrate) rate[i] = -c * kLog2e * softplus_exact(a_param[i < dim ? i : dim - 1]);
@@ -282,8 +285,12 @@ hipError_t launch_fwd(const RecFwdArgs& a) {
     const int ntiles = static_cast<int>((a.seqlen + kTileTokens - 1) / kTileTokens);
     const int64_t tiles = nct * a.batch * ntiles;
     Chain ch;
-    const hipError_t e = clear_chains(a.ws, a.batch, a.dim, ntiles, a.a_param, a.c, &ch, a.stream);
-    if (e != hipSuccess) return e;
+    if (a.chain != nullptr) {
+        ch = *a.chain;
+    } else {
+        const hipError_t e = clear_chains(a.ws, 1, 0, a.batch, a.dim, ntiles, a.a_param, a.c, &ch, a.stream);
+        if (e != hipSuccess) return e;
+    }
     const int64_t grid = ntiles > 1 && tiles > kResident ? kResident : tiles;
     hipLaunchKernelGGL((rec_fwd_kernel<T, ALIGNED, PIN, HAS_Z, SAVE, OUT>), dim3(static_cast<unsigned>(grid)),
                        dim3(kThreads), 0, a.stream, RecFwdKernelArgs{a, ch, nct, ntiles});
@@ -392,20 +399,21 @@ size_t recurrence_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
     return static_cast<size_t>(batch * width * ntiles) * 12 + 64 + static_cast<size_t>(width) * 4;
 }
 
-hipError_t clear_chains(void* ws, int64_t batch, int64_t dim, int64_t ntiles, const float* a_param, float c, Chain* ch,
-                        hipStream_t stream) {
-    *ch = Chain{nullptr, nullptr, nullptr, nullptr};
+hipError_t clear_chains(void* ws, int count, size_t stride, int64_t batch, int64_t dim, int64_t ntiles,
+                        const float* a_param, float c, Chain* ch, hipStream_t stream) {
+    for (int i = 0; i < count; ++i) ch[i] = Chain{nullptr, nullptr, nullptr, nullptr};
     if (ntiles <= 1) return hipSuccess;
     const int64_t width = (dim + kTileChannels - 1) / kTileChannels * kTileChannels;
     const int64_t words = batch * width * ntiles;
-    ch->map = static_cast<uint64_t*>(ws);
-    ch->value = reinterpret_cast<uint32_t*>(ch->map + words);
-    ch->next = ch->value + words;
-    float* rate = reinterpret_cast<float*>(ch->next + 16);
-    ch->rate = rate;
+    for (int i = 0; i < count; ++i) {
+        ch[i].map = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + i * stride);
+        ch[i].value = reinterpret_cast<uint32_t*>(ch[i].map + words);
+        ch[i].next = ch[i].value + words;
+        ch[i].rate = reinterpret_cast<float*>(ch[i].next + 16);
+    }
     const int64_t n = words * 12 / 16;   // words is a multiple of 64, and 3 words at least a width: n covers the rates
-    hipLaunchKernelGGL(rec_clear_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream,
-                       static_cast<uint4*>(ws), n, ch->next, rate, static_cast<int>(width), a_param,
+    hipLaunchKernelGGL(rec_clear_kernel, dim3(static_cast<unsigned>((n + 255) / 256), static_cast<unsigned>(count)),
+                       dim3(256), 0, stream, static_cast<char*>(ws), stride, n, static_cast<int>(width), a_param,
                        static_cast<int>(dim), c);
     return hipGetLastError();
 }

@@ -693,8 +693,9 @@ struct Walk {
 
 }  // namespace rec
 
-// The chains' words in a launch's workspace (recurrence_workspace_bytes), cleared on
-// the stream, and the rates (recurrence.hip).  Nothing for rows of one tile.
-hipError_t clear_chains(void* ws, int64_t batch, int64_t dim, int64_t ntiles, const float* a_param, float c,
-                        rec::Chain* ch, hipStream_t stream);
+// The chains' words in `count` workspaces (recurrence_workspace_bytes each, `stride`
+// bytes apart), cleared on the stream, and the rates (recurrence.hip).  Nothing for
+// rows of one tile.
+hipError_t clear_chains(void* ws, int count, size_t stride, int64_t batch, int64_t dim, int64_t ntiles,
+                        const float* a_param, float c, rec::Chain* ch, hipStream_t stream);
 }  // namespace mamba

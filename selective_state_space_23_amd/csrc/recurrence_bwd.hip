@@ -438,7 +438,7 @@ __global__ __launch_bounds__(1024) void rec_bwd_reduce_kernel(const float* __res
 constexpr int kResident = 256;   // one workgroup a CU
 
 struct BwdWs {
-    size_t part, chain, states, fwd, total;
+    size_t part, chain, chain_bytes, states, total;
 };
 
 BwdWs bwd_ws(int64_t batch, int64_t seqlen, int64_t dim, bool have_states) {
@@ -447,9 +447,10 @@ BwdWs bwd_ws(int64_t batch, int64_t seqlen, int64_t dim, bool have_states) {
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t o = off; off += (bytes + 255) / 256 * 256; return o; };
     w.part = take(n * 4);
-    w.chain = take(recurrence_workspace_bytes(batch, seqlen, dim));
+    w.chain = off;   // and the recomputation's behind it
+    w.chain_bytes = (recurrence_workspace_bytes(batch, seqlen, dim) + 255) / 256 * 256;
+    take((have_states ? 1 : 2) * w.chain_bytes);
     w.states = take(have_states ? 0 : n * 4);
-    w.fwd = take(have_states ? 0 : recurrence_workspace_bytes(batch, seqlen, dim));
     w.total = off;
     return w;
 }
@@ -462,21 +463,25 @@ hipError_t launch_bwd(const RecBwdArgs& a) {
     const BwdWs w = bwd_ws(a.batch, a.seqlen, a.dim, a.states != nullptr);
     char* ws = static_cast<char*>(a.ws);
     RecBwdKernelArgs k{a, Chain{}, reinterpret_cast<float*>(ws + w.part), nct, ntiles};
-    hipError_t e;
-    if (a.states == nullptr && ntiles > 1) {
+    const bool recompute = a.states == nullptr && ntiles > 1;
+    Chain chains[2];
+    hipError_t e = clear_chains(ws + w.chain, recompute ? 2 : 1, w.chain_bytes, a.batch, a.dim, ntiles, a.a_param, a.c,
+                                chains, a.stream);
+    if (e != hipSuccess) return e;
+    k.ch = chains[0];
+    if (recompute) {
         RecFwdArgs f{};
         f.x = a.x; f.gate_a = a.gate_a; f.gate_x = a.gate_x;
         for (int i = 0; i < 3; ++i) f.in[i] = a.in[i];
         f.a_param = a.a_param; f.doc_start = a.doc_start; f.initial_state = a.initial_state;
         f.states = reinterpret_cast<float*>(ws + w.states);
-        f.ws = ws + w.fwd;
+        f.chain = &chains[1];
         f.batch = a.batch; f.seqlen = a.seqlen; f.dim = a.dim;
         f.ld_x = a.ld_x; f.ld_a = a.ld_a; f.ld_g = a.ld_g;
         f.c = a.c; f.bf16 = a.bf16; f.aligned = a.aligned; f.stream = a.stream;
         if ((e = launch_recurrence_fwd(f)) != hipSuccess) return e;
         k.a.states = f.states;
     }
-    if ((e = clear_chains(ws + w.chain, a.batch, a.dim, ntiles, a.a_param, a.c, &k.ch, a.stream)) != hipSuccess) return e;
     const int64_t grid = ntiles > 1 && tiles > kResident ? kResident : tiles;
     hipLaunchKernelGGL((rec_bwd_kernel<T, ALIGNED, PIN, HAS_Z>), dim3(static_cast<unsigned>(grid)),
                        dim3(Shape<T, ALIGNED>::kThreads), 0, a.stream, k);

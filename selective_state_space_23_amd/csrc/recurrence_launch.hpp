@@ -17,6 +17,10 @@ struct Packed {
     float* scale = nullptr;
 };
 
+namespace rec {
+struct Chain;   // recurrence.hpp
+}
+
 struct RecFwdArgs {
     // inputs; with packed inputs (the backward's recomputation of the states) x,
     // gate_a and gate_x are null and `in` holds their checkpoints
@@ -33,6 +37,7 @@ struct RecFwdArgs {
     float* states;                 // (B, ceil(L / 128), D) or null
     Packed save[4];                // q null: not written
     void* ws;
+    const rec::Chain* chain;       // cleared already, in place of ws; or null
     int64_t batch, seqlen, dim;
     int ld_x, ld_a, ld_g, ld_z;       // elements between two tokens
     float c;
