@@ -163,6 +163,44 @@ def test_packed_training_step(ssm, B, L, D, z, dtype):
             assert equal(a[k], b[k]), k
 
 
+# widths: odd; quads whose rows do not lie on 16 bytes; rows that do
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("z", [False, True])
+@pytest.mark.parametrize("D", [701, 700, 704])
+def test_more_tiles_than_workgroups(ssm, D, z, dtype):
+    """594 tiles of 128 tokens and 64 channels: workgroups take several, one after the other."""
+    B, L = 2, 3333
+    v = draw(B, L, D, dtype, z, 300, True, seed=D)
+    d = dev(v, dtype)
+    out, fin, kept = forward(ssm, d, save="packed")
+    ref = oracle_fwd(v)
+    close(out, ref[0], dtype, "out")
+    close(fin, ref[1], "f32", "final_state")
+    close(kept["states"], ref[2], "f32", "states")
+    plain = forward(ssm, d, save="states")
+    assert equal(out, plain[0]) and equal(fin, plain[1]) and equal(kept["states"], plain[2]["states"])
+    ref = oracle_bwd(v)
+    g = backward(ssm, d)
+    g2 = backward(ssm, d, states=kept["states"])
+    for k in ref:
+        close(g[k], ref[k], dtype if g[k].dtype != d["a_param"].dtype else "f32", k)
+        assert equal(g[k], g2[k]), k
+    seen = dict(v)
+    for k in ("x", "gate_a", "gate_x") + (("z",) if z else ()):
+        p = ssm.activation_pack(d[k])
+        assert equal(p.q, kept[k].q) and equal(p.scale, kept[k].scale), k
+        seen[k] = R.unpack8(*R.pack8(v[k]))
+    ref = oracle_bwd(seen, states=kept["states"].cpu().numpy())
+    dp = dict(d, **{k: kept.get(k) for k in ("x", "gate_a", "gate_x", "z")})
+    g = backward(ssm, dp, states=kept["states"])
+    for k in ref:
+        close(g[k], ref[k], dtype if g[k].dtype != d["a_param"].dtype else "f32", k)
+    ref = oracle_bwd(seen)
+    g = backward(ssm, dp)
+    for k in ref:
+        close(g[k], ref[k], dtype if g[k].dtype != d["a_param"].dtype else "f32", k)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_document_edges(ssm, dtype):
     """Starts on and around tile and lane edges, every token a start, and a start at token 0."""
@@ -432,6 +470,44 @@ def test_repeats_and_streams(ssm):
     torch.cuda.synchronize()
     for r in [step(), *got]:
         assert all(equal(a, b) for a, b in zip(r, want))
+
+
+def test_two_calls_at_once(ssm):
+    """Calls with workspaces of their own, under way together on two streams and from
+    two captured graphs, each larger than the card holds at a time."""
+    import torch
+
+    ds = [dev(draw(2, 3333, 704, "bf16", True, 300, True, seed=s), "bf16") for s in (31, 32)]
+
+    def step(d):
+        out, fin, kept = forward(ssm, d, save="packed")
+        g = backward(ssm, dict(d, **{k: kept[k] for k in ("x", "gate_a", "gate_x", "z")}), states=kept["states"])
+        return [out, fin, *g.values()]
+
+    want = [step(d) for d in ds]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ds]
+    graphs, held = [], []
+    for s, d in zip(streams, ds):
+        with torch.cuda.stream(s):
+            step(d)
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            held.append(step(d))
+        graphs.append(graph)
+    for _ in range(3):
+        got = []
+        for s, d in zip(streams, ds):
+            with torch.cuda.stream(s):
+                got.append(step(d))
+        torch.cuda.synchronize()
+        for s, graph in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for a, b, c in zip(want, got, held):
+            assert all(equal(p, q) for p, q in zip(a, b)) and all(equal(p, q) for p, q in zip(a, c))
 
 
 def test_captured_training_step(ssm):
