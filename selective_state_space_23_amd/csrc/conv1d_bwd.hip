@@ -81,7 +81,10 @@ constexpr int kBlock = 256;
 // The conv's input: x as stored, or its 8-bit checkpoint (codes (tokens, D), one
 // scale per token and 64 channels laid out (blocks, tokens)).  The channels of a
 // thread lie in one block: its scale comes with one 4-byte load per token, the
-// same address in the lanes of a block.
+// same address in the lanes of a block.  (Scales held a token a lane and broadcast
+// from there take as long; four tokens ahead in the general loop are slower, 188 us
+// for 155.)  2 x 32768 x 1536 in bfloat16: 141 us from a checkpoint (593 MB, 4.2 TB/s),
+// 144 from x as stored (693 MB, 4.8 TB/s).
 template <typename T, int VEC> struct PlainX {
     using Raw = typename VecRaw<T, VEC>::type;
     const void* __restrict__ x;
@@ -185,7 +188,8 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(
     const int64_t own_end = (t0 + kTile < seqlen) ? t0 + kTile : seqlen;
     // Tiles inside a row without a document start among their tokens, the 3 before and
     // the 3 after take every tap: the same operations without the masks, four tokens at a
-    // time, the next four under way.
+    // time, the next four under way (both loops in place of the general one alone: 168 us
+    // to 148 from a checkpoint, sums of the partials included).
     const bool all_taps = t0 >= 3 && t0 + kTile + 3 <= seqlen && (starts & ((1ull << (kTile + 6)) - 1)) == 0;
     if (all_taps) {
         constexpr int kStep = 4;

@@ -23,9 +23,20 @@ constexpr int kThreads = kWaves * 64;
 
 // One pass over the data.  A workgroup works off tiles until none is left (rows
 // of one tile: one workgroup each); a tile's maps stay in registers while the value
-// entering it is found by wave 0, and the next tile's inputs are under way from the
-// start of the tile on.  OUT: writes out, the final state and the checkpoints; else the states
-// alone (the backward's recomputation).
+// entering it is found by wave 0, the other waves write the checkpoints meanwhile, and
+// the next tile's inputs are under way from then on.  OUT: writes out, the final state
+// and the checkpoints; else the states alone (the backward's recomputation).
+//
+// What bounds it is memory, then the vector unit (41 issue slots an element, 34 of them
+// in the maps): one row of 65536 x 5120 in
+// bfloat16 without z moves 2.79 GB, of which 2.68 are inputs and outputs, in 641 us:
+// 4.3 TB/s where a copy reaches 5.2, the vector unit issues for 56% of it.  8 rows of 2048 x 1536
+// with z take 77 us (3.3 TB/s): six tiles a workgroup, whose first and last are not
+// hidden.  Three passes (maps, joining, outputs) read the inputs twice: 1348 us for
+// the first.  A tile's 16 waves a CU, in two workgroups, fill the registers; what a
+// workgroup waits for its neighbours (a third of its time) the other one's work covers.
+// Staging through LDS in place of registers took the first case from 785 us to 708,
+// drawing tickets one tile ahead and not two the second from 91 to 82.
 struct RecFwdKernelArgs {
     RecFwdArgs a;
     Chain ch;
@@ -44,7 +55,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
     const auto first = kernel_args<RecFwdKernelArgs>();
     const int dim = static_cast<int>(first->a.dim), nct = first->nct, ntiles = first->ntiles;
     const int tok = (wave * 2 + half) * kK;
-    Walk walk;
+    Walk<false> walk;
     walk.init(nct, ntiles, static_cast<int>(first->a.batch));
     auto draw = [&]() { return walk.draw(kernel_args<RecFwdKernelArgs>()->ch.next); };
     auto place = [&](int ticket) { return walk.place<false>(ticket, kernel_args<RecFwdKernelArgs>()->a.seqlen); };
@@ -273,7 +284,7 @@ __global__ __launch_bounds__(256) void rec_clear_kernel(char* __restrict__ ws, s
     uint32_t* next = reinterpret_cast<uint32_t*>(words + n);
     float* rate = reinterpret_cast<float*>(next + 16);
     if (i < n) words[i] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
-    if (i == 0) next[0] = 0;
+    if (i < 8) next[i] = 0;
     if (i < nrate) rate[i] = -c * kLog2e * softplus_exact(a_param[i < dim ? i : dim - 1]);
 }
 
@@ -330,7 +341,9 @@ __device__ __forceinline__ void quad_store(void* p, int64_t off, int left, const
 }
 
 // One token per row: a thread per four channels of R rows, whose decay parameters it
-// turns into rates once.  2^shift threads lie along a row, `nblocks` workgroups.
+// turns into rates once.  2^shift threads lie along a row, `nblocks` workgroups.  Bound
+// by the launch and one trip to memory: 256 rows of 5120 with z take 9.6 us (23.6 MB,
+// 2.5 TB/s), two rows of 1536 3.4 us.
 template <typename T, bool ALIGNED, int R>
 __global__ __launch_bounds__(256) void rec_update_kernel(const RecUpdateArgs a, unsigned nblocks, int shift) {
     const int dim = static_cast<int>(a.dim);

@@ -557,17 +557,17 @@ __device__ __forceinline__ void save_packed(const LaneIn<T, ALIGNED, false, K>& 
 // workgroup waits for have lower tickets: of the tickets not yet worked off, the
 // lowest is the current one of a workgroup that runs, and all that it waits for is
 // published.  Against a workspace that another call overwrites meanwhile (which
-// the caller has to exclude) the wait is bounded too: after kMaxPolls, seconds,
+// the caller has to exclude) the wait is bounded too: after kMaxPolls, 1.5 seconds,
 // the value is NaN.
 struct Chain {
     uint64_t* map;     // [chain][position][64]
     uint32_t* value;   // [chain][position][64]
-    uint32_t* next;    // tickets drawn
+    uint32_t* next;    // [group]: tickets drawn
     const float* rate; // [64 * channel tiles]: -c log2(e) softplus(a_param)
 };
 
-constexpr int kLook = 2;             // earlier positions looked at
-constexpr int kMaxPolls = 1 << 22;   // about a microsecond each
+constexpr int kLook = 2;             // earlier positions looked at (4: 3 x 1001 x 771 backward 73 us for 68, others alike)
+constexpr int kMaxPolls = 1 << 22;   // a third of a microsecond each
 
 __device__ __forceinline__ uint32_t not_all_ones(float x) {
     const uint32_t b = __float_as_uint(x);
@@ -651,21 +651,35 @@ struct ChainWords {
 
 constexpr int kNone = 0x7fffffff;   // a ticket behind all others
 
-// The tiles a workgroup draws: by tickets, position by position over the chains.
-struct Walk {
-    int nct, ntiles, chains, tickets;
+// The chains in groups of neighbours, each with tickets of its own for the workgroups
+// of one blockIdx % 8 (one XCD, as they are dealt out): as many, up to 8, as divide
+// the chains evenly.
+__host__ __device__ inline int chain_groups(int64_t chains) {
+    return chains % 8 == 0 ? 8 : chains % 4 == 0 ? 4 : chains % 2 == 0 ? 2 : 1;
+}
+
+// The tiles a workgroup draws: by tickets, position by position over the chains of its
+// group.  GROUPED: chain_groups(), else one group, which lets no group run ahead of
+// another.  Groups are for 8-bit inputs, whose rows of a tile are half a 128-byte line:
+// with neighbours on one XCD the other half is not fetched again (the backward of
+// 2 x 32768 x 1536 reads 652 MB in place of 988, training step 841 us in place of 857);
+// elsewhere one group is as fast or faster (65536 x 5120 forward 647 us, grouped 678).
+template <bool GROUPED> struct Walk {
+    int nct, ntiles, groups, group, chains, tickets;   // chains and tickets of the group
     bool once;   // a workgroup for every tile
     __device__ __forceinline__ void init(int nct_, int ntiles_, int batch) {
         nct = nct_;
         ntiles = ntiles_;
-        chains = nct * batch;
+        groups = GROUPED && ntiles > 1 ? chain_groups(nct * batch) : 1;
+        group = GROUPED ? static_cast<int>(blockIdx.x) % groups : 0;
+        chains = nct * batch / groups;
         tickets = chains * ntiles;
-        once = static_cast<unsigned>(tickets) <= gridDim.x;
+        once = static_cast<unsigned>(tickets) * groups <= gridDim.x;
     }
     // By a whole wave: lane 0 adds 1 at agent scope, the other lanes' offsets lie
     // past the counter.  The ticket is lane 0's.
     __device__ __forceinline__ int draw(uint32_t* next) const {
-        const Rsrc rs = tile_rsrc(next, 4);
+        const Rsrc rs = tile_rsrc(next + group, 4);
         return __builtin_amdgcn_raw_ptr_buffer_atomic_add_i32(1, rs, lane_now() == 0 ? 0u : kNoStore, 0, kAgentScope);
     }
     // The tile of a ticket, counted from the row's end with REVERSE; of no tokens
@@ -673,7 +687,7 @@ struct Walk {
     template <bool REVERSE>
     __device__ __forceinline__ Tile place(int ticket, int64_t seqlen) const {
         Tile t;
-        const int chain = ticket % chains;
+        const int chain = group * chains + ticket % chains;
         t.pos = ticket / chains;
         t.tile = REVERSE ? ntiles - 1 - t.pos : t.pos;
         t.ct = chain % nct;

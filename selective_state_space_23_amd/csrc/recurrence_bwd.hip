@@ -41,8 +41,18 @@ struct RecBwdKernelArgs {
 };
 
 // One pass over the data, from the row ends back.  A workgroup works off tiles as
-// the forward does; everything the gradients need of a token is formed once, before
-// the adjoint entering the tile is known, and kept in registers.
+// the forward does; what the gradients need of a token is formed before the adjoint
+// entering the tile is known, as far as registers hold it: five values of a token and
+// channel are kept, x, dout and z are read again from LDS and the gates' terms formed
+// while the workgroup waits for that adjoint.
+//
+// What bounds it is the vector unit (129 issue slots an element from 8-bit inputs and
+// 114 from tensors, 74% and 66% of the time), then memory: 2 rows of 32768 x 1536 from checkpoints
+// with z take 470 us and move 1.47 GB (3.1 TB/s), 8 rows of 2048 x 1536 from tensors
+// 115 us and 460 MB (4.0 TB/s; 5.2 for a copy).  One workgroup of 16 waves fills a CU's
+// registers and, with two places for x, dout and z, its LDS.  A register too many costs
+// more than the work it saves: with the gates' terms kept as well, their spills
+// reloaded behind the loads of the next tile, the first case took 770 us.
 template <typename T, bool ALIGNED, bool PIN, bool HAS_Z>
 __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(const RecBwdKernelArgs) {
     constexpr bool kStaged = Shape<T, ALIGNED>::kStaged;
@@ -56,10 +66,10 @@ __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(
     using Place = LanePlace<kK>;
     const auto first = kernel_args<RecBwdKernelArgs>();
     const int dim = static_cast<int>(first->a.dim), nct = first->nct, ntiles = first->ntiles;
-    Walk walk;
+    Walk<PIN> walk;
     walk.init(nct, ntiles, static_cast<int>(first->a.batch));
     auto draw = [&]() { return walk.draw(kernel_args<RecBwdKernelArgs>()->ch.next); };
-    auto place = [&](int ticket) { return walk.place<true>(ticket, kernel_args<RecBwdKernelArgs>()->a.seqlen); };
+    auto place = [&](int ticket) { return walk.template place<true>(ticket, kernel_args<RecBwdKernelArgs>()->a.seqlen); };
 
     // The next tile's inputs: staged in LDS (each wave its own part) while a tile is
     // worked off; float32 (too large) and unaligned ones are loaded at its start.
