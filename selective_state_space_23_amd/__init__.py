@@ -721,7 +721,7 @@ def gated_recurrence_fwd(x, gate_a, gate_x, a_param, z=None, doc_start=None, c: 
     if doc_start is not None and doc_start.dtype == torch.bool:
         doc_start = doc_start.to(torch.uint8)
     if out is None:
-        out = torch.empty((Bt, L, Dm), dtype=dt, device=dev)
+        out = torch.empty_like(x) if x.is_contiguous() else torch.empty(shape, dtype=dt, device=dev)
     if final_state is True:
         final_state = torch.empty((Bt, Dm), dtype=f32, device=dev)
     elif final_state is False:
@@ -843,7 +843,7 @@ def gated_recurrence_update(state, x, gate_a, gate_x, a_param, z=None, reset=Non
     if reset is not None and reset.dtype == torch.bool:
         reset = reset.to(torch.uint8)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
+        out = torch.empty_like(x) if x.is_contiguous() else torch.empty(shape, dtype=dt, device=dev)
     px, lx = _strided(x, "x", dev, dt, shape)
     pa, la = _strided(gate_a, "gate_a", dev, dt, shape)
     pg, lg = _strided(gate_x, "gate_x", dev, dt, shape)
