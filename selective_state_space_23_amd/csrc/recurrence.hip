@@ -43,7 +43,7 @@ struct RecFwdKernelArgs {
     int nct, ntiles;
 };
 
-template <typename T, bool ALIGNED, bool PIN, bool HAS_Z, bool SAVE, bool OUT>
+template <typename T, bool ALIGNED, bool PIN, bool HAS_Z, bool SAVE, bool OUT, int LOOK>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void rec_fwd_kernel(const RecFwdKernelArgs) {
     __shared__ float s_rate[kTileChannels];
     __shared__ float s_in[kTileChannels];                 // the values entering the tile
@@ -187,10 +187,10 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
             compose(p, h, ep[j], eh[j]);
             s_agg[half ? wave : kWaves][kV * li + j] = make_float2(p, h);
         }
-        ChainWords::Seen seen = {};
+        typename ChainWords<LOOK>::Seen seen = {};
         auto words = [&]() {
             const auto p = kernel_args<RecFwdKernelArgs>();
-            return walk.words(Chain{p->ch.map, p->ch.value, p->ch.next, p->ch.rate}, t);
+            return walk.template words<LOOK>(Chain{p->ch.map, p->ch.value, p->ch.next, p->ch.rate}, t);
         };
         if (wave == 0) {
             if (ntiles > 1) seen = words().peek(t.pos);
@@ -218,7 +218,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void r
             const int d = t.ct * kTileChannels + lane;
             const auto p = kernel_args<RecFwdKernelArgs>();
             const auto& a = p->a;
-            const ChainWords chain = words();
+            const ChainWords<LOOK> chain = words();
             float in = row_load(a.initial_state, t.b, a.dim, d);
             in = chain.look_back(t.pos, in, seen);
             const float leaving = apply(m.x, m.y, in);
@@ -303,8 +303,10 @@ hipError_t launch_fwd(const RecFwdArgs& a) {
         if (e != hipSuccess) return e;
     }
     const int64_t grid = ntiles > 1 && tiles > kResident ? kResident : tiles;
-    hipLaunchKernelGGL((rec_fwd_kernel<T, ALIGNED, PIN, HAS_Z, SAVE, OUT>), dim3(static_cast<unsigned>(grid)),
-                       dim3(kThreads), 0, a.stream, RecFwdKernelArgs{a, ch, nct, ntiles});
+    auto kernel = rec_fwd_kernel<T, ALIGNED, PIN, HAS_Z, SAVE, OUT, kLookNear>;
+    if (look_far(nct * a.batch, ntiles, kResident)) kernel = rec_fwd_kernel<T, ALIGNED, PIN, HAS_Z, SAVE, OUT, kLookFar>;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, a.stream,
+                       RecFwdKernelArgs{a, ch, nct, ntiles});
     return hipGetLastError();
 }
 

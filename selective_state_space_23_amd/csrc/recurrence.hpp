@@ -572,7 +572,15 @@ struct Chain {
     const float* rate; // [64 * channel tiles]: -c log2(e) softplus(a_param)
 };
 
-constexpr int kLook = 2;             // earlier positions looked at (4: 3 x 1001 x 771 backward 73 us for 68, others alike)
+// Earlier positions looked at.  A long row's value goes from tile to tile by as many
+// positions a trip: where 32 and more of a chain's tiles are under way, that is what a call
+// takes (65536 x 512 in bfloat16 132 us for 194, 32768 x 128 in float32 43 for 81); where
+// fewer are, more words to read gain nothing (from 24 chains on) or cost some.
+constexpr int kLookNear = 2, kLookFar = 8;
+inline bool look_far(int64_t chains, int64_t ntiles, int64_t workgroups) {
+    const int64_t under_way = workgroups / chains;
+    return (under_way < ntiles ? under_way : ntiles) >= 32;
+}
 constexpr int kMaxPolls = 1 << 22;   // a third of a microsecond each
 
 __device__ __forceinline__ uint32_t not_all_ones(float x) {
@@ -583,7 +591,7 @@ __device__ __forceinline__ uint32_t not_all_ones(float x) {
 // The words of one chain, as buffers: accesses at agent scope (the cache-policy
 // bit kAgentScope), each word whole.
 constexpr int kAgentScope = 16;
-struct ChainWords {
+template <int kLook> struct ChainWords {
     Rsrc map, value;
     __device__ __forceinline__ void init(uint64_t* maps, uint32_t* values, int64_t word0, int ntiles) {
         map = tile_rsrc(maps + word0, static_cast<int64_t>(ntiles) * kTileChannels * 8);
@@ -704,8 +712,8 @@ template <bool GROUPED> struct Walk {
         t.nv = t.pos >= ntiles || left < 0 ? 0 : left < kTileTokens ? static_cast<int>(left) : kTileTokens;
         return t;
     }
-    __device__ __forceinline__ ChainWords words(const Chain& ch, const Tile& t) const {
-        ChainWords w;
+    template <int LOOK> __device__ __forceinline__ ChainWords<LOOK> words(const Chain& ch, const Tile& t) const {
+        ChainWords<LOOK> w;
         w.init(ch.map, ch.value, (t.b * nct + t.ct) * ntiles * kTileChannels, ntiles);
         return w;
     }

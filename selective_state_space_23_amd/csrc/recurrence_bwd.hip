@@ -53,7 +53,7 @@ struct RecBwdKernelArgs {
 // registers and, with two places for x, dout and z, its LDS.  A register too many costs
 // more than the work it saves: with the gates' terms kept as well, their spills
 // reloaded behind the loads of the next tile, the first case took 770 us.
-template <typename T, bool ALIGNED, bool PIN, bool HAS_Z>
+template <typename T, bool ALIGNED, bool PIN, bool HAS_Z, int LOOK>
 __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(const RecBwdKernelArgs) {
     constexpr bool kStaged = Shape<T, ALIGNED>::kStaged;
     constexpr int kK = Shape<T, ALIGNED>::kK, kWaves = Shape<T, ALIGNED>::kWaves;
@@ -255,10 +255,10 @@ __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(
                 oh[j] = l.half ? h1 : x1;
             }
         }
-        ChainWords::Seen seen = {};
+        typename ChainWords<LOOK>::Seen seen = {};
         auto words = [&]() {
             const auto p = kernel_args<RecBwdKernelArgs>();
-            return walk.words(Chain{p->ch.map, p->ch.value, p->ch.next, p->ch.rate}, t);
+            return walk.template words<LOOK>(Chain{p->ch.map, p->ch.value, p->ch.next, p->ch.rate}, t);
         };
         int ticket = 0;   // wave 0's: the tile after the next one
         if (wave == 0 && ntiles > 1) {
@@ -270,7 +270,7 @@ __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(
             const int lane = static_cast<int>(lane_now()), d = t.ct * kTileChannels + lane;
             const auto p = kernel_args<RecBwdKernelArgs>();
             const auto& a = p->a;
-            const ChainWords chain = words();
+            const ChainWords<LOOK> chain = words();
             float e = row_load(a.d_final_state, t.b, a.dim, d);
             float2 m = s_rev[kWaves - 1][lane];
             s_rev[kWaves - 1][lane] = make_float2(1.0f, 0.0f);   // from here on of all behind a wave
@@ -493,8 +493,13 @@ hipError_t launch_bwd(const RecBwdArgs& a) {
         k.a.states = f.states;
     }
     const int64_t grid = ntiles > 1 && tiles > kResident ? kResident : tiles;
-    hipLaunchKernelGGL((rec_bwd_kernel<T, ALIGNED, PIN, HAS_Z>), dim3(static_cast<unsigned>(grid)),
-                       dim3(Shape<T, ALIGNED>::kThreads), 0, a.stream, k);
+    // (Looking far costs the other variants registers they do not have: float32 with z,
+    // 4 rows of 64 channels 125 us for 103.)
+    auto kernel = rec_bwd_kernel<T, ALIGNED, PIN, HAS_Z, kLookNear>;
+    if constexpr (Shape<T, ALIGNED>::kStaged) {
+        if (look_far(nct * a.batch, ntiles, kResident)) kernel = rec_bwd_kernel<T, ALIGNED, PIN, HAS_Z, kLookFar>;
+    }
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(Shape<T, ALIGNED>::kThreads), 0, a.stream, k);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL(rec_bwd_reduce_kernel, dim3(static_cast<unsigned>((a.dim + 63) / 64)), dim3(1024), 0, a.stream,
                        k.part, a.a_param, a.da_param, a.batch * ntiles, static_cast<int>(a.dim), a.c);

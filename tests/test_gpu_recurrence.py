@@ -472,6 +472,30 @@ def test_repeats_and_streams(ssm):
         assert all(equal(a, b) for a, b in zip(r, want))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,L,D", [(1, 9000, 1), (1, 5000, 68), (3, 4200, 64), (1, 4096, 200)])
+def test_few_long_chains(ssm, B, L, D, dtype):
+    """Rows of 32 tiles and more over few channels: values handed on several tiles at a time."""
+    v = draw(B, L, D, dtype, True, 2000, True, seed=L + D)
+    d = dev(v, dtype)
+    out, fin, kept = forward(ssm, d, save="packed")
+    ref = oracle_fwd(v)
+    close(out, ref[0], dtype, "out")
+    close(fin, ref[1], "f32", "final_state")
+    close(kept["states"], ref[2], "f32", "states")
+    ref = oracle_bwd(v)
+    g, g2 = backward(ssm, d), backward(ssm, d, states=kept["states"])
+    for k in ref:
+        close(g[k], ref[k], dtype if g[k].dtype != d["a_param"].dtype else "f32", k)
+        assert equal(g[k], g2[k]), k
+    dp = dict(d, **{k: kept[k] for k in ("x", "gate_a", "gate_x", "z")})
+    seen = dict(v, **{k: R.unpack8(*R.pack8(v[k])) for k in ("x", "gate_a", "gate_x", "z")})
+    ref = oracle_bwd(seen)
+    g = backward(ssm, dp)
+    for k in ref:
+        close(g[k], ref[k], dtype if g[k].dtype != d["a_param"].dtype else "f32", k)
+
+
 def test_two_calls_at_once(ssm):
     """Calls with workspaces of their own, under way together on two streams and from
     two captured graphs, each larger than the card holds at a time."""
