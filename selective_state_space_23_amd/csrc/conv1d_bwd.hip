@@ -88,8 +88,7 @@ constexpr int kBlock = 256;
 // thread lie in one block: its scale comes with one 4-byte load per token, the
 // same address in the lanes of a block.  (Scales held a token a lane and broadcast
 // from there take as long; four tokens ahead in the general loop are slower, 188 us
-// for 155.)  2 x 32768 x 1536 in bfloat16: 141 us from a checkpoint (593 MB, 4.2 TB/s),
-// 144 from x as stored (693 MB, 4.8 TB/s).
+// for 155.)  2 x 32768 x 1536 in bfloat16: 128 us from a checkpoint (590 MB, 4.6 TB/s).
 template <typename T, int VEC> struct PlainX {
     using Raw = typename VecRaw<T, VEC>::type;
     const void* __restrict__ x;

@@ -29,9 +29,9 @@ constexpr int kThreads = kWaves * 64;
 //
 // What bounds it is memory, then the vector unit (41 issue slots an element, 34 of them
 // in the maps): one row of 65536 x 5120 in
-// bfloat16 without z moves 2.79 GB, of which 2.68 are inputs and outputs, in 641 us:
-// 4.3 TB/s where a copy reaches 5.2, the vector unit issues for 56% of it.  8 rows of 2048 x 1536
-// with z take 77 us (3.3 TB/s): six tiles a workgroup, whose first and last are not
+// bfloat16 without z moves 2.78 GB, of which 2.68 are inputs and outputs, in 620 us:
+// 4.5 TB/s where a copy reaches 5.2, the vector unit issues for 58% of it.  8 rows of
+// 2048 x 1536 with z take 76 us (3.4 TB/s): six tiles a workgroup, whose first and last are not
 // hidden.  Three passes (maps, joining, outputs) read the inputs twice: 1348 us for
 // the first.  A tile's 16 waves a CU, in two workgroups, fill the registers; what a
 // workgroup waits for its neighbours (a third of its time) the other one's work covers.
@@ -344,7 +344,7 @@ __device__ __forceinline__ void quad_store(void* p, int64_t off, int left, const
 
 // One token per row: a thread per four channels of R rows, whose decay parameters it
 // turns into rates once.  2^shift threads lie along a row, `nblocks` workgroups.  Bound
-// by the launch and one trip to memory: 256 rows of 5120 with z take 9.6 us (23.6 MB,
+// by the launch and one trip to memory: 256 rows of 5120 with z take 9.5 us (23.6 MB,
 // 2.5 TB/s), two rows of 1536 3.4 us.
 template <typename T, bool ALIGNED, int R>
 __global__ __launch_bounds__(256) void rec_update_kernel(const RecUpdateArgs a, unsigned nblocks, int shift) {

@@ -47,9 +47,9 @@ struct RecBwdKernelArgs {
 // while the workgroup waits for that adjoint.
 //
 // What bounds it is the vector unit (129 issue slots an element from 8-bit inputs and
-// 114 from tensors, 74% and 66% of the time), then memory: 2 rows of 32768 x 1536 from checkpoints
-// with z take 470 us and move 1.47 GB (3.1 TB/s), 8 rows of 2048 x 1536 from tensors
-// 115 us and 460 MB (4.0 TB/s; 5.2 for a copy).  One workgroup of 16 waves fills a CU's
+// 114 from tensors, 76% and 68% of the time), then memory: 2 rows of 32768 x 1536 from checkpoints
+// with z take 455 us and move 1.47 GB (3.2 TB/s), 8 rows of 2048 x 1536 from tensors
+// 111 us and 460 MB (4.1 TB/s; 5.2 for a copy).  One workgroup of 16 waves fills a CU's
 // registers and, with two places for x, dout and z, its LDS.  A register too many costs
 // more than the work it saves: with the gates' terms kept as well, their spills
 // reloaded behind the loads of the next tile, the first case took 770 us.
