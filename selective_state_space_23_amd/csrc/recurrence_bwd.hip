@@ -198,6 +198,9 @@ __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(
                 oc.template take<k>(y);
                 if constexpr (HAS_Z) zc.template take<k>(z);
                 const bool start = GEN && ((st >> k) & 1u), out = GEN && k >= left;
+                // A start among the lane's tokens so far: told by its bits and not by the sign
+                // of P, which a NaN decay may set or clear.
+                const bool cut = GEN && (st & ((2u << k) - 1u)) != 0;
 #pragma unroll
                 for (int j = 0; j < kV; ++j) {
                     const float r = sigmoid_f(ga[j]);
@@ -221,15 +224,16 @@ __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(
                     }
                     A[k][j] = al;
                     if constexpr (k == 0) {
-                        P[j] = start ? -0.0f : al;
+                        P[j] = cut ? -0.0f : __builtin_fabsf(al);
                         H[j] = bb;
-                        X[j] = start ? 0.0f : al * y[j];
+                        X[j] = cut ? 0.0f : al * y[j];
                     } else {
-                        float p = P[j] * al, h = __builtin_fmaf(al, H[j], bb);
-                        if constexpr (GEN) asm volatile("" : "+v"(p), "+v"(h));   // selects, not a branch
-                        P[j] = start ? -0.0f : p;
+                        float p = __builtin_fabsf(P[j] * al), h = __builtin_fmaf(al, H[j], bb);
+                        float x1 = __builtin_fmaf(p, y[j], X[j]);
+                        if constexpr (GEN) asm volatile("" : "+v"(p), "+v"(h), "+v"(x1));   // selects, not a branch
+                        P[j] = cut ? -0.0f : p;
                         H[j] = start ? bb : h;
-                        X[j] = apply<GEN>(P[j], X[j], y[j]);
+                        X[j] = cut ? X[j] : x1;
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);

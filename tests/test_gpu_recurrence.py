@@ -627,3 +627,46 @@ def test_offsets_past_4_gib(ssm):
     g2 = ssm.gated_recurrence_bwd(k2["x"], k2["gate_a"], k2["gate_x"], ap[s], o2, states=k2["states"])
     for k in g2:
         assert equal(g2[k], grads[k][..., s]), k
+
+
+def nan_bits(t, index, sign):
+    """Sets one element to a NaN with the given sign bit."""
+    import torch
+
+    if t.dtype == torch.bfloat16:
+        t.view(torch.int16)[index] = -64 if sign else 0x7FC0
+    else:
+        t.view(torch.int32)[index] = -0x400000 if sign else 0x7FC00000
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sign", [0, 1])
+@pytest.mark.parametrize("z", [False, True])
+def test_nan_gates_reach_their_document(ssm, dtype, sign, z):
+    """A NaN decay, whatever its sign, spoils the gradients of the earlier tokens of its
+    document, and of no other document: the oracle's finite elements are finite and
+    close, the others are not."""
+    B, L, D = 1, 520, 12
+    v = draw(B, L, D, dtype, z, None, True, seed=41)
+    v["doc_start"] = np.zeros((B, L), np.uint8)
+    v["doc_start"][0, [130, 200, 300, 301, 381]] = 1
+    d = dev(v, dtype)
+    # in the lane of a start (behind, before, at it), inside a document, in a tile without
+    # starts, in the row's last tile, and between two starts of one lane
+    for c, t in enumerate((201, 199, 200, 210, 60, 519, 301, 300, 382, 383)):
+        nan_bits(d["gate_a"], (0, t, c), sign)
+        v["gate_a"][0, t, c] = np.nan
+    states = forward(ssm, d, save="states")[2]["states"]
+    ref = oracle_bwd(v)
+    for kw in ({}, {"states": states}):
+        g = backward(ssm, d, **kw)
+        for k in ("dx", "dgate_a", "dgate_x", "d_initial_state", "da_param") + (("dz",) if z else ()):
+            fine = np.isfinite(ref[k])
+            assert np.array_equal(np.isfinite(to_host(g[k])), fine), k
+            close(g[k][np_mask(fine, g[k])], ref[k][fine], dtype if g[k].dtype == d["x"].dtype else "f32", k)
+
+
+def np_mask(m, like):
+    import torch
+
+    return torch.from_numpy(m).to(like.device)
