@@ -284,9 +284,6 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(
                 since = 0;
             }
             const bool own = t < own_end;
-            const float m1 = since >= 1 ? 1.0f : 0.0f;
-            const float m2 = since >= 2 ? 1.0f : 0.0f;
-            const float m3 = since >= 3 ? 1.0f : 0.0f;
             float out[VEC];
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
@@ -306,10 +303,12 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(
                     gw1[i] = __builtin_fmaf(g, h2[i], gw1[i]);
                     gw0[i] = __builtin_fmaf(g, h3[i], gw0[i]);
                 }
-                // dx_{t-3} is complete after token t's tap; shift the others along.
-                out[i] = __builtin_fmaf(g * m3, w0[i], p3[i]);
-                p3[i] = __builtin_fmaf(g * m2, w1[i], p2[i]);
-                p2[i] = __builtin_fmaf(g * m1, w2[i], p1[i]);
+                // dx_{t-3} is complete after token t's tap; shift the others along.  Taps on
+                // another document are left out by selects: a NaN or an infinity in g times
+                // zero would reach it.
+                out[i] = since >= 3 ? __builtin_fmaf(g, w0[i], p3[i]) : p3[i];
+                p3[i] = since >= 2 ? __builtin_fmaf(g, w1[i], p2[i]) : p2[i];
+                p2[i] = since >= 1 ? __builtin_fmaf(g, w2[i], p1[i]) : p1[i];
                 p1[i] = g * w3[i];
                 h3[i] = h2[i];
                 h2[i] = h1[i];
