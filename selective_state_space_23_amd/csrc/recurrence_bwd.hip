@@ -38,6 +38,7 @@ struct RecBwdKernelArgs {
     Chain ch;
     float* part;       // (B * tiles, D): sum of r dlog a over a tile
     int nct, ntiles;
+    int tile0;         // rows of one tile: the launch's first
 };
 
 // One pass over the data, from the row ends back.  A workgroup works off tiles as
@@ -128,7 +129,7 @@ __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(
         if (cur >= walk.tickets) return;
         if constexpr (kStaged) fetch(place(cur));
     } else {
-        cur = static_cast<int>(blockIdx.x);
+        cur = first->tile0 + static_cast<int>(blockIdx.x);
         next = kNone;
         const Tile t = place(cur);
         fetch(t);
@@ -450,6 +451,9 @@ __global__ __launch_bounds__(1024) void rec_bwd_reduce_kernel(const float* __res
 }
 
 constexpr int kResident = 256;   // one workgroup a CU
+// A launch holds fewer than 2^32 threads: of rows of one tile, which take a workgroup
+// each, a call with more tiles is launched in pieces.
+constexpr int64_t kMaxGrid = int64_t(1) << 21;
 
 struct BwdWs {
     size_t part, chain, chain_bytes, states, total;
@@ -476,7 +480,7 @@ hipError_t launch_bwd(const RecBwdArgs& a) {
     const int64_t tiles = nct * a.batch * ntiles;
     const BwdWs w = bwd_ws(a.batch, a.seqlen, a.dim, a.states != nullptr);
     char* ws = static_cast<char*>(a.ws);
-    RecBwdKernelArgs k{a, Chain{}, reinterpret_cast<float*>(ws + w.part), nct, ntiles};
+    RecBwdKernelArgs k{a, Chain{}, reinterpret_cast<float*>(ws + w.part), nct, ntiles, 0};
     const bool recompute = a.states == nullptr && ntiles > 1;
     Chain chains[2];
     hipError_t e = clear_chains(ws + w.chain, recompute ? 2 : 1, w.chain_bytes, a.batch, a.dim, ntiles, a.a_param, a.c,
@@ -503,8 +507,13 @@ hipError_t launch_bwd(const RecBwdArgs& a) {
     if constexpr (Shape<T, ALIGNED>::kStaged) {
         if (look_far(nct * a.batch, ntiles, kResident)) kernel = rec_bwd_kernel<T, ALIGNED, PIN, HAS_Z, kLookFar>;
     }
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(Shape<T, ALIGNED>::kThreads), 0, a.stream, k);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    static_assert(kMaxGrid * Shape<T, ALIGNED>::kThreads < (int64_t(1) << 32) && kMaxGrid >= kResident);
+    for (int64_t first = 0; first < grid; first += kMaxGrid) {
+        k.tile0 = static_cast<int>(first);
+        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid - first < kMaxGrid ? grid - first : kMaxGrid)),
+                           dim3(Shape<T, ALIGNED>::kThreads), 0, a.stream, k);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
     hipLaunchKernelGGL(rec_bwd_reduce_kernel, dim3(static_cast<unsigned>((a.dim + 63) / 64)), dim3(1024), 0, a.stream,
                        k.part, a.a_param, a.da_param, a.batch * ntiles, static_cast<int>(a.dim), a.c);
     return hipGetLastError();

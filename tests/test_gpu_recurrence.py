@@ -670,3 +670,29 @@ def np_mask(m, like):
     import torch
 
     return torch.from_numpy(m).to(like.device)
+
+
+def test_backward_of_many_short_rows(ssm):
+    """4.26 million tiles of one token, more than one launch's 2^32 threads hold: the same bits
+    as in calls of 4096 rows, and their da_param.
+
+    x and dout are positive and no state enters, so that every term of da_param has one sign:
+    a sum of 65535 of them, 4096 one after the other and 16 such sums, is off by at most
+    4112 x 2^-24 of itself, the calls' own (256 and 16, 16 calls in 64 bits) by 272 x 2^-24."""
+    import torch
+
+    B, L, D = 65535, 1, 4160
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x, dout = (torch.rand(B, L, D, generator=g, device="cuda", dtype=torch.bfloat16) + 0.5 for _ in range(2))
+    ga, gx = (torch.randn(B, L, D, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    ap = torch.linspace(-5.0, -1.0, D, device="cuda")
+    full = ssm.gated_recurrence_bwd(x, ga, gx, ap, dout)
+    total = torch.zeros(D, dtype=torch.float64, device="cuda")
+    for r in range(0, B, 4096):
+        s = slice(r, r + 4096)
+        part = ssm.gated_recurrence_bwd(x[s], ga[s], gx[s], ap, dout[s])
+        for k in ("dx", "dgate_a", "dgate_x"):
+            assert equal(full[k][s], part[k]), (r, k)
+        total += part["da_param"].double()
+    assert total.abs().min() > 0
+    assert ((full["da_param"].double() - total).abs() <= 4400 * 2.0 ** -24 * total.abs()).all()
