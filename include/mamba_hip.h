@@ -501,7 +501,8 @@ int mamba_gated_recurrence_bwd(const mamba_recurrence_dims_t* dims, const void* 
 
 /* One token per row: h <- a h + sqrt(1 - a^2) i x (h read as 0 where reset is set),
  * out = h silu(z).
- *   dims       with seqlen == 1; strides are between rows.
+ *   dims       with seqlen == 1; strides are between rows, of up to 2^40 elements (a
+ *              column of (B, L, D) tensors is a step's input as it is).
  *   state      (B, D) float32, in place.
  *   x, gate_a, gate_x, z (B, D); reset (B,) uint8 or NULL; out (B, D). */
 int mamba_gated_recurrence_update(const mamba_recurrence_dims_t* dims, float* state, const void* x,

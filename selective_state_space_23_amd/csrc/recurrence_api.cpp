@@ -20,6 +20,7 @@ namespace {
 using namespace mamba::api;
 
 constexpr int64_t kMaxWidth = int64_t(1) << 21;   // channels and strides: a tile's offsets fit 32 bits
+constexpr int64_t kMaxRowStride = kMaxElems;      // the one-token step's, which addresses in 64 bits
 constexpr int64_t kMaxTiles = 8000000;            // workgroups of one launch
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -47,7 +48,8 @@ size_t span(int64_t rows, int64_t dim, int64_t ld, size_t esz) {
     return static_cast<size_t>((rows - 1) * ld + dim) * esz;
 }
 
-int check_rec_dims(const mamba_recurrence_dims_t* d) {
+// `max_ld`: of the step's own inputs (dout is none of them).
+int check_rec_dims(const mamba_recurrence_dims_t* d, int64_t max_ld = kMaxWidth) {
     if (!d) return MAMBA_ERR_INVALID_ARGUMENT;
     if (d->batch < 0 || d->seqlen < 0 || d->dim < 0 || d->batch > 65535) return MAMBA_ERR_INVALID_ARGUMENT;
     if (d->dtype != MAMBA_DTYPE_F32 && d->dtype != MAMBA_DTYPE_BF16) return MAMBA_ERR_INVALID_ARGUMENT;
@@ -55,8 +57,9 @@ int check_rec_dims(const mamba_recurrence_dims_t* d) {
     const int64_t lds[] = {d->ld_x, d->ld_gate_a, d->ld_gate_x, d->ld_z, d->ld_dout};
     for (int64_t ld : lds) {
         if (ld < 0 || (ld != 0 && ld < d->dim)) return MAMBA_ERR_INVALID_ARGUMENT;
-        if (ld > kMaxWidth) return MAMBA_ERR_UNSUPPORTED;
+        if (ld > max_ld) return MAMBA_ERR_UNSUPPORTED;
     }
+    if (d->ld_dout > kMaxWidth) return MAMBA_ERR_UNSUPPORTED;
     if (d->dim > kMaxWidth || d->seqlen > kMaxSeqlen) return MAMBA_ERR_UNSUPPORTED;
     if (d->batch * ceil_div(d->seqlen, mamba::kRecChunk) * ceil_div(d->dim, mamba::kPackBlock) > kMaxTiles)
         return MAMBA_ERR_UNSUPPORTED;
@@ -307,7 +310,7 @@ int mamba_gated_recurrence_bwd(const mamba_recurrence_dims_t* dims, const void* 
 int mamba_gated_recurrence_update(const mamba_recurrence_dims_t* dims, float* state, const void* x,
                                   const void* gate_a, const void* gate_x, const float* a_param, const void* z,
                                   const uint8_t* reset, void* out, void* stream) {
-    const int st = check_rec_dims(dims);
+    const int st = check_rec_dims(dims, kMaxRowStride);
     if (st != MAMBA_OK) return st;
     if (dims->seqlen != 1) return MAMBA_ERR_INVALID_ARGUMENT;
     const int64_t B = dims->batch, D = dims->dim;
@@ -318,10 +321,10 @@ int mamba_gated_recurrence_update(const mamba_recurrence_dims_t* dims, float* st
         (z && !aligned(z, esz)) || !aligned(out, esz) || !aligned(a_param, 4))
         return MAMBA_ERR_MISALIGNED;
     mamba::RecUpdateArgs a{};
-    a.ld_x = static_cast<int>(dims->ld_x ? dims->ld_x : D);
-    a.ld_a = static_cast<int>(dims->ld_gate_a ? dims->ld_gate_a : D);
-    a.ld_g = static_cast<int>(dims->ld_gate_x ? dims->ld_gate_x : D);
-    a.ld_z = static_cast<int>(dims->ld_z ? dims->ld_z : D);
+    a.ld_x = dims->ld_x ? dims->ld_x : D;
+    a.ld_a = dims->ld_gate_a ? dims->ld_gate_a : D;
+    a.ld_g = dims->ld_gate_x ? dims->ld_gate_x : D;
+    a.ld_z = dims->ld_z ? dims->ld_z : D;
     const Span ins[] = {{x, span(B, D, a.ld_x, esz)}, {gate_a, span(B, D, a.ld_a, esz)},
                         {gate_x, span(B, D, a.ld_g, esz)}, {z, span(B, D, a.ld_z, esz)},
                         {a_param, static_cast<size_t>(D) * 4}, {reset, static_cast<size_t>(B)}};

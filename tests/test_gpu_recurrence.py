@@ -696,3 +696,26 @@ def test_backward_of_many_short_rows(ssm):
         total += part["da_param"].double()
     assert total.abs().min() > 0
     assert ((full["da_param"].double() - total).abs() <= 4400 * 2.0 ** -24 * total.abs()).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [1024, 1022])
+def test_step_on_columns_of_long_rows(ssm, dtype, D):
+    """One token of (B, L, D) tensors whose rows lie 2.1 million elements and more apart."""
+    import torch
+
+    B, L, t = 3, 2100, 2099
+    v = draw(B, 1, D, dtype, True, None, True, seed=45)
+    d = dev(v, dtype)
+    names = ("x", "gate_a", "gate_x", "z")
+    long = {n: torch.zeros(B, L, D, dtype=d["x"].dtype, device="cuda") for n in names}
+    for n in names:
+        long[n][:, t] = d[n][:, 0]
+    got = []
+    for x, ga, gx, z in ([d[n][:, 0] for n in names], [long[n][:, t] for n in names]):
+        state = d["initial_state"].clone()
+        got.append((ssm.gated_recurrence_update(state, x, ga, gx, d["a_param"], z), state))
+    ref = oracle_fwd(v)
+    close(got[1][0], ref[0][:, 0], dtype, "out")
+    close(got[1][1], ref[1], "f32", "state")
+    assert equal(got[0][0], got[1][0]) and equal(got[0][1], got[1][1])

@@ -211,3 +211,16 @@ def test_binding_strides():
         at(proj, (2, 5, 11))
     with pytest.raises(ValueError, match="must be"):
         at(proj.double())
+
+
+def test_step_strides(lib):
+    """The step's rows may lie further apart than a tile's tokens: refused for the missing
+    state, not for the stride."""
+    far = 1 << 22
+    for k in ("ld_x", "ld_gate_a", "ld_gate_x", "ld_z"):
+        assert update(lib, dims(seqlen=1, **{k: far}), state=None) == INVALID, k
+        assert update(lib, dims(seqlen=1, **{k: (1 << 40) + 1})) == UNSUPPORTED, k
+        assert update(lib, dims(seqlen=1, **{k: 63}), state=None) == INVALID, k
+        assert fwd(lib, dims(seqlen=1, **{k: far})) == UNSUPPORTED and bwd(lib, dims(seqlen=1, **{k: far})) == UNSUPPORTED, k
+    # an output inside the last, far row of an input
+    assert update(lib, dims(seqlen=1, ld_x=far), out=AT["x"] + 2 * far) == INVALID
