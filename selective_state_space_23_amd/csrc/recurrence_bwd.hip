@@ -33,6 +33,20 @@ template <typename T, bool ALIGNED> struct Shape {
     static constexpr int kThreads = kWaves * 64;
 };
 
+// A gate's sigmoid r and the rest 1 - r in one register, each to its own size: the
+// difference from the rounded r is 1% off at a gate of 12 and gone from 17 on.  With
+// e = exp(-gate) the rest is e r; kept is r, or minus the rest where that is the smaller
+// (never 0: its sign tells which), and both are s - floor(s) of it and of its negative.
+// An r of 0 leaves a rest of 0 in place of 1; every term it multiplies is 0 then.
+struct SplitGate {
+    __device__ __forceinline__ static float pack(float gate, float e, float r) {
+        const float rest = __builtin_fmaxf(e * r, 0x1p-126f);
+        return gate > 0.0f ? -rest : r;
+    }
+    __device__ __forceinline__ static float r(float s) { return __builtin_amdgcn_fractf(s); }
+    __device__ __forceinline__ static float rest(float s) { return __builtin_amdgcn_fractf(-s); }
+};
+
 struct RecBwdKernelArgs {
     RecBwdArgs a;
     Chain ch;
@@ -185,7 +199,7 @@ __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(
             wait_lds_reads();
         }
         if constexpr (kStaged) fetch(place(next));   // past the last ticket: a tile of no tokens, nothing is read
-        // Of every token: a, r, w i, 1 - i and r v / w.
+        // Of every token: a, r or r - 1 (SplitGate), w i, 1 - i and r v / w.
         float A[kK][kV], R[kK][kV], W[kK][kV], O[kK][kV], V[kK][kV];
         float P[kV], H[kV], X[kV];
         auto maps = [&](auto gen) {
@@ -204,18 +218,19 @@ __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(
                 const bool cut = GEN && (st & ((2u << k) - 1u)) != 0;
 #pragma unroll
                 for (int j = 0; j < kV; ++j) {
-                    const float r = sigmoid_f(ga[j]);
+                    const float ea = exp2_fast(-ga[j] * kLog2e), r = rcp_fast(1.0f + ea);
                     float al, om;
                     decay_terms(rc[j] * r, al, om);
                     float rw = __builtin_amdgcn_rsqf(om);
                     asm volatile("" : "+v"(rw));
                     rw = om >= 0x1p-126f ? rw : 0.0f;   // denormals count as 0
-                    const float ig = sigmoid_f(gx[j]);
+                    const float eg = exp2_fast(-gx[j] * kLog2e), ig = rcp_fast(1.0f + eg);
                     rw *= ig;
                     if constexpr (HAS_Z) y[j] *= silu_f(z[j]);
-                    R[k][j] = r;
+                    R[k][j] = SplitGate::pack(ga[j], ea, r);
                     W[k][j] = om * rw;
-                    O[k][j] = 1.0f - ig;
+                    O[k][j] = __builtin_fminf(eg, 0x1p126f) * ig;   // 1 - ig; past the bound W is 0 or denormal
+                    asm volatile("" : "+v"(R[k][j]), "+v"(O[k][j]));   // here, not where they are used
                     V[k][j] = (r * rw) * x[j];
                     float bb = W[k][j] * x[j];
                     if constexpr (GEN) {
@@ -333,6 +348,8 @@ __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(
                 zc.template take<k>(z);
 #pragma unroll
                 for (int j = 0; j < kV; ++j) {
+                    // (float32: formed anew, the ones of the maps take registers that spill)
+                    if constexpr (sizeof(T) == 4) asm volatile("" : "+v"(z[j]));
                     const float sg = sigmoid_f(z[j]);
                     Z[k][j] = y[j] * (sg * __builtin_fmaf(z[j], 1.0f - sg, 1.0f));
                     Y[k][j] = y[j] * (z[j] * sg);
@@ -398,8 +415,10 @@ __global__ __launch_bounds__((Shape<T, ALIGNED>::kThreads)) void rec_bwd_kernel(
                         const float G = y[j] + e[j];
                         dx[j] = G * W[k][j];
                         dg[j] = dx[j] * x[j] * O[k][j];
-                        const float q = G * (A[k][j] * __builtin_fmaf(-A[k][j], V[k][j], R[k][j] * before));
-                        da[j] = (kLn2 * rc[j]) * (1.0f - R[k][j]) * q;   // kLn2 rate = -c softplus(a_param)
+                        float s = R[k][j];
+                        asm volatile("" : "+v"(s));   // taken apart here, not in both parts where it is formed
+                        const float q = G * (A[k][j] * __builtin_fmaf(-A[k][j], V[k][j], SplitGate::r(s) * before));
+                        da[j] = (kLn2 * rc[j]) * SplitGate::rest(s) * q;   // kLn2 rate = -c softplus(a_param)
                         sum[j] += out ? 0.0f : q;
                         e[j] = start ? 0.0f : A[k][j] * G;
                     }

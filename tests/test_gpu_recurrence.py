@@ -719,3 +719,26 @@ def test_step_on_columns_of_long_rows(ssm, dtype, D):
     close(got[1][0], ref[0][:, 0], dtype, "out")
     close(got[1][1], ref[1], "f32", "state")
     assert equal(got[0][0], got[1][0]) and equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 67])
+def test_gradients_of_far_gates(ssm, dtype, D):
+    """Gates of 10 to 16 and -16 to -10: every element of the gate gradients to its own size.
+
+    Every token starts a document and there is no z, so that both gradients are products:
+    dgate_x = dout w i x (1 - i), dgate_a = -c softplus (1 - r) r dout (-a^2 i x / w).  Their factors
+    round some 2^-24 each, 30 of them at most, and an exponential of 16 log2(e) = 23
+    (rounded by 2^-24 of it) is off by 23 x 0.7 x 2^-24, twice where both gates enter: 64 x 2^-24."""
+    B, L = 2, 140
+    v = draw(B, L, D, dtype, False, None, False, seed=43)
+    g = np.random.default_rng(44)
+    for n in ("gate_a", "gate_x"):
+        far = (g.uniform(10, 16, (B, L, D)) * g.choice([-1.0, 1.0], (B, L, D))).astype(np.float32)
+        v[n] = bf16_round(far) if dtype == "bf16" else far
+    v["doc_start"] = np.ones((B, L), np.uint8)
+    got, ref = backward(ssm, dev(v, dtype)), oracle_bwd(v)
+    rtol = 64 * 2.0 ** -24 + (2.0 ** -8 if dtype == "bf16" else 0.0)
+    for k in ("dx", "dgate_x", "dgate_a"):
+        err = np.abs(to_host(got[k]) - ref[k]) / np.abs(ref[k])
+        assert err.max() <= rtol, f"{k}: off by {err.max()} of the element, {int((err > rtol).sum())} of {err.size}"
