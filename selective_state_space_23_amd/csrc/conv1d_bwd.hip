@@ -37,9 +37,7 @@ template <> struct VecIO<bf16_t, 2> {
         v[1] = __uint_as_float(raw & 0xffff0000u);
     }
     __device__ __forceinline__ static void store(void* base, int64_t off, const float (&v)[2]) {
-        // written once, whole lines a wave: first to leave the L2
-        __builtin_nontemporal_store(pack_bf16x2(v[0], v[1]),
-                                    reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(base) + off));
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(base) + off) = pack_bf16x2(v[0], v[1]);
     }
 };
 template <> struct VecIO<float, 2> {
@@ -120,7 +118,17 @@ template <int VEC> struct PackedX {
     }
 };
 
-template <typename T, int VEC, bool SILU, typename X>
+// dx of a token.  LARGE: whole lines written once leave the L2 first.
+template <typename T, int VEC, bool LARGE>
+__device__ __forceinline__ void store_dx(void* base, int64_t off, const float (&v)[VEC]) {
+    if constexpr (LARGE && sizeof(T) == 2 && VEC == 2)
+        __builtin_nontemporal_store(pack_bf16x2(v[0], v[1]),
+                                    reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(base) + off));
+    else
+        VecIO<T, VEC>::store(base, off, v);
+}
+
+template <typename T, int VEC, bool SILU, typename X, bool LARGE>
 __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(
     const X x, const float* __restrict__ weight, const float* __restrict__ bias,
     const uint8_t* __restrict__ doc_start, const void* __restrict__ conv_state, const void* __restrict__ du,
@@ -190,12 +198,8 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(
     for (int k = 0; k < 3; ++k)
         if ((starts >> k) & 1ull) since = 3 - k;
     const int64_t own_end = (t0 + kTile < seqlen) ? t0 + kTile : seqlen;
-    // Tiles inside a row without a document start among their tokens, the 3 before and
-    // the 3 after take every tap: the same operations without the masks, four tokens at a
-    // time, the next four under way (both loops in place of the general one alone: 168 us
-    // to 148 from a checkpoint, sums of the partials included).
     const bool all_taps = t0 >= 3 && t0 + kTile + 3 <= seqlen && (starts & ((1ull << (kTile + 6)) - 1)) == 0;
-    if (all_taps) {
+    if (LARGE && all_taps) {   // a tile whose taps all stay in the row and one document: no selects, four tokens at a time
         constexpr int kStep = 4;
         static_assert(kTile % kStep == 0);
         typename X::Raw xn[kStep];
@@ -245,7 +249,7 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(
                 VecRaw<T, VEC>::get(gn[k], gv);
                 fetch(k, t + kStep + k);
                 taps(xv, gv, out, true);
-                if (t + k >= t0 + 3) VecIO<T, VEC>::store(dx, (row + t + k - 3) * dim + d0, out);
+                if (t + k >= t0 + 3) store_dx<T, VEC, LARGE>(dx, (row + t + k - 3) * dim + d0, out);
             }
         }
 #pragma unroll
@@ -254,7 +258,7 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(
             X::get(xn[k], xv);
             VecRaw<T, VEC>::get(gn[k], gv);
             taps(xv, gv, out, false);
-            VecIO<T, VEC>::store(dx, (row + t0 + kTile + k - 3) * dim + d0, out);
+            store_dx<T, VEC, LARGE>(dx, (row + t0 + kTile + k - 3) * dim + d0, out);
         }
     } else {
         // x and du of the next token are fetched while the current one computes.
@@ -317,7 +321,7 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(
             since = since < 3 ? since + 1 : 3;
             const int64_t s = t - 3;
             if (s >= t0 && s < own_end) {
-                VecIO<T, VEC>::store(dx, (row + s) * dim + d0, out);
+                store_dx<T, VEC, LARGE>(dx, (row + s) * dim + d0, out);
             } else if (s < 0 && d_conv_state != nullptr) {
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) d_conv_state[(b * dim + d0 + i) * 3 + (3 + s)] = out[i];
@@ -372,20 +376,34 @@ __global__ __launch_bounds__(1024) void conv1d_bwd_reduce_kernel(const float* __
     else if (dbias) dbias[d] = tot;
 }
 
+template <typename T, int VEC, typename X, bool LARGE>
+hipError_t launch_conv_bwd_tiles(const ConvBwdArgs& a, const X& x, dim3 grid) {
+    if (a.apply_silu)
+        hipLaunchKernelGGL((conv1d_bwd_kernel<T, VEC, true, X, LARGE>), grid, dim3(kBlock), 0, a.stream, x, a.weight,
+                           a.bias, a.doc_start, a.conv_state, a.du, a.dx, a.d_conv_state, a.ws, a.seqlen,
+                           static_cast<int>(a.dim));
+    else
+        hipLaunchKernelGGL((conv1d_bwd_kernel<T, VEC, false, X, LARGE>), grid, dim3(kBlock), 0, a.stream, x, a.weight,
+                           a.bias, a.doc_start, a.conv_state, a.du, a.dx, a.d_conv_state, a.ws, a.seqlen,
+                           static_cast<int>(a.dim));
+    return hipGetLastError();
+}
+
 template <typename T, int VEC, typename X>
 hipError_t launch_conv_bwd_x(const ConvBwdArgs& a, const X& x) {
     const int ngroups = static_cast<int>((a.dim + VEC - 1) / VEC);
     const int64_t ntiles = (a.seqlen + kTile - 1) / kTile;
-    dim3 grid((ngroups + kBlock - 1) / kBlock, static_cast<unsigned>(ntiles), static_cast<unsigned>(a.batch));
-    if (a.apply_silu)
-        hipLaunchKernelGGL((conv1d_bwd_kernel<T, VEC, true, X>), grid, dim3(kBlock), 0, a.stream, x, a.weight,
-                           a.bias, a.doc_start, a.conv_state, a.du, a.dx, a.d_conv_state, a.ws, a.seqlen,
-                           static_cast<int>(a.dim));
-    else
-        hipLaunchKernelGGL((conv1d_bwd_kernel<T, VEC, false, X>), grid, dim3(kBlock), 0, a.stream, x, a.weight,
-                           a.bias, a.doc_start, a.conv_state, a.du, a.dx, a.d_conv_state, a.ws, a.seqlen,
-                           static_cast<int>(a.dim));
-    hipError_t e = hipGetLastError();
+    const dim3 grid((ngroups + kBlock - 1) / kBlock, static_cast<unsigned>(ntiles), static_cast<unsigned>(a.batch));
+    // The general loop alone leaves room for 8 waves a SIMD, 2048 workgroups; beside the fast
+    // loop it has 6 or 7.  A grid that is there at once waits for its slowest tiles, and a
+    // row's ends always take the general loop: the fast one gains nothing (8 x 2048 x 1536 in bfloat16 46
+    // us alone and 53 with both; 15 x 2048 74 and 84; float32 as fast or slower from 1536 workgroups
+    // on, from a checkpoint 131 and 124).  What such a call writes fits the caches and stays there.
+    // Above, the inner tiles' share decides: 2 x 32768 x 1536 in bfloat16 164 alone and 140 with
+    // both, in documents of 30 tokens 165 and 172 (float32 301 and 279, 300 and 316).
+    const bool large = static_cast<int64_t>(grid.x) * ntiles * a.batch > (sizeof(T) == 4 ? 1536 : 2048);
+    const hipError_t e = large ? launch_conv_bwd_tiles<T, VEC, X, true>(a, x, grid)
+                               : launch_conv_bwd_tiles<T, VEC, X, false>(a, x, grid);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(conv1d_bwd_reduce_kernel, dim3(static_cast<unsigned>((5 * a.dim + 63) / 64)), dim3(1024), 0,
                        a.stream, static_cast<const float*>(a.ws), a.dweight, a.dbias, a.batch * ntiles,
@@ -413,9 +431,10 @@ size_t conv_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
 }
 
 // Pairs of channels for either dtype: the history, pending-dx and gradient
-// registers of 2 channels leave room for 8 waves per SIMD, which hides the
-// loads' latency better than 4 channels a thread at 4 waves (measured 187 vs
-// 233 us on the packed 32K workload; fetching 2 or 3 tokens ahead did not help).
+// registers of 2 channels leave room for 8 waves per SIMD (6 or 7 with both loops),
+// which hides the loads' latency better than 4 channels a thread at 4 waves (187 and
+// 233 us on the packed 32K workload with the general loop alone, where fetching 2 or 3
+// tokens ahead did not help).
 hipError_t launch_causal_conv1d_bwd(const ConvBwdArgs& a) { return launch_conv_bwd(a, nullptr); }
 hipError_t launch_causal_conv1d_bwd_packed(const ConvBwdArgs& a, const Packed& in) { return launch_conv_bwd(a, &in); }
 
