@@ -20,6 +20,12 @@ namespace {
 constexpr int kK = 8;                                // tokens a lane walks
 constexpr int kWaves = kTileTokens / (2 * kK);       // two halves of 32 lanes a wave
 constexpr int kThreads = kWaves * 64;
+constexpr int kCus = 256;
+
+// Workgroups of a variant that a CU holds, 2 waves a SIMD each: float32 and unaligned inputs, which
+// wait in registers, leave room for two where nothing but out is written, or nothing at all.
+template <typename T, bool ALIGNED, bool HAS_Z, bool SAVE, bool OUT, int LOOK>
+constexpr int kPerCu = (sizeof(T) == 2 && ALIGNED) || !OUT || (!HAS_Z && !SAVE && LOOK == kLookNear) ? 2 : 1;
 
 // One pass over the data.  A workgroup works off tiles until none is left (rows
 // of one tile: one workgroup each); a tile's maps stay in registers while the value
@@ -33,8 +39,9 @@ constexpr int kThreads = kWaves * 64;
 // 4.5 TB/s where a copy reaches 5.2, the vector unit issues for 58% of it.  8 rows of
 // 2048 x 1536 with z take 76 us (3.4 TB/s): six tiles a workgroup, whose first and last are not
 // hidden.  Three passes (maps, joining, outputs) read the inputs twice: 1348 us for
-// the first.  A tile's 16 waves a CU, in two workgroups, fill the registers; what a
-// workgroup waits for its neighbours (a third of its time) the other one's work covers.
+// the first.  A tile's 16 waves a CU, in two workgroups, fill the registers (float32 and unaligned
+// inputs: kPerCu); what a workgroup waits for its neighbours (a third of its time) the
+// other one's work covers.
 // Staging through LDS in place of registers took the first case from 785 us to 708,
 // drawing tickets one tile ahead and not two the second from 91 to 82.
 struct RecFwdKernelArgs {
@@ -44,7 +51,8 @@ struct RecFwdKernelArgs {
 };
 
 template <typename T, bool ALIGNED, bool PIN, bool HAS_Z, bool SAVE, bool OUT, int LOOK>
-__global__ __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 4 : 2) void rec_fwd_kernel(const RecFwdKernelArgs) {
+__global__ __launch_bounds__(kThreads, (2 * kPerCu<T, ALIGNED, HAS_Z, SAVE, OUT, LOOK>)) void rec_fwd_kernel(
+    const RecFwdKernelArgs) {
     __shared__ float s_rate[kTileChannels];
     __shared__ float s_in[kTileChannels];                 // the values entering the tile
     __shared__ float2 s_agg[kWaves + 1][kTileChannels];   // the waves' maps; the last row takes what no one reads
@@ -288,7 +296,6 @@ __global__ __launch_bounds__(256) void rec_clear_kernel(char* __restrict__ ws, s
     if (i < nrate) rate[i] = -c * kLog2e * softplus_exact(a_param[i < dim ? i : dim - 1]);
 }
 
-constexpr int kResident = 512;   // two workgroups a CU: 4 waves per SIMD
 
 template <typename T, bool ALIGNED, bool PIN, bool HAS_Z, bool SAVE, bool OUT>
 hipError_t launch_fwd(const RecFwdArgs& a) {
@@ -302,9 +309,13 @@ hipError_t launch_fwd(const RecFwdArgs& a) {
         const hipError_t e = clear_chains(a.ws, 1, 0, a.batch, a.dim, ntiles, a.a_param, a.c, &ch, a.stream);
         if (e != hipSuccess) return e;
     }
-    const int64_t grid = ntiles > 1 && tiles > kResident ? kResident : tiles;
     auto kernel = rec_fwd_kernel<T, ALIGNED, PIN, HAS_Z, SAVE, OUT, kLookNear>;
-    if (look_far(nct * a.batch, ntiles, kResident)) kernel = rec_fwd_kernel<T, ALIGNED, PIN, HAS_Z, SAVE, OUT, kLookFar>;
+    int64_t resident = kCus * kPerCu<T, ALIGNED, HAS_Z, SAVE, OUT, kLookNear>;
+    if (look_far(nct * a.batch, ntiles, 16)) {
+        kernel = rec_fwd_kernel<T, ALIGNED, PIN, HAS_Z, SAVE, OUT, kLookFar>;
+        resident = kCus * kPerCu<T, ALIGNED, HAS_Z, SAVE, OUT, kLookFar>;
+    }
+    const int64_t grid = ntiles > 1 && tiles > resident ? resident : tiles;
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, a.stream,
                        RecFwdKernelArgs{a, ch, nct, ntiles});
     return hipGetLastError();

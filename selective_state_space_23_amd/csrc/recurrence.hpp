@@ -573,14 +573,13 @@ struct Chain {
 };
 
 // Earlier positions looked at.  A long row's value goes from tile to tile by as many
-// positions a trip: where 32 and more of a chain's tiles are under way, that is what a call
-// takes (65536 x 512 in bfloat16 132 us for 194, 32768 x 128 in float32 43 for 81); where
-// fewer are, more words to read gain nothing (from 24 chains on) or cost some.
+// positions a trip: with few chains that is what a call takes (65536 x 512 in bfloat16 132
+// us for 194, 32768 x 128 in float32 43 for 81).  `most` chains, of 32 tiles and more, look
+// far: 16 in the forward, whatever the type (16384 tokens, far and near: bfloat16 with
+// z and checkpoints 12 chains 66 and 75, 16 81 and 83; float32 9 chains 44 and 74, 16 62 and 78, 24 95 and
+// 96; with z 9 chains 54 and 59, 16 74 and 74, 24 111 and 108), 8 in the backward.
 constexpr int kLookNear = 2, kLookFar = 8;
-inline bool look_far(int64_t chains, int64_t ntiles, int64_t workgroups) {
-    const int64_t under_way = workgroups / chains;
-    return (under_way < ntiles ? under_way : ntiles) >= 32;
-}
+inline bool look_far(int64_t chains, int64_t ntiles, int64_t most) { return chains <= most && ntiles >= 32; }
 constexpr int kMaxPolls = 1 << 22;   // a third of a microsecond each
 
 __device__ __forceinline__ uint32_t not_all_ones(float x) {

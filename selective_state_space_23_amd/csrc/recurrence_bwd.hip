@@ -524,7 +524,7 @@ hipError_t launch_bwd(const RecBwdArgs& a) {
     // 4 rows of 64 channels 125 us for 103.)
     auto kernel = rec_bwd_kernel<T, ALIGNED, PIN, HAS_Z, kLookNear>;
     if constexpr (Shape<T, ALIGNED>::kStaged) {
-        if (look_far(nct * a.batch, ntiles, kResident)) kernel = rec_bwd_kernel<T, ALIGNED, PIN, HAS_Z, kLookFar>;
+        if (look_far(nct * a.batch, ntiles, 8)) kernel = rec_bwd_kernel<T, ALIGNED, PIN, HAS_Z, kLookFar>;
     }
     static_assert(kMaxGrid * Shape<T, ALIGNED>::kThreads < (int64_t(1) << 32) && kMaxGrid >= kResident);
     for (int64_t first = 0; first < grid; first += kMaxGrid) {

@@ -742,3 +742,9 @@ def test_gradients_of_far_gates(ssm, dtype, D):
     for k in ("dx", "dgate_x", "dgate_a"):
         err = np.abs(to_host(got[k]) - ref[k]) / np.abs(ref[k])
         assert err.max() <= rtol, f"{k}: off by {err.max()} of the element, {int((err > rtol).sum())} of {err.size}"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sixteen_long_chains(ssm, dtype):
+    """The most chains that hand values on eight tiles at a time, with more tiles than workgroups."""
+    test_few_long_chains(ssm, 2, 4200, 500, dtype)
