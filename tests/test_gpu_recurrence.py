@@ -748,3 +748,20 @@ def test_gradients_of_far_gates(ssm, dtype, D):
 def test_sixteen_long_chains(ssm, dtype):
     """The most chains that hand values on eight tiles at a time, with more tiles than workgroups."""
     test_few_long_chains(ssm, 2, 4200, 500, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,L,D", [(4, 700, 128), (8, 300, 40), (4, 2600, 512)])
+def test_eight_groups_of_chains(ssm, B, L, D, dtype):
+    """Backward from checkpoints over rows times channel tiles that are a multiple of 8: tickets
+    in eight groups (the last shape: more tiles than workgroups)."""
+    v = draw(B, L, D, dtype, True, 200, True, seed=D)
+    d = dev(v, dtype)
+    kept = forward(ssm, d, save="packed")[2]
+    dp = dict(d, **{k: kept[k] for k in ("x", "gate_a", "gate_x", "z")})
+    seen = dict(v, **{k: R.unpack8(*R.pack8(v[k])) for k in ("x", "gate_a", "gate_x", "z")})
+    for states in (kept["states"], None):
+        ref = oracle_bwd(seen, states=None if states is None else states.cpu().numpy())
+        g = backward(ssm, dp, states=states)
+        for k in ref:
+            close(g[k], ref[k], dtype if g[k].dtype != d["a_param"].dtype else "f32", k)
