@@ -35,8 +35,8 @@ constexpr int kPerCu = (sizeof(T) == 2 && ALIGNED) || !OUT || (!HAS_Z && !SAVE &
 //
 // What bounds it is memory, then the vector unit (41 issue slots an element, 34 of them
 // in the maps): one row of 65536 x 5120 in
-// bfloat16 without z moves 2.78 GB, of which 2.68 are inputs and outputs, in 620 us:
-// 4.5 TB/s where a copy reaches 5.2, the vector unit issues for 58% of it.  8 rows of
+// bfloat16 without z moves 2.78 GB, of which 2.68 are inputs and outputs, in 620 to 630 us:
+// 4.4 TB/s where a copy reaches 5.2, the vector unit issues for 58% of it.  8 rows of
 // 2048 x 1536 with z take 76 us (3.4 TB/s): six tiles a workgroup, whose first and last are not
 // hidden.  Three passes (maps, joining, outputs) read the inputs twice: 1348 us for
 // the first.  A tile's 16 waves a CU, in two workgroups, fill the registers (float32 and unaligned

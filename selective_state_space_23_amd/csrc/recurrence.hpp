@@ -141,9 +141,12 @@ __device__ __forceinline__ Raw<T, V> load_raw(Rsrc rs, uint32_t off) {
     return r;
 }
 
-// Cache policy of whole lines that a call reads or writes once: they leave the L2 first
+// Cache policy of whole lines that a call reads or writes once: they leave the caches first
 // (2 x 32768 x 1536 training step 796 us for 812, 8 x 2048 x 1536 backward 112 for 116,
-// forward 81 for 82; only reads or only writes give half of it).
+// forward 81 for 82; only reads or only writes give half of it).  Between products that write its inputs
+// and read its outputs a call gains where its tensors pass the 256 MB that the card
+// caches (16 x 2048 x 1536 forward with those products 306 us for 310, backward 367 for 381) and loses
+// below (forward 4 x 2048 97 for 92, 8 x 2048 165 for 157; backward 4 x 2048 117 for 110).
 constexpr int kStreamed = 2;   // nt
 
 // `off` is past the buffer where the first channel is past D; `left` of the

@@ -61,10 +61,10 @@ struct RecBwdKernelArgs {
 // channel are kept, x, dout and z are read again from LDS and the gates' terms formed
 // while the workgroup waits for that adjoint.
 //
-// What bounds it is the vector unit (129 issue slots an element from 8-bit inputs and
-// 114 from tensors, 76% and 68% of the time), then memory: 2 rows of 32768 x 1536 from checkpoints
-// with z take 455 us and move 1.47 GB (3.2 TB/s), 8 rows of 2048 x 1536 from tensors
-// 111 us and 460 MB (4.1 TB/s; 5.2 for a copy).  One workgroup of 16 waves fills a CU's
+// What bounds it is the vector unit (136 issue slots an element from 8-bit inputs and
+// 120 from tensors, 79% and 69% of the time; 6 of them keep 1 - r and 1 - i to their own size, which costs
+// 1% and 4%), then memory: 2 rows of 32768 x 1536 from checkpoints with z take 463 us and move 1.47 GB
+// (3.2 TB/s), 8 rows of 2048 x 1536 from tensors 116 us and 460 MB (4.0 TB/s; 5.2 for a copy).  One workgroup of 16 waves fills a CU's
 // registers and, with two places for x, dout and z, its LDS.  A register too many costs
 // more than the work it saves: with the gates' terms kept as well, their spills
 // reloaded behind the loads of the next tile, the first case took 770 us.
