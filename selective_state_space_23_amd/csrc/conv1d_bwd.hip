@@ -397,8 +397,8 @@ hipError_t launch_conv_bwd_x(const ConvBwdArgs& a, const X& x) {
     // The general loop alone leaves room for 8 waves a SIMD, 2048 workgroups; beside the fast
     // loop it has 6 or 7.  A grid that is there at once waits for its slowest tiles, and a
     // row's ends always take the general loop: the fast one gains nothing (8 x 2048 x 1536 in bfloat16 46
-    // us alone and 53 with both; 15 x 2048 74 and 84; float32 as fast or slower from 1536 workgroups
-    // on, from a checkpoint 131 and 124).  What such a call writes fits the caches and stays there.
+    // us alone and 53 with both; 15 x 2048 74 and 84).  Float32 gains by both from 1536 workgroups on (15 x
+    // 2048 from a checkpoint 131 and 124).  What such a call writes fits the caches and stays there.
     // Above, the inner tiles' share decides: 2 x 32768 x 1536 in bfloat16 164 alone and 140 with
     // both, in documents of 30 tokens 165 and 172 (float32 301 and 279, 300 and 316).
     const bool large = static_cast<int64_t>(grid.x) * ntiles * a.batch > (sizeof(T) == 4 ? 1536 : 2048);
