@@ -23,8 +23,9 @@
  * Further entry points: the two in one call (mamba_conv_scan_fwd), one-token
  * decode steps, the backward passes of the conv and of the scan
  * (mamba_causal_conv1d_bwd, mamba_selective_scan_bwd), a gated linear recurrence
- * (forward, backward, one-token step: mamba_gated_recurrence_*) and 8-bit
- * activation checkpoints (mamba_activation_pack, mamba_activation_unpack), each
+ * (forward, backward, one-token step: mamba_gated_recurrence_*), 8-bit
+ * activation checkpoints (mamba_activation_pack, mamba_activation_unpack) and a
+ * gated delta rule (forward, backward, one-token step: mamba_gated_delta_rule_*), each
  * described at its declaration below.
  *
  * Conventions shared by every entry point
@@ -508,6 +509,74 @@ int mamba_gated_recurrence_bwd(const mamba_recurrence_dims_t* dims, const void* 
 int mamba_gated_recurrence_update(const mamba_recurrence_dims_t* dims, float* state, const void* x,
                                   const void* gate_a, const void* gate_x, const float* a_param, const void* z,
                                   const uint8_t* reset, void* out, void* stream);
+
+/* ---- Gated delta rule: a linear recurrence as in the Mamba skill page ("Dual
+ * Computation Modes": recurrent for generation, in parallel over a sequence for
+ * training) whose state is a matrix per head that each token corrects by one
+ * rank: what the state holds under the token's key is replaced, in the share beta,
+ * by the token's value.  Per row and value head h, with the queries and keys of
+ * key head h / (value_heads / key_heads), state S (K, V) and a_t = exp(g_t):
+ *   S' = a_t S_{t-1},   u_t = beta_t (v_t - S'^T k_t),   S_t = S' + k_t u_t^T,
+ *   out_t = scale S_t^T q_t.
+ * Keys of norm at most 1 and beta in [0, 2] keep it from growing.  Documents, token 0
+ * and initial_state as in mamba_selective_scan_fwd.  A decay below exp(-200) counts as
+ * 0 (g = -inf included).  A NaN or an infinity reaches no other document and, in
+ * the forward, no earlier token; where it reaches, results are NaN. */
+#define MAMBA_DELTA_CHUNK 64
+typedef struct {
+    int64_t batch;       /* B                                                       */
+    int64_t seqlen;      /* L                                                       */
+    int32_t key_heads;   /* Hk                                                      */
+    int32_t value_heads; /* Hv, a multiple of Hk                                    */
+    int32_t key_dim;     /* K, 1..128                                               */
+    int32_t value_dim;   /* V, 1..128                                               */
+    int64_t ld_q;        /* elements between two tokens of q, of k, of v and of     */
+    int64_t ld_k;        /* dout: 0 for dense, else at least Hk K (Hv V), as in a   */
+    int64_t ld_v;        /* slice of one projection's output; tokens of two rows    */
+    int64_t ld_dout;     /* follow each other at the same distance.                 */
+    int32_t dtype;       /* mamba_dtype_t of q, k, v, out, dout, dq, dk, dv         */
+    float scale;         /* finite (K^-1/2 is usual)                                */
+} mamba_delta_dims_t;
+
+/* Bytes of device workspace mamba_gated_delta_rule_fwd needs (about 310 per token
+ * and value head, in whole chunks of 64 tokens). */
+int mamba_gated_delta_rule_workspace_bytes(const mamba_delta_dims_t* dims, size_t* bytes);
+
+/* Forward.
+ *   q, k       (B, L, Hk, K), v (B, L, Hv, V): `dtype`, strides in dims.
+ *   g          (B, L, Hv) float32 log decays, or NULL (0: no decay); beta (B, L, Hv)
+ *              float32.
+ *   doc_start  (B, L) uint8 or NULL.
+ *   initial_state (B, Hv, K, V) float32 or NULL.
+ *   out        (B, L, Hv, V), dense, `dtype`.
+ *   final_state (B, Hv, K, V) float32 or NULL: S after token L - 1.
+ *   states     (B, Hv, ceil(L / 64), K, V) float32 or NULL: the states entering tokens
+ *              0, 64, 128, ... (before a document start there takes effect), for
+ *              the backward.
+ *   workspace  at least mamba_gated_delta_rule_workspace_bytes bytes, 256-byte aligned.
+ * Supported: K and V up to 128, Hk K, Hv V and strides up to 2^21, L up to 3,000,000
+ * and at most 8,000,000 chunks of 64 tokens over all rows and value heads, else
+ * MAMBA_ERR_UNSUPPORTED.  Any alignment to the element size; K and strides of whole
+ * 16-byte pieces with 16-byte aligned q and k select the vectorised kernels.
+ * Arithmetic and states are float32 (bf16 outputs: sums of products with operands of 16
+ * bits and more, rounded once).  L of 0 writes final_state = initial_state (or 0).
+ * Outputs must not overlap anything else of the call.  Repeated calls give bitwise
+ * identical results. */
+int mamba_gated_delta_rule_fwd(const mamba_delta_dims_t* dims, const void* q, const void* k, const void* v,
+                               const float* g, const float* beta, const uint8_t* doc_start,
+                               const float* initial_state, void* out, float* final_state, float* states,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token per row.
+ *   dims       with seqlen == 1; strides are between rows, of up to 2^40 elements.
+ *   state      (B, Hv, K, V) float32, updated in place.
+ *   q, k (B, Hk, K), v (B, Hv, V); g (or NULL) and beta (B, Hv) float32; reset (B,)
+ *   uint8 or NULL: nonzero where the token starts a document (the state reads as 0);
+ *   out (B, Hv, V), dense.
+ * A state aligned to 16 bytes with V a multiple of 4 selects the vectorised kernel. */
+int mamba_gated_delta_rule_update(const mamba_delta_dims_t* dims, float* state, const void* q, const void* k,
+                                  const void* v, const float* g, const float* beta, const uint8_t* reset, void* out,
+                                  void* stream);
 
 #ifdef __cplusplus
 }

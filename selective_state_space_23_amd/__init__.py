@@ -28,6 +28,10 @@ missing or the tensors are not on a GPU the calls raise.
     p = activation_pack(x)
     dx, dweight, dbias = causal_conv1d_bwd(p, weight, du, bias, doc_start)
     u = activation_unpack(activation_pack(u), torch.bfloat16)          # e.g. for selective_scan_bwd
+
+    # gated delta rule: a K x V state per head, q and k (B, L, Hk, K), v (B, L, Hv, V), g and beta (B, L, Hv)
+    out, S, kept = gated_delta_rule_fwd(q, k, v, g, beta, doc_start, save="states")
+    out_t = gated_delta_rule_update(S, q_t, k_t, v_t, g_t, beta_t)
 """
 
 from __future__ import annotations
@@ -59,6 +63,9 @@ __all__ = [
     "PackedActivation",
     "activation_pack",
     "activation_unpack",
+    "gated_delta_rule_fwd",
+    "gated_delta_rule_update",
+    "gated_delta_rule_workspace_bytes",
     "MambaError",
     "MambaArgumentError",
     "library_path",
@@ -855,4 +862,127 @@ def gated_recurrence_update(state, x, gate_a, gate_x, a_param, z=None, reset=Non
         _ptr(a_param, "a_param", dev, f32, (Dm,)), pz, _ptr(reset, "reset", dev, torch.uint8, (Bt,)),
         _ptr(out, "out", dev, dt, shape))
     _lib.check(st, "mamba_gated_recurrence_update")
+    return out
+
+
+def _heads(t, name, dev, dtype, shape):
+    """(pointer, elements between two tokens) of a (..., H, D) tensor whose heads lie one
+    behind the other and whose tokens lie at one distance: dense, or a slice of one
+    projection's output.  (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous() and t.device == dev and t.dtype is dtype:
+        return t.data_ptr(), 0
+    H, D = shape[-2:]
+    if (D > 1 and t.stride(-1) != 1) or (H > 1 and D > 0 and t.stride(-2) != D):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    flat = t.as_strided(tuple(shape[:-2]) + (H * D,), t.stride()[:-2] + (1,))
+    return _strided(flat, name, dev, dtype, flat.shape)
+
+
+def _delta_dims(q, k, v, lead, scale, code, lds=(0, 0, 0, 0)):
+    """mamba_delta_dims_t of q, k (*lead, Hk, K) and v (*lead, Hv, V)."""
+    Hk, K = q.shape[-2:]
+    Hv, V = v.shape[-2:]
+    batch, seqlen = lead if len(lead) == 2 else (lead[0], 1)
+    return _lib.DeltaDims(batch, seqlen, Hk, Hv, K, V, *lds, code, K ** -0.5 if scale is None else scale)
+
+
+def gated_delta_rule_workspace_bytes(batch, seqlen, key_heads, value_heads, key_dim, value_dim, dtype="bf16") -> int:
+    code = _lib.MAMBA_DTYPE_BF16 if dtype == "bf16" else _lib.MAMBA_DTYPE_F32
+    dims = _lib.DeltaDims(batch, seqlen, key_heads, value_heads, key_dim, value_dim, 0, 0, 0, 0, code, 1.0)
+    n = ctypes.c_size_t(0)
+    _lib.check(_lib.load().mamba_gated_delta_rule_workspace_bytes(ctypes.byref(dims), ctypes.byref(n)),
+               "mamba_gated_delta_rule_workspace_bytes")
+    return int(n.value)
+
+
+def gated_delta_rule_fwd(q, k, v, g, beta, doc_start=None, scale=None, initial_state=None, final_state=True, out=None,
+                         save=None, workspace=None):
+    """Gated delta rule; see mamba_gated_delta_rule_fwd.
+
+    q, k (B, L, Hk, K) and v (B, L, Hv, V) float32/bfloat16, dense or slices of one
+    projection's output; g (or None: no decay) and beta (B, L, Hv) float32; doc_start
+    (B, L) uint8/bool; ``scale``: K ** -0.5 if not given; initial_state (B, Hv, K, V)
+    float32.  ``final_state``: True to allocate and return it, False/None to skip, or a
+    tensor to fill.  ``save``: None; "states" to keep the states the backward
+    starts its chunks from; or a dict of one such tensor to fill ("states" (B, Hv,
+    ceil(L / 64), K, V) float32).  Returns (out (B, L, Hv, V), final_state or None),
+    with ``save`` also the dict of what was kept."""
+    torch = _torch()
+    dev = _check_device(q)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be (B, L, Hk, K) and v (B, L, Hv, V)")
+    code, dt, f32 = _dtype_code(q), q.dtype, torch.float32
+    Bt, L, Hk, K = q.shape
+    Hv, V = v.shape[-2:]
+    state = (Bt, Hv, K, V)
+    if doc_start is not None and doc_start.dtype == torch.bool:
+        doc_start = doc_start.to(torch.uint8)
+    if out is None:
+        out = torch.empty((Bt, L, Hv, V), dtype=dt, device=dev)
+    if final_state is True:
+        final_state = torch.empty(state, dtype=f32, device=dev)
+    elif final_state is False:
+        final_state = None
+    pq, lq = _heads(q, "q", dev, dt, q.shape)
+    pk, lk = _heads(k, "k", dev, dt, q.shape)
+    pv, lv = _heads(v, "v", dev, dt, (Bt, L, Hv, V))
+    kept, states, saved = None, None, (Bt, Hv, -(-L // _lib.DELTA_CHUNK), K, V)
+    if save is not None:
+        if isinstance(save, dict):
+            if set(save) - {"states"}:
+                raise ValueError(f"save: unknown entries {sorted(set(save) - {'states'})}")
+            kept = save
+        elif save == "states":
+            kept = {"states": torch.empty(saved, dtype=f32, device=dev)}
+        else:
+            raise ValueError('save must be None, "states" or a dict')
+        states = kept.get("states")
+    dims = _delta_dims(q, k, v, (Bt, L), scale, code, (lq, lk, lv, 0))
+    lib = _lib.load()
+    if workspace is None:
+        workspace = _recurrence_workspace(lib.mamba_gated_delta_rule_workspace_bytes,
+                                          "mamba_gated_delta_rule_workspace_bytes", dev, ctypes.byref(dims))
+    st = _launch(
+        dev, lib.mamba_gated_delta_rule_fwd, ctypes.byref(dims), pq, pk, pv,
+        _ptr(g, "g", dev, f32, (Bt, L, Hv)), _ptr(beta, "beta", dev, f32, (Bt, L, Hv)),
+        _ptr(doc_start, "doc_start", dev, torch.uint8, (Bt, L)),
+        _ptr(initial_state, "initial_state", dev, f32, state), _ptr(out, "out", dev, dt, (Bt, L, Hv, V)),
+        _ptr(final_state, "final_state", dev, f32, state), _ptr(states, "states", dev, f32, saved),
+        _ptr(workspace, "workspace", dev, torch.uint8), 0 if workspace is None else workspace.numel())
+    _lib.check(st, "mamba_gated_delta_rule_fwd")
+    return (out, final_state) if save is None else (out, final_state, kept)
+
+
+def gated_delta_rule_update(state, q, k, v, g, beta, reset=None, scale=None, out=None):
+    """One step of the gated delta rule per row; see mamba_gated_delta_rule_update.
+    state (B, Hv, K, V) float32, updated in place; q, k (B, Hk, K), v (B, Hv, V), dense
+    or slices; g (or None) and beta (B, Hv) float32; reset (B,) uint8/bool.  Returns out
+    (B, Hv, V)."""
+    torch = _torch()
+    dev = _check_device(q)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q must be (B, Hk, K) and v (B, Hv, V)")
+    code, dt, f32 = _dtype_code(q), q.dtype, torch.float32
+    Bt, Hk, K = q.shape
+    Hv, V = v.shape[-2:]
+    if reset is not None and reset.dtype == torch.bool:
+        reset = reset.to(torch.uint8)
+    if out is None:
+        out = torch.empty((Bt, Hv, V), dtype=dt, device=dev)
+    pq, lq = _heads(q, "q", dev, dt, q.shape)
+    pk, lk = _heads(k, "k", dev, dt, q.shape)
+    pv, lv = _heads(v, "v", dev, dt, (Bt, Hv, V))
+    dims = _delta_dims(q, k, v, (Bt,), scale, code, (lq, lk, lv, 0))
+    st = _launch(
+        dev, _lib.load().mamba_gated_delta_rule_update, ctypes.byref(dims),
+        _ptr(state, "state", dev, f32, (Bt, Hv, K, V)), pq, pk, pv, _ptr(g, "g", dev, f32, (Bt, Hv)),
+        _ptr(beta, "beta", dev, f32, (Bt, Hv)), _ptr(reset, "reset", dev, torch.uint8, (Bt,)),
+        _ptr(out, "out", dev, dt, (Bt, Hv, V)))
+    _lib.check(st, "mamba_gated_delta_rule_update")
     return out

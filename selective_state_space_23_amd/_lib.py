@@ -41,10 +41,14 @@ EXPORTED = (
     "mamba_gated_recurrence_bwd_workspace_bytes",
     "mamba_gated_recurrence_bwd",
     "mamba_gated_recurrence_update",
+    "mamba_gated_delta_rule_workspace_bytes",
+    "mamba_gated_delta_rule_fwd",
+    "mamba_gated_delta_rule_update",
 )
 
 PACK_BLOCK = 64          # MAMBA_PACK_BLOCK: channels that share one scale
 RECURRENCE_CHUNK = 128   # MAMBA_RECURRENCE_CHUNK: tokens between two saved states
+DELTA_CHUNK = 64         # MAMBA_DELTA_CHUNK: the same of the delta rule
 
 
 class ScanDims(ctypes.Structure):
@@ -76,6 +80,25 @@ class RecurrenceDims(ctypes.Structure):
         ("ld_dout", ctypes.c_int64),
         ("dtype", ctypes.c_int32),
         ("c", ctypes.c_float),
+    ]
+
+
+class DeltaDims(ctypes.Structure):
+    """mamba_delta_dims_t"""
+
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("key_heads", ctypes.c_int32),
+        ("value_heads", ctypes.c_int32),
+        ("key_dim", ctypes.c_int32),
+        ("value_dim", ctypes.c_int32),
+        ("ld_q", ctypes.c_int64),
+        ("ld_k", ctypes.c_int64),
+        ("ld_v", ctypes.c_int64),
+        ("ld_dout", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
     ]
 
 
@@ -158,6 +181,13 @@ def load() -> ctypes.CDLL:
     lib.mamba_gated_recurrence_bwd.restype = ctypes.c_int
     lib.mamba_gated_recurrence_update.argtypes = [rd] + [vp] * 9
     lib.mamba_gated_recurrence_update.restype = ctypes.c_int
+    dd = ctypes.POINTER(DeltaDims)
+    lib.mamba_gated_delta_rule_workspace_bytes.argtypes = [dd, ctypes.POINTER(sz)]
+    lib.mamba_gated_delta_rule_workspace_bytes.restype = ctypes.c_int
+    lib.mamba_gated_delta_rule_fwd.argtypes = [dd] + [vp] * 11 + [sz, vp]
+    lib.mamba_gated_delta_rule_fwd.restype = ctypes.c_int
+    lib.mamba_gated_delta_rule_update.argtypes = [dd] + [vp] * 9
+    lib.mamba_gated_delta_rule_update.restype = ctypes.c_int
     _lib = lib
     return lib
 

@@ -28,5 +28,30 @@ inline bool mul_ok(int64_t a, int64_t b, int64_t c, int64_t* out) {
     return true;
 }
 
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+
+// No output overlaps an input, another output or the workspace, nor the
+// workspace an input.
+template <size_t NI, size_t NO>
+bool disjoint(const Span (&ins)[NI], const Span (&outs)[NO]) {
+    for (size_t o = 0; o < NO; ++o) {
+        for (const Span& i : ins)
+            if (overlap(outs[o].p, outs[o].bytes, i.p, i.bytes)) return false;
+        for (size_t k = o + 1; k < NO; ++k)
+            if (overlap(outs[o].p, outs[o].bytes, outs[k].p, outs[k].bytes)) return false;
+    }
+    return true;
+}
+
+// Bytes from the first to behind the last element of `rows` strided rows.
+inline size_t span(int64_t rows, int64_t dim, int64_t ld, size_t esz) {
+    return static_cast<size_t>((rows - 1) * ld + dim) * esz;
+}
+
 }  // namespace api
 }  // namespace mamba

@@ -1,0 +1,183 @@
+// C ABI of the gated delta rule: argument validation and dispatch.  Every check
+// runs on the host before any launch.
+#include "mamba_hip.h"
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "api_checks.hpp"
+#include "delta_launch.hpp"
+#include "fill.hpp"
+
+static_assert(MAMBA_DELTA_CHUNK == mamba::kDeltaChunk, "the header and the kernels agree");
+
+namespace {
+
+using namespace mamba::api;
+
+constexpr int64_t kMaxWidth = int64_t(1) << 21;   // channels and strides of a token: a chunk's offsets fit 32 bits
+constexpr int64_t kMaxChunks = 8000000;           // chunks of all rows and heads
+
+int hip_status(hipError_t e) { return e == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP; }
+
+int64_t chunks_of(const mamba_delta_dims_t* d) { return ceil_div(d->seqlen, MAMBA_DELTA_CHUNK); }
+
+// `max_ld`: of the one-token step's rows, which are addressed in 64 bits.
+int check_dims(const mamba_delta_dims_t* d, int64_t max_ld = kMaxWidth) {
+    if (!d) return MAMBA_ERR_INVALID_ARGUMENT;
+    if (d->batch < 0 || d->seqlen < 0 || d->batch > 65535) return MAMBA_ERR_INVALID_ARGUMENT;
+    if (d->key_heads <= 0 || d->value_heads <= 0 || d->key_dim <= 0 || d->value_dim <= 0 ||
+        d->value_heads % d->key_heads != 0)
+        return MAMBA_ERR_INVALID_ARGUMENT;
+    if (d->dtype != MAMBA_DTYPE_F32 && d->dtype != MAMBA_DTYPE_BF16) return MAMBA_ERR_INVALID_ARGUMENT;
+    if (!std::isfinite(d->scale)) return MAMBA_ERR_INVALID_ARGUMENT;
+    const int64_t kw = int64_t(d->key_heads) * d->key_dim, vw = int64_t(d->value_heads) * d->value_dim;
+    const int64_t lds[][2] = {{d->ld_q, kw}, {d->ld_k, kw}, {d->ld_v, vw}, {d->ld_dout, vw}};
+    for (const auto& ld : lds)
+        if (ld[0] < 0 || (ld[0] != 0 && ld[0] < ld[1])) return MAMBA_ERR_INVALID_ARGUMENT;
+    for (const auto& ld : lds)
+        if (ld[0] > max_ld) return MAMBA_ERR_UNSUPPORTED;
+    if (d->ld_dout > kMaxWidth) return MAMBA_ERR_UNSUPPORTED;
+    if (d->key_dim > mamba::kDeltaMaxHead || d->value_dim > mamba::kDeltaMaxHead) return MAMBA_ERR_UNSUPPORTED;
+    if (kw > kMaxWidth || vw > kMaxWidth || d->seqlen > kMaxSeqlen) return MAMBA_ERR_UNSUPPORTED;
+    if (d->batch * d->value_heads * (chunks_of(d) > 0 ? chunks_of(d) : 1) > kMaxChunks) return MAMBA_ERR_UNSUPPORTED;
+    return MAMBA_OK;
+}
+
+struct Sizes {
+    size_t esz, k, v, gate, state;   // bytes of q or k and of v if dense, of a (B, L, Hv) array, of a state
+    int64_t tokens, ld_q, ld_k, ld_v, ld_o;
+    int64_t kw, vw;
+};
+
+Sizes sizes(const mamba_delta_dims_t* d) {
+    Sizes s{};
+    s.esz = d->dtype == MAMBA_DTYPE_BF16 ? 2 : 4;
+    s.tokens = d->batch * d->seqlen;
+    s.kw = int64_t(d->key_heads) * d->key_dim;
+    s.vw = int64_t(d->value_heads) * d->value_dim;
+    s.k = static_cast<size_t>(s.tokens * s.kw) * s.esz;
+    s.v = static_cast<size_t>(s.tokens * s.vw) * s.esz;
+    s.gate = static_cast<size_t>(s.tokens * d->value_heads) * 4;
+    s.state = static_cast<size_t>(d->batch * s.vw) * d->key_dim * 4;
+    s.ld_q = d->ld_q ? d->ld_q : s.kw;
+    s.ld_k = d->ld_k ? d->ld_k : s.kw;
+    s.ld_v = d->ld_v ? d->ld_v : s.vw;
+    s.ld_o = d->ld_dout ? d->ld_dout : s.vw;
+    return s;
+}
+
+// q and k may be read in 16-byte pieces of eight channels.
+bool pieces(const void* p, int64_t ld, size_t esz, int dim) {
+    return dim % 8 == 0 && aligned(p, 16) && ld * esz % 16 == 0;
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t record_bytes(const mamba_delta_dims_t* d) {
+    return round256(static_cast<size_t>(d->batch * d->value_heads * chunks_of(d)) * mamba::delta_chunk_bytes());
+}
+size_t solve_bytes(const mamba_delta_dims_t* d) {
+    return round256(static_cast<size_t>(d->batch * d->value_heads * chunks_of(d)) * mamba::delta_solve_bytes());
+}
+
+size_t fwd_workspace(const mamba_delta_dims_t* d) {
+    return d->batch * d->seqlen == 0 ? 0 : record_bytes(d) + solve_bytes(d);
+}
+
+mamba::DeltaArgs base_args(const mamba_delta_dims_t* d, const Sizes& s, const void* q, const void* k, const void* v,
+                           const float* g, const float* beta, const uint8_t* doc_start, const float* initial_state,
+                           void* workspace, void* stream) {
+    mamba::DeltaArgs a{};
+    a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.doc_start = doc_start; a.initial_state = initial_state;
+    a.chunks = static_cast<char*>(workspace);
+    a.solve = a.chunks + record_bytes(d);
+    a.batch = d->batch; a.seqlen = d->seqlen;
+    a.ld_q = s.ld_q; a.ld_k = s.ld_k; a.ld_v = s.ld_v; a.ld_o = s.ld_o;
+    a.kheads = d->key_heads; a.vheads = d->value_heads; a.kdim = d->key_dim; a.vdim = d->value_dim;
+    a.nchunks = static_cast<int>(chunks_of(d));
+    a.scale = d->scale;
+    a.bf16 = d->dtype == MAMBA_DTYPE_BF16;
+    a.vec_k = pieces(q, s.ld_q, s.esz, d->key_dim) && pieces(k, s.ld_k, s.esz, d->key_dim);
+    a.stream = static_cast<hipStream_t>(stream);
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mamba_gated_delta_rule_workspace_bytes(const mamba_delta_dims_t* dims, size_t* bytes) {
+    if (!bytes) return MAMBA_ERR_INVALID_ARGUMENT;
+    *bytes = 0;
+    const int st = check_dims(dims);
+    if (st != MAMBA_OK) return st;
+    *bytes = fwd_workspace(dims);
+    return MAMBA_OK;
+}
+
+int mamba_gated_delta_rule_fwd(const mamba_delta_dims_t* dims, const void* q, const void* k, const void* v,
+                               const float* g, const float* beta, const uint8_t* doc_start,
+                               const float* initial_state, void* out, float* final_state, float* states,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+    const int st = check_dims(dims);
+    if (st != MAMBA_OK) return st;
+    const float* f32s[] = {g, beta, initial_state, final_state, states};
+    for (const float* p : f32s)
+        if (p && !aligned(p, 4)) return MAMBA_ERR_MISALIGNED;
+    const Sizes s = sizes(dims);
+    if (dims->batch == 0) return MAMBA_OK;
+    if (dims->seqlen == 0) {
+        if (overlap(final_state, s.state, initial_state, s.state)) return MAMBA_ERR_INVALID_ARGUMENT;
+        return hip_status(mamba::launch_fill(final_state, initial_state, static_cast<int64_t>(s.state / 4),
+                                             static_cast<hipStream_t>(stream)));
+    }
+    if (!q || !k || !v || !beta || !out) return MAMBA_ERR_INVALID_ARGUMENT;
+    if (!aligned(q, s.esz) || !aligned(k, s.esz) || !aligned(v, s.esz) || !aligned(out, s.esz))
+        return MAMBA_ERR_MISALIGNED;
+    const size_t need = fwd_workspace(dims);
+    if (!workspace || workspace_bytes < need) return MAMBA_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return MAMBA_ERR_MISALIGNED;
+    const Span ins[] = {{q, span(s.tokens, s.kw, s.ld_q, s.esz)}, {k, span(s.tokens, s.kw, s.ld_k, s.esz)},
+                        {v, span(s.tokens, s.vw, s.ld_v, s.esz)}, {g, s.gate}, {beta, s.gate},
+                        {doc_start, static_cast<size_t>(s.tokens)}, {initial_state, s.state}};
+    const Span outs[] = {{out, s.v}, {final_state, s.state}, {states, s.state * chunks_of(dims)}, {workspace, need}};
+    if (!disjoint(ins, outs)) return MAMBA_ERR_INVALID_ARGUMENT;
+    mamba::DeltaArgs a = base_args(dims, s, q, k, v, g, beta, doc_start, initial_state, workspace, stream);
+    a.out = out; a.final_state = final_state; a.states = states;
+    const hipError_t e = mamba::launch_delta_prepare(a);
+    return hip_status(e != hipSuccess ? e : mamba::launch_delta_fwd(a));
+}
+
+int mamba_gated_delta_rule_update(const mamba_delta_dims_t* dims, float* state, const void* q, const void* k,
+                                  const void* v, const float* g, const float* beta, const uint8_t* reset, void* out,
+                                  void* stream) {
+    const int st = check_dims(dims, kMaxElems);
+    if (st != MAMBA_OK) return st;
+    if (dims->seqlen != 1) return MAMBA_ERR_INVALID_ARGUMENT;
+    if (dims->batch == 0) return MAMBA_OK;
+    if (!state || !q || !k || !v || !beta || !out) return MAMBA_ERR_INVALID_ARGUMENT;
+    const Sizes s = sizes(dims);
+    if (!aligned(state, 4) || (g && !aligned(g, 4)) || !aligned(beta, 4) || !aligned(q, s.esz) ||
+        !aligned(k, s.esz) || !aligned(v, s.esz) || !aligned(out, s.esz))
+        return MAMBA_ERR_MISALIGNED;
+    const Span ins[] = {{q, span(s.tokens, s.kw, s.ld_q, s.esz)}, {k, span(s.tokens, s.kw, s.ld_k, s.esz)},
+                        {v, span(s.tokens, s.vw, s.ld_v, s.esz)}, {g, s.gate}, {beta, s.gate},
+                        {reset, static_cast<size_t>(dims->batch)}};
+    const Span outs[] = {{state, s.state}, {out, s.v}};
+    if (!disjoint(ins, outs)) return MAMBA_ERR_INVALID_ARGUMENT;
+    mamba::DeltaUpdateArgs a{};
+    a.state = state; a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.reset = reset; a.out = out;
+    a.batch = dims->batch;
+    a.ld_q = s.ld_q; a.ld_k = s.ld_k; a.ld_v = s.ld_v;
+    a.kheads = dims->key_heads; a.vheads = dims->value_heads; a.kdim = dims->key_dim; a.vdim = dims->value_dim;
+    a.scale = dims->scale;
+    a.bf16 = dims->dtype == MAMBA_DTYPE_BF16;
+    a.vec = dims->value_dim % 4 == 0 && aligned(state, 16);
+    a.stream = static_cast<hipStream_t>(stream);
+    return hip_status(mamba::launch_delta_update(a));
+}
+
+}  // extern "C"

@@ -1,0 +1,215 @@
+// Device helpers of the gated delta rule (delta_prepare.hip, delta_fwd.hip,
+// delta_bwd.hip, delta_grads.hip).
+//
+// Precision.  Every product of the chunked form runs on
+// v_mfma_f32_16x16x32_bf16 with float32 accumulators.  A float32 operand is cut
+// into three bf16 pieces of 8 bits each, x = hi + mid + lo exactly (cut by masking, so the
+// remainders are exact); the pieces of two operands are multiplied as far as
+// they reach 2^-24 of the product: 3 products where one operand is bf16 as stored, 6
+// where both are float32.  That is float32 arithmetic at 1/3 to 1/6 of the bf16 rate (the fp32
+// instructions have 1/16), and states, solved triangles and float32 gradients need it:
+// they carry over thousands of tokens.  Products that only feed a bf16 output
+// take two pieces (2^-16).
+//
+// Layout.  With lane l = 16 g + m of a wave, an accumulator tile holds row 4 g + r
+// (r = 0..3), column m; an operand of 32 contracted values holds row (column) m and eight of them in
+// lane group g.  Which eight is free as long as both operands agree.  So an accumulated
+// result is an operand of the next product as it stands: two tiles give
+// group g the rows 4 g + 0..3 of each, and no lane needs another's values.
+#pragma once
+
+#include "device_common.hpp"
+#include "delta_launch.hpp"
+
+namespace mamba {
+namespace delta {
+
+constexpr int C = kDeltaChunk;
+constexpr int kTiles = C / 16;            // token tiles of a chunk
+constexpr int kBlocks = 6;                // 16 x 32 pieces of a 64 x 64 triangle that are not all zero
+constexpr uint32_t kPast = 0x7fffff00u;   // a byte offset behind any buffer
+constexpr int64_t kSolveBytes = kBlocks * 3 * 1024;   // a chunk's solved triangle in three pieces
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+using Rsrc = __amdgpu_buffer_rsrc_t;
+
+// An eighth of a row of 32 contracted values in N pieces.
+template <int N> struct Frag {
+    u32x4 p[N];
+};
+
+// Per-chunk record of the first pass: what the tokens' decays come to.
+struct ChunkRec {
+    float hi[C], lo[C];   // sum of log2 decays from the chunk's start (document starts count 0), as hi + lo
+    float into[C];        // exp2 of it where no document start lies before: what the entering state has kept
+    float outof[C];       // from the token to the chunk's end, 0 where a later document starts
+    float beta[C];
+    float keep;           // the entering state's part of the leaving one (0 with a start inside)
+    uint32_t pad;
+    uint64_t starts;      // bit t: token t starts a document
+    uint64_t bad;         // bit t: a key, gate or decay of token t or before it in its document is not finite
+};
+
+__device__ __forceinline__ Rsrc rsrc(const void* p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), 0x00027000);
+}
+
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+
+// acc += a b with the products of pieces i, j with i + j < ORDER, the smallest first.
+template <int ORDER, int NA, int NB>
+__device__ __forceinline__ void product(f32x4& acc, const Frag<NA>& a, const Frag<NB>& b) {
+#pragma unroll
+    for (int s = ORDER - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB) acc = mfma(a.p[i], b.p[s - i], acc);
+}
+
+// The bf16 pieces of pairs of floats.
+__device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    const uint32_t u0 = __float_as_uint(x0), u1 = __float_as_uint(x1);
+    hi = __builtin_amdgcn_perm(u1, u0, 0x07060302u);
+    const float r0 = x0 - __uint_as_float(u0 & 0xffff0000u), r1 = x1 - __uint_as_float(u1 & 0xffff0000u);
+    const uint32_t v0 = __float_as_uint(r0), v1 = __float_as_uint(r1);
+    mid = __builtin_amdgcn_perm(v1, v0, 0x07060302u);
+    const float s0 = r0 - __uint_as_float(v0 & 0xffff0000u), s1 = r1 - __uint_as_float(v1 & 0xffff0000u);
+    lo = __builtin_amdgcn_perm(__float_as_uint(s1), __float_as_uint(s0), 0x07060302u);
+}
+
+// Eight floats in three pieces: slots 0..3 from a, 4..7 from b.
+__device__ __forceinline__ Frag<3> split(f32x4 a, f32x4 b) {
+    Frag<3> f;
+    uint32_t h, m, l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const f32x4 x = i < 2 ? a : b;
+        split_pair(x[2 * (i & 1)], x[2 * (i & 1) + 1], h, m, l);
+        f.p[0][i] = h;
+        f.p[1][i] = m;
+        f.p[2][i] = l;
+    }
+    return f;
+}
+
+// Eight floats in two rounded pieces: what is left out is below 2^-17 of a value, of either
+// sign, and the product of two second pieces (left out too) below 2^-16.  (The first two cut
+// pieces leave out remainders of one sign: sums of 64 terms that cancel were off by 2e-4.)
+__device__ __forceinline__ Frag<2> split_rounded(f32x4 a, f32x4 b) {
+    Frag<2> f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const f32x4 x = i < 2 ? a : b;
+        const float x0 = x[2 * (i & 1)], x1 = x[2 * (i & 1) + 1];
+        const uint32_t h = pack_bf16x2(x0, x1);
+        f.p[0][i] = h;
+        f.p[1][i] = pack_bf16x2(x0 - __uint_as_float(h << 16), x1 - __uint_as_float(h & 0xffff0000u));
+    }
+    return f;
+}
+
+// Eight floats of an operand that only reaches an output: two pieces, or all three.
+template <int N>
+__device__ __forceinline__ Frag<N> split_out(f32x4 a, f32x4 b) {
+    if constexpr (N == 2) return split_rounded(a, b);
+    else return split(a, b);
+}
+
+// The rows of one chunk of one tensor as a buffer: reads behind the last token
+// give zero, writes there are dropped.
+template <int ESZ>
+__device__ __forceinline__ Rsrc rows_rsrc(const void* p, int64_t first, int rows, int64_t ld, int width) {
+    return rsrc(static_cast<const char*>(p) + first * ESZ, rows > 0 ? ((rows - 1) * ld + width) * ESZ : 0);
+}
+
+// Eight consecutive channels c .. c + 7 of a row, as stored, zeros past `width`.  VEC: in 16-byte pieces
+// (width and strides multiples of 8, pointers aligned), else one by one.
+template <typename T, bool VEC> struct Eight;
+template <bool VEC> struct Eight<bf16_t, VEC> {
+    u32x4 w;
+    __device__ __forceinline__ void load(Rsrc rs, uint32_t row_off, int c, int width) {
+        if constexpr (VEC) {
+            w = __builtin_amdgcn_raw_buffer_load_b128(rs, c < width ? row_off + 2 * c : kPast, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t o = row_off + 2 * (c + 2 * i);
+                const uint32_t x = static_cast<uint16_t>(
+                    __builtin_amdgcn_raw_buffer_load_b16(rs, c + 2 * i < width ? o : kPast, 0, 0));
+                const uint32_t y = static_cast<uint16_t>(
+                    __builtin_amdgcn_raw_buffer_load_b16(rs, c + 2 * i + 1 < width ? o + 2 : kPast, 0, 0));
+                w[i] = x | (y << 16);
+            }
+        }
+    }
+    __device__ __forceinline__ Frag<1> frag() const { return Frag<1>{{w}}; }
+};
+template <bool VEC> struct Eight<float, VEC> {
+    u32x4 a, b;
+    __device__ __forceinline__ void load(Rsrc rs, uint32_t row_off, int c, int width) {
+        if constexpr (VEC) {
+            const uint32_t o = c < width ? row_off + 4 * c : kPast;
+            a = __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0);
+            b = __builtin_amdgcn_raw_buffer_load_b128(rs, o + (c < width ? 16 : 0), 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, c + i < width ? row_off + 4 * (c + i) : kPast, 0, 0);
+                b[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, c + 4 + i < width ? row_off + 4 * (c + 4 + i) : kPast,
+                                                            0, 0);
+            }
+        }
+    }
+    __device__ __forceinline__ Frag<3> frag() const {
+        return split(__builtin_bit_cast(f32x4, a), __builtin_bit_cast(f32x4, b));
+    }
+};
+
+// Pieces of an operand as stored.
+template <typename T> constexpr int kPieces = sizeof(T) == 2 ? 1 : 3;
+
+// One element of T at a byte offset of a buffer.
+template <typename T>
+__device__ __forceinline__ uint32_t load_one(Rsrc rs, uint32_t off) {
+    if constexpr (sizeof(T) == 2)
+        return static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(rs, off, 0, 0));
+    else
+        return __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0);
+}
+template <typename T>
+__device__ __forceinline__ float one_value(uint32_t raw) {
+    return sizeof(T) == 2 ? __uint_as_float(raw << 16) : __uint_as_float(raw);
+}
+template <typename T>
+__device__ __forceinline__ void store_one(Rsrc rs, uint32_t off, float v) {
+    if constexpr (sizeof(T) == 2)
+        __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v), rs, off, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rs, off, 0, 0);
+}
+
+// Bits from each set bit of `m` up to the end of its document (next bit of `starts`).
+__device__ __forceinline__ uint64_t smear(uint64_t m, uint64_t starts) {
+    uint64_t walls = starts;
+#pragma unroll
+    for (int s = 1; s < 64; s *= 2) {
+        m |= (m << s) & ~walls;
+        walls |= walls << s;
+    }
+    return m;
+}
+
+__device__ __forceinline__ bool not_finite(float x) { return __builtin_isfpclass(x, 0x207); }   // nan, +-inf
+
+// Four consecutive token values of a record.
+__device__ __forceinline__ f32x4 four(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+
+}  // namespace delta
+}  // namespace mamba

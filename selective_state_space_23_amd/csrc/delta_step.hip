@@ -1,0 +1,184 @@
+// Gated delta rule token by token: the one-token step, and rows too short for the chunked form.
+//
+// A workgroup keeps the K x (4 COLS) part of one head's state in registers, four
+// consecutive columns and K COLS / 256 consecutive rows a thread:
+//     S' = a S;  u = beta (v - S'^T k);  S = S' + k u^T;  out = scale S^T q,
+// the sums over rows by lane exchanges, then over the four waves through LDS. Bound by memory
+// (the state read and written once); the columns of one head are
+// split over workgroups where there are few heads, whose time is a trip to memory.
+#include "delta_rule.hpp"
+
+namespace mamba {
+
+namespace {
+
+using namespace delta;
+
+struct StepArgs {
+    const float* state_in;    // may be state_out, or null: zeros
+    float* state_out;         // or null
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* g;
+    const float* beta;
+    const uint8_t* starts;    // (B, L) or null
+    void* out;
+    int64_t seqlen, ld_q, ld_k, ld_v;
+    int kheads, vheads, kdim, vdim, cols;
+    float scale;
+};
+
+// The sum over the workgroup's row groups of four columns, in every thread.
+template <int COLS>
+__device__ __forceinline__ f32x4 over_rows(f32x4 x, f32x4 (*red)[COLS], int wave, int lane) {
+#pragma unroll
+    for (int s = COLS; s < 64; s *= 2)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] += __shfl_xor(x[e], s);
+    if (lane < COLS) red[wave][lane] = x;
+    __syncthreads();
+    const int c = lane % COLS;
+    return (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
+}
+
+template <typename T, int KT, int COLS, bool VEC>
+__global__ __launch_bounds__(256) void step_kernel(StepArgs a) {
+    constexpr int R = KT * COLS / 256;   // rows a thread
+    __shared__ __align__(16) float kv[KT], qv[KT];
+    __shared__ __align__(16) f32x4 red[2][4][COLS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t bh = blockIdx.x / a.cols;
+    const int hv = static_cast<int>(bh % a.vheads), hk = hv / (a.vheads / a.kheads);
+    const int64_t b = bh / a.vheads;
+    const int v0 = (static_cast<int>(blockIdx.x % a.cols) * COLS + lane % COLS) * 4;
+    const int row0 = (wave * (64 / COLS) + lane / COLS) * R;
+    const int64_t cells = static_cast<int64_t>(a.kdim) * a.vdim;
+
+    f32x4 S[R];
+    {
+        const Rsrc rs = rsrc(a.state_in + (a.state_in ? bh * cells : 0), a.state_in ? cells * 4 : 0);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const bool row_in = row0 + i < a.kdim;
+            if constexpr (VEC) {
+                S[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                    rs, row_in && v0 < a.vdim ? ((row0 + i) * a.vdim + v0) * 4 : kPast, 0, 0));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    S[i][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                        rs, row_in && v0 + e < a.vdim ? ((row0 + i) * a.vdim + v0 + e) * 4 : kPast, 0, 0));
+            }
+        }
+    }
+    for (int64_t t = 0; t < a.seqlen; ++t) {
+        const int64_t tok = b * a.seqlen + t;
+        const bool start = a.starts != nullptr && a.starts[tok] != 0;
+        float gate = a.g != nullptr ? a.g[tok * a.vheads + hv] : 0.0f;
+        if (gate < -200.0f) gate = -200.0f;
+        const float decay = exp2_fast(gate * kLog2e), beta = a.beta[tok * a.vheads + hv];
+        f32x4 vals;
+        {
+            const Rsrc vr = rsrc(static_cast<const T*>(a.v) + tok * a.ld_v + static_cast<int64_t>(hv) * a.vdim,
+                                 a.vdim * static_cast<int>(sizeof(T)));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                vals[e] = one_value<T>(load_one<T>(vr, static_cast<uint32_t>((v0 + e) * sizeof(T))));
+        }
+        if (tid < KT) {
+            const Rsrc kr = rsrc(static_cast<const T*>(a.k) + tok * a.ld_k + static_cast<int64_t>(hk) * a.kdim,
+                                 a.kdim * static_cast<int>(sizeof(T)));
+            kv[tid] = one_value<T>(load_one<T>(kr, static_cast<uint32_t>(tid * sizeof(T))));
+        } else if (tid >= 128 && tid < 128 + KT) {
+            const Rsrc qr = rsrc(static_cast<const T*>(a.q) + tok * a.ld_q + static_cast<int64_t>(hk) * a.kdim,
+                                 a.kdim * static_cast<int>(sizeof(T)));
+            qv[tid - 128] = one_value<T>(load_one<T>(qr, static_cast<uint32_t>((tid - 128) * sizeof(T))));
+        }
+        __syncthreads();
+        float kr[R], qr[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            kr[i] = kv[row0 + i];
+            qr[i] = qv[row0 + i];
+        }
+        f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                S[i][e] = start ? 0.0f : S[i][e] * decay;
+                sum[e] = __builtin_fmaf(S[i][e], kr[i], sum[e]);
+            }
+        sum = over_rows<COLS>(sum, red[0], wave, lane);
+        f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float u = beta * (vals[e] - sum[e]);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                S[i][e] = __builtin_fmaf(kr[i], u, S[i][e]);
+                o[e] = __builtin_fmaf(S[i][e], qr[i], o[e]);
+            }
+        }
+        o = over_rows<COLS>(o, red[1], wave, lane);
+        const Rsrc orr = rsrc(static_cast<T*>(a.out) + (tok * a.vheads + hv) * a.vdim, a.vdim * static_cast<int>(sizeof(T)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            store_one<T>(orr, tid < COLS ? static_cast<uint32_t>((v0 + e) * sizeof(T)) : kPast, a.scale * o[e]);
+    }
+    if (a.state_out != nullptr) {
+        const Rsrc rs = rsrc(a.state_out + bh * cells, cells * 4);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const bool row_in = row0 + i < a.kdim;
+            if constexpr (VEC) {
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    __builtin_bit_cast(u32x4, S[i]), rs,
+                    row_in && v0 < a.vdim ? ((row0 + i) * a.vdim + v0) * 4 : kPast, 0, 0);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    __builtin_amdgcn_raw_buffer_store_b32(
+                        __float_as_uint(S[i][e]), rs,
+                        row_in && v0 + e < a.vdim ? ((row0 + i) * a.vdim + v0 + e) * 4 : kPast, 0, 0);
+            }
+        }
+    }
+}
+
+template <typename T, int KT, int COLS>
+hipError_t launch(StepArgs s, int64_t heads, bool vec, hipStream_t stream) {
+    s.cols = (s.vdim + 4 * COLS - 1) / (4 * COLS);
+    const dim3 grid(static_cast<unsigned>(heads * s.cols));
+    if (vec) hipLaunchKernelGGL((step_kernel<T, KT, COLS, true>), grid, dim3(256), 0, stream, s);
+    else hipLaunchKernelGGL((step_kernel<T, KT, COLS, false>), grid, dim3(256), 0, stream, s);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t by_size(const StepArgs& s, int64_t heads, bool vec, hipStream_t stream) {
+    const bool few = heads < 512;
+    if (s.kdim > 64)
+        return few ? launch<T, 128, 8>(s, heads, vec, stream) : launch<T, 128, 32>(s, heads, vec, stream);
+    return few ? launch<T, 64, 8>(s, heads, vec, stream) : launch<T, 64, 32>(s, heads, vec, stream);
+}
+
+}  // namespace
+
+hipError_t launch_delta_update(const DeltaUpdateArgs& a) {
+    StepArgs s{};
+    s.state_in = a.state;
+    s.state_out = a.state;
+    s.q = a.q; s.k = a.k; s.v = a.v; s.g = a.g; s.beta = a.beta;
+    s.starts = a.reset;
+    s.out = a.out;
+    s.seqlen = 1;
+    s.ld_q = a.ld_q; s.ld_k = a.ld_k; s.ld_v = a.ld_v;
+    s.kheads = a.kheads; s.vheads = a.vheads; s.kdim = a.kdim; s.vdim = a.vdim;
+    s.scale = a.scale;
+    return a.bf16 ? by_size<bf16_t>(s, a.batch * a.vheads, a.vec, a.stream)
+                  : by_size<float>(s, a.batch * a.vheads, a.vec, a.stream);
+}
+
+}  // namespace mamba

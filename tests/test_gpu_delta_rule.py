@@ -1,0 +1,301 @@
+"""Gated delta rule on the GPU against the fp64 oracle.
+
+Tolerances, set from the arithmetic before the first run.  A state's element is a sum
+over tokens of products that are right to 2^-22; a token's readout and its
+correction are sums of up to 128 + 64 of them, off by at most 2^-22 of the sum of their
+magnitudes, which is up to sqrt(192) = 14 times the result's rms: 3.3e-6.  The
+corrections contract (keys of norm 1, 0 < beta < 1), so an error lives as long as
+the state, up to a few hundred tokens here, and errors of different tokens add as a root: ten
+to twenty times that, 5e-5 of the rms.  With bf16 the products that only reach an output keep
+operands of 16 bits (2^-16 in place of 2^-24: no more than 2e-4 of the rms), and outputs round
+once more, by at most 2^-8 relative."""
+
+import numpy as np
+import pytest
+
+import oracle.delta_rule as R
+from workloads import bf16_round
+from workloads.device import to_dev, to_host
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ssm():
+    import torch
+
+    import selective_state_space_23_amd as s
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU")
+    return s
+
+
+def close(got, ref, what, bf16=False):
+    """bf16: an output in bfloat16."""
+    got = to_host(got)
+    assert got.shape == ref.shape, (what, got.shape, ref.shape)
+    assert np.isfinite(got).all(), f"{what}: non-finite"
+    if got.size == 0:
+        return
+    tol = (2.0 ** -8 if bf16 else 2.0 ** -24) * np.abs(ref) + (2e-4 if bf16 else 5e-5) * np.sqrt(np.mean(ref ** 2))
+    err = np.abs(got - ref)
+    i = np.unravel_index(np.argmax(err - tol), err.shape)
+    assert (err <= tol).all(), f"{what}: {int((err > tol).sum())} of {err.size} off, worst at {i}: {got[i]} for {ref[i]}"
+
+
+def draw(B, L, Hk, Hv, K, V, dtype, docs=None, carry=False, seed=0, rate=0.1):
+    g = np.random.default_rng(seed)
+    rnd = bf16_round if dtype == "bf16" else (lambda a: a)
+    unit = lambda x: x / np.linalg.norm(x, axis=-1, keepdims=True)  # noqa: E731
+    d = dict(q=rnd(unit(g.standard_normal((B, L, Hk, K))).astype(np.float32)),
+             k=rnd(unit(g.standard_normal((B, L, Hk, K))).astype(np.float32)),
+             v=rnd(g.standard_normal((B, L, Hv, V)).astype(np.float32)),
+             g=(-rate * g.exponential(1.0, (B, L, Hv))).astype(np.float32),
+             beta=g.uniform(0.05, 1.0, (B, L, Hv)).astype(np.float32), doc_start=None, initial_state=None)
+    if docs is not None:
+        d["doc_start"] = (g.random((B, L)) < 1.0 / docs).astype(np.uint8)
+        if L:
+            d["doc_start"][::2, 0] = 1
+    if carry:
+        d["initial_state"] = g.standard_normal((B, Hv, K, V)).astype(np.float32)
+    d["dout"] = rnd(g.standard_normal((B, L, Hv, V)).astype(np.float32))
+    d["d_final_state"] = g.standard_normal((B, Hv, K, V)).astype(np.float32) if carry else None
+    return d
+
+
+def dev(d, dtype):
+    import torch
+
+    up = {n: None if d[n] is None else to_dev(d[n], dtype) for n in ("q", "k", "v", "dout")}
+    for n in ("g", "beta", "doc_start", "initial_state", "d_final_state"):
+        up[n] = None if d[n] is None else torch.from_numpy(d[n]).cuda()
+    return up
+
+
+FWD = ("q", "k", "v", "g", "beta", "doc_start", "initial_state")
+
+
+def forward(ssm, t, **kw):
+    return ssm.gated_delta_rule_fwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["doc_start"],
+                                    initial_state=t["initial_state"], **kw)
+
+
+SHAPES = [
+    # B, L, Hk, Hv, K, V, dtype, docs, carry
+    (1, 1, 1, 1, 16, 16, "f32", None, False),
+    (2, 1, 1, 2, 128, 128, "bf16", None, True),
+    (1, 2, 1, 1, 1, 1, "f32", None, True),
+    (2, 15, 2, 2, 8, 24, "bf16", None, False),
+    (1, 63, 1, 1, 64, 64, "bf16", None, False),
+    (2, 64, 1, 1, 128, 128, "f32", None, True),
+    (2, 65, 1, 3, 100, 75, "f32", 20, True),
+    (1, 127, 2, 2, 65, 17, "bf16", 30, True),
+    (3, 200, 2, 4, 96, 128, "bf16", 50, False),
+    (2, 321, 1, 1, 128, 128, "bf16", None, True),
+    (1, 300, 3, 3, 33, 31, "f32", 7, True),
+    (2, 257, 1, 2, 7, 120, "f32", 1, False),
+    (1, 1001, 1, 1, 128, 64, "bf16", 150, False),
+]
+ids = lambda s: "-".join(map(str, s))  # noqa: E731
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=ids)
+def test_forward(ssm, shape):
+    B, L, Hk, Hv, K, V, dtype, docs, carry = shape
+    d = draw(B, L, Hk, Hv, K, V, dtype, docs, carry, seed=L)
+    out, S, kept = forward(ssm, dev(d, dtype), save="states")
+    ro, rS, rs = R.gated_delta_rule(**{n: d[n] for n in FWD})
+    close(out, ro, "out", dtype == "bf16")
+    close(S, rS, "final_state")
+    close(kept["states"], rs, "states")
+
+
+def test_slices_of_one_projection(ssm):
+    import torch
+
+    d = draw(2, 150, 2, 4, 32, 24, "bf16", 40, True, seed=5)
+    t = dev(d, "bf16")
+    plain = forward(ssm, t)
+    for pad in (0, 1):     # whole 16-byte pieces, and not
+        proj = torch.full((2, 150, 2 * 64 + 96 + pad), float("nan"), dtype=torch.bfloat16, device="cuda")
+        cut, at = dict(t), 0
+        for n, w in (("q", 64), ("k", 64), ("v", 96)):
+            proj[..., at:at + w] = t[n].flatten(-2)
+            cut[n] = proj[..., at:at + w].unflatten(-1, t[n].shape[-2:])
+            at += w
+        for a, b in zip(forward(ssm, cut), plain):
+            assert torch.equal(a, b)
+
+
+def test_no_decay_equal_keys(ssm):
+    """The worst-conditioned triangle: one key throughout, beta = 1, nothing decays."""
+    d = draw(1, 200, 1, 1, 64, 32, "bf16", seed=8)
+    d["k"][:] = d["k"][:, :1]
+    d["beta"][:] = 1.0
+    d["g"] = None
+    out, S = forward(ssm, dev(d, "bf16"))
+    ro, rS, _ = R.gated_delta_rule(**{n: d[n] for n in FWD})
+    close(out, ro, "out", True)
+    close(S, rS, "final_state")
+
+
+@pytest.mark.parametrize("rate", [0.0, 3.0, 400.0])
+def test_decays_of_any_size(ssm, rate):
+    d = draw(2, 190, 1, 2, 40, 24, "f32", 60, True, seed=9, rate=rate)
+    if rate == 400.0:
+        d["g"][0, 70] = -np.inf
+    out, S = forward(ssm, dev(d, "f32"))
+    ro, rS, _ = R.gated_delta_rule(**{n: d[n] for n in FWD})
+    close(out, ro, "out")
+    close(S, rS, "final_state")
+
+
+@pytest.mark.parametrize("where", ["q", "k", "v", "g", "beta", "initial_state"])
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_not_finite_stays_in_its_document(ssm, where, value, dtype):
+    """Neither another document nor an earlier token sees it; its document's later tokens do."""
+    L, at = 200, 100
+    d = draw(2, L, 1, 2, 32, 24, dtype, seed=11, carry=True)
+    d["doc_start"] = np.zeros((2, L), np.uint8)
+    d["doc_start"][:, [30, 85, 110, 111, 190]] = 1
+    ref, rS, _ = R.gated_delta_rule(**{n: d[n] for n in FWD})
+    bad = {n: None if x is None else x.copy() for n, x in d.items()}
+    if where == "initial_state":
+        bad[where][0, 0, 3, 5] = value
+        first, last = 0, 30
+    else:
+        bad[where][(0, at, 0) if where in ("g", "beta") else (0, at, 0, 3)] = value
+        first, last = at, 110
+    out, S = forward(ssm, dev(bad, dtype))
+    got = to_host(out)
+    tol = (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) * np.abs(ref) + 2e-4 * np.sqrt(np.mean(ref ** 2))
+    clean = np.ones((2, L), bool)
+    clean[0, first:last] = False
+    assert (np.abs(got - ref) <= tol)[clean].all()
+    close(S, rS, "final_state")
+    hurt = got[0, first:last, 0]
+    if where == "q":
+        assert not np.isfinite(hurt[0]).any() and np.isfinite(hurt[1:]).all()
+    elif where in ("k", "g", "beta"):
+        assert not np.isfinite(hurt).any()
+    else:
+        col = 5 if where == "initial_state" else 3
+        assert not np.isfinite(hurt[:, col]).any()
+        assert np.isfinite(np.delete(hurt, col, 1)).all()
+
+
+def test_lost_state_and_its_end(ssm):
+    """A bad value in the last document makes the final state NaN; with no more documents, all that follows."""
+    d = draw(1, 150, 1, 1, 32, 16, "f32", seed=12)
+    d["v"][0, 40, 0, 2] = np.nan
+    out, S = forward(ssm, dev(d, "f32"))
+    got, S = to_host(out), to_host(S)
+    assert np.isfinite(got[0, :40]).all() and np.isnan(got[0, 40:, 0, 2]).all()
+    assert np.isnan(S[0, 0, :, 2]).all() and np.isfinite(np.delete(S, 2, -1)).all()
+
+
+STEPS = [(2, 12, 12, 128, 128, "bf16"), (3, 1, 3, 100, 75, "f32"), (1, 1, 1, 1, 1, "f32"), (5, 2, 4, 33, 64, "bf16"),
+         (40, 4, 16, 64, 128, "bf16"), (600, 1, 1, 128, 96, "f32"), (520, 1, 1, 17, 21, "bf16")]
+
+
+@pytest.mark.parametrize("shape", STEPS, ids=ids)
+def test_step(ssm, shape):
+    import torch
+
+    B, Hk, Hv, K, V, dtype = shape
+    d = draw(B, 3, Hk, Hv, K, V, dtype, carry=True, seed=B)
+    d["doc_start"] = np.zeros((B, 3), np.uint8)
+    d["doc_start"][B // 2, 1] = 1
+    t = dev(d, dtype)
+    state = t["initial_state"].clone()
+    ro, rS, _ = R.gated_delta_rule(**{n: d[n] for n in FWD})
+    for i in range(3):     # a column of (B, L, H, D) tensors as it is
+        out = ssm.gated_delta_rule_update(state, t["q"][:, i], t["k"][:, i], t["v"][:, i], t["g"][:, i].contiguous(),
+                                          t["beta"][:, i].contiguous(), t["doc_start"][:, i].contiguous())
+        close(out, ro[:, i], f"out {i}", dtype == "bf16")
+    close(state, rS, "state")
+    bare = ssm.gated_delta_rule_update(t["initial_state"].clone(), t["q"][:, 0], t["k"][:, 0], t["v"][:, 0], None,
+                                       t["beta"][:, 0].contiguous(), scale=1.0)
+    first = {n: d[n][:, :1] for n in ("q", "k", "v", "beta")}
+    rb, _, _ = R.gated_delta_rule(g=None, scale=1.0, initial_state=d["initial_state"], **first)
+    close(bare, rb[:, 0], "without decay", dtype == "bf16")
+    assert torch.isfinite(bare).all()
+
+
+def test_prefill_then_steps(ssm):
+    d = draw(2, 140, 2, 4, 64, 32, "f32", 50, seed=21)
+    t = dev(d, "f32")
+    ro, rS, _ = R.gated_delta_rule(**{n: d[n] for n in FWD})
+    part = {n: x if x is None or n == "initial_state" else x[:, :133].contiguous() for n, x in t.items()}
+    _, S = forward(ssm, part)
+    for i in range(133, 140):
+        out = ssm.gated_delta_rule_update(S, *(t[n][:, i].contiguous() for n in ("q", "k", "v", "g", "beta")),
+                                          t["doc_start"][:, i].contiguous())
+        close(out, ro[:, i], f"token {i}")
+    close(S, rS, "state")
+
+
+def test_empty(ssm):
+    import torch
+
+    d = draw(2, 0, 1, 2, 8, 8, "f32", carry=True)
+    t = dev(d, "f32")
+    out, S = forward(ssm, t)
+    assert out.shape == (2, 0, 2, 8) and torch.equal(S, t["initial_state"])
+    t["initial_state"] = None
+    out, S = forward(ssm, t, final_state=torch.full((2, 2, 8, 8), float("nan"), device="cuda"))
+    assert torch.equal(S, torch.zeros_like(S))
+
+
+def test_forward_writes_nothing_else(ssm):
+    """Guard values around outputs whose rows and heads end inside a tile stay as they were."""
+    import torch
+
+    B, L, H, K, V = 2, 70, 2, 20, 13
+    t = dev(draw(B, L, H, H, K, V, "bf16", seed=3), "bf16")
+    want = forward(ssm, t)
+    n = B * L * H * V
+    room = torch.full((n + 128,), 7.0, dtype=torch.bfloat16, device="cuda")
+    fin = torch.full((B * H * K * V + 128,), 7.0, device="cuda")
+    out, S = forward(ssm, t, out=room[64:64 + n].view(B, L, H, V), final_state=fin[64:-64].view(B, H, K, V))
+    assert torch.equal(out, want[0]) and torch.equal(S, want[1])
+    assert (room[:64] == 7).all() and (room[-64:] == 7).all() and (fin[:64] == 7).all() and (fin[-64:] == 7).all()
+
+
+def test_streams_and_graphs(ssm):
+    """Two calls under way on streams of their own, and a captured prefill and step replayed between eager work."""
+    import torch
+
+    a = dev(draw(2, 300, 2, 2, 64, 64, "bf16", 80, seed=1), "bf16")
+    b = dev(draw(1, 500, 1, 3, 128, 128, "bf16", seed=2), "bf16")
+    wa, wb = forward(ssm, a), forward(ssm, b)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            ga = forward(ssm, a)
+        with torch.cuda.stream(s2):
+            gb = forward(ssm, b)
+        got.append((ga, gb))
+    torch.cuda.synchronize()
+    for ga, gb in got:
+        assert all(torch.equal(x, y) for x, y in zip(ga + gb, wa + wb))
+
+    ws = torch.empty(ssm.gated_delta_rule_workspace_bytes(2, 300, 2, 2, 64, 64), dtype=torch.uint8, device="cuda")
+    out, fin = torch.empty_like(wa[0]), torch.empty_like(wa[1])
+    one = {n: a[n][:, 0].contiguous() for n in ("q", "k", "v", "g", "beta")}
+    step_out = torch.empty_like(one["v"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        forward(ssm, a, out=out, final_state=fin, workspace=ws)
+        ssm.gated_delta_rule_update(fin, *one.values(), out=step_out)
+    want = wa[1].clone()
+    want_out = ssm.gated_delta_rule_update(want, *one.values())
+    for _ in range(4):
+        out.zero_(); fin.zero_(); step_out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, wa[0]) and torch.equal(fin, want) and torch.equal(step_out, want_out)
+        forward(ssm, b)
