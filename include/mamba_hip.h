@@ -567,6 +567,30 @@ int mamba_gated_delta_rule_fwd(const mamba_delta_dims_t* dims, const void* q, co
                                const float* initial_state, void* out, float* final_state, float* states,
                                void* workspace, size_t workspace_bytes, void* stream);
 
+/* Bytes of device workspace mamba_gated_delta_rule_bwd needs: some 600 per token and
+ * value head, and 4 K V per chunk of 64 for the gradients at the states between
+ * chunks (8 K V without `states`). */
+int mamba_gated_delta_rule_bwd_workspace_bytes(const mamba_delta_dims_t* dims, int32_t have_states, size_t* bytes);
+
+/* Backward: the gradients of sum(dout out) + sum(d_final_state final_state).
+ *   dims ... initial_state: as the forward call.
+ *   states     what the forward wrote, or NULL: recomputed.
+ *   dout       (B, L, Hv, V); d_final_state (B, Hv, K, V) float32 or NULL (0).
+ *   dq, dk     (B, L, Hk, K), sums over the value heads that share the key head, and dv
+ *              (B, L, Hv, V): dense, `dtype`.
+ *   dg         (B, L, Hv) float32, 0 where a document starts; non-NULL exactly when g
+ *              is.  dbeta (B, L, Hv) float32.
+ *   d_initial_state (B, Hv, K, V) float32 or NULL; requires initial_state.
+ *   workspace  at least mamba_gated_delta_rule_bwd_workspace_bytes, 256-byte aligned.
+ * A decay below exp(-200) counts as 0 and has gradient 0.  A NaN or an infinity in a document makes
+ * gradients of that document NaN, and of no other.  L of 0 writes d_initial_state =
+ * d_final_state (or 0).  Repeated calls give bitwise identical results. */
+int mamba_gated_delta_rule_bwd(const mamba_delta_dims_t* dims, const void* q, const void* k, const void* v,
+                               const float* g, const float* beta, const uint8_t* doc_start,
+                               const float* initial_state, const float* states, const void* dout,
+                               const float* d_final_state, void* dq, void* dk, void* dv, float* dg, float* dbeta,
+                               float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream);
+
 /* One token per row.
  *   dims       with seqlen == 1; strides are between rows, of up to 2^40 elements.
  *   state      (B, Hv, K, V) float32, updated in place.

@@ -31,6 +31,7 @@ missing or the tensors are not on a GPU the calls raise.
 
     # gated delta rule: a K x V state per head, q and k (B, L, Hk, K), v (B, L, Hv, V), g and beta (B, L, Hv)
     out, S, kept = gated_delta_rule_fwd(q, k, v, g, beta, doc_start, save="states")
+    grads = gated_delta_rule_bwd(q, k, v, g, beta, dout, doc_start, states=kept["states"])
     out_t = gated_delta_rule_update(S, q_t, k_t, v_t, g_t, beta_t)
 """
 
@@ -64,8 +65,10 @@ __all__ = [
     "activation_pack",
     "activation_unpack",
     "gated_delta_rule_fwd",
+    "gated_delta_rule_bwd",
     "gated_delta_rule_update",
     "gated_delta_rule_workspace_bytes",
+    "gated_delta_rule_bwd_workspace_bytes",
     "MambaError",
     "MambaArgumentError",
     "library_path",
@@ -957,6 +960,72 @@ def gated_delta_rule_fwd(q, k, v, g, beta, doc_start=None, scale=None, initial_s
         _ptr(workspace, "workspace", dev, torch.uint8), 0 if workspace is None else workspace.numel())
     _lib.check(st, "mamba_gated_delta_rule_fwd")
     return (out, final_state) if save is None else (out, final_state, kept)
+
+
+def gated_delta_rule_bwd_workspace_bytes(batch, seqlen, key_heads, value_heads, key_dim, value_dim, dtype="bf16",
+                                         states=False) -> int:
+    code = _lib.MAMBA_DTYPE_BF16 if dtype == "bf16" else _lib.MAMBA_DTYPE_F32
+    dims = _lib.DeltaDims(batch, seqlen, key_heads, value_heads, key_dim, value_dim, 0, 0, 0, 0, code, 1.0)
+    n = ctypes.c_size_t(0)
+    _lib.check(_lib.load().mamba_gated_delta_rule_bwd_workspace_bytes(ctypes.byref(dims), int(bool(states)),
+                                                                      ctypes.byref(n)),
+               "mamba_gated_delta_rule_bwd_workspace_bytes")
+    return int(n.value)
+
+
+def gated_delta_rule_bwd(q, k, v, g, beta, dout, doc_start=None, scale=None, initial_state=None, d_final_state=None,
+                         states=None, workspace=None, grads=None):
+    """Gradients of sum(dout * out) + sum(d_final_state * final_state) for the gated
+    delta rule; see mamba_gated_delta_rule_bwd.
+
+    q ... initial_state as given to gated_delta_rule_fwd; ``states`` what it kept (or
+    None: recomputed); dout (B, L, Hv, V), dense or a slice.  Returns a dict with dq, dk
+    (summed over the value heads of a key head), dv (q's dtype), dbeta (B, L, Hv)
+    float32 and, for each optional input given, dg (B, L, Hv) and d_initial_state
+    (B, Hv, K, V) float32.  ``grads``: optional dict of preallocated outputs with the
+    same keys."""
+    torch = _torch()
+    dev = _check_device(q)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be (B, L, Hk, K) and v (B, L, Hv, V)")
+    code, dt, f32 = _dtype_code(q), q.dtype, torch.float32
+    Bt, L, Hk, K = q.shape
+    Hv, V = v.shape[-2:]
+    state = (Bt, Hv, K, V)
+    if doc_start is not None and doc_start.dtype == torch.bool:
+        doc_start = doc_start.to(torch.uint8)
+    pq, lq = _heads(q, "q", dev, dt, q.shape)
+    pk, lk = _heads(k, "k", dev, dt, q.shape)
+    pv, lv = _heads(v, "v", dev, dt, (Bt, L, Hv, V))
+    po, lo = _heads(dout, "dout", dev, dt, (Bt, L, Hv, V))
+    shapes = {"dq": ((Bt, L, Hk, K), dt), "dk": ((Bt, L, Hk, K), dt), "dv": ((Bt, L, Hv, V), dt)}
+    if g is not None:
+        shapes["dg"] = ((Bt, L, Hv), f32)
+    shapes["dbeta"] = ((Bt, L, Hv), f32)
+    if initial_state is not None:
+        shapes["d_initial_state"] = (state, f32)
+    res = dict(grads) if grads else {}
+    for n, (sh, d) in shapes.items():
+        if n not in res:
+            res[n] = torch.empty(sh, dtype=d, device=dev)
+    dims = _delta_dims(q, k, v, (Bt, L), scale, code, (lq, lk, lv, lo))
+    lib = _lib.load()
+    if workspace is None:
+        workspace = _recurrence_workspace(lib.mamba_gated_delta_rule_bwd_workspace_bytes,
+                                          "mamba_gated_delta_rule_bwd_workspace_bytes", dev, ctypes.byref(dims),
+                                          int(states is not None))
+    to = lambda n: _ptr(res[n], n, dev, shapes[n][1], shapes[n][0]) if n in shapes else None  # noqa: E731
+    st = _launch(
+        dev, lib.mamba_gated_delta_rule_bwd, ctypes.byref(dims), pq, pk, pv,
+        _ptr(g, "g", dev, f32, (Bt, L, Hv)), _ptr(beta, "beta", dev, f32, (Bt, L, Hv)),
+        _ptr(doc_start, "doc_start", dev, torch.uint8, (Bt, L)),
+        _ptr(initial_state, "initial_state", dev, f32, state),
+        _ptr(states, "states", dev, f32, (Bt, Hv, -(-L // _lib.DELTA_CHUNK), K, V)), po,
+        _ptr(d_final_state, "d_final_state", dev, f32, state),
+        to("dq"), to("dk"), to("dv"), to("dg"), to("dbeta"), to("d_initial_state"),
+        _ptr(workspace, "workspace", dev, torch.uint8), 0 if workspace is None else workspace.numel())
+    _lib.check(st, "mamba_gated_delta_rule_bwd")
+    return {n: res[n] for n in shapes}
 
 
 def gated_delta_rule_update(state, q, k, v, g, beta, reset=None, scale=None, out=None):

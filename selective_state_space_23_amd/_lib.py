@@ -43,6 +43,8 @@ EXPORTED = (
     "mamba_gated_recurrence_update",
     "mamba_gated_delta_rule_workspace_bytes",
     "mamba_gated_delta_rule_fwd",
+    "mamba_gated_delta_rule_bwd_workspace_bytes",
+    "mamba_gated_delta_rule_bwd",
     "mamba_gated_delta_rule_update",
 )
 
@@ -186,6 +188,10 @@ def load() -> ctypes.CDLL:
     lib.mamba_gated_delta_rule_workspace_bytes.restype = ctypes.c_int
     lib.mamba_gated_delta_rule_fwd.argtypes = [dd] + [vp] * 11 + [sz, vp]
     lib.mamba_gated_delta_rule_fwd.restype = ctypes.c_int
+    lib.mamba_gated_delta_rule_bwd_workspace_bytes.argtypes = [dd, i32, ctypes.POINTER(sz)]
+    lib.mamba_gated_delta_rule_bwd_workspace_bytes.restype = ctypes.c_int
+    lib.mamba_gated_delta_rule_bwd.argtypes = [dd] + [vp] * 17 + [sz, vp]
+    lib.mamba_gated_delta_rule_bwd.restype = ctypes.c_int
     lib.mamba_gated_delta_rule_update.argtypes = [dd] + [vp] * 9
     lib.mamba_gated_delta_rule_update.restype = ctypes.c_int
     _lib = lib

@@ -87,6 +87,14 @@ size_t fwd_workspace(const mamba_delta_dims_t* d) {
     return d->batch * d->seqlen == 0 ? 0 : record_bytes(d) + solve_bytes(d);
 }
 
+size_t state_bytes(const mamba_delta_dims_t* d) {   // of every chunk
+    return round256(static_cast<size_t>(d->batch * d->value_heads * chunks_of(d)) * d->key_dim * d->value_dim * 4);
+}
+
+size_t bwd_workspace(const mamba_delta_dims_t* d, bool have_states) {
+    return d->batch * d->seqlen == 0 ? 0 : record_bytes(d) + 2 * solve_bytes(d) + (have_states ? 1 : 2) * state_bytes(d);
+}
+
 mamba::DeltaArgs base_args(const mamba_delta_dims_t* d, const Sizes& s, const void* q, const void* k, const void* v,
                            const float* g, const float* beta, const uint8_t* doc_start, const float* initial_state,
                            void* workspace, void* stream) {
@@ -149,6 +157,62 @@ int mamba_gated_delta_rule_fwd(const mamba_delta_dims_t* dims, const void* q, co
     a.out = out; a.final_state = final_state; a.states = states;
     const hipError_t e = mamba::launch_delta_prepare(a);
     return hip_status(e != hipSuccess ? e : mamba::launch_delta_fwd(a));
+}
+
+int mamba_gated_delta_rule_bwd_workspace_bytes(const mamba_delta_dims_t* dims, int32_t have_states, size_t* bytes) {
+    if (!bytes) return MAMBA_ERR_INVALID_ARGUMENT;
+    *bytes = 0;
+    const int st = check_dims(dims);
+    if (st != MAMBA_OK) return st;
+    *bytes = bwd_workspace(dims, have_states != 0);
+    return MAMBA_OK;
+}
+
+int mamba_gated_delta_rule_bwd(const mamba_delta_dims_t* dims, const void* q, const void* k, const void* v,
+                               const float* g, const float* beta, const uint8_t* doc_start,
+                               const float* initial_state, const float* states, const void* dout,
+                               const float* d_final_state, void* dq, void* dk, void* dv, float* dg, float* dbeta,
+                               float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream) {
+    const int st = check_dims(dims);
+    if (st != MAMBA_OK) return st;
+    const float* f32s[] = {g, beta, initial_state, states, d_final_state, dg, dbeta, d_initial_state};
+    for (const float* p : f32s)
+        if (p && !aligned(p, 4)) return MAMBA_ERR_MISALIGNED;
+    if (d_initial_state && !initial_state) return MAMBA_ERR_INVALID_ARGUMENT;
+    const Sizes s = sizes(dims);
+    if (dims->batch == 0) return MAMBA_OK;
+    if (dims->seqlen == 0) {
+        if (overlap(d_initial_state, s.state, d_final_state, s.state)) return MAMBA_ERR_INVALID_ARGUMENT;
+        return hip_status(mamba::launch_fill(d_initial_state, d_final_state, static_cast<int64_t>(s.state / 4),
+                                             static_cast<hipStream_t>(stream)));
+    }
+    if (!q || !k || !v || !beta || !dout || !dq || !dk || !dv || !dbeta || (g != nullptr) != (dg != nullptr))
+        return MAMBA_ERR_INVALID_ARGUMENT;
+    const void* acts[] = {q, k, v, dout, dq, dk, dv};
+    for (const void* p : acts)
+        if (!aligned(p, s.esz)) return MAMBA_ERR_MISALIGNED;
+    const size_t need = bwd_workspace(dims, states != nullptr);
+    if (!workspace || workspace_bytes < need) return MAMBA_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return MAMBA_ERR_MISALIGNED;
+    const Span ins[] = {{q, span(s.tokens, s.kw, s.ld_q, s.esz)}, {k, span(s.tokens, s.kw, s.ld_k, s.esz)},
+                        {v, span(s.tokens, s.vw, s.ld_v, s.esz)}, {dout, span(s.tokens, s.vw, s.ld_o, s.esz)},
+                        {g, s.gate}, {beta, s.gate}, {doc_start, static_cast<size_t>(s.tokens)},
+                        {initial_state, s.state}, {d_final_state, s.state}, {states, s.state * chunks_of(dims)}};
+    const Span outs[] = {{dq, s.k}, {dk, s.k}, {dv, s.v}, {dg, s.gate}, {dbeta, s.gate}, {d_initial_state, s.state},
+                         {workspace, need}};
+    if (!disjoint(ins, outs)) return MAMBA_ERR_INVALID_ARGUMENT;
+    mamba::DeltaArgs a = base_args(dims, s, q, k, v, g, beta, doc_start, initial_state, workspace, stream);
+    a.solve_t = a.solve + solve_bytes(dims);
+    a.dstates = reinterpret_cast<float*>(a.solve_t + solve_bytes(dims));
+    a.states = states ? const_cast<float*>(states) : a.dstates + state_bytes(dims) / 4;
+    a.dout = dout; a.d_final_state = d_final_state;
+    a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.d_initial_state = d_initial_state;
+    a.vec_o = pieces(dout, s.ld_o, s.esz, dims->value_dim) && aligned(a.states, 16);
+    hipError_t e = mamba::launch_delta_prepare(a);
+    if (e == hipSuccess && !states) e = mamba::launch_delta_fwd(a);   // no output: the states alone
+    if (e == hipSuccess) e = mamba::launch_delta_bwd_states(a);
+    if (e == hipSuccess) e = mamba::launch_delta_bwd_grads(a);
+    return hip_status(e);
 }
 
 int mamba_gated_delta_rule_update(const mamba_delta_dims_t* dims, float* state, const void* q, const void* k,

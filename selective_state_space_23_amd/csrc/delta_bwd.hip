@@ -1,0 +1,309 @@
+// Gated delta rule, backward: the gradient dS at every chunk's end state, the chunks of a
+// row from last to first.
+//
+//     dU = P^T dO + exp(gamma_C - gamma) K dS,   P = scale D o Q K^T,   dX = (I + b M)^-T dU,
+//     dS <- exp(gamma_C) dS + (scale exp(gamma) Q)^T dO - (exp(gamma) K)^T (beta dX).
+//
+// Columns do not mix here either: a wave owns 16, as in the forward (delta_fwd.hip), with dS
+// in its accumulators.  Everything that sums over columns is left to delta_grads.hip,
+// which works off the chunks at once from the states and gradients between them.
+//
+// What is not finite makes the whole of its document NaN (through the state a gradient
+// reaches every token before, through the keys it came by every token after), and
+// no other: its rows are taken out of every sum over tokens.
+#include "delta_rule.hpp"
+
+namespace mamba {
+
+namespace {
+
+using namespace delta;
+
+template <typename T, int KT, int NW, bool VEC>
+__global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
+    constexpr int N = kPieces<T>, ESZ = sizeof(T), STEPS = KT / 32, THREADS = NW * 64;
+    using KQ = Tile<T, KT, THREADS, VEC>;
+    constexpr int ROW = KQ::ROW;
+    constexpr int RECW = sizeof(ChunkRec) / 4, RECP = (RECW + THREADS - 1) / THREADS;
+    constexpr int TP = (kBlocks * 3 + NW - 1) / NW;
+    __shared__ __align__(16) char smem[2 * KQ::kBytes + kSolveBytes + RECP * THREADS * 4];
+    u32x4* Tl = reinterpret_cast<u32x4*>(smem);
+    ChunkRec* rec = reinterpret_cast<ChunkRec*>(Tl + kBlocks * 3 * 64);
+    uint16_t* Kl = reinterpret_cast<uint16_t*>(smem + kSolveBytes + RECP * THREADS * 4);
+    uint16_t* Ql = Kl + N * C * ROW;
+
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, m = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t bh = blockIdx.x / cols;
+    const int col = static_cast<int>(blockIdx.x % cols);
+    const int hv = static_cast<int>(bh % a.vheads), hk = hv / (a.vheads / a.kheads);
+    const int64_t b = bh / a.vheads;
+    const int v = (col * NW + wave) * 16 + m;
+    const bool v_in = v < a.vdim;
+    const int n = a.nchunks;
+    const int64_t cells = static_cast<int64_t>(a.kdim) * a.vdim;
+
+    auto state_off = [&](int i, int r) {
+        const int kd = state_row(i, g, r);
+        return v_in && kd < a.kdim ? static_cast<uint32_t>((kd * a.vdim + v) * 4) : kPast;
+    };
+    f32x4 S[2 * STEPS];   // dS
+    {
+        const Rsrc rs = rsrc(a.d_final_state + (a.d_final_state ? bh * cells : 0), a.d_final_state ? cells * 4 : 0);
+#pragma unroll
+        for (int i = 0; i < 2 * STEPS; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                S[i][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, state_off(i, r), 0, 0));
+    }
+    auto store_state = [&](float* to) {
+        const Rsrc rs = rsrc(to, cells * 4);
+#pragma unroll
+        for (int i = 0; i < 2 * STEPS; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][r]), rs, state_off(i, r), 0, 0);
+    };
+
+    KQ kraw, qraw;
+    u32x4 traw[TP];
+    uint32_t oraw[16], recraw[RECP];
+    auto fetch = [&](int c) {
+        const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, left = a.seqlen - static_cast<int64_t>(c) * C;
+        const int rows = static_cast<int>(left < C ? left : C);
+        kraw.fetch(rows_rsrc<ESZ>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k, a.kdim), a.ld_k,
+                   a.kdim, tid);
+        qraw.fetch(rows_rsrc<ESZ>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_q, a.kdim), a.ld_q,
+                   a.kdim, tid);
+        const int64_t id = bh * n + c;
+        const Rsrc tr = rsrc(a.solve_t + id * kSolveBytes, kSolveBytes);
+#pragma unroll
+        for (int p = 0; p < TP; ++p) traw[p] = __builtin_amdgcn_raw_buffer_load_b128(tr, (p * THREADS + tid) * 16, 0, 0);
+        const Rsrc rr = rsrc(a.chunks + id * rec_bytes, RECW * 4);
+#pragma unroll
+        for (int p = 0; p < RECP; ++p) recraw[p] = __builtin_amdgcn_raw_buffer_load_b32(rr, (p * THREADS + tid) * 4, 0, 0);
+        const Rsrc orr = rows_rsrc<ESZ>(a.dout, first * a.ld_o + static_cast<int64_t>(hv) * a.vdim, rows, a.ld_o, a.vdim);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                oraw[4 * i + r] = load_one<T>(
+                    orr, v_in ? static_cast<uint32_t>(((16 * i + 4 * g + r) * a.ld_o + v) * ESZ) : kPast);
+    };
+
+    fetch(n - 1);
+    for (int c = n - 1; c >= 0; --c) {
+        kraw.land(Kl, tid);
+        qraw.land(Ql, tid);
+#pragma unroll
+        for (int p = 0; p < TP; ++p)
+            if (p * NW + wave < kBlocks * 3) Tl[p * THREADS + tid] = traw[p];
+#pragma unroll
+        for (int p = 0; p < RECP; ++p) reinterpret_cast<uint32_t*>(rec)[p * THREADS + tid] = recraw[p];
+        lds_barrier();
+        f32x4 dO[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dO[i][r] = one_value<T>(oraw[4 * i + r]);
+        if (c > 0) fetch(c - 1);
+
+        const uint64_t starts = uniform(rec->starts), bad = uniform(rec->bad);
+        const int first_start = starts ? __builtin_ctzll(starts) : C;
+        const int last_start = starts ? 63 - __builtin_clzll(starts) : 0;
+        store_state(a.dstates + (bh * n + c) * cells);
+        __builtin_amdgcn_sched_barrier(0);
+
+        // Rows whose gradient is not finite take no part, with the rest of their document
+        uint64_t sick = 0;
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) odd = odd || not_finite(dO[i][r]);
+        if (bad != 0 || __ballot(odd) != 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sick |= not_finite(dO[i][r]) ? uint64_t(1) << (16 * i + 4 * g + r) : 0;
+            sick |= __shfl_xor(sick, 16);
+            sick |= __shfl_xor(sick, 32);
+            sick = whole(sick | bad, starts);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) dO[i][r] = (sick >> (16 * i + 4 * g + r)) & 1 ? 0.0f : dO[i][r];
+        }
+
+        // K dS and Q K^T
+        f32x4 ks[4], pq[4][4];   // pq[it][is]: rows t of tile it, columns s of tile is
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ks[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pq[i][j] = f32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j) {
+            __builtin_amdgcn_sched_barrier(0);
+            const Frag<3> sf = split(S[2 * j], S[2 * j + 1]);
+            Frag<N> kf[4], qf[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                kf[i] = rows_frag<N, ROW>(Kl, 16 * i + m, 32 * j + 8 * g);
+                qf[i] = rows_frag<N, ROW>(Ql, 16 * i + m, 32 * j + 8 * g);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) product<3>(ks[i], kf[i], sf);
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
+#pragma unroll
+                for (int is = 0; is <= it; ++is) product<3>(pq[it][is], qf[it], kf[is]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+
+        // dU
+        f32x4 U[4];
+        {
+            f32x4 th[4], tl[4];
+            Frag<3> of[2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                th[i] = four(rec->hi + 16 * i + 4 * g);
+                tl[i] = four(rec->lo + 16 * i + 4 * g);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) of[j] = split(dO[2 * j], dO[2 * j + 1]);
+#pragma unroll
+            for (int is = 0; is < 4; ++is) {
+                const f32x4 outof = four(rec->outof + 16 * is + 4 * g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    U[is][r] = 16 * is + 4 * g + r >= last_start ? outof[r] * ks[is][r] : 0.0f;
+                const int s = 16 * is + m, end = doc_end(starts, s);
+                const float sh = rec->hi[s], sl = rec->lo[s];
+                f32x4 P[4];
+#pragma unroll
+                for (int it = is & 2; it < 4; ++it)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int t = 16 * it + 4 * g + r;
+                        const float d = exp2_fast((th[it][r] - sh) + (tl[it][r] - sl));
+                        P[it][r] = it >= is && t >= s && t < end ? a.scale * pq[it > is ? it : is][is][r] * d : 0.0f;
+                    }
+#pragma unroll
+                for (int j = is / 2; j < 2; ++j) {
+                    const Frag<3> pf = split(P[2 * j], P[2 * j + 1]);
+                    if constexpr (N == 1) product<3>(U[is], pf, Frag<1>{{of[j].p[0]}});   // dO as stored is one piece
+                    else product<3>(U[is], pf, of[j]);
+                }
+            }
+        }
+        odd = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) odd = odd || not_finite(U[i][r]);
+        const bool any_sick = __ballot(odd || sick != 0) != 0;
+        uint64_t drop = 0;   // rows out in all of the wave's columns: their keys and queries may be what is not finite
+        if (any_sick) {
+            uint64_t more = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) more |= not_finite(U[i][r]) ? uint64_t(1) << (16 * i + 4 * g + r) : 0;
+            more |= __shfl_xor(more, 16);
+            more |= __shfl_xor(more, 32);
+            sick = whole(sick | more, starts);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    U[i][r] = (sick >> (16 * i + 4 * g + r)) & 1 ? 0.0f : U[i][r];
+                    dO[i][r] = (sick >> (16 * i + 4 * g + r)) & 1 ? 0.0f : dO[i][r];
+                }
+            drop = sick;
+#pragma unroll
+            for (int s = 1; s < 16; s *= 2) drop &= __shfl_xor(drop, s);
+            drop = uniform(drop);
+        }
+
+        // beta dX, then with what the entering state has kept; the same of dO
+        f32x4 X[4];
+        {
+            const Frag<3> uf[2] = {split(U[0], U[1]), split(U[2], U[3])};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                X[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int j = i / 2; j < 2; ++j) {
+                    Frag<3> tf;
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) tf.p[p] = Tl[(high_block(i, j) * 3 + p) * 64 + lane];
+                    product<3>(X[i], tf, uf[j]);
+                }
+                const f32x4 beta = four(rec->beta + 16 * i + 4 * g), into = four(rec->into + 16 * i + 4 * g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const bool old = 16 * i + 4 * g + r < first_start;
+                    X[i][r] = old ? -into[r] * (beta[r] * X[i][r]) : 0.0f;
+                    dO[i][r] = old ? a.scale * into[r] * dO[i][r] : 0.0f;
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+
+        // dS
+        const float keep = rec->keep;
+#pragma unroll
+        for (int i = 0; i < 2 * STEPS; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[i][r] = starts != 0 ? 0.0f : keep * S[i][r];
+        const Frag<3> xf[2] = {split(X[0], X[1]), split(X[2], X[3])};
+        const Frag<3> of[2] = {split(dO[0], dO[1]), split(dO[2], dO[3])};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 2 * STEPS; ++i) {
+                Frag<N> kf = cols_frag<N, ROW>(Kl, j, g, m, state_cols4(i, m));
+                Frag<N> qf = cols_frag<N, ROW>(Ql, j, g, m, state_cols4(i, m));
+                if (any_sick) {
+                    drop_rows<N>(kf, j, g, drop);
+                    drop_rows<N>(qf, j, g, drop);
+                }
+                product<3>(S[i], qf, of[j]);
+                product<3>(S[i], kf, xf[j]);
+            }
+        if (any_sick) {
+            const bool dead = (sick & 1) != 0 && first_start > 0;
+#pragma unroll
+            for (int i = 0; i < 2 * STEPS; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[i][r] = dead ? __builtin_nanf("") : S[i][r];
+        }
+        lds_barrier();
+    }
+    if (a.d_initial_state) store_state(a.d_initial_state + bh * cells);
+}
+
+template <typename T, int KT, int NW, bool VEC>
+hipError_t launch(const DeltaArgs& a) {
+    const int cols = (a.vdim + 16 * NW - 1) / (16 * NW);
+    hipLaunchKernelGGL((bwd_states_kernel<T, KT, NW, VEC>), dim3(static_cast<unsigned>(a.batch * a.vheads * cols)),
+                       dim3(NW * 64), 0, a.stream, a, static_cast<int64_t>(delta_chunk_bytes()), cols);
+    return hipGetLastError();
+}
+
+template <typename T, bool VEC>
+hipError_t by_width(const DeltaArgs& a) {
+    return a.kdim > 64 ? launch<T, 128, 4, VEC>(a) : launch<T, 64, 4, VEC>(a);
+}
+
+}  // namespace
+
+hipError_t launch_delta_bwd_states(const DeltaArgs& a) {
+    if (a.bf16) return a.vec_k ? by_width<bf16_t, true>(a) : by_width<bf16_t, false>(a);
+    return a.vec_k ? by_width<float, true>(a) : by_width<float, false>(a);
+}
+
+}  // namespace mamba

@@ -43,6 +43,7 @@ struct DeltaArgs {
     float scale;
     bool bf16;
     bool vec_k;                 // q and k: 16-byte pieces of eight channels
+    bool vec_o;                 // dout and the states: the same
     hipStream_t stream;
 };
 

@@ -3,13 +3,15 @@
 //
 // With gamma the running sum of log decays and D[t,s] = exp(gamma_t - gamma_s) for s <= t
 // of one document, the values the chunk's tokens write obey
-//     u_t = beta_t (v_t - exp(gamma_t) S_in^T k_t) - sum_{s<t} A[t,s] u_s,   A[t,s] = beta_t D[t,s] k_t.k_s,
-// so U = T R with T = (I + A)^-1, a unit lower triangle.  One wave forms K K^T on the matrix cores,
-// solves the four 16 x 16 triangles on the diagonal by substitution (lane = column; with equal keys
+//     u_t = beta_t (v_t - exp(gamma_t) S_in^T k_t - sum_{s<t} D[t,s] k_t.k_s u_s),
+// so with M[t,s] = D[t,s] k_t.k_s (s < t), b = diag(beta) and R = V - exp(gamma) K S_in the errors are
+// E = (I + M b)^-1 R and U = b E; the backward needs (I + b M)^-T besides.  Both are unit triangles
+// (dbeta_t is E_t times a gradient: dividing U_t by beta_t instead fails where that is 0).
+// One wave forms K K^T on the matrix cores, solves the four 16 x 16 triangles on the diagonal by substitution (lane = column; with equal keys
 // and beta = 1 the powers of A that a doubling scheme adds up reach 10^17, a substitution's
 // terms stay at 1) and the blocks below them as T_ij = -T_ii sum_m A_im T_mj on the fp32 matrix
-// instructions, and writes T in three bf16 pieces in the order in which the later
-// passes' matrix instructions read it (and its transpose for the backward).
+// instructions, and writes the triangle in three bf16 pieces in the order in which the later
+// passes' matrix instructions read it.
 //
 // gamma is summed in float64 and kept as two floats: gamma_t - gamma_s is
 // then right to float32 of itself however far the sum has run.  A decay below
@@ -43,7 +45,6 @@ __global__ __launch_bounds__(64) void prepare_kernel(DeltaArgs a, size_t rec_byt
     __shared__ __align__(16) float As[C * kRowA];
     __shared__ __align__(16) float Td[4 * 16 * kRowD];
     __shared__ __align__(16) float hi[C], lo[C], bet[C], kk[C];
-    __shared__ __align__(16) int seg[C];
     constexpr int N = kPieces<T>, ESZ = sizeof(T);
     const int lane = threadIdx.x, g = lane >> 4, m = lane & 15;
     const int64_t id = blockIdx.x;
@@ -78,7 +79,6 @@ __global__ __launch_bounds__(64) void prepare_kernel(DeltaArgs a, size_t rec_byt
     const int last_seg = __popcll(starts);
     hi[lane] = h;
     lo[lane] = l;
-    seg[lane] = my_seg;
 
     // K K^T, lower tiles
     const T* kp = static_cast<const T*>(a.k);
@@ -134,117 +134,108 @@ __global__ __launch_bounds__(64) void prepare_kernel(DeltaArgs a, size_t rec_byt
     }
     __syncthreads();
 
-    // A into LDS: rows 4 g + r, columns m of each lower tile
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const f32x4 th = four(hi + 16 * i + 4 * g), tl = four(lo + 16 * i + 4 * g), tb = four(bet + 16 * i + 4 * g);
-        const int4 ts = *reinterpret_cast<const int4*>(seg + 16 * i + 4 * g);
-        const int tseg[4] = {ts.x, ts.y, ts.z, ts.w};
+    for (int which = 0; which < (BWD ? 2 : 1); ++which) {
+        // A = M b, or b M, into LDS: rows 4 g + r, columns m of each lower tile
 #pragma unroll
-        for (int j = 0; j <= i; ++j) {
-            const int s = 16 * j + m;
-            const float sh = hi[s], sl = lo[s];
-            const int ss = seg[s];
+        for (int i = 0; i < 4; ++i) {
+            const f32x4 th = four(hi + 16 * i + 4 * g), tl = four(lo + 16 * i + 4 * g), tb = four(bet + 16 * i + 4 * g);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = 16 * i + 4 * g + r;
-                const float d = exp2_fast((th[r] - sh) + (tl[r] - sl));
-                const bool on = s < t && ss == tseg[r] && !((bad >> t) & 1);
-                As[t * kRowA + s] = on ? tb[r] * (d * acc[i][j][r]) : 0.0f;
-            }
-        }
-    }
-    __syncthreads();
-
-    // The diagonal triangles: group g solves block g, lane m its column m.
-    {
-        float x[16];
-        const float* blk = As + (16 * g) * kRowA + 16 * g;
-#pragma unroll
-        for (int t = 0; t < 16; ++t) {
-            float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-            for (int q = 0; q < t; q += 4) {
-                const f32x4 row = four(blk + t * kRowA + q);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (q + e < t) {
-                        if (e & 1) s1 = __builtin_fmaf(row[e], x[q + e], s1);
-                        else s0 = __builtin_fmaf(row[e], x[q + e], s0);
-                    }
-            }
-            x[t] = (t == m ? 1.0f : 0.0f) - (s0 + s1);
-            Td[(16 * g + t) * kRowD + m] = x[t];
-        }
-    }
-    __syncthreads();
-
-    // The blocks below, one diagonal of blocks after the other.
-    f32x4 tri[4][4], diag[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) tri[i][i][r] = Td[(16 * i + 4 * g + r) * kRowD + m];
-        diag[i] = four(Td + (16 * i + m) * kRowD + 4 * g);
-    }
-#pragma unroll
-    for (int d = 1; d < 4; ++d)
-#pragma unroll
-        for (int j = 0; j + d < 4; ++j) {
-            const int i = j + d;
-            f32x4 x = {0, 0, 0, 0};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (k >= j && k < i) x = mfma_f32(four(As + (16 * i + m) * kRowA + 16 * k + 4 * g), tri[k][j], x);
-            f32x4 y = {0, 0, 0, 0};
-            y = mfma_f32(diag[i], x, y);
-            tri[i][j] = -y;
-        }
-    __syncthreads();
-
-    // T over A (zeros above the diagonal tiles and between documents), then out in pieces.
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int4 ts = *reinterpret_cast<const int4*>(seg + 16 * i + 4 * g);
-        const int tseg[4] = {ts.x, ts.y, ts.z, ts.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
+            for (int j = 0; j <= i; ++j) {
                 const int s = 16 * j + m;
-                const bool on = j <= i && seg[s] == tseg[r];
-                As[(16 * i + 4 * g + r) * kRowA + s] = on ? tri[i][j <= i ? j : i][r] : 0.0f;
+                const float sh = hi[s], sl = lo[s], sb = bet[s];
+                const int end = doc_end(starts, s);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = 16 * i + 4 * g + r;
+                    const float d = exp2_fast((th[r] - sh) + (tl[r] - sl));
+                    const bool on = s < t && t < end && !((bad >> t) & 1);
+                    As[t * kRowA + s] = on ? (which ? tb[r] : sb) * (d * acc[i][j][r]) : 0.0f;
+                }
             }
-    }
-    __syncthreads();
-    u32x4* out = reinterpret_cast<u32x4*>(a.solve + id * kSolveBytes);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j <= i / 2; ++j) {
-            const float* row = As + (16 * i + m) * kRowA + 32 * j + 4 * g;
-            const Frag<3> f = split(four(row), four(row + 16));
-            const int blk = i < 2 ? i : 2 + (i - 2) * 2 + j;
-#pragma unroll
-            for (int n = 0; n < 3; ++n) out[(blk * 3 + n) * 64 + lane] = f.p[n];
         }
-    if constexpr (BWD) {
-        u32x4* outt = reinterpret_cast<u32x4*>(a.solve_t + id * kSolveBytes);
+        __syncthreads();
+
+        // The diagonal triangles: group g solves block g, lane m its column m.
+        {
+            float x[16];
+            const float* blk = As + (16 * g) * kRowA + 16 * g;
+#pragma unroll
+            for (int t = 0; t < 16; ++t) {
+                float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+                for (int q = 0; q < t; q += 4) {
+                    const f32x4 row = four(blk + t * kRowA + q);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (q + e < t) {
+                            if (e & 1) s1 = __builtin_fmaf(row[e], x[q + e], s1);
+                            else s0 = __builtin_fmaf(row[e], x[q + e], s0);
+                        }
+                }
+                x[t] = (t == m ? 1.0f : 0.0f) - (s0 + s1);
+                Td[(16 * g + t) * kRowD + m] = x[t];
+            }
+        }
+        __syncthreads();
+
+        // The blocks below, one diagonal of blocks after the other.
+        f32x4 tri[4][4], diag[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) tri[i][i][r] = Td[(16 * i + 4 * g + r) * kRowD + m];
+            diag[i] = four(Td + (16 * i + m) * kRowD + 4 * g);
+        }
+#pragma unroll
+        for (int d = 1; d < 4; ++d)
+#pragma unroll
+            for (int j = 0; j + d < 4; ++j) {
+                const int i = j + d;
+                f32x4 x = {0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k >= j && k < i) x = mfma_f32(four(As + (16 * i + m) * kRowA + 16 * k + 4 * g), tri[k][j], x);
+                tri[i][j] = -mfma_f32(diag[i], x, f32x4{0, 0, 0, 0});
+            }
+        __syncthreads();
+
+        // The triangle over A (zeros above the diagonal tiles and between documents), then out in pieces.
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = i / 2; j < 2; ++j) {
-                f32x4 x, y;
+            for (int j = 0; j < 4; ++j) {
+                const int s = 16 * j + m, end = doc_end(starts, s);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[e] = As[(32 * j + 4 * g + e) * kRowA + 16 * i + m];
-                    y[e] = As[(32 * j + 16 + 4 * g + e) * kRowA + 16 * i + m];
+                for (int r = 0; r < 4; ++r) {
+                    const int t = 16 * i + 4 * g + r;
+                    As[t * kRowA + s] = j <= i && t < end ? tri[i][j <= i ? j : i][r] : 0.0f;
+                }
+            }
+        __syncthreads();
+        u32x4* out = reinterpret_cast<u32x4*>((which ? a.solve_t : a.solve) + id * kSolveBytes);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (which ? j < i / 2 : j > i / 2) continue;
+                f32x4 x, y;
+                if (which) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] = As[(32 * j + 4 * g + e) * kRowA + 16 * i + m];
+                        y[e] = As[(32 * j + 16 + 4 * g + e) * kRowA + 16 * i + m];
+                    }
+                } else {
+                    x = four(As + (16 * i + m) * kRowA + 32 * j + 4 * g);
+                    y = four(As + (16 * i + m) * kRowA + 32 * j + 16 + 4 * g);
                 }
                 const Frag<3> f = split(x, y);
-                const int blk = i < 2 ? i * 2 + j : 4 + (i - 2);
+                const int blk = which ? high_block(i, j) : low_block(i, j);
 #pragma unroll
-                for (int n = 0; n < 3; ++n) outt[(blk * 3 + n) * 64 + lane] = f.p[n];
+                for (int n = 0; n < 3; ++n) out[(blk * 3 + n) * 64 + lane] = f.p[n];
             }
+        __syncthreads();
     }
 }
 

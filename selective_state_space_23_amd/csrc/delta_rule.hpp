@@ -195,6 +195,110 @@ __device__ __forceinline__ void store_one(Rsrc rs, uint32_t off, float v) {
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rs, off, 0, 0);
 }
 
+// A chunk of q or k on its way to LDS as [pieces][C][KT + 8] bf16: 16-byte pieces of 16
+// rows meet no bank twice.
+template <typename T, int KT, int THREADS, bool VEC> struct Tile {
+    static constexpr int N = kPieces<T>, ROW = KT + 8, PER = C * KT / 8 / THREADS;
+    static constexpr size_t kBytes = size_t(N) * C * ROW * 2;
+    Eight<T, VEC> raw[PER];
+    __device__ __forceinline__ void fetch(Rsrc rs, int64_t ld, int width, int tid) {
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+            const int x = p * THREADS + tid, t = x / (KT / 8), ch = x % (KT / 8) * 8;
+            raw[p].load(rs, static_cast<uint32_t>(t * ld * sizeof(T)), ch, width);
+        }
+    }
+    __device__ __forceinline__ void land(uint16_t* lds, int tid) const {
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+            const int x = p * THREADS + tid, t = x / (KT / 8), ch = x % (KT / 8) * 8;
+            const Frag<N> f = raw[p].frag();
+#pragma unroll
+            for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(lds + (i * C + t) * ROW + ch) = f.p[i];
+        }
+    }
+    // The same with the rows of `out` as zeros.
+    __device__ __forceinline__ void land_without(uint16_t* lds, int tid, uint64_t out) const {
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+            const int x = p * THREADS + tid, t = x / (KT / 8), ch = x % (KT / 8) * 8;
+            const Frag<N> f = raw[p].frag();
+            const uint32_t on = (out >> t) & 1 ? 0u : ~0u;
+#pragma unroll
+            for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(lds + (i * C + t) * ROW + ch) = f.p[i] & on;
+        }
+    }
+};
+
+// Operands from such a tile: row `row`, eight channels from `ch` on ...
+template <int N, int ROW>
+__device__ __forceinline__ Frag<N> rows_frag(const uint16_t* lds, int row, int ch) {
+    Frag<N> f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) f.p[i] = *reinterpret_cast<const u32x4*>(lds + (i * C + row) * ROW + ch);
+    return f;
+}
+// ... or column `col` of rows 32 j + 4 g + 0..3 and 16 further, by transposing reads: 16 lanes
+// read four rows of 16 columns, lane m giving the address of row m / 4, columns `col4`.. + 3, and
+// getting the m-th of the 16 columns.
+template <int N, int ROW>
+__device__ __forceinline__ Frag<N> cols_frag(const uint16_t* lds, int j, int g, int m, int col4) {
+    Frag<N> f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint16_t* at = lds + (i * C + 32 * j + 4 * g + m / 4) * ROW + col4;
+        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at));
+        const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + 16 * ROW));
+        const u32x2 xw = __builtin_bit_cast(u32x2, x), yw = __builtin_bit_cast(u32x2, y);
+        f.p[i] = u32x4{xw[0], xw[1], yw[0], yw[1]};
+    }
+    return f;
+}
+// Zeros in the slots of the rows of `out`.
+template <int N>
+__device__ __forceinline__ void drop_rows(Frag<N>& f, int j, int g, uint64_t out) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int s = 32 * j + (e < 4 ? 4 * g + e : 12 + 4 * g + e);
+        const uint32_t mask = (out >> s) & 1 ? (e & 1 ? 0x0000ffffu : 0xffff0000u) : 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < N; ++i) f.p[i][e / 2] &= mask;
+    }
+}
+
+// The channel of a state that row 4 g + r of tile i stands for: with it an operand of 32
+// contracted channels reads 8 consecutive ones of a row of q or k.
+__device__ __forceinline__ int state_row(int i, int g, int r) { return 32 * (i / 2) + 8 * g + 4 * (i % 2) + r; }
+__device__ __forceinline__ int state_cols4(int i, int m) { return 32 * (i / 2) + 8 * (m % 4) + 4 * (i % 2); }
+
+// The 6 pieces of a triangle's operand order: rows of tile i, columns 32 j .. 32 j + 31
+__device__ __forceinline__ constexpr int low_block(int i, int j) { return i < 2 ? i : 2 + (i - 2) * 2 + j; }
+__device__ __forceinline__ constexpr int high_block(int i, int j) { return i < 2 ? i * 2 + j : i + 2; }   // of its transpose
+
+// The thread, formed where it is used: offsets of every phase held across the loops around them
+// overflow the registers.
+__device__ __forceinline__ int thread_now() {
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+}
+
+__device__ __forceinline__ uint64_t uniform(uint64_t x) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(x));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<int>(x >> 32));
+    return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+
+// The first token of t's document, as far as the chunk holds it, and the end of s's.
+__device__ __forceinline__ int doc_first(uint64_t starts, int t) {
+    const uint64_t at = starts & (~0ull >> (63 - t));
+    return at ? 63 - __builtin_clzll(at) : 0;
+}
+__device__ __forceinline__ int doc_end(uint64_t starts, int s) {
+    const uint64_t at = starts >> s >> 1;
+    return at ? s + 1 + __builtin_ctzll(at) : C;
+}
+
 // Bits from each set bit of `m` up to the end of its document (next bit of `starts`).
 __device__ __forceinline__ uint64_t smear(uint64_t m, uint64_t starts) {
     uint64_t walls = starts;
@@ -202,6 +306,18 @@ __device__ __forceinline__ uint64_t smear(uint64_t m, uint64_t starts) {
     for (int s = 1; s < 64; s *= 2) {
         m |= (m << s) & ~walls;
         walls |= walls << s;
+    }
+    return m;
+}
+
+// Bits of the whole documents that a set bit of `m` lies in.
+__device__ __forceinline__ uint64_t whole(uint64_t m, uint64_t starts) {
+    m = smear(m, starts);
+    uint64_t walls = starts >> 1;   // a start at t + 1 ends the document of t
+#pragma unroll
+    for (int s = 1; s < 64; s *= 2) {
+        m |= (m >> s) & ~walls;
+        walls |= walls >> s;
     }
     return m;
 }

@@ -36,18 +36,18 @@ __device__ __forceinline__ f32x4 over_rows(f32x4 x, f32x4 (*red)[COLS], int wave
     for (int s = COLS; s < 64; s *= 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] += __shfl_xor(x[e], s);
-    if (lane < COLS) red[wave][lane] = x;
-    __syncthreads();
     const int c = lane % COLS;
+    red[wave][c] = x;   // the same from all lanes of a column
+    __syncthreads();
     return (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
 }
 
 template <typename T, int KT, int COLS, bool VEC>
 __global__ __launch_bounds__(256) void step_kernel(StepArgs a) {
     constexpr int R = KT * COLS / 256;   // rows a thread
-    __shared__ __align__(16) float kv[KT], qv[KT];
+    __shared__ __align__(16) float kv[128], qv[128];
     __shared__ __align__(16) f32x4 red[2][4][COLS];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t bh = blockIdx.x / a.cols;
     const int hv = static_cast<int>(bh % a.vheads), hk = hv / (a.vheads / a.kheads);
     const int64_t b = bh / a.vheads;
@@ -86,14 +86,14 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a) {
             for (int e = 0; e < 4; ++e)
                 vals[e] = one_value<T>(load_one<T>(vr, static_cast<uint32_t>((v0 + e) * sizeof(T))));
         }
-        if (tid < KT) {
-            const Rsrc kr = rsrc(static_cast<const T*>(a.k) + tok * a.ld_k + static_cast<int64_t>(hk) * a.kdim,
-                                 a.kdim * static_cast<int>(sizeof(T)));
-            kv[tid] = one_value<T>(load_one<T>(kr, static_cast<uint32_t>(tid * sizeof(T))));
-        } else if (tid >= 128 && tid < 128 + KT) {
-            const Rsrc qr = rsrc(static_cast<const T*>(a.q) + tok * a.ld_q + static_cast<int64_t>(hk) * a.kdim,
-                                 a.kdim * static_cast<int>(sizeof(T)));
-            qv[tid - 128] = one_value<T>(load_one<T>(qr, static_cast<uint32_t>((tid - 128) * sizeof(T))));
+        {   // k by the first two waves, q by the others
+            const bool key = wave < 2;
+            const int ch = tid & 127;
+            const Rsrc r = key ? rsrc(static_cast<const T*>(a.k) + tok * a.ld_k + static_cast<int64_t>(hk) * a.kdim,
+                                      a.kdim * static_cast<int>(sizeof(T)))
+                               : rsrc(static_cast<const T*>(a.q) + tok * a.ld_q + static_cast<int64_t>(hk) * a.kdim,
+                                      a.kdim * static_cast<int>(sizeof(T)));
+            (key ? kv : qv)[ch] = one_value<T>(load_one<T>(r, static_cast<uint32_t>(ch * sizeof(T))));
         }
         __syncthreads();
         float kr[R], qr[R];

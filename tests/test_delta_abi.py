@@ -34,6 +34,15 @@ def fwd(lib, d=None, ws_bytes=1 << 26, **kw):
                                           None)
 
 
+def bwd(lib, d=None, ws_bytes=1 << 28, **kw):
+    at = dict(AT, **kw)
+    d = d or dims()
+    return lib.mamba_gated_delta_rule_bwd(
+        ctypes.byref(d), at["q"], at["k"], at["v"], at["g"], at["beta"], at["doc"], at["initial"], at["states"],
+        at["dout"], at["dfinal"], at["dq"], at["dk"], at["dv"], at["dg"], at["dbeta"], at["dinit"], at["ws"], ws_bytes,
+        None)
+
+
 def update(lib, d=None, **kw):
     at = dict(AT, **kw)
     d = d or dims(seqlen=1)
@@ -56,11 +65,12 @@ LONG = [(dict(seqlen=-1), INVALID), (dict(seqlen=3000001), UNSUPPORTED),
 
 @pytest.mark.parametrize("kw,status", BAD_DIMS + LONG, ids=lambda v: str(v))
 def test_dims(lib, kw, status):
-    assert fwd(lib, dims(**kw)) == status
+    assert fwd(lib, dims(**kw)) == status and bwd(lib, dims(**kw)) == status
     if (kw, status) in BAD_DIMS:
         assert update(lib, dims(**dict(kw, seqlen=1))) == status
     n = ctypes.c_size_t(7)
     assert lib.mamba_gated_delta_rule_workspace_bytes(ctypes.byref(dims(**kw)), ctypes.byref(n)) == status
+    assert lib.mamba_gated_delta_rule_bwd_workspace_bytes(ctypes.byref(dims(**kw)), 0, ctypes.byref(n)) == status
     assert n.value == 0
 
 
@@ -72,6 +82,15 @@ def test_workspace(lib):
     assert query(ctypes.byref(dims()), ctypes.byref(n)) == 0 and n.value > 0
     assert fwd(lib, ws_bytes=n.value - 1) == WORKSPACE and fwd(lib, ws=None) == WORKSPACE
     assert fwd(lib, ws=AT["ws"] + 64) == MISALIGNED
+    query = lib.mamba_gated_delta_rule_bwd_workspace_bytes
+    assert query(ctypes.byref(dims(batch=0)), 0, ctypes.byref(n)) == 0 and n.value == 0
+    assert query(ctypes.byref(dims()), 0, None) == INVALID and query(None, 0, ctypes.byref(n)) == INVALID
+    assert query(ctypes.byref(dims()), 0, ctypes.byref(n)) == 0
+    without = n.value
+    assert query(ctypes.byref(dims()), 1, ctypes.byref(n)) == 0 and 0 < n.value < without
+    assert bwd(lib, ws_bytes=n.value - 1) == WORKSPACE and bwd(lib, ws=None) == WORKSPACE
+    assert bwd(lib, states=None, ws_bytes=without - 1) == WORKSPACE
+    assert bwd(lib, ws=AT["ws"] + 64) == MISALIGNED
 
 
 def test_required_pointers(lib):
@@ -79,6 +98,10 @@ def test_required_pointers(lib):
         assert fwd(lib, **{k: None}) == INVALID, k
     for k in ("state", "q", "k", "v", "beta", "out"):
         assert update(lib, **{k: None}) == INVALID, k
+    for k in ("q", "k", "v", "beta", "dout", "dq", "dk", "dv", "dbeta"):
+        assert bwd(lib, **{k: None}) == INVALID, k
+    assert bwd(lib, g=None) == INVALID and bwd(lib, dg=None) == INVALID      # dg exactly with g
+    assert bwd(lib, initial=None) == INVALID                                 # d_initial_state without initial_state
     assert update(lib, dims(seqlen=2)) == INVALID and update(lib, dims(seqlen=0)) == INVALID
 
 
@@ -89,6 +112,10 @@ def test_alignment(lib):
         assert update(lib, **{k: AT[k] + 1}) == MISALIGNED, k
     for k in ("g", "beta", "initial", "final", "states"):
         assert fwd(lib, **{k: AT[k] + 2}) == MISALIGNED, k
+    for k in ("q", "k", "v", "dout", "dq", "dk", "dv"):
+        assert bwd(lib, **{k: AT[k] + 1}) == MISALIGNED, k
+    for k in ("g", "beta", "initial", "states", "dfinal", "dg", "dbeta", "dinit"):
+        assert bwd(lib, **{k: AT[k] + 2}) == MISALIGNED, k
     for k in ("g", "beta", "state"):
         assert update(lib, **{k: AT[k] + 2}) == MISALIGNED, k
 
@@ -98,6 +125,10 @@ def test_overlap(lib):
         for o in ("out", "final", "states", "ws"):
             assert fwd(lib, **{k: AT[o]}) == INVALID, (k, o)
     assert fwd(lib, out=AT["states"]) == INVALID and fwd(lib, final=AT["ws"]) == INVALID
+    for k in ("q", "k", "v", "g", "beta", "doc", "initial", "states", "dout", "dfinal"):
+        for o in ("dq", "dk", "dv", "dg", "dbeta", "dinit", "ws"):
+            assert bwd(lib, **{k: AT[o]}) == INVALID, (k, o)
+    assert bwd(lib, dq=AT["dk"]) == INVALID and bwd(lib, dinit=AT["dbeta"]) == INVALID
     # a strided input ends where its last token does
     assert fwd(lib, dims(ld_q=256), out=AT["q"] + 2 * 600 * 200) == INVALID
     for k in ("q", "k", "v", "g", "beta", "reset"):
@@ -112,6 +143,9 @@ def test_empty_calls(lib):
     assert fwd(lib, dims(batch=0), q=None, out=None) == 0
     assert fwd(lib, dims(seqlen=0), final=None) == 0
     assert fwd(lib, dims(seqlen=0), final=AT["initial"]) == INVALID
+    assert bwd(lib, dims(batch=0), q=None, dq=None) == 0
+    assert bwd(lib, dims(seqlen=0), dinit=None) == 0
+    assert bwd(lib, dims(seqlen=0), dinit=AT["dfinal"]) == INVALID
     assert update(lib, dims(seqlen=1, batch=0), state=None) == 0
 
 

@@ -30,14 +30,14 @@ def ssm():
     return s
 
 
-def close(got, ref, what, bf16=False):
-    """bf16: an output in bfloat16."""
+def close(got, ref, what, bf16=False, scale=1.0):
+    """bf16: an output in bfloat16; scale: of the floor."""
     got = to_host(got)
     assert got.shape == ref.shape, (what, got.shape, ref.shape)
     assert np.isfinite(got).all(), f"{what}: non-finite"
     if got.size == 0:
         return
-    tol = (2.0 ** -8 if bf16 else 2.0 ** -24) * np.abs(ref) + (2e-4 if bf16 else 5e-5) * np.sqrt(np.mean(ref ** 2))
+    tol = (2.0 ** -8 if bf16 else 2.0 ** -24) * np.abs(ref) + scale * (2e-4 if bf16 else 5e-5) * np.sqrt(np.mean(ref ** 2))
     err = np.abs(got - ref)
     i = np.unravel_index(np.argmax(err - tol), err.shape)
     assert (err <= tol).all(), f"{what}: {int((err > tol).sum())} of {err.size} off, worst at {i}: {got[i]} for {ref[i]}"
@@ -195,6 +195,129 @@ def test_lost_state_and_its_end(ssm):
     assert np.isnan(S[0, 0, :, 2]).all() and np.isfinite(np.delete(S, 2, -1)).all()
 
 
+def backward(ssm, t, **kw):
+    return ssm.gated_delta_rule_bwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["dout"], t["doc_start"],
+                                    initial_state=t["initial_state"], d_final_state=t["d_final_state"], **kw)
+
+
+IO = ("dq", "dk", "dv")
+
+
+@pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("shape", SHAPES, ids=ids)
+def test_backward(ssm, shape, saved):
+    """The gradients' own sums are as long as the forward's, and one chain of them follows another: twice its
+    bound.  dg sums differences of two dot products over the rest of its chunk: its terms' rms sets
+    the scale, not what is left of them."""
+    B, L, Hk, Hv, K, V, dtype, docs, carry = shape
+    d = draw(B, L, Hk, Hv, K, V, dtype, docs, carry, seed=L + 1)
+    t = dev(d, dtype)
+    states = forward(ssm, t, save="states")[2]["states"] if saved else None
+    got = backward(ssm, t, states=states)
+    ref = R.gated_delta_rule_bwd(**{n: d[n] for n in FWD}, dout=d["dout"], d_final_state=d["d_final_state"])
+    assert set(got) == set(ref)
+    out = R.gated_delta_rule(**{n: d[n] for n in FWD})[0]
+    terms = np.abs(d["dout"] * out).sum(-1) + np.abs(ref["dv"] * d["v"]).sum(-1)
+    for n in ref:
+        if n == "dg":
+            err = np.abs(to_host(got[n]) - ref[n])
+            assert (err <= 1e-4 * (np.sqrt(np.mean(ref[n] ** 2)) + np.sqrt(np.mean(terms ** 2)))).all(), err.max()
+        else:
+            close(got[n], ref[n], n, n in IO and dtype == "bf16", 2.0)
+
+
+def test_backward_of_slices_without_decay(ssm):
+    import torch
+
+    d = draw(2, 150, 2, 4, 32, 24, "bf16", 40, True, seed=6)
+    t = dev(d, "bf16")
+    plain = backward(ssm, t)
+    for pad in (0, 1):
+        proj = torch.full((2, 150, 2 * 64 + 2 * 96 + pad), float("nan"), dtype=torch.bfloat16, device="cuda")
+        cut, at = dict(t), 0
+        for n, w in (("q", 64), ("k", 64), ("v", 96), ("dout", 96)):
+            proj[..., at:at + w] = t[n].flatten(-2)
+            cut[n] = proj[..., at:at + w].unflatten(-1, t[n].shape[-2:])
+            at += w
+        got = backward(ssm, cut)
+        assert all(torch.equal(got[n], plain[n]) for n in plain)
+    d["g"] = None
+    got = backward(ssm, dev(d, "bf16"))
+    ref = R.gated_delta_rule_bwd(**{n: d[n] for n in FWD}, dout=d["dout"], d_final_state=d["d_final_state"])
+    assert "dg" not in got
+    for n in got:
+        close(got[n], ref[n], n, n in IO, 2.0)
+
+
+def test_backward_in_two_pieces(ssm):
+    """A row cut at a token inside a chunk and differentiated back to front."""
+    d = draw(2, 190, 1, 2, 48, 32, "f32", 60, True, seed=14)
+    t = dev(d, "f32")
+    ref = R.gated_delta_rule_bwd(**{n: d[n] for n in FWD}, dout=d["dout"], d_final_state=d["d_final_state"])
+    seq = ("q", "k", "v", "g", "beta", "doc_start", "dout")
+    head = {n: x[:, :83].contiguous() if n in seq else x for n, x in t.items()}
+    tail = {n: x[:, 83:].contiguous() if n in seq else x for n, x in t.items()}
+    tail["initial_state"] = forward(ssm, head)[1]
+    g2 = backward(ssm, tail)
+    head["d_final_state"] = g2["d_initial_state"]
+    g1 = backward(ssm, head)
+    for n in ("dq", "dk", "dv", "dbeta"):
+        close(g1[n], ref[n][:, :83], n + " head", scale=3.0)
+        close(g2[n], ref[n][:, 83:], n + " tail", scale=3.0)
+    close(g1["d_initial_state"], ref["d_initial_state"], "d_initial_state", scale=3.0)
+
+
+def test_gradients_by_differences(ssm):
+    """Along random directions: (f(x + e d) - f(x - e d)) / 2 e in float32.  f sums 2 x 70 x 2 x 16 products to
+    some 50 of rms; its rounding, 2^-22 of that a side, over e = 1/64 is 8e-4, the third order below it."""
+    import torch
+
+    d = draw(2, 70, 1, 2, 32, 16, "f32", 25, True, seed=15)
+    t = dev(d, "f32")
+    grads = backward(ssm, t)
+
+    def f(x):
+        out, S = forward(ssm, x)
+        return (out.double() * t["dout"].double()).sum().item() + (S.double() * t["d_final_state"].double()).sum().item()
+
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    for n in ("q", "k", "v", "g", "beta", "initial_state"):
+        dirn = torch.randn(t[n].shape, generator=gen, device="cuda")
+        dirn /= dirn.norm()
+        e = 1 / 64
+        num = (f(dict(t, **{n: t[n] + e * dirn})) - f(dict(t, **{n: t[n] - e * dirn}))) / (2 * e)
+        got = (grads["d_" + n if n == "initial_state" else "d" + n].double() * dirn.double()).sum().item()
+        assert abs(num - got) <= 5e-3 * max(1.0, abs(num)), (n, num, got)
+
+
+@pytest.mark.parametrize("where", ["q", "k", "v", "g", "beta", "dout", "initial_state", "d_final_state"])
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_backward_not_finite_stays_in_its_document(ssm, where, value, dtype):
+    L, at = 200, 100
+    d = draw(2, L, 1, 2, 32, 24, dtype, seed=16, carry=True)
+    d["doc_start"] = np.zeros((2, L), np.uint8)
+    d["doc_start"][:, [30, 85, 110, 111, 190]] = 1
+    ref = R.gated_delta_rule_bwd(**{n: d[n] for n in FWD}, dout=d["dout"], d_final_state=d["d_final_state"])
+    bad = {n: None if x is None else x.copy() for n, x in d.items()}
+    if "state" in where:
+        bad[where][0, 0, 3, 5] = value
+        first, last = (0, 30) if where == "initial_state" else (190, L)
+    else:
+        bad[where][(0, at, 0) if where in ("g", "beta") else (0, at, 0, 3)] = value
+        first, last = 85, 110
+    got = backward(ssm, dev(bad, dtype))
+    clean = np.ones((2, L), bool)
+    clean[0, first:last] = False
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        x, r = to_host(got[n]), ref[n]
+        tol = (2.0 ** -8 if dtype == "bf16" and n in IO else 0.0) * np.abs(r) + 4e-4 * np.sqrt(np.mean(r ** 2))
+        assert (np.abs(x - r) <= tol)[clean].all(), n
+    assert not np.isfinite(to_host(got["dk"])[0, first:last]).all()
+    if first > 0:
+        close(got["d_initial_state"], ref["d_initial_state"], "d_initial_state", scale=2.0)
+
+
 STEPS = [(2, 12, 12, 128, 128, "bf16"), (3, 1, 3, 100, 75, "f32"), (1, 1, 1, 1, 1, "f32"), (5, 2, 4, 33, 64, "bf16"),
          (40, 4, 16, 64, 128, "bf16"), (600, 1, 1, 128, 96, "f32"), (520, 1, 1, 17, 21, "bf16")]
 
@@ -243,6 +366,8 @@ def test_empty(ssm):
     t = dev(d, "f32")
     out, S = forward(ssm, t)
     assert out.shape == (2, 0, 2, 8) and torch.equal(S, t["initial_state"])
+    g = backward(ssm, t)
+    assert torch.equal(g["d_initial_state"], t["d_final_state"]) and g["dq"].shape == (2, 0, 1, 8)
     t["initial_state"] = None
     out, S = forward(ssm, t, final_state=torch.full((2, 2, 8, 8), float("nan"), device="cuda"))
     assert torch.equal(S, torch.zeros_like(S))
