@@ -25,7 +25,8 @@
  * (mamba_causal_conv1d_bwd, mamba_selective_scan_bwd), a gated linear recurrence
  * (forward, backward, one-token step: mamba_gated_recurrence_*), 8-bit
  * activation checkpoints (mamba_activation_pack, mamba_activation_unpack) and a
- * gated delta rule (forward, backward, one-token step: mamba_gated_delta_rule_*), each
+ * gated delta rule (forward, backward, one-token step: mamba_gated_delta_rule_*) with the
+ * head norms and rotation of its queries and keys (mamba_qk_norm_rotary_*), each
  * described at its declaration below.
  *
  * Conventions shared by every entry point
@@ -601,6 +602,66 @@ int mamba_gated_delta_rule_bwd(const mamba_delta_dims_t* dims, const void* q, co
 int mamba_gated_delta_rule_update(const mamba_delta_dims_t* dims, float* state, const void* q, const void* k,
                                   const void* v, const float* g, const float* beta, const uint8_t* reset, void* out,
                                   void* stream);
+
+/* ---- Norms of queries and keys for each head, with the position rotation in the
+ * same pass: what stands between the conv and the delta rule, whose keys are to have
+ * norm 1 at most.  Per token and head of q and of k, x (D,):
+ *   y = x w (mean(x^2) + eps)^-1/2 (MAMBA_NORM_RMS) or x w (sum(x^2) + eps)^-1/2
+ *   (MAMBA_NORM_L2), w = 1 without a weight; then the first rotary_dim channels in
+ *   pairs (i, i + rotary_dim / 2), or (2i, 2i + 1) with `interleaved`:
+ *   (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s), c and s the i-th of the tables' row
+ *   at the token's position. */
+enum { MAMBA_NORM_RMS = 0, MAMBA_NORM_L2 = 1 };
+typedef struct {
+    int64_t batch;       /* B                                                       */
+    int64_t seqlen;      /* L (1: one token of each row)                            */
+    int32_t q_heads;     /* Hq                                                      */
+    int32_t k_heads;     /* Hk, or 0: queries alone (k and what belongs to it NULL) */
+    int32_t head_dim;    /* D, 1..256                                               */
+    int32_t rotary_dim;  /* R, even, 0 (no rotation) .. D                           */
+    int64_t table_rows;  /* rows of cos and sin (ignored without rotation)          */
+    int64_t ld_q;        /* elements between two tokens of q, of k and (backward)   */
+    int64_t ld_k;        /* of the gradients at the outputs: 0 for dense, else at   */
+    int64_t ld_dq_out;   /* least Hq D (Hk D); tokens of two rows follow each other */
+    int64_t ld_dk_out;   /* at the same distance.                                   */
+    int32_t dtype;       /* mamba_dtype_t of q, k, outputs and their gradients      */
+    int32_t norm;        /* MAMBA_NORM_*                                            */
+    int32_t interleaved; /* nonzero: pairs of neighbours                            */
+    float eps;           /* finite, >= 0 (0: a head of zeros gives NaN)             */
+} mamba_qk_norm_dims_t;
+
+/* Forward.
+ *   q (B, L, Hq, D), k (B, L, Hk, D): `dtype`, strides in dims.
+ *   q_weight, k_weight (D,) float32 or NULL, each on its own.
+ *   cos, sin   (table_rows, R / 2) float32; NULL exactly when R is 0.
+ *   positions  (B, L) int32 rows of the tables, or NULL: the token's index in its row
+ *              (L <= table_rows then).  A position outside the tables gives NaN in the
+ *              rotated channels.
+ *   q_out, k_out: dense, `dtype`.
+ * Supported: D up to 256, heads times D up to 2^21, strides up to 2^40, B L below 2^31.
+ * Arithmetic is float32, outputs are rounded once.  Any alignment to the element size; D and
+ * R multiples of 8 with everything aligned to 16 bytes selects the vectorised kernels.
+ * Outputs must not overlap anything else of the call. */
+int mamba_qk_norm_rotary_fwd(const mamba_qk_norm_dims_t* dims, const void* q, const void* k, const float* q_weight,
+                             const float* k_weight, const float* cos, const float* sin, const int32_t* positions,
+                             void* q_out, void* k_out, void* stream);
+
+/* Bytes of device workspace mamba_qk_norm_rotary_bwd needs with weights (0 without:
+ * NULL will do). */
+int mamba_qk_norm_rotary_bwd_workspace_bytes(const mamba_qk_norm_dims_t* dims, size_t* bytes);
+
+/* Backward: the gradients of sum(dq_out q_out) + sum(dk_out k_out).
+ *   dims ... positions: as the forward call.  dq_out (B, L, Hq, D), dk_out (B, L, Hk, D).
+ *   dq, dk     dense, `dtype`.
+ *   dq_weight, dk_weight (D,) float32, non-NULL exactly when the weight is: sums over all
+ *              tokens and heads.
+ *   workspace  at least mamba_qk_norm_rotary_bwd_workspace_bytes, 256-byte aligned.
+ * With no tokens the weights' gradients are 0.  Repeated calls give bitwise identical
+ * results. */
+int mamba_qk_norm_rotary_bwd(const mamba_qk_norm_dims_t* dims, const void* q, const void* k, const float* q_weight,
+                             const float* k_weight, const float* cos, const float* sin, const int32_t* positions,
+                             const void* dq_out, const void* dk_out, void* dq, void* dk, float* dq_weight,
+                             float* dk_weight, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

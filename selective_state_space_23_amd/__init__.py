@@ -29,6 +29,10 @@ missing or the tensors are not on a GPU the calls raise.
     dx, dweight, dbias = causal_conv1d_bwd(p, weight, du, bias, doc_start)
     u = activation_unpack(activation_pack(u), torch.bfloat16)          # e.g. for selective_scan_bwd
 
+    # queries and keys normed per head and rotated by their positions, for the delta rule
+    q, k = qk_norm_rotary_fwd(q_in, k_in, cos=cos, sin=sin, positions=positions, norm="l2")
+    grads = qk_norm_rotary_bwd(q_in, k_in, dq, dk, cos=cos, sin=sin, positions=positions, norm="l2")
+
     # gated delta rule: a K x V state per head, q and k (B, L, Hk, K), v (B, L, Hv, V), g and beta (B, L, Hv)
     out, S, kept = gated_delta_rule_fwd(q, k, v, g, beta, doc_start, save="states")
     grads = gated_delta_rule_bwd(q, k, v, g, beta, dout, doc_start, states=kept["states"])
@@ -64,6 +68,8 @@ __all__ = [
     "PackedActivation",
     "activation_pack",
     "activation_unpack",
+    "qk_norm_rotary_fwd",
+    "qk_norm_rotary_bwd",
     "gated_delta_rule_fwd",
     "gated_delta_rule_bwd",
     "gated_delta_rule_update",
@@ -1055,3 +1061,96 @@ def gated_delta_rule_update(state, q, k, v, g, beta, reset=None, scale=None, out
         _ptr(out, "out", dev, dt, (Bt, Hv, V)))
     _lib.check(st, "mamba_gated_delta_rule_update")
     return out
+
+
+def _qk_norm_call(q, k, q_weight, k_weight, cos, sin, positions, norm, eps, interleaved, grads=()):
+    """(dims, pointers of the inputs, device, lead, shapes of q and k) of a head norm's call; ``grads``: the gradients
+    at the outputs."""
+    torch = _torch()
+    dev = _check_device(q)
+    if q.dim() < 3:
+        raise ValueError("q must be (B, L, Hq, D) or (B, Hq, D)")
+    if norm not in _lib.NORMS:
+        raise ValueError(f"norm must be one of {sorted(_lib.NORMS)}")
+    code, dt, f32 = _dtype_code(q), q.dtype, torch.float32
+    lead, (Hq, D) = q.shape[:-2], q.shape[-2:]
+    if len(lead) > 2:
+        raise ValueError("q must be (B, L, Hq, D) or (B, Hq, D)")
+    Hk = 0 if k is None else k.shape[-2]
+    shapes = (q.shape, None if k is None else lead + (Hk, D))
+    pq, lq = _heads(q, "q", dev, dt, shapes[0])
+    pk, lk = _heads(k, "k", dev, dt, shapes[1])
+    lds, pg = [0, 0], [None, None]
+    for i, (t, n) in enumerate(zip(grads, ("dq_out", "dk_out"))):
+        if (t is None) != (shapes[i] is None):
+            raise ValueError(f"{n} goes with its input")
+        pg[i], lds[i] = _heads(t, n, dev, dt, shapes[i])
+    rot, table = 0, None
+    if cos is not None:
+        if cos.dim() != 2:
+            raise ValueError("cos must be (rows, R / 2)")
+        table = cos.shape
+        rot = 2 * table[1]
+    elif sin is not None:
+        raise ValueError("cos and sin go together")
+    dims = _lib.QkNormDims(lead[0], lead[1] if len(lead) == 2 else 1, Hq, Hk, D, rot, 0 if table is None else table[0],
+                           lq, lk, *lds, code, _lib.NORMS[norm], int(bool(interleaved)), eps)
+    ptrs = (pq, pk, _ptr(q_weight, "q_weight", dev, f32, (D,)), _ptr(k_weight, "k_weight", dev, f32, (D,)),
+            _ptr(cos, "cos", dev, f32, table), _ptr(sin, "sin", dev, f32, table),
+            _ptr(positions, "positions", dev, torch.int32, lead))
+    return dims, ptrs + tuple(pg[:len(grads)]), dev, shapes
+
+
+def qk_norm_rotary_fwd(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, norm="rms", eps=1e-6,
+                       interleaved=False, q_out=None, k_out=None):
+    """Norms of queries and keys for each head, with the position rotation; see
+    mamba_qk_norm_rotary_fwd.
+
+    q (B, L, Hq, D) and k (B, L, Hk, D), or (B, Hq, D) and (B, Hk, D) for one token of
+    each row, float32/bfloat16, dense or slices of one projection's output; k may be None.
+    q_weight, k_weight (D,) float32 or None; cos, sin (rows, R / 2) float32 or None: no
+    rotation; positions (B, L) or (B,) int32 (None: a token's index in its row).  ``norm``:
+    "rms" (mean of squares) or "l2" (their sum); ``interleaved``: pairs of neighbouring
+    channels, else of the two halves.  Returns (q_out, k_out), dense."""
+    torch = _torch()
+    dims, ptrs, dev, shapes = _qk_norm_call(q, k, q_weight, k_weight, cos, sin, positions, norm, eps, interleaved)
+    if q_out is None:
+        q_out = torch.empty(shapes[0], dtype=q.dtype, device=dev)
+    if k_out is None and k is not None:
+        k_out = torch.empty(shapes[1], dtype=q.dtype, device=dev)
+    st = _launch(dev, _lib.load().mamba_qk_norm_rotary_fwd, ctypes.byref(dims), *ptrs,
+                 _ptr(q_out, "q_out", dev, q.dtype, shapes[0]), _ptr(k_out, "k_out", dev, q.dtype, shapes[1]))
+    _lib.check(st, "mamba_qk_norm_rotary_fwd")
+    return q_out, k_out
+
+
+def qk_norm_rotary_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
+                       norm="rms", eps=1e-6, interleaved=False, workspace=None, grads=None):
+    """Gradients of sum(dq_out * q_out) + sum(dk_out * k_out) for qk_norm_rotary_fwd on
+    the same arguments; see mamba_qk_norm_rotary_bwd.  dq_out, dk_out: shaped as q and k,
+    dense or slices.  Returns a dict with dq, dk (with a k) and, for each weight given,
+    dq_weight, dk_weight (D,) float32.  ``grads``: optional dict of preallocated outputs
+    with the same keys."""
+    torch = _torch()
+    dims, ptrs, dev, shapes = _qk_norm_call(q, k, q_weight, k_weight, cos, sin, positions, norm, eps, interleaved,
+                                            (dq_out, dk_out))
+    want = {"dq": (shapes[0], q.dtype)}
+    if k is not None:
+        want["dk"] = (shapes[1], q.dtype)
+    for n, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
+        if w is not None:
+            want[n] = (q.shape[-1:], torch.float32)
+    res = dict(grads) if grads else {}
+    for n, (sh, d) in want.items():
+        if n not in res:
+            res[n] = torch.empty(sh, dtype=d, device=dev)
+    lib = _lib.load()
+    if workspace is None and len(want) > (1 if k is None else 2):
+        workspace = _recurrence_workspace(lib.mamba_qk_norm_rotary_bwd_workspace_bytes,
+                                          "mamba_qk_norm_rotary_bwd_workspace_bytes", dev, ctypes.byref(dims))
+    to = lambda n: _ptr(res[n], n, dev, want[n][1], want[n][0]) if n in want else None  # noqa: E731
+    st = _launch(dev, lib.mamba_qk_norm_rotary_bwd, ctypes.byref(dims), *ptrs, to("dq"), to("dk"), to("dq_weight"),
+                 to("dk_weight"), _ptr(workspace, "workspace", dev, torch.uint8),
+                 0 if workspace is None else workspace.numel())
+    _lib.check(st, "mamba_qk_norm_rotary_bwd")
+    return {n: res[n] for n in want}

@@ -46,10 +46,14 @@ EXPORTED = (
     "mamba_gated_delta_rule_bwd_workspace_bytes",
     "mamba_gated_delta_rule_bwd",
     "mamba_gated_delta_rule_update",
+    "mamba_qk_norm_rotary_fwd",
+    "mamba_qk_norm_rotary_bwd_workspace_bytes",
+    "mamba_qk_norm_rotary_bwd",
 )
 
 PACK_BLOCK = 64          # MAMBA_PACK_BLOCK: channels that share one scale
 RECURRENCE_CHUNK = 128   # MAMBA_RECURRENCE_CHUNK: tokens between two saved states
+NORMS = {"rms": 0, "l2": 1}   # MAMBA_NORM_*
 DELTA_CHUNK = 64         # MAMBA_DELTA_CHUNK: the same of the delta rule
 
 
@@ -101,6 +105,28 @@ class DeltaDims(ctypes.Structure):
         ("ld_dout", ctypes.c_int64),
         ("dtype", ctypes.c_int32),
         ("scale", ctypes.c_float),
+    ]
+
+
+class QkNormDims(ctypes.Structure):
+    """mamba_qk_norm_dims_t"""
+
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("q_heads", ctypes.c_int32),
+        ("k_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("table_rows", ctypes.c_int64),
+        ("ld_q", ctypes.c_int64),
+        ("ld_k", ctypes.c_int64),
+        ("ld_dq_out", ctypes.c_int64),
+        ("ld_dk_out", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("norm", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("eps", ctypes.c_float),
     ]
 
 
@@ -194,6 +220,13 @@ def load() -> ctypes.CDLL:
     lib.mamba_gated_delta_rule_bwd.restype = ctypes.c_int
     lib.mamba_gated_delta_rule_update.argtypes = [dd] + [vp] * 9
     lib.mamba_gated_delta_rule_update.restype = ctypes.c_int
+    qn = ctypes.POINTER(QkNormDims)
+    lib.mamba_qk_norm_rotary_fwd.argtypes = [qn] + [vp] * 10
+    lib.mamba_qk_norm_rotary_fwd.restype = ctypes.c_int
+    lib.mamba_qk_norm_rotary_bwd_workspace_bytes.argtypes = [qn, ctypes.POINTER(sz)]
+    lib.mamba_qk_norm_rotary_bwd_workspace_bytes.restype = ctypes.c_int
+    lib.mamba_qk_norm_rotary_bwd.argtypes = [qn] + [vp] * 14 + [sz, vp]
+    lib.mamba_qk_norm_rotary_bwd.restype = ctypes.c_int
     _lib = lib
     return lib
 

@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["api.cpp", "noalloc.hip", "conv1d.hip", "conv1d_bwd.hip", "scan.hip", "scan_bwd.hip", "ssd.hip",
            "decode.hip", "fill.hip", "pad.hip", "heads_bwd.hip", "recurrence_api.cpp", "recurrence.hip",
            "recurrence_bwd.hip", "checkpoint.hip", "delta_api.cpp", "delta_prepare.hip", "delta_fwd.hip",
-           "delta_bwd.hip", "delta_grads.hip", "delta_step.hip"]
+           "delta_bwd.hip", "delta_grads.hip", "delta_step.hip", "qk_norm_api.cpp", "qk_norm.hip"]
 # The ALU issue-rate probe bench.py runs (measurement only, not part of the C ABI).
 PROBE_SRC = os.path.join(PKG_DIR, "probe", "alu_rates.hip")
 PROBE_PATH = os.path.join(PKG_DIR, "libmamba_probe.so")
