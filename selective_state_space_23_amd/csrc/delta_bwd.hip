@@ -34,19 +34,19 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, m = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t bh = blockIdx.x / cols;
-    const int col = static_cast<int>(blockIdx.x % cols);
-    const int hv = static_cast<int>(bh % a.vheads), hk = hv / (a.vheads / a.kheads);
-    const int64_t b = bh / a.vheads;
+    const int64_t bh = quotient(blockIdx.x, cols);
+    const int col = remainder(blockIdx.x, cols);
+    const int hv = remainder(bh, a.vheads), hk = quotient(hv, a.vheads / a.kheads);
+    const int64_t b = quotient(bh, a.vheads);
     const int v = (col * NW + wave) * 16 + m;
     const bool v_in = v < a.vdim;
     const int n = a.nchunks;
     const int64_t cells = static_cast<int64_t>(a.kdim) * a.vdim;
 
-    auto state_off = [&](int i, int r) {
-        const int kd = state_row(i, g, r);
-        return v_in && kd < a.kdim ? static_cast<uint32_t>((kd * a.vdim + v) * 4) : kPast;
-    };
+    // Offsets of lanes without a column, and of rows behind the last, lie behind the buffer.
+    const uint32_t state_lane = v_in ? v * 4 : kPast;
+    auto state_off = [&](int i, int r) { return state_lane + static_cast<uint32_t>(state_row(i, g, r) * a.vdim * 4); };
+    const uint32_t value_lane = v_in ? v * ESZ : kPast;
     f32x4 S[2 * STEPS];   // dS
     {
         const Rsrc rs = rsrc(a.d_final_state + (a.d_final_state ? bh * cells : 0), a.d_final_state ? cells * 4 : 0);
@@ -88,7 +88,7 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 oraw[4 * i + r] = load_one<T>(
-                    orr, v_in ? static_cast<uint32_t>(((16 * i + 4 * g + r) * a.ld_o + v) * ESZ) : kPast);
+                    orr, value_lane + static_cast<uint32_t>((16 * i + 4 * g + r) * static_cast<int>(a.ld_o) * ESZ));
     };
 
     fetch(n - 1);
@@ -120,19 +120,19 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) odd = odd || not_finite(dO[i][r]);
+            for (int r = 0; r < 4; ++r) odd |= not_finite(dO[i][r]);
         if (bad != 0 || __ballot(odd) != 0) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) sick |= not_finite(dO[i][r]) ? uint64_t(1) << (16 * i + 4 * g + r) : 0;
+                for (int r = 0; r < 4; ++r) sick |= uint64_t(not_finite(dO[i][r])) << (16 * i + 4 * g + r);
             sick |= __shfl_xor(sick, 16);
             sick |= __shfl_xor(sick, 32);
             sick = whole(sick | bad, starts);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) dO[i][r] = (sick >> (16 * i + 4 * g + r)) & 1 ? 0.0f : dO[i][r];
+                for (int r = 0; r < 4; ++r) dO[i][r] = keep_if(!((sick >> (16 * i + 4 * g + r)) & 1), dO[i][r]);
         }
 
         // K dS and Q K^T
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
                 const f32x4 outof = four(rec->outof + 16 * is + 4 * g);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    U[is][r] = 16 * is + 4 * g + r >= last_start ? outof[r] * ks[is][r] : 0.0f;
+                    U[is][r] = keep_if(16 * is + 4 * g + r >= last_start, outof[r] * ks[is][r]);
                 const int s = 16 * is + m, end = doc_end(starts, s);
                 const float sh = rec->hi[s], sl = rec->lo[s];
                 f32x4 P[4];
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
                     for (int r = 0; r < 4; ++r) {
                         const int t = 16 * it + 4 * g + r;
                         const float d = exp2_fast((th[it][r] - sh) + (tl[it][r] - sl));
-                        P[it][r] = it >= is && t >= s && t < end ? a.scale * pq[it > is ? it : is][is][r] * d : 0.0f;
+                        P[it][r] = it >= is ? keep_if(t >= s && t < end, a.scale * pq[it > is ? it : is][is][r] * d) : 0.0f;
                     }
 #pragma unroll
                 for (int j = is / 2; j < 2; ++j) {
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) odd = odd || not_finite(U[i][r]);
+            for (int r = 0; r < 4; ++r) odd |= not_finite(U[i][r]);
         const bool any_sick = __ballot(odd || sick != 0) != 0;
         uint64_t drop = 0;   // rows out in all of the wave's columns: their keys and queries may be what is not finite
         if (any_sick) {
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) more |= not_finite(U[i][r]) ? uint64_t(1) << (16 * i + 4 * g + r) : 0;
+                for (int r = 0; r < 4; ++r) more |= uint64_t(not_finite(U[i][r])) << (16 * i + 4 * g + r);
             more |= __shfl_xor(more, 16);
             more |= __shfl_xor(more, 32);
             sick = whole(sick | more, starts);
@@ -219,8 +219,8 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    U[i][r] = (sick >> (16 * i + 4 * g + r)) & 1 ? 0.0f : U[i][r];
-                    dO[i][r] = (sick >> (16 * i + 4 * g + r)) & 1 ? 0.0f : dO[i][r];
+                    U[i][r] = keep_if(!((sick >> (16 * i + 4 * g + r)) & 1), U[i][r]);
+                    dO[i][r] = keep_if(!((sick >> (16 * i + 4 * g + r)) & 1), dO[i][r]);
                 }
             drop = sick;
 #pragma unroll
@@ -246,8 +246,8 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const bool old = 16 * i + 4 * g + r < first_start;
-                    X[i][r] = old ? -into[r] * (beta[r] * X[i][r]) : 0.0f;
-                    dO[i][r] = old ? a.scale * into[r] * dO[i][r] : 0.0f;
+                    X[i][r] = keep_if(old, -into[r] * (beta[r] * X[i][r]));
+                    dO[i][r] = keep_if(old, a.scale * into[r] * dO[i][r]);
                 }
             }
         }
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
 #pragma unroll
         for (int i = 0; i < 2 * STEPS; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S[i][r] = starts != 0 ? 0.0f : keep * S[i][r];
+            for (int r = 0; r < 4; ++r) S[i][r] = keep_if(starts == 0, keep * S[i][r]);
         const Frag<3> xf[2] = {split(X[0], X[1]), split(X[2], X[3])};
         const Frag<3> of[2] = {split(dO[0], dO[1]), split(dO[2], dO[3])};
 #pragma unroll
@@ -279,7 +279,7 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
 #pragma unroll
             for (int i = 0; i < 2 * STEPS; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) S[i][r] = dead ? __builtin_nanf("") : S[i][r];
+                for (int r = 0; r < 4; ++r) S[i][r] = nan_if(dead, S[i][r]);
         }
         lds_barrier();
     }

@@ -32,19 +32,19 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, m = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t bh = blockIdx.x / cols;
-    const int col = static_cast<int>(blockIdx.x % cols);
-    const int hv = static_cast<int>(bh % a.vheads), hk = hv / (a.vheads / a.kheads);
-    const int64_t b = bh / a.vheads;
+    const int64_t bh = quotient(blockIdx.x, cols);
+    const int col = remainder(blockIdx.x, cols);
+    const int hv = remainder(bh, a.vheads), hk = quotient(hv, a.vheads / a.kheads);
+    const int64_t b = quotient(bh, a.vheads);
     const int v = (col * NW + wave) * 16 + m;
     const bool v_in = v < a.vdim;
     const int n = a.nchunks;
     const int64_t cells = static_cast<int64_t>(a.kdim) * a.vdim;
 
-    auto state_off = [&](int i, int r) {
-        const int kd = state_row(i, g, r);
-        return v_in && kd < a.kdim ? static_cast<uint32_t>((kd * a.vdim + v) * 4) : kPast;
-    };
+    // Offsets of lanes without a column, and of rows behind the last, lie behind the buffer.
+    const uint32_t state_lane = v_in ? v * 4 : kPast;
+    auto state_off = [&](int i, int r) { return state_lane + static_cast<uint32_t>(state_row(i, g, r) * a.vdim * 4); };
+    const uint32_t value_lane = v_in ? v * ESZ : kPast;
     f32x4 S[2 * STEPS];
     {
         const Rsrc rs = rsrc(a.initial_state + (a.initial_state ? bh * cells : 0), a.initial_state ? cells * 4 : 0);
@@ -91,7 +91,7 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 vraw[4 * i + r] = load_one<T>(
-                    vr, v_in ? static_cast<uint32_t>(((16 * i + 4 * g + r) * a.ld_v + v) * ESZ) : kPast);
+                    vr, value_lane + static_cast<uint32_t>((16 * i + 4 * g + r) * static_cast<int>(a.ld_v) * ESZ));
     };
 
     fetch(0);
@@ -155,8 +155,8 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const bool old = 16 * i + 4 * g + r < first_start;
-                R[i][r] = old ? __builtin_fmaf(-into[r], ks[i][r], vals[4 * i + r]) : vals[4 * i + r];
-                odd = odd || not_finite(R[i][r]);
+                R[i][r] = vals[4 * i + r] - keep_if(old, into[r] * ks[i][r]);
+                odd |= not_finite(R[i][r]);
             }
         }
         // Values that are not finite: the rows from there to the document's end take no part, and give NaN
@@ -167,14 +167,14 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    lost |= not_finite(R[i][r]) ? uint64_t(1) << (16 * i + 4 * g + r) : 0;
+                    lost |= uint64_t(not_finite(R[i][r])) << (16 * i + 4 * g + r);
             lost |= __shfl_xor(lost, 16);
             lost |= __shfl_xor(lost, 32);
             lost = smear(lost | bad, starts);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) R[i][r] = (lost >> (16 * i + 4 * g + r)) & 1 ? 0.0f : R[i][r];
+                for (int r = 0; r < 4; ++r) R[i][r] = keep_if(!((lost >> (16 * i + 4 * g + r)) & 1), R[i][r]);
         }
 
         // U = beta T R
@@ -212,7 +212,7 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
                 const f32x4 into = four(rec->into + 16 * it + 4 * g);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    O[it][r] = 16 * it + 4 * g + r < first_start ? a.scale * into[r] * qs[it][r] : 0.0f;
+                    O[it][r] = keep_if(16 * it + 4 * g + r < first_start, a.scale * into[r] * qs[it][r]);
                 const int t = 16 * it + m, from = doc_first(starts, t);
                 const float th = rec->hi[t], tl = rec->lo[t];
                 f32x4 P[4];
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
                     for (int r = 0; r < 4; ++r) {
                         const int s = 16 * is + 4 * g + r;
                         const float d = exp2_fast((th - sh[is][r]) + (tl - sl[is][r]));
-                        P[is][r] = is <= it && s <= t && s >= from ? a.scale * pt[is < it ? is : it][it][r] * d : 0.0f;
+                        P[is][r] = is <= it ? keep_if(s <= t && s >= from, a.scale * pt[is < it ? is : it][it][r] * d) : 0.0f;
                     }
 #pragma unroll
                 for (int j = 0; j <= it / 2; ++j) product<OUT>(O[it], split_out<OUT>(P[2 * j], P[2 * j + 1]), uf[j]);
@@ -232,7 +232,7 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        O[i][r] = (lost >> (16 * i + 4 * g + r)) & 1 ? __builtin_nanf("") : O[i][r];
+                        O[i][r] = nan_if((lost >> (16 * i + 4 * g + r)) & 1, O[i][r]);
             }
             const int64_t ldo = static_cast<int64_t>(a.vheads) * a.vdim;
             const Rsrc orr = rows_rsrc<ESZ>(a.out, (b * a.seqlen + static_cast<int64_t>(c) * C) * ldo + hv * a.vdim, rows,
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    store_one<T>(orr, v_in ? static_cast<uint32_t>(((16 * i + 4 * g + r) * ldo + v) * ESZ) : kPast, O[i][r]);
+                    store_one<T>(orr, value_lane + static_cast<uint32_t>((16 * i + 4 * g + r) * static_cast<int>(ldo) * ESZ), O[i][r]);
         }
         __builtin_amdgcn_sched_barrier(0);
 
@@ -257,7 +257,7 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
 #pragma unroll
         for (int i = 0; i < 2 * STEPS; ++i) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S[i][r] = starts != 0 ? 0.0f : keep * S[i][r];
+            for (int r = 0; r < 4; ++r) S[i][r] = keep_if(starts == 0, keep * S[i][r]);
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -272,7 +272,7 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
 #pragma unroll
             for (int i = 0; i < 2 * STEPS; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) S[i][r] = dead ? __builtin_nanf("") : S[i][r];
+                for (int r = 0; r < 4; ++r) S[i][r] = nan_if(dead, S[i][r]);
         }
         lds_barrier();
     }

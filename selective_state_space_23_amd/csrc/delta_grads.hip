@@ -96,7 +96,7 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
     __shared__ __align__(16) char region1[ONE];
     __shared__ __align__(16) ChunkRec rec_;
     __shared__ float ends[kWaves];
-    __shared__ unsigned long long sick_rows;
+    __shared__ uint64_t odd_rows[kWaves];
     uint16_t* Kl = reinterpret_cast<uint16_t*>(region0);
     uint16_t* Ql = Kl + N * C * ROW;
     uint16_t* Ul = reinterpret_cast<uint16_t*>(region0);          // [OUT][C][kRowV]
@@ -108,10 +108,10 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
     const ChunkRec* rec = &rec_;
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t bh = blockIdx.x / a.nchunks;   // row and key head
-    const int c = static_cast<int>(blockIdx.x % a.nchunks);
-    const int hk = static_cast<int>(bh % a.kheads), group = a.vheads / a.kheads;
-    const int64_t b = bh / a.kheads;
+    const int bh = quotient(blockIdx.x, a.nchunks);   // row and key head
+    const int c = remainder(blockIdx.x, a.nchunks);
+    const int hk = remainder(bh, a.kheads), group = quotient(a.vheads, a.kheads);
+    const int64_t b = quotient(bh, a.kheads);
     const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, left = a.seqlen - static_cast<int64_t>(c) * C;
     const int rows = static_cast<int>(left < C ? left : C);
     const int64_t cells = static_cast<int64_t>(a.kdim) * a.vdim;
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                 constexpr int RECW = sizeof(ChunkRec) / 4;
                 static_assert(RECW <= kThreads, "one word a thread");
                 reinterpret_cast<uint32_t*>(&rec_)[tid < RECW ? tid : RECW - 1] = from[tid < RECW ? tid : RECW - 1];
-                if (wave == 0) sick_rows = 0;
+                odd_rows[wave] = 0;
                 kraw.land_without(Kl, tid, sick);
                 qraw.land_without(Ql, tid, sick);
             }
@@ -164,7 +164,9 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
             const bool no_state = (sick & 1) != 0 && first_start > 0, no_dstate = (sick >> 63) != 0;
             if (wave < vwaves) {
                 const int v = 16 * wave + m;
-                const bool v_in = v < a.vdim;
+                const uint32_t value_lane = v < a.vdim ? v * ESZ : kPast;
+                const uint32_t state_lane = v < a.vdim && !no_state ? v * 4 : kPast;
+                const uint32_t dstate_lane = v < a.vdim && !no_dstate ? v * 4 : kPast;
                 f32x4 V[4], dO[4];
                 uint64_t odd = 0;
 #pragma unroll
@@ -172,10 +174,10 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int t = 16 * i + 4 * g + r;
-                        const bool on = v_in && !((sick >> t) & 1);
-                        V[i][r] = one_value<T>(load_one<T>(vr, on ? static_cast<uint32_t>((t * a.ld_v + v) * ESZ) : kPast));
-                        dO[i][r] = one_value<T>(load_one<T>(orr, on ? static_cast<uint32_t>((t * a.ld_o + v) * ESZ) : kPast));
-                        odd |= not_finite(dO[i][r]) ? uint64_t(1) << t : 0;
+                        const uint32_t at = (sick >> t) & 1 ? kPast : value_lane;
+                        V[i][r] = one_value<T>(load_one<T>(vr, at + static_cast<uint32_t>(t * static_cast<int>(a.ld_v) * ESZ)));
+                        dO[i][r] = one_value<T>(load_one<T>(orr, at + static_cast<uint32_t>(t * static_cast<int>(a.ld_o) * ESZ)));
+                        odd |= uint64_t(not_finite(dO[i][r])) << t;
                     }
                 f32x4 ks[4], qs[4], kd[4];
                 float inner = 0.0f;   // <dS, S> of this column, this group's channels
@@ -187,12 +189,9 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                     f32x4 s0, s1, d0, d1;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const int ch = 32 * j + 8 * g + e;
-                        const uint32_t off = static_cast<uint32_t>((ch * a.vdim + v) * 4);
-                        const float x = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-                            sr, v_in && ch < a.kdim && !no_state ? off : kPast, 0, 0));
-                        const float y = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-                            dr, v_in && ch < a.kdim && !no_dstate ? off : kPast, 0, 0));
+                        const uint32_t row = static_cast<uint32_t>((32 * j + 8 * g + e) * a.vdim * 4);
+                        const float x = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sr, state_lane + row, 0, 0));
+                        const float y = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(dr, dstate_lane + row, 0, 0));
                         (e < 4 ? s0 : s1)[e & 3] = x;
                         (e < 4 ? d0 : d1)[e & 3] = y;
                         inner = __builtin_fmaf(x, y, inner);
@@ -217,11 +216,11 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                     for (int r = 0; r < 4; ++r) {
                         const int t = 16 * i + 4 * g + r;
                         const bool old = t < first_start;
-                        R[i][r] = old ? __builtin_fmaf(-into[r], ks[i][r], V[i][r]) : V[i][r];
-                        const bool bad_row = not_finite(R[i][r]) || (old && not_finite(qs[i][r])) ||
-                                             (t >= last_start && not_finite(kd[i][r]));
-                        odd |= bad_row ? uint64_t(1) << t : 0;
-                        qs[i][r] = old ? a.scale * into[r] * qs[i][r] : 0.0f;
+                        R[i][r] = V[i][r] - keep_if(old, into[r] * ks[i][r]);
+                        const float y = keep_if(t >= last_start, kd[i][r]);
+                        odd |= uint64_t(not_finite(R[i][r])) << t | uint64_t(not_finite(y)) << t;
+                        qs[i][r] = keep_if(old, a.scale * into[r] * qs[i][r]);
+                        odd |= uint64_t(not_finite(qs[i][r])) << t;
                     }
                 }
                 // E, U
@@ -263,7 +262,7 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                         }
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            odd |= 4 * g + r == m && not_finite(P[it][r]) ? uint64_t(1) << (16 * it + m) : 0;
+                            odd |= uint64_t(not_finite(keep_if(4 * g + r == m, P[it][r]))) << (16 * it + m);
                         const int t = 16 * it + m, from = doc_first(starts, t);
                         const float th = rec->hi[t], tl = rec->lo[t];
 #pragma unroll
@@ -273,7 +272,7 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                             for (int r = 0; r < 4; ++r) {
                                 const int s = 16 * is + 4 * g + r;
                                 const float d = exp2_fast((th - sh[r]) + (tl - sl[r]));
-                                P[is][r] = s <= t && s >= from ? a.scale * P[is][r] * d : 0.0f;
+                                P[is][r] = keep_if(s <= t && s >= from, a.scale * P[is][r] * d);
                             }
                         }
 #pragma unroll
@@ -297,7 +296,7 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                         const f32x4 outof = four(rec->outof + 16 * is + 4 * g);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            dU[is][r] = 16 * is + 4 * g + r >= last_start ? outof[r] * kd[is][r] : 0.0f;
+                            dU[is][r] = keep_if(16 * is + 4 * g + r >= last_start, outof[r] * kd[is][r]);
                             end = __builtin_fmaf(U[is][r], dU[is][r], end);
                         }
                         f32x4 P[4];   // rows t, columns s
@@ -319,7 +318,7 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                             for (int r = 0; r < 4; ++r) {
                                 const int t = 16 * it + 4 * g + r;
                                 const float d = exp2_fast((th[r] - sh) + (tl[r] - sl));
-                                P[it][r] = t >= s && t < stop ? a.scale * P[it][r] * d : 0.0f;
+                                P[it][r] = keep_if(t >= s && t < stop, a.scale * P[it][r] * d);
                             }
                         }
 #pragma unroll
@@ -360,8 +359,8 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                         const float x = row_sum(X[i][r] * E[i][r]), y = row_sum(dv * V[i][r]);
                         pb = m == 4 * i + r ? x : pb;
                         pg -= m == 4 * i + r ? y : 0.0f;
-                        store_one<T>(dvr, v_in ? static_cast<uint32_t>((t * ldv + v) * ESZ) : kPast,
-                                     (sick >> t) & 1 ? __builtin_nanf("") : dv);
+                        store_one<T>(dvr, value_lane + static_cast<uint32_t>(t * static_cast<int>(ldv) * ESZ),
+                                     nan_if((sick >> t) & 1, dv));
                     }
                 }
                 const int t = 16 * (m / 4) + 4 * g + m % 4;
@@ -370,11 +369,14 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                 if (__ballot(odd != 0) != 0) {
 #pragma unroll
                     for (int s = 1; s < 64; s *= 2) odd |= __shfl_xor(odd, s);
-                    atomicOr(&sick_rows, static_cast<unsigned long long>(odd));
+                    odd_rows[wave] = odd;
                 }
             }
             __syncthreads();
-            const uint64_t found = whole(uniform(sick_rows) | uniform(rec->bad), starts);
+            uint64_t found = rec->bad;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) found |= odd_rows[w];
+            found = whole(uniform(found), starts);
             if (pass == 1 || found == 0) break;
             sick = found;
         }
@@ -399,9 +401,9 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
             const bool nan = (sick >> lane) & 1, start = (starts >> lane) & 1;
             const Rsrc br = rows_rsrc<4>(a.dbeta, first * a.vheads + hv, rows, a.vheads, 1);
             const Rsrc gr = rows_rsrc<4>(a.dg, a.dg ? first * a.vheads + hv : 0, a.dg ? rows : 0, a.vheads, 1);
-            store_one<float>(br, static_cast<uint32_t>(lane * a.vheads * 4), nan ? __builtin_nanf("") : pb);
+            store_one<float>(br, static_cast<uint32_t>(lane * a.vheads * 4), nan_if(nan, pb));
             store_one<float>(gr, static_cast<uint32_t>(lane * a.vheads * 4),
-                             nan ? __builtin_nanf("") : start ? 0.0f : static_cast<float>(sum));
+                             nan_if(nan, keep_if(!start, static_cast<float>(sum))));
         }
         // (2) U and dX over K and Q
         if (wave < vwaves) {
@@ -420,7 +422,7 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
         const int lane = thread_now() & 63, g = lane >> 4, m = lane & 15;
         auto dout_frag = [&](int i, int j) {
             Eight<T, VEC> e;
-            e.load(orr, static_cast<uint32_t>((16 * i + m) * a.ld_o * ESZ), 32 * j + 8 * g, a.vdim);
+            e.load(orr, static_cast<uint32_t>((16 * i + m) * static_cast<int>(a.ld_o) * ESZ), 32 * j + 8 * g, a.vdim);
             Frag<N> f = e.frag();
             clear_if<N>(f, (sick >> (16 * i + m)) & 1);
             return f;
@@ -441,8 +443,8 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                 const int t = 16 * it + 4 * g + r;
                 const float d = exp2_fast((rec->hi[t] - sh) + (rec->lo[t] - sl));
                 const bool on = t >= s && t < stop;
-                put<OUT>(Pl, PLANE_P, t * kRowP + s, on ? a.scale * d * P[r] : 0.0f);
-                const float n = on && t > s ? -rec->beta[t] * d * G[r] : 0.0f;
+                put<OUT>(Pl, PLANE_P, t * kRowP + s, keep_if(on, a.scale * d * P[r]));
+                const float n = keep_if(on && t > s, -rec->beta[t] * d * G[r]);
                 const int pad = t * kRowP + C;   // for the lanes above the diagonal
                 put<OUT>(Nl, PLANE_P, t >= s ? t * kRowP + s : pad, n);
                 put<OUT>(Nl, PLANE_P, t > s ? s * kRowP + t : pad, n);
@@ -478,8 +480,8 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                 for (int r = 0; r < 4; ++r) {
                     const int t = 16 * i + 4 * g + r;
                     const bool old = t < first_start;
-                    dq[i][r] += old ? a.scale * into[r] * os[i][r] : 0.0f;
-                    dk[i][r] += (t >= last_start ? outof[r] * us[i][r] : 0.0f) - (old ? into[r] * beta[r] * xs[i][r] : 0.0f);
+                    dq[i][r] += keep_if(old, a.scale * into[r] * os[i][r]);
+                    dk[i][r] += keep_if(t >= last_start, outof[r] * us[i][r]) - keep_if(old, into[r] * beta[r] * xs[i][r]);
                 }
             }
         }
@@ -511,6 +513,7 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
 
     const int lane = thread_now() & 63, g = lane >> 4, m = lane & 15;
     const int ch = 16 * wave + m;
+    const uint32_t key_lane = ch < a.kdim ? ch * ESZ : kPast;
     const int64_t ldk = static_cast<int64_t>(a.kheads) * a.kdim;
     const Rsrc dqr = rows_rsrc<ESZ>(a.dq, first * ldk + hk * a.kdim, rows, ldk, a.kdim);
     const Rsrc dkr = rows_rsrc<ESZ>(a.dk, first * ldk + hk * a.kdim, rows, ldk, a.kdim);
@@ -520,10 +523,10 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int t = 16 * i + 4 * g + r;
-                const uint32_t off = ch < a.kdim ? static_cast<uint32_t>((t * ldk + ch) * ESZ) : kPast;
+                const uint32_t off = key_lane + static_cast<uint32_t>(t * static_cast<int>(ldk) * ESZ);
                 const bool nan = (sick_any >> t) & 1;
-                store_one<T>(dqr, off, nan ? __builtin_nanf("") : dq[i][r]);
-                store_one<T>(dkr, off, nan ? __builtin_nanf("") : dk[i][r]);
+                store_one<T>(dqr, off, nan_if(nan, dq[i][r]));
+                store_one<T>(dkr, off, nan_if(nan, dk[i][r]));
             }
     }
 }

@@ -48,10 +48,9 @@ __global__ __launch_bounds__(64) void prepare_kernel(DeltaArgs a, size_t rec_byt
     constexpr int N = kPieces<T>, ESZ = sizeof(T);
     const int lane = threadIdx.x, g = lane >> 4, m = lane & 15;
     const int64_t id = blockIdx.x;
-    const int c = static_cast<int>(id % a.nchunks);
-    const int64_t bh = id / a.nchunks;
-    const int hv = static_cast<int>(bh % a.vheads), hk = hv / (a.vheads / a.kheads);
-    const int64_t b = bh / a.vheads, t0 = static_cast<int64_t>(c) * C;
+    const int c = remainder(blockIdx.x, a.nchunks), bh = quotient(blockIdx.x, a.nchunks);
+    const int hv = remainder(bh, a.vheads), hk = quotient(hv, a.vheads / a.kheads);
+    const int64_t b = quotient(bh, a.vheads), t0 = static_cast<int64_t>(c) * C;
     const int rows = static_cast<int>(a.seqlen - t0 < C ? a.seqlen - t0 : C);
 
     // decays
@@ -94,7 +93,7 @@ __global__ __launch_bounds__(64) void prepare_kernel(DeltaArgs a, size_t rec_byt
         Eight<T, VEC> raw[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            raw[i].load(kr, static_cast<uint32_t>((16 * i + m) * a.ld_k * ESZ), 32 * j + 8 * g, a.kdim);
+            raw[i].load(kr, static_cast<uint32_t>((16 * i + m) * static_cast<int>(a.ld_k) * ESZ), 32 * j + 8 * g, a.kdim);
         Frag<N> f[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = raw[i].frag();
@@ -150,7 +149,7 @@ __global__ __launch_bounds__(64) void prepare_kernel(DeltaArgs a, size_t rec_byt
                     const int t = 16 * i + 4 * g + r;
                     const float d = exp2_fast((th[r] - sh) + (tl[r] - sl));
                     const bool on = s < t && t < end && !((bad >> t) & 1);
-                    As[t * kRowA + s] = on ? (which ? tb[r] : sb) * (d * acc[i][j][r]) : 0.0f;
+                    As[t * kRowA + s] = keep_if(on, (which ? tb[r] : sb) * (d * acc[i][j][r]));
                 }
             }
         }

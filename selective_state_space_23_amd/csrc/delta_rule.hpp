@@ -205,7 +205,7 @@ template <typename T, int KT, int THREADS, bool VEC> struct Tile {
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
             const int x = p * THREADS + tid, t = x / (KT / 8), ch = x % (KT / 8) * 8;
-            raw[p].load(rs, static_cast<uint32_t>(t * ld * sizeof(T)), ch, width);
+            raw[p].load(rs, static_cast<uint32_t>(t * static_cast<int>(ld) * static_cast<int>(sizeof(T))), ch, width);
         }
     }
     __device__ __forceinline__ void land(uint16_t* lds, int tid) const {
@@ -283,6 +283,11 @@ __device__ __forceinline__ int thread_now() {
     return t;
 }
 
+// a / b and a % b of values that all lanes share, in scalar registers (the division itself runs
+// on the vector unit, and a buffer's address that comes from there costs a loop at every access).
+__device__ __forceinline__ int quotient(uint32_t a, uint32_t b) { return __builtin_amdgcn_readfirstlane(a / b); }
+__device__ __forceinline__ int remainder(uint32_t a, uint32_t b) { return __builtin_amdgcn_readfirstlane(a % b); }
+
 __device__ __forceinline__ uint64_t uniform(uint64_t x) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(x));
     const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<int>(x >> 32));
@@ -321,6 +326,14 @@ __device__ __forceinline__ uint64_t whole(uint64_t m, uint64_t starts) {
     }
     return m;
 }
+
+// x or 0, whatever x is, by its bits: a select of a costly x becomes a divergent branch, which is slower here and
+// not safe in a loop with this many registers (the compiler has been seen to copy live registers at the join
+// before it restores the execution mask).
+__device__ __forceinline__ float keep_if(bool on, float x) { return __uint_as_float(__float_as_uint(x) & (on ? ~0u : 0u)); }
+
+// x, or a NaN.
+__device__ __forceinline__ float nan_if(bool on, float x) { return __uint_as_float(__float_as_uint(x) | (on ? 0x7fc00000u : 0u)); }
 
 __device__ __forceinline__ bool not_finite(float x) { return __builtin_isfpclass(x, 0x207); }   // nan, +-inf
 

@@ -48,27 +48,29 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a) {
     __shared__ __align__(16) float kv[128], qv[128];
     __shared__ __align__(16) f32x4 red[2][4][COLS];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t bh = blockIdx.x / a.cols;
-    const int hv = static_cast<int>(bh % a.vheads), hk = hv / (a.vheads / a.kheads);
-    const int64_t b = bh / a.vheads;
-    const int v0 = (static_cast<int>(blockIdx.x % a.cols) * COLS + lane % COLS) * 4;
+    const int64_t bh = quotient(blockIdx.x, a.cols);
+    const int hv = remainder(bh, a.vheads), hk = quotient(hv, a.vheads / a.kheads);
+    const int64_t b = quotient(bh, a.vheads);
+    const int v0 = (remainder(blockIdx.x, a.cols) * COLS + lane % COLS) * 4;
     const int row0 = (wave * (64 / COLS) + lane / COLS) * R;
     const int64_t cells = static_cast<int64_t>(a.kdim) * a.vdim;
 
+    // Offsets of columns behind the last lie behind the buffer, as those of rows do.
+    uint32_t lane_off[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) lane_off[e] = v0 + e < a.vdim ? (v0 + e) * 4 : kPast;
     f32x4 S[R];
     {
         const Rsrc rs = rsrc(a.state_in + (a.state_in ? bh * cells : 0), a.state_in ? cells * 4 : 0);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const bool row_in = row0 + i < a.kdim;
+            const uint32_t row = static_cast<uint32_t>((row0 + i) * a.vdim * 4);
             if constexpr (VEC) {
-                S[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                    rs, row_in && v0 < a.vdim ? ((row0 + i) * a.vdim + v0) * 4 : kPast, 0, 0));
+                S[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, lane_off[0] + row, 0, 0));
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    S[i][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-                        rs, row_in && v0 + e < a.vdim ? ((row0 + i) * a.vdim + v0 + e) * 4 : kPast, 0, 0));
+                    S[i][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, lane_off[e] + row, 0, 0));
             }
         }
     }
@@ -131,17 +133,13 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a) {
         const Rsrc rs = rsrc(a.state_out + bh * cells, cells * 4);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const bool row_in = row0 + i < a.kdim;
+            const uint32_t row = static_cast<uint32_t>((row0 + i) * a.vdim * 4);
             if constexpr (VEC) {
-                __builtin_amdgcn_raw_buffer_store_b128(
-                    __builtin_bit_cast(u32x4, S[i]), rs,
-                    row_in && v0 < a.vdim ? ((row0 + i) * a.vdim + v0) * 4 : kPast, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[i]), rs, lane_off[0] + row, 0, 0);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    __builtin_amdgcn_raw_buffer_store_b32(
-                        __float_as_uint(S[i][e]), rs,
-                        row_in && v0 + e < a.vdim ? ((row0 + i) * a.vdim + v0 + e) * 4 : kPast, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][e]), rs, lane_off[e] + row, 0, 0);
             }
         }
     }

@@ -198,15 +198,17 @@ __global__ __launch_bounds__(kWaves * 64) void norm_kernel(Kernel p) {
 
     const uint32_t tasks = static_cast<uint32_t>(a.tokens) * splits, step = static_cast<uint32_t>(blocks) * kWaves;
     for (uint32_t task = static_cast<uint32_t>(block) * kWaves + wave; task < tasks; task += step) {
-        const int64_t token = splits == 1 ? task : task / splits;
-        const int split = splits == 1 ? 0 : static_cast<int>(task % splits);
+        const uint32_t token_ = splits == 1 ? task : task / splits;   // (the vector unit's division: one value all the same)
+        const int64_t token = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(token_));
+        const int split = __builtin_amdgcn_readfirstlane(task - static_cast<uint32_t>(token) * splits);
         const Rsrc xr = rsrc(static_cast<const T*>(a.x[which]) + token * a.ld_x[which], int64_t(heads) * a.dim * ESZ);
         const Rsrc yr = rsrc(static_cast<T*>(a.out[which]) + token * heads * a.dim, int64_t(heads) * a.dim * ESZ);
         const Rsrc gr = rsrc(static_cast<const T*>(BWD ? a.dy[which] : a.x[which]) + (BWD ? token * a.ld_dy[which] : 0),
                              BWD ? int64_t(heads) * a.dim * ESZ : 0);
         f32x4 c = {1, 1, 1, 1}, s = {0, 0, 0, 0};
         if (a.cos) {
-            const int64_t pos = a.positions ? a.positions[token] : static_cast<uint32_t>(token) % static_cast<uint32_t>(a.seqlen);
+            const int64_t pos = a.positions ? a.positions[token] : static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(
+                static_cast<uint32_t>(token) % static_cast<uint32_t>(a.seqlen)));
             const bool in = pos >= 0 && pos < a.table_rows;
             const int64_t row = in ? pos * (a.rot / 2) : 0;
             c = angles<MODE>(rsrc(a.cos + row, a.rot * 2), w, 1.0f);
