@@ -83,8 +83,13 @@ size_t solve_bytes(const mamba_delta_dims_t* d) {
     return round256(static_cast<size_t>(d->batch * d->value_heads * chunks_of(d)) * mamba::delta_solve_bytes());
 }
 
+size_t pairs_bytes(const mamba_delta_dims_t* d, bool backward) {
+    return round256(static_cast<size_t>(d->batch * d->value_heads * chunks_of(d)) *
+                    mamba::delta_pairs_bytes(d->dtype == MAMBA_DTYPE_BF16, backward));
+}
+
 size_t fwd_workspace(const mamba_delta_dims_t* d) {
-    return d->batch * d->seqlen == 0 ? 0 : record_bytes(d) + solve_bytes(d);
+    return d->batch * d->seqlen == 0 ? 0 : record_bytes(d) + solve_bytes(d) + pairs_bytes(d, false);
 }
 
 size_t state_bytes(const mamba_delta_dims_t* d) {   // of every chunk
@@ -92,7 +97,8 @@ size_t state_bytes(const mamba_delta_dims_t* d) {   // of every chunk
 }
 
 size_t bwd_workspace(const mamba_delta_dims_t* d, bool have_states) {
-    return d->batch * d->seqlen == 0 ? 0 : record_bytes(d) + 2 * solve_bytes(d) + (have_states ? 1 : 2) * state_bytes(d);
+    return d->batch * d->seqlen == 0 ? 0 : record_bytes(d) + 2 * solve_bytes(d) + pairs_bytes(d, true) +
+                                                (have_states ? 1 : 2) * state_bytes(d);
 }
 
 mamba::DeltaArgs base_args(const mamba_delta_dims_t* d, const Sizes& s, const void* q, const void* k, const void* v,
@@ -154,6 +160,7 @@ int mamba_gated_delta_rule_fwd(const mamba_delta_dims_t* dims, const void* q, co
     const Span outs[] = {{out, s.v}, {final_state, s.state}, {states, s.state * chunks_of(dims)}, {workspace, need}};
     if (!disjoint(ins, outs)) return MAMBA_ERR_INVALID_ARGUMENT;
     mamba::DeltaArgs a = base_args(dims, s, q, k, v, g, beta, doc_start, initial_state, workspace, stream);
+    a.pairs = a.solve + solve_bytes(dims);
     a.out = out; a.final_state = final_state; a.states = states;
     const hipError_t e = mamba::launch_delta_prepare(a);
     return hip_status(e != hipSuccess ? e : mamba::launch_delta_fwd(a));
@@ -203,7 +210,8 @@ int mamba_gated_delta_rule_bwd(const mamba_delta_dims_t* dims, const void* q, co
     if (!disjoint(ins, outs)) return MAMBA_ERR_INVALID_ARGUMENT;
     mamba::DeltaArgs a = base_args(dims, s, q, k, v, g, beta, doc_start, initial_state, workspace, stream);
     a.solve_t = a.solve + solve_bytes(dims);
-    a.dstates = reinterpret_cast<float*>(a.solve_t + solve_bytes(dims));
+    a.pairs = a.solve_t + solve_bytes(dims);
+    a.dstates = reinterpret_cast<float*>(a.pairs + pairs_bytes(dims, true));
     a.states = states ? const_cast<float*>(states) : a.dstates + state_bytes(dims) / 4;
     a.dout = dout; a.d_final_state = d_final_state;
     a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.d_initial_state = d_initial_state;

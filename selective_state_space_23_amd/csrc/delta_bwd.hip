@@ -22,15 +22,11 @@ using namespace delta;
 template <typename T, int KT, int NW, bool VEC>
 __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
     constexpr int N = kPieces<T>, ESZ = sizeof(T), STEPS = KT / 32, THREADS = NW * 64;
+    constexpr bool DIRECT = VEC && N == 1;   // to LDS without registers, in two buffers
     using KQ = Tile<T, KT, THREADS, VEC>;
-    constexpr int ROW = KQ::ROW;
-    constexpr int RECW = sizeof(ChunkRec) / 4, RECP = (RECW + THREADS - 1) / THREADS;
-    constexpr int TP = (kBlocks * 3 + NW - 1) / NW;
-    __shared__ __align__(16) char smem[2 * KQ::kBytes + kSolveBytes + RECP * THREADS * 4];
-    u32x4* Tl = reinterpret_cast<u32x4*>(smem);
-    ChunkRec* rec = reinterpret_cast<ChunkRec*>(Tl + kBlocks * 3 * 64);
-    uint16_t* Kl = reinterpret_cast<uint16_t*>(smem + kSolveBytes + RECP * THREADS * 4);
-    uint16_t* Ql = Kl + N * C * ROW;
+    constexpr int TKB = kBlocks * 3, RKB = 2, BKB = 2 * TKB + RKB;   // KB of the triangle, of P and of a record
+    constexpr size_t BUF = BKB * 1024 + 2 * KQ::kBytes;
+    __shared__ __align__(16) char smem[(DIRECT ? 2 : 1) * BUF];
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, m = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -65,23 +61,34 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
                 __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][r]), rs, state_off(i, r), 0, 0);
     };
 
-    KQ kraw, qraw;
-    u32x4 traw[TP];
-    uint32_t oraw[16], recraw[RECP];
-    auto fetch = [&](int c) {
+    KQ kraw, qraw;   // not DIRECT: the next chunk in registers
+    u32x4 braw[(BKB + NW - 1) / NW];
+    uint32_t oraw[16];
+    auto fetch = [&](int c, char* buf) {
         const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, left = a.seqlen - static_cast<int64_t>(c) * C;
-        const int rows = static_cast<int>(left < C ? left : C);
-        kraw.fetch(rows_rsrc<ESZ>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k, a.kdim), a.ld_k,
-                   a.kdim, tid);
-        qraw.fetch(rows_rsrc<ESZ>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_q, a.kdim), a.ld_q,
-                   a.kdim, tid);
         const int64_t id = bh * n + c;
-        const Rsrc tr = rsrc(a.solve_t + id * kSolveBytes, kSolveBytes);
+        const int rows = static_cast<int>(left < C ? left : C);
+        const Rsrc kr = rows_rsrc<ESZ>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k, a.kdim);
+        const Rsrc qr = rows_rsrc<ESZ>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_q, a.kdim);
+        const Rsrc tr = rsrc(a.solve_t + id * kSolveBytes, kSolveBytes), pr = rsrc(a.pairs + id * kSolveBytes, kSolveBytes);
+        const Rsrc rr = rsrc(a.chunks + id * rec_bytes, sizeof(ChunkRec));
+        if constexpr (DIRECT) {
+            uint16_t* Kl = reinterpret_cast<uint16_t*>(buf + BKB * 1024);
+            rows_to_lds<KT, NW>(Kl, kr, a.ld_k, a.kdim, wave, lane);
+            block_to_lds<RKB, NW>(buf + 2 * TKB * 1024, rr, wave, lane);
+            block_to_lds<TKB, NW>(buf + TKB * 1024, pr, wave, lane);
+            block_to_lds<TKB, NW>(buf, tr, wave, lane);
+            rows_to_lds<KT, NW>(Kl + C * KT, qr, a.ld_q, a.kdim, wave, lane);
+        } else {
+            kraw.fetch(kr, a.ld_k, a.kdim, tid);
+            qraw.fetch(qr, a.ld_q, a.kdim, tid);
 #pragma unroll
-        for (int p = 0; p < TP; ++p) traw[p] = __builtin_amdgcn_raw_buffer_load_b128(tr, (p * THREADS + tid) * 16, 0, 0);
-        const Rsrc rr = rsrc(a.chunks + id * rec_bytes, RECW * 4);
-#pragma unroll
-        for (int p = 0; p < RECP; ++p) recraw[p] = __builtin_amdgcn_raw_buffer_load_b32(rr, (p * THREADS + tid) * 4, 0, 0);
+            for (int p = 0; p < (BKB + NW - 1) / NW; ++p) {
+                const int kb = p * NW + wave;
+                const int at = ((kb < TKB ? kb : kb < 2 * TKB ? kb - TKB : kb - 2 * TKB) * 64 + lane) * 16;
+                braw[p] = __builtin_amdgcn_raw_buffer_load_b128(kb < TKB ? tr : kb < 2 * TKB ? pr : rr, at, 0, 0);
+            }
+        }
         const Rsrc orr = rows_rsrc<ESZ>(a.dout, first * a.ld_o + static_cast<int64_t>(hv) * a.vdim, rows, a.ld_o, a.vdim);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -91,28 +98,34 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
                     orr, value_lane + static_cast<uint32_t>((16 * i + 4 * g + r) * static_cast<int>(a.ld_o) * ESZ));
     };
 
-    fetch(n - 1);
+    fetch(n - 1, smem + (DIRECT && ((n - 1) & 1) ? BUF : 0));
     for (int c = n - 1; c >= 0; --c) {
-        kraw.land(Kl, tid);
-        qraw.land(Ql, tid);
+        char* buf = smem + (DIRECT && (c & 1) ? BUF : 0);
+        const u32x4* Tl = reinterpret_cast<const u32x4*>(buf);   // [2][kBlocks][3][64]: the triangle, P
+        const ChunkRec* rec = reinterpret_cast<const ChunkRec*>(buf + 2 * TKB * 1024);
+        uint16_t* Kl = reinterpret_cast<uint16_t*>(buf + BKB * 1024);
+        uint16_t* Ql = Kl + N * C * KT;
+        if constexpr (!DIRECT) {
+            kraw.land(Kl, tid);
+            qraw.land(Ql, tid);
 #pragma unroll
-        for (int p = 0; p < TP; ++p)
-            if (p * NW + wave < kBlocks * 3) Tl[p * THREADS + tid] = traw[p];
-#pragma unroll
-        for (int p = 0; p < RECP; ++p) reinterpret_cast<uint32_t*>(rec)[p * THREADS + tid] = recraw[p];
-        lds_barrier();
+            for (int p = 0; p < (BKB + NW - 1) / NW; ++p)
+                if (p * NW + wave < BKB) reinterpret_cast<u32x4*>(buf)[p * THREADS + tid] = braw[p];
+        } else {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
         f32x4 dO[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r) dO[i][r] = one_value<T>(oraw[4 * i + r]);
-        if (c > 0) fetch(c - 1);
+        lds_barrier();
+        if (c > 0) fetch(c - 1, smem + (DIRECT && !(c & 1) ? BUF : 0));
 
         const uint64_t starts = uniform(rec->starts), bad = uniform(rec->bad);
         const int first_start = starts ? __builtin_ctzll(starts) : C;
         const int last_start = starts ? 63 - __builtin_clzll(starts) : 0;
         store_state(a.dstates + (bh * n + c) * cells);
-        __builtin_amdgcn_sched_barrier(0);
 
         // Rows whose gradient is not finite take no part, with the rest of their document
         uint64_t sick = 0;
@@ -135,67 +148,46 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
                 for (int r = 0; r < 4; ++r) dO[i][r] = keep_if(!((sick >> (16 * i + 4 * g + r)) & 1), dO[i][r]);
         }
 
-        // K dS and Q K^T
-        f32x4 ks[4], pq[4][4];   // pq[it][is]: rows t of tile it, columns s of tile is
+        // K dS
+        f32x4 ks[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            ks[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) pq[i][j] = f32x4{0, 0, 0, 0};
-        }
+        for (int i = 0; i < 4; ++i) ks[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < STEPS; ++j) {
-            __builtin_amdgcn_sched_barrier(0);
-            const Frag<3> sf = split(S[2 * j], S[2 * j + 1]);
-            Frag<N> kf[4], qf[4];
+            Frag<N> kf[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                kf[i] = rows_frag<N, ROW>(Kl, 16 * i + m, 32 * j + 8 * g);
-                qf[i] = rows_frag<N, ROW>(Ql, 16 * i + m, 32 * j + 8 * g);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) product<3>(ks[i], kf[i], sf);
-#pragma unroll
-            for (int it = 0; it < 4; ++it)
-#pragma unroll
-                for (int is = 0; is <= it; ++is) product<3>(pq[it][is], qf[it], kf[is]);
+            for (int i = 0; i < 4; ++i) kf[i] = rows_frag<N, KT>(Kl, 16 * i + m, 4 * j + g);
+            products<3, 4>(ks, kf, split(S[2 * j], S[2 * j + 1]));
         }
-        __builtin_amdgcn_sched_barrier(0);
 
         // dU
+        auto block = [&](int which, int i, int j) {
+            Frag<3> f;
+#pragma unroll
+            for (int p = 0; p < 3; ++p) f.p[p] = Tl[((which * kBlocks + high_block(i, j)) * 3 + p) * 64 + lane];
+            return f;
+        };
         f32x4 U[4];
         {
-            f32x4 th[4], tl[4];
-            Frag<3> of[2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                th[i] = four(rec->hi + 16 * i + 4 * g);
-                tl[i] = four(rec->lo + 16 * i + 4 * g);
+                const f32x4 outof = four(rec->outof + 16 * i + 4 * g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) U[i][r] = keep_if(16 * i + 4 * g + r >= last_start, outof[r] * ks[i][r]);
             }
+            Frag<3> pf[4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) of[j] = split(dO[2 * j], dO[2 * j + 1]);
+            for (int j = 1; j >= 0; --j) {
+                const Frag<3> of = split(dO[2 * j], dO[2 * j + 1]);
+                const int tiles = j ? 4 : 2;
 #pragma unroll
-            for (int is = 0; is < 4; ++is) {
-                const f32x4 outof = four(rec->outof + 16 * is + 4 * g);
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    U[is][r] = keep_if(16 * is + 4 * g + r >= last_start, outof[r] * ks[is][r]);
-                const int s = 16 * is + m, end = doc_end(starts, s);
-                const float sh = rec->hi[s], sl = rec->lo[s];
-                f32x4 P[4];
-#pragma unroll
-                for (int it = is & 2; it < 4; ++it)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int t = 16 * it + 4 * g + r;
-                        const float d = exp2_fast((th[it][r] - sh) + (tl[it][r] - sl));
-                        P[it][r] = it >= is ? keep_if(t >= s && t < end, a.scale * pq[it > is ? it : is][is][r] * d) : 0.0f;
-                    }
-#pragma unroll
-                for (int j = is / 2; j < 2; ++j) {
-                    const Frag<3> pf = split(P[2 * j], P[2 * j + 1]);
-                    if constexpr (N == 1) product<3>(U[is], pf, Frag<1>{{of[j].p[0]}});   // dO as stored is one piece
-                    else product<3>(U[is], pf, of[j]);
+                for (int i = 0; i < tiles; ++i) pf[i] = block(1, i, j);
+                if constexpr (N == 1) {   // dO as stored is one piece
+                    if (j) products<3, 4>(U, pf, Frag<1>{{of.p[0]}});
+                    else products<3, 2>(U, pf, Frag<1>{{of.p[0]}});
+                } else {
+                    if (j) products<3, 4>(U, pf, of);
+                    else products<3, 2>(U, pf, of);
                 }
             }
         }
@@ -231,17 +223,17 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
         // beta dX, then with what the entering state has kept; the same of dO
         f32x4 X[4];
         {
-            const Frag<3> uf[2] = {split(U[0], U[1]), split(U[2], U[3])};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) X[i] = f32x4{0, 0, 0, 0};
+            Frag<3> tf[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tf[i] = block(0, i, 1);
+            products<3, 4>(X, tf, split(U[2], U[3]));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tf[i] = block(0, i, 0);
+            products<3, 2>(X, tf, split(U[0], U[1]));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                X[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int j = i / 2; j < 2; ++j) {
-                    Frag<3> tf;
-#pragma unroll
-                    for (int p = 0; p < 3; ++p) tf.p[p] = Tl[(high_block(i, j) * 3 + p) * 64 + lane];
-                    product<3>(X[i], tf, uf[j]);
-                }
                 const f32x4 beta = four(rec->beta + 16 * i + 4 * g), into = four(rec->into + 16 * i + 4 * g);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -251,7 +243,6 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
                 }
             }
         }
-        __builtin_amdgcn_sched_barrier(0);
 
         // dS
         const float keep = rec->keep;
@@ -259,21 +250,28 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
         for (int i = 0; i < 2 * STEPS; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r) S[i][r] = keep_if(starts == 0, keep * S[i][r]);
-        const Frag<3> xf[2] = {split(X[0], X[1]), split(X[2], X[3])};
-        const Frag<3> of[2] = {split(dO[0], dO[1]), split(dO[2], dO[3])};
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j) {
+            const Frag<3> xf = split(X[2 * j], X[2 * j + 1]), of = split(dO[2 * j], dO[2 * j + 1]);
 #pragma unroll
-            for (int i = 0; i < 2 * STEPS; ++i) {
-                Frag<N> kf = cols_frag<N, ROW>(Kl, j, g, m, state_cols4(i, m));
-                Frag<N> qf = cols_frag<N, ROW>(Ql, j, g, m, state_cols4(i, m));
-                if (any_sick) {
-                    drop_rows<N>(kf, j, g, drop);
-                    drop_rows<N>(qf, j, g, drop);
+            for (int i0 = 0; i0 < 2 * STEPS; i0 += 4) {
+                Frag<N> kf[4], qf[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    kf[i] = cols_frag<N, KT>(Kl, j, g, m, state_cols4(i0 + i, m));
+                    qf[i] = cols_frag<N, KT>(Ql, j, g, m, state_cols4(i0 + i, m));
                 }
-                product<3>(S[i], qf, of[j]);
-                product<3>(S[i], kf, xf[j]);
+                if (any_sick) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        drop_rows<N>(kf[i], j, g, drop);
+                        drop_rows<N>(qf[i], j, g, drop);
+                    }
+                }
+                products<3, 4>(S + i0, qf, of);
+                products<3, 4>(S + i0, kf, xf);
             }
+        }
         if (any_sick) {
             const bool dead = (sick & 1) != 0 && first_start > 0;
 #pragma unroll
@@ -281,7 +279,7 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
 #pragma unroll
                 for (int r = 0; r < 4; ++r) S[i][r] = nan_if(dead, S[i][r]);
         }
-        lds_barrier();
+        if constexpr (!DIRECT) lds_barrier();
     }
     if (a.d_initial_state) store_state(a.d_initial_state + bh * cells);
 }

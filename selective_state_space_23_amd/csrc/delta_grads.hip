@@ -73,6 +73,24 @@ __device__ __forceinline__ Frag<N> token_frag(const uint16_t* lds, int row, int 
     return f;
 }
 
+// The same of column m, by transposing reads.
+template <int N>
+__device__ __forceinline__ Frag<N> token_cols(const uint16_t* lds, int j, int g, int m, int ch4) {
+    Frag<N> f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        f.p[i] = transposed(lds + (i * C + 32 * j + 4 * g + m / 4) * kRowP + ch4, 16 * kRowP);
+    return f;
+}
+// Row `row` of planes [N][C][kRowV], eight columns from `ch` on.
+template <int N>
+__device__ __forceinline__ Frag<N> plane_frag(const uint16_t* lds, int row, int ch) {
+    Frag<N> f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) f.p[i] = *reinterpret_cast<const u32x4*>(lds + (i * C + row) * kRowV + ch);
+    return f;
+}
+
 template <int N>
 __device__ __forceinline__ void clear_if(Frag<N>& f, bool out) {
     const uint32_t on = out ? 0u : ~0u;
@@ -87,7 +105,6 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
     constexpr int N = kPieces<T>, ESZ = sizeof(T), STEPS = KT / 32;
     constexpr int OUT = N == 1 ? 2 : 3;
     using KQ = Tile<T, KT, kThreads, VEC>;
-    constexpr int ROW = KQ::ROW;
     constexpr int PLANE_V = C * kRowV, PLANE_P = C * kRowP;
     constexpr size_t PARTS = 2 * kWaves * C * 4;
     constexpr size_t ZERO = larger(2 * KQ::kBytes, size_t(2) * OUT * PLANE_V * 2);
@@ -98,7 +115,7 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
     __shared__ float ends[kWaves];
     __shared__ uint64_t odd_rows[kWaves];
     uint16_t* Kl = reinterpret_cast<uint16_t*>(region0);
-    uint16_t* Ql = Kl + N * C * ROW;
+    uint16_t* Ql = Kl + N * C * KT;
     uint16_t* Ul = reinterpret_cast<uint16_t*>(region0);          // [OUT][C][kRowV]
     uint16_t* Xl = Ul + OUT * PLANE_V;
     const u32x4* Tl = reinterpret_cast<const u32x4*>(region1);
@@ -199,8 +216,8 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                     const Frag<3> sf = split(s0, s1), df = split(d0, d1);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const Frag<N> kf = rows_frag<N, ROW>(Kl, 16 * i + m, 32 * j + 8 * g);
-                        const Frag<N> qf = rows_frag<N, ROW>(Ql, 16 * i + m, 32 * j + 8 * g);
+                        const Frag<N> kf = rows_frag<N, KT>(Kl, 16 * i + m, 4 * j + g);
+                        const Frag<N> qf = rows_frag<N, KT>(Ql, 16 * i + m, 4 * j + g);
                         product<3>(ks[i], kf, sf);
                         product<3>(qs[i], qf, sf);
                         product<3>(kd[i], kf, df);
@@ -255,10 +272,10 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                         for (int is = 0; is < 4; ++is) P[is] = f32x4{0, 0, 0, 0};
 #pragma unroll
                         for (int j = 0; j < STEPS; ++j) {
-                            const Frag<N> qf = rows_frag<N, ROW>(Ql, 16 * it + m, 32 * j + 8 * g);
+                            const Frag<N> qf = rows_frag<N, KT>(Ql, 16 * it + m, 4 * j + g);
 #pragma unroll
                             for (int is = 0; is <= it; ++is)
-                                product<3>(P[is], rows_frag<N, ROW>(Kl, 16 * is + m, 32 * j + 8 * g), qf);
+                                product<3>(P[is], rows_frag<N, KT>(Kl, 16 * is + m, 4 * j + g), qf);
                         }
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
@@ -304,10 +321,10 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                         for (int it = 0; it < 4; ++it) P[it] = f32x4{0, 0, 0, 0};
 #pragma unroll
                         for (int j = 0; j < STEPS; ++j) {
-                            const Frag<N> kf = rows_frag<N, ROW>(Kl, 16 * is + m, 32 * j + 8 * g);
+                            const Frag<N> kf = rows_frag<N, KT>(Kl, 16 * is + m, 4 * j + g);
 #pragma unroll
                             for (int it = is; it < 4; ++it)
-                                product<3>(P[it], rows_frag<N, ROW>(Ql, 16 * it + m, 32 * j + 8 * g), kf);
+                                product<3>(P[it], rows_frag<N, KT>(Ql, 16 * it + m, 4 * j + g), kf);
                         }
                         const int s = 16 * is + m, stop = doc_end(starts, s);
                         const float sh = rec->hi[s], sl = rec->lo[s];
@@ -431,8 +448,8 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
             const int it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, is = tile - it * (it + 1) / 2;
             f32x4 P = {0, 0, 0, 0}, G = {0, 0, 0, 0};
             for (int j = 0; j < vsteps; ++j) {
-                const Frag<OUT> uf = rows_frag<OUT, kRowV>(Ul, 16 * is + m, 32 * j + 8 * g);
-                const Frag<OUT> xf = rows_frag<OUT, kRowV>(Xl, 16 * it + m, 32 * j + 8 * g);
+                const Frag<OUT> uf = plane_frag<OUT>(Ul, 16 * is + m, 32 * j + 8 * g);
+                const Frag<OUT> xf = plane_frag<OUT>(Xl, 16 * it + m, 32 * j + 8 * g);
                 product<OUT>(P, dout_frag(it, j), uf);
                 product<OUT>(G, xf, uf);
             }
@@ -468,8 +485,8 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     product<OUT>(os[i], dout_frag(i, j), sf);
-                    product<OUT>(xs[i], rows_frag<OUT, kRowV>(Xl, 16 * i + m, 32 * j + 8 * g), sf);
-                    product<OUT>(us[i], rows_frag<OUT, kRowV>(Ul, 16 * i + m, 32 * j + 8 * g), df);
+                    product<OUT>(xs[i], plane_frag<OUT>(Xl, 16 * i + m, 32 * j + 8 * g), sf);
+                    product<OUT>(us[i], plane_frag<OUT>(Ul, 16 * i + m, 32 * j + 8 * g), df);
                 }
             }
 #pragma unroll
@@ -499,12 +516,12 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
         if (16 * wave < KT) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const Frag<N> kf = cols_frag<N, ROW>(Kl, j, g, m, 16 * wave + 4 * (m % 4));
-                const Frag<N> qf = cols_frag<N, ROW>(Ql, j, g, m, 16 * wave + 4 * (m % 4));
+                const Frag<N> kf = cols_frag<N, KT>(Kl, j, g, m, 16 * wave + 4 * (m % 4));
+                const Frag<N> qf = cols_frag<N, KT>(Ql, j, g, m, 16 * wave + 4 * (m % 4));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (j <= i / 2) product<OUT>(dq[i], token_frag<OUT>(Pl, 16 * i + m, j, g), kf);
-                    if (j >= i / 2) product<OUT>(dk[i], cols_frag<OUT, kRowP>(Pl, j, g, m, 16 * i + 4 * (m % 4)), qf);
+                    if (j >= i / 2) product<OUT>(dk[i], token_cols<OUT>(Pl, j, g, m, 16 * i + 4 * (m % 4)), qf);
                     product<OUT>(dk[i], token_frag<OUT>(Nl, 16 * i + m, j, g), kf);
                 }
             }

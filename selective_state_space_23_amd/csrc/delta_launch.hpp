@@ -36,7 +36,8 @@ struct DeltaArgs {
     // workspace written by the first pass
     char* chunks;               // one record per (row, value head, chunk)
     char* solve;                // the solved triangles, in the order the matrix cores read them
-    char* solve_t;              // their transposes (backward)
+    char* solve_t;              // the backward's, transposed
+    char* pairs;                // scale D o Q K^T in the same order (forward), or its transpose (backward); or null
     int64_t batch, seqlen, ld_q, ld_k, ld_v, ld_o;
     int kheads, vheads, kdim, vdim;
     int nchunks;
@@ -67,6 +68,7 @@ struct DeltaUpdateArgs {
 // Bytes of each workspace part for one (row, value head, chunk).
 size_t delta_chunk_bytes();
 size_t delta_solve_bytes();
+size_t delta_pairs_bytes(bool bf16, bool backward);
 
 hipError_t launch_delta_prepare(const DeltaArgs& a);
 hipError_t launch_delta_fwd(const DeltaArgs& a);

@@ -11,7 +11,8 @@
 // and beta = 1 the powers of A that a doubling scheme adds up reach 10^17, a substitution's
 // terms stay at 1) and the blocks below them as T_ij = -T_ii sum_m A_im T_mj on the fp32 matrix
 // instructions, and writes the triangle in three bf16 pieces in the order in which the later
-// passes' matrix instructions read it.
+// passes' matrix instructions read it.  The weights P = scale D o Q K^T of the values in the outputs go the
+// same way (formed by every wave of the later passes instead: 440 vector instructions a chunk each).
 //
 // gamma is summed in float64 and kept as two floats: gamma_t - gamma_s is
 // then right to float32 of itself however far the sum has run.  A decay below
@@ -26,6 +27,9 @@ namespace mamba {
 
 size_t delta_chunk_bytes() { return (sizeof(delta::ChunkRec) + 255) / 256 * 256; }
 size_t delta_solve_bytes() { return static_cast<size_t>(delta::kSolveBytes); }
+size_t delta_pairs_bytes(bool bf16, bool backward) {
+    return static_cast<size_t>(delta::pairs_bytes(bf16 && !backward ? 2 : 3));
+}
 
 namespace {
 
@@ -83,11 +87,13 @@ __global__ __launch_bounds__(64) void prepare_kernel(DeltaArgs a, size_t rec_byt
     const T* kp = static_cast<const T*>(a.k);
     const Rsrc kr = rows_rsrc<ESZ>(kp, (b * a.seqlen + t0) * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k,
                                    a.kdim);
-    f32x4 acc[4][4];
+    const Rsrc qr = rows_rsrc<ESZ>(static_cast<const T*>(a.q), (b * a.seqlen + t0) * a.ld_q + static_cast<int64_t>(hk) * a.kdim,
+                                   rows, a.ld_q, a.kdim);
+    f32x4 acc[4][4], qk[4][4];   // rows t of tile i, columns s of tile j <= i
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+        for (int j = 0; j < 4; ++j) acc[i][j] = qk[i][j] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < KT / 32; ++j) {
         Eight<T, VEC> raw[4];
@@ -101,6 +107,17 @@ __global__ __launch_bounds__(64) void prepare_kernel(DeltaArgs a, size_t rec_byt
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int n = 0; n <= i; ++n) product<3>(acc[i][n], f[i], f[n]);
+        if (a.pairs) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                raw[i].load(qr, static_cast<uint32_t>((16 * i + m) * static_cast<int>(a.ld_q) * ESZ), 32 * j + 8 * g, a.kdim);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const Frag<N> q = raw[i].frag();
+#pragma unroll
+                for (int n = 0; n <= i; ++n) product<3>(qk[i][n], q, f[n]);
+            }
+        }
     }
     // squared norms tell which keys are not finite
 #pragma unroll
@@ -132,6 +149,54 @@ __global__ __launch_bounds__(64) void prepare_kernel(DeltaArgs a, size_t rec_byt
         rec->bad = bad;
     }
     __syncthreads();
+
+    // The lower tiles in As, out in N pieces in the order of an operand: rows (or, transposed, columns) in lanes
+    auto emit = [&](char* to, auto pieces, bool transposed) {
+        constexpr int P = decltype(pieces)::value;
+        u32x4* out = reinterpret_cast<u32x4*>(to + id * pairs_bytes(P));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (transposed ? j < i / 2 : j > i / 2) continue;
+                f32x4 x, y;
+                if (transposed) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] = As[(32 * j + 4 * g + e) * kRowA + 16 * i + m];
+                        y[e] = As[(32 * j + 16 + 4 * g + e) * kRowA + 16 * i + m];
+                    }
+                } else {
+                    x = four(As + (16 * i + m) * kRowA + 32 * j + 4 * g);
+                    y = four(As + (16 * i + m) * kRowA + 32 * j + 16 + 4 * g);
+                }
+                const Frag<P> f = split_out<P>(x, y);
+                const int blk = transposed ? high_block(i, j) : low_block(i, j);
+#pragma unroll
+                for (int n = 0; n < P; ++n) out[(blk * P + n) * 64 + lane] = f.p[n];
+            }
+        __syncthreads();
+    };
+    if (a.pairs) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f32x4 th = four(hi + 16 * i + 4 * g), tl = four(lo + 16 * i + 4 * g);
+#pragma unroll
+            for (int j = 0; j <= (i | 1); ++j) {
+                const int s = 16 * j + m, end = doc_end(starts, s);
+                const float sh = hi[s], sl = lo[s];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = 16 * i + 4 * g + r;
+                    const float d = exp2_fast((th[r] - sh) + (tl[r] - sl));
+                    As[t * kRowA + s] = j <= i ? keep_if(s <= t && t < end, a.scale * (d * qk[i][j <= i ? j : i][r])) : 0.0f;
+                }
+            }
+        }
+        __syncthreads();
+        if constexpr (BWD) emit(a.pairs, std::integral_constant<int, 3>{}, true);
+        else emit(a.pairs, std::integral_constant<int, N == 1 ? 2 : 3>{}, false);
+    }
 
 #pragma unroll
     for (int which = 0; which < (BWD ? 2 : 1); ++which) {
@@ -212,29 +277,7 @@ __global__ __launch_bounds__(64) void prepare_kernel(DeltaArgs a, size_t rec_byt
                 }
             }
         __syncthreads();
-        u32x4* out = reinterpret_cast<u32x4*>((which ? a.solve_t : a.solve) + id * kSolveBytes);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if (which ? j < i / 2 : j > i / 2) continue;
-                f32x4 x, y;
-                if (which) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[e] = As[(32 * j + 4 * g + e) * kRowA + 16 * i + m];
-                        y[e] = As[(32 * j + 16 + 4 * g + e) * kRowA + 16 * i + m];
-                    }
-                } else {
-                    x = four(As + (16 * i + m) * kRowA + 32 * j + 4 * g);
-                    y = four(As + (16 * i + m) * kRowA + 32 * j + 16 + 4 * g);
-                }
-                const Frag<3> f = split(x, y);
-                const int blk = which ? high_block(i, j) : low_block(i, j);
-#pragma unroll
-                for (int n = 0; n < 3; ++n) out[(blk * 3 + n) * 64 + lane] = f.p[n];
-            }
-        __syncthreads();
+        emit(which ? a.solve_t : a.solve, std::integral_constant<int, 3>{}, which != 0);
     }
 }
 

@@ -29,6 +29,7 @@ constexpr int kTiles = C / 16;            // token tiles of a chunk
 constexpr int kBlocks = 6;                // 16 x 32 pieces of a 64 x 64 triangle that are not all zero
 constexpr uint32_t kPast = 0x7fffff00u;   // a byte offset behind any buffer
 constexpr int64_t kSolveBytes = kBlocks * 3 * 1024;   // a chunk's solved triangle in three pieces
+constexpr int64_t pairs_bytes(int pieces) { return kBlocks * pieces * 1024; }
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -71,6 +72,19 @@ __device__ __forceinline__ void product(f32x4& acc, const Frag<NA>& a, const Fra
 #pragma unroll
         for (int i = 0; i < NA; ++i)
             if (s - i >= 0 && s - i < NB) acc = mfma(a.p[i], b.p[s - i], acc);
+}
+
+// The same for M accumulators in turn, so that none waits for its own last product (44 cycles against 16).
+template <int ORDER, int M, int NA, int NB>
+__device__ __forceinline__ void products(f32x4* acc, const Frag<NA>* a, const Frag<NB>& b) {
+#pragma unroll
+    for (int s = ORDER - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB) {
+#pragma unroll
+                for (int k = 0; k < M; ++k) acc[k] = mfma(a[k].p[i], b.p[s - i], acc[k]);
+            }
 }
 
 // The bf16 pieces of pairs of floats.
@@ -195,11 +209,43 @@ __device__ __forceinline__ void store_one(Rsrc rs, uint32_t off, float v) {
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rs, off, 0, 0);
 }
 
-// A chunk of q or k on its way to LDS as [pieces][C][KT + 8] bf16: 16-byte pieces of 16
-// rows meet no bank twice.
+// A chunk of q or k in LDS: [pieces][C][KT] bf16, rows of KT / 8 pieces of 16 bytes, piece q of row r
+// at place q ^ swizzle(r).  Then neither 16 rows' pieces of one number (operands with the rows
+// in lanes) nor the 4 x 4 half pieces that 16 lanes read to transpose meet on a bank, and a row is as long as
+// what goes to LDS straight from memory, 1 KB a wave.
+template <int KT> __device__ __forceinline__ int swizzle(int r) {
+    return KT == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : ((r & 2) << 1) | ((r >> 2) & 3);
+}
+template <int KT> __device__ __forceinline__ int place(int r, int q) { return r * KT + ((q ^ swizzle<KT>(r)) << 3); }
+
+typedef __attribute__((address_space(3))) void* Lds;
+
+// Straight from memory, by the NW waves of a workgroup: bf16 rows of whole 16-byte pieces.
+template <int KT, int NW>
+__device__ __forceinline__ void rows_to_lds(uint16_t* lds, Rsrc rs, int64_t ld, int width, int wave, int lane) {
+    constexpr int PIECES = KT / 8, ROWS = 64 / PIECES;
+#pragma unroll
+    for (int n = 0; n < C / ROWS / NW; ++n) {
+        const int first = (n * NW + wave) * ROWS, r = first + lane / PIECES;
+        const int q = (lane % PIECES) ^ swizzle<KT>(r);
+        const uint32_t off = q * 8 < width ? static_cast<uint32_t>(r * static_cast<int>(ld) * 2 + q * 16) : kPast;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (Lds)(lds + first * KT), 16, off, 0, 0, 0);
+    }
+}
+// KB of consecutive memory, piece p by wave p % NW; what lies behind `rs` reads as zeros.
+template <int KB, int NW>
+__device__ __forceinline__ void block_to_lds(char* lds, Rsrc rs, int wave, int lane) {
+#pragma unroll
+    for (int p = 0; p < (KB + NW - 1) / NW; ++p)
+        if (p * NW + wave < KB)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (Lds)(lds + (p * NW + wave) * 1024), 16,
+                                                     ((p * NW + wave) * 64 + lane) * 16, 0, 0, 0);
+}
+
+// Through registers: any type and alignment.
 template <typename T, int KT, int THREADS, bool VEC> struct Tile {
-    static constexpr int N = kPieces<T>, ROW = KT + 8, PER = C * KT / 8 / THREADS;
-    static constexpr size_t kBytes = size_t(N) * C * ROW * 2;
+    static constexpr int N = kPieces<T>, PER = C * KT / 8 / THREADS;
+    static constexpr size_t kBytes = size_t(N) * C * KT * 2;
     Eight<T, VEC> raw[PER];
     __device__ __forceinline__ void fetch(Rsrc rs, int64_t ld, int width, int tid) {
 #pragma unroll
@@ -208,50 +254,44 @@ template <typename T, int KT, int THREADS, bool VEC> struct Tile {
             raw[p].load(rs, static_cast<uint32_t>(t * static_cast<int>(ld) * static_cast<int>(sizeof(T))), ch, width);
         }
     }
-    __device__ __forceinline__ void land(uint16_t* lds, int tid) const {
-#pragma unroll
-        for (int p = 0; p < PER; ++p) {
-            const int x = p * THREADS + tid, t = x / (KT / 8), ch = x % (KT / 8) * 8;
-            const Frag<N> f = raw[p].frag();
-#pragma unroll
-            for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(lds + (i * C + t) * ROW + ch) = f.p[i];
-        }
-    }
-    // The same with the rows of `out` as zeros.
+    __device__ __forceinline__ void land(uint16_t* lds, int tid) const { land_without(lds, tid, 0); }
+    // With the rows of `out` as zeros.
     __device__ __forceinline__ void land_without(uint16_t* lds, int tid, uint64_t out) const {
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
-            const int x = p * THREADS + tid, t = x / (KT / 8), ch = x % (KT / 8) * 8;
+            const int x = p * THREADS + tid, t = x / (KT / 8), q = x % (KT / 8);
             const Frag<N> f = raw[p].frag();
             const uint32_t on = (out >> t) & 1 ? 0u : ~0u;
 #pragma unroll
-            for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(lds + (i * C + t) * ROW + ch) = f.p[i] & on;
+            for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(lds + i * C * KT + place<KT>(t, q)) = f.p[i] & on;
         }
     }
 };
 
-// Operands from such a tile: row `row`, eight channels from `ch` on ...
-template <int N, int ROW>
-__device__ __forceinline__ Frag<N> rows_frag(const uint16_t* lds, int row, int ch) {
+// Operands from such a tile: row `row`, its q-th eight channels ...
+template <int N, int KT>
+__device__ __forceinline__ Frag<N> rows_frag(const uint16_t* lds, int row, int q) {
     Frag<N> f;
+    const uint16_t* at = lds + place<KT>(row, q);
 #pragma unroll
-    for (int i = 0; i < N; ++i) f.p[i] = *reinterpret_cast<const u32x4*>(lds + (i * C + row) * ROW + ch);
+    for (int i = 0; i < N; ++i) f.p[i] = *reinterpret_cast<const u32x4*>(at + i * C * KT);
     return f;
 }
-// ... or column `col` of rows 32 j + 4 g + 0..3 and 16 further, by transposing reads: 16 lanes
-// read four rows of 16 columns, lane m giving the address of row m / 4, columns `col4`.. + 3, and
-// getting the m-th of the 16 columns.
-template <int N, int ROW>
-__device__ __forceinline__ Frag<N> cols_frag(const uint16_t* lds, int j, int g, int m, int col4) {
+// ... or a column of rows 32 j + 4 g + 0..3 and 16 further, by transposing reads: 16 lanes read four rows
+// of 16 columns, lane m giving the address of row m / 4, channels `ch4`.. + 3, and getting the m-th of the 16
+// columns.
+__device__ __forceinline__ u32x4 transposed(const uint16_t* at, int rows16) {
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at));
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + rows16));
+    const u32x2 xw = __builtin_bit_cast(u32x2, x), yw = __builtin_bit_cast(u32x2, y);
+    return u32x4{xw[0], xw[1], yw[0], yw[1]};
+}
+template <int N, int KT>
+__device__ __forceinline__ Frag<N> cols_frag(const uint16_t* lds, int j, int g, int m, int ch4) {
     Frag<N> f;
+    const uint16_t* at = lds + place<KT>(32 * j + 4 * g + m / 4, ch4 >> 3) + (ch4 & 4);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const uint16_t* at = lds + (i * C + 32 * j + 4 * g + m / 4) * ROW + col4;
-        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at));
-        const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + 16 * ROW));
-        const u32x2 xw = __builtin_bit_cast(u32x2, x), yw = __builtin_bit_cast(u32x2, y);
-        f.p[i] = u32x4{xw[0], xw[1], yw[0], yw[1]};
-    }
+    for (int i = 0; i < N; ++i) f.p[i] = transposed(at + i * C * KT, 16 * KT);
     return f;
 }
 // Zeros in the slots of the rows of `out`.
