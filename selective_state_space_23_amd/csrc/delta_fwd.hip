@@ -155,12 +155,16 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const f32x4 into = four(rec->into + 16 * i + 4 * g);
+            if (starts == 0) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const bool old = 16 * i + 4 * g + r < first_start;
-                R[i][r] = vals[4 * i + r] - keep_if(old, into[r] * ks[i][r]);
-                odd |= not_finite(R[i][r]);
+                for (int r = 0; r < 4; ++r) R[i][r] = __builtin_fmaf(-into[r], ks[i][r], vals[4 * i + r]);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    R[i][r] = vals[4 * i + r] - keep_if(16 * i + 4 * g + r < first_start, into[r] * ks[i][r]);
             }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) odd |= not_finite(R[i][r]);
         }
         // Values that are not finite: the rows from there to the document's end take no part, and give NaN
         uint64_t lost = 0;
@@ -285,6 +289,310 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
     if (a.final_state) store_state(a.final_state + bh * cells);
 }
 
+// The same for bf16 in whole 16-byte pieces, two waves for every 16 columns: one walks the chain
+// S -> R -> U -> S, which is what a row's time is, the other follows it by half a chunk with
+// everything that does not lead back to S: the outputs, from S and U as the first leaves them in LDS,
+// and all loads.  (One wave doing both, four to a workgroup: 64K tokens x 40 heads 6.0 ms; a chunk
+// then takes 1030 vector instructions, 182 matrix products and their waits one after the other.)
+//
+// Chunk c:  barrier;  A: the chain splits S, forms R;   the other loads chunk c + 1 and finishes O of c - 1;
+//           barrier;  B: the chain forms U, then S;     the other forms Q S, puts V of c + 1 in place.
+template <int KT, bool EMIT>
+__global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
+    constexpr int STEPS = KT / 32, NP = 2;                            // NP: pairs of waves
+    constexpr int TILE = C * KT * 2, TRI = kBlocks * 3 * 1024, PAIRS = kBlocks * 2 * 1024, REC = 2048;
+    __shared__ __align__(16) char smem[2 * TILE + 2 * TRI + 3 * REC + NP * 64 * 32 + NP * 64 * 8 +
+                                       (EMIT ? 2 * TILE + PAIRS + NP * (STEPS * 2048 + 4096) : 0)];
+    char* const Kb = smem;                       // [2] K
+    char* const Tb = Kb + 2 * TILE;              // [2] triangle
+    char* const Rb = Tb + 2 * TRI;               // [3] record
+    char* const Vb = Rb + 3 * REC;               // a lane's 16 values, packed
+    char* const Lb = Vb + NP * 64 * 32;          // a lane's lost rows
+    char* const Qb = Lb + NP * 64 * 8;           // [2] Q
+    char* const Pb = Qb + 2 * TILE;              // P
+    char* const Sb = Pb + PAIRS;                 // S's first two pieces, as operands
+    char* const Ub = Sb + NP * STEPS * 2048;     // U
+
+    const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), pair = wave & 1;
+    // workgroups of one head on one XCD (they are dealt out to the 8 in turn), which read its K, Q, T and P
+    const int64_t bh = quotient(blockIdx.x, 8 * cols) * 8 + (blockIdx.x & 7);
+    if (bh >= a.batch * a.vheads) return;
+    const int hv = remainder(bh, a.vheads), hk = quotient(hv, a.vheads / a.kheads);
+    const int64_t b = quotient(bh, a.vheads);
+    const int v = (remainder(blockIdx.x >> 3, cols) * NP + pair) * 16 + m;
+    const bool v_in = v < a.vdim;
+    const int n = a.nchunks;
+    auto rows_of = [&](int c) {
+        const int64_t left = a.seqlen - static_cast<int64_t>(c) * C;
+        return static_cast<int>(left < C ? left : C);
+    };
+    auto buffer = [&](char* first, int size, int c) { return first + (c & 1) * size; };
+
+    if (wave < NP) {
+        // ---- the chain
+        const int64_t cells = static_cast<int64_t>(a.kdim) * a.vdim;
+        const uint32_t state_lane = v_in ? v * 4 : kPast;
+        auto state_off = [&](int i, int r) { return state_lane + static_cast<uint32_t>(state_row(i, g, r) * a.vdim * 4); };
+        auto store_state = [&](float* to, const f32x4* S) {
+            const Rsrc rs = rsrc(to, cells * 4);
+#pragma unroll
+            for (int i = 0; i < 2 * STEPS; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][r]), rs, state_off(i, r), 0, 0);
+        };
+        f32x4 S[2 * STEPS];
+        {
+            const Rsrc rs = rsrc(a.initial_state + (a.initial_state ? bh * cells : 0), a.initial_state ? cells * 4 : 0);
+#pragma unroll
+            for (int i = 0; i < 2 * STEPS; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    S[i][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, state_off(i, r), 0, 0));
+        }
+        int third = 0;   // c % 3
+        for (int c = 0; c < n; ++c) {
+            const uint16_t* Kl = reinterpret_cast<const uint16_t*>(buffer(Kb, TILE, c));
+            const u32x4* Tl = reinterpret_cast<const u32x4*>(buffer(Tb, TRI, c));
+            const ChunkRec* rec = reinterpret_cast<const ChunkRec*>(Rb + third * REC);
+            third = third == 2 ? 0 : third + 1;
+            lds_barrier();
+            // A: R = V - exp(gamma) K S
+            f32x4 R[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) R[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < STEPS; ++j) {
+                const Frag<3> sf = split(S[2 * j], S[2 * j + 1]);
+                if constexpr (EMIT) {
+                    u32x4* to = reinterpret_cast<u32x4*>(Sb + (pair * STEPS + j) * 2048) + lane;
+                    to[0] = sf.p[0];
+                    to[64] = sf.p[1];
+                }
+                Frag<1> kf[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) kf[i] = rows_frag<1, KT>(Kl, 16 * i + m, 4 * j + g);
+                products<3, 4>(R, kf, sf);
+            }
+            if (a.states) store_state(a.states + (bh * n + c) * cells, S);
+            const uint64_t starts = uniform(rec->starts), bad = uniform(rec->bad);
+            const int first_start = starts ? __builtin_ctzll(starts) : C;
+            const u32x4* vals = reinterpret_cast<const u32x4*>(Vb + (pair * 64 + lane) * 32);
+            const u32x4 v01 = vals[0], v23 = vals[1];
+            float check = 0.0f;   // stays 0 as long as everything is finite
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 into = four(rec->into + 16 * i + 4 * g);
+                const uint32_t lo = (i < 2 ? v01 : v23)[2 * (i & 1)], hi = (i < 2 ? v01 : v23)[2 * (i & 1) + 1];
+                const f32x4 val = {__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u), __uint_as_float(hi << 16),
+                                   __uint_as_float(hi & 0xffff0000u)};
+                if (starts == 0) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) R[i][r] = __builtin_fmaf(-into[r], R[i][r], val[r]);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        R[i][r] = val[r] - keep_if(16 * i + 4 * g + r < first_start, into[r] * R[i][r]);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) check = __builtin_fmaf(R[i][r], 0.0f, check);
+            }
+            // Values that are not finite: the rows from there to the document's end take no part, and give NaN
+            uint64_t lost = 0;
+            const bool any_lost = bad != 0 || __ballot(not_finite(check)) != 0;
+            if (any_lost) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) lost |= uint64_t(not_finite(R[i][r])) << (16 * i + 4 * g + r);
+                lost |= __shfl_xor(lost, 16);
+                lost |= __shfl_xor(lost, 32);
+                lost = smear(lost | bad, starts);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) R[i][r] = keep_if(!((lost >> (16 * i + 4 * g + r)) & 1), R[i][r]);
+            }
+            const Frag<3> rf0 = split(R[0], R[1]), rf1 = split(R[2], R[3]);
+            lds_barrier();
+            // B: U = beta T R
+            f32x4 U[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) U[i] = f32x4{0, 0, 0, 0};
+            {
+                Frag<3> tf[4];
+                auto triangle = [&](int i, int j) {
+                    Frag<3> f;
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) f.p[p] = Tl[(low_block(i, j) * 3 + p) * 64 + lane];
+                    return f;
+                };
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tf[i] = triangle(i, 0);
+                products<3, 4>(U, tf, rf0);
+#pragma unroll
+                for (int i = 2; i < 4; ++i) tf[i] = triangle(i, 1);
+                products<3, 2>(U + 2, tf + 2, rf1);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 beta = four(rec->beta + 16 * i + 4 * g), outof = four(rec->outof + 16 * i + 4 * g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) U[i][r] *= beta[r];
+                if constexpr (EMIT) *reinterpret_cast<f32x4*>(Ub + ((pair * 4 + i) * 64 + lane) * 16) = U[i];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) U[i][r] *= outof[r];
+            }
+            if constexpr (EMIT) *reinterpret_cast<uint64_t*>(Lb + (pair * 64 + lane) * 8) = lost;
+            // S
+            if (starts == 0) {
+                const float keep = rec->keep;
+#pragma unroll
+                for (int i = 0; i < 2 * STEPS; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) S[i][r] *= keep;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2 * STEPS; ++i) S[i] = f32x4{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const Frag<3> uf = split(U[2 * j], U[2 * j + 1]);
+#pragma unroll
+                for (int i0 = 0; i0 < 2 * STEPS; i0 += 4) {
+                    Frag<1> kf[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kf[i] = cols_frag<1, KT>(Kl, j, g, m, state_cols4(i0 + i, m));
+                    if (bad != 0) {   // keys that are not finite: their rows of U are 0
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) drop_rows<1>(kf[i], j, g, bad);
+                    }
+                    products<3, 4>(S + i0, kf, uf);
+                }
+            }
+            if (any_lost) {
+                const bool dead = (lost >> (rows_of(c) - 1)) & 1;
+#pragma unroll
+                for (int i = 0; i < 2 * STEPS; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) S[i][r] = nan_if(dead, S[i][r]);
+            }
+        }
+        lds_barrier();
+        if (a.final_state) store_state(a.final_state + bh * cells, S);
+    } else {
+        // ---- loads and outputs
+        const uint32_t value_lane = v_in ? v * 2 : kPast;
+        uint32_t vraw[16];
+        auto fetch = [&](int c, int slot) {
+            const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, id = bh * n + c;
+            const int rows = rows_of(c);
+            const Rsrc kr = rows_rsrc<2>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k, a.kdim);
+            rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(buffer(Kb, TILE, c)), kr, a.ld_k, a.kdim, pair, lane);
+            block_to_lds<2, NP>(Rb + slot * REC, rsrc(a.chunks + id * rec_bytes, sizeof(ChunkRec)), pair, lane);
+            block_to_lds<kBlocks * 3, NP>(buffer(Tb, TRI, c), rsrc(a.solve + id * kSolveBytes, kSolveBytes), pair, lane);
+            if constexpr (EMIT) {
+                const Rsrc qr = rows_rsrc<2>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_q, a.kdim);
+                rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(buffer(Qb, TILE, c)), qr, a.ld_q, a.kdim, pair, lane);
+            }
+            const Rsrc vr = rows_rsrc<2>(a.v, first * a.ld_v + static_cast<int64_t>(hv) * a.vdim, rows, a.ld_v, a.vdim);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    vraw[4 * i + r] = load_one<bf16_t>(
+                        vr, value_lane + static_cast<uint32_t>((16 * i + 4 * g + r) * static_cast<int>(a.ld_v) * 2));
+        };
+        auto put_values = [&]() {
+            u32x4* to = reinterpret_cast<u32x4*>(Vb + (pair * 64 + lane) * 32);
+            u32x4 w[2];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i / 4][i % 4] = vraw[2 * i] | (vraw[2 * i + 1] << 16);
+            to[0] = w[0];
+            to[1] = w[1];
+        };
+        fetch(0, 0);
+        put_values();
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        f32x4 O[4];
+        auto outputs = [&](int c, int slot) {   // from Q S in O
+            const ChunkRec* rec = reinterpret_cast<const ChunkRec*>(Rb + slot * REC);
+            const uint64_t starts = uniform(rec->starts);
+            const int first_start = starts ? __builtin_ctzll(starts) : C;
+            const u32x4* Pl = reinterpret_cast<const u32x4*>(Pb);
+            const f32x4* Ul = reinterpret_cast<const f32x4*>(Ub + pair * 4096);
+            Frag<2> pf[4];
+            auto pairs = [&](int i, int j) {
+                Frag<2> f;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) f.p[p] = Pl[(low_block(i, j) * 2 + p) * 64 + lane];
+                return f;
+            };
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                pf[i] = pairs(i, 0);
+                const f32x4 into = four(rec->into + 16 * i + 4 * g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    O[i][r] = keep_if(16 * i + 4 * g + r < first_start, a.scale * into[r] * O[i][r]);
+            }
+            products<2, 4>(O, pf, split_rounded(Ul[lane], Ul[64 + lane]));
+#pragma unroll
+            for (int i = 2; i < 4; ++i) pf[i] = pairs(i, 1);
+            products<2, 2>(O + 2, pf + 2, split_rounded(Ul[128 + lane], Ul[192 + lane]));
+            const uint64_t lost = *reinterpret_cast<const uint64_t*>(Lb + (pair * 64 + lane) * 8);
+            if (__ballot(lost != 0) != 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) O[i][r] = nan_if((lost >> (16 * i + 4 * g + r)) & 1, O[i][r]);
+            }
+            const int64_t ldo = static_cast<int64_t>(a.vheads) * a.vdim;
+            const Rsrc orr = rows_rsrc<2>(a.out, (b * a.seqlen + static_cast<int64_t>(c) * C) * ldo + hv * a.vdim, rows_of(c),
+                                          ldo, a.vdim);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    store_one<bf16_t>(orr, value_lane + static_cast<uint32_t>((16 * i + 4 * g + r) * static_cast<int>(ldo) * 2),
+                                      O[i][r]);
+        };
+        int third = 0;
+        for (int c = 0; c < n; ++c) {
+            const int last = third == 0 ? 2 : third - 1, next = third == 2 ? 0 : third + 1;
+            lds_barrier();
+            // A
+            if (c + 1 < n) fetch(c + 1, next);
+            if constexpr (EMIT) {
+                if (c > 0) outputs(c - 1, last);
+            }
+            lds_barrier();
+            // B
+            if constexpr (EMIT) {
+                block_to_lds<kBlocks * 2, NP>(Pb, rsrc(a.pairs + (bh * n + c) * pairs_bytes(2), pairs_bytes(2)), pair, lane);
+                const uint16_t* Ql = reinterpret_cast<const uint16_t*>(buffer(Qb, TILE, c));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) O[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < STEPS; ++j) {
+                    const u32x4* from = reinterpret_cast<const u32x4*>(Sb + (pair * STEPS + j) * 2048) + lane;
+                    const Frag<2> sf = {{from[0], from[64]}};
+                    Frag<1> qf[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) qf[i] = rows_frag<1, KT>(Ql, 16 * i + m, 4 * j + g);
+                    products<2, 4>(O, qf, sf);
+                }
+            }
+            if (c + 1 < n) put_values();
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            third = next;
+        }
+        lds_barrier();
+        if constexpr (EMIT) outputs(n - 1, third == 0 ? 2 : third - 1);
+    }
+}
+
 template <typename T, int KT, int NW, bool VEC>
 hipError_t launch(const DeltaArgs& a) {
     const int cols = (a.vdim + 16 * NW - 1) / (16 * NW);
@@ -298,6 +606,19 @@ hipError_t launch(const DeltaArgs& a) {
     return hipGetLastError();
 }
 
+template <int KT>
+hipError_t launch_pairs(const DeltaArgs& a) {
+    const int cols = (a.vdim + 31) / 32;
+    const dim3 grid(static_cast<unsigned>((a.batch * a.vheads + 7) / 8 * 8 * cols));
+    if (a.out)
+        hipLaunchKernelGGL((fwd_pairs_kernel<KT, true>), grid, dim3(256), 0, a.stream, a,
+                           static_cast<int64_t>(delta_chunk_bytes()), cols);
+    else
+        hipLaunchKernelGGL((fwd_pairs_kernel<KT, false>), grid, dim3(256), 0, a.stream, a,
+                           static_cast<int64_t>(delta_chunk_bytes()), cols);
+    return hipGetLastError();
+}
+
 template <typename T, bool VEC>
 hipError_t by_width(const DeltaArgs& a) {
     return a.kdim > 64 ? launch<T, 128, 4, VEC>(a) : launch<T, 64, 4, VEC>(a);
@@ -306,7 +627,8 @@ hipError_t by_width(const DeltaArgs& a) {
 }  // namespace
 
 hipError_t launch_delta_fwd(const DeltaArgs& a) {
-    if (a.bf16) return a.vec_k ? by_width<bf16_t, true>(a) : by_width<bf16_t, false>(a);
+    if (a.bf16 && a.vec_k) return a.kdim > 64 ? launch_pairs<128>(a) : launch_pairs<64>(a);
+    if (a.bf16) return by_width<bf16_t, false>(a);
     return a.vec_k ? by_width<float, true>(a) : by_width<float, false>(a);
 }
 

@@ -88,7 +88,9 @@ __device__ __forceinline__ void products(f32x4* acc, const Frag<NA>* a, const Fr
 }
 
 // The bf16 pieces of pairs of floats.
+// (No contraction: a remainder fused with the product that x came from is another number's.)
 __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+#pragma clang fp contract(off)
     const uint32_t u0 = __float_as_uint(x0), u1 = __float_as_uint(x1);
     hi = __builtin_amdgcn_perm(u1, u0, 0x07060302u);
     const float r0 = x0 - __uint_as_float(u0 & 0xffff0000u), r1 = x1 - __uint_as_float(u1 & 0xffff0000u);
@@ -117,6 +119,7 @@ __device__ __forceinline__ Frag<3> split(f32x4 a, f32x4 b) {
 // sign, and the product of two second pieces (left out too) below 2^-16.  (The first two cut
 // pieces leave out remainders of one sign: sums of 64 terms that cancel were off by 2e-4.)
 __device__ __forceinline__ Frag<2> split_rounded(f32x4 a, f32x4 b) {
+#pragma clang fp contract(off)
     Frag<2> f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
