@@ -295,19 +295,19 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
 // and all loads.  (One wave doing both, four to a workgroup: 64K tokens x 40 heads 6.0 ms; a chunk
 // then takes 1030 vector instructions, 182 matrix products and their waits one after the other.)
 //
-// Chunk c:  barrier;  A: the chain splits S, forms R;   the other loads chunk c + 1 and finishes O of c - 1;
-//           barrier;  B: the chain forms U, then S;     the other forms Q S, puts V of c + 1 in place.
+// Chunk c:  barrier;  A: the chain forms K S and R; the other loads K and T of c + 1 and finishes O of c - 1;
+//           barrier;  B: the chain forms U, then S;   the other loads V and Q of c + 1 and forms Q S.
 template <int KT, bool EMIT>
 __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
     constexpr int STEPS = KT / 32, NP = 2;                            // NP: pairs of waves
     constexpr int TILE = C * KT * 2, TRI = kBlocks * 3 * 1024, PAIRS = kBlocks * 2 * 1024, REC = 2048;
-    __shared__ __align__(16) char smem[2 * TILE + 2 * TRI + 3 * REC + NP * 64 * 32 + NP * 64 * 8 +
+    __shared__ __align__(16) char smem[2 * TILE + 2 * TRI + 3 * REC + 2 * NP * 64 * 32 + NP * 64 * 8 +
                                        (EMIT ? 2 * TILE + PAIRS + NP * (STEPS * 2048 + 4096) : 0)];
     char* const Kb = smem;                       // [2] K
     char* const Tb = Kb + 2 * TILE;              // [2] triangle
     char* const Rb = Tb + 2 * TRI;               // [3] record
-    char* const Vb = Rb + 3 * REC;               // a lane's 16 values, packed
-    char* const Lb = Vb + NP * 64 * 32;          // a lane's lost rows
+    char* const Vb = Rb + 3 * REC;               // [2] a lane's 16 values, packed
+    char* const Lb = Vb + 2 * NP * 64 * 32;          // a lane's lost rows
     char* const Qb = Lb + NP * 64 * 8;           // [2] Q
     char* const Pb = Qb + 2 * TILE;              // P
     char* const Sb = Pb + PAIRS;                 // S's first two pieces, as operands
@@ -352,55 +352,77 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
                     S[i][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, state_off(i, r), 0, 0));
         }
         int third = 0;   // c % 3
+        // S in pieces, step by step as its rows are final.  A matrix product takes 16 cycles, of which its issue is 4:
+        // the vector instructions of the next splits go in between (sched_barrier), not behind.
+        Frag<3> sf[STEPS];
+#pragma unroll
+        for (int j = 0; j < STEPS / 2; ++j) sf[j] = split(S[2 * j], S[2 * j + 1]);
         for (int c = 0; c < n; ++c) {
             const uint16_t* Kl = reinterpret_cast<const uint16_t*>(buffer(Kb, TILE, c));
             const u32x4* Tl = reinterpret_cast<const u32x4*>(buffer(Tb, TRI, c));
             const ChunkRec* rec = reinterpret_cast<const ChunkRec*>(Rb + third * REC);
             third = third == 2 ? 0 : third + 1;
             lds_barrier();
-            // A: R = V - exp(gamma) K S
+            // A: K S, R = V - exp(gamma) K S
+            const uint64_t starts_ = rec->starts, bad_ = rec->bad;
+            const float keep = rec->keep;
+            const u32x4* vals = reinterpret_cast<const u32x4*>(buffer(Vb, NP * 64 * 32, c) + (pair * 64 + lane) * 32);
+            const u32x4 v01 = vals[0], v23 = vals[1];
+            f32x4 into[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) into[i] = four(rec->into + 16 * i + 4 * g);
             f32x4 R[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) R[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < STEPS; ++j) {
-                const Frag<3> sf = split(S[2 * j], S[2 * j + 1]);
-                if constexpr (EMIT) {
-                    u32x4* to = reinterpret_cast<u32x4*>(Sb + (pair * STEPS + j) * 2048) + lane;
-                    to[0] = sf.p[0];
-                    to[64] = sf.p[1];
-                }
+                if (j >= STEPS / 2) sf[j] = split(S[2 * j], S[2 * j + 1]);
                 Frag<1> kf[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) kf[i] = rows_frag<1, KT>(Kl, 16 * i + m, 4 * j + g);
-                products<3, 4>(R, kf, sf);
+                products<3, 4>(R, kf, sf[j]);
+                if constexpr (EMIT) {
+                    u32x4* to = reinterpret_cast<u32x4*>(Sb + (pair * STEPS + j) * 2048) + lane;
+                    to[0] = sf[j].p[0];
+                    to[64] = sf[j].p[1];
+                }
             }
+            const uint64_t starts = uniform(starts_), bad = uniform(bad_);
             if (a.states) store_state(a.states + (bh * n + c) * cells, S);
-            const uint64_t starts = uniform(rec->starts), bad = uniform(rec->bad);
-            const int first_start = starts ? __builtin_ctzll(starts) : C;
-            const u32x4* vals = reinterpret_cast<const u32x4*>(Vb + (pair * 64 + lane) * 32);
-            const u32x4 v01 = vals[0], v23 = vals[1];
-            float check = 0.0f;   // stays 0 as long as everything is finite
+            f32x4 val[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const f32x4 into = four(rec->into + 16 * i + 4 * g);
                 const uint32_t lo = (i < 2 ? v01 : v23)[2 * (i & 1)], hi = (i < 2 ? v01 : v23)[2 * (i & 1) + 1];
-                const f32x4 val = {__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u), __uint_as_float(hi << 16),
-                                   __uint_as_float(hi & 0xffff0000u)};
-                if (starts == 0) {
+                val[i] = f32x4{__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u), __uint_as_float(hi << 16),
+                               __uint_as_float(hi & 0xffff0000u)};
+            }
+            if (starts == 0) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) R[i][r] = __builtin_fmaf(-into[r], R[i][r], val[r]);
-                } else {
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) R[i][r] = __builtin_fmaf(-into[i][r], R[i][r], val[i][r]);
+#pragma unroll
+                for (int i = 0; i < 2 * STEPS; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) S[i][r] *= keep;
+            } else {
+                const int first_start = __builtin_ctzll(starts);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        R[i][r] = val[r] - keep_if(16 * i + 4 * g + r < first_start, into[r] * R[i][r]);
-                }
+                        R[i][r] = val[i][r] - keep_if(16 * i + 4 * g + r < first_start, into[i][r] * R[i][r]);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) check = __builtin_fmaf(R[i][r], 0.0f, check);
+                for (int i = 0; i < 2 * STEPS; ++i) S[i] = f32x4{0, 0, 0, 0};
             }
+            float check[2] = {0.0f, 0.0f};   // stay 0 as long as everything is finite
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) check[i & 1] = __builtin_fmaf(R[i][r], 0.0f, check[i & 1]);
             // Values that are not finite: the rows from there to the document's end take no part, and give NaN
             uint64_t lost = 0;
-            const bool any_lost = bad != 0 || __ballot(not_finite(check)) != 0;
+            const bool any_lost = bad != 0 || __ballot(not_finite(check[0] + check[1])) != 0;
             if (any_lost) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -414,13 +436,13 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
 #pragma unroll
                     for (int r = 0; r < 4; ++r) R[i][r] = keep_if(!((lost >> (16 * i + 4 * g + r)) & 1), R[i][r]);
             }
-            const Frag<3> rf0 = split(R[0], R[1]), rf1 = split(R[2], R[3]);
             lds_barrier();
-            // B: U = beta T R
-            f32x4 U[4];
+            // B: U = beta T R, then S
+            auto rest = [&](auto lossy) {
+                constexpr bool LOSSY = decltype(lossy)::value;
+                f32x4 U[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) U[i] = f32x4{0, 0, 0, 0};
-            {
+                for (int i = 0; i < 4; ++i) U[i] = f32x4{0, 0, 0, 0};
                 Frag<3> tf[4];
                 auto triangle = [&](int i, int j) {
                     Frag<3> f;
@@ -430,54 +452,72 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
                 };
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tf[i] = triangle(i, 0);
-                products<3, 4>(U, tf, rf0);
+                products<3, 4>(U, tf, split(R[0], R[1]));
+                const Frag<3> rf = split(R[2], R[3]);
 #pragma unroll
                 for (int i = 2; i < 4; ++i) tf[i] = triangle(i, 1);
-                products<3, 2>(U + 2, tf + 2, rf1);
-            }
+                products<3, 2>(U + 2, tf + 2, rf);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f32x4 beta = four(rec->beta + 16 * i + 4 * g), outof = four(rec->outof + 16 * i + 4 * g);
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 beta = four(rec->beta + 16 * i + 4 * g), outof = four(rec->outof + 16 * i + 4 * g);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) U[i][r] *= beta[r];
-                if constexpr (EMIT) *reinterpret_cast<f32x4*>(Ub + ((pair * 4 + i) * 64 + lane) * 16) = U[i];
+                    for (int r = 0; r < 4; ++r) U[i][r] *= beta[r];
+                    if constexpr (EMIT) *reinterpret_cast<f32x4*>(Ub + ((pair * 4 + i) * 64 + lane) * 16) = U[i];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) U[i][r] *= outof[r];
-            }
-            if constexpr (EMIT) *reinterpret_cast<uint64_t*>(Lb + (pair * 64 + lane) * 8) = lost;
-            // S
-            if (starts == 0) {
-                const float keep = rec->keep;
-#pragma unroll
-                for (int i = 0; i < 2 * STEPS; ++i)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) S[i][r] *= keep;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2 * STEPS; ++i) S[i] = f32x4{0, 0, 0, 0};
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const Frag<3> uf = split(U[2 * j], U[2 * j + 1]);
-#pragma unroll
-                for (int i0 = 0; i0 < 2 * STEPS; i0 += 4) {
-                    Frag<1> kf[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) kf[i] = cols_frag<1, KT>(Kl, j, g, m, state_cols4(i0 + i, m));
-                    if (bad != 0) {   // keys that are not finite: their rows of U are 0
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) drop_rows<1>(kf[i], j, g, bad);
-                    }
-                    products<3, 4>(S + i0, kf, uf);
+                    for (int r = 0; r < 4; ++r) U[i][r] *= outof[r];
                 }
-            }
-            if (any_lost) {
-                const bool dead = (lost >> (rows_of(c) - 1)) & 1;
+                const Frag<3> uf[2] = {split(U[0], U[1]), split(U[2], U[3])};
+                auto keys = [&](Frag<1>* kf, int i0, int j) {
 #pragma unroll
-                for (int i = 0; i < 2 * STEPS; ++i)
+                    for (int i = 0; i < 4; ++i) {
+                        kf[i] = cols_frag<1, KT>(Kl, j, g, m, state_cols4(i0 + i, m));
+                        if (LOSSY) drop_rows<1>(kf[i], j, g, bad);   // keys that are not finite: their rows of U are 0
+                    }
+                };
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) S[i][r] = nan_if(dead, S[i][r]);
-            }
+                for (int j = 0; j < 2; ++j) {
+                    Frag<1> kf[4];
+                    keys(kf, 0, j);
+                    products<3, 4>(S, kf, uf[j]);
+                }
+                const bool dead = LOSSY && ((lost >> (rows_of(c) - 1)) & 1);
+                auto end = [&](int i0) {
+                    if constexpr (LOSSY) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) S[i0 + i][r] = nan_if(dead, S[i0 + i][r]);
+                    }
+                };
+                if constexpr (STEPS == 4) {
+                    Frag<1> kf[2][4];
+                    keys(kf[0], 4, 0);
+                    keys(kf[1], 4, 1);
+                    end(0);
+                    // the other half's products, three at a time between two of the first half's splits
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                        for (int q = 3 * k; q < 3 * k + 3; ++q)   // products<3, 4> over j, flattened
+                            S[4 + q % 4] = mfma(kf[q / 12][q % 4].p[0], uf[q / 12].p[2 - q / 4 % 3], S[4 + q % 4]);
+                        const f32x4 x = S[k / 2];
+                        uint32_t h, md, l;
+                        split_pair(x[2 * (k & 1)], x[2 * (k & 1) + 1], h, md, l);
+                        sf[k / 4].p[0][k % 4] = h;
+                        sf[k / 4].p[1][k % 4] = md;
+                        sf[k / 4].p[2][k % 4] = l;
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    end(4);
+                } else {
+                    end(0);
+                    sf[0] = split(S[0], S[1]);
+                }
+            };
+            if (any_lost) rest(std::true_type{});
+            else rest(std::false_type{});
+            if constexpr (EMIT) *reinterpret_cast<uint64_t*>(Lb + (pair * 64 + lane) * 8) = lost;
         }
         lds_barrier();
         if (a.final_state) store_state(a.final_state + bh * cells, S);
@@ -485,17 +525,16 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
         // ---- loads and outputs
         const uint32_t value_lane = v_in ? v * 2 : kPast;
         uint32_t vraw[16];
-        auto fetch = [&](int c, int slot) {
+        auto fetch_chain = [&](int c, int slot) {   // what the chain reads
             const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, id = bh * n + c;
-            const int rows = rows_of(c);
-            const Rsrc kr = rows_rsrc<2>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k, a.kdim);
+            const Rsrc kr = rows_rsrc<2>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows_of(c), a.ld_k, a.kdim);
             rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(buffer(Kb, TILE, c)), kr, a.ld_k, a.kdim, pair, lane);
             block_to_lds<2, NP>(Rb + slot * REC, rsrc(a.chunks + id * rec_bytes, sizeof(ChunkRec)), pair, lane);
             block_to_lds<kBlocks * 3, NP>(buffer(Tb, TRI, c), rsrc(a.solve + id * kSolveBytes, kSolveBytes), pair, lane);
-            if constexpr (EMIT) {
-                const Rsrc qr = rows_rsrc<2>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_q, a.kdim);
-                rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(buffer(Qb, TILE, c)), qr, a.ld_q, a.kdim, pair, lane);
-            }
+        };
+        auto fetch_rest = [&](int c) {
+            const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C;
+            const int rows = rows_of(c);
             const Rsrc vr = rows_rsrc<2>(a.v, first * a.ld_v + static_cast<int64_t>(hv) * a.vdim, rows, a.ld_v, a.vdim);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -503,17 +542,22 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
                 for (int r = 0; r < 4; ++r)
                     vraw[4 * i + r] = load_one<bf16_t>(
                         vr, value_lane + static_cast<uint32_t>((16 * i + 4 * g + r) * static_cast<int>(a.ld_v) * 2));
+            if constexpr (EMIT) {
+                const Rsrc qr = rows_rsrc<2>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_q, a.kdim);
+                rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(buffer(Qb, TILE, c)), qr, a.ld_q, a.kdim, pair, lane);
+            }
         };
-        auto put_values = [&]() {
-            u32x4* to = reinterpret_cast<u32x4*>(Vb + (pair * 64 + lane) * 32);
+        auto put_values = [&](int c) {
+            u32x4* to = reinterpret_cast<u32x4*>(buffer(Vb, NP * 64 * 32, c) + (pair * 64 + lane) * 32);
             u32x4 w[2];
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i / 4][i % 4] = vraw[2 * i] | (vraw[2 * i + 1] << 16);
             to[0] = w[0];
             to[1] = w[1];
         };
-        fetch(0, 0);
-        put_values();
+        fetch_chain(0, 0);
+        fetch_rest(0);
+        put_values(0);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         f32x4 O[4];
         auto outputs = [&](int c, int slot) {   // from Q S in O
@@ -563,12 +607,13 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
             const int last = third == 0 ? 2 : third - 1, next = third == 2 ? 0 : third + 1;
             lds_barrier();
             // A
-            if (c + 1 < n) fetch(c + 1, next);
+            if (c + 1 < n) fetch_chain(c + 1, next);
             if constexpr (EMIT) {
                 if (c > 0) outputs(c - 1, last);
             }
             lds_barrier();
             // B
+            if (c + 1 < n) fetch_rest(c + 1);
             if constexpr (EMIT) {
                 block_to_lds<kBlocks * 2, NP>(Pb, rsrc(a.pairs + (bh * n + c) * pairs_bytes(2), pairs_bytes(2)), pair, lane);
                 const uint16_t* Ql = reinterpret_cast<const uint16_t*>(buffer(Qb, TILE, c));
@@ -584,7 +629,7 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
                     products<2, 4>(O, qf, sf);
                 }
             }
-            if (c + 1 < n) put_values();
+            if (c + 1 < n) put_values(c + 1);
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             third = next;
         }
