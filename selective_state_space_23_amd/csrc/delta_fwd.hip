@@ -184,24 +184,20 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
                 for (int r = 0; r < 4; ++r) R[i][r] = keep_if(!((lost >> (16 * i + 4 * g + r)) & 1), R[i][r]);
         }
 
-        // U = beta T R
+        // U = beta T R, a piece of T at a time, the smallest first
         f32x4 U[4];
         {
 #pragma unroll
             for (int i = 0; i < 4; ++i) U[i] = f32x4{0, 0, 0, 0};
-            Frag<3> tf[4];
-            auto triangle = [&](int i, int j) {
-                Frag<3> f;
+            const Frag<3> rf[2] = {split(R[0], R[1]), split(R[2], R[3])};
 #pragma unroll
-                for (int p = 0; p < 3; ++p) f.p[p] = Tl[(low_block(i, j) * 3 + p) * 64 + lane];
-                return f;
-            };
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tf[i] = triangle(i, 0);
-            products<3, 4>(U, tf, split(R[0], R[1]));
+                for (int p = 2; p >= 0; --p)
 #pragma unroll
-            for (int i = 2; i < 4; ++i) tf[i] = triangle(i, 1);
-            products<3, 2>(U + 2, tf + 2, split(R[2], R[3]));
+                    for (int q = 2 - p; q >= 0; --q)
+#pragma unroll
+                        for (int i = 2 * j; i < 4; ++i) U[i] = mfma(Tl[(low_block(i, j) * 3 + p) * 64 + lane], rf[j].p[q], U[i]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const f32x4 beta = four(rec->beta + 16 * i + 4 * g);
@@ -401,10 +397,6 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) R[i][r] = __builtin_fmaf(-into[i][r], R[i][r], val[i][r]);
-#pragma unroll
-                for (int i = 0; i < 2 * STEPS; ++i)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) S[i][r] *= keep;
             } else {
                 const int first_start = __builtin_ctzll(starts);
 #pragma unroll
@@ -412,8 +404,6 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         R[i][r] = val[i][r] - keep_if(16 * i + 4 * g + r < first_start, into[i][r] * R[i][r]);
-#pragma unroll
-                for (int i = 0; i < 2 * STEPS; ++i) S[i] = f32x4{0, 0, 0, 0};
             }
             float check[2] = {0.0f, 0.0f};   // stay 0 as long as everything is finite
 #pragma unroll
@@ -437,86 +427,117 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
                     for (int r = 0; r < 4; ++r) R[i][r] = keep_if(!((lost >> (16 * i + 4 * g + r)) & 1), R[i][r]);
             }
             lds_barrier();
-            // B: U = beta T R, then S
-            auto rest = [&](auto lossy) {
-                constexpr bool LOSSY = decltype(lossy)::value;
-                f32x4 U[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) U[i] = f32x4{0, 0, 0, 0};
-                Frag<3> tf[4];
-                auto triangle = [&](int i, int j) {
-                    Frag<3> f;
-#pragma unroll
-                    for (int p = 0; p < 3; ++p) f.p[p] = Tl[(low_block(i, j) * 3 + p) * 64 + lane];
-                    return f;
-                };
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tf[i] = triangle(i, 0);
-                products<3, 4>(U, tf, split(R[0], R[1]));
-                const Frag<3> rf = split(R[2], R[3]);
-#pragma unroll
-                for (int i = 2; i < 4; ++i) tf[i] = triangle(i, 1);
-                products<3, 2>(U + 2, tf + 2, rf);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x4 beta = four(rec->beta + 16 * i + 4 * g), outof = four(rec->outof + 16 * i + 4 * g);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) U[i][r] *= beta[r];
-                    if constexpr (EMIT) *reinterpret_cast<f32x4*>(Ub + ((pair * 4 + i) * 64 + lane) * 16) = U[i];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) U[i][r] *= outof[r];
-                }
-                const Frag<3> uf[2] = {split(U[0], U[1]), split(U[2], U[3])};
+            // B: U = beta T R, then S.  PLAIN: one document, everything finite
+            auto rest = [&](auto plain) {
+                constexpr bool PLAIN = decltype(plain)::value;
+                auto triangle = [&](int i, int j, int p) { return Tl[(low_block(i, j) * 3 + p) * 64 + lane]; };
                 auto keys = [&](Frag<1>* kf, int i0, int j) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         kf[i] = cols_frag<1, KT>(Kl, j, g, m, state_cols4(i0 + i, m));
-                        if (LOSSY) drop_rows<1>(kf[i], j, g, bad);   // keys that are not finite: their rows of U are 0
+                        if (!PLAIN) drop_rows<1>(kf[i], j, g, bad);   // keys that are not finite: their rows of U are 0
                     }
                 };
+                f32x4 U[4];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    Frag<1> kf[4];
-                    keys(kf, 0, j);
-                    products<3, 4>(S, kf, uf[j]);
+                for (int i = 0; i < 4; ++i) U[i] = f32x4{0, 0, 0, 0};
+                // a piece of T at a time, the smallest first
+                const Frag<3> rf0 = split(R[0], R[1]);
+#pragma unroll
+                for (int p = 2; p >= 0; --p) {
+                    u32x4 tf[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tf[i] = triangle(i, 0, p);
+#pragma unroll
+                    for (int q = 2 - p; q >= 0; --q)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) U[i] = mfma(tf[i], rf0.p[q], U[i]);
                 }
-                const bool dead = LOSSY && ((lost >> (rows_of(c) - 1)) & 1);
+                const Frag<3> rf1 = split(R[2], R[3]);
+#pragma unroll
+                for (int p = 2; p >= 0; --p) {
+                    const u32x4 t2 = triangle(2, 1, p), t3 = triangle(3, 1, p);
+#pragma unroll
+                    for (int q = 2 - p; q >= 0; --q) {
+                        U[2] = mfma(t2, rf1.p[q], U[2]);
+                        U[3] = mfma(t3, rf1.p[q], U[3]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2 * STEPS; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) S[i][r] = PLAIN ? S[i][r] * keep : keep_if(starts == 0, S[i][r] * keep);
+                Frag<1> kf[2][4];
+                keys(kf[0], 0, 0);
+                keys(kf[1], 0, 1);
+                f32x4 beta[4], outof[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    beta[i] = four(rec->beta + 16 * i + 4 * g);
+                    outof[i] = four(rec->outof + 16 * i + 4 * g);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) U[i][r] *= beta[i][r];
+                    if constexpr (EMIT) *reinterpret_cast<f32x4*>(Ub + ((pair * 4 + i) * 64 + lane) * 16) = U[i];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) U[i][r] *= outof[i][r];
+                }
+                Frag<3> uf[2];
+                uf[0] = split(U[0], U[1]);
+                // Products and splits that do not wait for each other, three products and a split at a time.
+                auto step = [&](f32x4* acc, const Frag<1>* keyf, const Frag<3>& u, int from) {
+#pragma unroll
+                    for (int q = from; q < from + 3; ++q) acc[q % 4] = mfma(keyf[q % 4].p[0], u.p[2 - q / 4], acc[q % 4]);
+                };
+                auto cut = [&](Frag<3>& f, const f32x4& x, const f32x4& y, int k) {   // the k-th pair of eight values
+                    const f32x4& z = k < 2 ? x : y;
+                    uint32_t h, md, l;
+                    split_pair(z[2 * (k & 1)], z[2 * (k & 1) + 1], h, md, l);
+                    f.p[0][k] = h;
+                    f.p[1][k] = md;
+                    f.p[2][k] = l;
+                };
+                Frag<1> kg[2][4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    step(S, kf[0], uf[0], 3 * k);
+                    cut(uf[1], U[2], U[3], k);
+                }
+                if constexpr (STEPS == 4) {
+                    keys(kg[0], 4, 0);
+                    keys(kg[1], 4, 1);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                products<3, 4>(S, kf[1], uf[1]);
+                const bool dead = !PLAIN && ((lost >> (rows_of(c) - 1)) & 1);
                 auto end = [&](int i0) {
-                    if constexpr (LOSSY) {
+                    if constexpr (!PLAIN) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
 #pragma unroll
                             for (int r = 0; r < 4; ++r) S[i0 + i][r] = nan_if(dead, S[i0 + i][r]);
                     }
                 };
+                end(0);
                 if constexpr (STEPS == 4) {
-                    Frag<1> kf[2][4];
-                    keys(kf[0], 4, 0);
-                    keys(kf[1], 4, 1);
-                    end(0);
-                    // the other half's products, three at a time between two of the first half's splits
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                        for (int q = 3 * k; q < 3 * k + 3; ++q)   // products<3, 4> over j, flattened
-                            S[4 + q % 4] = mfma(kf[q / 12][q % 4].p[0], uf[q / 12].p[2 - q / 4 % 3], S[4 + q % 4]);
-                        const f32x4 x = S[k / 2];
-                        uint32_t h, md, l;
-                        split_pair(x[2 * (k & 1)], x[2 * (k & 1) + 1], h, md, l);
-                        sf[k / 4].p[0][k % 4] = h;
-                        sf[k / 4].p[1][k % 4] = md;
-                        sf[k / 4].p[2][k % 4] = l;
+                        step(S + 4, kg[k / 4], uf[k / 4], 3 * (k % 4));
+                        cut(sf[k / 4], S[k / 4 * 2], S[k / 4 * 2 + 1], k % 4);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                     end(4);
                 } else {
-                    end(0);
                     sf[0] = split(S[0], S[1]);
                 }
             };
-            if (any_lost) rest(std::true_type{});
-            else rest(std::false_type{});
+            if (any_lost || starts != 0) rest(std::false_type{});
+            else rest(std::true_type{});
             if constexpr (EMIT) *reinterpret_cast<uint64_t*>(Lb + (pair * 64 + lane) * 8) = lost;
         }
         lds_barrier();

@@ -31,6 +31,7 @@ constexpr uint32_t kPast = 0x7fffff00u;   // a byte offset behind any buffer
 constexpr int64_t kSolveBytes = kBlocks * 3 * 1024;   // a chunk's solved triangle in three pieces
 constexpr int64_t pairs_bytes(int pieces) { return kBlocks * pieces * 1024; }
 
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -87,17 +88,25 @@ __device__ __forceinline__ void products(f32x4* acc, const Frag<NA>* a, const Fr
             }
 }
 
-// The bf16 pieces of pairs of floats.
-// (No contraction: a remainder fused with the product that x came from is another number's.)
+// What is left of two floats without their bf16 pieces h = {x0's, x1's}: v_dot2_f32_bf16 is exact here, as its sum has
+// no more than 24 bits, and takes both a piece out of its pair and the difference (two instructions of 8 cycles each to a
+// lone wave, against four).  An infinity or NaN in one of the two makes both NaN: pairs lie along what is summed over.
+// (The multipliers are hidden from the compiler, which took {0, -1} for the constant -1.0f, read here as {-1, 0}.)
+__device__ __forceinline__ void without_pieces(uint32_t h, float& x0, float& x1) {
+    uint32_t first = 0x0000bf80u, second = 0xbf800000u;   // {-1, 0} and {0, -1}
+    asm("" : "+s"(first));
+    asm("" : "+s"(second));
+    x0 = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, h), __builtin_bit_cast(bf16x2_t, first), x0, false);
+    x1 = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, h), __builtin_bit_cast(bf16x2_t, second), x1, false);
+}
+
+// The bf16 pieces of pairs of floats, cut off: the highest 8 significant bits, the next and the last.
 __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-#pragma clang fp contract(off)
-    const uint32_t u0 = __float_as_uint(x0), u1 = __float_as_uint(x1);
-    hi = __builtin_amdgcn_perm(u1, u0, 0x07060302u);
-    const float r0 = x0 - __uint_as_float(u0 & 0xffff0000u), r1 = x1 - __uint_as_float(u1 & 0xffff0000u);
-    const uint32_t v0 = __float_as_uint(r0), v1 = __float_as_uint(r1);
-    mid = __builtin_amdgcn_perm(v1, v0, 0x07060302u);
-    const float s0 = r0 - __uint_as_float(v0 & 0xffff0000u), s1 = r1 - __uint_as_float(v1 & 0xffff0000u);
-    lo = __builtin_amdgcn_perm(__float_as_uint(s1), __float_as_uint(s0), 0x07060302u);
+    hi = __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302u);
+    without_pieces(hi, x0, x1);
+    mid = __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302u);
+    without_pieces(mid, x0, x1);
+    lo = __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302u);
 }
 
 // Eight floats in three pieces: slots 0..3 from a, 4..7 from b.
@@ -119,15 +128,15 @@ __device__ __forceinline__ Frag<3> split(f32x4 a, f32x4 b) {
 // sign, and the product of two second pieces (left out too) below 2^-16.  (The first two cut
 // pieces leave out remainders of one sign: sums of 64 terms that cancel were off by 2e-4.)
 __device__ __forceinline__ Frag<2> split_rounded(f32x4 a, f32x4 b) {
-#pragma clang fp contract(off)
     Frag<2> f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const f32x4 x = i < 2 ? a : b;
-        const float x0 = x[2 * (i & 1)], x1 = x[2 * (i & 1) + 1];
+        float x0 = x[2 * (i & 1)], x1 = x[2 * (i & 1) + 1];
         const uint32_t h = pack_bf16x2(x0, x1);
+        without_pieces(h, x0, x1);
         f.p[0][i] = h;
-        f.p[1][i] = pack_bf16x2(x0 - __uint_as_float(h << 16), x1 - __uint_as_float(h & 0xffff0000u));
+        f.p[1][i] = pack_bf16x2(x0, x1);
     }
     return f;
 }
