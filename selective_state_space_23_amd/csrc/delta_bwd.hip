@@ -297,24 +297,28 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
 // one walks dS -> dU -> dX -> dS, the other brings what does not depend on dS, P^T dO and
 // Z = (scale exp(gamma) Q)^T dO, and all loads.
 //
-// Chunk c:  barrier;  A: the chain forms K dS and dU;   the other forms Z of c, loads P and dO of c - 1;
-//           barrier;  B: the chain forms dX, then dS;   the other forms P^T dO of c - 1, loads K, T and Q of it.
-template <int KT>
-__global__ __launch_bounds__(256, 1) void bwd_pairs_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
-    constexpr int STEPS = KT / 32, NP = 2;
+// Chunk c:  barrier;  A: the chain forms K dS and dU;   the other forms Z of c, loads T of c, P and dO of c - 1;
+//           barrier;  B: the chain forms dX, then dS;   the other forms P^T dO of c - 1, loads K and Q of it.
+template <int KT, int NP>
+constexpr int kPairsLds = 3 * C * KT * 2 + 2 * kBlocks * 3072 + 2 * 2048 + NP * (KT / 16 * 1024 + 4096 + 512);
+// (LDS at the launch and two waves a SIMD: as in the forward, for sums in the lower registers)
+template <int KT, int NP>
+__global__ __launch_bounds__(NP * 128, 2) void bwd_pairs_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
+    constexpr int STEPS = KT / 32;
     constexpr int TILE = C * KT * 2, TRI = kBlocks * 3 * 1024, REC = 2048;
-    __shared__ __align__(16) char smem[2 * TILE + 2 * TRI + 2 * REC + TILE + TRI + NP * (2 * STEPS + 4) * 1024 + NP * 512];
+    extern __shared__ __align__(16) char smem[];
     char* const Kb = smem;                       // [2] K
-    char* const Tb = Kb + 2 * TILE;              // [2] triangle
-    char* const Rb = Tb + 2 * TRI;               // [2] record
-    char* const Qb = Rb + 2 * REC;               // Q
+    char* const Rb = Kb + 2 * TILE;              // [2] record
+    char* const Tb = Rb + 2 * REC;               // triangle
+    char* const Qb = Tb + TRI;                   // Q
     char* const Pb = Qb + TILE;                  // P
     char* const Zb = Pb + TRI;                   // Z
     char* const Ub = Zb + NP * 2 * STEPS * 1024; // P^T dO
     char* const Lb = Ub + NP * 4096;             // a lane's rows that take no part
+    static_assert(kPairsLds<KT, NP> == 3 * TILE + 2 * TRI + 2 * REC + NP * ((2 * STEPS + 4) * 1024 + 512));
 
     const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), pair = wave & 1;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), pair = wave & (NP - 1);
     const int64_t bh = quotient(blockIdx.x, 8 * cols) * 8 + (blockIdx.x & 7);   // a head's workgroups on one XCD
     if (bh >= a.batch * a.vheads) return;
     const int hv = remainder(bh, a.vheads), hk = quotient(hv, a.vheads / a.kheads);
@@ -331,15 +335,18 @@ __global__ __launch_bounds__(256, 1) void bwd_pairs_kernel(DeltaArgs a, int64_t 
     if (wave < NP) {
         // ---- the chain
         const int64_t cells = static_cast<int64_t>(a.kdim) * a.vdim;
-        const uint32_t state_lane = v_in ? v * 4 : kPast;
-        auto state_off = [&](int i, int r) { return state_lane + static_cast<uint32_t>(state_row(i, g, r) * a.vdim * 4); };
+        const uint32_t state_lane = v_in ? static_cast<uint32_t>(v * 4 + state_row(0, g, 0) * a.vdim * 4) : kPast;
+        auto state_off = [&](uint32_t from, int i, int r) {
+            return from + static_cast<uint32_t>(state_row(i, 0, r) * a.vdim * 4);
+        };
         auto store_state = [&](float* to, const f32x4* S) {
             const Rsrc rs = rsrc(to, cells * 4);
+            const uint32_t from = opaque(state_lane);
 #pragma unroll
             for (int i = 0; i < 2 * STEPS; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][r]), rs, state_off(i, r), 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][r]), rs, state_off(from, i, r), 0, 0);
         };
         f32x4 S[2 * STEPS];   // dS
         {
@@ -348,7 +355,7 @@ __global__ __launch_bounds__(256, 1) void bwd_pairs_kernel(DeltaArgs a, int64_t 
             for (int i = 0; i < 2 * STEPS; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    S[i][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, state_off(i, r), 0, 0));
+                    S[i][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, state_off(state_lane, i, r), 0, 0));
         }
         // dS in pieces as its rows are final, between the products that do not wait for them
         Frag<3> sf[STEPS];
@@ -357,7 +364,7 @@ __global__ __launch_bounds__(256, 1) void bwd_pairs_kernel(DeltaArgs a, int64_t 
         lds_barrier();   // the other waves' first loads
         for (int c = n - 1; c >= 0; --c) {
             const uint16_t* Kl = reinterpret_cast<const uint16_t*>(buffer(Kb, TILE, c));
-            const u32x4* Tl = reinterpret_cast<const u32x4*>(buffer(Tb, TRI, c));
+            const u32x4* Tl = reinterpret_cast<const u32x4*>(Tb);
             const ChunkRec* rec = reinterpret_cast<const ChunkRec*>(buffer(Rb, REC, c));
             lds_barrier();
             // A: dU = exp(gamma_C - gamma) K dS + P^T dO
@@ -527,16 +534,18 @@ __global__ __launch_bounds__(256, 1) void bwd_pairs_kernel(DeltaArgs a, int64_t 
         f32x4 dO[4];
         uint64_t sick = 0;
         bool any_sick = false;
-        auto fetch_chain = [&](int c) {
-            const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, id = bh * n + c;
+        auto fetch_early = [&](int c) {   // K and Q, read from phase A on
+            const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C;
             const int rows = rows_of(c);
             const Rsrc kr = rows_rsrc<2>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k, a.kdim);
             rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(buffer(Kb, TILE, c)), kr, a.ld_k, a.kdim, pair, lane);
-            block_to_lds<kBlocks * 3, NP>(buffer(Tb, TRI, c), rsrc(a.solve_t + id * kSolveBytes, kSolveBytes), pair, lane);
             const Rsrc qr = rows_rsrc<2>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_q, a.kdim);
             rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(Qb), qr, a.ld_q, a.kdim, pair, lane);
         };
-        auto fetch_rest = [&](int c) {
+        auto fetch_triangle = [&](int c) {   // from phase B on
+            block_to_lds<kBlocks * 3, NP>(Tb, rsrc(a.solve_t + (bh * n + c) * kSolveBytes, kSolveBytes), pair, lane);
+        };
+        auto fetch_rest = [&](int c) {   // from phase B of the chunk before on
             const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, id = bh * n + c;
             block_to_lds<2, NP>(buffer(Rb, REC, c), rsrc(a.chunks + id * rec_bytes, sizeof(ChunkRec)), pair, lane);
             block_to_lds<kBlocks * 3, NP>(Pb, rsrc(a.pairs + id * kSolveBytes, kSolveBytes), pair, lane);
@@ -667,20 +676,21 @@ __global__ __launch_bounds__(256, 1) void bwd_pairs_kernel(DeltaArgs a, int64_t 
         auto landed = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
         // the waves of this role share what they load: a barrier of all makes it whole
         fetch_rest(n - 1);
-        fetch_chain(n - 1);
+        fetch_early(n - 1);
         landed();
         lds_barrier();
         weighted(n - 1);
         for (int c = n - 1; c >= 0; --c) {
             lds_barrier();
             // A
+            fetch_triangle(c);
             if (c > 0) fetch_rest(c - 1);
             entering(c);
             landed();
             lds_barrier();
             // B
             if (c > 0) {
-                fetch_chain(c - 1);
+                fetch_early(c - 1);
                 weighted(c - 1);
                 landed();
             }
@@ -696,12 +706,16 @@ hipError_t launch(const DeltaArgs& a) {
     return hipGetLastError();
 }
 
-template <int KT>
+template <int KT, int NP>
 hipError_t launch_pairs(const DeltaArgs& a) {
-    const int cols = (a.vdim + 31) / 32;
-    hipLaunchKernelGGL((bwd_pairs_kernel<KT>), dim3(static_cast<unsigned>((a.batch * a.vheads + 7) / 8 * 8 * cols)), dim3(256),
-                       0, a.stream, a, static_cast<int64_t>(delta_chunk_bytes()), cols);
+    const int cols = (a.vdim + 16 * NP - 1) / (16 * NP);
+    hipLaunchKernelGGL((bwd_pairs_kernel<KT, NP>), dim3(static_cast<unsigned>((a.batch * a.vheads + 7) / 8 * 8 * cols)),
+                       dim3(NP * 128), (kPairsLds<KT, NP>), a.stream, a, static_cast<int64_t>(delta_chunk_bytes()), cols);
     return hipGetLastError();
+}
+template <int KT>
+hipError_t pairs_by_columns(const DeltaArgs& a) {
+    return wide_groups(a) ? launch_pairs<KT, 4>(a) : launch_pairs<KT, 2>(a);
 }
 
 template <typename T, bool VEC>
@@ -712,7 +726,7 @@ hipError_t by_width(const DeltaArgs& a) {
 }  // namespace
 
 hipError_t launch_delta_bwd_states(const DeltaArgs& a) {
-    if (a.bf16 && a.vec_k) return a.kdim > 64 ? launch_pairs<128>(a) : launch_pairs<64>(a);
+    if (a.bf16 && a.vec_k) return a.kdim > 64 ? pairs_by_columns<128>(a) : pairs_by_columns<64>(a);
     if (a.bf16) return by_width<bf16_t, false>(a);
     return a.vec_k ? by_width<float, true>(a) : by_width<float, false>(a);
 }

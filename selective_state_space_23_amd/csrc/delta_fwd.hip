@@ -291,26 +291,35 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
 // and all loads.  (One wave doing both, four to a workgroup: 64K tokens x 40 heads 6.0 ms; a chunk
 // then takes 1030 vector instructions, 182 matrix products and their waits one after the other.)
 //
-// Chunk c:  barrier;  A: the chain forms K S and R; the other loads K and T of c + 1 and finishes O of c - 1;
-//           barrier;  B: the chain forms U, then S;   the other loads V and Q of c + 1 and forms Q S.
-template <int KT, bool EMIT>
-__global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
-    constexpr int STEPS = KT / 32, NP = 2;                            // NP: pairs of waves
+// Chunk c:  barrier;  A: the chain forms K S and R; the other loads T and Q of c and finishes O of c - 1;
+//           barrier;  B: the chain forms U, then S;   the other loads K and V of c + 1 and P of c and forms Q S.
+//
+// A workgroup has NP such pairs, for as many 16 columns of one head, a chain and a follower on a SIMD with NP = 4: a wave
+// alone issues a vector instruction every 8 cycles, two together twice as many.
+template <int KT, int NP, bool EMIT>
+constexpr int kPairsLds = 2 * C * KT * 2 + kBlocks * 3072 + 2 * 2048 + NP * (2048 + 512) +
+                          (EMIT ? C * KT * 2 + kBlocks * 2048 + NP * (KT / 32 * 2048 + 4096) : 0);
+// (LDS given at the launch, and two waves a SIMD asked for: one workgroup fills a CU either way, but where the compiler
+// sees that, it takes 512 registers, keeps sums in the upper 256 and moves them, 8 cycles each.)
+template <int KT, int NP, bool EMIT, bool SAVE>
+__global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
+    constexpr int STEPS = KT / 32;
     constexpr int TILE = C * KT * 2, TRI = kBlocks * 3 * 1024, PAIRS = kBlocks * 2 * 1024, REC = 2048;
-    __shared__ __align__(16) char smem[2 * TILE + 2 * TRI + 3 * REC + 2 * NP * 64 * 32 + NP * 64 * 8 +
-                                       (EMIT ? 2 * TILE + PAIRS + NP * (STEPS * 2048 + 4096) : 0)];
+    extern __shared__ __align__(16) char smem[];
     char* const Kb = smem;                       // [2] K
-    char* const Tb = Kb + 2 * TILE;              // [2] triangle
-    char* const Rb = Tb + 2 * TRI;               // [3] record
-    char* const Vb = Rb + 3 * REC;               // [2] a lane's 16 values, packed
-    char* const Lb = Vb + 2 * NP * 64 * 32;          // a lane's lost rows
-    char* const Qb = Lb + NP * 64 * 8;           // [2] Q
-    char* const Pb = Qb + 2 * TILE;              // P
+    char* const Rb = Kb + 2 * TILE;              // [2] record
+    char* const Tb = Rb + 2 * REC;               // triangle
+    char* const Vb = Tb + TRI;                   // a lane's 16 values, packed
+    char* const Lb = Vb + NP * 64 * 32;          // a lane's lost rows
+    char* const Qb = Lb + NP * 64 * 8;           // Q
+    char* const Pb = Qb + TILE;                  // P
     char* const Sb = Pb + PAIRS;                 // S's first two pieces, as operands
     char* const Ub = Sb + NP * STEPS * 2048;     // U
+    static_assert(kPairsLds<KT, NP, EMIT> == 2 * (TILE + REC) + TRI + NP * (64 * 32 + 64 * 8) +
+                                                 (EMIT ? TILE + PAIRS + NP * (STEPS * 2048 + 4096) : 0));
 
     const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), pair = wave & 1;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), pair = wave & (NP - 1);
     // workgroups of one head on one XCD (they are dealt out to the 8 in turn), which read its K, Q, T and P
     const int64_t bh = quotient(blockIdx.x, 8 * cols) * 8 + (blockIdx.x & 7);
     if (bh >= a.batch * a.vheads) return;
@@ -328,15 +337,18 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
     if (wave < NP) {
         // ---- the chain
         const int64_t cells = static_cast<int64_t>(a.kdim) * a.vdim;
-        const uint32_t state_lane = v_in ? v * 4 : kPast;
-        auto state_off = [&](int i, int r) { return state_lane + static_cast<uint32_t>(state_row(i, g, r) * a.vdim * 4); };
+        const uint32_t state_lane = v_in ? static_cast<uint32_t>(v * 4 + state_row(0, g, 0) * a.vdim * 4) : kPast;
+        auto state_off = [&](uint32_t from, int i, int r) {
+            return from + static_cast<uint32_t>(state_row(i, 0, r) * a.vdim * 4);
+        };
         auto store_state = [&](float* to, const f32x4* S) {
             const Rsrc rs = rsrc(to, cells * 4);
+            const uint32_t from = opaque(state_lane);   // 32 offsets would be kept in registers
 #pragma unroll
             for (int i = 0; i < 2 * STEPS; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][r]), rs, state_off(i, r), 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][r]), rs, state_off(from, i, r), 0, 0);
         };
         f32x4 S[2 * STEPS];
         {
@@ -345,9 +357,8 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
             for (int i = 0; i < 2 * STEPS; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    S[i][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, state_off(i, r), 0, 0));
+                    S[i][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, state_off(state_lane, i, r), 0, 0));
         }
-        int third = 0;   // c % 3
         // S in pieces, step by step as its rows are final.  A matrix product takes 16 cycles, of which its issue is 4:
         // the vector instructions of the next splits go in between (sched_barrier), not behind.
         Frag<3> sf[STEPS];
@@ -355,14 +366,13 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
         for (int j = 0; j < STEPS / 2; ++j) sf[j] = split(S[2 * j], S[2 * j + 1]);
         for (int c = 0; c < n; ++c) {
             const uint16_t* Kl = reinterpret_cast<const uint16_t*>(buffer(Kb, TILE, c));
-            const u32x4* Tl = reinterpret_cast<const u32x4*>(buffer(Tb, TRI, c));
-            const ChunkRec* rec = reinterpret_cast<const ChunkRec*>(Rb + third * REC);
-            third = third == 2 ? 0 : third + 1;
+            const u32x4* Tl = reinterpret_cast<const u32x4*>(Tb);
+            const ChunkRec* rec = reinterpret_cast<const ChunkRec*>(buffer(Rb, REC, c));
             lds_barrier();
             // A: K S, R = V - exp(gamma) K S
             const uint64_t starts_ = rec->starts, bad_ = rec->bad;
             const float keep = rec->keep;
-            const u32x4* vals = reinterpret_cast<const u32x4*>(buffer(Vb, NP * 64 * 32, c) + (pair * 64 + lane) * 32);
+            const u32x4* vals = reinterpret_cast<const u32x4*>(Vb + (pair * 64 + lane) * 32);
             const u32x4 v01 = vals[0], v23 = vals[1];
             f32x4 into[4];
 #pragma unroll
@@ -384,7 +394,7 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
                 }
             }
             const uint64_t starts = uniform(starts_), bad = uniform(bad_);
-            if (a.states) store_state(a.states + (bh * n + c) * cells, S);
+            if constexpr (SAVE) store_state(a.states + (bh * n + c) * cells, S);
             f32x4 val[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -546,15 +556,8 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
         // ---- loads and outputs
         const uint32_t value_lane = v_in ? v * 2 : kPast;
         uint32_t vraw[16];
-        auto fetch_chain = [&](int c, int slot) {   // what the chain reads
+        auto fetch_early = [&](int c) {   // what is read from phase A on
             const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, id = bh * n + c;
-            const Rsrc kr = rows_rsrc<2>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows_of(c), a.ld_k, a.kdim);
-            rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(buffer(Kb, TILE, c)), kr, a.ld_k, a.kdim, pair, lane);
-            block_to_lds<2, NP>(Rb + slot * REC, rsrc(a.chunks + id * rec_bytes, sizeof(ChunkRec)), pair, lane);
-            block_to_lds<kBlocks * 3, NP>(buffer(Tb, TRI, c), rsrc(a.solve + id * kSolveBytes, kSolveBytes), pair, lane);
-        };
-        auto fetch_rest = [&](int c) {
-            const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C;
             const int rows = rows_of(c);
             const Rsrc vr = rows_rsrc<2>(a.v, first * a.ld_v + static_cast<int64_t>(hv) * a.vdim, rows, a.ld_v, a.vdim);
 #pragma unroll
@@ -563,26 +566,34 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
                 for (int r = 0; r < 4; ++r)
                     vraw[4 * i + r] = load_one<bf16_t>(
                         vr, value_lane + static_cast<uint32_t>((16 * i + 4 * g + r) * static_cast<int>(a.ld_v) * 2));
+            const Rsrc kr = rows_rsrc<2>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k, a.kdim);
+            rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(buffer(Kb, TILE, c)), kr, a.ld_k, a.kdim, pair, lane);
+            block_to_lds<2, NP>(buffer(Rb, REC, c), rsrc(a.chunks + id * rec_bytes, sizeof(ChunkRec)), pair, lane);
+        };
+        auto fetch_late = [&](int c) {   // from phase B on
+            const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, id = bh * n + c;
+            block_to_lds<kBlocks * 3, NP>(Tb, rsrc(a.solve + id * kSolveBytes, kSolveBytes), pair, lane);
             if constexpr (EMIT) {
-                const Rsrc qr = rows_rsrc<2>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_q, a.kdim);
-                rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(buffer(Qb, TILE, c)), qr, a.ld_q, a.kdim, pair, lane);
+                const Rsrc qr =
+                    rows_rsrc<2>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows_of(c), a.ld_q, a.kdim);
+                rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(Qb), qr, a.ld_q, a.kdim, pair, lane);
             }
         };
-        auto put_values = [&](int c) {
-            u32x4* to = reinterpret_cast<u32x4*>(buffer(Vb, NP * 64 * 32, c) + (pair * 64 + lane) * 32);
+        auto landed = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
+        auto put_values = [&] {
+            u32x4* to = reinterpret_cast<u32x4*>(Vb + (pair * 64 + lane) * 32);
             u32x4 w[2];
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i / 4][i % 4] = vraw[2 * i] | (vraw[2 * i + 1] << 16);
             to[0] = w[0];
             to[1] = w[1];
         };
-        fetch_chain(0, 0);
-        fetch_rest(0);
-        put_values(0);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        fetch_early(0);
+        put_values();
+        landed();
         f32x4 O[4];
-        auto outputs = [&](int c, int slot) {   // from Q S in O
-            const ChunkRec* rec = reinterpret_cast<const ChunkRec*>(Rb + slot * REC);
+        auto outputs = [&](int c) {   // from Q S in O
+            const ChunkRec* rec = reinterpret_cast<const ChunkRec*>(buffer(Rb, REC, c));
             const uint64_t starts = uniform(rec->starts);
             const int first_start = starts ? __builtin_ctzll(starts) : C;
             const u32x4* Pl = reinterpret_cast<const u32x4*>(Pb);
@@ -613,6 +624,7 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
 #pragma unroll
                     for (int r = 0; r < 4; ++r) O[i][r] = nan_if((lost >> (16 * i + 4 * g + r)) & 1, O[i][r]);
             }
+            landed();   // before the stores, which need not be waited for
             const int64_t ldo = static_cast<int64_t>(a.vheads) * a.vdim;
             const Rsrc orr = rows_rsrc<2>(a.out, (b * a.seqlen + static_cast<int64_t>(c) * C) * ldo + hv * a.vdim, rows_of(c),
                                           ldo, a.vdim);
@@ -623,21 +635,18 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
                     store_one<bf16_t>(orr, value_lane + static_cast<uint32_t>((16 * i + 4 * g + r) * static_cast<int>(ldo) * 2),
                                       O[i][r]);
         };
-        int third = 0;
         for (int c = 0; c < n; ++c) {
-            const int last = third == 0 ? 2 : third - 1, next = third == 2 ? 0 : third + 1;
             lds_barrier();
             // A
-            if (c + 1 < n) fetch_chain(c + 1, next);
-            if constexpr (EMIT) {
-                if (c > 0) outputs(c - 1, last);
-            }
+            fetch_late(c);
+            if (EMIT && c > 0) outputs(c - 1);
+            else landed();
             lds_barrier();
             // B
-            if (c + 1 < n) fetch_rest(c + 1);
+            if (c + 1 < n) fetch_early(c + 1);
             if constexpr (EMIT) {
                 block_to_lds<kBlocks * 2, NP>(Pb, rsrc(a.pairs + (bh * n + c) * pairs_bytes(2), pairs_bytes(2)), pair, lane);
-                const uint16_t* Ql = reinterpret_cast<const uint16_t*>(buffer(Qb, TILE, c));
+                const uint16_t* Ql = reinterpret_cast<const uint16_t*>(Qb);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) O[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -650,12 +659,11 @@ __global__ __launch_bounds__(256, 1) void fwd_pairs_kernel(DeltaArgs a, int64_t 
                     products<2, 4>(O, qf, sf);
                 }
             }
-            if (c + 1 < n) put_values(c + 1);
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            third = next;
+            if (c + 1 < n) put_values();
+            landed();
         }
         lds_barrier();
-        if constexpr (EMIT) outputs(n - 1, third == 0 ? 2 : third - 1);
+        if constexpr (EMIT) outputs(n - 1);
     }
 }
 
@@ -672,17 +680,21 @@ hipError_t launch(const DeltaArgs& a) {
     return hipGetLastError();
 }
 
-template <int KT>
+template <int KT, int NP, bool EMIT, bool SAVE>
 hipError_t launch_pairs(const DeltaArgs& a) {
-    const int cols = (a.vdim + 31) / 32;
-    const dim3 grid(static_cast<unsigned>((a.batch * a.vheads + 7) / 8 * 8 * cols));
-    if (a.out)
-        hipLaunchKernelGGL((fwd_pairs_kernel<KT, true>), grid, dim3(256), 0, a.stream, a,
-                           static_cast<int64_t>(delta_chunk_bytes()), cols);
-    else
-        hipLaunchKernelGGL((fwd_pairs_kernel<KT, false>), grid, dim3(256), 0, a.stream, a,
-                           static_cast<int64_t>(delta_chunk_bytes()), cols);
+    const int cols = (a.vdim + 16 * NP - 1) / (16 * NP);
+    hipLaunchKernelGGL((fwd_pairs_kernel<KT, NP, EMIT, SAVE>), dim3(static_cast<unsigned>((a.batch * a.vheads + 7) / 8 * 8 * cols)),
+                       dim3(NP * 128), (kPairsLds<KT, NP, EMIT>), a.stream, a, static_cast<int64_t>(delta_chunk_bytes()), cols);
     return hipGetLastError();
+}
+template <int KT, int NP>
+hipError_t pairs_by_outputs(const DeltaArgs& a) {
+    if (!a.out) return launch_pairs<KT, NP, false, true>(a);
+    return a.states ? launch_pairs<KT, NP, true, true>(a) : launch_pairs<KT, NP, true, false>(a);
+}
+template <int KT>
+hipError_t pairs_by_columns(const DeltaArgs& a) {
+    return wide_groups(a) ? pairs_by_outputs<KT, 4>(a) : pairs_by_outputs<KT, 2>(a);
 }
 
 template <typename T, bool VEC>
@@ -693,7 +705,7 @@ hipError_t by_width(const DeltaArgs& a) {
 }  // namespace
 
 hipError_t launch_delta_fwd(const DeltaArgs& a) {
-    if (a.bf16 && a.vec_k) return a.kdim > 64 ? launch_pairs<128>(a) : launch_pairs<64>(a);
+    if (a.bf16 && a.vec_k) return a.kdim > 64 ? pairs_by_columns<128>(a) : pairs_by_columns<64>(a);
     if (a.bf16) return by_width<bf16_t, false>(a);
     return a.vec_k ? by_width<float, true>(a) : by_width<float, false>(a);
 }

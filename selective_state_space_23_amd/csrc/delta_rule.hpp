@@ -100,6 +100,15 @@ __device__ __forceinline__ void without_pieces(uint32_t h, float& x0, float& x1)
     x1 = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, h), __builtin_bit_cast(bf16x2_t, second), x1, false);
 }
 
+// A value that the compiler does not know: what is computed from it stays where it is used.
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// Whether a workgroup takes 64 columns of a head rather than 32.
+inline bool wide_groups(const DeltaArgs& a) { return a.batch * a.vheads * ((a.vdim + 31) / 32) > 256; }
+
 // The bf16 pieces of pairs of floats, cut off: the highest 8 significant bits, the next and the last.
 __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
     hi = __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302u);

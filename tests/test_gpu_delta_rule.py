@@ -249,6 +249,31 @@ def test_backward_of_slices_without_decay(ssm):
         close(got[n], ref[n], n, n in IO, 2.0)
 
 
+@pytest.mark.parametrize("K,V", [(128, 100), (48, 40)])
+def test_many_heads(ssm, K, V):
+    """Enough rows for wider workgroups: each row as it is alone, to the bit, also where a value is not finite."""
+    import torch
+
+    d = draw(2, 150, 2, 4, K, V, "bf16", 60, True, seed=23)
+    d["v"][0, 70, 1, 5] = np.nan
+    d["q"][1, 20, 0, 3] = np.inf
+    d["dout"][1, 100, 2, 7] = np.nan
+    t = dev(d, "bf16")
+    many = {n: None if x is None else x.repeat((70,) + (1,) * (x.ndim - 1)) for n, x in t.items()}
+    bits = lambda x: x.view(torch.int16 if x.dtype == torch.bfloat16 else torch.int32)  # noqa: E731
+
+    def same(got, ref, what):
+        assert (bits(got).unflatten(0, (70, 2)) == bits(ref)).all(), what
+
+    few, lot = forward(ssm, t, save="states"), forward(ssm, many, save="states")
+    for got, ref, what in zip(lot[:2] + (lot[2]["states"],), few[:2] + (few[2]["states"],), ("out", "final", "states")):
+        same(got, ref, what)
+    same(forward(ssm, many)[0], few[0], "out alone")
+    few, lot = backward(ssm, t), backward(ssm, many)
+    for n in few:
+        same(lot[n], few[n], n)
+
+
 def test_backward_in_two_pieces(ssm):
     """A row cut at a token inside a chunk and differentiated back to front."""
     d = draw(2, 190, 1, 2, 48, 32, "f32", 60, True, seed=14)
