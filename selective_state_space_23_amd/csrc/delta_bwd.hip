@@ -297,10 +297,10 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
 // one walks dS -> dU -> dX -> dS, the other brings what does not depend on dS, P^T dO and
 // Z = (scale exp(gamma) Q)^T dO, and all loads.
 //
-// Chunk c:  barrier;  A: the chain forms K dS and dU;   the other forms Z of c, loads T of c, P and dO of c - 1;
-//           barrier;  B: the chain forms dX, then dS;   the other forms P^T dO of c - 1, loads K and Q of it.
+// Chunk c:  barrier;  A: the chain forms K dS and dU;   the other forms Z of c, loads P and dO of c - 1;
+//           barrier;  B: the chain forms dX, then dS;   the other forms P^T dO of c - 1, loads K, T and Q of it.
 template <int KT, int NP>
-constexpr int kPairsLds = 3 * C * KT * 2 + 2 * kBlocks * 3072 + 2 * 2048 + NP * (KT / 16 * 1024 + 4096 + 512);
+constexpr int kPairsLds = 3 * C * KT * 2 + 3 * kBlocks * 3072 + 2 * 2048 + NP * (KT / 16 * 1024 + 4096 + 512);
 // (LDS at the launch and two waves a SIMD: as in the forward, for sums in the lower registers)
 template <int KT, int NP>
 __global__ __launch_bounds__(NP * 128, 2) void bwd_pairs_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
@@ -309,13 +309,13 @@ __global__ __launch_bounds__(NP * 128, 2) void bwd_pairs_kernel(DeltaArgs a, int
     extern __shared__ __align__(16) char smem[];
     char* const Kb = smem;                       // [2] K
     char* const Rb = Kb + 2 * TILE;              // [2] record
-    char* const Tb = Rb + 2 * REC;               // triangle
-    char* const Qb = Tb + TRI;                   // Q
+    char* const Tb = Rb + 2 * REC;               // [2] triangle
+    char* const Qb = Tb + 2 * TRI;                   // Q
     char* const Pb = Qb + TILE;                  // P
     char* const Zb = Pb + TRI;                   // Z
     char* const Ub = Zb + NP * 2 * STEPS * 1024; // P^T dO
     char* const Lb = Ub + NP * 4096;             // a lane's rows that take no part
-    static_assert(kPairsLds<KT, NP> == 3 * TILE + 2 * TRI + 2 * REC + NP * ((2 * STEPS + 4) * 1024 + 512));
+    static_assert(kPairsLds<KT, NP> == 3 * TILE + 3 * TRI + 2 * REC + NP * ((2 * STEPS + 4) * 1024 + 512));
 
     const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), pair = wave & (NP - 1);
@@ -364,7 +364,7 @@ __global__ __launch_bounds__(NP * 128, 2) void bwd_pairs_kernel(DeltaArgs a, int
         lds_barrier();   // the other waves' first loads
         for (int c = n - 1; c >= 0; --c) {
             const uint16_t* Kl = reinterpret_cast<const uint16_t*>(buffer(Kb, TILE, c));
-            const u32x4* Tl = reinterpret_cast<const u32x4*>(Tb);
+            const u32x4* Tl = reinterpret_cast<const u32x4*>(buffer(Tb, TRI, c));
             const ChunkRec* rec = reinterpret_cast<const ChunkRec*>(buffer(Rb, REC, c));
             lds_barrier();
             // A: dU = exp(gamma_C - gamma) K dS + P^T dO
@@ -534,16 +534,14 @@ __global__ __launch_bounds__(NP * 128, 2) void bwd_pairs_kernel(DeltaArgs a, int
         f32x4 dO[4];
         uint64_t sick = 0;
         bool any_sick = false;
-        auto fetch_early = [&](int c) {   // K and Q, read from phase A on
-            const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C;
+        auto fetch_early = [&](int c) {
+            const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, id = bh * n + c;
             const int rows = rows_of(c);
             const Rsrc kr = rows_rsrc<2>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k, a.kdim);
             rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(buffer(Kb, TILE, c)), kr, a.ld_k, a.kdim, pair, lane);
             const Rsrc qr = rows_rsrc<2>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_q, a.kdim);
             rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(Qb), qr, a.ld_q, a.kdim, pair, lane);
-        };
-        auto fetch_triangle = [&](int c) {   // from phase B on
-            block_to_lds<kBlocks * 3, NP>(Tb, rsrc(a.solve_t + (bh * n + c) * kSolveBytes, kSolveBytes), pair, lane);
+            block_to_lds<kBlocks * 3, NP>(buffer(Tb, TRI, c), rsrc(a.solve_t + id * kSolveBytes, kSolveBytes), pair, lane);
         };
         auto fetch_rest = [&](int c) {   // from phase B of the chunk before on
             const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, id = bh * n + c;
@@ -683,7 +681,6 @@ __global__ __launch_bounds__(NP * 128, 2) void bwd_pairs_kernel(DeltaArgs a, int
         for (int c = n - 1; c >= 0; --c) {
             lds_barrier();
             // A
-            fetch_triangle(c);
             if (c > 0) fetch_rest(c - 1);
             entering(c);
             landed();

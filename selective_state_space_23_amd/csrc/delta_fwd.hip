@@ -291,32 +291,36 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
 // and all loads.  (One wave doing both, four to a workgroup: 64K tokens x 40 heads 6.0 ms; a chunk
 // then takes 1030 vector instructions, 182 matrix products and their waits one after the other.)
 //
-// Chunk c:  barrier;  A: the chain forms K S and R; the other loads T and Q of c and finishes O of c - 1;
-//           barrier;  B: the chain forms U, then S;   the other loads K and V of c + 1 and P of c and forms Q S.
+// Chunk c:  barrier;  A: the chain forms K S and R; the other loads K and T of c + 1 and finishes O of c - 1;
+//           barrier;  B: the chain forms U, then S;   the other loads V and Q of c + 1 and P of c and forms Q S.
+// NP = 4, whose LDS has no room for a second T and Q: those of c + 1 are loaded when U and Q S of c are there, behind a
+// third barrier.  (Loaded in A of their own chunk, and waited for there: 8 x 2048 tokens, 16 heads, 146 against XXX us.)
 //
 // A workgroup has NP such pairs, for as many 16 columns of one head, a chain and a follower on a SIMD with NP = 4: a wave
 // alone issues a vector instruction every 8 cycles, two together twice as many.
+template <int NP> constexpr int kBuffers = NP == 2 ? 2 : 1;   // of T and Q
 template <int KT, int NP, bool EMIT>
-constexpr int kPairsLds = 2 * C * KT * 2 + kBlocks * 3072 + 2 * 2048 + NP * (2048 + 512) +
-                          (EMIT ? C * KT * 2 + kBlocks * 2048 + NP * (KT / 32 * 2048 + 4096) : 0);
+constexpr int kPairsLds = 2 * C * KT * 2 + kBuffers<NP> * kBlocks * 3072 + 2 * 2048 + NP * (2048 + 512) +
+                          (EMIT ? kBuffers<NP> * C * KT * 2 + kBlocks * 2048 + NP * (KT / 32 * 2048 + 4096) : 0);
 // (LDS given at the launch, and two waves a SIMD asked for: one workgroup fills a CU either way, but where the compiler
 // sees that, it takes 512 registers, keeps sums in the upper 256 and moves them, 8 cycles each.)
 template <int KT, int NP, bool EMIT, bool SAVE>
 __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
     constexpr int STEPS = KT / 32;
     constexpr int TILE = C * KT * 2, TRI = kBlocks * 3 * 1024, PAIRS = kBlocks * 2 * 1024, REC = 2048;
+    constexpr int BUFFERS = kBuffers<NP>;
     extern __shared__ __align__(16) char smem[];
     char* const Kb = smem;                       // [2] K
     char* const Rb = Kb + 2 * TILE;              // [2] record
-    char* const Tb = Rb + 2 * REC;               // triangle
-    char* const Vb = Tb + TRI;                   // a lane's 16 values, packed
+    char* const Tb = Rb + 2 * REC;               // [BUFFERS] triangle
+    char* const Vb = Tb + BUFFERS * TRI;                   // a lane's 16 values, packed
     char* const Lb = Vb + NP * 64 * 32;          // a lane's lost rows
-    char* const Qb = Lb + NP * 64 * 8;           // Q
-    char* const Pb = Qb + TILE;                  // P
+    char* const Qb = Lb + NP * 64 * 8;           // [BUFFERS] Q
+    char* const Pb = Qb + BUFFERS * TILE;                // P
     char* const Sb = Pb + PAIRS;                 // S's first two pieces, as operands
     char* const Ub = Sb + NP * STEPS * 2048;     // U
-    static_assert(kPairsLds<KT, NP, EMIT> == 2 * (TILE + REC) + TRI + NP * (64 * 32 + 64 * 8) +
-                                                 (EMIT ? TILE + PAIRS + NP * (STEPS * 2048 + 4096) : 0));
+    static_assert(kPairsLds<KT, NP, EMIT> == 2 * (TILE + REC) + BUFFERS * TRI + NP * (64 * 32 + 64 * 8) +
+                                                 (EMIT ? BUFFERS * TILE + PAIRS + NP * (STEPS * 2048 + 4096) : 0));
 
     const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), pair = wave & (NP - 1);
@@ -333,6 +337,7 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
         return static_cast<int>(left < C ? left : C);
     };
     auto buffer = [&](char* first, int size, int c) { return first + (c & 1) * size; };
+    auto buffer2 = [&](char* first, int size, int c) { return BUFFERS == 2 ? first + (c & 1) * size : first; };
 
     if (wave < NP) {
         // ---- the chain
@@ -366,7 +371,7 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
         for (int j = 0; j < STEPS / 2; ++j) sf[j] = split(S[2 * j], S[2 * j + 1]);
         for (int c = 0; c < n; ++c) {
             const uint16_t* Kl = reinterpret_cast<const uint16_t*>(buffer(Kb, TILE, c));
-            const u32x4* Tl = reinterpret_cast<const u32x4*>(Tb);
+            const u32x4* Tl = reinterpret_cast<const u32x4*>(buffer2(Tb, TRI, c));
             const ChunkRec* rec = reinterpret_cast<const ChunkRec*>(buffer(Rb, REC, c));
             lds_barrier();
             // A: K S, R = V - exp(gamma) K S
@@ -473,6 +478,7 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
                         U[3] = mfma(t3, rf1.p[q], U[3]);
                     }
                 }
+                if constexpr (BUFFERS == 1) lds_barrier();   // T has been read
 #pragma unroll
                 for (int i = 0; i < 2 * STEPS; ++i)
 #pragma unroll
@@ -556,28 +562,31 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
         // ---- loads and outputs
         const uint32_t value_lane = v_in ? v * 2 : kPast;
         uint32_t vraw[16];
-        auto fetch_early = [&](int c) {   // what is read from phase A on
-            const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, id = bh * n + c;
-            const int rows = rows_of(c);
-            const Rsrc vr = rows_rsrc<2>(a.v, first * a.ld_v + static_cast<int64_t>(hv) * a.vdim, rows, a.ld_v, a.vdim);
+        auto fetch_keys = [&](int c) {
+            const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C;
+            const Rsrc kr = rows_rsrc<2>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows_of(c), a.ld_k, a.kdim);
+            rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(buffer(Kb, TILE, c)), kr, a.ld_k, a.kdim, pair, lane);
+        };
+        auto fetch_triangle = [&](int c) {
+            block_to_lds<kBlocks * 3, NP>(buffer2(Tb, TRI, c), rsrc(a.solve + (bh * n + c) * kSolveBytes, kSolveBytes), pair,
+                                          lane);
+        };
+        auto fetch_values = [&](int c) {
+            const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C;
+            const Rsrc vr = rows_rsrc<2>(a.v, first * a.ld_v + static_cast<int64_t>(hv) * a.vdim, rows_of(c), a.ld_v, a.vdim);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     vraw[4 * i + r] = load_one<bf16_t>(
                         vr, value_lane + static_cast<uint32_t>((16 * i + 4 * g + r) * static_cast<int>(a.ld_v) * 2));
-            const Rsrc kr = rows_rsrc<2>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k, a.kdim);
-            rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(buffer(Kb, TILE, c)), kr, a.ld_k, a.kdim, pair, lane);
-            block_to_lds<2, NP>(buffer(Rb, REC, c), rsrc(a.chunks + id * rec_bytes, sizeof(ChunkRec)), pair, lane);
+            block_to_lds<2, NP>(buffer(Rb, REC, c), rsrc(a.chunks + (bh * n + c) * rec_bytes, sizeof(ChunkRec)), pair, lane);
         };
-        auto fetch_late = [&](int c) {   // from phase B on
-            const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, id = bh * n + c;
-            block_to_lds<kBlocks * 3, NP>(Tb, rsrc(a.solve + id * kSolveBytes, kSolveBytes), pair, lane);
-            if constexpr (EMIT) {
-                const Rsrc qr =
-                    rows_rsrc<2>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows_of(c), a.ld_q, a.kdim);
-                rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(Qb), qr, a.ld_q, a.kdim, pair, lane);
-            }
+        auto queries = [&](int c) { return reinterpret_cast<uint16_t*>(buffer2(Qb, TILE, c)); };
+        auto fetch_queries = [&](int c) {
+            const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C;
+            const Rsrc qr = rows_rsrc<2>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows_of(c), a.ld_q, a.kdim);
+            rows_to_lds<KT, NP>(queries(c), qr, a.ld_q, a.kdim, pair, lane);
         };
         auto landed = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
         auto put_values = [&] {
@@ -588,7 +597,10 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
             to[0] = w[0];
             to[1] = w[1];
         };
-        fetch_early(0);
+        fetch_values(0);
+        fetch_keys(0);
+        fetch_triangle(0);
+        if constexpr (EMIT) fetch_queries(0);
         put_values();
         landed();
         f32x4 O[4];
@@ -624,7 +636,6 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
 #pragma unroll
                     for (int r = 0; r < 4; ++r) O[i][r] = nan_if((lost >> (16 * i + 4 * g + r)) & 1, O[i][r]);
             }
-            landed();   // before the stores, which need not be waited for
             const int64_t ldo = static_cast<int64_t>(a.vheads) * a.vdim;
             const Rsrc orr = rows_rsrc<2>(a.out, (b * a.seqlen + static_cast<int64_t>(c) * C) * ldo + hv * a.vdim, rows_of(c),
                                           ldo, a.vdim);
@@ -638,15 +649,20 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
         for (int c = 0; c < n; ++c) {
             lds_barrier();
             // A
-            fetch_late(c);
-            if (EMIT && c > 0) outputs(c - 1);
-            else landed();
+            if (c + 1 < n) {
+                fetch_keys(c + 1);
+                if constexpr (BUFFERS == 2) fetch_triangle(c + 1);
+            }
+            if constexpr (EMIT) {
+                if (c > 0) outputs(c - 1);
+            }
             lds_barrier();
             // B
-            if (c + 1 < n) fetch_early(c + 1);
+            if (c + 1 < n) fetch_values(c + 1);
             if constexpr (EMIT) {
+                if (BUFFERS == 2 && c + 1 < n) fetch_queries(c + 1);
                 block_to_lds<kBlocks * 2, NP>(Pb, rsrc(a.pairs + (bh * n + c) * pairs_bytes(2), pairs_bytes(2)), pair, lane);
-                const uint16_t* Ql = reinterpret_cast<const uint16_t*>(Qb);
+                const uint16_t* Ql = queries(c);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) O[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -657,6 +673,13 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
 #pragma unroll
                     for (int i = 0; i < 4; ++i) qf[i] = rows_frag<1, KT>(Ql, 16 * i + m, 4 * j + g);
                     products<2, 4>(O, qf, sf);
+                }
+            }
+            if constexpr (BUFFERS == 1) {
+                lds_barrier();
+                if (c + 1 < n) {
+                    fetch_triangle(c + 1);
+                    if constexpr (EMIT) fetch_queries(c + 1);
                 }
             }
             if (c + 1 < n) put_values();
