@@ -96,9 +96,12 @@ size_t state_bytes(const mamba_delta_dims_t* d) {   // of every chunk
     return round256(static_cast<size_t>(d->batch * d->value_heads * chunks_of(d)) * d->key_dim * d->value_dim * 4);
 }
 
+size_t dx_bytes(const mamba_delta_dims_t* d) {   // whole groups of 16 columns
+    return static_cast<size_t>(d->batch * d->value_heads * chunks_of(d)) * ((d->value_dim + 15) / 16) * mamba::kGroupFloats * 4;
+}
 size_t bwd_workspace(const mamba_delta_dims_t* d, bool have_states) {
     return d->batch * d->seqlen == 0 ? 0 : record_bytes(d) + 2 * solve_bytes(d) + pairs_bytes(d, true) +
-                                                (have_states ? 1 : 2) * state_bytes(d);
+                                                dx_bytes(d) + (have_states ? 1 : 2) * state_bytes(d);
 }
 
 mamba::DeltaArgs base_args(const mamba_delta_dims_t* d, const Sizes& s, const void* q, const void* k, const void* v,
@@ -211,7 +214,8 @@ int mamba_gated_delta_rule_bwd(const mamba_delta_dims_t* dims, const void* q, co
     mamba::DeltaArgs a = base_args(dims, s, q, k, v, g, beta, doc_start, initial_state, workspace, stream);
     a.solve_t = a.solve + solve_bytes(dims);
     a.pairs = a.solve_t + solve_bytes(dims);
-    a.dstates = reinterpret_cast<float*>(a.pairs + pairs_bytes(dims, true));
+    a.dx = reinterpret_cast<float*>(a.pairs + pairs_bytes(dims, true));
+    a.dstates = a.dx + dx_bytes(dims) / 4;
     a.states = states ? const_cast<float*>(states) : a.dstates + state_bytes(dims) / 4;
     a.dout = dout; a.d_final_state = d_final_state;
     a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.d_initial_state = d_initial_state;

@@ -19,6 +19,20 @@ namespace {
 
 using namespace delta;
 
+// dX of 64 tokens and the 16 columns of group `group`, as the lanes hold it; NaN where the rows took no part.
+__device__ __forceinline__ void store_dx(const DeltaArgs& a, int64_t id, int group, int lane, const f32x4* X, uint64_t sick) {
+    const int groups = (a.vdim + 15) / 16, at = __builtin_amdgcn_readfirstlane(group);
+    const Rsrc to = rsrc(a.dx + (id * groups + at) * kGroupFloats, at < groups ? kGroupFloats * 4 : 0);
+    const uint64_t mine = sick >> (4 * (opaque(lane) >> 4));   // (row numbers would be kept in registers)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f32x4 x = X[i];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = nan_if((mine >> (16 * i + r)) & 1, x[r]);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), to, lane * 16 + i * 1024, 0, 0);
+    }
+}
+
 template <typename T, int KT, int NW, bool VEC>
 __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
     constexpr int N = kPieces<T>, ESZ = sizeof(T), STEPS = KT / 32, THREADS = NW * 64;
@@ -238,6 +252,7 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
                     for (int q = 2 - p; q >= 0; --q)
 #pragma unroll
                         for (int i = 0; i < 2 * j + 2; ++i) X[i] = mfma(Tl[(high_block(i, j) * 3 + p) * 64 + lane], uf[j].p[q], X[i]);
+            store_dx(a, bh * n + c, v >> 4, lane, X, sick);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const f32x4 beta = four(rec->beta + 16 * i + 4 * g), into = four(rec->into + 16 * i + 4 * g);
@@ -452,6 +467,9 @@ __global__ __launch_bounds__(NP * 128, 2) void bwd_pairs_kernel(DeltaArgs a, int
                         X[1] = mfma(t1, uf0.p[q], X[1]);
                     }
                 }
+                __builtin_amdgcn_sched_barrier(0);
+                store_dx(a, bh * n + c, v >> 4, lane, X, PLAIN ? 0 : sick);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int i = 0; i < 2 * STEPS; ++i) {
                     const f32x4 z = *reinterpret_cast<const f32x4*>(Zb + ((pair * 2 * STEPS + i) * 64 + lane) * 16);

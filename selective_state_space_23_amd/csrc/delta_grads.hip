@@ -1,23 +1,23 @@
-// Gated delta rule, backward: every gradient of a chunk of 64 tokens, from the state S that
-// enters it and the gradient dS at the state that leaves it (delta_bwd.hip), all chunks at
-// once.  A workgroup takes one key head of a chunk and its value heads in turn, so that
-// dq and dk sum over them in a fixed order.
+// Gated delta rule, backward: every gradient of a chunk of 64 tokens, from the state S that enters it, the gradient dS at
+// the state that leaves it and the dX that the chain of dS went through (delta_bwd.hip), all chunks at once.  A workgroup
+// takes one key head of a chunk and its value heads in turn, so that dq and dk sum over them in a fixed order.
 //
-//     R = V - exp(gamma) K S,  E = (I + M b)^-1 R,  U = b E,  O = scale exp(gamma) Q S + P U,
-//     dU = P^T dO + exp(gamma_C - gamma) K dS,   dX = (I + b M)^-T dU,   dV = beta dX,
-//     dbeta = dX . E,   dgamma = dO . O - dV . V   (row by row),
+//     R = V - exp(gamma) K S,  E = (I + M b)^-1 R,  U = b E,  dX = (I + b M)^-T (P^T dO + exp(gamma_C - gamma) K dS),
+//     dV = beta dX,   dbeta = dX . E,   dgamma = q . dq - dV . V   (row by row, this value head's part of dq),
 //     dq = scale exp(gamma) dO S^T + dP K,                       dP = scale D o dO U^T (s <= t),
-//     dk = exp(gamma_C - gamma) U dS^T - exp(gamma) dV S^T + dP^T Q + N K,   N = G + G^T, G = -b D o dX U^T (s < t).
+//     dk = W - exp(gamma) dV S^T + dP^T Q + N K,   W = exp(gamma_C - gamma) U dS^T,   N = G + G^T, G = -b D o dX U^T (s < t).
 //
 // dgamma's form follows from every decay multiplying the key and value sums alike: scaling a
 // row's decay scales o . dO and v . dV by what it scales the row's query and value side, so the 64 x 64
-// matrices' row and column sums cancel to these two dot products.  At the chunk's end
-// <dS, S_out> = exp(gamma_C) <dS, S> + sum_t U . (exp(gamma_C - gamma) K dS) is added, and dg is the
+// matrices' row and column sums cancel to these two dot products; and o . dO = q . dq, as o is linear in q.  At the chunk's
+// end <dS, S_out> = exp(gamma_C) <dS, S> + sum_t k . W is added, and dg is the
 // sum of dgamma from its token to its document's (or the chunk's) end.
 //
-// Phases: (1) a wave owns 16 value columns, with K, Q and the triangles in LDS; (2) the tiles of
-// dP and N, contracted over the columns, with U and dX in LDS over K and Q; (3) a wave owns 16 key
-// channels: the products with S and dS; (4) those with K and Q, back in LDS.
+// Phases: (1) a wave owns 16 value columns, with K and the triangle in LDS; (2) the tiles of
+// dP and N, contracted over the columns, with U and dX in LDS over K; (3) a wave owns 16 key
+// channels: the products with S and dS; (4) those with K and Q, in LDS over U and dX.
+// What dgamma is made of has three pieces (U, dS, S beside dO, dP): its two dot products cancel.  dX beside S and U, and
+// N, only reach bf16 outputs when the inputs are bf16, and have two.
 #include "delta_rule.hpp"
 
 namespace mamba {
@@ -29,18 +29,35 @@ using namespace delta;
 constexpr int kWaves = 8, kThreads = kWaves * 64;
 constexpr int kRowV = 136, kRowP = 72;   // bf16 of a row of U and dX, of dP and N
 
-// Sum over the 16 lanes of a DPP row, in each of them.
-__device__ __forceinline__ float row_sum(float x) {
-    auto moved = [](float v, auto ctrl) {
-        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v),
-                                                                     decltype(ctrl)::value, 0xf, 0xf, false));
+template <int CTRL>
+__device__ __forceinline__ float moved(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, false));
+}
+// Sums over the 16 lanes of a DPP row: lane m gets that of the m-th value.  Lanes keep half of what they hold and pass
+// the other half on, four times: 45 instructions in place of 80 and a selection.
+__device__ __forceinline__ float row_sums(float (&x)[16], int m) {
+    auto turn = [&](int n, bool high, auto ctrl) {
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+            const float kept = high ? x[k + n] : x[k], passed = high ? x[k] : x[k + n];
+            x[k] = kept + moved<decltype(ctrl)::value>(passed);
+        }
     };
-    using I = int;
-    x += moved(x, std::integral_constant<I, 0xB1>{});    // quad_perm [1, 0, 3, 2]
-    x += moved(x, std::integral_constant<I, 0x4E>{});    // quad_perm [2, 3, 0, 1]
-    x += moved(x, std::integral_constant<I, 0x141>{});   // row_half_mirror
-    x += moved(x, std::integral_constant<I, 0x140>{});   // row_mirror
-    return x;
+    using std::integral_constant;
+    turn(8, (m & 8) != 0, integral_constant<int, 0x140>{});   // row_mirror: lane m with m ^ 15
+    turn(4, (m & 4) != 0, integral_constant<int, 0x141>{});   // row_half_mirror: m ^ 7
+    turn(2, (m & 2) != 0, integral_constant<int, 0x4E>{});    // quad_perm [2, 3, 0, 1]: m ^ 2
+    turn(1, (m & 1) != 0, integral_constant<int, 0xB1>{});    // quad_perm [1, 0, 3, 2]: m ^ 1
+    return x[0];
+}
+// Sum over a wave, in each lane.
+__device__ __forceinline__ float wave_sum(float x) {
+    x += moved<0xB1>(x);
+    x += moved<0x4E>(x);
+    x += moved<0x141>(x);
+    x += moved<0x140>(x);
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
 }
 
 // One value in N pieces, to element `at` of N planes of `plane` elements.
@@ -107,21 +124,23 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
     using KQ = Tile<T, KT, kThreads, VEC>;
     constexpr int PLANE_V = C * kRowV, PLANE_P = C * kRowP;
     constexpr size_t PARTS = 2 * kWaves * C * 4;
-    constexpr size_t ZERO = larger(2 * KQ::kBytes, size_t(2) * OUT * PLANE_V * 2);
-    constexpr size_t ONE = larger(2 * kSolveBytes + PARTS, size_t(2) * OUT * PLANE_P * 2);
+    constexpr size_t ZERO = larger(2 * KQ::kBytes, size_t(3 + OUT) * PLANE_V * 2);
+    constexpr size_t ONE = larger(kSolveBytes + PARTS, size_t(3 + OUT) * PLANE_P * 2);
     __shared__ __align__(16) char region0[ZERO];
     __shared__ __align__(16) char region1[ONE];
+    __shared__ __align__(16) uint16_t dout_[N == 1 ? PLANE_V : 8];   // dO [C][kRowV], where there is room for it
     __shared__ __align__(16) ChunkRec rec_;
     __shared__ float ends[kWaves];
+    __shared__ float turns[kWaves][C];   // q . dq, a wave's channels
     __shared__ uint64_t odd_rows[kWaves];
     uint16_t* Kl = reinterpret_cast<uint16_t*>(region0);
     uint16_t* Ql = Kl + N * C * KT;
-    uint16_t* Ul = reinterpret_cast<uint16_t*>(region0);          // [OUT][C][kRowV]
-    uint16_t* Xl = Ul + OUT * PLANE_V;
+    uint16_t* Ul = reinterpret_cast<uint16_t*>(region0);          // [3][C][kRowV]
+    uint16_t* Xl = Ul + 3 * PLANE_V;                              // [OUT] ...
     const u32x4* Tl = reinterpret_cast<const u32x4*>(region1);
-    float* parts = reinterpret_cast<float*>(region1 + 2 * kSolveBytes);   // [2][kWaves][C]
-    uint16_t* Pl = reinterpret_cast<uint16_t*>(region1);          // [OUT][C][kRowP]
-    uint16_t* Nl = Pl + OUT * PLANE_P;
+    float* parts = reinterpret_cast<float*>(region1 + kSolveBytes);   // [2][kWaves][C]
+    uint16_t* Pl = reinterpret_cast<uint16_t*>(region1);          // [3][C][kRowP]
+    uint16_t* Nl = Pl + 3 * PLANE_P;                              // [OUT] ...
     const ChunkRec* rec = &rec_;
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -132,7 +151,7 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
     const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, left = a.seqlen - static_cast<int64_t>(c) * C;
     const int rows = static_cast<int>(left < C ? left : C);
     const int64_t cells = static_cast<int64_t>(a.kdim) * a.vdim;
-    const int vsteps = (a.vdim + 31) / 32, vwaves = 2 * vsteps;
+    const int vsteps = (a.vdim + 31) / 32, vwaves = 2 * vsteps, groups = (a.vdim + 15) / 16;
     const Rsrc kr = rows_rsrc<ESZ>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k, a.kdim);
     const Rsrc qr = rows_rsrc<ESZ>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_q, a.kdim);
 
@@ -148,6 +167,7 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
         const Rsrc orr = rows_rsrc<ESZ>(a.dout, first * a.ld_o + static_cast<int64_t>(hv) * a.vdim, rows, a.ld_o, a.vdim);
         const Rsrc sr = rsrc(a.states + id * cells, cells * 4);
         const Rsrc dr = rsrc(a.dstates + id * cells, cells * 4);
+        const Rsrc xr = rsrc(a.dx + (id * groups + wave) * kGroupFloats, wave < groups ? kGroupFloats * 4 : 0);
 
         f32x4 U[4], X[4];
         uint64_t sick = 0, starts = 0;
@@ -156,74 +176,77 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
             const int tid = thread_now(), lane = tid & 63, g = lane >> 4, m = lane & 15;
             // (1) once more without the documents in which something is not finite, if there are any
             __syncthreads();
+            const bool no_state_ = pass != 0 && (sick & 1) != 0 && first_start > 0;
+            const int v = 16 * wave + m;
+            const uint32_t state_lane =
+                v < a.vdim && !no_state_ ? static_cast<uint32_t>(v * 4 + 8 * g * a.vdim * 4) : kPast;
+            f32x4 S[2 * STEPS];
             {
-                KQ kraw, qraw;
+                KQ kraw;
                 kraw.fetch(kr, a.ld_k, a.kdim, tid);
-                qraw.fetch(qr, a.ld_q, a.kdim, tid);
+                Eight<T, VEC> oraw[2];
+                if constexpr (N == 1) {
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+                        oraw[p].load(orr, static_cast<uint32_t>((32 * p + tid / 16) * static_cast<int>(a.ld_o) * ESZ),
+                                     tid % 16 * 8, a.vdim);
+                }
+                if (wave < vwaves) {
+#pragma unroll
+                    for (int i = 0; i < 2 * STEPS; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            S[i][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                                sr, state_lane + static_cast<uint32_t>(state_row(i, 0, r) * a.vdim * 4), 0, 0));
+                }
                 u32x4* Tw = reinterpret_cast<u32x4*>(region1);
-                const Rsrc t0 = rsrc(a.solve + id * kSolveBytes, kSolveBytes), t1 = rsrc(a.solve_t + id * kSolveBytes, kSolveBytes);
-                for (int p = wave; p < 2 * kBlocks * 3; p += kWaves)
-                    Tw[p * 64 + lane] = p < kBlocks * 3
-                        ? __builtin_amdgcn_raw_buffer_load_b128(t0, (p * 64 + lane) * 16, 0, 0)
-                        : __builtin_amdgcn_raw_buffer_load_b128(t1, ((p - kBlocks * 3) * 64 + lane) * 16, 0, 0);
+                const Rsrc t0 = rsrc(a.solve + id * kSolveBytes, kSolveBytes);
+                for (int p = wave; p < kBlocks * 3; p += kWaves)
+                    Tw[p * 64 + lane] = __builtin_amdgcn_raw_buffer_load_b128(t0, (p * 64 + lane) * 16, 0, 0);
                 const uint32_t* from = reinterpret_cast<const uint32_t*>(a.chunks + id * rec_bytes);
                 constexpr int RECW = sizeof(ChunkRec) / 4;
                 static_assert(RECW <= kThreads, "one word a thread");
                 reinterpret_cast<uint32_t*>(&rec_)[tid < RECW ? tid : RECW - 1] = from[tid < RECW ? tid : RECW - 1];
                 odd_rows[wave] = 0;
                 kraw.land_without(Kl, tid, sick);
-                qraw.land_without(Ql, tid, sick);
+                if constexpr (N == 1) {
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const int t = 32 * p + tid / 16;
+                        Frag<N> f = oraw[p].frag();
+                        clear_if<N>(f, (sick >> t) & 1);
+                        *reinterpret_cast<u32x4*>(dout_ + t * kRowV + tid % 16 * 8) = f.p[0];
+                    }
+                }
             }
             __syncthreads();
             starts = uniform(rec->starts);
             first_start = starts ? __builtin_ctzll(starts) : C;
             last_start = starts ? 63 - __builtin_clzll(starts) : 0;
-            const bool no_state = (sick & 1) != 0 && first_start > 0, no_dstate = (sick >> 63) != 0;
             if (wave < vwaves) {
-                const int v = 16 * wave + m;
                 const uint32_t value_lane = v < a.vdim ? v * ESZ : kPast;
-                const uint32_t state_lane = v < a.vdim && !no_state ? v * 4 : kPast;
-                const uint32_t dstate_lane = v < a.vdim && !no_dstate ? v * 4 : kPast;
-                f32x4 V[4], dO[4];
+                f32x4 V[4];
                 uint64_t odd = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i) {
+                    X[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, lane * 16 + i * 1024, 0, 0));
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int t = 16 * i + 4 * g + r;
                         const uint32_t at = (sick >> t) & 1 ? kPast : value_lane;
                         V[i][r] = one_value<T>(load_one<T>(vr, at + static_cast<uint32_t>(t * static_cast<int>(a.ld_v) * ESZ)));
-                        dO[i][r] = one_value<T>(load_one<T>(orr, at + static_cast<uint32_t>(t * static_cast<int>(a.ld_o) * ESZ)));
-                        odd |= uint64_t(not_finite(dO[i][r])) << t;
-                    }
-                f32x4 ks[4], qs[4], kd[4];
-                float inner = 0.0f;   // <dS, S> of this column, this group's channels
-#pragma unroll
-                for (int i = 0; i < 4; ++i) ks[i] = qs[i] = kd[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int j = 0; j < STEPS; ++j) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    f32x4 s0, s1, d0, d1;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t row = static_cast<uint32_t>((32 * j + 8 * g + e) * a.vdim * 4);
-                        const float x = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sr, state_lane + row, 0, 0));
-                        const float y = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(dr, dstate_lane + row, 0, 0));
-                        (e < 4 ? s0 : s1)[e & 3] = x;
-                        (e < 4 ? d0 : d1)[e & 3] = y;
-                        inner = __builtin_fmaf(x, y, inner);
-                    }
-                    const Frag<3> sf = split(s0, s1), df = split(d0, d1);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const Frag<N> kf = rows_frag<N, KT>(Kl, 16 * i + m, 4 * j + g);
-                        const Frag<N> qf = rows_frag<N, KT>(Ql, 16 * i + m, 4 * j + g);
-                        product<3>(ks[i], kf, sf);
-                        product<3>(qs[i], qf, sf);
-                        product<3>(kd[i], kf, df);
                     }
                 }
-                __builtin_amdgcn_sched_barrier(0);
+                f32x4 ks[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ks[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < STEPS; ++j) {
+                    Frag<N> kf[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kf[i] = rows_frag<N, KT>(Kl, 16 * i + m, 4 * j + g);
+                    products<3, 4>(ks, kf, split(S[2 * j], S[2 * j + 1]));
+                }
                 // R, and what is not finite row by row (before sums over tokens mix the rows)
                 f32x4 R[4];
 #pragma unroll
@@ -232,12 +255,9 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int t = 16 * i + 4 * g + r;
-                        const bool old = t < first_start;
-                        R[i][r] = V[i][r] - keep_if(old, into[r] * ks[i][r]);
-                        const float y = keep_if(t >= last_start, kd[i][r]);
-                        odd |= uint64_t(not_finite(R[i][r])) << t | uint64_t(not_finite(y)) << t;
-                        qs[i][r] = keep_if(old, a.scale * into[r] * qs[i][r]);
-                        odd |= uint64_t(not_finite(qs[i][r])) << t;
+                        R[i][r] = V[i][r] - keep_if(t < first_start, into[r] * ks[i][r]);
+                        X[i][r] = keep_if(!((sick >> t) & 1), X[i][r]);
+                        odd |= uint64_t(not_finite(R[i][r])) << t | uint64_t(not_finite(X[i][r])) << t;
                     }
                 }
                 // E, U
@@ -245,125 +265,25 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                 {
                     const Frag<3> rf[2] = {split(R[0], R[1]), split(R[2], R[3])};
 #pragma unroll
+                    for (int i = 0; i < 4; ++i) E[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int p = 2; p >= 0; --p)
+#pragma unroll
+                            for (int q = 2 - p; q >= 0; --q)
+#pragma unroll
+                                for (int i = 2 * j; i < 4; ++i)
+                                    E[i] = mfma(Tl[(low_block(i, j) * 3 + p) * 64 + lane], rf[j].p[q], E[i]);
+#pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        E[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                        for (int j = 0; j <= i / 2; ++j) {
-                            Frag<3> tf;
-#pragma unroll
-                            for (int p = 0; p < 3; ++p) tf.p[p] = Tl[(low_block(i, j) * 3 + p) * 64 + lane];
-                            product<3>(E[i], tf, rf[j]);
-                        }
                         const f32x4 beta = four(rec->beta + 16 * i + 4 * g);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) U[i][r] = beta[r] * E[i][r];
                     }
                 }
-                __builtin_amdgcn_sched_barrier(0);
-                // O, a tile of rows at a time, and dO . O over this wave's columns
-                float pb = 0.0f, pg = 0.0f;
-                {
-                    const Frag<3> uf[2] = {split(U[0], U[1]), split(U[2], U[3])};
-#pragma unroll
-                    for (int it = 0; it < 4; ++it) {
-                        __builtin_amdgcn_sched_barrier(0);
-                        f32x4 P[4];   // rows s, columns t
-#pragma unroll
-                        for (int is = 0; is < 4; ++is) P[is] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                        for (int j = 0; j < STEPS; ++j) {
-                            const Frag<N> qf = rows_frag<N, KT>(Ql, 16 * it + m, 4 * j + g);
-#pragma unroll
-                            for (int is = 0; is <= it; ++is)
-                                product<3>(P[is], rows_frag<N, KT>(Kl, 16 * is + m, 4 * j + g), qf);
-                        }
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            odd |= uint64_t(not_finite(keep_if(4 * g + r == m, P[it][r]))) << (16 * it + m);
-                        const int t = 16 * it + m, from = doc_first(starts, t);
-                        const float th = rec->hi[t], tl = rec->lo[t];
-#pragma unroll
-                        for (int is = 0; is <= it; ++is) {
-                            const f32x4 sh = four(rec->hi + 16 * is + 4 * g), sl = four(rec->lo + 16 * is + 4 * g);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const int s = 16 * is + 4 * g + r;
-                                const float d = exp2_fast((th - sh[r]) + (tl - sl[r]));
-                                P[is][r] = keep_if(s <= t && s >= from, a.scale * P[is][r] * d);
-                            }
-                        }
-#pragma unroll
-                        for (int j = 0; j <= it / 2; ++j) product<3>(qs[it], split(P[2 * j], P[2 * j + 1]), uf[j]);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const float y = row_sum(dO[it][r] * qs[it][r]);
-                            pg = m == 4 * it + r ? y : pg;
-                        }
-                    }
-                }
-                __builtin_amdgcn_sched_barrier(0);
-                // dU = outof K dS + P^T dO, and dX
-                {
-                    f32x4 dU[4];
-                    const Frag<3> of[2] = {split(dO[0], dO[1]), split(dO[2], dO[3])};
-                    float end = starts == 0 ? rec->keep * inner : 0.0f;
-#pragma unroll
-                    for (int is = 0; is < 4; ++is) {
-                        __builtin_amdgcn_sched_barrier(0);
-                        const f32x4 outof = four(rec->outof + 16 * is + 4 * g);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            dU[is][r] = keep_if(16 * is + 4 * g + r >= last_start, outof[r] * kd[is][r]);
-                            end = __builtin_fmaf(U[is][r], dU[is][r], end);
-                        }
-                        f32x4 P[4];   // rows t, columns s
-#pragma unroll
-                        for (int it = 0; it < 4; ++it) P[it] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                        for (int j = 0; j < STEPS; ++j) {
-                            const Frag<N> kf = rows_frag<N, KT>(Kl, 16 * is + m, 4 * j + g);
-#pragma unroll
-                            for (int it = is; it < 4; ++it)
-                                product<3>(P[it], rows_frag<N, KT>(Ql, 16 * it + m, 4 * j + g), kf);
-                        }
-                        const int s = 16 * is + m, stop = doc_end(starts, s);
-                        const float sh = rec->hi[s], sl = rec->lo[s];
-#pragma unroll
-                        for (int it = is; it < 4; ++it) {
-                            const f32x4 th = four(rec->hi + 16 * it + 4 * g), tl = four(rec->lo + 16 * it + 4 * g);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const int t = 16 * it + 4 * g + r;
-                                const float d = exp2_fast((th[r] - sh) + (tl[r] - sl));
-                                P[it][r] = keep_if(t >= s && t < stop, a.scale * P[it][r] * d);
-                            }
-                        }
-#pragma unroll
-                        for (int j = is / 2; j < 2; ++j) {
-                            const Frag<3> pf = split(P[2 * j], P[2 * j + 1]);
-                            if constexpr (N == 1) product<3>(dU[is], pf, Frag<1>{{of[j].p[0]}});   // dO as stored is one piece
-                            else product<3>(dU[is], pf, of[j]);
-                        }
-                    }
-                    end = row_sum(end);
-                    end += __shfl_xor(end, 16);
-                    end += __shfl_xor(end, 32);
-                    ends[wave] = end;
-                    __builtin_amdgcn_sched_barrier(0);
-                    const Frag<3> uf[2] = {split(dU[0], dU[1]), split(dU[2], dU[3])};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        X[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                        for (int j = i / 2; j < 2; ++j) {
-                            Frag<3> tf;
-#pragma unroll
-                            for (int p = 0; p < 3; ++p) tf.p[p] = Tl[((kBlocks + high_block(i, j)) * 3 + p) * 64 + lane];
-                            product<3>(X[i], tf, uf[j]);
-                        }
-                    }
-                }
-                // dv, and the rows' other dot products over this wave's columns
+                float xe[16], vv[16];
+                // dv, and the rows' dot products over this wave's columns
                 const int64_t ldv = static_cast<int64_t>(a.vheads) * a.vdim;
                 const Rsrc dvr = rows_rsrc<ESZ>(a.dv, first * ldv + hv * a.vdim, rows, ldv, a.vdim);
 #pragma unroll
@@ -373,16 +293,15 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                     for (int r = 0; r < 4; ++r) {
                         const int t = 16 * i + 4 * g + r;
                         const float dv = beta[r] * X[i][r];
-                        const float x = row_sum(X[i][r] * E[i][r]), y = row_sum(dv * V[i][r]);
-                        pb = m == 4 * i + r ? x : pb;
-                        pg -= m == 4 * i + r ? y : 0.0f;
+                        xe[4 * i + r] = X[i][r] * E[i][r];
+                        vv[4 * i + r] = -dv * V[i][r];
                         store_one<T>(dvr, value_lane + static_cast<uint32_t>(t * static_cast<int>(ldv) * ESZ),
                                      nan_if((sick >> t) & 1, dv));
                     }
                 }
                 const int t = 16 * (m / 4) + 4 * g + m % 4;
-                parts[wave * C + t] = pb;
-                parts[(kWaves + wave) * C + t] = pg;
+                parts[wave * C + t] = row_sums(xe, m);
+                parts[(kWaves + wave) * C + t] = row_sums(vv, m);
                 if (__ballot(odd != 0) != 0) {
 #pragma unroll
                     for (int s = 1; s < 64; s *= 2) odd |= __shfl_xor(odd, s);
@@ -399,30 +318,18 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
         }
         sick_any |= sick;
 
+        double turn = 0.0;   // wave 0: -dV . V of token `lane`
         if (wave == 0) {
             const int lane = thread_now() & 63;
-            float pb = 0.0f, end = 0.0f;
-            double sum = 0.0;
+            float pb = 0.0f;
             for (int w = 0; w < vwaves; ++w) {
                 pb += parts[w * C + lane];
-                sum += parts[(kWaves + w) * C + lane];
-                end += ends[w];
+                turn += parts[(kWaves + w) * C + lane];
             }
-            const int stop = doc_end(starts, lane);
-#pragma unroll
-            for (int s = 1; s < 64; s *= 2) {
-                const double other = __shfl_down(sum, s);
-                sum += lane + s < stop ? other : 0.0;
-            }
-            if (lane >= last_start) sum += end;
-            const bool nan = (sick >> lane) & 1, start = (starts >> lane) & 1;
             const Rsrc br = rows_rsrc<4>(a.dbeta, first * a.vheads + hv, rows, a.vheads, 1);
-            const Rsrc gr = rows_rsrc<4>(a.dg, a.dg ? first * a.vheads + hv : 0, a.dg ? rows : 0, a.vheads, 1);
-            store_one<float>(br, static_cast<uint32_t>(lane * a.vheads * 4), nan_if(nan, pb));
-            store_one<float>(gr, static_cast<uint32_t>(lane * a.vheads * 4),
-                             nan_if(nan, keep_if(!start, static_cast<float>(sum))));
+            store_one<float>(br, static_cast<uint32_t>(lane * a.vheads * 4), nan_if((sick >> lane) & 1, pb));
         }
-        // (2) U and dX over K and Q
+        // (2) U and dX over K
         if (wave < vwaves) {
             const int lane = thread_now() & 63, g = lane >> 4, m = lane & 15;
             const int v = 16 * wave + m;
@@ -431,26 +338,41 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int at = (16 * i + 4 * g + r) * kRowV + v;
-                    put<OUT>(Ul, PLANE_V, at, U[i][r]);
+                    put<3>(Ul, PLANE_V, at, U[i][r]);
                     put<OUT>(Xl, PLANE_V, at, X[i][r]);
                 }
         }
         __syncthreads();
         const int lane = thread_now() & 63, g = lane >> 4, m = lane & 15;
         auto dout_frag = [&](int i, int j) {
-            Eight<T, VEC> e;
-            e.load(orr, static_cast<uint32_t>((16 * i + m) * static_cast<int>(a.ld_o) * ESZ), 32 * j + 8 * g, a.vdim);
-            Frag<N> f = e.frag();
-            clear_if<N>(f, (sick >> (16 * i + m)) & 1);
-            return f;
+            if constexpr (N == 1) {
+                return plane_frag<1>(dout_, 16 * i + m, 32 * j + 8 * g);
+            } else {
+                Eight<T, VEC> e;
+                e.load(orr, static_cast<uint32_t>((16 * i + m) * static_cast<int>(a.ld_o) * ESZ), 32 * j + 8 * g, a.vdim);
+                Frag<N> f = e.frag();
+                clear_if<N>(f, (sick >> (16 * i + m)) & 1);
+                return f;
+            }
         };
+        // the first rows of S and dS for (3)
+        const bool no_state = (sick & 1) != 0 && first_start > 0, no_dstate = (sick >> 63) != 0;
+        const uint32_t state_row_at = static_cast<uint32_t>((16 * wave + m) * a.vdim * 4);
+        Eight<float, VEC> se, de;
+        auto fetch_states = [&](int j) {
+            se.load(sr, state_row_at, 32 * j + 8 * g, no_state ? 0 : a.vdim);
+            de.load(dr, state_row_at, 32 * j + 8 * g, no_dstate ? 0 : a.vdim);
+        };
+        if constexpr (N == 1) fetch_states(0);   // (channels behind the last: zeros)
         for (int tile = wave; tile < 10; tile += kWaves) {
             const int it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, is = tile - it * (it + 1) / 2;
             f32x4 P = {0, 0, 0, 0}, G = {0, 0, 0, 0};
             for (int j = 0; j < vsteps; ++j) {
-                const Frag<OUT> uf = plane_frag<OUT>(Ul, 16 * is + m, 32 * j + 8 * g);
+                const Frag<3> uf = plane_frag<3>(Ul, 16 * is + m, 32 * j + 8 * g);
                 const Frag<OUT> xf = plane_frag<OUT>(Xl, 16 * it + m, 32 * j + 8 * g);
-                product<OUT>(P, dout_frag(it, j), uf);
+                const Frag<N> of = dout_frag(it, j);
+                __builtin_amdgcn_sched_barrier(0);
+                product<3>(P, of, uf);
                 product<OUT>(G, xf, uf);
             }
             const int s = 16 * is + m, stop = doc_end(starts, s);
@@ -460,35 +382,57 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                 const int t = 16 * it + 4 * g + r;
                 const float d = exp2_fast((rec->hi[t] - sh) + (rec->lo[t] - sl));
                 const bool on = t >= s && t < stop;
-                put<OUT>(Pl, PLANE_P, t * kRowP + s, keep_if(on, a.scale * d * P[r]));
+                put<3>(Pl, PLANE_P, t * kRowP + s, keep_if(on, a.scale * d * P[r]));
                 const float n = keep_if(on && t > s, -rec->beta[t] * d * G[r]);
                 const int pad = t * kRowP + C;   // for the lanes above the diagonal
                 put<OUT>(Nl, PLANE_P, t >= s ? t * kRowP + s : pad, n);
                 put<OUT>(Nl, PLANE_P, t > s ? s * kRowP + t : pad, n);
-                if (it == is + 1 && (is & 1) == 0) put<OUT>(Pl, PLANE_P, s * kRowP + t, 0.0f);   // read with the tile beside it
+                if (it == is + 1 && (is & 1) == 0) put<3>(Pl, PLANE_P, s * kRowP + t, 0.0f);   // read with the tile beside it
             }
         }
 
         // (3) the products with S and dS
-        const bool no_state = (sick & 1) != 0 && first_start > 0, no_dstate = (sick >> 63) != 0;
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 dqh[4], W[4];   // this value head's dq; what dS gives to dk
+        float end = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dqh[i] = W[i] = f32x4{0, 0, 0, 0};
         if (16 * wave < KT) {
-            f32x4 os[4], xs[4], us[4];
+            f32x4 xs[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) os[i] = xs[i] = us[i] = f32x4{0, 0, 0, 0};
-            const uint32_t row = static_cast<uint32_t>((16 * wave + m) * a.vdim * 4);
+            for (int i = 0; i < 4; ++i) xs[i] = f32x4{0, 0, 0, 0};
             for (int j = 0; j < vsteps; ++j) {
-                Eight<float, VEC> se, de;
-                se.load(sr, row, 32 * j + 8 * g, no_state ? 0 : a.vdim);
-                de.load(dr, row, 32 * j + 8 * g, no_dstate ? 0 : a.vdim);
-                const Frag<OUT> sf = split_out<OUT>(__builtin_bit_cast(f32x4, se.a), __builtin_bit_cast(f32x4, se.b));
-                const Frag<OUT> df = split_out<OUT>(__builtin_bit_cast(f32x4, de.a), __builtin_bit_cast(f32x4, de.b));
+                if constexpr (N != 1) fetch_states(j);   // (fewer registers are free)
+                const f32x4 s0 = __builtin_bit_cast(f32x4, se.a), s1 = __builtin_bit_cast(f32x4, se.b);
+                const f32x4 d0 = __builtin_bit_cast(f32x4, de.a), d1 = __builtin_bit_cast(f32x4, de.b);
+                if (N == 1 && j + 1 < vsteps) fetch_states(j + 1);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    product<OUT>(os[i], dout_frag(i, j), sf);
-                    product<OUT>(xs[i], plane_frag<OUT>(Xl, 16 * i + m, 32 * j + 8 * g), sf);
-                    product<OUT>(us[i], plane_frag<OUT>(Ul, 16 * i + m, 32 * j + 8 * g), df);
+                for (int r = 0; r < 4; ++r) end = __builtin_fmaf(s0[r], d0[r], __builtin_fmaf(s1[r], d1[r], end));
+                const Frag<3> sf = split(s0, s1), df = split(d0, d1);
+                if constexpr (N == 1) {
+                    Frag<N> of[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) of[i] = dout_frag(i, j);
+                    Frag<OUT> xf[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) xf[i] = plane_frag<OUT>(Xl, 16 * i + m, 32 * j + 8 * g);
+                    products<3, 4>(dqh, of, sf);
+                    products<OUT, 4>(xs, xf, sf);
+                    __builtin_amdgcn_sched_barrier(0);
+                    Frag<3> uf[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) uf[i] = plane_frag<3>(Ul, 16 * i + m, 32 * j + 8 * g);
+                    products<3, 4>(W, uf, df);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        product<3>(dqh[i], dout_frag(i, j), sf);
+                        product<OUT>(xs[i], plane_frag<OUT>(Xl, 16 * i + m, 32 * j + 8 * g), sf);
+                        product<3>(W[i], plane_frag<3>(Ul, 16 * i + m, 32 * j + 8 * g), df);
+                    }
                 }
             }
+            end = starts == 0 ? rec->keep * end : 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const f32x4 into = four(rec->into + 16 * i + 4 * g), outof = four(rec->outof + 16 * i + 4 * g);
@@ -497,8 +441,9 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                 for (int r = 0; r < 4; ++r) {
                     const int t = 16 * i + 4 * g + r;
                     const bool old = t < first_start;
-                    dq[i][r] += keep_if(old, a.scale * into[r] * os[i][r]);
-                    dk[i][r] += keep_if(t >= last_start, outof[r] * us[i][r]) - keep_if(old, into[r] * beta[r] * xs[i][r]);
+                    dqh[i][r] = keep_if(old, a.scale * into[r] * dqh[i][r]);
+                    W[i][r] = keep_if(t >= last_start, outof[r] * W[i][r]);
+                    dk[i][r] += W[i][r] - keep_if(old, into[r] * beta[r] * xs[i][r]);
                 }
             }
         }
@@ -513,18 +458,96 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
             qraw.land_without(Ql, tid, sick);
         }
         __syncthreads();
+        const int lane4 = thread_now() & 63;
+        float dots = 0.0f;   // q . dq of row 16 (m / 4) + 4 g + m % 4
         if (16 * wave < KT) {
+            const int g = lane4 >> 4, m = lane4 & 15;
+            // (loads in front of what uses them: the compiler would wait for each in turn)
+            auto values = [&](float (&x)[16], const uint16_t* from) {
+                uint32_t raw[N][16];
+#pragma unroll
+                for (int p = 0; p < N; ++p)
+#pragma unroll
+                    for (int n = 0; n < 16; ++n)
+                        raw[p][n] = from[place<KT>(16 * (n / 4) + 4 * g + n % 4, 2 * wave + m / 8) + m % 8 + p * C * KT];
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int n = 0; n < 16; ++n) {
+                    x[n] = 0.0f;
+#pragma unroll
+                    for (int p = N - 1; p >= 0; --p) x[n] += __uint_as_float(raw[p][n] << 16);
+                }
+            };
+            {
+                float kv[16];
+                values(kv, Kl);
+#pragma unroll
+                for (int n = 0; n < 16; ++n) end = __builtin_fmaf(kv[n], W[n / 4][n % 4], end);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            const Frag<N> kf[2] = {cols_frag<N, KT>(Kl, 0, g, m, 16 * wave + 4 * (m % 4)),
+                                   cols_frag<N, KT>(Kl, 1, g, m, 16 * wave + 4 * (m % 4))};
+            const Frag<N> qf[2] = {cols_frag<N, KT>(Ql, 0, g, m, 16 * wave + 4 * (m % 4)),
+                                   cols_frag<N, KT>(Ql, 1, g, m, 16 * wave + 4 * (m % 4))};
+            Frag<3> pf[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pf[i] = token_frag<3>(Pl, 16 * i + m, 0, g);
+            __builtin_amdgcn_sched_barrier(0);
+            products<3, 4>(dqh, pf, kf[0]);
+#pragma unroll
+            for (int i = 2; i < 4; ++i) pf[i] = token_frag<3>(Pl, 16 * i + m, 1, g);
+            __builtin_amdgcn_sched_barrier(0);
+            products<3, 2>(dqh + 2, pf + 2, kf[1]);
+            Frag<OUT> nf[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const Frag<N> kf = cols_frag<N, KT>(Kl, j, g, m, 16 * wave + 4 * (m % 4));
-                const Frag<N> qf = cols_frag<N, KT>(Ql, j, g, m, 16 * wave + 4 * (m % 4));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (j <= i / 2) product<OUT>(dq[i], token_frag<OUT>(Pl, 16 * i + m, j, g), kf);
-                    if (j >= i / 2) product<OUT>(dk[i], token_cols<OUT>(Pl, j, g, m, 16 * i + 4 * (m % 4)), qf);
-                    product<OUT>(dk[i], token_frag<OUT>(Nl, 16 * i + m, j, g), kf);
-                }
+                for (int i = 0; i < 4; ++i) nf[i] = token_frag<OUT>(Nl, 16 * i + m, j, g);
+                __builtin_amdgcn_sched_barrier(0);
+                products<OUT, 4>(dk, nf, kf[j]);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) nf[i] = token_cols<OUT>(Pl, 1, g, m, 16 * i + 4 * (m % 4));
+            __builtin_amdgcn_sched_barrier(0);
+            products<OUT, 4>(dk, nf, qf[1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) nf[i] = token_cols<OUT>(Pl, 0, g, m, 16 * i + 4 * (m % 4));
+            __builtin_amdgcn_sched_barrier(0);
+            products<OUT, 2>(dk, nf, qf[0]);
+            __builtin_amdgcn_sched_barrier(0);
+            float qv[16];
+            values(qv, Ql);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    qv[4 * i + r] *= dqh[i][r];
+                    dq[i][r] += dqh[i][r];
+                }
+            dots = row_sums(qv, m);
+        }
+        end = wave_sum(end);
+        ends[wave] = end;
+        turns[wave][16 * (m / 4) + 4 * g + m % 4] = dots;
+        __syncthreads();
+        if (wave == 0) {
+            const int lane = thread_now() & 63;
+            float end = 0.0f;
+            for (int w = 0; w < KT / 16; ++w) {
+                turn += turns[w][lane];
+                end += ends[w];
+            }
+            const int stop = doc_end(starts, lane);
+#pragma unroll
+            for (int s = 1; s < 64; s *= 2) {
+                const double other = __shfl_down(turn, s);
+                turn += lane + s < stop ? other : 0.0;
+            }
+            if (lane >= last_start) turn += end;
+            const bool nan = (sick >> lane) & 1, start = (starts >> lane) & 1;
+            const Rsrc gr = rows_rsrc<4>(a.dg, a.dg ? first * a.vheads + hv : 0, a.dg ? rows : 0, a.vheads, 1);
+            store_one<float>(gr, static_cast<uint32_t>(lane * a.vheads * 4),
+                             nan_if(nan, keep_if(!start, static_cast<float>(turn))));
         }
     }
 

@@ -8,6 +8,7 @@
 namespace mamba {
 
 constexpr int kDeltaChunk = 64;       // tokens of a chunk, and between two saved states
+constexpr int kGroupFloats = kDeltaChunk * 16;
 constexpr int kDeltaMaxHead = 128;    // widest key and value heads
 
 // What every pass of one call shares.  Strides are elements between two tokens.
@@ -33,6 +34,7 @@ struct DeltaArgs {
     float* dbeta;
     float* d_initial_state;
     float* dstates;             // workspace: gradients at the chunks' end states
+    float* dx;                  // and the dX of their columns, 16 at a time
     // workspace written by the first pass
     char* chunks;               // one record per (row, value head, chunk)
     char* solve;                // the solved triangles, in the order the matrix cores read them
