@@ -36,7 +36,7 @@ namespace {
 using namespace delta;
 
 constexpr int kRowA = 68;   // floats between two rows of A in LDS (16-byte rows, 4 banks apart)
-constexpr int kRowD = 20;
+constexpr int kLds = (C * kRowA + 4 * C) * 4;   // eight workgroups of one wave a CU, as many as their registers leave room for
 
 __device__ __forceinline__ f32x4 mfma_f32(f32x4 a, f32x4 b, f32x4 c) {   // 16 x 16 x 16: a row m, b column m
 #pragma unroll
@@ -45,10 +45,15 @@ __device__ __forceinline__ f32x4 mfma_f32(f32x4 a, f32x4 b, f32x4 c) {   // 16 x
 }
 
 template <typename T, int KT, bool VEC, bool BWD>
-__global__ __launch_bounds__(64) void prepare_kernel(DeltaArgs a, size_t rec_bytes) {
-    __shared__ __align__(16) float As[C * kRowA];
-    __shared__ __align__(16) float Td[4 * 16 * kRowD];
-    __shared__ __align__(16) float hi[C], lo[C], bet[C], kk[C];
+__global__ __launch_bounds__(64, 2) void prepare_kernel(DeltaArgs a, size_t rec_bytes) {
+    // (given at the launch: where the compiler sees how few workgroups fit, it moves sums to the upper 256 registers and back)
+    extern __shared__ __align__(16) float As[];
+    float* const hi = As + C * kRowA;
+    float* const lo = hi + C;
+    float* const bet = lo + C;
+    float* const kk = bet + C;
+    // The solved diagonal blocks, in rows and columns of A that nothing else is in
+    auto solved = [&](int block, int t) { return As + (16 * (block & 1) + t) * kRowA + 32 + 16 * (block >> 1); };
     constexpr int N = kPieces<T>, ESZ = sizeof(T);
     const int lane = threadIdx.x, g = lane >> 4, m = lane & 15;
     const int64_t id = blockIdx.x;
@@ -238,7 +243,7 @@ __global__ __launch_bounds__(64) void prepare_kernel(DeltaArgs a, size_t rec_byt
                         }
                 }
                 x[t] = (t == m ? 1.0f : 0.0f) - (s0 + s1);
-                Td[(16 * g + t) * kRowD + m] = x[t];
+                solved(g, t)[m] = x[t];
             }
         }
         __syncthreads();
@@ -248,8 +253,8 @@ __global__ __launch_bounds__(64) void prepare_kernel(DeltaArgs a, size_t rec_byt
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) tri[i][i][r] = Td[(16 * i + 4 * g + r) * kRowD + m];
-            diag[i] = four(Td + (16 * i + m) * kRowD + 4 * g);
+            for (int r = 0; r < 4; ++r) tri[i][i][r] = solved(i, 4 * g + r)[m];
+            diag[i] = four(solved(i, m) + 4 * g);
         }
 #pragma unroll
         for (int d = 1; d < 4; ++d)
@@ -284,10 +289,10 @@ __global__ __launch_bounds__(64) void prepare_kernel(DeltaArgs a, size_t rec_byt
 template <typename T, int KT, bool VEC>
 hipError_t launch(const DeltaArgs& a, unsigned blocks) {
     if (a.solve_t)
-        hipLaunchKernelGGL((prepare_kernel<T, KT, VEC, true>), dim3(blocks), dim3(64), 0, a.stream, a,
+        hipLaunchKernelGGL((prepare_kernel<T, KT, VEC, true>), dim3(blocks), dim3(64), kLds, a.stream, a,
                            delta_chunk_bytes());
     else
-        hipLaunchKernelGGL((prepare_kernel<T, KT, VEC, false>), dim3(blocks), dim3(64), 0, a.stream, a,
+        hipLaunchKernelGGL((prepare_kernel<T, KT, VEC, false>), dim3(blocks), dim3(64), kLds, a.stream, a,
                            delta_chunk_bytes());
     return hipGetLastError();
 }
