@@ -99,28 +99,41 @@ __global__ __launch_bounds__(64, 2) void prepare_kernel(DeltaArgs a, size_t rec_
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = qk[i][j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < KT / 32; ++j) {
-        Eight<T, VEC> raw[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            raw[i].load(kr, static_cast<uint32_t>((16 * i + m) * static_cast<int>(a.ld_k) * ESZ), 32 * j + 8 * g, a.kdim);
-        Frag<N> f[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = raw[i].frag();
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int n = 0; n <= i; ++n) product<3>(acc[i][n], f[i], f[n]);
-        if (a.pairs) {
+    {
+        // all of a tensor's rows asked for before the first is waited for (bf16; floats would take twice the registers)
+        constexpr int STEPS = KT / 32, AHEAD = N == 1 ? STEPS : 1;
+        Eight<T, VEC> kraw[AHEAD][4], qraw[AHEAD][4];
+        auto fetch = [&](Eight<T, VEC> (*raw)[4], Rsrc rs, int64_t ld, int j) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                raw[i].load(qr, static_cast<uint32_t>((16 * i + m) * static_cast<int>(a.ld_q) * ESZ), 32 * j + 8 * g, a.kdim);
+                raw[j % AHEAD][i].load(rs, static_cast<uint32_t>((16 * i + m) * static_cast<int>(ld) * ESZ), 32 * j + 8 * g, a.kdim);
+        };
+        if constexpr (AHEAD > 1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const Frag<N> q = raw[i].frag();
+            for (int j = 0; j < STEPS; ++j) {
+                fetch(kraw, kr, a.ld_k, j);
+                if (a.pairs) fetch(qraw, qr, a.ld_q, j);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
-                for (int n = 0; n <= i; ++n) product<3>(qk[i][n], q, f[n]);
+        for (int j = 0; j < STEPS; ++j) {
+            if constexpr (AHEAD == 1) fetch(kraw, kr, a.ld_k, j);
+            Frag<N> f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = kraw[j % AHEAD][i].frag();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int n = 0; n <= i; ++n) product<3>(acc[i][n], f[i], f[n]);
+            if (a.pairs) {
+                if constexpr (AHEAD == 1) fetch(qraw, qr, a.ld_q, j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const Frag<N> q = qraw[j % AHEAD][i].frag();
+#pragma unroll
+                    for (int n = 0; n <= i; ++n) product<3>(qk[i][n], q, f[n]);
+                }
             }
         }
     }
