@@ -539,8 +539,8 @@ typedef struct {
     float scale;         /* finite (K^-1/2 is usual)                                */
 } mamba_delta_dims_t;
 
-/* Bytes of device workspace mamba_gated_delta_rule_fwd needs (about 310 per token
- * and value head, in whole chunks of 64 tokens). */
+/* Bytes of device workspace mamba_gated_delta_rule_fwd needs (504 per token
+ * and value head in bf16, 600 in float32, in whole chunks of 64 tokens). */
 int mamba_gated_delta_rule_workspace_bytes(const mamba_delta_dims_t* dims, size_t* bytes);
 
 /* Forward.
@@ -568,9 +568,9 @@ int mamba_gated_delta_rule_fwd(const mamba_delta_dims_t* dims, const void* q, co
                                const float* initial_state, void* out, float* final_state, float* states,
                                void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of device workspace mamba_gated_delta_rule_bwd needs: some 600 per token and
- * value head, and 4 K V per chunk of 64 for the gradients at the states between
- * chunks (8 K V without `states`). */
+/* Bytes of device workspace mamba_gated_delta_rule_bwd needs: 888 + 4 V (V rounded up
+ * to 16) per token and value head, and 4 K V per chunk of 64 for the gradients at the
+ * states between chunks (8 K V without `states`). */
 int mamba_gated_delta_rule_bwd_workspace_bytes(const mamba_delta_dims_t* dims, int32_t have_states, size_t* bytes);
 
 /* Backward: the gradients of sum(dout out) + sum(d_final_state final_state).

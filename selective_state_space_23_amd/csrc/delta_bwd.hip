@@ -6,7 +6,10 @@
 //
 // Columns do not mix here either: a wave owns 16, as in the forward (delta_fwd.hip), with dS
 // in its accumulators.  Everything that sums over columns is left to delta_grads.hip,
-// which works off the chunks at once from the states and gradients between them.
+// which works off the chunks at once from the states and gradients between them, and from dX as it is stored here.
+//
+// Bound by the chain as the forward is: 32768 tokens, 24 heads of 128 x 128, 512 chunks of 9000 cycles in 1.95 ms (3.27 ms
+// with one wave for everything).
 //
 // What is not finite makes the whole of its document NaN (through the state a gradient
 // reaches every token before, through the keys it came by every token after), and
@@ -36,11 +39,10 @@ __device__ __forceinline__ void store_dx(const DeltaArgs& a, int64_t id, int gro
 template <typename T, int KT, int NW, bool VEC>
 __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
     constexpr int N = kPieces<T>, ESZ = sizeof(T), STEPS = KT / 32, THREADS = NW * 64;
-    constexpr bool DIRECT = VEC && N == 1;   // to LDS without registers, in two buffers
     using KQ = Tile<T, KT, THREADS, VEC>;
     constexpr int TKB = kBlocks * 3, RKB = 2, BKB = 2 * TKB + RKB;   // KB of the triangle, of P and of a record
     constexpr size_t BUF = BKB * 1024 + 2 * KQ::kBytes;
-    __shared__ __align__(16) char smem[(DIRECT ? 2 : 1) * BUF];
+    __shared__ __align__(16) char buf[BUF];
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, m = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -75,10 +77,10 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
                 __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][r]), rs, state_off(i, r), 0, 0);
     };
 
-    KQ kraw, qraw;   // not DIRECT: the next chunk in registers
+    KQ kraw, qraw;   // the next chunk in registers
     u32x4 braw[(BKB + NW - 1) / NW];
     uint32_t oraw[16];
-    auto fetch = [&](int c, char* buf) {
+    auto fetch = [&](int c) {
         const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, left = a.seqlen - static_cast<int64_t>(c) * C;
         const int64_t id = bh * n + c;
         const int rows = static_cast<int>(left < C ? left : C);
@@ -86,22 +88,13 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
         const Rsrc qr = rows_rsrc<ESZ>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_q, a.kdim);
         const Rsrc tr = rsrc(a.solve_t + id * kSolveBytes, kSolveBytes), pr = rsrc(a.pairs + id * kSolveBytes, kSolveBytes);
         const Rsrc rr = rsrc(a.chunks + id * rec_bytes, sizeof(ChunkRec));
-        if constexpr (DIRECT) {
-            uint16_t* Kl = reinterpret_cast<uint16_t*>(buf + BKB * 1024);
-            rows_to_lds<KT, NW>(Kl, kr, a.ld_k, a.kdim, wave, lane);
-            block_to_lds<RKB, NW>(buf + 2 * TKB * 1024, rr, wave, lane);
-            block_to_lds<TKB, NW>(buf + TKB * 1024, pr, wave, lane);
-            block_to_lds<TKB, NW>(buf, tr, wave, lane);
-            rows_to_lds<KT, NW>(Kl + C * KT, qr, a.ld_q, a.kdim, wave, lane);
-        } else {
-            kraw.fetch(kr, a.ld_k, a.kdim, tid);
-            qraw.fetch(qr, a.ld_q, a.kdim, tid);
+        kraw.fetch(kr, a.ld_k, a.kdim, tid);
+        qraw.fetch(qr, a.ld_q, a.kdim, tid);
 #pragma unroll
-            for (int p = 0; p < (BKB + NW - 1) / NW; ++p) {
-                const int kb = p * NW + wave;
-                const int at = ((kb < TKB ? kb : kb < 2 * TKB ? kb - TKB : kb - 2 * TKB) * 64 + lane) * 16;
-                braw[p] = __builtin_amdgcn_raw_buffer_load_b128(kb < TKB ? tr : kb < 2 * TKB ? pr : rr, at, 0, 0);
-            }
+        for (int p = 0; p < (BKB + NW - 1) / NW; ++p) {
+            const int kb = p * NW + wave;
+            const int at = ((kb < TKB ? kb : kb < 2 * TKB ? kb - TKB : kb - 2 * TKB) * 64 + lane) * 16;
+            braw[p] = __builtin_amdgcn_raw_buffer_load_b128(kb < TKB ? tr : kb < 2 * TKB ? pr : rr, at, 0, 0);
         }
         const Rsrc orr = rows_rsrc<ESZ>(a.dout, first * a.ld_o + static_cast<int64_t>(hv) * a.vdim, rows, a.ld_o, a.vdim);
 #pragma unroll
@@ -112,29 +105,24 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
                     orr, value_lane + static_cast<uint32_t>((16 * i + 4 * g + r) * static_cast<int>(a.ld_o) * ESZ));
     };
 
-    fetch(n - 1, smem + (DIRECT && ((n - 1) & 1) ? BUF : 0));
+    fetch(n - 1);
     for (int c = n - 1; c >= 0; --c) {
-        char* buf = smem + (DIRECT && (c & 1) ? BUF : 0);
         const u32x4* Tl = reinterpret_cast<const u32x4*>(buf);   // [2][kBlocks][3][64]: the triangle, P
         const ChunkRec* rec = reinterpret_cast<const ChunkRec*>(buf + 2 * TKB * 1024);
         uint16_t* Kl = reinterpret_cast<uint16_t*>(buf + BKB * 1024);
         uint16_t* Ql = Kl + N * C * KT;
-        if constexpr (!DIRECT) {
-            kraw.land(Kl, tid);
-            qraw.land(Ql, tid);
+        kraw.land(Kl, tid);
+        qraw.land(Ql, tid);
 #pragma unroll
-            for (int p = 0; p < (BKB + NW - 1) / NW; ++p)
-                if (p * NW + wave < BKB) reinterpret_cast<u32x4*>(buf)[p * THREADS + tid] = braw[p];
-        } else {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        }
+        for (int p = 0; p < (BKB + NW - 1) / NW; ++p)
+            if (p * NW + wave < BKB) reinterpret_cast<u32x4*>(buf)[p * THREADS + tid] = braw[p];
         f32x4 dO[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r) dO[i][r] = one_value<T>(oraw[4 * i + r]);
         lds_barrier();
-        if (c > 0) fetch(c - 1, smem + (DIRECT && !(c & 1) ? BUF : 0));
+        if (c > 0) fetch(c - 1);
 
         const uint64_t starts = uniform(rec->starts), bad = uniform(rec->bad);
         const int first_start = starts ? __builtin_ctzll(starts) : C;
@@ -303,7 +291,7 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
 #pragma unroll
                 for (int r = 0; r < 4; ++r) S[i][r] = nan_if(dead, S[i][r]);
         }
-        if constexpr (!DIRECT) lds_barrier();
+        lds_barrier();
     }
     if (a.d_initial_state) store_state(a.d_initial_state + bh * cells);
 }
@@ -475,7 +463,8 @@ __global__ __launch_bounds__(NP * 128, 2) void bwd_pairs_kernel(DeltaArgs a, int
                     const f32x4 z = *reinterpret_cast<const f32x4*>(Zb + ((pair * 2 * STEPS + i) * 64 + lane) * 16);
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        S[i][r] = __builtin_fmaf(PLAIN ? S[i][r] : keep_if(starts == 0, S[i][r]), PLAIN ? keep : keep_if(starts == 0, keep), z[r]);
+                        S[i][r] = __builtin_fmaf(PLAIN ? S[i][r] : keep_if(starts == 0, S[i][r]),
+                                                 PLAIN ? keep : keep_if(starts == 0, keep), z[r]);
                 }
                 Frag<1> kf[2][4];
                 keys(kf[0], 0, 0);

@@ -6,10 +6,16 @@
 //
 // The columns of V, U, O and S do not mix, so a wave owns 16 of them for the whole
 // row and keeps S (K x 16) in its accumulators; R and U go from accumulator to
-// operand in place. The waves of a workgroup share what has no columns: K, Q, T and P in LDS;
-// where they are bf16 in whole 16-byte pieces the next chunk's go there straight from memory
-// while this one is worked off.
+// operand in place. The waves of a workgroup share what has no columns: K, Q, T and P in LDS, the next chunk's on
+// their way while this one is worked off.
 // Without an output the same walk forms the states alone, for the backward.
+//
+// A product of float32 operands, each in three bf16 pieces whose sum it is, takes the six products of pieces that reach
+// 2^-24 of it; a bf16 operand is one piece, and what only reaches a bf16 output has two.
+//
+// Bound by the chain of a row's chunks: 132 matrix products and some 400 vector instructions one behind the other
+// in a wave, with too few rows, heads and groups of columns to fill the card.  64K tokens x 40 heads of
+// 128 x 128: 2.7 ms, 1024 chunks of 6400 cycles; reading and writing it takes 0.5 ms.
 #include "delta_rule.hpp"
 
 namespace mamba {
@@ -18,16 +24,16 @@ namespace {
 
 using namespace delta;
 
+// float32, and bf16 that is not in whole 16-byte pieces.  (3 x 1001 tokens, 6 heads of 100 x 75 in float32: 141 us.)
 template <typename T, int KT, int NW, bool VEC, bool EMIT>
 __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
     constexpr int N = kPieces<T>, ESZ = sizeof(T), STEPS = KT / 32, THREADS = NW * 64;
-    constexpr bool DIRECT = VEC && N == 1;   // to LDS without registers, in two buffers
     using KQ = Tile<T, KT, THREADS, VEC>;
     constexpr int OUT = N == 1 ? 2 : 3;      // pieces that reach an output
     constexpr int TKB = kBlocks * 3, PKB = EMIT ? kBlocks * OUT : 0;
     constexpr int RKB = 2;                   // a record's 1304 bytes
     constexpr size_t BUF = (TKB + PKB + RKB) * 1024 + (EMIT ? 2 : 1) * KQ::kBytes;
-    __shared__ __align__(16) char smem[(DIRECT ? 2 : 1) * BUF];
+    __shared__ __align__(16) char buf[BUF];
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, m = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -65,10 +71,10 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
         return static_cast<int>(left < C ? left : C);
     };
 
-    KQ kraw, qraw;   // not DIRECT: the next chunk in registers
+    KQ kraw, qraw;   // the next chunk in registers
     u32x4 braw[(TKB + PKB + RKB + NW - 1) / NW];
     uint32_t vraw[16];
-    auto fetch = [&](int c, char* buf) {
+    auto fetch = [&](int c) {
         const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, id = bh * n + c;
         const int rows = rows_of(c);
         const Rsrc kr = rows_rsrc<ESZ>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k, a.kdim);
@@ -76,24 +82,13 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
         const Rsrc tr = rsrc(a.solve + id * kSolveBytes, kSolveBytes);
         const Rsrc pr = rsrc(a.pairs + (EMIT ? id * pairs_bytes(OUT) : 0), EMIT ? pairs_bytes(OUT) : 0);
         const Rsrc rr = rsrc(a.chunks + id * rec_bytes, sizeof(ChunkRec));
-        if constexpr (DIRECT) {
-            uint16_t* Kl = reinterpret_cast<uint16_t*>(buf + (TKB + PKB + RKB) * 1024);
-            rows_to_lds<KT, NW>(Kl, kr, a.ld_k, a.kdim, wave, lane);
-            block_to_lds<RKB, NW>(buf + (TKB + PKB) * 1024, rr, wave, lane);
-            block_to_lds<TKB, NW>(buf, tr, wave, lane);
-            if constexpr (EMIT) {
-                rows_to_lds<KT, NW>(Kl + C * KT, qr, a.ld_q, a.kdim, wave, lane);
-                block_to_lds<PKB, NW>(buf + TKB * 1024, pr, wave, lane);
-            }
-        } else {
-            kraw.fetch(kr, a.ld_k, a.kdim, tid);
-            if constexpr (EMIT) qraw.fetch(qr, a.ld_q, a.kdim, tid);
+        kraw.fetch(kr, a.ld_k, a.kdim, tid);
+        if constexpr (EMIT) qraw.fetch(qr, a.ld_q, a.kdim, tid);
 #pragma unroll
-            for (int p = 0; p < (TKB + PKB + RKB + NW - 1) / NW; ++p) {
-                const int kb = p * NW + wave;
-                const int at = ((kb < TKB ? kb : kb < TKB + PKB ? kb - TKB : kb - TKB - PKB) * 64 + lane) * 16;
-                braw[p] = __builtin_amdgcn_raw_buffer_load_b128(kb < TKB ? tr : kb < TKB + PKB ? pr : rr, at, 0, 0);
-            }
+        for (int p = 0; p < (TKB + PKB + RKB + NW - 1) / NW; ++p) {
+            const int kb = p * NW + wave;
+            const int at = ((kb < TKB ? kb : kb < TKB + PKB ? kb - TKB : kb - TKB - PKB) * 64 + lane) * 16;
+            braw[p] = __builtin_amdgcn_raw_buffer_load_b128(kb < TKB ? tr : kb < TKB + PKB ? pr : rr, at, 0, 0);
         }
         const Rsrc vr = rows_rsrc<ESZ>(a.v, first * a.ld_v + static_cast<int64_t>(hv) * a.vdim, rows, a.ld_v, a.vdim);
 #pragma unroll
@@ -104,28 +99,23 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
                     vr, value_lane + static_cast<uint32_t>((16 * i + 4 * g + r) * static_cast<int>(a.ld_v) * ESZ));
     };
 
-    fetch(0, smem);
+    fetch(0);
     for (int c = 0; c < n; ++c) {
-        char* buf = smem + (DIRECT && (c & 1) ? BUF : 0);
         const u32x4* Tl = reinterpret_cast<const u32x4*>(buf);                     // [kBlocks][3][64]
         const u32x4* Pl = Tl + TKB * 64;                                           // [kBlocks][OUT][64]
         const ChunkRec* rec = reinterpret_cast<const ChunkRec*>(buf + (TKB + PKB) * 1024);
         uint16_t* Kl = reinterpret_cast<uint16_t*>(buf + (TKB + PKB + RKB) * 1024);   // [N][C][KT]
         uint16_t* Ql = Kl + N * C * KT;
-        if constexpr (!DIRECT) {
-            kraw.land(Kl, tid);
-            if constexpr (EMIT) qraw.land(Ql, tid);
+        kraw.land(Kl, tid);
+        if constexpr (EMIT) qraw.land(Ql, tid);
 #pragma unroll
-            for (int p = 0; p < (TKB + PKB + RKB + NW - 1) / NW; ++p)
-                if (p * NW + wave < TKB + PKB + RKB) reinterpret_cast<u32x4*>(buf)[p * THREADS + tid] = braw[p];
-        } else {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        }
+        for (int p = 0; p < (TKB + PKB + RKB + NW - 1) / NW; ++p)
+            if (p * NW + wave < TKB + PKB + RKB) reinterpret_cast<u32x4*>(buf)[p * THREADS + tid] = braw[p];
         float vals[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) vals[i] = one_value<T>(vraw[i]);
         lds_barrier();
-        if (c + 1 < n) fetch(c + 1, smem + (DIRECT && !(c & 1) ? BUF : 0));
+        if (c + 1 < n) fetch(c + 1);
 
         const uint64_t starts = uniform(rec->starts), bad = uniform(rec->bad);
         const int first_start = starts ? __builtin_ctzll(starts) : C;
@@ -280,7 +270,7 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
 #pragma unroll
                 for (int r = 0; r < 4; ++r) S[i][r] = nan_if(dead, S[i][r]);
         }
-        if constexpr (!DIRECT) lds_barrier();
+        lds_barrier();
     }
     if (a.final_state) store_state(a.final_state + bh * cells);
 }
@@ -288,13 +278,12 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
 // The same for bf16 in whole 16-byte pieces, two waves for every 16 columns: one walks the chain
 // S -> R -> U -> S, which is what a row's time is, the other follows it by half a chunk with
 // everything that does not lead back to S: the outputs, from S and U as the first leaves them in LDS,
-// and all loads.  (One wave doing both, four to a workgroup: 64K tokens x 40 heads 6.0 ms; a chunk
-// then takes 1030 vector instructions, 182 matrix products and their waits one after the other.)
+// and all loads, straight to LDS.  (One wave doing both, four to a workgroup: 64K tokens x 40 heads 6.0 ms.)
 //
 // Chunk c:  barrier;  A: the chain forms K S and R; the other loads K and T of c + 1 and finishes O of c - 1;
 //           barrier;  B: the chain forms U, then S;   the other loads V and Q of c + 1 and P of c and forms Q S.
 // NP = 4, whose LDS has no room for a second T and Q: those of c + 1 are loaded when U and Q S of c are there, behind a
-// third barrier.  (Loaded in A of their own chunk, and waited for there: 8 x 2048 tokens, 16 heads, 146 against XXX us.)
+// third barrier.  (Loaded in A of their own chunk, and waited for there: 8 x 2048 tokens, 12 heads of 128 x 128, 146 us for 128.)
 //
 // A workgroup has NP such pairs, for as many 16 columns of one head, a chain and a follower on a SIMD with NP = 4: a wave
 // alone issues a vector instruction every 8 cycles, two together twice as many.

@@ -1,11 +1,11 @@
-// Gated delta rule token by token: the one-token step, and rows too short for the chunked form.
+// Gated delta rule: the step of one token.
 //
 // A workgroup keeps the K x (4 COLS) part of one head's state in registers, four
 // consecutive columns and K COLS / 256 consecutive rows a thread:
 //     S' = a S;  u = beta (v - S'^T k);  S = S' + k u^T;  out = scale S^T q,
-// the sums over rows by lane exchanges, then over the four waves through LDS. Bound by memory
-// (the state read and written once); the columns of one head are
-// split over workgroups where there are few heads, whose time is a trip to memory.
+// the sums over rows by lane exchanges, then over the four waves through LDS.  Bound by memory
+// (the state read and written once: 128 rows of 40 heads of 128 x 128 in 131 us, the time of a copy as large); the columns
+// of one head are split over workgroups where there are few heads, whose time is a trip to memory (two rows of 12: 8 us).
 #include "delta_rule.hpp"
 
 namespace mamba {
@@ -13,21 +13,6 @@ namespace mamba {
 namespace {
 
 using namespace delta;
-
-struct StepArgs {
-    const float* state_in;    // may be state_out, or null: zeros
-    float* state_out;         // or null
-    const void* q;
-    const void* k;
-    const void* v;
-    const float* g;
-    const float* beta;
-    const uint8_t* starts;    // (B, L) or null
-    void* out;
-    int64_t seqlen, ld_q, ld_k, ld_v;
-    int kheads, vheads, kdim, vdim, cols;
-    float scale;
-};
 
 // The sum over the workgroup's row groups of four columns, in every thread.
 template <int COLS>
@@ -43,15 +28,15 @@ __device__ __forceinline__ f32x4 over_rows(f32x4 x, f32x4 (*red)[COLS], int wave
 }
 
 template <typename T, int KT, int COLS, bool VEC>
-__global__ __launch_bounds__(256) void step_kernel(StepArgs a) {
+__global__ __launch_bounds__(256) void step_kernel(DeltaUpdateArgs a, int cols) {
     constexpr int R = KT * COLS / 256;   // rows a thread
     __shared__ __align__(16) float kv[128], qv[128];
     __shared__ __align__(16) f32x4 red[2][4][COLS];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t bh = quotient(blockIdx.x, a.cols);
+    const int64_t bh = quotient(blockIdx.x, cols);
     const int hv = remainder(bh, a.vheads), hk = quotient(hv, a.vheads / a.kheads);
     const int64_t b = quotient(bh, a.vheads);
-    const int v0 = (remainder(blockIdx.x, a.cols) * COLS + lane % COLS) * 4;
+    const int v0 = (remainder(blockIdx.x, cols) * COLS + lane % COLS) * 4;
     const int row0 = (wave * (64 / COLS) + lane / COLS) * R;
     const int64_t cells = static_cast<int64_t>(a.kdim) * a.vdim;
 
@@ -61,7 +46,7 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a) {
     for (int e = 0; e < 4; ++e) lane_off[e] = v0 + e < a.vdim ? (v0 + e) * 4 : kPast;
     f32x4 S[R];
     {
-        const Rsrc rs = rsrc(a.state_in + (a.state_in ? bh * cells : 0), a.state_in ? cells * 4 : 0);
+        const Rsrc rs = rsrc(a.state + bh * cells, cells * 4);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const uint32_t row = static_cast<uint32_t>((row0 + i) * a.vdim * 4);
@@ -74,63 +59,60 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a) {
             }
         }
     }
-    for (int64_t t = 0; t < a.seqlen; ++t) {
-        const int64_t tok = b * a.seqlen + t;
-        const bool start = a.starts != nullptr && a.starts[tok] != 0;
-        float gate = a.g != nullptr ? a.g[tok * a.vheads + hv] : 0.0f;
-        if (gate < -200.0f) gate = -200.0f;
-        const float decay = exp2_fast(gate * kLog2e), beta = a.beta[tok * a.vheads + hv];
-        f32x4 vals;
-        {
-            const Rsrc vr = rsrc(static_cast<const T*>(a.v) + tok * a.ld_v + static_cast<int64_t>(hv) * a.vdim,
-                                 a.vdim * static_cast<int>(sizeof(T)));
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                vals[e] = one_value<T>(load_one<T>(vr, static_cast<uint32_t>((v0 + e) * sizeof(T))));
-        }
-        {   // k by the first two waves, q by the others
-            const bool key = wave < 2;
-            const int ch = tid & 127;
-            const Rsrc r = key ? rsrc(static_cast<const T*>(a.k) + tok * a.ld_k + static_cast<int64_t>(hk) * a.kdim,
-                                      a.kdim * static_cast<int>(sizeof(T)))
-                               : rsrc(static_cast<const T*>(a.q) + tok * a.ld_q + static_cast<int64_t>(hk) * a.kdim,
-                                      a.kdim * static_cast<int>(sizeof(T)));
-            (key ? kv : qv)[ch] = one_value<T>(load_one<T>(r, static_cast<uint32_t>(ch * sizeof(T))));
-        }
-        __syncthreads();
-        float kr[R], qr[R];
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            kr[i] = kv[row0 + i];
-            qr[i] = qv[row0 + i];
-        }
-        f32x4 sum = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                S[i][e] = start ? 0.0f : S[i][e] * decay;
-                sum[e] = __builtin_fmaf(S[i][e], kr[i], sum[e]);
-            }
-        sum = over_rows<COLS>(sum, red[0], wave, lane);
-        f32x4 o = {0, 0, 0, 0};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float u = beta * (vals[e] - sum[e]);
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                S[i][e] = __builtin_fmaf(kr[i], u, S[i][e]);
-                o[e] = __builtin_fmaf(S[i][e], qr[i], o[e]);
-            }
-        }
-        o = over_rows<COLS>(o, red[1], wave, lane);
-        const Rsrc orr = rsrc(static_cast<T*>(a.out) + (tok * a.vheads + hv) * a.vdim, a.vdim * static_cast<int>(sizeof(T)));
+    const bool start = a.reset != nullptr && a.reset[b] != 0;
+    float gate = a.g != nullptr ? a.g[b * a.vheads + hv] : 0.0f;
+    if (gate < -200.0f) gate = -200.0f;
+    const float decay = exp2_fast(gate * kLog2e), beta = a.beta[b * a.vheads + hv];
+    f32x4 vals;
+    {
+        const Rsrc vr = rsrc(static_cast<const T*>(a.v) + b * a.ld_v + static_cast<int64_t>(hv) * a.vdim,
+                             a.vdim * static_cast<int>(sizeof(T)));
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            store_one<T>(orr, tid < COLS ? static_cast<uint32_t>((v0 + e) * sizeof(T)) : kPast, a.scale * o[e]);
+            vals[e] = one_value<T>(load_one<T>(vr, static_cast<uint32_t>((v0 + e) * sizeof(T))));
     }
-    if (a.state_out != nullptr) {
-        const Rsrc rs = rsrc(a.state_out + bh * cells, cells * 4);
+    {   // k by the first two waves, q by the others
+        const bool key = wave < 2;
+        const int ch = tid & 127;
+        const Rsrc r = key ? rsrc(static_cast<const T*>(a.k) + b * a.ld_k + static_cast<int64_t>(hk) * a.kdim,
+                                  a.kdim * static_cast<int>(sizeof(T)))
+                           : rsrc(static_cast<const T*>(a.q) + b * a.ld_q + static_cast<int64_t>(hk) * a.kdim,
+                                  a.kdim * static_cast<int>(sizeof(T)));
+        (key ? kv : qv)[ch] = one_value<T>(load_one<T>(r, static_cast<uint32_t>(ch * sizeof(T))));
+    }
+    __syncthreads();
+    float kr[R], qr[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        kr[i] = kv[row0 + i];
+        qr[i] = qv[row0 + i];
+    }
+    f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            S[i][e] = start ? 0.0f : S[i][e] * decay;
+            sum[e] = __builtin_fmaf(S[i][e], kr[i], sum[e]);
+        }
+    sum = over_rows<COLS>(sum, red[0], wave, lane);
+    f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float u = beta * (vals[e] - sum[e]);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            S[i][e] = __builtin_fmaf(kr[i], u, S[i][e]);
+            o[e] = __builtin_fmaf(S[i][e], qr[i], o[e]);
+        }
+    }
+    o = over_rows<COLS>(o, red[1], wave, lane);
+    const Rsrc orr = rsrc(static_cast<T*>(a.out) + (b * a.vheads + hv) * a.vdim, a.vdim * static_cast<int>(sizeof(T)));
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        store_one<T>(orr, tid < COLS ? static_cast<uint32_t>((v0 + e) * sizeof(T)) : kPast, a.scale * o[e]);
+    {
+        const Rsrc rs = rsrc(a.state + bh * cells, cells * 4);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const uint32_t row = static_cast<uint32_t>((row0 + i) * a.vdim * 4);
@@ -146,37 +128,24 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a) {
 }
 
 template <typename T, int KT, int COLS>
-hipError_t launch(StepArgs s, int64_t heads, bool vec, hipStream_t stream) {
-    s.cols = (s.vdim + 4 * COLS - 1) / (4 * COLS);
-    const dim3 grid(static_cast<unsigned>(heads * s.cols));
-    if (vec) hipLaunchKernelGGL((step_kernel<T, KT, COLS, true>), grid, dim3(256), 0, stream, s);
-    else hipLaunchKernelGGL((step_kernel<T, KT, COLS, false>), grid, dim3(256), 0, stream, s);
+hipError_t launch(const DeltaUpdateArgs& a) {
+    const int cols = (a.vdim + 4 * COLS - 1) / (4 * COLS);
+    const dim3 grid(static_cast<unsigned>(a.batch * a.vheads * cols));
+    if (a.vec) hipLaunchKernelGGL((step_kernel<T, KT, COLS, true>), grid, dim3(256), 0, a.stream, a, cols);
+    else hipLaunchKernelGGL((step_kernel<T, KT, COLS, false>), grid, dim3(256), 0, a.stream, a, cols);
     return hipGetLastError();
 }
 
+// Few heads: 32 columns a workgroup, more of them.  128 heads of 128 x 128: 4.6 us, 5.2 with 128 columns; 512: 9.3 and 8.7.
 template <typename T>
-hipError_t by_size(const StepArgs& s, int64_t heads, bool vec, hipStream_t stream) {
-    const bool few = heads < 512;
-    if (s.kdim > 64)
-        return few ? launch<T, 128, 8>(s, heads, vec, stream) : launch<T, 128, 32>(s, heads, vec, stream);
-    return few ? launch<T, 64, 8>(s, heads, vec, stream) : launch<T, 64, 32>(s, heads, vec, stream);
+hipError_t by_size(const DeltaUpdateArgs& a) {
+    const bool few = a.batch * a.vheads < 256;
+    if (a.kdim > 64) return few ? launch<T, 128, 8>(a) : launch<T, 128, 32>(a);
+    return few ? launch<T, 64, 8>(a) : launch<T, 64, 32>(a);
 }
 
 }  // namespace
 
-hipError_t launch_delta_update(const DeltaUpdateArgs& a) {
-    StepArgs s{};
-    s.state_in = a.state;
-    s.state_out = a.state;
-    s.q = a.q; s.k = a.k; s.v = a.v; s.g = a.g; s.beta = a.beta;
-    s.starts = a.reset;
-    s.out = a.out;
-    s.seqlen = 1;
-    s.ld_q = a.ld_q; s.ld_k = a.ld_k; s.ld_v = a.ld_v;
-    s.kheads = a.kheads; s.vheads = a.vheads; s.kdim = a.kdim; s.vdim = a.vdim;
-    s.scale = a.scale;
-    return a.bf16 ? by_size<bf16_t>(s, a.batch * a.vheads, a.vec, a.stream)
-                  : by_size<float>(s, a.batch * a.vheads, a.vec, a.stream);
-}
+hipError_t launch_delta_update(const DeltaUpdateArgs& a) { return a.bf16 ? by_size<bf16_t>(a) : by_size<float>(a); }
 
 }  // namespace mamba
