@@ -289,7 +289,9 @@ __global__ __launch_bounds__(kWaves * 64) void norm_kernel(Kernel p) {
                 if (lane < LPR && j < a.dim) sums[wave][j] = dw.b[e];
             }
             __syncthreads();
-            for (int i = threadIdx.x; i < a.dim; i += kWaves * 64)
+            static_assert(kNormMaxDim <= kWaves * 64, "a channel a thread");
+            const int i = threadIdx.x;
+            if (i < a.dim)
                 a.parts[static_cast<int64_t>(blockIdx.x) * a.dim + i] = (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
         }
     }
