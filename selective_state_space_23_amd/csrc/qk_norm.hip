@@ -139,13 +139,13 @@ __device__ __forceinline__ void store(Rsrc rs, uint32_t head, const Where& w, co
 
 // A lane's four cosines or sines (1 or 0 behind the rotated channels).
 template <int MODE>
-__device__ __forceinline__ f32x4 angles(Rsrc rs, const Where& w, float behind) {
+__device__ __forceinline__ f32x4 angles(Rsrc rs, const Where& w, float behind, uint32_t row = 0) {
     f32x4 t;
     if constexpr (MODE == kAny) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) t[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, 4 * (4 * w.l + e), 0, 0));
+        for (int e = 0; e < 4; ++e) t[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, row + 4 * (4 * w.l + e), 0, 0));
     } else {
-        t = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, 16 * w.l, 0, 0));
+        t = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, row + 16 * w.l, 0, 0));
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) t[e] = 4 * w.l + e < w.rot / 2 ? t[e] : behind;
@@ -171,6 +171,7 @@ __device__ __forceinline__ float head_sum(float x) {
 struct Split {            // one tensor's share of a launch
     int blocks;           // workgroups
     int splits, groups;   // waves a token, groups of heads a wave
+    int head_bits;        // PACKED: the lanes' groups divide into tokens of 1 << head_bits heads
 };
 
 struct Kernel {
@@ -178,7 +179,51 @@ struct Kernel {
     Split s[2];
 };
 
-template <typename T, int MODE, int LPR, bool BWD>
+// One head's pairs: normed and rotated, or (BWD) their gradients from dy, with the weight's into dw.
+template <int LPR, bool BWD>
+__device__ __forceinline__ Pairs normed(const Pairs& x, const Pairs& dy, const Pairs& weight, f32x4 c, f32x4 s, float inv_n,
+                                        float eps, Pairs& dw) {
+    float sq = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        sq = __builtin_fmaf(x.a[e], x.a[e], sq);
+        sq = __builtin_fmaf(x.b[e], x.b[e], sq);
+    }
+    const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(head_sum<LPR>(sq), inv_n, eps));
+    Pairs y;
+    if constexpr (!BWD) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float na = x.a[e] * r * weight.a[e], nb = x.b[e] * r * weight.b[e];
+            y.a[e] = __builtin_fmaf(na, c[e], -(nb * s[e]));
+            y.b[e] = __builtin_fmaf(nb, c[e], na * s[e]);
+        }
+    } else {
+        float dot = 0.0f;
+        Pairs dn;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float da = __builtin_fmaf(dy.a[e], c[e], dy.b[e] * s[e]);
+            const float db = __builtin_fmaf(dy.b[e], c[e], -(dy.a[e] * s[e]));
+            dw.a[e] = __builtin_fmaf(da * r, x.a[e], dw.a[e]);
+            dw.b[e] = __builtin_fmaf(db * r, x.b[e], dw.b[e]);
+            dn.a[e] = da * weight.a[e];
+            dn.b[e] = db * weight.b[e];
+            dot = __builtin_fmaf(dn.a[e], x.a[e], dot);
+            dot = __builtin_fmaf(dn.b[e], x.b[e], dot);
+        }
+        const float k = r * r * head_sum<LPR>(dot) * inv_n;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            y.a[e] = r * __builtin_fmaf(-k, x.a[e], dn.a[e]);
+            y.b[e] = r * __builtin_fmaf(-k, x.b[e], dn.b[e]);
+        }
+    }
+    return y;
+}
+
+// PACKED: tokens of few heads, several to a wave.
+template <typename T, int MODE, int LPR, bool BWD, bool PACKED>
 __global__ __launch_bounds__(kWaves * 64) void norm_kernel(Kernel p) {
     constexpr int G = 64 / LPR, ESZ = Elem<T>::kBytes;   // G: heads of a group
     constexpr int U = 2;                                 // groups under way
@@ -196,78 +241,94 @@ __global__ __launch_bounds__(kWaves * 64) void norm_kernel(Kernel p) {
     if (a.weight[which]) weight = load<float, MODE>(rsrc(a.weight[which], a.dim * 4), 0, w);
     Pairs dw = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
 
-    const uint32_t tasks = static_cast<uint32_t>(a.tokens) * splits, step = static_cast<uint32_t>(blocks) * kWaves;
-    for (uint32_t task = static_cast<uint32_t>(block) * kWaves + wave; task < tasks; task += step) {
-        const uint32_t token_ = splits == 1 ? task : task / splits;   // (the vector unit's division: one value all the same)
-        const int64_t token = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(token_));
-        const int split = __builtin_amdgcn_readfirstlane(task - static_cast<uint32_t>(token) * splits);
-        const Rsrc xr = rsrc(static_cast<const T*>(a.x[which]) + token * a.ld_x[which], int64_t(heads) * a.dim * ESZ);
-        const Rsrc yr = rsrc(static_cast<T*>(a.out[which]) + token * heads * a.dim, int64_t(heads) * a.dim * ESZ);
-        const Rsrc gr = rsrc(static_cast<const T*>(BWD ? a.dy[which] : a.x[which]) + (BWD ? token * a.ld_dy[which] : 0),
-                             BWD ? int64_t(heads) * a.dim * ESZ : 0);
-        f32x4 c = {1, 1, 1, 1}, s = {0, 0, 0, 0};
-        if (a.cos) {
-            const int64_t pos = a.positions ? a.positions[token] : static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(
-                static_cast<uint32_t>(token) % static_cast<uint32_t>(a.seqlen)));
-            const bool in = pos >= 0 && pos < a.table_rows;
-            const int64_t row = in ? pos * (a.rot / 2) : 0;
-            c = angles<MODE>(rsrc(a.cos + row, a.rot * 2), w, 1.0f);
-            s = angles<MODE>(rsrc(a.sin + row, a.rot * 2), w, 0.0f);
-            if (!in) {   // no row of the tables: nothing to rotate by
+    const uint32_t step = static_cast<uint32_t>(blocks) * kWaves;
+    if constexpr (PACKED) {
+        const int bits = p.s[which].head_bits, sub = (lane / LPR) >> bits, h = (lane / LPR) & ((1 << bits) - 1);
+        const uint32_t per = G >> bits, tokens = static_cast<uint32_t>(a.tokens);   // tokens of U groups under way: U * per
+        const uint32_t tasks = (tokens + U * per - 1) / (U * per);
+        const Rsrc cr = rsrc(a.cos, a.table_rows * a.rot * 2), sr = rsrc(a.sin, a.table_rows * a.rot * 2);
+        for (uint32_t task = static_cast<uint32_t>(block) * kWaves + wave; task < tasks; task += step) {
+            const int64_t first = static_cast<int64_t>(task) * (U * per);
+            const int64_t rows = a.tokens - first < U * per ? a.tokens - first : U * per;
+            auto from = [&](const void* base, int64_t ld) {
+                return rsrc(static_cast<const T*>(base) + first * ld, ((rows - 1) * ld + int64_t(heads) * a.dim) * ESZ);
+            };
+            const int64_t dense = int64_t(heads) * a.dim;
+            const Rsrc xr = from(a.x[which], a.ld_x[which]), yr = from(a.out[which], dense);
+            const Rsrc gr = BWD ? from(a.dy[which], a.ld_dy[which]) : xr;
+            Pairs x[U], dy[U] = {};
+            uint32_t at[U];
+            f32x4 c[U], s[U];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) c[e] = 4 * l + e < a.rot / 2 ? __builtin_nanf("") : 1.0f;
+            for (int u = 0; u < U; ++u) {
+                const uint32_t row = u * per + sub;
+                uint32_t head = h < heads && row < rows ? 0 : kPast;
+                asm("" : "+v"(head));   // (no branch around the loads)
+                head += static_cast<uint32_t>(h * a.dim * ESZ);
+                at[u] = row * static_cast<uint32_t>(dense * ESZ) + head;
+                x[u] = load<T, MODE>(xr, row * static_cast<uint32_t>(a.ld_x[which] * ESZ) + head, w);
+                if constexpr (BWD) dy[u] = load<T, MODE>(gr, row * static_cast<uint32_t>(a.ld_dy[which] * ESZ) + head, w);
+                c[u] = f32x4{1, 1, 1, 1};
+                s[u] = f32x4{0, 0, 0, 0};
+                if (a.cos) {
+                    const uint32_t token = static_cast<uint32_t>(first) + (row < rows ? row : 0);
+                    const int64_t pos = a.positions ? a.positions[token] : token % static_cast<uint32_t>(a.seqlen);
+                    const bool in = pos >= 0 && pos < a.table_rows;
+                    uint32_t nan = in ? 0 : 0x7fc00000;   // no row of the tables: nothing to rotate by
+                    asm("" : "+v"(nan));
+                    const uint32_t line = in ? static_cast<uint32_t>(pos) * static_cast<uint32_t>(a.rot * 2) : 0;
+                    c[u] = angles<MODE>(cr, w, 1.0f, line);
+                    s[u] = angles<MODE>(sr, w, 0.0f, line);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        c[u][e] = __uint_as_float(__float_as_uint(c[u][e]) | (4 * l + e < a.rot / 2 ? nan : 0));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const Pairs y = normed<LPR, BWD>(x[u], dy[u], weight, c[u], s[u], inv_n, a.eps, dw);
+                store<T, MODE>(yr, at[u], w, y);
             }
         }
-        const int end = (split + 1) * groups * G < heads ? (split + 1) * groups * G : heads;
-        for (int h0 = split * groups * G; h0 < end; h0 += U * G) {
-            Pairs x[U], dy[U];
-            uint32_t at[U];
+    } else {
+        const uint32_t tasks = static_cast<uint32_t>(a.tokens) * splits;
+        for (uint32_t task = static_cast<uint32_t>(block) * kWaves + wave; task < tasks; task += step) {
+            const uint32_t token_ = splits == 1 ? task : task / splits;   // (the vector unit's division: one value all the same)
+            const int64_t token = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(token_));
+            const int split = __builtin_amdgcn_readfirstlane(task - static_cast<uint32_t>(token) * splits);
+            const Rsrc xr = rsrc(static_cast<const T*>(a.x[which]) + token * a.ld_x[which], int64_t(heads) * a.dim * ESZ);
+            const Rsrc yr = rsrc(static_cast<T*>(a.out[which]) + token * heads * a.dim, int64_t(heads) * a.dim * ESZ);
+            const Rsrc gr = rsrc(static_cast<const T*>(BWD ? a.dy[which] : a.x[which]) + (BWD ? token * a.ld_dy[which] : 0),
+                                 BWD ? int64_t(heads) * a.dim * ESZ : 0);
+            f32x4 c = {1, 1, 1, 1}, s = {0, 0, 0, 0};
+            if (a.cos) {
+                const int64_t pos = a.positions ? a.positions[token] : static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(
+                    static_cast<uint32_t>(token) % static_cast<uint32_t>(a.seqlen)));
+                const bool in = pos >= 0 && pos < a.table_rows;
+                const int64_t row = in ? pos * (a.rot / 2) : 0;
+                c = angles<MODE>(rsrc(a.cos + row, a.rot * 2), w, 1.0f);
+                s = angles<MODE>(rsrc(a.sin + row, a.rot * 2), w, 0.0f);
+                if (!in) {   // no row of the tables: nothing to rotate by
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = h0 + u * G + lane / LPR;
-                at[u] = h < end ? static_cast<uint32_t>(h * a.dim * ESZ) : kPast;
-                x[u] = load<T, MODE>(xr, at[u], w);
-                if constexpr (BWD) dy[u] = load<T, MODE>(gr, at[u], w);
+                    for (int e = 0; e < 4; ++e) c[e] = 4 * l + e < a.rot / 2 ? __builtin_nanf("") : 1.0f;
+                }
             }
+            const int end = (split + 1) * groups * G < heads ? (split + 1) * groups * G : heads;
+            for (int h0 = split * groups * G; h0 < end; h0 += U * G) {
+                Pairs x[U], dy[U] = {};
+                uint32_t at[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float sq = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    sq = __builtin_fmaf(x[u].a[e], x[u].a[e], sq);
-                    sq = __builtin_fmaf(x[u].b[e], x[u].b[e], sq);
+                for (int u = 0; u < U; ++u) {
+                    const int h = h0 + u * G + lane / LPR;
+                    at[u] = h < end ? static_cast<uint32_t>(h * a.dim * ESZ) : kPast;
+                    x[u] = load<T, MODE>(xr, at[u], w);
+                    if constexpr (BWD) dy[u] = load<T, MODE>(gr, at[u], w);
                 }
-                const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(head_sum<LPR>(sq), inv_n, a.eps));
-                Pairs y;
-                if constexpr (!BWD) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float na = x[u].a[e] * r * weight.a[e], nb = x[u].b[e] * r * weight.b[e];
-                        y.a[e] = __builtin_fmaf(na, c[e], -(nb * s[e]));
-                        y.b[e] = __builtin_fmaf(nb, c[e], na * s[e]);
-                    }
-                } else {
-                    float dot = 0.0f;
-                    Pairs dn;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float da = __builtin_fmaf(dy[u].a[e], c[e], dy[u].b[e] * s[e]);
-                        const float db = __builtin_fmaf(dy[u].b[e], c[e], -(dy[u].a[e] * s[e]));
-                        dw.a[e] = __builtin_fmaf(da * r, x[u].a[e], dw.a[e]);
-                        dw.b[e] = __builtin_fmaf(db * r, x[u].b[e], dw.b[e]);
-                        dn.a[e] = da * weight.a[e];
-                        dn.b[e] = db * weight.b[e];
-                        dot = __builtin_fmaf(dn.a[e], x[u].a[e], dot);
-                        dot = __builtin_fmaf(dn.b[e], x[u].b[e], dot);
-                    }
-                    const float k = r * r * head_sum<LPR>(dot) * inv_n;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        y.a[e] = r * __builtin_fmaf(-k, x[u].a[e], dn.a[e]);
-                        y.b[e] = r * __builtin_fmaf(-k, x[u].b[e], dn.b[e]);
-                    }
+                for (int u = 0; u < U; ++u) {
+                    const Pairs y = normed<LPR, BWD>(x[u], dy[u], weight, c, s, inv_n, a.eps, dw);
+                    store<T, MODE>(yr, at[u], w, y);
                 }
-                store<T, MODE>(yr, at[u], w, y);
             }
         }
     }
@@ -312,20 +373,38 @@ __global__ __launch_bounds__(64) void weight_sum_kernel(Kernel p) {
 
 int lanes_of(int dim) { return dim <= 32 ? 4 : dim <= 64 ? 8 : dim <= 128 ? 16 : 32; }
 
+// Tokens of few heads go several to a wave where one would leave half of its lanes without a head, of q or of k (196K
+// tokens of 3 + 1 heads of 26: 67 us backward, 625 one by one).
+bool packed(const QkNormArgs& a) {
+    for (int i = 0; i < 2; ++i)   // 32 tokens, and the tables, in 32-bit offsets
+        if (a.heads[i] > 0 && (a.ld_x[i] > 1 << 23 || a.ld_dy[i] > 1 << 23)) return false;
+    if (a.table_rows * a.rot * 2 >= int64_t(kPast)) return false;
+    const int g = 64 / lanes_of(a.dim), most = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1];
+    const int least = a.heads[0] + a.heads[1] - most > 0 ? a.heads[0] + a.heads[1] - most : most;
+    return most <= g && 2 * least <= g;
+}
+
 // A token's heads are split over waves where there are few tokens: some 8192 waves fill the card.
-void plan(Kernel& k, bool bwd) {
+void plan(Kernel& k, bool bwd, bool several) {
     const QkNormArgs& a = k.a;
     const int g = 64 / lanes_of(a.dim);
     for (int i = 0; i < 2; ++i) {
         Split& s = k.s[i];
-        if (a.heads[i] == 0) { s = {0, 1, 1}; continue; }
+        if (a.heads[i] == 0) { s = {0, 1, 1, 0}; continue; }
+        const int64_t most = bwd && (a.dweight[0] || a.dweight[1]) ? kMaxBlocks : 1 << 20;
+        if (several) {
+            s = {0, 1, 1, 0};
+            while (1 << s.head_bits < a.heads[i]) ++s.head_bits;
+            const int64_t each = 2 * (g >> s.head_bits) * kWaves, blocks = (a.tokens + each - 1) / each;
+            s.blocks = static_cast<int>(blocks < most ? blocks : most);
+            continue;
+        }
         const int groups = (a.heads[i] + g - 1) / g;
         int64_t per = a.tokens * groups / 8192;
         per = per < 1 ? 1 : per > groups ? groups : per;
         s.groups = static_cast<int>(per);
         s.splits = (groups + s.groups - 1) / s.groups;
         int64_t blocks = (a.tokens * s.splits + kWaves - 1) / kWaves;
-        const int64_t most = bwd && (a.dweight[0] || a.dweight[1]) ? kMaxBlocks : 1 << 20;
         s.blocks = static_cast<int>(blocks < most ? blocks : most);
     }
 }
@@ -333,8 +412,9 @@ void plan(Kernel& k, bool bwd) {
 template <typename T, int MODE, int LPR>
 hipError_t run(const Kernel& k, bool bwd) {
     const dim3 grid(static_cast<unsigned>(k.s[0].blocks + k.s[1].blocks));
-    if (bwd) hipLaunchKernelGGL((norm_kernel<T, MODE, LPR, true>), grid, dim3(kWaves * 64), 0, k.a.stream, k);
-    else hipLaunchKernelGGL((norm_kernel<T, MODE, LPR, false>), grid, dim3(kWaves * 64), 0, k.a.stream, k);
+    auto start = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kWaves * 64), 0, k.a.stream, k); };
+    if (packed(k.a)) bwd ? start(norm_kernel<T, MODE, LPR, true, true>) : start(norm_kernel<T, MODE, LPR, false, true>);
+    else bwd ? start(norm_kernel<T, MODE, LPR, true, false>) : start(norm_kernel<T, MODE, LPR, false, false>);
     return hipGetLastError();
 }
 
@@ -356,7 +436,7 @@ hipError_t by_mode(const Kernel& k, bool bwd) {
 
 hipError_t launch(const QkNormArgs& a, bool bwd) {
     Kernel k{a, {}};
-    plan(k, bwd);
+    plan(k, bwd, packed(a));
     hipError_t e = a.bf16 ? by_mode<bf16_t>(k, bwd) : by_mode<float>(k, bwd);
     if (e != hipSuccess || !bwd || !(a.dweight[0] || a.dweight[1])) return e;
     hipLaunchKernelGGL(weight_sum_kernel, dim3(2 * a.dim), dim3(64), 0, a.stream, k);
@@ -373,7 +453,7 @@ size_t qk_norm_bwd_workspace_bytes(int64_t tokens, int q_heads, int k_heads, int
     k.a.heads[1] = k_heads;
     float any;
     k.a.dweight[0] = &any;
-    plan(k, true);
+    plan(k, true, false);   // no fewer workgroups than with several tokens a wave
     return (static_cast<size_t>(k.s[0].blocks + k.s[1].blocks) * dim * 4 + 255) / 256 * 256;
 }
 
