@@ -540,7 +540,8 @@ typedef struct {
 } mamba_delta_dims_t;
 
 /* Bytes of device workspace mamba_gated_delta_rule_fwd needs (504 per token
- * and value head in bf16, 600 in float32, in whole chunks of 64 tokens). */
+ * and value head in bf16, 600 in float32, in whole chunks of 64 tokens, and a copy of q and of
+ * k where K is no multiple of 8 or a stride no multiple of 16 bytes). */
 int mamba_gated_delta_rule_workspace_bytes(const mamba_delta_dims_t* dims, size_t* bytes);
 
 /* Forward.
@@ -570,7 +571,7 @@ int mamba_gated_delta_rule_fwd(const mamba_delta_dims_t* dims, const void* q, co
 
 /* Bytes of device workspace mamba_gated_delta_rule_bwd needs: 888 + 4 V (V rounded up
  * to 16) per token and value head, and 4 K V per chunk of 64 for the gradients at the
- * states between chunks (8 K V without `states`). */
+ * states between chunks (8 K V without `states`); copies as in the forward. */
 int mamba_gated_delta_rule_bwd_workspace_bytes(const mamba_delta_dims_t* dims, int32_t have_states, size_t* bytes);
 
 /* Backward: the gradients of sum(dout out) + sum(d_final_state final_state).

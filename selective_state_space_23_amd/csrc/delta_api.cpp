@@ -88,8 +88,21 @@ size_t pairs_bytes(const mamba_delta_dims_t* d, bool backward) {
                     mamba::delta_pairs_bytes(d->dtype == MAMBA_DTYPE_BF16, backward));
 }
 
+// Rows of q and k that are not in whole 16-byte pieces of eight channels are copied to such, with zeros behind.
+// (3 x 18380 tokens, 3 heads of 118 in bf16, states and documents, backward: 2.76 ms, 5.99 read element by element.)
+int pitch_of(const mamba_delta_dims_t* d) { return (d->key_dim + 7) / 8 * 8; }
+bool copied(const mamba_delta_dims_t* d) {
+    const int64_t piece = d->dtype == MAMBA_DTYPE_BF16 ? 8 : 4;
+    return d->key_dim % 8 != 0 || d->ld_q % piece != 0 || d->ld_k % piece != 0;
+}
+size_t copy_bytes(const mamba_delta_dims_t* d) {   // of q or of k
+    return copied(d) ? round256(static_cast<size_t>(d->batch * d->seqlen * d->key_heads) * pitch_of(d) *
+                                (d->dtype == MAMBA_DTYPE_BF16 ? 2 : 4))
+                     : 0;
+}
+
 size_t fwd_workspace(const mamba_delta_dims_t* d) {
-    return d->batch * d->seqlen == 0 ? 0 : record_bytes(d) + solve_bytes(d) + pairs_bytes(d, false);
+    return d->batch * d->seqlen == 0 ? 0 : 2 * copy_bytes(d) + record_bytes(d) + solve_bytes(d) + pairs_bytes(d, false);
 }
 
 size_t state_bytes(const mamba_delta_dims_t* d) {   // of every chunk
@@ -100,7 +113,7 @@ size_t dx_bytes(const mamba_delta_dims_t* d) {   // whole groups of 16 columns
     return static_cast<size_t>(d->batch * d->value_heads * chunks_of(d)) * ((d->value_dim + 15) / 16) * mamba::kGroupFloats * 4;
 }
 size_t bwd_workspace(const mamba_delta_dims_t* d, bool have_states) {
-    return d->batch * d->seqlen == 0 ? 0 : record_bytes(d) + 2 * solve_bytes(d) + pairs_bytes(d, true) +
+    return d->batch * d->seqlen == 0 ? 0 : 2 * copy_bytes(d) + record_bytes(d) + 2 * solve_bytes(d) + pairs_bytes(d, true) +
                                                 dx_bytes(d) + (have_states ? 1 : 2) * state_bytes(d);
 }
 
@@ -109,7 +122,7 @@ mamba::DeltaArgs base_args(const mamba_delta_dims_t* d, const Sizes& s, const vo
                            void* workspace, void* stream) {
     mamba::DeltaArgs a{};
     a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.doc_start = doc_start; a.initial_state = initial_state;
-    a.chunks = static_cast<char*>(workspace);
+    a.chunks = static_cast<char*>(workspace) + 2 * copy_bytes(d);
     a.solve = a.chunks + record_bytes(d);
     a.batch = d->batch; a.seqlen = d->seqlen;
     a.ld_q = s.ld_q; a.ld_k = s.ld_k; a.ld_v = s.ld_v; a.ld_o = s.ld_o;
@@ -119,7 +132,20 @@ mamba::DeltaArgs base_args(const mamba_delta_dims_t* d, const Sizes& s, const vo
     a.bf16 = d->dtype == MAMBA_DTYPE_BF16;
     a.vec_k = pieces(q, s.ld_q, s.esz, d->key_dim) && pieces(k, s.ld_k, s.esz, d->key_dim);
     a.stream = static_cast<hipStream_t>(stream);
+    a.kpitch = d->key_dim;
+    if (copied(d)) {
+        a.kpitch = pitch_of(d);
+        a.q = workspace;
+        a.k = static_cast<char*>(workspace) + copy_bytes(d);
+        a.ld_q = a.ld_k = int64_t(d->key_heads) * a.kpitch;
+        a.vec_k = true;
+    }
     return a;
+}
+
+// The copies of q and k, where the arguments read such.
+hipError_t copy_rows(const mamba::DeltaArgs& a, const mamba_delta_dims_t* d, const Sizes& s, const void* q, const void* k) {
+    return copied(d) ? mamba::launch_delta_pad(a, q, k, s.ld_q, s.ld_k) : hipSuccess;
 }
 
 }  // namespace
@@ -165,7 +191,8 @@ int mamba_gated_delta_rule_fwd(const mamba_delta_dims_t* dims, const void* q, co
     mamba::DeltaArgs a = base_args(dims, s, q, k, v, g, beta, doc_start, initial_state, workspace, stream);
     a.pairs = a.solve + solve_bytes(dims);
     a.out = out; a.final_state = final_state; a.states = states;
-    const hipError_t e = mamba::launch_delta_prepare(a);
+    hipError_t e = copy_rows(a, dims, s, q, k);
+    if (e == hipSuccess) e = mamba::launch_delta_prepare(a);
     return hip_status(e != hipSuccess ? e : mamba::launch_delta_fwd(a));
 }
 
@@ -220,7 +247,8 @@ int mamba_gated_delta_rule_bwd(const mamba_delta_dims_t* dims, const void* q, co
     a.dout = dout; a.d_final_state = d_final_state;
     a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.d_initial_state = d_initial_state;
     a.vec_o = pieces(dout, s.ld_o, s.esz, dims->value_dim) && aligned(a.states, 16);
-    hipError_t e = mamba::launch_delta_prepare(a);
+    hipError_t e = copy_rows(a, dims, s, q, k);
+    if (e == hipSuccess) e = mamba::launch_delta_prepare(a);
     if (e == hipSuccess && !states) e = mamba::launch_delta_fwd(a);   // no output: the states alone
     if (e == hipSuccess) e = mamba::launch_delta_bwd_states(a);
     if (e == hipSuccess) e = mamba::launch_delta_bwd_grads(a);

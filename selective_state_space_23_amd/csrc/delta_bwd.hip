@@ -84,12 +84,12 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
         const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, left = a.seqlen - static_cast<int64_t>(c) * C;
         const int64_t id = bh * n + c;
         const int rows = static_cast<int>(left < C ? left : C);
-        const Rsrc kr = rows_rsrc<ESZ>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k, a.kdim);
-        const Rsrc qr = rows_rsrc<ESZ>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_q, a.kdim);
+        const Rsrc kr = rows_rsrc<ESZ>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kpitch, rows, a.ld_k, a.kpitch);
+        const Rsrc qr = rows_rsrc<ESZ>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kpitch, rows, a.ld_q, a.kpitch);
         const Rsrc tr = rsrc(a.solve_t + id * kSolveBytes, kSolveBytes), pr = rsrc(a.pairs + id * kSolveBytes, kSolveBytes);
         const Rsrc rr = rsrc(a.chunks + id * rec_bytes, sizeof(ChunkRec));
-        kraw.fetch(kr, a.ld_k, a.kdim, tid);
-        qraw.fetch(qr, a.ld_q, a.kdim, tid);
+        kraw.fetch(kr, a.ld_k, a.kpitch, tid);
+        qraw.fetch(qr, a.ld_q, a.kpitch, tid);
 #pragma unroll
         for (int p = 0; p < (BKB + NW - 1) / NW; ++p) {
             const int kb = p * NW + wave;
@@ -544,10 +544,10 @@ __global__ __launch_bounds__(NP * 128, 2) void bwd_pairs_kernel(DeltaArgs a, int
         auto fetch_early = [&](int c) {
             const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, id = bh * n + c;
             const int rows = rows_of(c);
-            const Rsrc kr = rows_rsrc<2>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k, a.kdim);
-            rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(buffer(Kb, TILE, c)), kr, a.ld_k, a.kdim, pair, lane);
-            const Rsrc qr = rows_rsrc<2>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_q, a.kdim);
-            rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(Qb), qr, a.ld_q, a.kdim, pair, lane);
+            const Rsrc kr = rows_rsrc<2>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kpitch, rows, a.ld_k, a.kpitch);
+            rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(buffer(Kb, TILE, c)), kr, a.ld_k, a.kpitch, pair, lane);
+            const Rsrc qr = rows_rsrc<2>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kpitch, rows, a.ld_q, a.kpitch);
+            rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(Qb), qr, a.ld_q, a.kpitch, pair, lane);
             block_to_lds<kBlocks * 3, NP>(buffer(Tb, TRI, c), rsrc(a.solve_t + id * kSolveBytes, kSolveBytes), pair, lane);
         };
         auto fetch_rest = [&](int c) {   // from phase B of the chunk before on

@@ -77,13 +77,13 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
     auto fetch = [&](int c) {
         const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C, id = bh * n + c;
         const int rows = rows_of(c);
-        const Rsrc kr = rows_rsrc<ESZ>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k, a.kdim);
-        const Rsrc qr = rows_rsrc<ESZ>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_q, a.kdim);
+        const Rsrc kr = rows_rsrc<ESZ>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kpitch, rows, a.ld_k, a.kpitch);
+        const Rsrc qr = rows_rsrc<ESZ>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kpitch, rows, a.ld_q, a.kpitch);
         const Rsrc tr = rsrc(a.solve + id * kSolveBytes, kSolveBytes);
         const Rsrc pr = rsrc(a.pairs + (EMIT ? id * pairs_bytes(OUT) : 0), EMIT ? pairs_bytes(OUT) : 0);
         const Rsrc rr = rsrc(a.chunks + id * rec_bytes, sizeof(ChunkRec));
-        kraw.fetch(kr, a.ld_k, a.kdim, tid);
-        if constexpr (EMIT) qraw.fetch(qr, a.ld_q, a.kdim, tid);
+        kraw.fetch(kr, a.ld_k, a.kpitch, tid);
+        if constexpr (EMIT) qraw.fetch(qr, a.ld_q, a.kpitch, tid);
 #pragma unroll
         for (int p = 0; p < (TKB + PKB + RKB + NW - 1) / NW; ++p) {
             const int kb = p * NW + wave;
@@ -553,8 +553,8 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
         uint32_t vraw[16];
         auto fetch_keys = [&](int c) {
             const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C;
-            const Rsrc kr = rows_rsrc<2>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows_of(c), a.ld_k, a.kdim);
-            rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(buffer(Kb, TILE, c)), kr, a.ld_k, a.kdim, pair, lane);
+            const Rsrc kr = rows_rsrc<2>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kpitch, rows_of(c), a.ld_k, a.kpitch);
+            rows_to_lds<KT, NP>(reinterpret_cast<uint16_t*>(buffer(Kb, TILE, c)), kr, a.ld_k, a.kpitch, pair, lane);
         };
         auto fetch_triangle = [&](int c) {
             block_to_lds<kBlocks * 3, NP>(buffer2(Tb, TRI, c), rsrc(a.solve + (bh * n + c) * kSolveBytes, kSolveBytes), pair,
@@ -574,8 +574,8 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
         auto queries = [&](int c) { return reinterpret_cast<uint16_t*>(buffer2(Qb, TILE, c)); };
         auto fetch_queries = [&](int c) {
             const int64_t first = b * a.seqlen + static_cast<int64_t>(c) * C;
-            const Rsrc qr = rows_rsrc<2>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows_of(c), a.ld_q, a.kdim);
-            rows_to_lds<KT, NP>(queries(c), qr, a.ld_q, a.kdim, pair, lane);
+            const Rsrc qr = rows_rsrc<2>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kpitch, rows_of(c), a.ld_q, a.kpitch);
+            rows_to_lds<KT, NP>(queries(c), qr, a.ld_q, a.kpitch, pair, lane);
         };
         auto landed = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
         auto put_values = [&] {

@@ -156,8 +156,8 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
     const int rows = static_cast<int>(left < C ? left : C);
     const int64_t cells = static_cast<int64_t>(a.kdim) * a.vdim;
     const int vsteps = (a.vdim + 31) / 32, vwaves = 2 * vsteps, groups = (a.vdim + 15) / 16;
-    const Rsrc kr = rows_rsrc<ESZ>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k, a.kdim);
-    const Rsrc qr = rows_rsrc<ESZ>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_q, a.kdim);
+    const Rsrc kr = rows_rsrc<ESZ>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kpitch, rows, a.ld_k, a.kpitch);
+    const Rsrc qr = rows_rsrc<ESZ>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kpitch, rows, a.ld_q, a.kpitch);
 
     f32x4 dq[4], dk[4];
 #pragma unroll
@@ -187,7 +187,7 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
             f32x4 S[2 * STEPS];
             {
                 KQ kraw;
-                kraw.fetch(kr, a.ld_k, a.kdim, tid);
+                kraw.fetch(kr, a.ld_k, a.kpitch, tid);
                 Eight<T, VEC> oraw[2];
                 if constexpr (N == 1) {
 #pragma unroll
@@ -456,8 +456,8 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
         {
             const int tid = thread_now();
             KQ kraw, qraw;
-            kraw.fetch(kr, a.ld_k, a.kdim, tid);
-            qraw.fetch(qr, a.ld_q, a.kdim, tid);
+            kraw.fetch(kr, a.ld_k, a.kpitch, tid);
+            qraw.fetch(qr, a.ld_q, a.kpitch, tid);
             kraw.land_without(Kl, tid, sick);
             qraw.land_without(Ql, tid, sick);
         }

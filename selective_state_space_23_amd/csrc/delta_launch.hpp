@@ -42,6 +42,7 @@ struct DeltaArgs {
     char* pairs;                // scale D o Q K^T in the same order (forward), or its transpose (backward); or null
     int64_t batch, seqlen, ld_q, ld_k, ld_v, ld_o;
     int kheads, vheads, kdim, vdim;
+    int kpitch;                 // channels from one head of q and k to the next: kdim, or more with zeros behind
     int nchunks;
     float scale;
     bool bf16;
@@ -72,6 +73,8 @@ size_t delta_chunk_bytes();
 size_t delta_solve_bytes();
 size_t delta_pairs_bytes(bool bf16, bool backward);
 
+// q's and k's heads of a.kdim channels to a.q and a.k, heads of a.kpitch (a multiple of 8) one behind the other, zeros behind.
+hipError_t launch_delta_pad(const DeltaArgs& a, const void* q, const void* k, int64_t ld_q, int64_t ld_k);
 hipError_t launch_delta_prepare(const DeltaArgs& a);
 hipError_t launch_delta_fwd(const DeltaArgs& a);
 hipError_t launch_delta_bwd_states(const DeltaArgs& a);

@@ -47,6 +47,36 @@ __device__ __forceinline__ f32x4 mfma_f32(f32x4 a, f32x4 b, f32x4 c) {   // 16 x
     return c;
 }
 
+struct Pad {
+    const void* from[2];
+    void* to[2];
+    int64_t ld[2];
+    int64_t pieces;
+    int heads, dim, pitch;
+};
+// One thread a piece of eight channels, of q or (second row of workgroups) of k.
+template <typename T>
+__global__ __launch_bounds__(256) void pad_kernel(Pad p) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= p.pieces) return;
+    const T* from = static_cast<const T*>(p.from[blockIdx.y]);
+    T* to = static_cast<T*>(p.to[blockIdx.y]);
+    const int heads = p.heads, dim = p.dim;
+    const int64_t ld = p.ld[blockIdx.y];
+    const int per = p.pitch / 8, piece = static_cast<int>(i % per);
+    const int64_t head = i / per;
+    const T* row = from + head / heads * ld + head % heads * dim;
+    __align__(16) T x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const T y = row[8 * piece + e < dim ? 8 * piece + e : 0];
+        x[e] = 8 * piece + e < dim ? y : T{};
+    }
+#pragma unroll
+    for (int n = 0; n < static_cast<int>(sizeof(x) / 16); ++n)
+        reinterpret_cast<u32x4*>(to + i * 8)[n] = reinterpret_cast<const u32x4*>(x)[n];
+}
+
 template <typename T, int KT, bool VEC, bool BWD>
 __global__ __launch_bounds__(64, 2) void prepare_kernel(DeltaArgs a, size_t rec_bytes) {
     // (given at the launch: where the compiler sees how few workgroups fit, it moves sums to the upper 256 registers and back)
@@ -93,10 +123,10 @@ __global__ __launch_bounds__(64, 2) void prepare_kernel(DeltaArgs a, size_t rec_
 
     // K K^T, lower tiles
     const T* kp = static_cast<const T*>(a.k);
-    const Rsrc kr = rows_rsrc<ESZ>(kp, (b * a.seqlen + t0) * a.ld_k + static_cast<int64_t>(hk) * a.kdim, rows, a.ld_k,
-                                   a.kdim);
-    const Rsrc qr = rows_rsrc<ESZ>(static_cast<const T*>(a.q), (b * a.seqlen + t0) * a.ld_q + static_cast<int64_t>(hk) * a.kdim,
-                                   rows, a.ld_q, a.kdim);
+    const Rsrc kr = rows_rsrc<ESZ>(kp, (b * a.seqlen + t0) * a.ld_k + static_cast<int64_t>(hk) * a.kpitch, rows, a.ld_k,
+                                   a.kpitch);
+    const Rsrc qr = rows_rsrc<ESZ>(static_cast<const T*>(a.q), (b * a.seqlen + t0) * a.ld_q + static_cast<int64_t>(hk) * a.kpitch,
+                                   rows, a.ld_q, a.kpitch);
     f32x4 acc[4][4], qk[4][4];   // rows t of tile i, columns s of tile j <= i
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -109,7 +139,7 @@ __global__ __launch_bounds__(64, 2) void prepare_kernel(DeltaArgs a, size_t rec_
         auto fetch = [&](Eight<T, VEC> (*raw)[4], Rsrc rs, int64_t ld, int j) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                raw[j % AHEAD][i].load(rs, static_cast<uint32_t>((16 * i + m) * static_cast<int>(ld) * ESZ), 32 * j + 8 * g, a.kdim);
+                raw[j % AHEAD][i].load(rs, static_cast<uint32_t>((16 * i + m) * static_cast<int>(ld) * ESZ), 32 * j + 8 * g, a.kpitch);
         };
         if constexpr (AHEAD > 1) {
 #pragma unroll
@@ -314,6 +344,15 @@ hipError_t launch(const DeltaArgs& a, unsigned blocks) {
 }
 
 }  // namespace
+
+hipError_t launch_delta_pad(const DeltaArgs& a, const void* q, const void* k, int64_t ld_q, int64_t ld_k) {
+    const int64_t pieces = a.batch * a.seqlen * a.kheads * (a.kpitch / 8);
+    const Pad p{{q, k}, {const_cast<void*>(a.q), const_cast<void*>(a.k)}, {ld_q, ld_k}, pieces, a.kheads, a.kdim, a.kpitch};
+    const dim3 grid(static_cast<unsigned>((pieces + 255) / 256), 2);
+    if (a.bf16) hipLaunchKernelGGL(pad_kernel<uint16_t>, grid, dim3(256), 0, a.stream, p);
+    else hipLaunchKernelGGL(pad_kernel<uint32_t>, grid, dim3(256), 0, a.stream, p);
+    return hipGetLastError();
+}
 
 hipError_t launch_delta_prepare(const DeltaArgs& a) {
     const unsigned blocks = static_cast<unsigned>(a.batch * a.vheads * a.nchunks);

@@ -249,6 +249,27 @@ def test_backward_of_slices_without_decay(ssm):
         close(got[n], ref[n], n, n in IO, 2.0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K,V", [(128, 24), (64, 17)])
+def test_pointers_between_pieces(ssm, dtype, K, V):
+    """Strides of whole 16-byte pieces with q, k and dout an element behind one: the same results to the bit."""
+    import torch
+
+    d = draw(2, 130, 2, 4, K, V, dtype, 40, True, seed=31)
+    t = dev(d, dtype)
+    moved = dict(t)
+    for n in ("q", "k", "dout"):
+        width = t[n].shape[-2] * t[n].shape[-1]
+        wide = torch.full((2, 130, (width + 16) // 8 * 8), float("nan"), dtype=t[n].dtype, device="cuda")
+        wide[..., 1:1 + width] = t[n].flatten(-2)
+        moved[n] = wide[..., 1:1 + width].unflatten(-1, t[n].shape[-2:])
+    for a, b in zip(forward(ssm, t)[:2], forward(ssm, moved)[:2]):
+        assert torch.equal(a, b)
+    want, got = backward(ssm, t), backward(ssm, moved)
+    for n in want:
+        assert torch.equal(want[n], got[n]), n
+
+
 @pytest.mark.parametrize("K,V", [(128, 100), (48, 40)])
 def test_many_heads(ssm, K, V):
     """Enough rows for wider workgroups: each row as it is alone, to the bit, also where a value is not finite."""
