@@ -901,9 +901,17 @@ def _delta_dims(q, k, v, lead, scale, code, lds=(0, 0, 0, 0)):
     return _lib.DeltaDims(batch, seqlen, Hk, Hv, K, V, *lds, code, K ** -0.5 if scale is None else scale)
 
 
-def gated_delta_rule_workspace_bytes(batch, seqlen, key_heads, value_heads, key_dim, value_dim, dtype="bf16") -> int:
+def _any_strides(batch, seqlen, key_heads, value_heads, key_dim, value_dim, dtype):
+    """mamba_delta_dims_t whose workspaces are large enough for any strides of q and k: odd ones make the library copy them."""
     code = _lib.MAMBA_DTYPE_BF16 if dtype == "bf16" else _lib.MAMBA_DTYPE_F32
-    dims = _lib.DeltaDims(batch, seqlen, key_heads, value_heads, key_dim, value_dim, 0, 0, 0, 0, code, 1.0)
+    width = key_heads * key_dim
+    ld = width | 1 if 0 < width < 2 ** 21 else 0
+    return _lib.DeltaDims(batch, seqlen, key_heads, value_heads, key_dim, value_dim, ld, ld, 0, 0, code, 1.0)
+
+
+def gated_delta_rule_workspace_bytes(batch, seqlen, key_heads, value_heads, key_dim, value_dim, dtype="bf16") -> int:
+    """Bytes of workspace that are enough for gated_delta_rule_fwd, q and k dense or slices of anything."""
+    dims = _any_strides(batch, seqlen, key_heads, value_heads, key_dim, value_dim, dtype)
     n = ctypes.c_size_t(0)
     _lib.check(_lib.load().mamba_gated_delta_rule_workspace_bytes(ctypes.byref(dims), ctypes.byref(n)),
                "mamba_gated_delta_rule_workspace_bytes")
@@ -970,8 +978,8 @@ def gated_delta_rule_fwd(q, k, v, g, beta, doc_start=None, scale=None, initial_s
 
 def gated_delta_rule_bwd_workspace_bytes(batch, seqlen, key_heads, value_heads, key_dim, value_dim, dtype="bf16",
                                          states=False) -> int:
-    code = _lib.MAMBA_DTYPE_BF16 if dtype == "bf16" else _lib.MAMBA_DTYPE_F32
-    dims = _lib.DeltaDims(batch, seqlen, key_heads, value_heads, key_dim, value_dim, 0, 0, 0, 0, code, 1.0)
+    """The same for gated_delta_rule_bwd (``states``: with those that the forward kept)."""
+    dims = _any_strides(batch, seqlen, key_heads, value_heads, key_dim, value_dim, dtype)
     n = ctypes.c_size_t(0)
     _lib.check(_lib.load().mamba_gated_delta_rule_bwd_workspace_bytes(ctypes.byref(dims), int(bool(states)),
                                                                       ctypes.byref(n)),

@@ -21,7 +21,7 @@
 //
 // Bound by memory's latency: 32768 tokens, 24 heads of 128 x 128, 1.68 ms.  A workgroup fills a CU (154 KB of LDS), a head
 // of a chunk takes it 50000 cycles, of which 9000 wait for S, K, dO and the triangle, and what all read (S twice) and write,
-// 3.8 GB, takes 0.75 ms.  (With P formed by every wave and o . dO from O: 2.17 ms and three times the instructions.)
+// 4.7 GB, takes 0.92 ms.  (With P formed by every wave and o . dO from O: 2.17 ms and three times the instructions.)
 #include "delta_rule.hpp"
 
 namespace mamba {

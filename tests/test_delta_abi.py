@@ -173,3 +173,26 @@ def test_binding_heads():
         _heads(whole, "q", cpu, f32, torch.Size((2, 5, 4, 5)))
     with pytest.raises(ValueError, match="must be"):
         at(whole.double())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_workspace_of_any_strides(lib, dtype):
+    """What the binding's helpers say is enough for dense rows and for rows that have to be copied."""
+    import selective_state_space_23_amd as ssm
+
+    shape = (2, 300, 2, 4, 32, 48)
+    for states in (None, False, True):
+        if states is None:
+            enough = ssm.gated_delta_rule_workspace_bytes(*shape, dtype=dtype)
+        else:
+            enough = ssm.gated_delta_rule_bwd_workspace_bytes(*shape, dtype=dtype, states=states)
+        most = 0
+        for ld in (0, 64, 66, 67, 72, 4096):
+            n = ctypes.c_size_t(0)
+            d = dims(dtype=1 if dtype == "bf16" else 0, ld_q=ld, ld_k=ld)
+            if states is None:
+                assert lib.mamba_gated_delta_rule_workspace_bytes(ctypes.byref(d), ctypes.byref(n)) == 0
+            else:
+                assert lib.mamba_gated_delta_rule_bwd_workspace_bytes(ctypes.byref(d), int(states), ctypes.byref(n)) == 0
+            most = max(most, n.value)
+        assert enough == most

@@ -470,3 +470,42 @@ def test_streams_and_graphs(ssm):
         torch.cuda.synchronize()
         assert torch.equal(out, wa[0]) and torch.equal(fin, want) and torch.equal(step_out, want_out)
         forward(ssm, b)
+
+
+def test_backward_on_streams_and_captured(ssm):
+    """Two backward passes under way on streams of their own, and one captured with its forward, replayed between eager work."""
+    import torch
+
+    a = dev(draw(2, 190, 2, 4, 60, 40, "bf16", 50, True, seed=8), "bf16")   # (rows of q and k that are copied)
+    b = dev(draw(1, 260, 1, 2, 128, 64, "f32", None, True, seed=9), "f32")
+    wa, wb = backward(ssm, a), backward(ssm, b)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            ga = backward(ssm, a)
+        with torch.cuda.stream(s2):
+            gb = backward(ssm, b)
+        got.append((ga, gb))
+    torch.cuda.synchronize()
+    for ga, gb in got:
+        assert all(torch.equal(ga[n], wa[n]) for n in wa) and all(torch.equal(gb[n], wb[n]) for n in wb)
+
+    grads = {n: torch.empty_like(x) for n, x in wa.items()}
+    size = max(ssm.gated_delta_rule_bwd_workspace_bytes(2, 190, 2, 4, 60, 40, states=True),
+               ssm.gated_delta_rule_workspace_bytes(2, 190, 2, 4, 60, 40))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    out, fin = torch.empty_like(a["v"]), torch.empty_like(a["initial_state"])
+    kept = {"states": torch.empty(2, 4, 3, 60, 40, device="cuda")}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        forward(ssm, a, out=out, final_state=fin, save=kept, workspace=ws)
+        backward(ssm, a, states=kept["states"], workspace=ws, grads=grads)
+    for _ in range(4):
+        for x in (*grads.values(), ws, out):
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(grads[n], wa[n]) for n in wa)
+        backward(ssm, b)
