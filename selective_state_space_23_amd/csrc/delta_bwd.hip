@@ -8,7 +8,7 @@
 // in its accumulators.  Everything that sums over columns is left to delta_grads.hip,
 // which works off the chunks at once from the states and gradients between them, and from dX as it is stored here.
 //
-// Bound by the chain as the forward is: 32768 tokens, 24 heads of 128 x 128, 512 chunks of 9000 cycles in 1.95 ms (3.27 ms
+// Bound by the chain as the forward is: 2 x 32768 tokens, 12 heads of 128 x 128, 512 chunks of 9000 cycles in 1.95 ms (3.27 ms
 // with one wave for everything).
 //
 // What is not finite makes the whole of its document NaN (through the state a gradient
@@ -303,7 +303,7 @@ __global__ __launch_bounds__(NW * 64, 1) void bwd_states_kernel(DeltaArgs a, int
 // Chunk c:  barrier;  A: the chain forms K dS and dU;   the other forms Z of c, loads P and dO of c - 1;
 //           barrier;  B: the chain forms dX, then dS;   the other forms P^T dO of c - 1, loads K, T and Q of it.
 template <int KT, int NP>
-constexpr int kPairsLds = 3 * C * KT * 2 + 3 * kBlocks * 3072 + 2 * 2048 + NP * (KT / 16 * 1024 + 4096 + 512);
+constexpr int kPairsLds = 3 * C * KT * 2 + 3 * kBlocks * 3 * 1024 + 2 * 2048 + NP * (KT / 16 * 1024 + 4096 + 512);
 // (LDS at the launch and two waves a SIMD: as in the forward, for sums in the lower registers)
 template <int KT, int NP>
 __global__ __launch_bounds__(NP * 128, 2) void bwd_pairs_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {

@@ -289,7 +289,7 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
 // alone issues a vector instruction every 8 cycles, two together twice as many.
 template <int NP> constexpr int kBuffers = NP == 2 ? 2 : 1;   // of T and Q
 template <int KT, int NP, bool EMIT>
-constexpr int kPairsLds = 2 * C * KT * 2 + kBuffers<NP> * kBlocks * 3072 + 2 * 2048 + NP * (2048 + 512) +
+constexpr int kPairsLds = 2 * C * KT * 2 + kBuffers<NP> * kBlocks * 3 * 1024 + 2 * 2048 + NP * (2048 + 512) +
                           (EMIT ? kBuffers<NP> * C * KT * 2 + kBlocks * 2048 + NP * (KT / 32 * 2048 + 4096) : 0);
 // (LDS given at the launch, and two waves a SIMD asked for: one workgroup fills a CU either way, but where the compiler
 // sees that, it takes 512 registers, keeps sums in the upper 256 and moves them, 8 cycles each.)

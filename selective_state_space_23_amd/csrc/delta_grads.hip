@@ -19,7 +19,7 @@
 // What dgamma is made of has three pieces (U, dS, S beside dO, dP): its two dot products cancel.  dX beside S and U, and
 // N, only reach bf16 outputs when the inputs are bf16, and have two.
 //
-// Bound by memory's latency: 32768 tokens, 24 heads of 128 x 128, 1.68 ms.  A workgroup fills a CU (154 KB of LDS), a head
+// Bound by memory's latency: 2 x 32768 tokens, 12 heads of 128 x 128, 1.68 ms.  A workgroup fills a CU (154 KB of LDS), a head
 // of a chunk takes it 50000 cycles, of which 9000 wait for S, K, dO and the triangle, and what all read (S twice) and write,
 // 4.7 GB, takes 0.92 ms.  (With P formed by every wave and o . dO from O: 2.17 ms and three times the instructions.)
 #include "delta_rule.hpp"
