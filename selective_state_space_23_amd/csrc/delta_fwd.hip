@@ -24,7 +24,7 @@ namespace {
 
 using namespace delta;
 
-// float32, and bf16 that is not in whole 16-byte pieces.  (3 x 1001 tokens, 6 heads of 100 x 75 in float32: 141 us.)
+// float32, and bf16 that is not in whole 16-byte pieces.  (3 x 1001 tokens, 6 heads of 100 x 75 in float32: 152 us.)
 template <typename T, int KT, int NW, bool VEC, bool EMIT>
 __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
     constexpr int N = kPieces<T>, ESZ = sizeof(T), STEPS = KT / 32, THREADS = NW * 64;
