@@ -539,8 +539,8 @@ typedef struct {
     float scale;         /* finite (K^-1/2 is usual)                                */
 } mamba_delta_dims_t;
 
-/* Bytes of device workspace mamba_gated_delta_rule_fwd needs (504 per token
- * and value head in bf16, 600 in float32, in whole chunks of 64 tokens, and a copy of q and of
+/* Bytes of device workspace mamba_gated_delta_rule_fwd needs (600 per token
+ * and value head, in whole chunks of 64 tokens, and a copy of q and of
  * k where K is no multiple of 8 or a stride no multiple of 16 bytes). */
 int mamba_gated_delta_rule_workspace_bytes(const mamba_delta_dims_t* dims, size_t* bytes);
 
@@ -560,8 +560,8 @@ int mamba_gated_delta_rule_workspace_bytes(const mamba_delta_dims_t* dims, size_
  * and at most 8,000,000 chunks of 64 tokens over all rows and value heads, else
  * MAMBA_ERR_UNSUPPORTED.  Any alignment to the element size; K and strides of whole
  * 16-byte pieces with 16-byte aligned q and k select the vectorised kernels.
- * Arithmetic and states are float32 (bf16 outputs: sums of products with operands of 16
- * bits and more, rounded once).  L of 0 writes final_state = initial_state (or 0).
+ * Arithmetic and states are float32, outputs are rounded once.  L of 0 writes final_state =
+ * initial_state (or 0).
  * Outputs must not overlap anything else of the call.  Repeated calls give bitwise
  * identical results. */
 int mamba_gated_delta_rule_fwd(const mamba_delta_dims_t* dims, const void* q, const void* k, const void* v,

@@ -79,13 +79,8 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 size_t record_bytes(const mamba_delta_dims_t* d) {
     return round256(static_cast<size_t>(d->batch * d->value_heads * chunks_of(d)) * mamba::delta_chunk_bytes());
 }
-size_t solve_bytes(const mamba_delta_dims_t* d) {
+size_t solve_bytes(const mamba_delta_dims_t* d) {   // of the triangles, of their transposes and of P
     return round256(static_cast<size_t>(d->batch * d->value_heads * chunks_of(d)) * mamba::delta_solve_bytes());
-}
-
-size_t pairs_bytes(const mamba_delta_dims_t* d, bool backward) {
-    return round256(static_cast<size_t>(d->batch * d->value_heads * chunks_of(d)) *
-                    mamba::delta_pairs_bytes(d->dtype == MAMBA_DTYPE_BF16, backward));
 }
 
 // Rows of q and k that are not in whole 16-byte pieces of eight channels are copied to such, with zeros behind.
@@ -102,7 +97,7 @@ size_t copy_bytes(const mamba_delta_dims_t* d) {   // of q or of k
 }
 
 size_t fwd_workspace(const mamba_delta_dims_t* d) {
-    return d->batch * d->seqlen == 0 ? 0 : 2 * copy_bytes(d) + record_bytes(d) + solve_bytes(d) + pairs_bytes(d, false);
+    return d->batch * d->seqlen == 0 ? 0 : 2 * copy_bytes(d) + record_bytes(d) + 2 * solve_bytes(d);
 }
 
 size_t state_bytes(const mamba_delta_dims_t* d) {   // of every chunk
@@ -113,7 +108,7 @@ size_t dx_bytes(const mamba_delta_dims_t* d) {   // whole groups of 16 columns
     return static_cast<size_t>(d->batch * d->value_heads * chunks_of(d)) * ((d->value_dim + 15) / 16) * mamba::kGroupFloats * 4;
 }
 size_t bwd_workspace(const mamba_delta_dims_t* d, bool have_states) {
-    return d->batch * d->seqlen == 0 ? 0 : 2 * copy_bytes(d) + record_bytes(d) + 2 * solve_bytes(d) + pairs_bytes(d, true) +
+    return d->batch * d->seqlen == 0 ? 0 : 2 * copy_bytes(d) + record_bytes(d) + 3 * solve_bytes(d) +
                                                 dx_bytes(d) + (have_states ? 1 : 2) * state_bytes(d);
 }
 
@@ -241,7 +236,7 @@ int mamba_gated_delta_rule_bwd(const mamba_delta_dims_t* dims, const void* q, co
     mamba::DeltaArgs a = base_args(dims, s, q, k, v, g, beta, doc_start, initial_state, workspace, stream);
     a.solve_t = a.solve + solve_bytes(dims);
     a.pairs = a.solve_t + solve_bytes(dims);
-    a.dx = reinterpret_cast<float*>(a.pairs + pairs_bytes(dims, true));
+    a.dx = reinterpret_cast<float*>(a.pairs + solve_bytes(dims));
     a.dstates = a.dx + dx_bytes(dims) / 4;
     a.states = states ? const_cast<float*>(states) : a.dstates + state_bytes(dims) / 4;
     a.dout = dout; a.d_final_state = d_final_state;

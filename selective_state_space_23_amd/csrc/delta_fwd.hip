@@ -11,11 +11,12 @@
 // Without an output the same walk forms the states alone, for the backward.
 //
 // A product of float32 operands, each in three bf16 pieces whose sum it is, takes the six products of pieces that reach
-// 2^-24 of it; a bf16 operand is one piece, and what only reaches a bf16 output has two.
+// 2^-24 of it; a bf16 operand is one piece.
 //
 // Bound by the chain of a row's chunks: 132 matrix products and some 400 vector instructions one behind the other
 // in a wave, with too few rows, heads and groups of columns to fill the card.  64K tokens x 40 heads of
-// 128 x 128: 2.7 ms, 1024 chunks of 6400 cycles; reading and writing it takes 0.5 ms.
+// 128 x 128: 2.95 ms, 1024 chunks of 7000 cycles (2.7 ms where what only reaches an output had two pieces, which is off by
+// 1e-5 of the terms in the outputs of terms that cancel); reading and writing it takes 0.5 ms.
 #include "delta_rule.hpp"
 
 namespace mamba {
@@ -29,8 +30,7 @@ template <typename T, int KT, int NW, bool VEC, bool EMIT>
 __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
     constexpr int N = kPieces<T>, ESZ = sizeof(T), STEPS = KT / 32, THREADS = NW * 64;
     using KQ = Tile<T, KT, THREADS, VEC>;
-    constexpr int OUT = N == 1 ? 2 : 3;      // pieces that reach an output
-    constexpr int TKB = kBlocks * 3, PKB = EMIT ? kBlocks * OUT : 0;
+    constexpr int TKB = kBlocks * 3, PKB = EMIT ? kBlocks * 3 : 0;
     constexpr int RKB = 2;                   // a record's 1304 bytes
     constexpr size_t BUF = (TKB + PKB + RKB) * 1024 + (EMIT ? 2 : 1) * KQ::kBytes;
     __shared__ __align__(16) char buf[BUF];
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
         const Rsrc kr = rows_rsrc<ESZ>(a.k, first * a.ld_k + static_cast<int64_t>(hk) * a.kpitch, rows, a.ld_k, a.kpitch);
         const Rsrc qr = rows_rsrc<ESZ>(a.q, first * a.ld_q + static_cast<int64_t>(hk) * a.kpitch, rows, a.ld_q, a.kpitch);
         const Rsrc tr = rsrc(a.solve + id * kSolveBytes, kSolveBytes);
-        const Rsrc pr = rsrc(a.pairs + (EMIT ? id * pairs_bytes(OUT) : 0), EMIT ? pairs_bytes(OUT) : 0);
+        const Rsrc pr = rsrc(a.pairs + (EMIT ? id * kSolveBytes : 0), EMIT ? kSolveBytes : 0);
         const Rsrc rr = rsrc(a.chunks + id * rec_bytes, sizeof(ChunkRec));
         kraw.fetch(kr, a.ld_k, a.kpitch, tid);
         if constexpr (EMIT) qraw.fetch(qr, a.ld_q, a.kpitch, tid);
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
     fetch(0);
     for (int c = 0; c < n; ++c) {
         const u32x4* Tl = reinterpret_cast<const u32x4*>(buf);                     // [kBlocks][3][64]
-        const u32x4* Pl = Tl + TKB * 64;                                           // [kBlocks][OUT][64]
+        const u32x4* Pl = Tl + TKB * 64;                                           // [kBlocks][3][64]
         const ChunkRec* rec = reinterpret_cast<const ChunkRec*>(buf + (TKB + PKB) * 1024);
         uint16_t* Kl = reinterpret_cast<uint16_t*>(buf + (TKB + PKB + RKB) * 1024);   // [N][C][KT]
         uint16_t* Ql = Kl + N * C * KT;
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
                 if constexpr (EMIT) qf[i] = rows_frag<N, KT>(Ql, 16 * i + m, 4 * j + g);
             }
             products<3, 4>(ks, kf, sf);
-            if constexpr (EMIT) products<OUT, 4>(qs, qf, sf);
+            if constexpr (EMIT) products<3, 4>(qs, qf, sf);
         }
 
         // R
@@ -199,11 +199,11 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
         // O
         if constexpr (EMIT) {
             f32x4 O[4];
-            Frag<OUT> pf[4];
+            Frag<3> pf[4];
             auto pairs = [&](int i, int j) {
-                Frag<OUT> f;
+                Frag<3> f;
 #pragma unroll
-                for (int p = 0; p < OUT; ++p) f.p[p] = Pl[(low_block(i, j) * OUT + p) * 64 + lane];
+                for (int p = 0; p < 3; ++p) f.p[p] = Pl[(low_block(i, j) * 3 + p) * 64 + lane];
                 return f;
             };
 #pragma unroll
@@ -214,10 +214,10 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
                 for (int r = 0; r < 4; ++r)
                     O[i][r] = keep_if(16 * i + 4 * g + r < first_start, a.scale * into[r] * qs[i][r]);
             }
-            products<OUT, 4>(O, pf, split_out<OUT>(U[0], U[1]));
+            products<3, 4>(O, pf, split(U[0], U[1]));
 #pragma unroll
             for (int i = 2; i < 4; ++i) pf[i] = pairs(i, 1);
-            products<OUT, 2>(O + 2, pf + 2, split_out<OUT>(U[2], U[3]));
+            products<3, 2>(O + 2, pf + 2, split(U[2], U[3]));
             if (any_lost) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -290,13 +290,13 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
 template <int NP> constexpr int kBuffers = NP == 2 ? 2 : 1;   // of T and Q
 template <int KT, int NP, bool EMIT>
 constexpr int kPairsLds = 2 * C * KT * 2 + kBuffers<NP> * kBlocks * 3 * 1024 + 2 * 2048 + NP * (2048 + 512) +
-                          (EMIT ? kBuffers<NP> * C * KT * 2 + kBlocks * 2048 + NP * (KT / 32 * 2048 + 4096) : 0);
+                          (EMIT ? kBuffers<NP> * C * KT * 2 + kBlocks * 3072 + NP * (KT / 32 * 2048 + 4096) : 0);
 // (LDS given at the launch, and two waves a SIMD asked for: one workgroup fills a CU either way, but where the compiler
 // sees that, it takes 512 registers, keeps sums in the upper 256 and moves them, 8 cycles each.)
 template <int KT, int NP, bool EMIT, bool SAVE>
 __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
     constexpr int STEPS = KT / 32;
-    constexpr int TILE = C * KT * 2, TRI = kBlocks * 3 * 1024, PAIRS = kBlocks * 2 * 1024, REC = 2048;
+    constexpr int TILE = C * KT * 2, TRI = kBlocks * 3 * 1024, REC = 2048;
     constexpr int BUFFERS = kBuffers<NP>;
     extern __shared__ __align__(16) char smem[];
     char* const Kb = smem;                       // [2] K
@@ -306,10 +306,10 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
     char* const Lb = Vb + NP * 64 * 32;          // a lane's lost rows
     char* const Qb = Lb + NP * 64 * 8;           // [BUFFERS] Q
     char* const Pb = Qb + BUFFERS * TILE;                // P
-    char* const Sb = Pb + PAIRS;                 // S's first two pieces, as operands
+    char* const Sb = Pb + TRI;                   // S
     char* const Ub = Sb + NP * STEPS * 2048;     // U
     static_assert(kPairsLds<KT, NP, EMIT> == 2 * (TILE + REC) + BUFFERS * TRI + NP * (64 * 32 + 64 * 8) +
-                                                 (EMIT ? BUFFERS * TILE + PAIRS + NP * (STEPS * 2048 + 4096) : 0));
+                                                 (EMIT ? BUFFERS * TILE + TRI + NP * (STEPS * 2048 + 4096) : 0));
 
     const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), pair = wave & (NP - 1);
@@ -382,9 +382,9 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
                 for (int i = 0; i < 4; ++i) kf[i] = rows_frag<1, KT>(Kl, 16 * i + m, 4 * j + g);
                 products<3, 4>(R, kf, sf[j]);
                 if constexpr (EMIT) {
-                    u32x4* to = reinterpret_cast<u32x4*>(Sb + (pair * STEPS + j) * 2048) + lane;
-                    to[0] = sf[j].p[0];
-                    to[64] = sf[j].p[1];
+                    f32x4* to = reinterpret_cast<f32x4*>(Sb + (pair * STEPS + j) * 2048) + lane;
+                    to[0] = S[2 * j];
+                    to[64] = S[2 * j + 1];
                 }
             }
             const uint64_t starts = uniform(starts_), bad = uniform(bad_);
@@ -599,11 +599,11 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
             const int first_start = starts ? __builtin_ctzll(starts) : C;
             const u32x4* Pl = reinterpret_cast<const u32x4*>(Pb);
             const f32x4* Ul = reinterpret_cast<const f32x4*>(Ub + pair * 4096);
-            Frag<2> pf[4];
+            Frag<3> pf[4];
             auto pairs = [&](int i, int j) {
-                Frag<2> f;
+                Frag<3> f;
 #pragma unroll
-                for (int p = 0; p < 2; ++p) f.p[p] = Pl[(low_block(i, j) * 2 + p) * 64 + lane];
+                for (int p = 0; p < 3; ++p) f.p[p] = Pl[(low_block(i, j) * 3 + p) * 64 + lane];
                 return f;
             };
 #pragma unroll
@@ -614,10 +614,10 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
                 for (int r = 0; r < 4; ++r)
                     O[i][r] = keep_if(16 * i + 4 * g + r < first_start, a.scale * into[r] * O[i][r]);
             }
-            products<2, 4>(O, pf, split_rounded(Ul[lane], Ul[64 + lane]));
+            products<3, 4>(O, pf, split(Ul[lane], Ul[64 + lane]));
 #pragma unroll
             for (int i = 2; i < 4; ++i) pf[i] = pairs(i, 1);
-            products<2, 2>(O + 2, pf + 2, split_rounded(Ul[128 + lane], Ul[192 + lane]));
+            products<3, 2>(O + 2, pf + 2, split(Ul[128 + lane], Ul[192 + lane]));
             const uint64_t lost = *reinterpret_cast<const uint64_t*>(Lb + (pair * 64 + lane) * 8);
             if (__ballot(lost != 0) != 0) {
 #pragma unroll
@@ -650,18 +650,18 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
             if (c + 1 < n) fetch_values(c + 1);
             if constexpr (EMIT) {
                 if (BUFFERS == 2 && c + 1 < n) fetch_queries(c + 1);
-                block_to_lds<kBlocks * 2, NP>(Pb, rsrc(a.pairs + (bh * n + c) * pairs_bytes(2), pairs_bytes(2)), pair, lane);
+                block_to_lds<kBlocks * 3, NP>(Pb, rsrc(a.pairs + (bh * n + c) * kSolveBytes, kSolveBytes), pair, lane);
                 const uint16_t* Ql = queries(c);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) O[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int j = 0; j < STEPS; ++j) {
-                    const u32x4* from = reinterpret_cast<const u32x4*>(Sb + (pair * STEPS + j) * 2048) + lane;
-                    const Frag<2> sf = {{from[0], from[64]}};
+                    const f32x4* from = reinterpret_cast<const f32x4*>(Sb + (pair * STEPS + j) * 2048) + lane;
+                    const Frag<3> sf = split(from[0], from[64]);
                     Frag<1> qf[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) qf[i] = rows_frag<1, KT>(Ql, 16 * i + m, 4 * j + g);
-                    products<2, 4>(O, qf, sf);
+                    products<3, 4>(O, qf, sf);
                 }
             }
             if constexpr (BUFFERS == 1) {

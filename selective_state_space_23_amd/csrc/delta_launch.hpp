@@ -71,7 +71,6 @@ struct DeltaUpdateArgs {
 // Bytes of each workspace part for one (row, value head, chunk).
 size_t delta_chunk_bytes();
 size_t delta_solve_bytes();
-size_t delta_pairs_bytes(bool bf16, bool backward);
 
 // q's and k's heads of a.kdim channels to a.q and a.k, heads of a.kpitch (a multiple of 8) one behind the other, zeros behind.
 hipError_t launch_delta_pad(const DeltaArgs& a, const void* q, const void* k, int64_t ld_q, int64_t ld_k);

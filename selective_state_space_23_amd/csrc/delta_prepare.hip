@@ -30,9 +30,6 @@ namespace mamba {
 
 size_t delta_chunk_bytes() { return (sizeof(delta::ChunkRec) + 255) / 256 * 256; }
 size_t delta_solve_bytes() { return static_cast<size_t>(delta::kSolveBytes); }
-size_t delta_pairs_bytes(bool bf16, bool backward) {
-    return static_cast<size_t>(delta::pairs_bytes(bf16 && !backward ? 2 : 3));
-}
 
 namespace {
 
@@ -201,10 +198,9 @@ __global__ __launch_bounds__(64, 2) void prepare_kernel(DeltaArgs a, size_t rec_
     }
     __syncthreads();
 
-    // The lower tiles in As, out in N pieces in the order of an operand: rows (or, transposed, columns) in lanes
-    auto emit = [&](char* to, auto pieces, bool transposed) {
-        constexpr int P = decltype(pieces)::value;
-        u32x4* out = reinterpret_cast<u32x4*>(to + id * pairs_bytes(P));
+    // The lower tiles in As, out in pieces in the order of an operand: rows (or, transposed, columns) in lanes
+    auto emit = [&](char* to, bool transposed) {
+        u32x4* out = reinterpret_cast<u32x4*>(to + id * kSolveBytes);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -221,10 +217,10 @@ __global__ __launch_bounds__(64, 2) void prepare_kernel(DeltaArgs a, size_t rec_
                     x = four(As + (16 * i + m) * kRowA + 32 * j + 4 * g);
                     y = four(As + (16 * i + m) * kRowA + 32 * j + 16 + 4 * g);
                 }
-                const Frag<P> f = split_out<P>(x, y);
+                const Frag<3> f = split(x, y);
                 const int blk = transposed ? high_block(i, j) : low_block(i, j);
 #pragma unroll
-                for (int n = 0; n < P; ++n) out[(blk * P + n) * 64 + lane] = f.p[n];
+                for (int n = 0; n < 3; ++n) out[(blk * 3 + n) * 64 + lane] = f.p[n];
             }
         __syncthreads();
     };
@@ -245,8 +241,7 @@ __global__ __launch_bounds__(64, 2) void prepare_kernel(DeltaArgs a, size_t rec_
             }
         }
         __syncthreads();
-        if constexpr (BWD) emit(a.pairs, std::integral_constant<int, 3>{}, true);
-        else emit(a.pairs, std::integral_constant<int, N == 1 ? 2 : 3>{}, false);
+        emit(a.pairs, BWD);
     }
 
 #pragma unroll
@@ -328,7 +323,7 @@ __global__ __launch_bounds__(64, 2) void prepare_kernel(DeltaArgs a, size_t rec_
                 }
             }
         __syncthreads();
-        emit(which ? a.solve_t : a.solve, std::integral_constant<int, 3>{}, which != 0);
+        emit(which ? a.solve_t : a.solve, which != 0);
     }
 }
 

@@ -8,8 +8,7 @@
 // they reach 2^-24 of the product: 3 products where one operand is bf16 as stored, 6
 // where both are float32.  That is float32 arithmetic at 1/3 to 1/6 of the bf16 rate (the fp32
 // instructions have 1/16), and states, solved triangles and float32 gradients need it:
-// they carry over thousands of tokens.  Products that only feed a bf16 output
-// take two pieces (2^-16).
+// they carry over thousands of tokens.
 //
 // Layout.  With lane l = 16 g + m of a wave, an accumulator tile holds row 4 g + r
 // (r = 0..3), column m; an operand of 32 contracted values holds row (column) m and eight of them in
@@ -28,8 +27,7 @@ constexpr int C = kDeltaChunk;
 constexpr int kTiles = C / 16;            // token tiles of a chunk
 constexpr int kBlocks = 6;                // 16 x 32 pieces of a 64 x 64 triangle that are not all zero
 constexpr uint32_t kPast = 0x7fffff00u;   // a byte offset behind any buffer
-constexpr int64_t kSolveBytes = kBlocks * 3 * 1024;   // a chunk's solved triangle in three pieces
-constexpr int64_t pairs_bytes(int pieces) { return kBlocks * pieces * 1024; }
+constexpr int64_t kSolveBytes = kBlocks * 3 * 1024;   // a chunk's solved triangle, or P, in three pieces
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -135,30 +133,6 @@ __device__ __forceinline__ Frag<3> split(f32x4 a, f32x4 b) {
         f.p[2][i] = l;
     }
     return f;
-}
-
-// Eight floats in two rounded pieces: what is left out is below 2^-17 of a value, of either
-// sign, and the product of two second pieces (left out too) below 2^-16.  (The first two cut
-// pieces leave out remainders of one sign: sums of 64 terms that cancel were off by 2e-4.)
-__device__ __forceinline__ Frag<2> split_rounded(f32x4 a, f32x4 b) {
-    Frag<2> f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const f32x4 x = i < 2 ? a : b;
-        float x0 = x[2 * (i & 1)], x1 = x[2 * (i & 1) + 1];
-        const uint32_t h = pack_bf16x2(x0, x1);
-        without_pieces(h, x0, x1);
-        f.p[0][i] = h;
-        f.p[1][i] = pack_bf16x2(x0, x1);
-    }
-    return f;
-}
-
-// Eight floats of an operand that only reaches an output: two pieces, or all three.
-template <int N>
-__device__ __forceinline__ Frag<N> split_out(f32x4 a, f32x4 b) {
-    if constexpr (N == 2) return split_rounded(a, b);
-    else return split(a, b);
 }
 
 // The rows of one chunk of one tensor as a buffer: reads behind the last token

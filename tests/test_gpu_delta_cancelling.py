@@ -1,0 +1,82 @@
+"""Gated delta rule in bf16 where terms cancel: what is left shows with how many bits the float32 operands of a
+product were held, which the rounding of the output hides elsewhere."""
+
+import numpy as np
+import pytest
+
+import oracle.delta_rule as R
+from workloads import bf16_round
+from workloads.device import to_dev, to_host
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ssm():
+    import torch
+
+    import selective_state_space_23_amd as s
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU")
+    return s
+
+
+def up(x):
+    import torch
+
+    return None if x is None else torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).cuda()
+
+
+# K, V, rows: narrow and wide keys, two and four groups of columns to a workgroup
+SIZES = [(16, 24, 1), (128, 64, 2), (64, 128, 65), (128, 128, 65)]
+
+
+@pytest.mark.parametrize("K,V,rows", SIZES)
+def test_entering_state_in_the_outputs(ssm, K, V, rows):
+    """Each query reads two channels whose rows of the state, which no token changes, cancel but for 1e-4.  The products
+    with q's ones are exact, their sum is right to 2^-24 of the terms and scale exp(gamma) to 2^-22 of what is left: 2^-23 of
+    the terms, and 2^-8 of the result as it is rounded.  An operand cut to 16 bits is off by up to 2^-15 of a term."""
+    g = np.random.default_rng(K + V)
+    L = 70
+    S = g.standard_normal((rows, 4, K, V)).astype(np.float32)
+    S[:, :, 1::2] = -S[:, :, ::2] * (1 + 1e-4 * g.standard_normal(S[:, :, ::2].shape).astype(np.float32))
+    q = np.zeros((rows, L, 4, K), np.float32)
+    pick = g.integers(0, K // 2, (rows, L, 4))[..., None] * 2
+    np.put_along_axis(q, pick, 1.0, -1)
+    np.put_along_axis(q, pick + 1, 1.0, -1)
+    k = np.roll(q, 1, 1)
+    v = bf16_round(g.standard_normal((rows, L, 4, V)).astype(np.float32))
+    beta = np.zeros((rows, L, 4), np.float32)
+    out, _ = ssm.gated_delta_rule_fwd(*(to_dev(x, "bf16") for x in (q, k, v)), None, up(beta), initial_state=up(S), scale=0.5)
+    ref = 0.5 * np.einsum("blhk,bhkv->blhv", q.astype(np.float64), S.astype(np.float64))
+    terms = 0.5 * np.einsum("blhk,bhkv->blhv", q, np.abs(S))
+    assert (np.abs(to_host(out) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -22 * terms).all()
+
+
+@pytest.mark.parametrize("K,V,rows", SIZES)
+def test_tokens_of_the_chunk_in_the_outputs(ssm, K, V, rows):
+    """Keys along the axes, so u = beta v; values in pairs that are each other's negative, whose shares at the later
+    token's end differ by 1e-4; each query reads one pair.  The decays between tokens, products of the kernel's own, are
+    right to 2^-21 (their logarithm, below 2, to 2^-23, and the exponential to 2^-22), u to 2^-23: 2^-20 of the terms with
+    their sum."""
+    g = np.random.default_rng(K + V + 1)
+    L = min(K, 64)
+    k = np.zeros((rows, L, 4, K), np.float32)
+    k[:, np.arange(L), :, np.arange(L)] = 1.0
+    gate = -0.02 * g.random((rows, L, 4)).astype(np.float32)
+    beta = (0.5 + 0.5 * g.random((rows, L, 4))).astype(np.float32)
+    beta[:, 1::2] = beta[:, ::2] * np.exp(gate[:, 1::2]) * (1 + 1e-4 * g.standard_normal((rows, L // 2, 4)))
+    v = bf16_round(g.standard_normal((rows, L, 4, V)).astype(np.float32))
+    v[:, 1::2] = -v[:, ::2]
+    q = np.zeros_like(k)
+    for t in range(1, L):
+        at = 2 * g.integers(0, (t + 1) // 2, (rows, 4))[..., None]
+        np.put_along_axis(q[:, t], at, 1.0, -1)
+        np.put_along_axis(q[:, t], at + 1, 1.0, -1)
+    out, _ = ssm.gated_delta_rule_fwd(*(to_dev(x, "bf16") for x in (q, k, v)), up(gate), up(beta), scale=0.7)
+    few = min(rows, 3)
+    args = [x[:few] for x in (q, k, v, gate, beta)]
+    scale = float(np.float32(0.7))
+    ref = R.gated_delta_rule(*args, scale=scale)[0]
+    terms = R.gated_delta_rule(args[0], args[1], np.abs(args[2]), *args[3:], scale=scale)[0]
+    assert (np.abs(to_host(out)[:few] - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -20 * terms).all()
