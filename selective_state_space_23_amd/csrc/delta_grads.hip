@@ -15,12 +15,11 @@
 //
 // Phases: (1) a wave owns 16 value columns, with K and the triangle in LDS; (2) the tiles of
 // dP and N, contracted over the columns, with U and dX in LDS over K; (3) a wave owns 16 key
-// channels: the products with S and dS; (4) those with K and Q, in LDS over U and dX.
-// What dgamma is made of has three pieces (U, dS, S beside dO, dP): its two dot products cancel.  dX beside S and U, and
-// N, only reach bf16 outputs when the inputs are bf16, and have two.
+// channels: the products with S and dS; (4) those with K and Q, in LDS over U and dX.  dP and N lie in LDS as floats, cut
+// into pieces where they are read: as pieces they leave no room for dO.
 //
-// Bound by memory's latency: 2 x 32768 tokens, 12 heads of 128 x 128, 1.68 ms.  A workgroup fills a CU (154 KB of LDS), a head
-// of a chunk takes it 50000 cycles, of which 9000 wait for S, K, dO and the triangle, and what all read (S twice) and write,
+// Bound by memory's latency: 2 x 32768 tokens, 12 heads of 128 x 128, 1.78 ms.  A workgroup fills a CU (157 KB of LDS), a head
+// of a chunk takes it 53000 cycles, of which 9000 wait for S, K, dO and the triangle, and what all read (S twice) and write,
 // 4.7 GB, takes 0.92 ms.  (With P formed by every wave and o . dO from O: 2.17 ms and three times the instructions.)
 #include "delta_rule.hpp"
 
@@ -31,7 +30,7 @@ namespace {
 using namespace delta;
 
 constexpr int kWaves = 8, kThreads = kWaves * 64;
-constexpr int kRowV = 136, kRowP = 72;   // bf16 of a row of U and dX, of dP and N
+constexpr int kRowV = 136, kRowP = 68;   // bf16 of a row of U and dX, floats of one of dP and N
 
 template <int CTRL>
 __device__ __forceinline__ float moved(float x) {
@@ -64,44 +63,31 @@ __device__ __forceinline__ float wave_sum(float x) {
     return x + __shfl_xor(x, 32);
 }
 
-// One value in N pieces, to element `at` of N planes of `plane` elements.
-template <int N>
+// One value in three pieces, to element `at` of planes of `plane` elements.
 __device__ __forceinline__ void put(uint16_t* to, int plane, int at, float x) {
-    if constexpr (N == 2) {
-        const uint32_t h = f32_to_bf16(x);
-        to[at] = static_cast<uint16_t>(h);
-        to[plane + at] = f32_to_bf16(x - __uint_as_float(h << 16));
-    } else {
-        const uint32_t u = __float_as_uint(x);
-        const float r = x - __uint_as_float(u & 0xffff0000u);
-        const uint32_t w = __float_as_uint(r);
-        to[at] = static_cast<uint16_t>(u >> 16);
-        to[plane + at] = static_cast<uint16_t>(w >> 16);
-        to[2 * plane + at] = static_cast<uint16_t>(__float_as_uint(r - __uint_as_float(w & 0xffff0000u)) >> 16);
-    }
+    const uint32_t u = __float_as_uint(x);
+    const float r = x - __uint_as_float(u & 0xffff0000u);
+    const uint32_t w = __float_as_uint(r);
+    to[at] = static_cast<uint16_t>(u >> 16);
+    to[plane + at] = static_cast<uint16_t>(w >> 16);
+    to[2 * plane + at] = static_cast<uint16_t>(__float_as_uint(r - __uint_as_float(w & 0xffff0000u)) >> 16);
 }
 
-// Row `row` of planes [N][C][kRowP], the tokens of step j in the order of cols_frag.
-template <int N>
-__device__ __forceinline__ Frag<N> token_frag(const uint16_t* lds, int row, int j, int g) {
-    Frag<N> f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const uint16_t* at = lds + (i * C + row) * kRowP + 32 * j + 4 * g;
-        const u32x2 x = *reinterpret_cast<const u32x2*>(at), y = *reinterpret_cast<const u32x2*>(at + 16);
-        f.p[i] = u32x4{x[0], x[1], y[0], y[1]};
-    }
-    return f;
+// Row `row` of [C][kRowP], the tokens of step j in the order of cols_frag ...
+__device__ __forceinline__ Frag<3> token_frag(const float* lds, int row, int j, int g) {
+    const float* at = lds + row * kRowP + 32 * j + 4 * g;
+    return split(four(at), four(at + 16));
 }
-
-// The same of column m, by transposing reads.
-template <int N>
-__device__ __forceinline__ Frag<N> token_cols(const uint16_t* lds, int j, int g, int m, int ch4) {
-    Frag<N> f;
+// ... and column `col`.
+__device__ __forceinline__ Frag<3> token_cols(const float* lds, int col, int j, int g) {
+    const float* at = lds + (32 * j + 4 * g) * kRowP + col;
+    f32x4 x, y;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        f.p[i] = transposed(lds + (i * C + 32 * j + 4 * g + m / 4) * kRowP + ch4, 16 * kRowP);
-    return f;
+    for (int e = 0; e < 4; ++e) {
+        x[e] = at[e * kRowP];
+        y[e] = at[(16 + e) * kRowP];
+    }
+    return split(x, y);
 }
 // Row `row` of planes [N][C][kRowV], eight columns from `ch` on.
 template <int N>
@@ -124,12 +110,11 @@ constexpr size_t larger(size_t a, size_t b) { return a > b ? a : b; }
 template <typename T, int KT, bool VEC>
 __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t rec_bytes) {
     constexpr int N = kPieces<T>, ESZ = sizeof(T), STEPS = KT / 32;
-    constexpr int OUT = N == 1 ? 2 : 3;
     using KQ = Tile<T, KT, kThreads, VEC>;
-    constexpr int PLANE_V = C * kRowV, PLANE_P = C * kRowP;
+    constexpr int PLANE_V = C * kRowV;
     constexpr size_t PARTS = 2 * kWaves * C * 4;
-    constexpr size_t ZERO = larger(2 * KQ::kBytes, size_t(3 + OUT) * PLANE_V * 2);
-    constexpr size_t ONE = larger(kSolveBytes + PARTS, size_t(3 + OUT) * PLANE_P * 2);
+    constexpr size_t ZERO = larger(2 * KQ::kBytes, size_t(6) * PLANE_V * 2);
+    constexpr size_t ONE = larger(kSolveBytes + PARTS, size_t(2) * C * kRowP * 4);
     __shared__ __align__(16) char region0[ZERO];
     __shared__ __align__(16) char region1[ONE];
     __shared__ __align__(16) uint16_t dout_[N == 1 ? PLANE_V : 8];   // dO [C][kRowV], where there is room for it
@@ -140,11 +125,11 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
     uint16_t* Kl = reinterpret_cast<uint16_t*>(region0);
     uint16_t* Ql = Kl + N * C * KT;
     uint16_t* Ul = reinterpret_cast<uint16_t*>(region0);          // [3][C][kRowV]
-    uint16_t* Xl = Ul + 3 * PLANE_V;                              // [OUT] ...
+    uint16_t* Xl = Ul + 3 * PLANE_V;                              // the same
     const u32x4* Tl = reinterpret_cast<const u32x4*>(region1);
     float* parts = reinterpret_cast<float*>(region1 + kSolveBytes);   // [2][kWaves][C]
-    uint16_t* Pl = reinterpret_cast<uint16_t*>(region1);          // [3][C][kRowP]
-    uint16_t* Nl = Pl + 3 * PLANE_P;                              // [OUT] ...
+    float* Pl = reinterpret_cast<float*>(region1);                // [C][kRowP]
+    float* Nl = Pl + C * kRowP;
     const ChunkRec* rec = &rec_;
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -342,8 +327,8 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int at = (16 * i + 4 * g + r) * kRowV + v;
-                    put<3>(Ul, PLANE_V, at, U[i][r]);
-                    put<OUT>(Xl, PLANE_V, at, X[i][r]);
+                    put(Ul, PLANE_V, at, U[i][r]);
+                    put(Xl, PLANE_V, at, X[i][r]);
                 }
         }
         __syncthreads();
@@ -373,11 +358,11 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
             f32x4 P = {0, 0, 0, 0}, G = {0, 0, 0, 0};
             for (int j = 0; j < vsteps; ++j) {
                 const Frag<3> uf = plane_frag<3>(Ul, 16 * is + m, 32 * j + 8 * g);
-                const Frag<OUT> xf = plane_frag<OUT>(Xl, 16 * it + m, 32 * j + 8 * g);
+                const Frag<3> xf = plane_frag<3>(Xl, 16 * it + m, 32 * j + 8 * g);
                 const Frag<N> of = dout_frag(it, j);
                 __builtin_amdgcn_sched_barrier(0);
                 product<3>(P, of, uf);
-                product<OUT>(G, xf, uf);
+                product<3>(G, xf, uf);
             }
             const int s = 16 * is + m, stop = doc_end(starts, s);
             const float sh = rec->hi[s], sl = rec->lo[s];
@@ -386,12 +371,12 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                 const int t = 16 * it + 4 * g + r;
                 const float d = exp2_fast((rec->hi[t] - sh) + (rec->lo[t] - sl));
                 const bool on = t >= s && t < stop;
-                put<3>(Pl, PLANE_P, t * kRowP + s, keep_if(on, a.scale * d * P[r]));
+                Pl[t * kRowP + s] = keep_if(on, a.scale * d * P[r]);
                 const float n = keep_if(on && t > s, -rec->beta[t] * d * G[r]);
                 const int pad = t * kRowP + C;   // for the lanes above the diagonal
-                put<OUT>(Nl, PLANE_P, t >= s ? t * kRowP + s : pad, n);
-                put<OUT>(Nl, PLANE_P, t > s ? s * kRowP + t : pad, n);
-                if (it == is + 1 && (is & 1) == 0) put<3>(Pl, PLANE_P, s * kRowP + t, 0.0f);   // read with the tile beside it
+                Nl[t >= s ? t * kRowP + s : pad] = n;
+                Nl[t > s ? s * kRowP + t : pad] = n;
+                if (it == is + 1 && (is & 1) == 0) Pl[s * kRowP + t] = 0.0f;   // read with the tile beside it
             }
         }
 
@@ -417,11 +402,11 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                     Frag<N> of[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) of[i] = dout_frag(i, j);
-                    Frag<OUT> xf[4];
+                    Frag<3> xf[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) xf[i] = plane_frag<OUT>(Xl, 16 * i + m, 32 * j + 8 * g);
+                    for (int i = 0; i < 4; ++i) xf[i] = plane_frag<3>(Xl, 16 * i + m, 32 * j + 8 * g);
                     products<3, 4>(dqh, of, sf);
-                    products<OUT, 4>(xs, xf, sf);
+                    products<3, 4>(xs, xf, sf);
                     __builtin_amdgcn_sched_barrier(0);
                     Frag<3> uf[4];
 #pragma unroll
@@ -431,7 +416,7 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         product<3>(dqh[i], dout_frag(i, j), sf);
-                        product<OUT>(xs[i], plane_frag<OUT>(Xl, 16 * i + m, 32 * j + 8 * g), sf);
+                        product<3>(xs[i], plane_frag<3>(Xl, 16 * i + m, 32 * j + 8 * g), sf);
                         product<3>(W[i], plane_frag<3>(Ul, 16 * i + m, 32 * j + 8 * g), df);
                     }
                 }
@@ -495,29 +480,29 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                                    cols_frag<N, KT>(Ql, 1, g, m, 16 * wave + 4 * (m % 4))};
             Frag<3> pf[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) pf[i] = token_frag<3>(Pl, 16 * i + m, 0, g);
+            for (int i = 0; i < 4; ++i) pf[i] = token_frag(Pl, 16 * i + m, 0, g);
             __builtin_amdgcn_sched_barrier(0);
             products<3, 4>(dqh, pf, kf[0]);
 #pragma unroll
-            for (int i = 2; i < 4; ++i) pf[i] = token_frag<3>(Pl, 16 * i + m, 1, g);
+            for (int i = 2; i < 4; ++i) pf[i] = token_frag(Pl, 16 * i + m, 1, g);
             __builtin_amdgcn_sched_barrier(0);
             products<3, 2>(dqh + 2, pf + 2, kf[1]);
-            Frag<OUT> nf[4];
+            Frag<3> nf[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) nf[i] = token_frag<OUT>(Nl, 16 * i + m, j, g);
+                for (int i = 0; i < 4; ++i) nf[i] = token_frag(Nl, 16 * i + m, j, g);
                 __builtin_amdgcn_sched_barrier(0);
-                products<OUT, 4>(dk, nf, kf[j]);
+                products<3, 4>(dk, nf, kf[j]);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) nf[i] = token_cols<OUT>(Pl, 1, g, m, 16 * i + 4 * (m % 4));
+            for (int i = 0; i < 4; ++i) nf[i] = token_cols(Pl, 16 * i + m, 1, g);
             __builtin_amdgcn_sched_barrier(0);
-            products<OUT, 4>(dk, nf, qf[1]);
+            products<3, 4>(dk, nf, qf[1]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) nf[i] = token_cols<OUT>(Pl, 0, g, m, 16 * i + 4 * (m % 4));
+            for (int i = 0; i < 2; ++i) nf[i] = token_cols(Pl, 16 * i + m, 0, g);
             __builtin_amdgcn_sched_barrier(0);
-            products<OUT, 2>(dk, nf, qf[0]);
+            products<3, 2>(dk, nf, qf[0]);
             __builtin_amdgcn_sched_barrier(0);
             float qv[16];
             values(qv, Ql);

@@ -80,3 +80,30 @@ def test_tokens_of_the_chunk_in_the_outputs(ssm, K, V, rows):
     ref = R.gated_delta_rule(*args, scale=scale)[0]
     terms = R.gated_delta_rule(args[0], args[1], np.abs(args[2]), *args[3:], scale=scale)[0]
     assert (np.abs(to_host(out)[:few] - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -20 * terms).all()
+
+
+@pytest.mark.parametrize("K,rows", [(16, 1), (64, 3), (128, 2)])
+def test_keys_gradient_of_columns_that_cancel(ssm, K, rows):
+    """Two columns of state and values alike but for 1e-4, with gradients that are each other's negative: what both give to dk
+    cancels.  Every sum of dk's is as a readout and a correction of up to 128 + 64 terms each (3.3e-6 of what they are without
+    cancelling): 2^-17 together, and 2^-8 of the result as it is rounded.  An operand cut to 16 bits is off by up to
+    2^-15 of a term, and the largest of thousands are several times the rms."""
+    g = np.random.default_rng(K)
+    L, V = 8, 16
+    unit = lambda x: bf16_round((x / np.linalg.norm(x, axis=-1, keepdims=True)).astype(np.float32))  # noqa: E731
+    q, k = (unit(g.standard_normal((rows, L, 2, K))) for _ in range(2))
+    v = bf16_round(g.standard_normal((rows, L, 4, V)).astype(np.float32))
+    v[..., 1::2] = v[..., ::2]
+    S = g.standard_normal((rows, 4, K, V)).astype(np.float32)
+    S[..., 1::2] = S[..., ::2] * (1 + 1e-4 * g.standard_normal(S[..., ::2].shape).astype(np.float32))
+    gate = -0.1 * g.random((rows, L, 4)).astype(np.float32)
+    beta = (0.5 + 0.5 * g.random((rows, L, 4))).astype(np.float32)
+    dout = np.zeros_like(v)
+    dout[..., 6] = bf16_round(g.standard_normal((rows, L, 4)).astype(np.float32))
+    alone = R.gated_delta_rule_bwd(q, k, v, gate, beta, dout, initial_state=S)["dk"]
+    dout[..., 7] = -dout[..., 6]
+    ref = R.gated_delta_rule_bwd(q, k, v, gate, beta, dout, initial_state=S)["dk"]
+    got = ssm.gated_delta_rule_bwd(*(to_dev(x, "bf16") for x in (q, k, v)), up(gate), up(beta), to_dev(dout, "bf16"),
+                                   initial_state=up(S))["dk"]
+    assert np.sqrt(np.mean(ref ** 2)) < 1e-3 * np.sqrt(np.mean(alone ** 2))
+    assert (np.abs(to_host(got) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -17 * np.sqrt(np.mean(alone ** 2))).all()
