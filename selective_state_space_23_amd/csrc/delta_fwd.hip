@@ -11,7 +11,7 @@
 // Without an output the same walk forms the states alone, for the backward.
 //
 // A product of float32 operands, each in three bf16 pieces whose sum it is, takes the six products of pieces that reach
-// 2^-24 of it; a bf16 operand is one piece.
+// 2^-22 of it; a bf16 operand is one piece.
 //
 // Bound by the chain of a row's chunks: 132 matrix products and some 400 vector instructions one behind the other
 // in a wave, with too few rows, heads and groups of columns to fill the card.  64K tokens x 40 heads of

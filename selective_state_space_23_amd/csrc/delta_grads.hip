@@ -67,10 +67,10 @@ __device__ __forceinline__ float wave_sum(float x) {
 __device__ __forceinline__ void put(uint16_t* to, int plane, int at, float x) {
     const uint32_t u = __float_as_uint(x);
     const float r = x - __uint_as_float(u & 0xffff0000u);
-    const uint32_t w = __float_as_uint(r);
+    const uint32_t mid = f32_to_bf16(r);
     to[at] = static_cast<uint16_t>(u >> 16);
-    to[plane + at] = static_cast<uint16_t>(w >> 16);
-    to[2 * plane + at] = static_cast<uint16_t>(__float_as_uint(r - __uint_as_float(w & 0xffff0000u)) >> 16);
+    to[plane + at] = static_cast<uint16_t>(mid);
+    to[2 * plane + at] = static_cast<uint16_t>(__float_as_uint(r - __uint_as_float(mid << 16)) >> 16);
 }
 
 // Row `row` of [C][kRowP], the tokens of step j in the order of cols_frag ...

@@ -3,12 +3,13 @@
 //
 // Precision.  Every product of the chunked form runs on
 // v_mfma_f32_16x16x32_bf16 with float32 accumulators.  A float32 operand is cut
-// into three bf16 pieces of 8 bits each, x = hi + mid + lo exactly (cut by masking, so the
-// remainders are exact); the pieces of two operands are multiplied as far as
-// they reach 2^-24 of the product: 3 products where one operand is bf16 as stored, 6
-// where both are float32.  That is float32 arithmetic at 1/3 to 1/6 of the bf16 rate (the fp32
-// instructions have 1/16), and states, solved triangles and float32 gradients need it:
-// they carry over thousands of tokens.
+// into three bf16 pieces of 8 bits each, x = hi + mid + lo exactly (hi by masking, which no finite
+// value overflows, mid rounded, so lo is of either sign and at most 2^-16 of x, hi's remainder below 2^-7); the
+// pieces of two operands are multiplied as far as they reach 2^-22 of the product: 3 products, and nothing left out,
+// where one operand is bf16 as stored, 6 where both are float32, with mid lo, lo mid and lo lo left out, below 2^-22
+// of the product at their largest and of either sign (2^-21 and of the product's own sign with mid cut too).  That is
+// float32 arithmetic at 1/3 to 1/6 of the bf16 rate (the fp32 instructions have 1/16), and states, solved triangles
+// and float32 gradients need it: they carry over thousands of tokens.
 //
 // Layout.  With lane l = 16 g + m of a wave, an accumulator tile holds row 4 g + r
 // (r = 0..3), column m; an operand of 32 contracted values holds row (column) m and eight of them in
@@ -111,11 +112,11 @@ inline bool wide_groups(const DeltaArgs& a) {
     return a.vdim > 32 && a.batch * a.vheads * ((a.vdim + 31) / 32) > 256;
 }
 
-// The bf16 pieces of pairs of floats, cut off: the highest 8 significant bits, the next and the last.
+// The bf16 pieces of pairs of floats: the highest 8 significant bits, the rest rounded to as many, and what is left.
 __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
     hi = __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302u);
     without_pieces(hi, x0, x1);
-    mid = __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302u);
+    mid = pack_bf16x2(x0, x1);
     without_pieces(mid, x0, x1);
     lo = __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302u);
 }

@@ -1,5 +1,5 @@
-"""Gated delta rule in bf16 where terms cancel: what is left shows with how many bits the float32 operands of a
-product were held, which the rounding of the output hides elsewhere."""
+"""Gated delta rule where terms cancel or are single: what is left shows with how many bits the float32 operands of a
+product were held, which roundings and sums hide elsewhere."""
 
 import numpy as np
 import pytest
@@ -107,3 +107,19 @@ def test_keys_gradient_of_columns_that_cancel(ssm, K, rows):
                                    initial_state=up(S))["dk"]
     assert np.sqrt(np.mean(ref ** 2)) < 1e-3 * np.sqrt(np.mean(alone ** 2))
     assert (np.abs(to_host(got) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -17 * np.sqrt(np.mean(alone ** 2))).all()
+
+
+@pytest.mark.parametrize("K,V", [(16, 16), (128, 64)])
+def test_single_products(ssm, K, V):
+    """One token's state in float32 is k v^T.  A product leaves out no more than 2^-22 of itself, of either sign, and is
+    summed from pieces with its largest last: 2^-23 more if that sum is cut.  Values as unkind to pieces as can be are
+    among them (those of 1 + 2^-7 - 2^-23: pieces cut throughout leave out 2^-21)."""
+    g = np.random.default_rng(K)
+    near = 1 + 2.0 ** -7 - 2.0 ** -23 * np.arange(1, 9)
+    k = (g.choice(near, (2, 1, 3, K)) * 2.0 ** g.integers(-6, 1, (2, 1, 3, K))).astype(np.float32)
+    v = (g.choice(near, (2, 1, 3, V)) * 2.0 ** g.integers(-6, 7, (2, 1, 3, V))).astype(np.float32)
+    v[1] = g.standard_normal(v[1].shape)
+    k[1] = g.standard_normal(k[1].shape)
+    S = ssm.gated_delta_rule_fwd(up(k), up(k), up(v), None, up(np.ones((2, 1, 3))))[1]
+    ref = np.einsum("bhk,bhv->bhkv", k[:, 0].astype(np.float64), v[:, 0].astype(np.float64))
+    assert (np.abs(to_host(S) - ref) <= (2.0 ** -22 + 2.0 ** -23) * np.abs(ref)).all()
