@@ -179,17 +179,18 @@ struct Kernel {
     Split s[2];
 };
 
-// One head's pairs: normed and rotated, or (BWD) their gradients from dy, with the weight's into dw.
+// One head's pairs: normed and rotated, or (BWD) their gradients from dy, with the weight's into dw.  A lane whose place
+// `at` lies behind the tensor has no head: its root of 0 + eps, infinite with eps = 0, is taken out by its bits.
 template <int LPR, bool BWD>
-__device__ __forceinline__ Pairs normed(const Pairs& x, const Pairs& dy, const Pairs& weight, f32x4 c, f32x4 s, float inv_n,
-                                        float eps, Pairs& dw) {
+__device__ __forceinline__ Pairs normed(uint32_t at, const Pairs& x, const Pairs& dy, const Pairs& weight, f32x4 c, f32x4 s,
+                                        float inv_n, float eps, Pairs& dw) {
     float sq = 0.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         sq = __builtin_fmaf(x.a[e], x.a[e], sq);
         sq = __builtin_fmaf(x.b[e], x.b[e], sq);
     }
-    const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(head_sum<LPR>(sq), inv_n, eps));
+    float r = __builtin_amdgcn_rsqf(__builtin_fmaf(head_sum<LPR>(sq), inv_n, eps));
     Pairs y;
     if constexpr (!BWD) {
 #pragma unroll
@@ -199,6 +200,7 @@ __device__ __forceinline__ Pairs normed(const Pairs& x, const Pairs& dy, const P
             y.b[e] = __builtin_fmaf(nb, c[e], na * s[e]);
         }
     } else {
+        r = __uint_as_float(__float_as_uint(r) & (at < kPast ? ~0u : 0u));
         float dot = 0.0f;
         Pairs dn;
 #pragma unroll
@@ -286,7 +288,7 @@ __global__ __launch_bounds__(kWaves * 64) void norm_kernel(Kernel p) {
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const Pairs y = normed<LPR, BWD>(x[u], dy[u], weight, c[u], s[u], inv_n, a.eps, dw);
+                const Pairs y = normed<LPR, BWD>(at[u], x[u], dy[u], weight, c[u], s[u], inv_n, a.eps, dw);
                 store<T, MODE>(yr, at[u], w, y);
             }
         }
@@ -326,7 +328,7 @@ __global__ __launch_bounds__(kWaves * 64) void norm_kernel(Kernel p) {
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const Pairs y = normed<LPR, BWD>(x[u], dy[u], weight, c, s, inv_n, a.eps, dw);
+                    const Pairs y = normed<LPR, BWD>(at[u], x[u], dy[u], weight, c, s, inv_n, a.eps, dw);
                     store<T, MODE>(yr, at[u], w, y);
                 }
             }

@@ -262,3 +262,31 @@ def test_layer(ssm):
         got = to_host(got)
         err = np.abs(got - ref)
         assert (err <= 2.0 ** -6 * np.abs(ref) + 2.0 ** -5 * np.sqrt(np.mean(ref ** 2))).all(), (what, err.max())
+
+
+@pytest.mark.parametrize("case", [
+    (2, 37, 12, 5, 128, 64, "bf16", "l2", "qk", False),     # groups of four heads, two under way: one without heads
+    (1, 19, 17, 9, 40, 0, "f32", "rms", "qk", False),
+    (3, 70, 5, 5, 99, 50, "f32", "rms", "qk", True),
+    (1, 301, 3, 1, 26, 12, "f32", "rms", "qk", False),      # several tokens to a wave, with spare places and a ragged end
+    (2, 23, 1, 1, 128, 128, "bf16", "l2", "qk", True),
+    (1, 5, 3, 0, 16, 16, "f32", "l2", "q", False),
+], ids=lambda c: "-".join(map(str, c)))
+def test_without_eps(ssm, case):
+    """eps = 0 and heads that are not zero: as with any eps, wherever the heads do not fill the waves."""
+    d, how = draw(case, seed=11)
+    how["eps"] = 0.0
+    t = dev(d, case[6])
+    outs, grads = fwd(ssm, t, how), bwd(ssm, t, how)
+    for i, n in enumerate("qk"):
+        if d[n] is None:
+            continue
+        kw = dict(weight=d[n + "w"], cos=d["cos"], sin=d["sin"], positions=d["pos"], **how)
+        ref = R.head_norm(d[n], **kw)
+        close(outs[i], ref, case[6], n, 2.0 ** -20 * np.abs(ref).max(-1, keepdims=True))
+        dx, dw = R.head_norm_bwd(d[n], d["d" + n], **kw)
+        x = d[n].astype(np.float64)
+        r = ((x * x).sum(-1, keepdims=True) / (x.shape[-1] if how["norm"] == "rms" else 1)) ** -0.5
+        close(grads["d" + n], dx, case[6], "d" + n, 2.0 ** -18 * 3 * (r * np.abs(d["d" + n]).max(-1, keepdims=True)))
+        parts = (np.abs(d["d" + n]).max(-1, keepdims=True) * np.abs(x) * r * 2).sum((0, 1, 2))
+        close(grads[f"d{n}_weight"], dw, "f32", f"d{n}_weight", 2.0 ** -18 * parts)
