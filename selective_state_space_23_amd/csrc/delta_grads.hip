@@ -11,7 +11,8 @@
 // row's decay scales o . dO and v . dV by what it scales the row's query and value side, so the 64 x 64
 // matrices' row and column sums cancel to these two dot products; and o . dO = q . dq, as o is linear in q.  At the chunk's
 // end <dS, S_out> = exp(gamma_C) <dS, S> + sum_t k . W is added, and dg is the
-// sum of dgamma from its token to its document's (or the chunk's) end.
+// sum of dgamma from its token to its document's (or the chunk's) end.  A decay that counts as 0 ends that sum as
+// a document start does, and has 0 itself: the sum across it is 0, of which rounding would leave something.
 //
 // Phases: (1) a wave owns 16 value columns, with K and the triangle in LDS; (2) the tiles of
 // dP and N, contracted over the columns, with U and dX in LDS over K; (3) a wave owns 16 key
@@ -526,17 +527,18 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                 turn += turns[w][lane];
                 end += ends[w];
             }
-            const int stop = doc_end(starts, lane);
+            const uint64_t walls = uniform(rec->walls);
+            const int stop = doc_end(walls, lane), last_wall = walls ? 63 - __builtin_clzll(walls) : 0;
 #pragma unroll
             for (int s = 1; s < 64; s *= 2) {
                 const double other = __shfl_down(turn, s);
                 turn += lane + s < stop ? other : 0.0;
             }
-            if (lane >= last_start) turn += end;
-            const bool nan = (sick >> lane) & 1, start = (starts >> lane) & 1;
+            if (lane >= last_wall) turn += end;
+            const bool nan = (sick >> lane) & 1, wall = (walls >> lane) & 1;
             const Rsrc gr = rows_rsrc<4>(a.dg, a.dg ? first * a.vheads + hv : 0, a.dg ? rows : 0, a.vheads, 1);
             store_one<float>(gr, static_cast<uint32_t>(lane * a.vheads * 4),
-                             nan_if(nan, keep_if(!start, static_cast<float>(turn))));
+                             nan_if(nan, keep_if(!wall, static_cast<float>(turn))));
         }
     }
 

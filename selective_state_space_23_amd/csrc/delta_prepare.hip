@@ -101,6 +101,7 @@ __global__ __launch_bounds__(64, 2) void prepare_kernel(DeltaArgs a, size_t rec_
     float gate = in && a.g != nullptr ? a.g[tok * a.vheads + hv] : 0.0f;
     float beta = in ? a.beta[tok * a.vheads + hv] : 0.0f;
     if (start) gate = 0.0f;
+    const uint64_t walls = starts | __ballot(gate < -200.0f);
     if (gate < -200.0f) gate = -200.0f;
     const bool bad_gate = not_finite(gate), bad_beta = not_finite(beta);
     if (bad_gate) gate = 0.0f;
@@ -194,6 +195,7 @@ __global__ __launch_bounds__(64, 2) void prepare_kernel(DeltaArgs a, size_t rec_
         rec->keep = last_seg == 0 ? exp2_fast(h) * __builtin_fmaf(l, kLn2, 1.0f) : 0.0f;
         rec->pad = 0;
         rec->starts = starts;
+        rec->walls = walls;
         rec->bad = bad;
     }
     __syncthreads();

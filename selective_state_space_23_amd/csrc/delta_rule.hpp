@@ -52,6 +52,7 @@ struct ChunkRec {
     float keep;           // the entering state's part of the leaving one (0 with a start inside)
     uint32_t pad;
     uint64_t starts;      // bit t: token t starts a document
+    uint64_t walls;       // bit t: it does, or its decay counts as 0: nothing reaches it from before
     uint64_t bad;         // bit t: a key, gate or decay of token t or before it in its document is not finite
 };
 

@@ -509,3 +509,27 @@ def test_backward_on_streams_and_captured(ssm):
         torch.cuda.synchronize()
         assert all(torch.equal(grads[n], wa[n]) for n in wa)
         backward(ssm, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rate", [3.0, 150.0, 400.0])
+def test_gradients_of_decays_of_any_size(ssm, rate, dtype):
+    """A log decay below -200 counts as 0 and has gradient 0, exactly; dg elsewhere, and all else, as ever: its terms' rms
+    sets the scale of dg.  What the decays leave of the state's gradient may lie below float32's normal numbers (2^-126),
+    which an output in float32 cannot be nearer than."""
+    d = draw(2, 190, 1, 2, 40, 24, dtype, 60, True, seed=10, rate=rate)
+    d["g"][0, 70] = -np.inf
+    d["g"][1, 63:65] = -200.5
+    d["g"][1, 127] = -1e30
+    got = backward(ssm, dev(d, dtype))
+    ref = R.gated_delta_rule_bwd(**{n: d[n] for n in FWD}, dout=d["dout"], d_final_state=d["d_final_state"])
+    out = R.gated_delta_rule(**{n: d[n] for n in FWD})[0]
+    terms = np.abs(d["dout"] * out).sum(-1) + np.abs(ref["dv"] * d["v"]).sum(-1)
+    dg = to_host(got["dg"])
+    assert (dg[d["g"] < -200] == 0).all()
+    assert (np.abs(dg - ref["dg"]) <= 1e-4 * (np.sqrt(np.mean(ref["dg"] ** 2)) + np.sqrt(np.mean(terms ** 2)))).all()
+    for n in ref:
+        if n != "dg" and np.sqrt(np.mean(ref[n] ** 2)) > 2.0 ** -100:
+            close(got[n], ref[n], n, n in IO and dtype == "bf16", 2.0)
+        elif n != "dg":
+            assert (np.abs(to_host(got[n]) - ref[n]) <= 2.0 ** -100).all()
