@@ -585,8 +585,9 @@ int mamba_gated_delta_rule_bwd_workspace_bytes(const mamba_delta_dims_t* dims, i
  *   d_initial_state (B, Hv, K, V) float32 or NULL; requires initial_state.
  *   workspace  at least mamba_gated_delta_rule_bwd_workspace_bytes, 256-byte aligned.
  * A decay below exp(-200) counts as 0 and has gradient 0.  A NaN or an infinity in a document makes
- * gradients of that document NaN, and of no other.  L of 0 writes d_initial_state =
- * d_final_state (or 0).  Repeated calls give bitwise identical results. */
+ * the gradients of all its tokens NaN (of the value heads that it belongs to, and dq and dk of their
+ * key head), and of no other document's; d_initial_state is NaN where the definition makes it so.
+ * L of 0 writes d_initial_state = d_final_state (or 0).  Repeated calls give bitwise identical results. */
 int mamba_gated_delta_rule_bwd(const mamba_delta_dims_t* dims, const void* q, const void* k, const void* v,
                                const float* g, const float* beta, const uint8_t* doc_start,
                                const float* initial_state, const float* states, const void* dout,

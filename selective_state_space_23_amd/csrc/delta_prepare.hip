@@ -197,6 +197,7 @@ __global__ __launch_bounds__(64, 2) void prepare_kernel(DeltaArgs a, size_t rec_
         rec->starts = starts;
         rec->walls = walls;
         rec->bad = bad;
+        rec->sick = 0;
     }
     __syncthreads();
 

@@ -54,6 +54,7 @@ struct ChunkRec {
     uint64_t starts;      // bit t: token t starts a document
     uint64_t walls;       // bit t: it does, or its decay counts as 0: nothing reaches it from before
     uint64_t bad;         // bit t: a key, gate or decay of token t or before it in its document is not finite
+    uint64_t sick;        // (backward) bit t: something in token t's document, as far as the chunk holds it, is not finite
 };
 
 __device__ __forceinline__ Rsrc rsrc(const void* p, int64_t bytes) {

@@ -533,3 +533,46 @@ def test_gradients_of_decays_of_any_size(ssm, rate, dtype):
             close(got[n], ref[n], n, n in IO and dtype == "bf16", 2.0)
         elif n != "dg":
             assert (np.abs(to_host(got[n]) - ref[n]) <= 2.0 ** -100).all()
+
+
+@pytest.mark.parametrize("where", ["q", "k", "v", "g", "beta", "dout", "initial_state", "d_final_state"])
+@pytest.mark.parametrize("dtype,L,starts", [
+    ("bf16", 400, [30, 395]),            # a document over seven chunks
+    ("f32", 330, [64, 128, 300]),        # documents that start where chunks do
+    ("bf16", 4500, [17, 4400]),          # more chunks than a wave has lanes
+    ("f32", 200, []),                    # one document, which the states before and behind belong to
+])
+def test_backward_not_finite_over_chunks(ssm, where, dtype, L, starts):
+    """Wherever the chunks end: every gradient of the document's tokens is NaN, those of other documents, of other rows
+    and of the other key head are what they are without it, to the bit.  (A decay that is not finite leaves the sums of
+    the chunk's other decays, which differences are taken of, shifted: rounded otherwise, within test_backward's bound.)"""
+    import torch
+
+    d = draw(2, L, 2, 4, 32, 24, dtype, seed=17, carry=True)
+    d["doc_start"] = np.zeros((2, L), np.uint8)
+    d["doc_start"][:, starts] = 1
+    ends = sorted({0, *starts, L})
+    want = backward(ssm, dev(d, dtype))
+    for at in (0 if where == "initial_state" else L - 1 if where == "d_final_state" else (ends[0] + ends[1]) // 2,
+               L - 1 if where == "d_final_state" else 0 if where == "initial_state" else (ends[-2] + ends[-1]) // 2,
+               *(() if "state" in where else (min(L, 4500) // 2 - 1,))):
+        first, last = max(e for e in ends if e <= at), min(e for e in ends if e > at)
+        bad = {n: None if x is None else x.copy() for n, x in d.items()}
+        if "state" in where:
+            bad[where][0, 1, 3, 5] = np.nan          # value head 1, of key head 0
+        else:
+            h = 0 if where in ("q", "k") else 1
+            bad[where][(0, at, h) if where in ("g", "beta") else (0, at, h, 3)] = np.inf
+        got = backward(ssm, dev(bad, dtype))
+        hurt = slice(0, 2) if where in ("q", "k") else slice(1, 2)     # value heads that it belongs to
+        for n in ("dq", "dk", "dv", "dg", "dbeta"):
+            place = (0, slice(first, last), slice(0, 1) if n in ("dq", "dk") else hurt)
+            assert torch.isnan(got[n][place]).all(), (n, at)
+            got[n][place] = want[n][place]
+            if where != "g":
+                assert torch.equal(got[n], want[n]), (n, at)
+                continue
+            rest, ref = got[n].double(), want[n].double()
+            bf16 = n in IO and dtype == "bf16"
+            tol = (2.0 ** -7 if bf16 else 0.0) * ref.abs() + (4e-4 if bf16 else 1e-4) * (ref ** 2).mean().sqrt()
+            assert ((rest - ref).abs() <= tol).all(), (n, at)
