@@ -557,8 +557,9 @@ int mamba_gated_delta_rule_workspace_bytes(const mamba_delta_dims_t* dims, size_
  *              the backward.
  *   workspace  at least mamba_gated_delta_rule_workspace_bytes bytes, 256-byte aligned.
  * Supported: K and V up to 128, Hk K, Hv V and strides up to 2^21, L up to 3,000,000
- * and at most 8,000,000 chunks of 64 tokens over all rows and value heads, else
- * MAMBA_ERR_UNSUPPORTED.  Any alignment to the element size; K and strides of whole
+ * and at most 8,000,000 chunks of 64 tokens over all rows and value heads; in bf16 with
+ * V > 64 fewer than 4,194,297 rows times value heads; and where q and k are copied fewer than
+ * 2^32 - 255 pieces of 8 channels of either; else MAMBA_ERR_UNSUPPORTED.  Any alignment to the element size; K and strides of whole
  * 16-byte pieces with 16-byte aligned q and k select the vectorised kernels.
  * Arithmetic and states are float32, outputs are rounded once.  L of 0 writes final_state =
  * initial_state (or 0).

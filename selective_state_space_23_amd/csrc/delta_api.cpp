@@ -96,6 +96,19 @@ size_t copy_bytes(const mamba_delta_dims_t* d) {   // of q or of k
                      : 0;
 }
 
+// What the passes over a sequence take: check_dims, and launches of fewer than 2^32 threads.  (The other kernels stay below
+// that for as many chunks as check_dims takes.)
+int check_sequence(const mamba_delta_dims_t* d) {
+    const int st = check_dims(d);
+    if (st != MAMBA_OK) return st;
+    constexpr int64_t kThreads = int64_t(1) << 32;
+    // bf16: 512 threads for 64 columns of a row and head, heads in eights
+    const int64_t groups = (d->batch * d->value_heads + 7) / 8 * 8 * ((d->value_dim + 63) / 64);
+    if (d->dtype == MAMBA_DTYPE_BF16 && groups * 512 >= kThreads) return MAMBA_ERR_UNSUPPORTED;
+    if (copied(d) && d->batch * d->seqlen * d->key_heads * (pitch_of(d) / 8) > kThreads - 256) return MAMBA_ERR_UNSUPPORTED;
+    return MAMBA_OK;
+}
+
 size_t fwd_workspace(const mamba_delta_dims_t* d) {
     return d->batch * d->seqlen == 0 ? 0 : 2 * copy_bytes(d) + record_bytes(d) + 2 * solve_bytes(d);
 }
@@ -150,7 +163,7 @@ extern "C" {
 int mamba_gated_delta_rule_workspace_bytes(const mamba_delta_dims_t* dims, size_t* bytes) {
     if (!bytes) return MAMBA_ERR_INVALID_ARGUMENT;
     *bytes = 0;
-    const int st = check_dims(dims);
+    const int st = check_sequence(dims);
     if (st != MAMBA_OK) return st;
     *bytes = fwd_workspace(dims);
     return MAMBA_OK;
@@ -160,7 +173,7 @@ int mamba_gated_delta_rule_fwd(const mamba_delta_dims_t* dims, const void* q, co
                                const float* g, const float* beta, const uint8_t* doc_start,
                                const float* initial_state, void* out, float* final_state, float* states,
                                void* workspace, size_t workspace_bytes, void* stream) {
-    const int st = check_dims(dims);
+    const int st = check_sequence(dims);
     if (st != MAMBA_OK) return st;
     const float* f32s[] = {g, beta, initial_state, final_state, states};
     for (const float* p : f32s)
@@ -194,7 +207,7 @@ int mamba_gated_delta_rule_fwd(const mamba_delta_dims_t* dims, const void* q, co
 int mamba_gated_delta_rule_bwd_workspace_bytes(const mamba_delta_dims_t* dims, int32_t have_states, size_t* bytes) {
     if (!bytes) return MAMBA_ERR_INVALID_ARGUMENT;
     *bytes = 0;
-    const int st = check_dims(dims);
+    const int st = check_sequence(dims);
     if (st != MAMBA_OK) return st;
     *bytes = bwd_workspace(dims, have_states != 0);
     return MAMBA_OK;
@@ -205,7 +218,7 @@ int mamba_gated_delta_rule_bwd(const mamba_delta_dims_t* dims, const void* q, co
                                const float* initial_state, const float* states, const void* dout,
                                const float* d_final_state, void* dq, void* dk, void* dv, float* dg, float* dbeta,
                                float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream) {
-    const int st = check_dims(dims);
+    const int st = check_sequence(dims);
     if (st != MAMBA_OK) return st;
     const float* f32s[] = {g, beta, initial_state, states, d_final_state, dg, dbeta, d_initial_state};
     for (const float* p : f32s)

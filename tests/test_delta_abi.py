@@ -196,3 +196,27 @@ def test_workspace_of_any_strides(lib, dtype):
                 assert lib.mamba_gated_delta_rule_bwd_workspace_bytes(ctypes.byref(d), int(states), ctypes.byref(n)) == 0
             most = max(most, n.value)
         assert enough == most
+
+
+@pytest.mark.parametrize("kw,too_many", [
+    (dict(batch=65535, seqlen=64, key_heads=65, value_heads=65, value_dim=128), True),
+    (dict(batch=65535, seqlen=1, key_heads=1, value_heads=65, value_dim=65), True),
+    (dict(batch=65535, seqlen=64, key_heads=64, value_heads=64, value_dim=128), False),
+    (dict(batch=65535, seqlen=64, key_heads=65, value_heads=65, value_dim=128, dtype=0), False),
+    (dict(batch=65535, seqlen=64, key_heads=122, value_heads=122, value_dim=64), False),
+    (dict(batch=1024, seqlen=262145, key_heads=1, value_heads=1, key_dim=127), True),
+    (dict(batch=1024, seqlen=262145, key_heads=1, value_heads=1, key_dim=127, dtype=0), True),
+    (dict(batch=1024, seqlen=262144, key_heads=1, value_heads=1, key_dim=127), True),
+    (dict(batch=1024, seqlen=262143, key_heads=1, value_heads=1, key_dim=127), False),
+    (dict(batch=1024, seqlen=262145, key_heads=1, value_heads=1, key_dim=128), False),
+], ids=lambda v: str(v))
+def test_launches_of_2_32_threads(lib, kw, too_many):
+    """Refused before anything is launched; the step's launches are smaller."""
+    d, n = dims(**kw), ctypes.c_size_t(7)
+    for st in (lib.mamba_gated_delta_rule_workspace_bytes(ctypes.byref(d), ctypes.byref(n)),
+               lib.mamba_gated_delta_rule_bwd_workspace_bytes(ctypes.byref(d), 0, ctypes.byref(n)),
+               lib.mamba_gated_delta_rule_bwd_workspace_bytes(ctypes.byref(d), 1, ctypes.byref(n))):
+        assert st == (UNSUPPORTED if too_many else 0)
+    assert fwd(lib, d, q=None) == bwd(lib, d, q=None) == (UNSUPPORTED if too_many else INVALID)
+    if kw["seqlen"] == 1:
+        assert update(lib, d, q=None) == INVALID
