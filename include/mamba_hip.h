@@ -522,7 +522,9 @@ int mamba_gated_recurrence_update(const mamba_recurrence_dims_t* dims, float* st
  * Keys of norm at most 1 and beta in [0, 2] keep it from growing.  Documents, token 0
  * and initial_state as in mamba_selective_scan_fwd.  A decay below exp(-200) counts as
  * 0 (g = -inf included).  A NaN or an infinity reaches no other document and, in
- * the forward, no earlier token; where it reaches, results are NaN. */
+ * the forward, no earlier token; where it reaches, results are NaN.  So it is with a value
+ * that passes float32's range on the way (v of the type's lowest value with beta above 1), but
+ * that a state may be infinite then. */
 #define MAMBA_DELTA_CHUNK 64
 typedef struct {
     int64_t batch;       /* B                                                       */

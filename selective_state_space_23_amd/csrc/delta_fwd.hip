@@ -158,7 +158,7 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
         }
         // Values that are not finite: the rows from there to the document's end take no part, and give NaN
         uint64_t lost = 0;
-        const bool any_lost = bad != 0 || __ballot(odd) != 0;
+        bool any_lost = bad != 0 || __ballot(odd) != 0;
         if (any_lost) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -194,6 +194,18 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
 #pragma unroll
                 for (int r = 0; r < 4; ++r) U[i][r] *= beta[r];
             }
+        }
+        // Nor has a U past float32's range: 0 times it is NaN, for other documents and earlier tokens
+        float check = 0.0f;   // stays 0 as long as everything is finite
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) check = __builtin_fmaf(U[i][r], 0.0f, check);
+        if (__ballot(not_finite(check)) != 0) {
+            any_lost = true;
+            lost = lost_with(lost, U, starts, g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) U[i] = without_rows(U[i], lost, i, g);
         }
 
         // O
@@ -434,6 +446,7 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
             // B: U = beta T R, then S.  PLAIN: one document, everything finite
             auto rest = [&](auto plain) {
                 constexpr bool PLAIN = decltype(plain)::value;
+                const int last_start = !PLAIN && starts != 0 ? 63 - __builtin_clzll(starts) : 0;
                 auto triangle = [&](int i, int j, int p) { return Tl[(low_block(i, j) * 3 + p) * 64 + lane]; };
                 auto keys = [&](Frag<1>* kf, int i0, int j) {
 #pragma unroll
@@ -488,7 +501,8 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
                     for (int r = 0; r < 4; ++r) U[i][r] *= beta[i][r];
                     if constexpr (EMIT) *reinterpret_cast<f32x4*>(Ub + ((pair * 4 + i) * 64 + lane) * 16) = U[i];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) U[i][r] *= outof[i][r];
+                    for (int r = 0; r < 4; ++r)   // (0 times what has passed float32's range would be NaN)
+                        U[i][r] = PLAIN ? U[i][r] * outof[i][r] : keep_if(16 * i + 4 * g + r >= last_start, U[i][r] * outof[i][r]);
                 }
                 Frag<3> uf[2];
                 uf[0] = split(U[0], U[1]);
@@ -599,26 +613,43 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
             const int first_start = starts ? __builtin_ctzll(starts) : C;
             const u32x4* Pl = reinterpret_cast<const u32x4*>(Pb);
             const f32x4* Ul = reinterpret_cast<const f32x4*>(Ub + pair * 4096);
-            Frag<3> pf[4];
-            auto pairs = [&](int i, int j) {
-                Frag<3> f;
-#pragma unroll
-                for (int p = 0; p < 3; ++p) f.p[p] = Pl[(low_block(i, j) * 3 + p) * 64 + lane];
-                return f;
-            };
+            f32x4 qs[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                pf[i] = pairs(i, 0);
                 const f32x4 into = four(rec->into + 16 * i + 4 * g);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    O[i][r] = keep_if(16 * i + 4 * g + r < first_start, a.scale * into[r] * O[i][r]);
+                    qs[i][r] = keep_if(16 * i + 4 * g + r < first_start, a.scale * into[r] * O[i][r]);
             }
-            products<3, 4>(O, pf, split(Ul[lane], Ul[64 + lane]));
+            auto weigh = [&](auto value) {
+                Frag<3> pf[4];
+                auto pairs = [&](int i, int j) {
+                    Frag<3> f;
 #pragma unroll
-            for (int i = 2; i < 4; ++i) pf[i] = pairs(i, 1);
-            products<3, 2>(O + 2, pf + 2, split(Ul[128 + lane], Ul[192 + lane]));
-            const uint64_t lost = *reinterpret_cast<const uint64_t*>(Lb + (pair * 64 + lane) * 8);
+                    for (int p = 0; p < 3; ++p) f.p[p] = Pl[(low_block(i, j) * 3 + p) * 64 + lane];
+                    return f;
+                };
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    pf[i] = pairs(i, 0);
+                    O[i] = qs[i];
+                }
+                products<3, 4>(O, pf, split(value(0), value(1)));
+#pragma unroll
+                for (int i = 2; i < 4; ++i) pf[i] = pairs(i, 1);
+                products<3, 2>(O + 2, pf + 2, split(value(2), value(3)));
+            };
+            weigh([&](int i) { return Ul[i * 64 + lane]; });
+            // A U past float32's range has no part in O: 0 times it is NaN, for other documents and earlier tokens, and so
+            // for all tokens of the last tile, of which one tells. (All 16 of a lane's U looked at: 64K tokens, 40 heads 3.70 ms.)
+            uint64_t lost = *reinterpret_cast<const uint64_t*>(Lb + (pair * 64 + lane) * 8);
+            if (__ballot(not_finite(O[3][0])) != 0) {
+                asm volatile("" ::: "memory");   // (loads from LDS once more, not kept for this)
+                const f32x4 U[4] = {Ul[lane], Ul[64 + lane], Ul[128 + lane], Ul[192 + lane]};
+                lost = lost_with(lost, U, starts, g);
+                asm volatile("" ::: "memory");
+                weigh([&](int i) { return without_rows(Ul[i * 64 + lane], lost, i, g); });
+            }
             if (__ballot(lost != 0) != 0) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)

@@ -379,6 +379,24 @@ __device__ __forceinline__ float nan_if(bool on, float x) { return __uint_as_flo
 
 __device__ __forceinline__ bool not_finite(float x) { return __builtin_isfpclass(x, 0x207); }   // nan, +-inf
 
+// `lost`, rows of a chunk for a lane's column, with those whose value x (rows 16 i + 4 g + r) is not finite and the rest of
+// their documents.
+__device__ __forceinline__ uint64_t lost_with(uint64_t lost, const f32x4 (&x)[4], uint64_t starts, int g) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) lost |= uint64_t(not_finite(x[i][r])) << (16 * i + 4 * g + r);
+    lost |= __shfl_xor(lost, 16);
+    lost |= __shfl_xor(lost, 32);
+    return smear(lost, starts);
+}
+// x of tile i without the rows of `lost`.
+__device__ __forceinline__ f32x4 without_rows(f32x4 x, uint64_t lost, int i, int g) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = keep_if(!((lost >> (16 * i + 4 * g + r)) & 1), x[r]);
+    return x;
+}
+
 // Four consecutive token values of a record.
 __device__ __forceinline__ f32x4 four(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 

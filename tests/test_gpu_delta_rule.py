@@ -576,3 +576,28 @@ def test_backward_not_finite_over_chunks(ssm, where, dtype, L, starts):
             bf16 = n in IO and dtype == "bf16"
             tol = (2.0 ** -7 if bf16 else 0.0) * ref.abs() + (4e-4 if bf16 else 1e-4) * (ref ** 2).mean().sqrt()
             assert ((rest - ref).abs() <= tol).all(), (n, at)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("at,docs", [(40, [30, 50, 85]), (100, []), (63, [64, 130]), (64, [64, 130])])
+def test_overflow_stays_in_its_document(ssm, at, docs, dtype):
+    """The type's lowest value at one token, which beta = 1.5 takes past float32's range: other documents, earlier tokens
+    and other columns do not see it."""
+    import torch
+
+    L = 200
+    d = draw(2, L, 1, 2, 32, 24, dtype, seed=18, carry=True)
+    d["doc_start"] = np.zeros((2, L), np.uint8)
+    d["doc_start"][:, docs] = 1
+    d["beta"][0, at, 0] = 1.5
+    last = min([e for e in docs if e > at] + [L])
+    low = {n: None if x is None else x.copy() for n, x in d.items()}
+    low["v"][0, at, 0, 3] = torch.finfo(torch.bfloat16 if dtype == "bf16" else torch.float32).min
+    (out, S), (want, wS) = forward(ssm, dev(low, dtype)), forward(ssm, dev(d, dtype))
+    assert not torch.isfinite(out[0, at:last, 0, 3]).any()
+    out[0, at:last, 0, 3] = want[0, at:last, 0, 3]
+    assert torch.equal(out, want)
+    if last == L:
+        assert not torch.isfinite(S[0, 0, :, 3]).any()
+        S[0, 0, :, 3] = wS[0, 0, :, 3]
+    assert torch.equal(S, wS)
