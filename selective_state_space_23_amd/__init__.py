@@ -901,21 +901,26 @@ def _delta_dims(q, k, v, lead, scale, code, lds=(0, 0, 0, 0)):
     return _lib.DeltaDims(batch, seqlen, Hk, Hv, K, V, *lds, code, K ** -0.5 if scale is None else scale)
 
 
-def _any_strides(batch, seqlen, key_heads, value_heads, key_dim, value_dim, dtype):
-    """mamba_delta_dims_t whose workspaces are large enough for any strides of q and k: odd ones make the library copy them."""
+def _any_strides(query, name, shape, dtype, *more):
+    """Bytes that are enough for any strides of q and k: odd ones make the library copy them.  (Where it refuses copies
+    as large, it refuses such strides.)"""
     code = _lib.MAMBA_DTYPE_BF16 if dtype == "bf16" else _lib.MAMBA_DTYPE_F32
-    width = key_heads * key_dim
-    ld = width | 1 if 0 < width < 2 ** 21 else 0
-    return _lib.DeltaDims(batch, seqlen, key_heads, value_heads, key_dim, value_dim, ld, ld, 0, 0, code, 1.0)
+    width = shape[2] * shape[4]
+    odd = width | 1 if 0 < width < 2 ** 21 else 0
+    n = ctypes.c_size_t(0)
+    for ld in (odd, 0):
+        dims = _lib.DeltaDims(*shape, ld, ld, 0, 0, code, 1.0)
+        st = query(ctypes.byref(dims), *more, ctypes.byref(n))
+        if st != _lib.MAMBA_ERR_UNSUPPORTED:
+            break
+    _lib.check(st, name)
+    return int(n.value)
 
 
 def gated_delta_rule_workspace_bytes(batch, seqlen, key_heads, value_heads, key_dim, value_dim, dtype="bf16") -> int:
     """Bytes of workspace that are enough for gated_delta_rule_fwd, q and k dense or slices of anything."""
-    dims = _any_strides(batch, seqlen, key_heads, value_heads, key_dim, value_dim, dtype)
-    n = ctypes.c_size_t(0)
-    _lib.check(_lib.load().mamba_gated_delta_rule_workspace_bytes(ctypes.byref(dims), ctypes.byref(n)),
-               "mamba_gated_delta_rule_workspace_bytes")
-    return int(n.value)
+    return _any_strides(_lib.load().mamba_gated_delta_rule_workspace_bytes, "mamba_gated_delta_rule_workspace_bytes",
+                        (batch, seqlen, key_heads, value_heads, key_dim, value_dim), dtype)
 
 
 def gated_delta_rule_fwd(q, k, v, g, beta, doc_start=None, scale=None, initial_state=None, final_state=True, out=None,
@@ -979,12 +984,9 @@ def gated_delta_rule_fwd(q, k, v, g, beta, doc_start=None, scale=None, initial_s
 def gated_delta_rule_bwd_workspace_bytes(batch, seqlen, key_heads, value_heads, key_dim, value_dim, dtype="bf16",
                                          states=False) -> int:
     """The same for gated_delta_rule_bwd (``states``: with those that the forward kept)."""
-    dims = _any_strides(batch, seqlen, key_heads, value_heads, key_dim, value_dim, dtype)
-    n = ctypes.c_size_t(0)
-    _lib.check(_lib.load().mamba_gated_delta_rule_bwd_workspace_bytes(ctypes.byref(dims), int(bool(states)),
-                                                                      ctypes.byref(n)),
-               "mamba_gated_delta_rule_bwd_workspace_bytes")
-    return int(n.value)
+    return _any_strides(_lib.load().mamba_gated_delta_rule_bwd_workspace_bytes,
+                        "mamba_gated_delta_rule_bwd_workspace_bytes",
+                        (batch, seqlen, key_heads, value_heads, key_dim, value_dim), dtype, int(bool(states)))
 
 
 def gated_delta_rule_bwd(q, k, v, g, beta, dout, doc_start=None, scale=None, initial_state=None, d_final_state=None,

@@ -220,3 +220,18 @@ def test_launches_of_2_32_threads(lib, kw, too_many):
     assert fwd(lib, d, q=None) == bwd(lib, d, q=None) == (UNSUPPORTED if too_many else INVALID)
     if kw["seqlen"] == 1:
         assert update(lib, d, q=None) == INVALID
+
+
+def test_workspace_where_copies_are_refused():
+    """Rows too many to copy: as much as dense ones need.  What is refused however the rows lie still is."""
+    import selective_state_space_23_amd as ssm
+
+    n = ctypes.c_size_t(0)
+    d = dims(batch=1024, seqlen=262145, key_heads=1, value_heads=1, key_dim=128, value_dim=64)
+    assert _lib.load().mamba_gated_delta_rule_workspace_bytes(ctypes.byref(d), ctypes.byref(n)) == 0
+    assert ssm.gated_delta_rule_workspace_bytes(1024, 262145, 1, 1, 128, 64) == n.value
+    assert ssm.gated_delta_rule_bwd_workspace_bytes(1024, 262145, 1, 1, 128, 64) > n.value
+    for shape in ((1024, 262145, 1, 1, 127, 64), (65535, 64, 65, 65, 128, 128)):
+        for helper in (ssm.gated_delta_rule_workspace_bytes, ssm.gated_delta_rule_bwd_workspace_bytes):
+            with pytest.raises(ssm.MambaArgumentError):
+                helper(*shape)
