@@ -898,7 +898,9 @@ def _delta_dims(q, k, v, lead, scale, code, lds=(0, 0, 0, 0)):
     Hk, K = q.shape[-2:]
     Hv, V = v.shape[-2:]
     batch, seqlen = lead if len(lead) == 2 else (lead[0], 1)
-    return _lib.DeltaDims(batch, seqlen, Hk, Hv, K, V, *lds, code, K ** -0.5 if scale is None else scale)
+    if scale is None:
+        scale = K ** -0.5 if K else 1.0   # (heads without channels: the library refuses them)
+    return _lib.DeltaDims(batch, seqlen, Hk, Hv, K, V, *lds, code, scale)
 
 
 def _any_strides(query, name, shape, dtype, *more):
