@@ -4,8 +4,9 @@
 // consecutive columns and K COLS / 256 consecutive rows a thread:
 //     S' = a S;  u = beta (v - S'^T k);  S = S' + k u^T;  out = scale S^T q,
 // the sums over rows by lane exchanges, then over the four waves through LDS.  Bound by memory
-// (the state read and written once: 128 rows of 40 heads of 128 x 128 in 131 us, the time of a copy as large); the columns
-// of one head are split over workgroups where there are few heads, whose time is a trip to memory (two rows of 12: 8 us).
+// (the state read and written once: 128 rows of 40 heads of 128 x 128, 675 MB, in 134 us over six states in turn, the time of a
+// copy as large; 113 us with one state again and again, part of which the last cache keeps); the columns
+// of one head are split over workgroups where there are few heads, whose time is a trip to memory (two rows of 12: 3.9 us).
 #include "delta_rule.hpp"
 
 namespace mamba {
@@ -136,10 +137,12 @@ hipError_t launch(const DeltaUpdateArgs& a) {
     return hipGetLastError();
 }
 
-// Few heads: 32 columns a workgroup, more of them.  128 heads of 128 x 128: 4.6 us, 5.2 with 128 columns; 512: 9.3 and 8.7.
+// Few heads: 32 columns a workgroup, more of them, where these are whole lines of memory (128 heads of 128 x 128, over states that
+// no cache holds: 6.5 us, 7.4 with 128 columns; 256: 9.7 and 10.1; 512: 16.2 and 17.2; 8192: 214 and 214).  Parts of lines cost
+// more than they gain: 128 heads of 128 x 100 9.8 us, 6.6 with whole rows; 240 heads of 64 x 36 5.7 and 4.6.
 template <typename T>
 hipError_t by_size(const DeltaUpdateArgs& a) {
-    const bool few = a.batch * a.vheads < 256;
+    const bool few = a.batch * a.vheads < 256 && (a.vdim <= 32 || a.vdim % 32 == 0);
     if (a.kdim > 64) return few ? launch<T, 128, 8>(a) : launch<T, 128, 32>(a);
     return few ? launch<T, 64, 8>(a) : launch<T, 64, 32>(a);
 }
