@@ -644,7 +644,8 @@ typedef struct {
  *              rotated channels.
  *   q_out, k_out: dense, `dtype`.
  * Supported: D up to 256, heads times D up to 2^21, strides up to 2^40, B L below 2^31.
- * Arithmetic is float32, outputs are rounded once.  Any alignment to the element size; D and
+ * Arithmetic is float32, outputs are rounded once; a head whose sum of squares passes float32's
+ * range gives 0, one whose sum is 0 there with eps = 0 what is not finite.  Any alignment to the element size; D and
  * R multiples of 8 with everything aligned to 16 bytes selects the vectorised kernels.
  * Outputs must not overlap anything else of the call. */
 int mamba_qk_norm_rotary_fwd(const mamba_qk_norm_dims_t* dims, const void* q, const void* k, const float* q_weight,

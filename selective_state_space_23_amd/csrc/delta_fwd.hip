@@ -25,7 +25,7 @@ namespace {
 
 using namespace delta;
 
-// float32, and bf16 that is not in whole 16-byte pieces.  (3 x 1001 tokens, 6 heads of 100 x 75 in float32: 152 us.)
+// float32, and bf16 that is not in whole 16-byte pieces.  (3 x 1001 tokens, 6 heads of 100 x 75 in float32: 157 us.)
 template <typename T, int KT, int NW, bool VEC, bool EMIT>
 __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t rec_bytes, int cols) {
     constexpr int N = kPieces<T>, ESZ = sizeof(T), STEPS = KT / 32, THREADS = NW * 64;
@@ -290,19 +290,19 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
 // The same for bf16 in whole 16-byte pieces, two waves for every 16 columns: one walks the chain
 // S -> R -> U -> S, which is what a row's time is, the other follows it by half a chunk with
 // everything that does not lead back to S: the outputs, from S and U as the first leaves them in LDS,
-// and all loads, straight to LDS.  (One wave doing both, four to a workgroup: 64K tokens x 40 heads 6.0 ms.)
+// and all loads, straight to LDS.  (One wave doing both, four to a workgroup: more than twice as long.)
 //
 // Chunk c:  barrier;  A: the chain forms K S and R; the other loads K and T of c + 1 and finishes O of c - 1;
 //           barrier;  B: the chain forms U, then S;   the other loads V and Q of c + 1 and P of c and forms Q S.
 // NP = 4, whose LDS has no room for a second T and Q: those of c + 1 are loaded when U and Q S of c are there, behind a
-// third barrier.  (Loaded in A of their own chunk, and waited for there: 8 x 2048 tokens, 12 heads of 128 x 128, 146 us for 128.)
+// third barrier.  (Loaded in A of their own chunk, and waited for there: 8 x 2048 tokens, 12 heads of 128 x 128, a seventh more.)
 //
 // A workgroup has NP such pairs, for as many 16 columns of one head, a chain and a follower on a SIMD with NP = 4: a wave
 // alone issues a vector instruction every 8 cycles, two together twice as many.
 template <int NP> constexpr int kBuffers = NP == 2 ? 2 : 1;   // of T and Q
 template <int KT, int NP, bool EMIT>
 constexpr int kPairsLds = 2 * C * KT * 2 + kBuffers<NP> * kBlocks * 3 * 1024 + 2 * 2048 + NP * (2048 + 512) +
-                          (EMIT ? kBuffers<NP> * C * KT * 2 + kBlocks * 3072 + NP * (KT / 32 * 2048 + 4096) : 0);
+                          (EMIT ? kBuffers<NP> * C * KT * 2 + kBlocks * 3 * 1024 + NP * (KT / 32 * 2048 + 4096) : 0);
 // (LDS given at the launch, and two waves a SIMD asked for: one workgroup fills a CU either way, but where the compiler
 // sees that, it takes 512 registers, keeps sums in the upper 256 and moves them, 8 cycles each.)
 template <int KT, int NP, bool EMIT, bool SAVE>

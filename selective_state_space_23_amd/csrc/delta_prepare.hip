@@ -14,8 +14,8 @@
 // passes' matrix instructions read it.  The weights P = scale D o Q K^T of the values in the outputs go the
 // same way (formed by every wave of the later passes instead: 440 vector instructions a chunk each).
 //
-// Near what memory allows: 64K tokens x 40 heads of 128, 549 us for 2.6 GB, 702 with the loads of each 32 channels waited
-// for in turn.
+// Near what memory allows: 64K tokens x 40 heads of 128, 599 us for the 3.6 GB that the counters see (a quarter more with the
+// loads of each 32 channels waited for in turn).
 //
 // gamma is summed in float64 and kept as two floats: gamma_t - gamma_s is
 // then right to float32 of itself however far the sum has run.  A decay below
