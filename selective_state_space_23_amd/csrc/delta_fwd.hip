@@ -179,7 +179,7 @@ __global__ __launch_bounds__(NW * 64, 1) void fwd_kernel(DeltaArgs a, int64_t re
         {
 #pragma unroll
             for (int i = 0; i < 4; ++i) U[i] = f32x4{0, 0, 0, 0};
-            const Frag<3> rf[2] = {split(R[0], R[1]), split(R[2], R[3])};
+            const Frag<3> rf[2] = {split_values(R[0], R[1]), split_values(R[2], R[3])};
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -459,7 +459,7 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
 #pragma unroll
                 for (int i = 0; i < 4; ++i) U[i] = f32x4{0, 0, 0, 0};
                 // a piece of T at a time, the smallest first
-                const Frag<3> rf0 = split(R[0], R[1]);
+                const Frag<3> rf0 = split_values(R[0], R[1]);
 #pragma unroll
                 for (int p = 2; p >= 0; --p) {
                     u32x4 tf[4];
@@ -470,7 +470,7 @@ __global__ __launch_bounds__(NP * 128, 2) void fwd_pairs_kernel(DeltaArgs a, int
 #pragma unroll
                         for (int i = 0; i < 4; ++i) U[i] = mfma(tf[i], rf0.p[q], U[i]);
                 }
-                const Frag<3> rf1 = split(R[2], R[3]);
+                const Frag<3> rf1 = split_values(R[2], R[3]);
 #pragma unroll
                 for (int p = 2; p >= 0; --p) {
                     const u32x4 t2 = triangle(2, 1, p), t3 = triangle(3, 1, p);

@@ -253,7 +253,7 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(DeltaArgs a, int64_t
                 // E, U
                 f32x4 E[4];
                 {
-                    const Frag<3> rf[2] = {split(R[0], R[1]), split(R[2], R[3])};
+                    const Frag<3> rf[2] = {split_values(R[0], R[1]), split_values(R[2], R[3])};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) E[i] = f32x4{0, 0, 0, 0};
 #pragma unroll

@@ -114,29 +114,37 @@ inline bool wide_groups(const DeltaArgs& a) {
     return a.vdim > 32 && a.batch * a.vheads * ((a.vdim + 31) / 32) > 256;
 }
 
-// The bf16 pieces of pairs of floats: the highest 8 significant bits, the rest rounded to as many, and what is left.
+// The bf16 pieces of pairs of floats: the highest 8 significant bits, the rest rounded (CUT: cut) to as many, and what is left.
+template <bool CUT = false>
 __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
     hi = __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302u);
     without_pieces(hi, x0, x1);
-    mid = pack_bf16x2(x0, x1);
+    mid = CUT ? __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302u) : pack_bf16x2(x0, x1);
     without_pieces(mid, x0, x1);
     lo = __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302u);
 }
 
 // Eight floats in three pieces: slots 0..3 from a, 4..7 from b.
+template <bool CUT = false>
 __device__ __forceinline__ Frag<3> split(f32x4 a, f32x4 b) {
     Frag<3> f;
     uint32_t h, m, l;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const f32x4 x = i < 2 ? a : b;
-        split_pair(x[2 * (i & 1)], x[2 * (i & 1) + 1], h, m, l);
+        split_pair<CUT>(x[2 * (i & 1)], x[2 * (i & 1) + 1], h, m, l);
         f.p[0][i] = h;
         f.p[1][i] = m;
         f.p[2][i] = l;
     }
     return f;
 }
+
+// Eight of the differences R = v - ..., which are v itself where no state and no other token has a part: the lowest float,
+// at tokens that count for nothing with beta = 0, has to come out of T R as it went in.  The matrix instruction cuts sums
+// towards minus infinity, and with a rounded second piece, -2^120 here, anything else in the sum makes it -2^128; with
+// cut pieces what lies below 2^96 does not reach it.  (What T R leaves out is up to 1.5 x 2^-22 of a product.)
+__device__ __forceinline__ Frag<3> split_values(f32x4 a, f32x4 b) { return split<true>(a, b); }
 
 // The rows of one chunk of one tensor as a buffer: reads behind the last token
 // give zero, writes there are dropped.

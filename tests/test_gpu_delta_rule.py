@@ -601,3 +601,24 @@ def test_overflow_stays_in_its_document(ssm, at, docs, dtype):
         assert not torch.isfinite(S[0, 0, :, 3]).any()
         S[0, 0, :, 3] = wS[0, 0, :, 3]
     assert torch.equal(S, wS)
+
+
+@pytest.mark.parametrize("dtype,K,V", [("f32", 64, 32), ("f32", 100, 75), ("bf16", 64, 32), ("bf16", 33, 40)])
+def test_lowest_values_that_count_for_nothing(ssm, dtype, K, V):
+    """The type's lowest value, and its highest, as v of tokens with beta = 0: results are those of any other v there, to
+    the bit, but for those tokens' dbeta."""
+    import torch
+
+    d = draw(2, 200, 1, 2, K, V, dtype, seed=24, carry=True)
+    where = [0, 1, 31, *range(50, 60), 63, 64, 100, 199]
+    d["beta"][:, where] = 0.0
+    info = torch.finfo(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    want, grads = forward(ssm, dev(d, dtype)), backward(ssm, dev(d, dtype))
+    for value in (info.min, info.max, info.min / 3):
+        low = {n: None if x is None else x.copy() for n, x in d.items()}
+        low["v"][:, where] = bf16_round(np.float32(value)) if dtype == "bf16" else value
+        assert all(torch.equal(a, b) for a, b in zip(forward(ssm, dev(low, dtype)), want)), value
+        got = backward(ssm, dev(low, dtype))
+        got["dbeta"][:, where] = grads["dbeta"][:, where]
+        for n in grads:
+            assert torch.equal(got[n], grads[n]), (n, value)
